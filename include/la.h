@@ -384,6 +384,119 @@ enum la_wait_site {
 int la_workspace_wait_site(void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Gated recurrence: linear attention whose memory decays. Per sequence and head,
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T,   out_t = S_t^T q_t,   t = 0 .. N-1,
+ * with one log-decay g_t per token and head. The feature map is the identity and
+ * there is no denominator (la_norm_gate normalises the outputs instead).
+ *
+ * g: [B][H][N] in `dtype`, natural logarithms, normally <= 0 (-inf empties the
+ * state before its token is added). Growing states (g > 0) work while exp() of g's
+ * sums over a segment of up to a few thousand tokens stays finite.
+ * Everything else is laid out as for la_forward; states are float32 [B][H][D][M].
+ * D, M: multiples of 8 in [8, 128]; dtype LA_F32 or LA_BF16. Sums and the carried
+ * state are float32; in bf16 the tensor cores take the state and the weights within
+ * a chunk of tokens rounded to bf16, as far as an output in bf16 shows them.
+ */
+
+/* Scratch needed by la_forward_gated and la_extend_gated, in bytes. */
+size_t la_gated_workspace_bytes(int B, int H, int N, int D, int M, int dtype);
+
+/*
+ * la_forward_gated -- out of N tokens, from the state S0 (float32 [B][H][D][M];
+ * nullptr: zero), and the state after them in S (nullptr: not wanted). S may be S0.
+ * N == 0 copies S0 (or zero) to S.
+ */
+int la_forward_gated(const void* q, const void* k, const void* v, const void* g, void* out,
+                     const float* S0, float* S, int B, int H, int N, int D, int M, int dtype,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * la_extend_gated -- la_extend for the gated recurrence: stream b continues from
+ * the entry slots[b] of S_pool [pool_size][H][D][M] (float32, updated in place;
+ * nullptr: entry b) by its first lens[b] tokens (nullptr: all N). slots are
+ * distinct. A slot outside the pool is neither read nor written: its stream starts
+ * from a zero state and la_workspace_status reports LA_ERR_INVALID_ARG. Rows of out
+ * at or past lens[b] are left as they were; those of q, k, v, g may hold anything.
+ */
+int la_extend_gated(const void* q, const void* k, const void* v, const void* g, void* out,
+                    float* S_pool, const int* slots, const int* lens, int pool_size, int B, int H,
+                    int N, int D, int M, int dtype, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/*
+ * la_decode_step_gated -- one token of each stream. q, k [n_streams][H][D],
+ * v, out [n_streams][H][M], g [n_streams][H]; S_pool, slots and pool_size as for
+ * la_extend_gated (without a workspace a slot outside the pool is not reported).
+ */
+int la_decode_step_gated(const void* q, const void* k, const void* v, const void* g, float* S_pool,
+                         const int* slots, void* out, int pool_size, int n_streams, int H, int D,
+                         int M, int dtype, void* stream);
+
+/* Scratch needed by la_backward_gated, in bytes. */
+size_t la_gated_backward_workspace_bytes(int B, int H, int N, int D, int M, int dtype);
+
+/*
+ * la_backward_gated -- gradients of sum(dout * out) + sum(dS * S) for the out and S
+ * that la_forward_gated gives for q, k, v, g, S0. dS: nullptr for zero. dq, dk
+ * [B][H][N][D], dv [B][H][N][M] and dg [B][H][N] in `dtype` (unlike la_backward's,
+ * which are float32: these are added to leaves of the inputs' type); dS0 float32
+ * [B][H][D][M], nullptr if not wanted. Nothing of the forward is needed: states are
+ * recomputed. N == 0 copies dS (or zero) to dS0.
+ */
+int la_backward_gated(const void* q, const void* k, const void* v, const void* g, const void* dout,
+                      const float* S0, const float* dS, void* dq, void* dk, void* dv, void* dg,
+                      float* dS0, int B, int H, int N, int D, int M, int dtype, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * la_rotary -- rotary positions on q [B][H][N][D] and k [B][Hk][N][D] (Hk == 0: no
+ * k). The pair i < R/2 of the first R elements of a head, elements (2i, 2i+1) if
+ * `interleaved`, else (i, i + R/2), is turned by positions * freqs[i] radians and
+ * scaled by mscale; the other D - R elements are copied. inverse != 0 turns the
+ * other way: the gradient with respect to the inputs, given that of the outputs.
+ *
+ * Each *_strides is a host array of three strides in elements, of the batch, the
+ * head and the token (a head's elements are contiguous); pointers are aligned to
+ * their element only, and 16-byte aligned rows run faster. An output may be its
+ * input (same pointer and strides).
+ * freqs: device double[R/2], radians per token. positions: device int[N] (or one
+ * row of N per batch entry, pos_stride_b entries apart; 0: shared), any sign;
+ * nullptr: offset + token index.
+ * D: a multiple of 8 in [8, 128]; R even in [2, D]; B <= 65535.
+ */
+int la_rotary(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides,
+              const void* k, const long long* k_strides, void* k_out, const long long* k_out_strides,
+              const double* freqs, const int* positions, long long pos_stride_b, long long offset,
+              int B, int H, int Hk, int N, int D, int R, int interleaved, int inverse, float mscale,
+              int dtype, void* stream);
+
+/*
+ * la_norm_gate -- y = x / sqrt(mean(x^2) + eps) * w * z sigmoid(z), the mean over
+ * the M elements of each row of x [B][H][N][M]. w: [M], or [H][M] if w_per_head.
+ * z and y are strided (host arrays of three strides in elements: batch, head, token;
+ * multiples of 16 bytes), so that y can be written token-major for the projection
+ * that follows. All pointers 16-byte aligned, everything in `dtype`, B * N < 2^31,
+ * eps >= 0. A row of zeros with eps == 0 gives NaN, as the formula does.
+ */
+int la_norm_gate(const void* x, const void* z, const long long* z_strides, const void* w, void* y,
+                 const long long* y_strides, int B, int H, int N, int M, int w_per_head, float eps,
+                 int dtype, void* stream);
+
+/* Scratch needed by la_norm_gate_backward, in bytes. */
+size_t la_norm_gate_workspace_bytes(int B, int H, int N, int M);
+
+/*
+ * la_norm_gate_backward -- dx [B][H][N][M], dz (strided) and dw (w's layout, summed
+ * over the rows that share it in a fixed order) from dy (strided), in `dtype`.
+ * N == 0 writes dw = 0.
+ */
+int la_norm_gate_backward(const void* x, const void* z, const long long* z_strides, const void* w,
+                          const void* dy, const long long* dy_strides, void* dx, void* dz,
+                          const long long* dz_strides, void* dw, int B, int H, int N, int M,
+                          int w_per_head, float eps, int dtype, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
  * Failure-detection test hooks (the pages have no counterpart; test use only).
  *
  * la_debug_forward_fault / la_debug_backward_fault run la_forward /

@@ -23,6 +23,10 @@ __all__ = [
     "la_state_sums", "la_forward_shard", "la_backward_shard_q", "la_backward_shard_kv",
     "la_forward_poly2", "la_poly2_workspace_bytes", "la_forward_rff", "la_rff_workspace_bytes",
     "LA_SITE_FORWARD_LOAD", "LA_SITE_BACKWARD_LOAD",
+    "la_forward_gated", "la_prefill_gated", "la_extend_gated", "la_decode_step_gated",
+    "la_backward_gated", "la_gated_workspace_bytes", "la_gated_backward_workspace_bytes",
+    "la_rotary", "la_rotary_freqs", "la_norm_gate", "la_norm_gate_backward",
+    "la_norm_gate_workspace_bytes",
 ]
 
 LA_OK, LA_ERR_INVALID_ARG, LA_ERR_WORKSPACE, LA_ERR_CUDA, LA_ERR_TIMEOUT = 0, 1, 2, 3, 4
@@ -61,6 +65,18 @@ _SIGNATURES = {
     "la_forward_shard": (_c_int, [_vp] * 6 + [_c_int] * 6 + [_vp, _c_size, _vp]),
     "la_backward_shard_q": (_c_int, [_vp] * 9 + [_c_int] * 6 + [_vp, _c_size, _vp]),
     "la_backward_shard_kv": (_c_int, [_vp] * 8 + [_c_int] * 6 + [_vp, _c_size, _vp]),
+    "la_gated_workspace_bytes": (_c_size, [_c_int] * 6),
+    "la_gated_backward_workspace_bytes": (_c_size, [_c_int] * 6),
+    "la_forward_gated": (_c_int, [_vp] * 7 + [_c_int] * 6 + [_vp, _c_size, _vp]),
+    "la_extend_gated": (_c_int, [_vp] * 8 + [_c_int] * 7 + [_vp, _c_size, _vp]),
+    "la_decode_step_gated": (_c_int, [_vp] * 7 + [_c_int] * 6 + [_vp]),
+    "la_backward_gated": (_c_int, [_vp] * 12 + [_c_int] * 6 + [_vp, _c_size, _vp]),
+    "la_rotary": (_c_int, [_vp] * 10 + [ctypes.c_longlong] * 2 + [_c_int] * 8
+                  + [ctypes.c_float, _c_int, _vp]),
+    "la_norm_gate": (_c_int, [_vp] * 6 + [_c_int] * 5 + [ctypes.c_float, _c_int, _vp]),
+    "la_norm_gate_workspace_bytes": (_c_size, [_c_int] * 4),
+    "la_norm_gate_backward": (_c_int, [_vp] * 10 + [_c_int] * 5
+                              + [ctypes.c_float, _c_int, _vp, _c_size, _vp]),
     "la_debug_noalloc_set_status": (_c_int, [_c_int, _c_int, _vp]),
     "la_workspace_wait_site": (_c_int, [_vp, _c_size, _vp]),
     "la_debug_forward_fault": (_c_int, [_vp] * 4 + [_c_int] * 7 + [_vp, _c_size, _c_int,
@@ -625,3 +641,368 @@ def la_forward_rff(q, k, v, W, bias, causal=True, out=None, workspace=None):
                                 ws.numel() * ws.element_size(), _stream_ptr(dev))
     _check(fn, st)
     return out
+
+
+# ---------------------------------------------------------- gated recurrence
+
+def la_gated_workspace_bytes(B, H, N, D, M, dtype=LA_BF16):
+    return load_library().la_gated_workspace_bytes(B, H, N, D, M, dtype)
+
+
+def la_gated_backward_workspace_bytes(B, H, N, D, M, dtype=LA_BF16):
+    return load_library().la_gated_backward_workspace_bytes(B, H, N, D, M, dtype)
+
+
+def _forward_gated(fn, q, k, v, g, S0, out, S, want_state, workspace):
+    import torch
+    (B, H, N), D, M = _dims(fn, q, v, 4)
+    _expect(fn, "k", k, q.shape, q.dtype)
+    _expect(fn, "v", v, (B, H, N, M), q.dtype)
+    _expect(fn, "g", g, (B, H, N), q.dtype)
+    for name, t in (("S0", S0), ("S", S)):
+        if t is not None:
+            _expect(fn, name, t, (B, H, D, M), torch.float32)
+    if out is not None:
+        _expect(fn, "out", out, (B, H, N, M), q.dtype)
+    dt = _dtype_code(q)
+    _need_cuda(q, k, v, g, *[t for t in (S0, S, out) if t is not None])
+    lib = load_library()
+    dev = q.device
+    out = torch.empty((B, H, N, M), dtype=q.dtype, device=dev) if out is None else out
+    if want_state and S is None:
+        S = torch.empty((B, H, D, M), dtype=torch.float32, device=dev)
+    ws = _workspace(lib.la_gated_workspace_bytes(B, H, N, D, M, dt), dev, workspace)
+    with _on_device(dev):
+        st = lib.la_forward_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                  out.data_ptr(), 0 if S0 is None else S0.data_ptr(),
+                                  0 if S is None else S.data_ptr(), B, H, N, D, M, dt,
+                                  ws.data_ptr(), ws.numel() * ws.element_size(), _stream_ptr(dev))
+    _check(fn, st)
+    return out, S
+
+
+def la_forward_gated(q, k, v, g, S0=None, out=None, workspace=None):
+    """out[B,H,N,M]: out_t = S_t^T q_t with S_t = exp(g_t) S_{t-1} + k_t v_t^T.
+
+    q, k [B,H,N,D], v [B,H,N,M]; g [B,H,N], in q's dtype: log-decays, normally <= 0.
+    S0 [B,H,D,M] float32: the state before the first token (None: zero)."""
+    return _forward_gated("la_forward_gated", q, k, v, g, S0, out, None, False, workspace)[0]
+
+
+def la_prefill_gated(q, k, v, g, S0=None, out=None, S=None, workspace=None):
+    """la_forward_gated plus the state S [B,H,D,M] (float32) after the last token; S may be S0."""
+    return _forward_gated("la_prefill_gated", q, k, v, g, S0, out, S, True, workspace)
+
+
+def _check_pool(fn, S_pool, H, D, M, B, slots):
+    import torch
+    if S_pool.dim() != 4:
+        raise ValueError(f"{fn}: S_pool must be [pool, H, D, M]")
+    _expect(fn, "S_pool", S_pool, (S_pool.shape[0], H, D, M), torch.float32)
+    if slots is not None and (slots.dtype != torch.int32 or slots.numel() != B):
+        raise ValueError("slots must be a contiguous int32 tensor of B entries")
+
+
+def la_extend_gated(q, k, v, g, S_pool, slots=None, lens=None, out=None, workspace=None):
+    """la_forward_gated over new tokens of B streams, from and to their states in a pool.
+
+    S_pool [P,H,D,M] float32; stream b uses entry slots[b] (int32 device tensor of B distinct
+    entries; None: entry b), advanced in place past the first lens[b] of the N tokens (int32
+    device tensor; None: all N). Returns out [B,H,N,M]; its rows at or past lens[b] are left
+    as they were (uninitialised if `out` is None)."""
+    import torch
+    fn = "la_extend_gated"
+    (B, H, N), D, M = _dims(fn, q, v, 4)
+    _expect(fn, "k", k, q.shape, q.dtype)
+    _expect(fn, "v", v, (B, H, N, M), q.dtype)
+    _expect(fn, "g", g, (B, H, N), q.dtype)
+    _check_pool(fn, S_pool, H, D, M, B, slots)
+    if lens is not None and (lens.dtype != torch.int32 or lens.numel() != B):
+        raise ValueError("lens must be a contiguous int32 tensor of B entries")
+    if out is not None:
+        _expect(fn, "out", out, (B, H, N, M), q.dtype)
+    dt = _dtype_code(q)
+    _need_cuda(q, k, v, g, S_pool, *[t for t in (out, slots, lens) if t is not None])
+    lib = load_library()
+    dev = q.device
+    out = torch.empty((B, H, N, M), dtype=q.dtype, device=dev) if out is None else out
+    ws = _workspace(lib.la_gated_workspace_bytes(B, H, N, D, M, dt), dev, workspace)
+    with _on_device(dev):
+        st = lib.la_extend_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                 out.data_ptr(), S_pool.data_ptr(),
+                                 0 if slots is None else slots.data_ptr(),
+                                 0 if lens is None else lens.data_ptr(), S_pool.shape[0],
+                                 B, H, N, D, M, dt, ws.data_ptr(),
+                                 ws.numel() * ws.element_size(), _stream_ptr(dev))
+    _check(fn, st)
+    return out
+
+
+def la_decode_step_gated(q, k, v, g, S_pool, slots=None, out=None):
+    """One token of each of n streams: q, k [n,H,D], v [n,H,M], g [n,H]; the states in S_pool
+    [P,H,D,M] (entries slots, as in la_extend_gated) are updated in place; returns out [n,H,M]."""
+    import torch
+    fn = "la_decode_step_gated"
+    (n, H), D, M = _dims(fn, q, v, 3)
+    _expect(fn, "k", k, q.shape, q.dtype)
+    _expect(fn, "v", v, (n, H, M), q.dtype)
+    _expect(fn, "g", g, (n, H), q.dtype)
+    _check_pool(fn, S_pool, H, D, M, n, slots)
+    if out is not None:
+        _expect(fn, "out", out, (n, H, M), q.dtype)
+    dt = _dtype_code(q)
+    _need_cuda(q, k, v, g, S_pool, *[t for t in (out, slots) if t is not None])
+    lib = load_library()
+    dev = q.device
+    out = torch.empty((n, H, M), dtype=q.dtype, device=dev) if out is None else out
+    with _on_device(dev):
+        st = lib.la_decode_step_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                      S_pool.data_ptr(), 0 if slots is None else slots.data_ptr(),
+                                      out.data_ptr(), S_pool.shape[0], n, H, D, M, dt,
+                                      _stream_ptr(dev))
+    _check(fn, st)
+    return out
+
+
+def la_backward_gated(q, k, v, g, dout, S0=None, dS=None, dq=None, dk=None, dv=None, dg=None,
+                      dS0=None, workspace=None):
+    """Gradients of sum(dout * out) + sum(dS * S) of la_prefill_gated(q, k, v, g, S0): (dq, dk,
+    dv, dg) in the inputs' dtype, and dS0 [B,H,D,M] (float32) behind them if S0 is given.
+
+    dS [B,H,D,M] float32: the gradient with respect to the final state (None: zero)."""
+    import torch
+    fn, f32 = "la_backward_gated", torch.float32
+    (B, H, N), D, M = _dims(fn, q, v, 4)
+    _expect(fn, "k", k, q.shape, q.dtype)
+    _expect(fn, "v", v, (B, H, N, M), q.dtype)
+    _expect(fn, "g", g, (B, H, N), q.dtype)
+    _expect(fn, "dout", dout, (B, H, N, M), q.dtype)
+    for name, t in (("S0", S0), ("dS", dS), ("dS0", dS0)):
+        if t is not None:
+            _expect(fn, name, t, (B, H, D, M), f32)
+    if dS0 is not None and S0 is None:
+        raise ValueError(f"{fn}: dS0 without S0")
+    grads = {"dq": (dq, (B, H, N, D)), "dk": (dk, (B, H, N, D)), "dv": (dv, (B, H, N, M)),
+             "dg": (dg, (B, H, N))}
+    for name, (t, shape) in grads.items():
+        if t is not None:
+            _expect(fn, name, t, shape, q.dtype)
+    dt = _dtype_code(q)
+    _need_cuda(q, k, v, g, dout,
+               *[t for t in (S0, dS, dS0, dq, dk, dv, dg) if t is not None])
+    lib = load_library()
+    dev = q.device
+    dq, dk, dv, dg = (torch.empty(shape, dtype=q.dtype, device=dev) if t is None else t
+                      for t, shape in grads.values())
+    if S0 is not None and dS0 is None:
+        dS0 = torch.empty((B, H, D, M), dtype=f32, device=dev)
+    ws = _workspace(lib.la_gated_backward_workspace_bytes(B, H, N, D, M, dt), dev, workspace)
+    with _on_device(dev):
+        st = lib.la_backward_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                   dout.data_ptr(), 0 if S0 is None else S0.data_ptr(),
+                                   0 if dS is None else dS.data_ptr(), dq.data_ptr(),
+                                   dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
+                                   0 if dS0 is None else dS0.data_ptr(), B, H, N, D, M, dt,
+                                   ws.data_ptr(), ws.numel() * ws.element_size(),
+                                   _stream_ptr(dev))
+    _check(fn, st)
+    return (dq, dk, dv, dg) if S0 is None else (dq, dk, dv, dg, dS0)
+
+
+# ------------------------------------------- rotary positions, gated head norm
+
+def _need_rows(*ts, device):
+    """CUDA tensors on `device` whose last dimension is contiguous (the others strided)."""
+    for t in ts:
+        if not t.is_cuda:
+            raise ValueError("tensors must be on a CUDA device")
+        if t.device != device:
+            raise ValueError(f"tensors must all be on {device}, got one on {t.device}")
+
+
+def _row_strides(fn, name, t, written=False):
+    """The strides of [B,H,N,*] t's first three dimensions, for the library (0 where a dimension
+    has one entry); rows that are written must not overlap."""
+    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{fn}: {name}'s last dimension must be contiguous")
+    if written and t.numel():
+        reach = t.shape[-1]
+        for stride, size in sorted((st, n) for st, n in zip(t.stride()[:3], t.shape[:3]) if n > 1):
+            if stride < reach:
+                raise ValueError(f"{fn}: rows of {name} overlap in memory")
+            reach = stride * (size - 1) + reach
+    return (ctypes.c_longlong * 3)(*[st if n > 1 else 0 for st, n in zip(t.stride()[:3], t.shape[:3])])
+
+
+def la_rotary_freqs(rot_dim, base=10000.0, scaling=None, factor=1.0, original_len=None, slow=1.0,
+                    fast=32.0, device="cuda"):
+    """(freqs, mscale) for la_rotary: float64 [rot_dim/2] radians per token, base^(-2i/rot_dim),
+    for contexts `factor` times longer than those trained on by one of
+
+    scaling=None       as they are;
+    scaling="linear"   every frequency divided by factor (positions interpolated);
+    scaling="base"     base * factor^(rot_dim/(rot_dim-2)): the slowest pair is divided by
+                       factor, the fastest kept;
+    scaling="ramp"     pairs that make fewer than `slow` turns in original_len tokens divided
+                       by factor, those of more than `fast` turns kept, a linear ramp between;
+                       mscale = 0.1 ln(factor) + 1 (1 for the others).
+    """
+    import math
+    import torch
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("la_rotary_freqs: rot_dim must be even and at least 2")
+    if not base > 0 or not factor > 0:
+        raise ValueError("la_rotary_freqs: base and factor must be positive")
+    if scaling not in (None, "linear", "base", "ramp"):
+        raise ValueError(f"la_rotary_freqs: unknown scaling {scaling!r}")
+    mscale = 1.0
+    if scaling == "base" and rot_dim > 2:
+        base = base * factor ** (rot_dim / (rot_dim - 2.0))
+    freqs = torch.tensor([base ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)],
+                         dtype=torch.float64)
+    if scaling == "linear":
+        freqs = freqs / factor
+    elif scaling == "ramp":
+        if original_len is None or not fast > slow:
+            raise ValueError("la_rotary_freqs: a ramp needs original_len and slow < fast")
+        turns = original_len * freqs / (2.0 * math.pi)
+        keep = ((turns - slow) / (fast - slow)).clamp(0.0, 1.0)
+        freqs = freqs * keep + freqs / factor * (1.0 - keep)
+        mscale = 0.1 * math.log(factor) + 1.0
+    return freqs.to(device), mscale
+
+
+def la_rotary(q, k, freqs, positions=None, offset=0, interleaved=False, mscale=1.0, inverse=False,
+              q_out=None, k_out=None):
+    """q and k with the first 2 * len(freqs) elements of each head rotated by their positions.
+
+    q [B,H,N,D] and k [B,Hk,N,D] (or None), or packed [T,H,D] and [T,Hk,D]; any strides with a
+    contiguous last dimension. freqs: float64 [R/2] radians per token (la_rotary_freqs). Pairs
+    are elements (2i, 2i+1) if interleaved, else (i, i + R/2). positions: int32 [N] or [B,N]
+    (packed: [T]); None: offset, offset + 1, ... mscale scales the rotated elements. inverse
+    turns the other way: la_rotary(dq, dk, ..., inverse=True) is the gradient. Outputs may be
+    the inputs themselves. Returns (q_out, k_out), contiguous unless passed in."""
+    import torch
+    fn = "la_rotary"
+    dt = _dtype_code(q)
+    if q.dim() not in (3, 4):
+        raise ValueError(f"{fn}: q must have 3 or 4 dimensions")
+    packed = q.dim() == 3
+
+    def lead(t):  # [B, H, N, D]
+        return t.transpose(0, 1).unsqueeze(0) if packed else t
+
+    if k is not None:
+        hk = k.shape[1] if k.dim() == q.dim() else -1
+        _expect(fn, "k", k, (q.shape[0], hk, *q.shape[2:]), q.dtype)
+    elif k_out is not None:
+        raise ValueError(f"{fn}: k_out without k")
+    for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k)):
+        if t is not None:
+            _expect(fn, name, t, like.shape, q.dtype)
+    B, H, N, D = lead(q).shape
+    Hk = 0 if k is None else lead(k).shape[1]
+    if freqs.dim() != 1 or freqs.dtype != torch.float64 or not freqs.is_contiguous():
+        raise ValueError(f"{fn}: freqs must be a contiguous float64 tensor of R/2 entries")
+    pos_b = 0
+    if positions is not None:
+        if positions.dtype != torch.int32 or not positions.is_contiguous() \
+                or tuple(positions.shape) not in ({(N,)} if packed else {(N,), (B, N)}):
+            raise ValueError(f"{fn}: positions must be a contiguous int32 tensor of [N] or [B, N]")
+        pos_b = N if positions.dim() == 2 else 0
+    dev = q.device
+    qs = _row_strides(fn, "q", lead(q))
+    ks = None if k is None else _row_strides(fn, "k", lead(k))
+    if q_out is not None:
+        _row_strides(fn, "q_out", lead(q_out), written=True)
+    if k_out is not None:
+        _row_strides(fn, "k_out", lead(k_out), written=True)
+    _need_rows(*[t for t in (q, k, freqs, positions, q_out, k_out) if t is not None], device=dev)
+    lib = load_library()
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    qos = _row_strides(fn, "q_out", lead(q_out))
+    kos = None if k is None else _row_strides(fn, "k_out", lead(k_out))
+    with _on_device(dev):
+        st = lib.la_rotary(q.data_ptr(), qs, q_out.data_ptr(), qos,
+                           0 if k is None else k.data_ptr(), ks,
+                           0 if k is None else k_out.data_ptr(), kos, freqs.data_ptr(),
+                           0 if positions is None else positions.data_ptr(), pos_b, int(offset),
+                           B, H, Hk, N, D, 2 * freqs.numel(), int(bool(interleaved)),
+                           int(bool(inverse)), float(mscale), dt, _stream_ptr(dev))
+    _check(fn, st)
+    return q_out, k_out
+
+
+def la_norm_gate_workspace_bytes(B, H, N, M):
+    return load_library().la_norm_gate_workspace_bytes(B, H, N, M)
+
+
+def _norm_checks(fn, x, z, w):
+    if x.dim() != 4:
+        raise ValueError(f"{fn}: x must have 4 dimensions")
+    B, H, N, M = x.shape
+    _expect(fn, "z", z, x.shape, x.dtype)
+    if w.dim() not in (1, 2):
+        raise ValueError(f"{fn}: w must be [M] or [H, M]")
+    _expect(fn, "w", w, (M,) if w.dim() == 1 else (H, M), x.dtype)
+    return B, H, N, M, _dtype_code(x)
+
+
+def la_norm_gate(x, z, w, eps=1e-6, out=None):
+    """out = x / sqrt(mean(x^2) + eps) * w * z sigmoid(z), the mean over each head's M elements.
+
+    x [B,H,N,M] contiguous (la_forward_gated's output), w [M] or [H,M]; z and out [B,H,N,M] with
+    any strides that are multiples of 16 bytes and a contiguous last dimension, so that out can
+    be a token-major [B,N,H,M] buffer's transpose. out: contiguous unless passed in."""
+    import torch
+    fn = "la_norm_gate"
+    B, H, N, M, dt = _norm_checks(fn, x, z, w)
+    if out is not None:
+        _expect(fn, "out", out, x.shape, x.dtype)
+        _row_strides(fn, "out", out, written=True)
+    zs = _row_strides(fn, "z", z)
+    _need_cuda(x, w)
+    _need_rows(z, *([] if out is None else [out]), device=x.device)
+    lib = load_library()
+    dev = x.device
+    out = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+    with _on_device(dev):
+        st = lib.la_norm_gate(x.data_ptr(), z.data_ptr(), zs, w.data_ptr(), out.data_ptr(),
+                              _row_strides(fn, "out", out), B, H, N, M, int(w.dim() == 2),
+                              float(eps), dt, _stream_ptr(dev))
+    _check(fn, st)
+    return out
+
+
+def la_norm_gate_backward(x, z, w, dy, eps=1e-6, dx=None, dz=None, dw=None, workspace=None):
+    """Gradients (dx, dz, dw) of sum(dy * la_norm_gate(x, z, w, eps)), in the inputs' dtype; dw
+    has w's shape. dy and dz are strided as z is (dz: contiguous unless passed in)."""
+    import torch
+    fn = "la_norm_gate_backward"
+    B, H, N, M, dt = _norm_checks(fn, x, z, w)
+    _expect(fn, "dy", dy, x.shape, x.dtype)
+    for name, t, like in (("dx", dx, x), ("dz", dz, x), ("dw", dw, w)):
+        if t is not None:
+            _expect(fn, name, t, like.shape, x.dtype)
+    zs, dys = _row_strides(fn, "z", z), _row_strides(fn, "dy", dy)
+    if dz is not None:
+        _row_strides(fn, "dz", dz, written=True)
+    _need_cuda(x, w, *[t for t in (dx, dw) if t is not None])
+    _need_rows(z, dy, *([] if dz is None else [dz]), device=x.device)
+    lib = load_library()
+    dev = x.device
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if dx is None else dx
+    dz = torch.empty(x.shape, dtype=x.dtype, device=dev) if dz is None else dz
+    dw = torch.empty(w.shape, dtype=x.dtype, device=dev) if dw is None else dw
+    ws = _workspace(lib.la_norm_gate_workspace_bytes(B, H, N, M), dev, workspace)
+    with _on_device(dev):
+        st = lib.la_norm_gate_backward(x.data_ptr(), z.data_ptr(), zs, w.data_ptr(), dy.data_ptr(),
+                                       dys, dx.data_ptr(), dz.data_ptr(),
+                                       _row_strides(fn, "dz", dz), dw.data_ptr(), B, H, N, M,
+                                       int(w.dim() == 2), float(eps), dt, ws.data_ptr(),
+                                       ws.numel() * ws.element_size(), _stream_ptr(dev))
+    _check(fn, st)
+    return dx, dz, dw

@@ -1,0 +1,578 @@
+// Gated recurrence on CUDA cores (float32 or bf16, D and M multiples of 8 up to
+// 128), its scan over segments, and its decode step.
+//
+// One kernel carries every direction. With X a state and u, w, z three of the
+// inputs, it walks a segment's tokens updating X by an outer product and reading
+// it out along its columns:
+//   forward   X = a_t X + u_t w_t^T;  y_t = X z_t
+//   reverse   X = X + u_t w_t^T;  y_t = X z_t;  X = a_t X       (a_t = exp(g_t))
+//   out   forward, X = S^T:  u = v,    w = k,    z = q
+//   dq    forward, X = S:    u = k,    w = v,    z = dout
+//   dk    reverse, X = dS:   u = q,    w = dout, z = v
+//   dv    reverse, X = dS^T: u = dout, w = q,    z = k
+// (dS_t is the loss's gradient with respect to S_t: dS_t = q_t dout_t^T + a_{t+1}
+// dS_{t+1}.) The rows of X are independent of each other, so they are split over
+// threads and CTAs freely, and the sum over columns stays within a thread and its
+// neighbours.
+//
+// The token's own term is read out apart, y_t = X' z_t + u_t (w_t . z_t) with X' the
+// state without it.
+//
+// The decay's gradient is dg_t = <dS_t, a_t S_{t-1}>. Its differences are two dots,
+//   dg_t - dg_{t+1} = q_t . (a_t S_{t-1} dout_t) - k_t . (a_{t+1} dS_{t+1} v_t),
+// with the token's own term left out of both (it would cancel, and outweighs the rest
+// under a strong gate). So dg is a sum from a segment's last token back, begun there
+// with <a S, E> of the segment's two states. It restarts in every segment, so that
+// rounding errors do not pile up over the sequence.
+#include "la_gated.cuh"
+#include "la_tc_common.cuh"
+
+namespace la {
+namespace {
+
+using tcx::fma2;
+using tcx::mul2;
+
+constexpr int kThreads = 128;
+constexpr int kTok = 16;       // tokens staged at a time
+constexpr int kCols = 32;      // columns of X per thread
+
+struct RecurArgs {
+  const void *u, *w, *z, *g;
+  void* y;               // outputs [BH][N][NR] (nullptr: state pass)
+  const void* p;         // [BH][N][NR]: dots[rb][bh][t] = sum over rows of p (X' z) (nullptr: none)
+  float* dots;
+  const float* E;        // forward: ends[rb][bh][seg] = <X', E[seg + 1]> at the segment's last
+  float* ends;           //   token (nullptr: none)
+  int NR, NC, N, BH, len, n_seg;
+  const int* lens;
+  int H;
+  // states: element (r, c) of an entry at r * rs + c * cs
+  int rs, cs, DM;
+  const float* seg_in;   // per-segment entries the walk starts from (nullptr: `init`)
+  float* seg_out;        // state pass: per-segment entries it leaves
+  float* decay;          // state pass: exp(sum of g) per segment
+  const float* init;     // one segment: the caller's state (nullptr: zero)
+  float* fin;            // one segment: the caller's final state (nullptr: not kept)
+  GatedEntries entries;
+  WorkspaceHeader* hdr;
+};
+
+// CP threads share a row, each with 32 of its columns (c = 4 (i CP + p) + 0..3, so
+// that the lanes of a warp read neighbouring 16-byte words).
+// Bound by the packed multiply-adds: three for two state elements per token,
+// ~100 cycles a token for a 64 x 64 state on one CTA.
+template <typename T, int CP, bool REV>
+__global__ void __launch_bounds__(kThreads) gated_recur_kernel(const RecurArgs a) {
+  constexpr int RB = kThreads / CP;
+  __shared__ __align__(16) float sw[kTok][kCols * CP], sz[kTok][kCols * CP];
+  __shared__ float su[kTok][RB], sy[kTok][RB + 1], sa[kTok], swz[kTok];
+  const int tid = threadIdx.x, part = tid % CP, row = tid / CP;
+  const int bh = blockIdx.x / a.n_seg, seg = blockIdx.x % a.n_seg;
+  const int r0 = blockIdx.y * RB, nr = min(RB, a.NR - r0);
+  const int n = gated_length(a.lens, a.H, bh, a.N);
+  const int tb = min(seg * a.len, n), te = min(tb + a.len, n);
+  const size_t seq = (size_t)bh * a.N;
+  const T* u = static_cast<const T*>(a.u) + seq * a.NR + r0;
+  const T* w = static_cast<const T*>(a.w) + seq * a.NC;
+  const T* z = static_cast<const T*>(a.z) + seq * a.NC;
+  const T* g = static_cast<const T*>(a.g) + seq;
+  T* y = static_cast<T*>(a.y) + (a.y ? seq * a.NR + r0 : 0);
+
+  const long long entry = a.entries.at(bh);
+  if (entry < 0 && seg == 0 && blockIdx.y == 0 && tid == 0 && a.hdr)
+    a.hdr->status = LA_ERR_INVALID_ARG;
+  const float* xin = nullptr;
+  if (a.seg_in)
+    xin = a.seg_in + ((size_t)bh * (a.n_seg + 1) + seg + (REV ? 1 : 0)) * a.DM;
+  else if (a.init && entry >= 0)
+    xin = a.init + (size_t)entry * a.DM;
+  float2 x[kCols / 2];
+#pragma unroll
+  for (int i = 0; i < kCols / 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = 4 * (i * CP + part) + j;
+      const bool in = xin && row < nr && c < a.NC;
+      (&x[2 * i + j / 2].x)[j % 2] = in ? xin[(size_t)(r0 + row) * a.rs + (size_t)c * a.cs] : 0.f;
+    }
+
+  float decay = 1.f, end = 0.f;
+  for (int done = 0; done < te - tb; done += kTok) {
+    const int m = min(kTok, te - tb - done);
+    const int t0 = REV ? te - done - m : tb + done;
+    __syncthreads();
+    for (int i = tid; i < kTok * kCols * CP; i += kThreads) {
+      const int t = i / (kCols * CP), c = i % (kCols * CP);
+      const bool in = t < m && c < a.NC;
+      sw[t][c] = in ? to_f32<T>(w[(size_t)(t0 + t) * a.NC + c]) : 0.f;
+      if (a.y) sz[t][c] = in ? to_f32<T>(z[(size_t)(t0 + t) * a.NC + c]) : 0.f;
+    }
+    for (int i = tid; i < kTok * RB; i += kThreads) {
+      const int t = i / RB, r = i % RB;
+      su[t][r] = t < m && r < nr ? to_f32<T>(u[(size_t)(t0 + t) * a.NR + r]) : 0.f;
+    }
+    if (tid < kTok) sa[tid] = tid < m ? gated_decay(to_f32<T>(g[t0 + tid])) : 1.f;
+    __syncthreads();
+    if (a.y) {  // w_t . z_t, eight threads a token
+      float s = 0.f;
+      for (int c = tid % 8; c < a.NC; c += 8) s = fmaf(sw[tid / 8][c], sz[tid / 8][c], s);
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (tid % 8 == 0) swz[tid / 8] = s;
+    }
+    for (int k = 0; k < m; ++k) {
+      const int t = REV ? m - 1 - k : k;
+      const float at = sa[t], ut = su[t][row];
+      const float2 a2 = make_float2(at, at), u2 = make_float2(ut, ut);
+      if (!REV && a.E && t0 + t == te - 1) {
+        const float* E = a.E + ((size_t)bh * (a.n_seg + 1) + seg + 1) * a.DM;
+        if (row < nr)
+#pragma unroll
+          for (int i = 0; i < kCols / 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int c = 4 * (i * CP + part) + j;
+              if (c < a.NC)
+                end = fmaf(at * (&x[2 * i + j / 2].x)[j % 2],
+                           E[(size_t)(r0 + row) * a.rs + (size_t)c * a.cs], end);
+            }
+      }
+      float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kCols / 4; ++i) {
+        const int c = 4 * (i * CP + part);
+        const float4 wv = *reinterpret_cast<const float4*>(&sw[t][c]);
+        if (!REV) {
+          x[2 * i] = mul2(a2, x[2 * i]);
+          x[2 * i + 1] = mul2(a2, x[2 * i + 1]);
+        }
+        if (a.y) {
+          const float4 zv = *reinterpret_cast<const float4*>(&sz[t][c]);
+          s2 = fma2(x[2 * i], make_float2(zv.x, zv.y), s2);
+          s2 = fma2(x[2 * i + 1], make_float2(zv.z, zv.w), s2);
+        }
+        x[2 * i] = fma2(u2, make_float2(wv.x, wv.y), x[2 * i]);
+        x[2 * i + 1] = fma2(u2, make_float2(wv.z, wv.w), x[2 * i + 1]);
+        if (REV) {
+          x[2 * i] = mul2(a2, x[2 * i]);
+          x[2 * i + 1] = mul2(a2, x[2 * i + 1]);
+        }
+      }
+      decay *= at;
+      if (a.y) {
+        float s = s2.x + s2.y;
+#pragma unroll
+        for (int o = 1; o < CP; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (part == 0) sy[t][row] = s;
+      }
+    }
+    if (a.y) {
+      __syncthreads();
+      for (int i = tid; i < m * RB; i += kThreads) {
+        const int t = i / RB, r = i % RB;
+        if (r < nr) y[(size_t)(t0 + t) * a.NR + r] = from_f32<T>(fmaf(su[t][r], swz[t], sy[t][r]));
+      }
+      if (a.p) {
+        const T* p = static_cast<const T*>(a.p) + seq * a.NR + r0;
+        const int t = tid / 8;
+        float s = 0.f;
+        if (t < m)
+          for (int r = tid % 8; r < nr; r += 8)
+            s += sy[t][r] * to_f32<T>(p[(size_t)(t0 + t) * a.NR + r]);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (t < m && tid % 8 == 0)
+          a.dots[((size_t)blockIdx.y * a.BH + bh) * a.N + t0 + t] = s;
+      }
+    }
+  }
+
+  if (!REV && a.E) {
+    for (int o = 16; o > 0; o >>= 1) end += __shfl_xor_sync(0xffffffffu, end, o);
+    __syncthreads();
+    if (tid % 32 == 0) sa[tid / 32] = end;
+    __syncthreads();
+    if (tid == 0)
+      a.ends[((size_t)blockIdx.y * a.BH + bh) * a.n_seg + seg] = sa[0] + sa[1] + sa[2] + sa[3];
+  }
+
+  float* xout = nullptr;
+  if (a.seg_out)
+    xout = a.seg_out + ((size_t)bh * (a.n_seg + 1) + seg) * a.DM;
+  else if (a.fin && entry >= 0)
+    xout = a.fin + (size_t)entry * a.DM;
+  if (xout && row < nr)
+#pragma unroll
+    for (int i = 0; i < kCols / 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = 4 * (i * CP + part) + j;
+        if (c < a.NC) xout[(size_t)(r0 + row) * a.rs + (size_t)c * a.cs] = (&x[2 * i + j / 2].x)[j % 2];
+      }
+  if (a.decay && blockIdx.y == 0 && tid == 0) a.decay[(size_t)bh * a.n_seg + seg] = decay;
+}
+
+// Joins the segments: forward X[s + 1] = decay[s] X[s] + U[s] from X[0] = init,
+// reverse X[s] = decay[s] X[s + 1] + U[s] from X[n_seg] = init; U[s] is read from
+// entry s and replaced there. One thread per state element.
+__global__ void __launch_bounds__(256)
+gated_scan_kernel(float* X, const float* __restrict__ decay, const float* init, float* fin,
+                  const GatedEntries entries, int n_seg, int DM, bool reverse,
+                  WorkspaceHeader* hdr) {
+  const int bh = blockIdx.x;
+  const int i = blockIdx.y * 256 + threadIdx.x;
+  const long long entry = entries.at(bh);
+  if (entry < 0 && i == 0) hdr->status = LA_ERR_INVALID_ARG;
+  if (i >= DM) return;
+  float* x = X + (size_t)bh * (n_seg + 1) * DM + i;
+  const float* dec = decay + (size_t)bh * n_seg;
+  float s = init && entry >= 0 ? init[(size_t)entry * DM + i] : 0.f;
+  if (reverse) {
+    float u = x[(size_t)(n_seg - 1) * DM];
+    x[(size_t)n_seg * DM] = s;
+    for (int k = n_seg - 1; k >= 0; --k) {
+      const float next = k > 0 ? x[(size_t)(k - 1) * DM] : 0.f;
+      s = fmaf(dec[k], s, u);
+      x[(size_t)k * DM] = s;
+      u = next;
+    }
+  } else {
+    float u = x[0];
+    for (int k = 0; k < n_seg; ++k) {
+      const float next = k + 1 < n_seg ? x[(size_t)(k + 1) * DM] : 0.f;
+      x[(size_t)k * DM] = s;
+      s = fmaf(dec[k], s, u);
+      u = next;
+    }
+    x[(size_t)n_seg * DM] = s;
+  }
+  if (fin && entry >= 0) fin[(size_t)entry * DM + i] = s;
+}
+
+// dg of one segment: from <X', E> at its last token back,
+//   dg_t = <X', E> + sum over s >= t of dot_q[s] - sum over t <= s < last of dot_k[s],
+// 256 tokens at a time (each dot the sum of its row blocks').
+template <typename T>
+__global__ void __launch_bounds__(256)
+gated_dg_kernel(const float* __restrict__ ends, const float* __restrict__ dot_q,
+                const float* __restrict__ dot_k, T* __restrict__ dg, int BH, int N, int len,
+                int n_seg, int rb) {
+  __shared__ float part[8];
+  const int bh = blockIdx.x / n_seg, seg = blockIdx.x % n_seg, tid = threadIdx.x;
+  const int tb = seg * len, te = min(tb + len, N);
+  float carry = 0.f;
+  for (int r = 0; r < rb; ++r) carry += ends[((size_t)r * BH + bh) * n_seg + seg];
+  for (int hi = te; hi > tb; hi -= 256) {
+    const int t = hi - 1 - tid;
+    float s = 0.f;
+    if (t >= tb) {
+      for (int r = 0; r < rb; ++r) s += dot_q[((size_t)r * BH + bh) * N + t];
+      float k = 0.f;
+      if (t < te - 1)
+        for (int r = 0; r < rb; ++r) k += dot_k[((size_t)r * BH + bh) * N + t];
+      s -= k;
+    }
+    for (int o = 1; o < 32; o <<= 1) {
+      const float other = __shfl_up_sync(0xffffffffu, s, o);
+      if (tid % 32 >= o) s += other;
+    }
+    __syncthreads();
+    if (tid % 32 == 31) part[tid / 32] = s;
+    __syncthreads();
+    float before = carry;
+    for (int i = 0; i < tid / 32; ++i) before += part[i];
+    if (t >= tb) dg[(size_t)bh * N + t] = from_f32<T>(before + s);
+    for (int i = 0; i < 8; ++i) carry += part[i];
+  }
+}
+
+template <typename T, bool REV>
+cudaError_t launch_recur(const RecurArgs& a, cudaStream_t st) {
+  const int cp = a.NC <= kCols ? 1 : a.NC <= 2 * kCols ? 2 : 4;
+  const int rb = kThreads / cp;
+  const dim3 grid((unsigned)(a.BH * a.n_seg), (unsigned)((a.NR + rb - 1) / rb));
+  if (cp == 1)
+    gated_recur_kernel<T, 1, REV><<<grid, kThreads, 0, st>>>(a);
+  else if (cp == 2)
+    gated_recur_kernel<T, 2, REV><<<grid, kThreads, 0, st>>>(a);
+  else
+    gated_recur_kernel<T, 4, REV><<<grid, kThreads, 0, st>>>(a);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+int row_blocks(int NR, int NC) {
+  const int rb = kThreads / (NC <= kCols ? 1 : NC <= 2 * kCols ? 2 : 4);
+  return (NR + rb - 1) / rb;
+}
+
+// Segments of the CUDA-core path: enough CTAs to give each of the 152 SMs four
+// (latency-bound walks overlap), but at least 64 tokens each, since a segment costs
+// a state pass and a scan step; a backward's at most 512, over which dg's sum from
+// the segment's end back keeps float32's accuracy.
+GatedPlan plan_simt(int BH, int N, int D, int M, bool backward) {
+  const long long per = (long long)BH * row_blocks(M, D);
+  long long n_seg = (4 * 152 + per - 1) / per;
+  const long long most = (N + 63) / 64;
+  if (n_seg > most) n_seg = most;
+  if (backward && n_seg < (N + 511) / 512) n_seg = (N + 511) / 512;
+  if (n_seg < 1) n_seg = 1;
+  const int len = (int)(((N + n_seg - 1) / n_seg + kTok - 1) / kTok * kTok);
+  return GatedPlan{BH, N, len > 0 ? len : kTok, N > 0 ? (N + len - 1) / len : 1};
+}
+
+GatedWorkspace carve(void* ws, const GatedPlan& p, int D, int M, bool backward, int dots) {
+  GatedWorkspace w{};
+  const uintptr_t base = reinterpret_cast<uintptr_t>(ws);
+  size_t at = kHeaderBytes;
+  const size_t dm = (size_t)D * M, seq = (size_t)p.BH;
+  auto take = [&](size_t floats) {
+    float* r = reinterpret_cast<float*>(base + at);
+    at += align_up(sizeof(float) * floats, 256);
+    return r;
+  };
+  w.hdr = static_cast<WorkspaceHeader*>(ws);
+  if (backward || p.n_seg > 1) {
+    w.decay = take(seq * p.n_seg);
+    w.S = take(seq * (p.n_seg + 1) * dm);
+  }
+  if (backward) {
+    w.E = take(seq * (p.n_seg + 1) * dm);
+    w.dot_q = take((size_t)dots * seq * p.N);
+    w.dot_k = take((size_t)dots * seq * p.N);
+    w.ends = take((size_t)dots * seq * p.n_seg);
+  }
+  w.bytes = at;
+  return w;
+}
+
+template <typename T>
+cudaError_t simt_forward_t(const GatedForward& f, void* ws, cudaStream_t st) {
+  const GatedPlan p = plan_simt(f.B * f.H, f.N, f.D, f.M, false);
+  const GatedWorkspace w = carve(ws, p, f.D, f.M, false, 0);
+  RecurArgs a{};
+  a.g = f.g;
+  a.N = f.N;
+  a.BH = p.BH;
+  a.len = p.len;
+  a.n_seg = p.n_seg;
+  a.lens = f.lens;
+  a.H = f.H;
+  a.DM = f.D * f.M;
+  a.entries = GatedEntries{f.slots, f.pool, f.H};
+  a.hdr = w.hdr;
+  cudaError_t e;
+  if (p.n_seg > 1) {
+    RecurArgs s = a;  // X = S: rows d
+    s.u = f.k;
+    s.w = f.v;
+    s.z = f.v;
+    s.NR = f.D;
+    s.NC = f.M;
+    s.rs = f.M;
+    s.cs = 1;
+    s.seg_out = w.S;
+    s.decay = w.decay;
+    if ((e = launch_recur<T, false>(s, st)) != cudaSuccess) return e;
+    if ((e = gated_scan(p, w, false, f.S0, f.S, a.entries, a.DM, st)) != cudaSuccess) return e;
+    a.seg_in = w.S;
+  } else {
+    a.init = f.S0;
+    a.fin = f.S;
+  }
+  a.u = f.v;  // X = S^T: rows m
+  a.w = f.k;
+  a.z = f.q;
+  a.y = f.out;
+  a.NR = f.M;
+  a.NC = f.D;
+  a.rs = 1;
+  a.cs = f.M;
+  return launch_recur<T, false>(a, st);
+}
+
+template <typename T>
+cudaError_t simt_backward_t(const GatedBackward& f, void* ws, cudaStream_t st) {
+  const GatedPlan p = plan_simt(f.B * f.H, f.N, f.D, f.M, true);
+  const int rb_dm = row_blocks(f.D, f.M);  // rows d: S, dS
+  const GatedWorkspace w = carve(ws, p, f.D, f.M, true, rb_dm);
+  RecurArgs a{};
+  a.g = f.g;
+  a.N = f.N;
+  a.BH = p.BH;
+  a.len = p.len;
+  a.n_seg = p.n_seg;
+  a.H = f.H;
+  a.DM = f.D * f.M;
+  a.entries = GatedEntries{nullptr, 0, f.H};
+  RecurArgs rows_d = a;
+  rows_d.NR = f.D;
+  rows_d.NC = f.M;
+  rows_d.rs = f.M;
+  rows_d.cs = 1;
+  cudaError_t e;
+  RecurArgs s = rows_d;  // the segments' own states and gradients
+  s.u = f.k;
+  s.w = s.z = f.v;
+  s.seg_out = w.S;
+  s.decay = w.decay;
+  if ((e = launch_recur<T, false>(s, st)) != cudaSuccess) return e;
+  s.u = f.q;
+  s.w = s.z = f.dout;
+  s.seg_out = w.E;
+  s.decay = nullptr;
+  if ((e = launch_recur<T, true>(s, st)) != cudaSuccess) return e;
+  if ((e = gated_scan(p, w, false, f.S0, nullptr, a.entries, a.DM, st)) != cudaSuccess) return e;
+  if ((e = gated_scan(p, w, true, f.dS, f.dS0, a.entries, a.DM, st)) != cudaSuccess) return e;
+  RecurArgs dq = rows_d;
+  dq.u = f.k;
+  dq.w = f.v;
+  dq.z = f.dout;
+  dq.y = f.dq;
+  dq.p = f.q;
+  dq.dots = w.dot_q;
+  dq.E = w.E;
+  dq.ends = w.ends;
+  dq.seg_in = w.S;
+  if ((e = launch_recur<T, false>(dq, st)) != cudaSuccess) return e;
+  RecurArgs dk = rows_d;
+  dk.u = f.q;
+  dk.w = f.dout;
+  dk.z = f.v;
+  dk.y = f.dk;
+  dk.p = f.k;
+  dk.dots = w.dot_k;
+  dk.seg_in = w.E;
+  if ((e = launch_recur<T, true>(dk, st)) != cudaSuccess) return e;
+  RecurArgs dv = a;  // rows m: dS^T
+  dv.u = f.dout;
+  dv.w = f.q;
+  dv.z = f.k;
+  dv.y = f.dv;
+  dv.NR = f.M;
+  dv.NC = f.D;
+  dv.rs = 1;
+  dv.cs = f.M;
+  dv.seg_in = w.E;
+  if ((e = launch_recur<T, true>(dv, st)) != cudaSuccess) return e;
+  gated_dg_kernel<T><<<(unsigned)(p.BH * p.n_seg), 256, 0, st>>>(
+      w.ends, w.dot_q, w.dot_k, static_cast<T*>(f.dg), p.BH, p.N, p.len, p.n_seg, rb_dm);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+// Decode step: one CTA per (stream, head). Bound by the state's read and write
+// (2 D M 4 bytes); a thread owns a float4 column group in every rgs-th row, and asks
+// for up to eight of its rows before it uses the first.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+gated_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                    const T* __restrict__ g, float* S, T* __restrict__ out,
+                    const GatedEntries entries, int D, int M) {
+  __shared__ float fq[128], fk[128];
+  __shared__ __align__(16) float vs[128];
+  __shared__ __align__(16) float red[kThreads * 4];
+  const size_t sh = blockIdx.x;
+  const int tid = threadIdx.x;
+  const long long entry = entries.at((int)sh);
+  const int cg = M >> 2, rgs = kThreads / cg, col = tid % cg, rg = tid / cg;
+  float4* S4 = reinterpret_cast<float4*>(S + (size_t)(entry < 0 ? 0 : entry) * D * M);
+  constexpr int kBatch = 8;
+  float4 s[kBatch];
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) {
+    const int d = rg + j * rgs;
+    s[j] = entry >= 0 && rg < rgs && d < D ? S4[d * cg + col] : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  const float a = gated_decay(to_f32<T>(g[sh]));
+  if (tid < D) {
+    fq[tid] = to_f32<T>(q[sh * D + tid]);
+    fk[tid] = to_f32<T>(k[sh * D + tid]);
+  }
+  if (tid < M) vs[tid] = to_f32<T>(v[sh * M + tid]);
+  __syncthreads();
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (rg < rgs) {
+    const float4 v4 = *reinterpret_cast<const float4*>(&vs[4 * col]);
+    for (int d0 = rg; d0 < D; d0 += kBatch * rgs) {
+      if (d0 != rg)
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int d = d0 + j * rgs;
+          s[j] = entry >= 0 && d < D ? S4[d * cg + col] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int d = d0 + j * rgs;
+        if (d >= D) break;
+        const float kd = fk[d], qd = fq[d];
+        s[j].x = fmaf(a, s[j].x, kd * v4.x);
+        s[j].y = fmaf(a, s[j].y, kd * v4.y);
+        s[j].z = fmaf(a, s[j].z, kd * v4.z);
+        s[j].w = fmaf(a, s[j].w, kd * v4.w);
+        if (entry >= 0) S4[d * cg + col] = s[j];
+        acc.x = fmaf(qd, s[j].x, acc.x);
+        acc.y = fmaf(qd, s[j].y, acc.y);
+        acc.z = fmaf(qd, s[j].z, acc.z);
+        acc.w = fmaf(qd, s[j].w, acc.w);
+      }
+    }
+    *reinterpret_cast<float4*>(&red[rg * M + 4 * col]) = acc;
+  }
+  __syncthreads();
+  if (tid < M) {
+    float o = 0.f;
+    for (int r = 0; r < rgs; ++r) o += red[r * M + tid];
+    out[sh * M + tid] = from_f32<T>(o);
+  }
+}
+
+}  // namespace
+
+cudaError_t gated_scan(const GatedPlan& p, const GatedWorkspace& w, bool reverse, const float* init,
+                       float* fin, const GatedEntries& e, int DM, cudaStream_t st) {
+  gated_scan_kernel<<<dim3(p.BH, (DM + 255) / 256), 256, 0, st>>>(
+      reverse ? w.E : w.S, w.decay, init, fin, e, p.n_seg, DM, reverse, w.hdr);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+size_t gated_forward_workspace(int BH, int N, int D, int M, int dtype) {
+  (void)dtype;
+  return carve(nullptr, plan_simt(BH, N, D, M, false), D, M, false, 0).bytes;
+}
+
+size_t gated_backward_workspace(int BH, int N, int D, int M, int dtype) {
+  (void)dtype;
+  return carve(nullptr, plan_simt(BH, N, D, M, true), D, M, true, row_blocks(D, M)).bytes;
+}
+
+cudaError_t gated_forward(const GatedForward& f, void* ws, cudaStream_t st) {
+  return f.dtype == LA_F32 ? simt_forward_t<float>(f, ws, st)
+                           : simt_forward_t<__nv_bfloat16>(f, ws, st);
+}
+
+cudaError_t gated_backward(const GatedBackward& f, void* ws, cudaStream_t st) {
+  return f.dtype == LA_F32 ? simt_backward_t<float>(f, ws, st)
+                           : simt_backward_t<__nv_bfloat16>(f, ws, st);
+}
+
+cudaError_t gated_decode(const void* q, const void* k, const void* v, const void* g, float* S,
+                         const int* slots, void* out, int pool, int n_streams, int H, int D, int M,
+                         int dtype, cudaStream_t st) {
+  const GatedEntries e{slots, pool, H};
+  const unsigned n = (unsigned)(n_streams * H);
+  if (dtype == LA_F32)
+    gated_decode_kernel<float><<<n, kThreads, 0, st>>>((const float*)q, (const float*)k,
+                                                      (const float*)v, (const float*)g, S,
+                                                      (float*)out, e, D, M);
+  else
+    gated_decode_kernel<__nv_bfloat16><<<n, kThreads, 0, st>>>(
+        (const __nv_bfloat16*)q, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v,
+        (const __nv_bfloat16*)g, S, (__nv_bfloat16*)out, e, D, M);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace la

@@ -119,4 +119,60 @@ cudaError_t rff_forward(const void* q, const void* k, const void* v, const void*
 cudaError_t decode_step(const void* q, const void* k, const void* v, float* S, float* Z, void* out,
                         int n_sh, int D, int M, int dtype, cudaStream_t st);
 
+// ---- gated recurrence: S_t = exp(g_t) S_{t-1} + k_t v_t^T, out_t = S_t^T q_t
+// S0 / S: the states before the first and after the last token, [BH][D][M] or entries of a
+// pool named by slots (int[B]; nullptr: entry bh); either may be nullptr, and they may be the
+// same memory. lens: int[B], token counts (nullptr: all N).
+struct GatedForward {
+  const void *q, *k, *v, *g;
+  void* out;
+  const float* S0;
+  float* S;
+  const int *slots, *lens;
+  int pool, B, H, N, D, M, dtype;
+};
+// dS: the gradient with respect to the final state (nullptr: zero), dS0: with respect to the
+// initial one (nullptr: not wanted).
+struct GatedBackward {
+  const void *q, *k, *v, *g, *dout;
+  const float *S0, *dS;
+  void *dq, *dk, *dv, *dg;
+  float* dS0;
+  int B, H, N, D, M, dtype;
+};
+size_t gated_forward_workspace(int BH, int N, int D, int M, int dtype);
+cudaError_t gated_forward(const GatedForward& f, void* ws, cudaStream_t st);
+size_t gated_backward_workspace(int BH, int N, int D, int M, int dtype);
+cudaError_t gated_backward(const GatedBackward& f, void* ws, cudaStream_t st);
+cudaError_t gated_decode(const void* q, const void* k, const void* v, const void* g, float* S,
+                         const int* slots, void* out, int pool, int n_streams, int H, int D, int M,
+                         int dtype, cudaStream_t st);
+
+// ---- rotary positions on q and (Hk > 0) k; strides in elements: batch, head, token
+struct Rotary {
+  const void *q, *k;
+  void *q_out, *k_out;
+  const long long *q_strides, *q_out_strides, *k_strides, *k_out_strides;
+  const double* freqs;
+  const int* positions;  // nullptr: offset + t
+  long long pos_stride_b, offset;
+  int B, H, Hk, N, D, R, dtype;
+  bool interleaved, inverse;
+  float mscale;
+};
+cudaError_t rotary(const Rotary& r, cudaStream_t st);
+
+// ---- gated head norm y = x / rms(x) * w * silu(z); x, dx [B][H][N][M], the others strided
+struct NormGate {
+  const void *x, *z, *w, *dy;
+  void *y, *dx, *dz, *dw;
+  const long long *z_strides, *y_strides, *dy_strides, *dz_strides;
+  int B, H, N, M, dtype;
+  bool w_per_head;
+  float eps;
+};
+size_t norm_gate_workspace(int B, int H, int N, int M);
+cudaError_t norm_gate(const NormGate& n, cudaStream_t st);
+cudaError_t norm_gate_backward(const NormGate& n, void* ws, cudaStream_t st);
+
 }  // namespace la

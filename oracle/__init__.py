@@ -10,8 +10,17 @@ brute force, the degree-2 polynomial special case, or central finite
 differences): elu_plus_one, elu_plus_one_grad, masked_attention,
 masked_attention_rows, linearized_attention, recurrent_attention, forward, prefill, decode_step,
 backward, denominators, poly2_feature, random_fourier_feature. No function here is parity
-unpinned.
+unpinned. gated_forward, gated_backward, rotary, norm_gate and norm_gate_backward are pinned
+in ``tests/test_gated_oracle.py``.
 """
+
+from .gated import (  # noqa: F401
+    gated_backward,
+    gated_forward,
+    norm_gate,
+    norm_gate_backward,
+    rotary,
+)
 
 from .linear_attention import (  # noqa: F401
     backward,
