@@ -25,6 +25,7 @@
 // with <a S, E> of the segment's two states. It restarts in every segment, so that
 // rounding errors do not pile up over the sequence.
 #include "la_gated.cuh"
+#include "la_gated_mma.cuh"
 #include "la_tc_common.cuh"
 
 namespace la {
@@ -347,8 +348,7 @@ GatedWorkspace carve(void* ws, const GatedPlan& p, int D, int M, bool backward, 
   return w;
 }
 
-template <typename T>
-cudaError_t simt_forward_t(const GatedForward& f, void* ws, cudaStream_t st) {
+cudaError_t simt_forward(const GatedForward& f, void* ws, cudaStream_t st) {
   const GatedPlan p = plan_simt(f.B * f.H, f.N, f.D, f.M, false);
   const GatedWorkspace w = carve(ws, p, f.D, f.M, false, 0);
   RecurArgs a{};
@@ -374,7 +374,7 @@ cudaError_t simt_forward_t(const GatedForward& f, void* ws, cudaStream_t st) {
     s.cs = 1;
     s.seg_out = w.S;
     s.decay = w.decay;
-    if ((e = launch_recur<T, false>(s, st)) != cudaSuccess) return e;
+    if ((e = launch_recur<float, false>(s, st)) != cudaSuccess) return e;
     if ((e = gated_scan(p, w, false, f.S0, f.S, a.entries, a.DM, st)) != cudaSuccess) return e;
     a.seg_in = w.S;
   } else {
@@ -389,7 +389,7 @@ cudaError_t simt_forward_t(const GatedForward& f, void* ws, cudaStream_t st) {
   a.NC = f.D;
   a.rs = 1;
   a.cs = f.M;
-  return launch_recur<T, false>(a, st);
+  return launch_recur<float, false>(a, st);
 }
 
 template <typename T>
@@ -538,9 +538,13 @@ cudaError_t gated_scan(const GatedPlan& p, const GatedWorkspace& w, bool reverse
   return cudaGetLastError();
 }
 
+// bf16 runs on tensor cores, float32 (which they would round) on CUDA cores.
+static GatedPlan forward_plan(int BH, int N, int D, int M, int dtype) {
+  return dtype == LA_BF16 ? gated_mma_forward_plan(BH, N, D, M) : plan_simt(BH, N, D, M, false);
+}
+
 size_t gated_forward_workspace(int BH, int N, int D, int M, int dtype) {
-  (void)dtype;
-  return carve(nullptr, plan_simt(BH, N, D, M, false), D, M, false, 0).bytes;
+  return carve(nullptr, forward_plan(BH, N, D, M, dtype), D, M, false, 0).bytes;
 }
 
 size_t gated_backward_workspace(int BH, int N, int D, int M, int dtype) {
@@ -549,8 +553,9 @@ size_t gated_backward_workspace(int BH, int N, int D, int M, int dtype) {
 }
 
 cudaError_t gated_forward(const GatedForward& f, void* ws, cudaStream_t st) {
-  return f.dtype == LA_F32 ? simt_forward_t<float>(f, ws, st)
-                           : simt_forward_t<__nv_bfloat16>(f, ws, st);
+  if (f.dtype == LA_F32) return simt_forward(f, ws, st);
+  const GatedPlan p = forward_plan(f.B * f.H, f.N, f.D, f.M, f.dtype);
+  return gated_mma_forward(f, carve(ws, p, f.D, f.M, false, 0), st);
 }
 
 cudaError_t gated_backward(const GatedBackward& f, void* ws, cudaStream_t st) {

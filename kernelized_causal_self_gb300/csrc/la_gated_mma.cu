@@ -1,0 +1,377 @@
+// Gated recurrence in bf16 on tensor cores: forward, and the states of segments.
+//
+// A chunk of 64 tokens is a masked product and a rank-64 update. With G_i the sum of
+// the chunk's g up to and including token i, G the whole chunk's, L_ij = exp(G_i - G_j)
+// for j <= i and 0 above:
+//   O = diag(exp(G_i)) (Q S) + ((Q K^T) * L) V
+//   S = exp(G) S + (diag(exp(G - G_j)) K)^T V
+// All exponents are <= 0 for g <= 0, so nothing overflows, and sums that reach a
+// weight are taken from the end that weight decays from (G - G_j as a sum from the
+// chunk's end), so that a strong gate elsewhere in the chunk costs no digits.
+//
+// Four warps share a chunk: warp r has its rows 16 r.. of Q and O and rows 16 r.. of
+// S (of each 64), S in float32 accumulators that stay in registers over the whole
+// segment. What is rounded to bf16: Q K^T * L as an operand, and the copy of S in
+// shared memory that Q multiplies; the outputs, bf16 too, cannot show more. The update
+// of S takes K's weighted rows as two bf16 terms (16 bits), since S itself is summed
+// over the whole sequence and may be returned in float32.
+//
+// Why warp-level products and not tcgen05: at 64 columns a chunk's products are small
+// next to its element-wise work (masks, weights, splits), which here happens in the
+// registers that hold the fragments, with no round trip through tensor memory, no
+// barrier between the product and its use, and three CTAs of four warps per SM to
+// hide one another's waits. The products of the longest case take ~31 us of the
+// tensor pipe at the 600 TFLOP/s these instructions reach; reading and writing
+// q, k, v and out takes 40 us.
+#include "la_gated.cuh"
+#include "la_gated_mma.cuh"
+#include "la_mma.cuh"
+#include "la_tc_common.cuh"
+
+namespace la {
+
+using namespace mma;
+
+namespace {
+
+constexpr int kThreads = 128;
+
+struct FwdArgs {
+  const bf16 *q, *k, *v, *g;  // state pass: k, v are the pair whose outer products are summed
+  bf16* out;
+  int D, M, N, len, n_seg;
+  const int* lens;
+  int H;
+  const float* seg_in;
+  float *seg_out, *decay;
+  const float* init;
+  float* fin;
+  GatedEntries entries;
+  WorkspaceHeader* hdr;
+};
+
+template <int DZ, bool OUT>
+struct FwdSmem {
+  static constexpr int kQ = OUT ? kC * DZ * 2 : 0, kK = kC * DZ * 2, kV = kC * 64 * 2;
+  static constexpr int kStage = kQ + kK + kV;
+  static constexpr int kS = OUT ? DZ * 64 * 2 : 0;  // S in bf16, [d][m], one of two
+  static constexpr int kBytes = 2 * kStage + 2 * kS + 4 * kC * 4 * 2;
+};
+
+// OUT: outputs (and, with one segment, the final state). Otherwise the state pass: the
+// segment's own S from zero, over k, v with weights exp(G - G_j), or (REV) its own
+// gradient of the incoming state from zero, over q, dout with weights exp(G_i), chunks
+// from the last to the first.
+template <int DZ, bool OUT, bool REV>
+__global__ void __launch_bounds__(kThreads, DZ == 64 ? 3 : 2) gated_chunk_kernel(const FwdArgs a) {
+  using Sm = FwdSmem<DZ, OUT>;
+  constexpr int KS = DZ / 16, DT = DZ / 64;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const uint32_t base = tc::smem_u32(smem);
+  const uint32_t s_op = base + 2 * Sm::kStage;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float* Gs = reinterpret_cast<float*>(smem + 2 * Sm::kStage + 2 * Sm::kS) + warp * 2 * kC;
+  float* Ws = Gs + kC;
+
+  tc::pdl_wait();
+  const int bh = blockIdx.x / a.n_seg, seg = blockIdx.x % a.n_seg;
+  const int m0 = blockIdx.y * 64;
+  // the causal product gives a chunk's last rows the most work: turn the rows' order
+  // from CTA to CTA, so that no scheduler gets all of them
+  const int rb = (warp + blockIdx.x) & 3;
+  const int n = gated_length(a.lens, a.H, bh, a.N);
+  const int tb = min(seg * a.len, n), te = min(tb + a.len, n);
+  const int chunks = (te - tb + kC - 1) / kC;
+  const size_t seq = (size_t)bh * a.N;
+  const long long entry = a.entries.at(bh);
+  if (entry < 0 && seg == 0 && m0 == 0 && tid == 0 && a.hdr) a.hdr->status = LA_ERR_INVALID_ARG;
+
+  const int row = lane >> 2, col = (lane & 3) * 2;  // of an accumulator
+  float s[DT][8][4];
+  {
+    const float* in = nullptr;
+    if (OUT && a.seg_in)
+      in = a.seg_in + ((size_t)bh * (a.n_seg + 1) + seg) * a.D * a.M;
+    else if (OUT && a.init && entry >= 0)
+      in = a.init + (size_t)entry * a.D * a.M;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int d = dt * 64 + rb * 16 + row + 8 * h, m = m0 + 8 * j + col;
+          float2 x = make_float2(0.f, 0.f);
+          if (in && d < a.D && m < a.M) x = *reinterpret_cast<const float2*>(in + (size_t)d * a.M + m);
+          s[dt][j][2 * h] = x.x;
+          s[dt][j][2 * h + 1] = x.y;
+        }
+  }
+  auto store_op = [&](int buf) {
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int d = dt * 64 + rb * 16 + row + 8 * h;
+          *reinterpret_cast<uint32_t*>(smem + (s_op - base) + buf * Sm::kS +
+                                       (tile_at<64>(0, d, j) + col * 2)) =
+              pack2(s[dt][j][2 * h], s[dt][j][2 * h + 1]);
+        }
+  };
+  auto load_chunk = [&](int c) {
+    const int t0 = tb + c * kC, rows = min(kC, te - t0);
+    const uint32_t at = base + (c & 1) * Sm::kStage;
+    if (OUT) load_tile<DZ, kThreads>(at, a.q + (seq + t0) * a.D, rows, a.D, 0);
+    load_tile<DZ, kThreads>(at + Sm::kQ, a.k + (seq + t0) * a.D, rows, a.D, 0);
+    load_tile<64, kThreads>(at + Sm::kQ + Sm::kK, a.v + (seq + t0) * a.M, rows, a.M, m0);
+  };
+  auto chunk_of = [&](int i) { return REV ? chunks - 1 - i : i; };
+  auto gates_of = [&](int c) { return load_gates(a.g + seq, tb + c * kC, te); };
+
+  float2 g_next = make_float2(0.f, 0.f);
+  float dec_all = 0.f;  // sum of the segment's g, base 2
+  if (chunks > 0) {
+    load_chunk(chunk_of(0));
+    g_next = gates_of(chunk_of(0));
+  }
+  cp_async_commit();
+  if (OUT) store_op(0);
+
+  for (int i = 0; i < chunks; ++i) {
+    const int c = chunk_of(i);
+    cp_async_wait<0>();
+    __syncthreads();  // chunk i has landed; every warp is done with chunk i - 1
+    const float2 g = g_next;
+    if (i + 1 < chunks) {
+      load_chunk(chunk_of(i + 1));
+      g_next = gates_of(chunk_of(i + 1));
+    }
+    cp_async_commit();
+    const float total = chunk_gates<REV>(g, Gs, Ws);
+    const float dec = gated_decay(total * kLn2);
+    dec_all += total;
+
+    const uint32_t q_at = base + (c & 1) * Sm::kStage, k_at = q_at + Sm::kQ, v_at = k_at + Sm::kK;
+    float o[8][4];
+    uint32_t qa[OUT ? KS : 1][4];
+    float gi[2] = {0.f, 0.f};
+    if (OUT) {
+      gi[0] = Gs[rb * 16 + row];
+      gi[1] = Gs[rb * 16 + row + 8];
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) load_a<DZ>(qa[ks], q_at, rb * 16, 2 * ks);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+      const uint32_t op = s_op + (i & 1) * Sm::kS;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int jp = 0; jp < 4; ++jp) {
+          uint32_t b[4];
+          load_b_t<64>(b, op, 16 * ks, 2 * jp);
+          mma16816(o[2 * jp], qa[ks], b[0], b[1]);
+          mma16816(o[2 * jp + 1], qa[ks], b[2], b[3]);
+        }
+      const float e0 = ex2(gi[0]), e1 = ex2(gi[1]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        o[j][0] *= e0;
+        o[j][1] *= e0;
+        o[j][2] *= e1;
+        o[j][3] *= e1;
+      }
+    }
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[dt][j][e] *= dec;
+
+#pragma unroll
+    for (int jb = 0; jb < 4; ++jb) {
+      uint32_t vb[4][4];
+#pragma unroll
+      for (int jp = 0; jp < 4; ++jp) load_b_t<64>(vb[jp], v_at, 16 * jb, 2 * jp);
+      if (OUT && jb <= rb) {
+        float p[2][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t b[4];
+          load_b<DZ>(b, k_at, 16 * jb, 2 * ks);
+          mma16816(p[0], qa[ks], b[0], b[1]);
+          mma16816(p[1], qa[ks], b[2], b[3]);
+        }
+        uint32_t pa[4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float2 gj = *reinterpret_cast<const float2*>(&Gs[16 * jb + 8 * t + col]);
+          float w[4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int j = 8 * t + col, r = row + 8 * h;  // within the diagonal block
+            w[2 * h] = jb < rb || j <= r ? p[t][2 * h] * ex2(gi[h] - gj.x) : 0.f;
+            w[2 * h + 1] = jb < rb || j + 1 <= r ? p[t][2 * h + 1] * ex2(gi[h] - gj.y) : 0.f;
+          }
+          pa[2 * t] = pack2(w[0], w[1]);
+          pa[2 * t + 1] = pack2(w[2], w[3]);
+        }
+#pragma unroll
+        for (int jp = 0; jp < 4; ++jp) {
+          mma16816(o[2 * jp], pa, vb[jp][0], vb[jp][1]);
+          mma16816(o[2 * jp + 1], pa, vb[jp][2], vb[jp][3]);
+        }
+      }
+      const float2 w0 = *reinterpret_cast<const float2*>(&Ws[16 * jb + col]);
+      const float2 w8 = *reinterpret_cast<const float2*>(&Ws[16 * jb + 8 + col]);
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) {
+        uint32_t ka[4], hi[4], lo[4];
+        load_a_t<DZ>(ka, k_at, 16 * jb, 8 * dt + 2 * rb);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 w = e < 2 ? w0 : w8;
+          scale_split(ka[e], w.x, w.y, hi[e], lo[e]);
+        }
+#pragma unroll
+        for (int jp = 0; jp < 4; ++jp) {
+          mma16816(s[dt][2 * jp], hi, vb[jp][0], vb[jp][1]);
+          mma16816(s[dt][2 * jp + 1], hi, vb[jp][2], vb[jp][3]);
+          mma16816(s[dt][2 * jp], lo, vb[jp][0], vb[jp][1]);
+          mma16816(s[dt][2 * jp + 1], lo, vb[jp][2], vb[jp][3]);
+        }
+      }
+    }
+    if (OUT) {
+      if (i + 1 < chunks) store_op((i + 1) & 1);
+      // outputs through this warp's rows of the Q tile (no other warp reads them), so
+      // that rows are written in 16-byte pieces
+      const int t0 = tb + c * kC + rb * 16;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<uint32_t*>(smem + (q_at - base) +
+                                       tile_at<DZ>(0, rb * 16 + row + 8 * h, j) + col * 2) =
+              pack2(o[j][2 * h], o[j][2 * h + 1]);
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = e * 4 + (lane >> 3), ch = lane & 7;
+        if (t0 + r < te && m0 + ch * 8 < a.M)
+          *reinterpret_cast<uint4*>(a.out + (seq + t0 + r) * a.M + m0 + ch * 8) =
+              *reinterpret_cast<const uint4*>(smem + (q_at - base) + tile_at<DZ>(0, rb * 16 + r, ch));
+      }
+    }
+  }
+
+  float* to = nullptr;
+  if (!OUT)
+    to = a.seg_out + ((size_t)bh * (a.n_seg + 1) + seg) * a.D * a.M;
+  else if (a.fin && entry >= 0)
+    to = a.fin + (size_t)entry * a.D * a.M;
+  if (to)
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int d = dt * 64 + rb * 16 + row + 8 * h, m = m0 + 8 * j + col;
+          if (d < a.D && m < a.M)
+            *reinterpret_cast<float2*>(to + (size_t)d * a.M + m) =
+                make_float2(s[dt][j][2 * h], s[dt][j][2 * h + 1]);
+        }
+  if (!OUT && a.decay && m0 == 0 && tid == 0)
+    a.decay[(size_t)bh * a.n_seg + seg] = gated_decay(dec_all * kLn2);
+}
+
+template <int DZ, bool OUT, bool REV>
+cudaError_t launch_chunks(const FwdArgs& a, int BH, cudaStream_t st) {
+  using Sm = FwdSmem<DZ, OUT>;
+  auto kernel = gated_chunk_kernel<DZ, OUT, REV>;
+  cudaError_t e = tcx::configure(kernel, Sm::kBytes);
+  if (e != cudaSuccess) return e;
+  e = tcx::launch_pdl(kernel, dim3((unsigned)(BH * a.n_seg), (unsigned)((a.M + 63) / 64)),
+                      dim3(kThreads), Sm::kBytes, st, a);
+  count_launches(1);
+  return e;
+}
+
+template <bool OUT, bool REV>
+cudaError_t launch_chunks(const FwdArgs& a, int BH, cudaStream_t st) {
+  return a.D <= 64 ? launch_chunks<64, OUT, REV>(a, BH, st) : launch_chunks<128, OUT, REV>(a, BH, st);
+}
+
+}  // namespace
+
+// Segments: one wave of the 152 SMs' resident CTAs, but no segment under four chunks
+// (each costs the state pass and the scan).
+GatedPlan gated_mma_plan(int BH, int N, int M, int resident) {
+  const long long per = (long long)BH * ((M + 63) / 64);
+  const long long chunks = (N + kC - 1) / kC;
+  long long n_seg = (long long)152 * resident / per;
+  if (n_seg > (chunks + 3) / 4) n_seg = (chunks + 3) / 4;
+  if (n_seg < 1) n_seg = 1;
+  long long len = (chunks + n_seg - 1) / n_seg;
+  if (len < 1) len = 1;
+  n_seg = (chunks + len - 1) / len;
+  return GatedPlan{BH, N, (int)(len * kC), n_seg < 1 ? 1 : (int)n_seg};
+}
+
+GatedPlan gated_mma_forward_plan(int BH, int N, int D, int M) {
+  return gated_mma_plan(BH, N, M, D <= 64 ? 3 : 2);
+}
+
+cudaError_t gated_mma_states(const GatedPlan& p, const void* a, const void* b, const void* g, int D,
+                             int M, const int* lens, int H, bool reverse, float* seg_out,
+                             float* decay, cudaStream_t st) {
+  FwdArgs s{};
+  s.k = static_cast<const bf16*>(a);
+  s.v = static_cast<const bf16*>(b);
+  s.g = static_cast<const bf16*>(g);
+  s.D = D;
+  s.M = M;
+  s.N = p.N;
+  s.len = p.len;
+  s.n_seg = p.n_seg;
+  s.lens = lens;
+  s.H = H;
+  s.entries.H = H;
+  s.seg_out = seg_out;
+  s.decay = decay;
+  return reverse ? launch_chunks<false, true>(s, p.BH, st) : launch_chunks<false, false>(s, p.BH, st);
+}
+
+cudaError_t gated_mma_forward(const GatedForward& f, const GatedWorkspace& w, cudaStream_t st) {
+  const GatedPlan p = gated_mma_forward_plan(f.B * f.H, f.N, f.D, f.M);
+  FwdArgs a{};
+  a.q = static_cast<const bf16*>(f.q);
+  a.k = static_cast<const bf16*>(f.k);
+  a.v = static_cast<const bf16*>(f.v);
+  a.g = static_cast<const bf16*>(f.g);
+  a.out = static_cast<bf16*>(f.out);
+  a.D = f.D;
+  a.M = f.M;
+  a.N = f.N;
+  a.len = p.len;
+  a.n_seg = p.n_seg;
+  a.lens = f.lens;
+  a.H = f.H;
+  a.entries = GatedEntries{f.slots, f.pool, f.H};
+  a.hdr = w.hdr;
+  if (p.n_seg > 1) {
+    cudaError_t e = gated_mma_states(p, f.k, f.v, f.g, f.D, f.M, f.lens, f.H, false, w.S, w.decay, st);
+    if (e != cudaSuccess) return e;
+    if ((e = gated_scan(p, w, false, f.S0, f.S, a.entries, f.D * f.M, st)) != cudaSuccess) return e;
+    a.seg_in = w.S;
+  } else {
+    a.init = f.S0;
+    a.fin = f.S;
+  }
+  return launch_chunks<true, false>(a, p.BH, st);
+}
+
+}  // namespace la

@@ -1,0 +1,60 @@
+// The gates of a 64-token chunk, as the tensor-core kernels use them.
+#pragma once
+
+#include "la_gated.cuh"
+#include "la_mma.cuh"
+
+namespace la {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// Gates of tokens t0 + 2 l, t0 + 2 l + 1 (l the lane), base 2; 0 from token `end` on.
+// No lower than -200: 2^-200 is zero in float32, and -inf less -inf is not.
+__device__ __forceinline__ float2 load_gates(const mma::bf16* g, int t0, int end) {
+  const int t = t0 + 2 * (threadIdx.x & 31);
+  const float a = t < end ? __bfloat162float(g[t]) * kLog2e : 0.f;
+  const float b = t + 1 < end ? __bfloat162float(g[t + 1]) * kLog2e : 0.f;
+  return make_float2(a < -200.f ? -200.f : a, b < -200.f ? -200.f : b);
+}
+
+// From a lane's two gates: G[i], their inclusive sums over the chunk, and W[i], the
+// weights of the token's outer product in the chunk's state: 2^(sum of the gates behind
+// it), or for the reverse direction 2^(sum up to and including it). Both are the
+// warp's own tables. Returns the chunk's sum.
+template <bool REV>
+__device__ __forceinline__ float chunk_gates(float2 g, float* G, float* W) {
+  const int lane = threadIdx.x & 31;
+  const float both = g.x + g.y;
+  float up = both, down = both;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float u = __shfl_up_sync(0xffffffffu, up, o);
+    const float d = __shfl_down_sync(0xffffffffu, down, o);
+    if (lane >= o) up += u;
+    if (lane + o < 32) down += d;
+  }
+  float before = __shfl_up_sync(0xffffffffu, up, 1);
+  float after = __shfl_down_sync(0xffffffffu, down, 1);
+  if (lane == 0) before = 0.f;
+  if (lane == 31) after = 0.f;
+  const float2 incl = make_float2(before + g.x, up);
+  __syncwarp();
+  *reinterpret_cast<float2*>(G + 2 * lane) = incl;
+  *reinterpret_cast<float2*>(W + 2 * lane) =
+      REV ? make_float2(mma::ex2(incl.x), mma::ex2(incl.y))
+          : make_float2(mma::ex2(after + g.y), mma::ex2(after));
+  __syncwarp();
+  return __shfl_sync(0xffffffffu, up, 31);
+}
+
+// Tensor-core path: bf16 (la_gated_mma.cu, la_gated_mma_bwd.cu)
+GatedPlan gated_mma_plan(int BH, int N, int M, int resident);
+GatedPlan gated_mma_forward_plan(int BH, int N, int D, int M);
+// each segment's own state (or gradient of the incoming one) from zero, and its decay
+// (nullptr: not written)
+cudaError_t gated_mma_states(const GatedPlan& p, const void* a, const void* b, const void* g, int D,
+                             int M, const int* lens, int H, bool reverse, float* seg_out,
+                             float* decay, cudaStream_t st);
+cudaError_t gated_mma_forward(const GatedForward& f, const GatedWorkspace& w, cudaStream_t st);
+
+}  // namespace la
