@@ -216,39 +216,63 @@ __global__ void __launch_bounds__(kThreads) gated_recur_kernel(const RecurArgs a
 
 // Joins the segments: forward X[s + 1] = decay[s] X[s] + U[s] from X[0] = init,
 // reverse X[s] = decay[s] X[s + 1] + U[s] from X[n_seg] = init; U[s] is read from
-// entry s and replaced there. One thread per state element.
+// entry s and replaced there. One thread per state element, its loads four segments
+// ahead of their use (the walk is bound by their latency). blockIdx.z: which of the
+// two jobs (states, gradients).
+struct ScanJob {
+  float* X;
+  const float* init;
+  float* fin;
+  bool reverse;
+};
 __global__ void __launch_bounds__(256)
-gated_scan_kernel(float* X, const float* __restrict__ decay, const float* init, float* fin,
-                  const GatedEntries entries, int n_seg, int DM, bool reverse,
-                  WorkspaceHeader* hdr) {
+gated_scan_kernel(const ScanJob first, const ScanJob second, const float* __restrict__ decay,
+                  const GatedEntries entries, int n_seg, int DM, WorkspaceHeader* hdr) {
+  constexpr int kAhead = 4;
+  const ScanJob& job = blockIdx.z == 0 ? first : second;
   const int bh = blockIdx.x;
   const int i = blockIdx.y * 256 + threadIdx.x;
+  tc::pdl_wait();
   const long long entry = entries.at(bh);
   if (entry < 0 && i == 0) hdr->status = LA_ERR_INVALID_ARG;
   if (i >= DM) return;
-  float* x = X + (size_t)bh * (n_seg + 1) * DM + i;
+  float* x = job.X + (size_t)bh * (n_seg + 1) * DM + i;
   const float* dec = decay + (size_t)bh * n_seg;
-  float s = init && entry >= 0 ? init[(size_t)entry * DM + i] : 0.f;
-  if (reverse) {
-    float u = x[(size_t)(n_seg - 1) * DM];
-    x[(size_t)n_seg * DM] = s;
-    for (int k = n_seg - 1; k >= 0; --k) {
-      const float next = k > 0 ? x[(size_t)(k - 1) * DM] : 0.f;
-      s = fmaf(dec[k], s, u);
-      x[(size_t)k * DM] = s;
-      u = next;
-    }
-  } else {
-    float u = x[0];
-    for (int k = 0; k < n_seg; ++k) {
-      const float next = k + 1 < n_seg ? x[(size_t)(k + 1) * DM] : 0.f;
-      x[(size_t)k * DM] = s;
-      s = fmaf(dec[k], s, u);
-      u = next;
-    }
-    x[(size_t)n_seg * DM] = s;
+  float s = job.init && entry >= 0 ? job.init[(size_t)entry * DM + i] : 0.f;
+  // segment k of the walk; a forward walk leaves the state before it there, a reverse
+  // one the gradient behind it one entry further on
+  auto at = [&](int k) { return job.reverse ? n_seg - 1 - k : k; };
+  float u[kAhead], d[kAhead];
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    u[j] = j < n_seg ? x[(size_t)at(j) * DM] : 0.f;
+    d[j] = j < n_seg ? dec[at(j)] : 0.f;
   }
-  if (fin && entry >= 0) fin[(size_t)entry * DM + i] = s;
+  if (job.reverse) x[(size_t)n_seg * DM] = s;
+  for (int k0 = 0; k0 < n_seg; k0 += kAhead) {
+    float un[kAhead], dn[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = k0 + kAhead + j;
+      un[j] = k < n_seg ? x[(size_t)at(k) * DM] : 0.f;
+      dn[j] = k < n_seg ? dec[at(k)] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = k0 + j;
+      if (k >= n_seg) break;
+      const float before = s;
+      s = fmaf(d[j], s, u[j]);
+      x[(size_t)at(k) * DM] = job.reverse ? s : before;
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      u[j] = un[j];
+      d[j] = dn[j];
+    }
+  }
+  if (!job.reverse) x[(size_t)n_seg * DM] = s;
+  if (job.fin && entry >= 0) job.fin[(size_t)entry * DM + i] = s;
 }
 
 // dg of one segment: from <X', E> at its last token back,
@@ -323,7 +347,8 @@ GatedPlan plan_simt(int BH, int N, int D, int M, bool backward) {
   return GatedPlan{BH, N, len > 0 ? len : kTok, N > 0 ? (N + len - 1) / len : 1};
 }
 
-GatedWorkspace carve(void* ws, const GatedPlan& p, int D, int M, bool backward, int dots) {
+GatedWorkspace carve(void* ws, const GatedPlan& p, int D, int M, bool backward, int dots,
+                     size_t scratch = 0) {
   GatedWorkspace w{};
   const uintptr_t base = reinterpret_cast<uintptr_t>(ws);
   size_t at = kHeaderBytes;
@@ -340,6 +365,7 @@ GatedWorkspace carve(void* ws, const GatedPlan& p, int D, int M, bool backward, 
   }
   if (backward) {
     w.E = take(seq * (p.n_seg + 1) * dm);
+    w.scratch = take(scratch / sizeof(float));
     w.dot_q = take((size_t)dots * seq * p.N);
     w.dot_k = take((size_t)dots * seq * p.N);
     w.ends = take((size_t)dots * seq * p.n_seg);
@@ -375,7 +401,7 @@ cudaError_t simt_forward(const GatedForward& f, void* ws, cudaStream_t st) {
     s.seg_out = w.S;
     s.decay = w.decay;
     if ((e = launch_recur<float, false>(s, st)) != cudaSuccess) return e;
-    if ((e = gated_scan(p, w, false, f.S0, f.S, a.entries, a.DM, st)) != cudaSuccess) return e;
+    if ((e = gated_scan(p, w, f.S0, f.S, a.entries, a.DM, st)) != cudaSuccess) return e;
     a.seg_in = w.S;
   } else {
     a.init = f.S0;
@@ -423,8 +449,8 @@ cudaError_t simt_backward_t(const GatedBackward& f, void* ws, cudaStream_t st) {
   s.seg_out = w.E;
   s.decay = nullptr;
   if ((e = launch_recur<T, true>(s, st)) != cudaSuccess) return e;
-  if ((e = gated_scan(p, w, false, f.S0, nullptr, a.entries, a.DM, st)) != cudaSuccess) return e;
-  if ((e = gated_scan(p, w, true, f.dS, f.dS0, a.entries, a.DM, st)) != cudaSuccess) return e;
+  const GatedGradients back{f.dS, f.dS0};
+  if ((e = gated_scan(p, w, f.S0, nullptr, a.entries, a.DM, st, &back)) != cudaSuccess) return e;
   RecurArgs dq = rows_d;
   dq.u = f.k;
   dq.w = f.v;
@@ -530,12 +556,15 @@ gated_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
 
 }  // namespace
 
-cudaError_t gated_scan(const GatedPlan& p, const GatedWorkspace& w, bool reverse, const float* init,
-                       float* fin, const GatedEntries& e, int DM, cudaStream_t st) {
-  gated_scan_kernel<<<dim3(p.BH, (DM + 255) / 256), 256, 0, st>>>(
-      reverse ? w.E : w.S, w.decay, init, fin, e, p.n_seg, DM, reverse, w.hdr);
+cudaError_t gated_scan(const GatedPlan& p, const GatedWorkspace& w, const float* S0, float* S,
+                       const GatedEntries& e, int DM, cudaStream_t st, const GatedGradients* back) {
+  const ScanJob first{w.S, S0, S, false};
+  const ScanJob second = back ? ScanJob{w.E, back->dS, back->dS0, true} : first;
+  const cudaError_t err =
+      tcx::launch_pdl(gated_scan_kernel, dim3((unsigned)p.BH, (unsigned)((DM + 255) / 256), back ? 2 : 1),
+                      dim3(256), 0, st, first, second, w.decay, e, p.n_seg, DM, w.hdr);
   count_launches(1);
-  return cudaGetLastError();
+  return err;
 }
 
 // bf16 runs on tensor cores, float32 (which they would round) on CUDA cores.
@@ -547,8 +576,15 @@ size_t gated_forward_workspace(int BH, int N, int D, int M, int dtype) {
   return carve(nullptr, forward_plan(BH, N, D, M, dtype), D, M, false, 0).bytes;
 }
 
+static bool backward_on_mma(int D, int M, int dtype) {
+  return dtype == LA_BF16 && gated_mma_backward_supported(D, M);
+}
+
 size_t gated_backward_workspace(int BH, int N, int D, int M, int dtype) {
-  (void)dtype;
+  if (backward_on_mma(D, M, dtype)) {
+    const GatedPlan p = gated_mma_backward_plan(BH, N);
+    return carve(nullptr, p, D, M, true, 0, gated_mma_backward_scratch(p)).bytes;
+  }
   return carve(nullptr, plan_simt(BH, N, D, M, true), D, M, true, row_blocks(D, M)).bytes;
 }
 
@@ -559,6 +595,11 @@ cudaError_t gated_forward(const GatedForward& f, void* ws, cudaStream_t st) {
 }
 
 cudaError_t gated_backward(const GatedBackward& f, void* ws, cudaStream_t st) {
+  if (backward_on_mma(f.D, f.M, f.dtype)) {
+    const GatedPlan p = gated_mma_backward_plan(f.B * f.H, f.N);
+    return gated_mma_backward(
+        f, p, carve(ws, p, f.D, f.M, true, 0, gated_mma_backward_scratch(p)), st);
+  }
   return f.dtype == LA_F32 ? simt_backward_t<float>(f, ws, st)
                            : simt_backward_t<__nv_bfloat16>(f, ws, st);
 }

@@ -23,12 +23,14 @@ struct GatedPlan {
 
 // Workspace: header | decay [BH][n_seg] | S [BH][n_seg + 1][D][M] and, for the
 // backward, E [BH][n_seg + 1][D][M] | dots of q with dq, of k with
-// dk, and the segments' ends (the decay's gradient is made of them).
+// dk, and the segments' ends (the decay's gradient is made of them; on the tensor-core
+// path one scratch area in their place).
 // S[.][s] is the state segment s receives (n_seg: the final one), E[.][s] the
 // loss's gradient with respect to it.
 struct GatedWorkspace {
   WorkspaceHeader* hdr;
   float *decay, *S, *E, *dot_q, *dot_k, *ends;
+  void* scratch;
   size_t bytes;
 };
 
@@ -54,8 +56,14 @@ __device__ __forceinline__ int gated_length(const int* lens, int H, int bh, int 
   return lens ? max(0, min(lens[bh / H], N)) : N;
 }
 
-// the scan over the segments (either path's partial states)
-cudaError_t gated_scan(const GatedPlan& p, const GatedWorkspace& w, bool reverse, const float* init,
-                       float* fin, const GatedEntries& e, int DM, cudaStream_t st);
+// The scan over the segments: of the states, from S0 to S (nullptr: zero, not wanted),
+// and with `back` of the gradients too, from dS to dS0.
+struct GatedGradients {
+  const float* dS;
+  float* dS0;
+};
+cudaError_t gated_scan(const GatedPlan& p, const GatedWorkspace& w, const float* S0, float* S,
+                       const GatedEntries& e, int DM, cudaStream_t st,
+                       const GatedGradients* back = nullptr);
 
 }  // namespace la

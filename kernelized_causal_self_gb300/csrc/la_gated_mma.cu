@@ -62,8 +62,13 @@ struct FwdSmem {
 // segment's own S from zero, over k, v with weights exp(G - G_j), or (REV) its own
 // gradient of the incoming state from zero, over q, dout with weights exp(G_i), chunks
 // from the last to the first.
-template <int DZ, bool OUT, bool REV>
-__global__ void __launch_bounds__(kThreads, DZ == 64 ? 3 : 2) gated_chunk_kernel(const FwdArgs a) {
+// FRESH: a chunk's update of S is summed apart and then added, in float32 arithmetic that
+// rounds; the tensor cores' own sums truncate, which over thousands of chunks would
+// leave a bias in a state that hardly decays. Taken wherever S leaves the kernel in
+// float32; where it only goes on as a bf16 operand, it is summed in place, which leaves
+// registers for a third CTA per SM.
+template <int DZ, bool OUT, bool REV, bool FRESH>
+__device__ __forceinline__ void walk_chunks(const FwdArgs& a) {
   using Sm = FwdSmem<DZ, OUT>;
   constexpr int KS = DZ / 16, DT = DZ / 64;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -183,12 +188,18 @@ __global__ void __launch_bounds__(kThreads, DZ == 64 ? 3 : 2) gated_chunk_kernel
         o[j][3] *= e1;
       }
     }
+    float u[FRESH ? DT : 1][8][4];
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[dt][j][e] *= dec;
+        for (int e = 0; e < 4; ++e) {
+          if (FRESH)
+            u[dt][j][e] = 0.f;
+          else
+            s[dt][j][e] *= dec;
+        }
 
 #pragma unroll
     for (int jb = 0; jb < 4; ++jb) {
@@ -235,14 +246,23 @@ __global__ void __launch_bounds__(kThreads, DZ == 64 ? 3 : 2) gated_chunk_kernel
           const float2 w = e < 2 ? w0 : w8;
           scale_split(ka[e], w.x, w.y, hi[e], lo[e]);
         }
+        float(&to)[8][4] = FRESH ? u[FRESH ? dt : 0] : s[dt];
 #pragma unroll
         for (int jp = 0; jp < 4; ++jp) {
-          mma16816(s[dt][2 * jp], hi, vb[jp][0], vb[jp][1]);
-          mma16816(s[dt][2 * jp + 1], hi, vb[jp][2], vb[jp][3]);
-          mma16816(s[dt][2 * jp], lo, vb[jp][0], vb[jp][1]);
-          mma16816(s[dt][2 * jp + 1], lo, vb[jp][2], vb[jp][3]);
+          mma16816(to[2 * jp], hi, vb[jp][0], vb[jp][1]);
+          mma16816(to[2 * jp + 1], hi, vb[jp][2], vb[jp][3]);
+          mma16816(to[2 * jp], lo, vb[jp][0], vb[jp][1]);
+          mma16816(to[2 * jp + 1], lo, vb[jp][2], vb[jp][3]);
         }
       }
+    }
+    if (FRESH) {
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[dt][j][e] = fmaf(dec, s[dt][j][e], u[dt][j][e]);
     }
     if (OUT) {
       if (i + 1 < chunks) store_op((i + 1) & 1);
@@ -288,10 +308,26 @@ __global__ void __launch_bounds__(kThreads, DZ == 64 ? 3 : 2) gated_chunk_kernel
     a.decay[(size_t)bh * a.n_seg + seg] = gated_decay(dec_all * kLn2);
 }
 
-template <int DZ, bool OUT, bool REV>
-cudaError_t launch_chunks(const FwdArgs& a, int BH, cudaStream_t st) {
-  using Sm = FwdSmem<DZ, OUT>;
-  auto kernel = gated_chunk_kernel<DZ, OUT, REV>;
+template <int DZ, bool FRESH>
+__global__ void __launch_bounds__(kThreads, DZ == 64 && !FRESH ? 3 : 2)
+gated_forward_kernel(const FwdArgs a) {
+  walk_chunks<DZ, true, false, FRESH>(a);
+}
+
+// blockIdx.z: the segments' states, or their gradients
+template <int DZ>
+__global__ void __launch_bounds__(kThreads, DZ == 64 ? 3 : 2)
+gated_states_kernel(const FwdArgs a, const FwdArgs back) {
+  if (blockIdx.z == 0)
+    walk_chunks<DZ, false, false, true>(a);
+  else
+    walk_chunks<DZ, false, true, true>(back);
+}
+
+template <int DZ, bool FRESH>
+cudaError_t launch_forward(const FwdArgs& a, int BH, cudaStream_t st) {
+  using Sm = FwdSmem<DZ, true>;
+  auto kernel = gated_forward_kernel<DZ, FRESH>;
   cudaError_t e = tcx::configure(kernel, Sm::kBytes);
   if (e != cudaSuccess) return e;
   e = tcx::launch_pdl(kernel, dim3((unsigned)(BH * a.n_seg), (unsigned)((a.M + 63) / 64)),
@@ -300,9 +336,16 @@ cudaError_t launch_chunks(const FwdArgs& a, int BH, cudaStream_t st) {
   return e;
 }
 
-template <bool OUT, bool REV>
-cudaError_t launch_chunks(const FwdArgs& a, int BH, cudaStream_t st) {
-  return a.D <= 64 ? launch_chunks<64, OUT, REV>(a, BH, st) : launch_chunks<128, OUT, REV>(a, BH, st);
+template <int DZ>
+cudaError_t launch_states(const FwdArgs& a, const FwdArgs* back, int BH, cudaStream_t st) {
+  using Sm = FwdSmem<DZ, false>;
+  auto kernel = gated_states_kernel<DZ>;
+  cudaError_t e = tcx::configure(kernel, Sm::kBytes);
+  if (e != cudaSuccess) return e;
+  e = tcx::launch_pdl(kernel, dim3((unsigned)(BH * a.n_seg), (unsigned)((a.M + 63) / 64), back ? 2 : 1),
+                      dim3(kThreads), Sm::kBytes, st, a, back ? *back : a);
+  count_launches(1);
+  return e;
 }
 
 }  // namespace
@@ -325,12 +368,12 @@ GatedPlan gated_mma_forward_plan(int BH, int N, int D, int M) {
   return gated_mma_plan(BH, N, M, D <= 64 ? 3 : 2);
 }
 
-cudaError_t gated_mma_states(const GatedPlan& p, const void* a, const void* b, const void* g, int D,
-                             int M, const int* lens, int H, bool reverse, float* seg_out,
-                             float* decay, cudaStream_t st) {
+cudaError_t gated_mma_states(const GatedPlan& p, const void* k, const void* v, const void* q,
+                             const void* dout, const void* g, int D, int M, const int* lens, int H,
+                             const GatedWorkspace& w, cudaStream_t st) {
   FwdArgs s{};
-  s.k = static_cast<const bf16*>(a);
-  s.v = static_cast<const bf16*>(b);
+  s.k = static_cast<const bf16*>(k);
+  s.v = static_cast<const bf16*>(v);
   s.g = static_cast<const bf16*>(g);
   s.D = D;
   s.M = M;
@@ -340,9 +383,15 @@ cudaError_t gated_mma_states(const GatedPlan& p, const void* a, const void* b, c
   s.lens = lens;
   s.H = H;
   s.entries.H = H;
-  s.seg_out = seg_out;
-  s.decay = decay;
-  return reverse ? launch_chunks<false, true>(s, p.BH, st) : launch_chunks<false, false>(s, p.BH, st);
+  s.seg_out = w.S;
+  s.decay = w.decay;
+  FwdArgs back = s;
+  back.k = static_cast<const bf16*>(q);
+  back.v = static_cast<const bf16*>(dout);
+  back.seg_out = w.E;
+  back.decay = nullptr;
+  const FwdArgs* b = dout ? &back : nullptr;
+  return D <= 64 ? launch_states<64>(s, b, p.BH, st) : launch_states<128>(s, b, p.BH, st);
 }
 
 cudaError_t gated_mma_forward(const GatedForward& f, const GatedWorkspace& w, cudaStream_t st) {
@@ -363,15 +412,17 @@ cudaError_t gated_mma_forward(const GatedForward& f, const GatedWorkspace& w, cu
   a.entries = GatedEntries{f.slots, f.pool, f.H};
   a.hdr = w.hdr;
   if (p.n_seg > 1) {
-    cudaError_t e = gated_mma_states(p, f.k, f.v, f.g, f.D, f.M, f.lens, f.H, false, w.S, w.decay, st);
+    cudaError_t e = gated_mma_states(p, f.k, f.v, nullptr, nullptr, f.g, f.D, f.M, f.lens, f.H, w, st);
     if (e != cudaSuccess) return e;
-    if ((e = gated_scan(p, w, false, f.S0, f.S, a.entries, f.D * f.M, st)) != cudaSuccess) return e;
+    if ((e = gated_scan(p, w, f.S0, f.S, a.entries, f.D * f.M, st)) != cudaSuccess) return e;
     a.seg_in = w.S;
   } else {
     a.init = f.S0;
     a.fin = f.S;
   }
-  return launch_chunks<true, false>(a, p.BH, st);
+  if (a.fin)
+    return f.D <= 64 ? launch_forward<64, true>(a, p.BH, st) : launch_forward<128, true>(a, p.BH, st);
+  return f.D <= 64 ? launch_forward<64, false>(a, p.BH, st) : launch_forward<128, false>(a, p.BH, st);
 }
 
 }  // namespace la

@@ -50,11 +50,17 @@ __device__ __forceinline__ float chunk_gates(float2 g, float* G, float* W) {
 // Tensor-core path: bf16 (la_gated_mma.cu, la_gated_mma_bwd.cu)
 GatedPlan gated_mma_plan(int BH, int N, int M, int resident);
 GatedPlan gated_mma_forward_plan(int BH, int N, int D, int M);
-// each segment's own state (or gradient of the incoming one) from zero, and its decay
-// (nullptr: not written)
-cudaError_t gated_mma_states(const GatedPlan& p, const void* a, const void* b, const void* g, int D,
-                             int M, const int* lens, int H, bool reverse, float* seg_out,
-                             float* decay, cudaStream_t st);
+// each segment's own state from zero and its decay, and (dout not nullptr) its own
+// gradient of the incoming state from zero
+cudaError_t gated_mma_states(const GatedPlan& p, const void* k, const void* v, const void* q,
+                             const void* dout, const void* g, int D, int M, const int* lens, int H,
+                             const GatedWorkspace& w, cudaStream_t st);
 cudaError_t gated_mma_forward(const GatedForward& f, const GatedWorkspace& w, cudaStream_t st);
+bool gated_mma_backward_supported(int D, int M);
+GatedPlan gated_mma_backward_plan(int BH, int N);
+// bytes of scratch behind the plan's states
+size_t gated_mma_backward_scratch(const GatedPlan& p);
+cudaError_t gated_mma_backward(const GatedBackward& f, const GatedPlan& p, const GatedWorkspace& w,
+                               cudaStream_t st);
 
 }  // namespace la
