@@ -92,6 +92,8 @@ __device__ __forceinline__ void walk_chunks(const FwdArgs& a) {
   if (entry < 0 && seg == 0 && m0 == 0 && tid == 0 && a.hdr) a.hdr->status = LA_ERR_INVALID_ARG;
 
   const int row = lane >> 2, col = (lane & 3) * 2;  // of an accumulator
+  const Lane<DZ> ln;
+  const Lane<64> ln64;
   float s[DT][8][4];
   {
     const float* in = nullptr;
@@ -112,18 +114,9 @@ __device__ __forceinline__ void walk_chunks(const FwdArgs& a) {
           s[dt][j][2 * h + 1] = x.y;
         }
   }
-  auto store_op = [&](int buf) {
+  auto keep_op = [&](int buf) {
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int d = dt * 64 + rb * 16 + row + 8 * h;
-          *reinterpret_cast<uint32_t*>(smem + (s_op - base) + buf * Sm::kS +
-                                       (tile_at<64>(0, d, j) + col * 2)) =
-              pack2(s[dt][j][2 * h], s[dt][j][2 * h + 1]);
-        }
+    for (int dt = 0; dt < DT; ++dt) store_op(ln64, s_op + buf * Sm::kS, dt * 64 + rb * 16, 0, s[dt]);
   };
   auto load_chunk = [&](int c) {
     const int t0 = tb + c * kC, rows = min(kC, te - t0);
@@ -133,25 +126,25 @@ __device__ __forceinline__ void walk_chunks(const FwdArgs& a) {
     load_tile<64, kThreads>(at + Sm::kQ + Sm::kK, a.v + (seq + t0) * a.M, rows, a.M, m0);
   };
   auto chunk_of = [&](int i) { return REV ? chunks - 1 - i : i; };
-  auto gates_of = [&](int c) { return load_gates(a.g + seq, tb + c * kC, te); };
+  auto raw_gates = [&](int c) { return load_gates(a.g + seq, tb + c * kC, te); };
 
-  float2 g_next = make_float2(0.f, 0.f);
+  ushort2 g_next = make_ushort2(0, 0);
   float dec_all = 0.f;  // sum of the segment's g, base 2
   if (chunks > 0) {
     load_chunk(chunk_of(0));
-    g_next = gates_of(chunk_of(0));
+    g_next = raw_gates(chunk_of(0));
   }
   cp_async_commit();
-  if (OUT) store_op(0);
+  if (OUT) keep_op(0);
 
   for (int i = 0; i < chunks; ++i) {
     const int c = chunk_of(i);
     cp_async_wait<0>();
     __syncthreads();  // chunk i has landed; every warp is done with chunk i - 1
-    const float2 g = g_next;
+    const float2 g = gates_of(g_next);
     if (i + 1 < chunks) {
       load_chunk(chunk_of(i + 1));
-      g_next = gates_of(chunk_of(i + 1));
+      g_next = raw_gates(chunk_of(i + 1));
     }
     cp_async_commit();
     const float total = chunk_gates<REV>(g, Gs, Ws);
@@ -160,131 +153,41 @@ __device__ __forceinline__ void walk_chunks(const FwdArgs& a) {
 
     const uint32_t q_at = base + (c & 1) * Sm::kStage, k_at = q_at + Sm::kQ, v_at = k_at + Sm::kK;
     float o[8][4];
-    uint32_t qa[OUT ? KS : 1][4];
-    float gi[2] = {0.f, 0.f};
     if (OUT) {
-      gi[0] = Gs[rb * 16 + row];
-      gi[1] = Gs[rb * 16 + row + 8];
+      uint32_t qa[KS][4];
+      const float gi[2] = {Gs[rb * 16 + row], Gs[rb * 16 + row + 8]};
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) load_a<DZ>(qa[ks], q_at, rb * 16, 2 * ks);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-      const uint32_t op = s_op + (i & 1) * Sm::kS;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int jp = 0; jp < 4; ++jp) {
-          uint32_t b[4];
-          load_b_t<64>(b, op, 16 * ks, 2 * jp);
-          mma16816(o[2 * jp], qa[ks], b[0], b[1]);
-          mma16816(o[2 * jp + 1], qa[ks], b[2], b[3]);
-        }
-      const float e0 = ex2(gi[0]), e1 = ex2(gi[1]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        o[j][0] *= e0;
-        o[j][1] *= e0;
-        o[j][2] *= e1;
-        o[j][3] *= e1;
+      for (int ks = 0; ks < KS; ++ks) ln.load_a(qa[ks], q_at, rb * 16, ks);
+      product<true>(ln64, o, qa, s_op + (i & 1) * Sm::kS);
+      scale_rows(o, ex2(gi[0]), ex2(gi[1]));
+      uint32_t p[4];
+#pragma unroll 1
+      for (int jb = 0; jb < rb; ++jb) {
+        masked_block<true, false>(ln, p, qa, k_at, jb, gi, Gs);
+        add_block(ln64, o, p, v_at, jb);
       }
+      masked_block<true, true>(ln, p, qa, k_at, rb, gi, Gs);
+      add_block(ln64, o, p, v_at, rb);
+      // through this warp's rows of the Q tile, which no other warp reads
+      const int t0 = tb + c * kC + rb * 16;
+      store_rows(ln, q_at, rb * 16, o, a.out + (seq + t0) * a.M + m0, te - t0, a.M - m0, a.M);
     }
-    float u[FRESH ? DT : 1][8][4];
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (FRESH)
-            u[dt][j][e] = 0.f;
-          else
-            s[dt][j][e] *= dec;
-        }
-
-#pragma unroll
-    for (int jb = 0; jb < 4; ++jb) {
-      uint32_t vb[4][4];
-#pragma unroll
-      for (int jp = 0; jp < 4; ++jp) load_b_t<64>(vb[jp], v_at, 16 * jb, 2 * jp);
-      if (OUT && jb <= rb) {
-        float p[2][4] = {};
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          uint32_t b[4];
-          load_b<DZ>(b, k_at, 16 * jb, 2 * ks);
-          mma16816(p[0], qa[ks], b[0], b[1]);
-          mma16816(p[1], qa[ks], b[2], b[3]);
-        }
-        uint32_t pa[4];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const float2 gj = *reinterpret_cast<const float2*>(&Gs[16 * jb + 8 * t + col]);
-          float w[4];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int j = 8 * t + col, r = row + 8 * h;  // within the diagonal block
-            w[2 * h] = jb < rb || j <= r ? p[t][2 * h] * ex2(gi[h] - gj.x) : 0.f;
-            w[2 * h + 1] = jb < rb || j + 1 <= r ? p[t][2 * h + 1] * ex2(gi[h] - gj.y) : 0.f;
-          }
-          pa[2 * t] = pack2(w[0], w[1]);
-          pa[2 * t + 1] = pack2(w[2], w[3]);
-        }
-#pragma unroll
-        for (int jp = 0; jp < 4; ++jp) {
-          mma16816(o[2 * jp], pa, vb[jp][0], vb[jp][1]);
-          mma16816(o[2 * jp + 1], pa, vb[jp][2], vb[jp][3]);
-        }
-      }
-      const float2 w0 = *reinterpret_cast<const float2*>(&Ws[16 * jb + col]);
-      const float2 w8 = *reinterpret_cast<const float2*>(&Ws[16 * jb + 8 + col]);
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt) {
-        uint32_t ka[4], hi[4], lo[4];
-        load_a_t<DZ>(ka, k_at, 16 * jb, 8 * dt + 2 * rb);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 w = e < 2 ? w0 : w8;
-          scale_split(ka[e], w.x, w.y, hi[e], lo[e]);
-        }
-        float(&to)[8][4] = FRESH ? u[FRESH ? dt : 0] : s[dt];
-#pragma unroll
-        for (int jp = 0; jp < 4; ++jp) {
-          mma16816(to[2 * jp], hi, vb[jp][0], vb[jp][1]);
-          mma16816(to[2 * jp + 1], hi, vb[jp][2], vb[jp][3]);
-          mma16816(to[2 * jp], lo, vb[jp][0], vb[jp][1]);
-          mma16816(to[2 * jp + 1], lo, vb[jp][2], vb[jp][3]);
-        }
-      }
-    }
-    if (FRESH) {
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt)
+    for (int dt = 0; dt < DT; ++dt) {
+      if (FRESH) {
+        float u[8][4];
+        add_outer<DZ, 8, true>(ln, ln64, u, k_at, Ws, 4 * dt + rb, v_at, 0);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[dt][j][e] = fmaf(dec, s[dt][j][e], u[dt][j][e]);
-    }
-    if (OUT) {
-      if (i + 1 < chunks) store_op((i + 1) & 1);
-      // outputs through this warp's rows of the Q tile (no other warp reads them), so
-      // that rows are written in 16-byte pieces
-      const int t0 = tb + c * kC + rb * 16;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<uint32_t*>(smem + (q_at - base) +
-                                       tile_at<DZ>(0, rb * 16 + row + 8 * h, j) + col * 2) =
-              pack2(o[j][2 * h], o[j][2 * h + 1]);
-      __syncwarp();
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = e * 4 + (lane >> 3), ch = lane & 7;
-        if (t0 + r < te && m0 + ch * 8 < a.M)
-          *reinterpret_cast<uint4*>(a.out + (seq + t0 + r) * a.M + m0 + ch * 8) =
-              *reinterpret_cast<const uint4*>(smem + (q_at - base) + tile_at<DZ>(0, rb * 16 + r, ch));
+          for (int h = 0; h < 2; ++h)
+            pair_of(s[dt][j], h) = fma2(make_float2(dec, dec), pair_of(s[dt][j], h), pair_of(u[j], h));
+      } else {
+        scale_rows(s[dt], dec, dec);
+        add_outer<DZ, 8>(ln, ln64, s[dt], k_at, Ws, 4 * dt + rb, v_at, 0);
       }
     }
+    if (OUT && i + 1 < chunks) keep_op((i + 1) & 1);
   }
 
   float* to = nullptr;

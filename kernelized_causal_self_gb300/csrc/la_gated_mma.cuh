@@ -8,12 +8,19 @@ namespace la {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Gates of tokens t0 + 2 l, t0 + 2 l + 1 (l the lane), base 2; 0 from token `end` on.
-// No lower than -200: 2^-200 is zero in float32, and -inf less -inf is not.
-__device__ __forceinline__ float2 load_gates(const mma::bf16* g, int t0, int end) {
+// Gates of tokens t0 + 2 l, t0 + 2 l + 1 (l the lane) as they are stored; 0 from token
+// `end` on. (Converted where they are used, so that the load's latency is not waited for
+// where it is issued.)
+__device__ __forceinline__ ushort2 load_gates(const mma::bf16* g, int t0, int end) {
   const int t = t0 + 2 * (threadIdx.x & 31);
-  const float a = t < end ? __bfloat162float(g[t]) * kLog2e : 0.f;
-  const float b = t + 1 < end ? __bfloat162float(g[t + 1]) * kLog2e : 0.f;
+  const unsigned short* p = reinterpret_cast<const unsigned short*>(g);
+  return make_ushort2(t < end ? p[t] : 0, t + 1 < end ? p[t + 1] : 0);
+}
+
+// Base 2, and no lower than -200: 2^-200 is zero in float32, and -inf less -inf is not.
+__device__ __forceinline__ float2 gates_of(ushort2 g) {
+  const float a = __uint_as_float((uint32_t)g.x << 16) * kLog2e;
+  const float b = __uint_as_float((uint32_t)g.y << 16) * kLog2e;
   return make_float2(a < -200.f ? -200.f : a, b < -200.f ? -200.f : b);
 }
 

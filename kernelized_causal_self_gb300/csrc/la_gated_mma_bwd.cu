@@ -1,7 +1,7 @@
 // Gated recurrence's backward in bf16 on tensor cores (D, M up to 64).
 //
 // Per chunk of 64 tokens, with S the state before it and E the loss's gradient with
-// respect to the state after it (G, L as in the forward; W_ij = exp(G - G_j)):
+// respect to the state after it (G, L as in the forward):
 //   dQ = ((dO V^T) * L) K + diag(exp(G_i)) dO S^T
 //   dK = ((dO V^T) * L)^T Q + diag(exp(G - G_j)) V E^T
 //   dV = ((Q K^T) * L)^T dO + diag(exp(G - G_j)) K E
@@ -9,15 +9,19 @@
 // A gate g_t scales what passes from tokens before t to tokens from t on:
 //   dg_t = sum_{i >= t > j} X_ij + sum_{i >= t} a_i + sum_{j < t} b_j + exp(G) <S, E>
 //   X = (Q K^T) * (dO V^T) * L,  a_i = exp(G_i) q_i S dO_i,  b_j = exp(G - G_j) k_j E v_j
-// X's sum is one over s >= t of its strict row sums less its column sums: both of the
-// same float32 products, which cancel to float32 where they have to.
+// X's sum is one over s >= t of its row sums less its column sums, and those are what
+// the products within the chunk add to q_s . dQ_s and to k_s . dK_s. Both products take
+// the same rounded operand (dO V^T) * L, so what has to cancel in the difference does.
 //
 // S is known going forward and E going back, so a CTA walks its segment of a few chunks
-// forward (dQ, a, and each chunk's S in bf16 to scratch of the CTA's own) and then back
-// (dK, dV, dg). Segments are short enough (up to 8 chunks) that the tiles' second read
-// comes from L2. Both walks keep their state in float32 accumulators; rounded to bf16
-// are the operands (L's products, the copies of S and E that are multiplied) and the
-// gradients.
+// forward (dQ; each chunk's S in bf16 to scratch of the CTA's own) and then back (dK, dV,
+// dg). Segments are short enough that the tiles' second read comes from L2. Both walks
+// keep their state in float32 accumulators; rounded to bf16 are the operands (L's
+// products, the copies of S and E that are multiplied) and the gradients.
+//
+// Four warps share a chunk, warp r with its rows 16 r.. of the outputs and of the states.
+// Going back, dV is finished before dK is begun, so that one set of output accumulators is
+// live at a time.
 #include "la_gated.cuh"
 #include "la_gated_mma.cuh"
 #include "la_mma.cuh"
@@ -29,14 +33,19 @@ using namespace mma;
 
 namespace {
 
-constexpr int kThreads = 128, kResident = 2, kMaxChunks = 8;
+constexpr int kThreads = 128, kResident = 2, kMaxChunks = 14;
 constexpr int kTile = kC * 64 * 2;
 constexpr int kStage = 4 * kTile;  // Q, K, V, dO
 constexpr int kOp = kTile;         // S or E in bf16, [d][m], one of two
-// floats: per-warp G, W, V tables; a of the segment; per parity: row sums of X by warp,
-// column sums, b, <S, E> by warp
-constexpr int kTables = 4 * 3 * kC, kAlpha = kMaxChunks * kC, kParts = 4 * kC + kC + kC + 4;
-constexpr int kSmem = 2 * kStage + 2 * kOp + 4 * (kTables + kAlpha + 2 * kParts);
+// floats per parity of the chunk: the gates' tables G, W, V and exp(G), and the parts of dg:
+// sums of X's columns, b, <S, E> by warp
+constexpr int kTable = 3 * kC + 4, kParts = 2 * kC + 4;
+// two stages of tiles, the operand's two, outputs on their way out
+constexpr int kSmem = 2 * kStage + 2 * kOp + kTile + 4 * 2 * (kTable + kParts);
+static_assert(kResident * (kSmem + 1024) <= 228 * 1024, "CTAs per SM");
+// scratch of a CTA: S of each chunk as the warps hold it, and q . dQ of each token
+constexpr int kScratchS = kMaxChunks * 4 * kThreads * (int)sizeof(uint4);
+constexpr int kScratch = kScratchS + kMaxChunks * kC * (int)sizeof(float);
 
 struct BwdArgs {
   const bf16 *q, *k, *v, *g, *dout;
@@ -44,39 +53,19 @@ struct BwdArgs {
   int D, M, N, BH, len, n_seg;
   const float *S, *E;    // per-segment entries (nullptr: one segment)
   const float *S0, *dS;  // one segment: the caller's (nullptr: zero)
-  uint4* scratch;        // [CTA][kMaxChunks][4][kThreads]
+  char* scratch;
 };
 
-// Rows 16 r.. of a tile of accumulators as bf16, through this warp's rows of the tile
-// at `at`, in 16-byte pieces.
-__device__ __forceinline__ void store_rows(uint8_t* tile, int r0, const float (&c)[8][4],
-                                           bf16* dst, int live, int width) {
-  const int lane = threadIdx.x & 31, row = lane >> 2, col = (lane & 3) * 2;
-  __syncwarp();
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<uint32_t*>(tile + tile_at<64>(0, r0 + row + 8 * h, j) + col * 2) =
-          pack2(c[j][2 * h], c[j][2 * h + 1]);
-  __syncwarp();
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int r = e * 4 + (lane >> 3), ch = lane & 7;
-    if (r < live && ch * 8 < width)
-      *reinterpret_cast<uint4*>(dst + (size_t)r * width + ch * 8) =
-          *reinterpret_cast<const uint4*>(tile + tile_at<64>(0, r0 + r, ch));
-  }
-}
-
-__device__ __forceinline__ void load_state(float (&x)[8][4], const float* from, int r0, int D,
-                                           int M) {
+// Rows r0.. of a state, 8 NT columns from c0 on
+template <int NT>
+__device__ __forceinline__ void load_state(float (&x)[NT][4], const float* from, int r0, int c0,
+                                           int D, int M) {
   const int lane = threadIdx.x & 31, row = lane >> 2, col = (lane & 3) * 2;
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int d = r0 + row + 8 * h, m = 8 * j + col;
+      const int d = r0 + row + 8 * h, m = c0 + 8 * j + col;
       float2 v = make_float2(0.f, 0.f);
       if (from && d < D && m < M) v = *reinterpret_cast<const float2*>(from + (size_t)d * M + m);
       x[j][2 * h] = v.x;
@@ -84,27 +73,20 @@ __device__ __forceinline__ void load_state(float (&x)[8][4], const float* from, 
     }
 }
 
-__device__ __forceinline__ void store_op(uint8_t* op, int r0, const float (&x)[8][4]) {
-  const int lane = threadIdx.x & 31, row = lane >> 2, col = (lane & 3) * 2;
+// Rows r0.. of a 64 x 64 tile times c, summed over the columns: rows l / 4 and l / 4 + 8
+__device__ __forceinline__ float2 row_dots(const Lane<64>& ln, uint32_t tile, int r0,
+                                           float (&c)[8][4]) {
+  float2 top = make_float2(0.f, 0.f), bottom = top;
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<uint32_t*>(op + tile_at<64>(0, r0 + row + 8 * h, j) + col * 2) =
-          pack2(x[j][2 * h], x[j][2 * h + 1]);
-}
-
-// this warp's rows of `tile` times c, summed over the columns: rows row, row + 8
-__device__ __forceinline__ float2 row_dots(const uint8_t* tile, int r0, const float (&c)[8][4]) {
-  const int lane = threadIdx.x & 31, row = lane >> 2, col = (lane & 3) * 2;
-  float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t a = *reinterpret_cast<const uint32_t*>(tile + tile_at<64>(0, r0 + row, j) + col * 2);
-    const uint32_t b = *reinterpret_cast<const uint32_t*>(tile + tile_at<64>(0, r0 + row + 8, j) + col * 2);
-    s.x = fmaf(lo_of(a), c[j][0], fmaf(hi_of(a), c[j][1], s.x));
-    s.y = fmaf(lo_of(b), c[j][2], fmaf(hi_of(b), c[j][3], s.y));
+  for (int jp = 0; jp < 4; ++jp) {
+    uint32_t r[4];
+    ln.load_a(r, tile, r0, jp);
+    top = fma2(both_of(r[0]), pair_of(c[2 * jp], 0), top);
+    bottom = fma2(both_of(r[1]), pair_of(c[2 * jp], 1), bottom);
+    top = fma2(both_of(r[2]), pair_of(c[2 * jp + 1], 0), top);
+    bottom = fma2(both_of(r[3]), pair_of(c[2 * jp + 1], 1), bottom);
   }
+  float2 s = make_float2(top.x + top.y, bottom.x + bottom.y);
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
     s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
@@ -113,34 +95,22 @@ __device__ __forceinline__ float2 row_dots(const uint8_t* tile, int r0, const fl
   return s;
 }
 
-__device__ __forceinline__ void zero(float (&c)[8][4]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.f;
-}
-
-__device__ __forceinline__ void scale_rows(float (&c)[8][4], float a, float b) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    c[j][0] *= a;
-    c[j][1] *= a;
-    c[j][2] *= b;
-    c[j][3] *= b;
-  }
-}
-
 __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(const BwdArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t base = tc::smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row = lane >> 2, col = (lane & 3) * 2;
-  uint8_t* ops = smem + 2 * kStage;
-  float* tables = reinterpret_cast<float*>(ops + 2 * kOp);
-  float* Gs = tables + warp * 3 * kC;
-  float *Ws = Gs + kC, *Vs = Ws + kC;
-  float* alpha = tables + kTables;
-  float* parts = alpha + kAlpha;
-  const int r0 = ((warp + blockIdx.x) & 3) * 16, rb = r0 >> 4;
-  uint4* scratch = a.scratch + (size_t)blockIdx.x * kMaxChunks * 4 * kThreads + tid;
+  const int row = lane >> 2;
+  // the causal products give a chunk's rows unequal work: turn their order from CTA to
+  // CTA, so that no scheduler gets all of the most
+  const int rb = (warp + blockIdx.x) & 3, r0 = rb * 16;
+  const Lane<64> ln;
+  uint8_t* op_mem = smem + 2 * kStage;
+  const uint32_t op_base = base + 2 * kStage, out_at = op_base + 2 * kOp;
+  float* tables = reinterpret_cast<float*>(op_mem + 2 * kOp + kTile);
+  float* parts = tables + 2 * kTable;
+  char* own = a.scratch + (size_t)blockIdx.x * kScratch;
+  uint4* states = reinterpret_cast<uint4*>(own) + tid;  // [chunk][4][thread]
+  float* alpha = reinterpret_cast<float*>(own + kScratchS);        // [chunk][64]: q . dQ
 
   tc::pdl_wait();
   const int items = a.BH * a.n_seg;
@@ -158,142 +128,85 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       load_tile<64, kThreads>(at + 2 * kTile, a.v + (seq + t0) * a.M, rows, a.M, 0);
       load_tile<64, kThreads>(at + 3 * kTile, a.dout + (seq + t0) * a.M, rows, a.M, 0);
     };
+    // A chunk's tables are made by one warp while the chunk before it is worked on
+    auto raw_gates = [&](int c) { return load_gates(a.g + seq, tb + c * kC, te); };
+    auto make_tables = [&](int c, ushort2 raw) {
+      float* G = tables + (c & 1) * kTable;
+      const float total = chunk_gates<false>(gates_of(raw), G, G + kC);
+      *reinterpret_cast<float2*>(G + 2 * kC + 2 * lane) =
+          make_float2(ex2(G[2 * lane]), ex2(G[2 * lane + 1]));
+      if (lane == 0) G[3 * kC] = gated_decay(total * kLn2);
+    };
 
-    __syncthreads();  // the tiles of the item before are done with
+    __syncthreads();  // the item before is done with
     load_chunk(0);
     cp_async_commit();
-    float2 g_next = load_gates(a.g + seq, tb, te);
+    if (warp == 0) make_tables(0, raw_gates(0));
+
+    // ---- forward: dQ
     float x[8][4];  // S, then E
     load_state(x, a.S ? a.S + ((size_t)bh * (a.n_seg + 1) + seg) * DM : a.S0 ? a.S0 + bh * DM : nullptr,
-               r0, a.D, a.M);
-    store_op(ops, r0, x);
-
-    // ---- forward: dQ, a
+               r0, 0, a.D, a.M);
+    store_op(ln, op_base, r0, 0, x);
     for (int c = 0; c < chunks; ++c) {
       cp_async_wait<0>();
       __syncthreads();
-      const float2 g = g_next;
-      if (c + 1 < chunks) {
-        load_chunk(c + 1);
-        g_next = load_gates(a.g + seq, tb + (c + 1) * kC, te);
-      }
+      if (c + 1 < chunks) load_chunk(c + 1);
       cp_async_commit();
-      const float total = chunk_gates<false>(g, Gs, Ws);
-      const float dec = gated_decay(total * kLn2);
+      const float *Gs = tables + (c & 1) * kTable, *Ws = Gs + kC;
       const uint32_t q_at = base + (c & 1) * kStage, k_at = q_at + kTile, v_at = k_at + kTile,
-                     do_at = v_at + kTile, op = base + 2 * kStage + (c & 1) * kOp;
-      // S of this chunk, for the way back
+                     do_at = v_at + kTile;
+      const bool maker = c + 1 < chunks && warp == (c & 3);
+      ushort2 raw = make_ushort2(0, 0);
+      if (maker) raw = raw_gates(c + 1);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        scratch[(c * 4 + e) * kThreads] =
+        states[(c * 4 + e) * kThreads] =
             make_uint4(pack2(x[2 * e][0], x[2 * e][1]), pack2(x[2 * e][2], x[2 * e][3]),
                        pack2(x[2 * e + 1][0], x[2 * e + 1][1]), pack2(x[2 * e + 1][2], x[2 * e + 1][3]));
-      uint32_t da[4][4];
-      float dq[8][4];
-      zero(dq);
+      uint32_t f[4][4], p[4];
+      float d[8][4];
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) load_a<64>(da[ks], do_at, r0, 2 * ks);
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-        for (int jp = 0; jp < 4; ++jp) {
-          uint32_t b[4];
-          load_b<64>(b, op, 16 * jp, 2 * ks);
-          mma16816(dq[2 * jp], da[ks], b[0], b[1]);
-          mma16816(dq[2 * jp + 1], da[ks], b[2], b[3]);
-        }
+      for (int ks = 0; ks < 4; ++ks) ln.load_a(f[ks], do_at, r0, ks);
+      product<false>(ln, d, f, op_base + (c & 1) * kOp);
       const float gi[2] = {Gs[r0 + row], Gs[r0 + row + 8]};
-      scale_rows(dq, ex2(gi[0]), ex2(gi[1]));
-      const float2 al = row_dots(smem + (q_at - base), r0, dq);
+      scale_rows(d, ex2(gi[0]), ex2(gi[1]));
+#pragma unroll 1
+      for (int jb = 0; jb < rb; ++jb) {
+        masked_block<true, false>(ln, p, f, v_at, jb, gi, Gs);
+        add_block(ln, d, p, k_at, jb);
+      }
+      masked_block<true, true>(ln, p, f, v_at, rb, gi, Gs);
+      add_block(ln, d, p, k_at, rb);
+      const float2 dots = row_dots(ln, q_at, r0, d);
       if ((lane & 3) == 0) {
-        alpha[c * kC + r0 + row] = al.x;
-        alpha[c * kC + r0 + row + 8] = al.y;
+        alpha[c * kC + r0 + row] = dots.x;
+        alpha[c * kC + r0 + row + 8] = dots.y;
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[j][e] *= dec;
-#pragma unroll
-      for (int jb = 0; jb < 4; ++jb) {
-        if (jb <= rb) {
-          float p[2][4] = {};
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            uint32_t b[4];
-            load_b<64>(b, v_at, 16 * jb, 2 * ks);
-            mma16816(p[0], da[ks], b[0], b[1]);
-            mma16816(p[1], da[ks], b[2], b[3]);
-          }
-          uint32_t pa[4];
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const float2 gj = *reinterpret_cast<const float2*>(&Gs[16 * jb + 8 * t + col]);
-            float w[4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int j = 8 * t + col, r = row + 8 * h;
-              w[2 * h] = jb < rb || j <= r ? p[t][2 * h] * ex2(gi[h] - gj.x) : 0.f;
-              w[2 * h + 1] = jb < rb || j + 1 <= r ? p[t][2 * h + 1] * ex2(gi[h] - gj.y) : 0.f;
-            }
-            pa[2 * t] = pack2(w[0], w[1]);
-            pa[2 * t + 1] = pack2(w[2], w[3]);
-          }
-#pragma unroll
-          for (int jp = 0; jp < 4; ++jp) {
-            uint32_t b[4];
-            load_b_t<64>(b, k_at, 16 * jb, 2 * jp);
-            mma16816(dq[2 * jp], pa, b[0], b[1]);
-            mma16816(dq[2 * jp + 1], pa, b[2], b[3]);
-          }
-        }
-        if (c + 1 < chunks) {
-          uint32_t ka[4], hi[4], lo[4];
-          load_a_t<64>(ka, k_at, 16 * jb, 2 * rb);
-          const float2 w0 = *reinterpret_cast<const float2*>(&Ws[16 * jb + col]);
-          const float2 w8 = *reinterpret_cast<const float2*>(&Ws[16 * jb + 8 + col]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 w = e < 2 ? w0 : w8;
-            scale_split(ka[e], w.x, w.y, hi[e], lo[e]);
-          }
-#pragma unroll
-          for (int jp = 0; jp < 4; ++jp) {
-            uint32_t b[4];
-            load_b_t<64>(b, v_at, 16 * jb, 2 * jp);
-            mma16816(x[2 * jp], hi, b[0], b[1]);
-            mma16816(x[2 * jp + 1], hi, b[2], b[3]);
-            mma16816(x[2 * jp], lo, b[0], b[1]);
-            mma16816(x[2 * jp + 1], lo, b[2], b[3]);
-          }
-        }
-      }
-      if (c + 1 < chunks) store_op(ops + ((c + 1) & 1) * kOp, r0, x);
       const int t0 = tb + c * kC + r0;
-      store_rows(smem + (do_at - base), r0, dq, a.dq + (seq + t0) * a.D, te - t0, a.D);
+      store_rows(ln, out_at, r0, d, a.dq + (seq + t0) * a.D, te - t0, a.D, a.D);
+      if (c + 1 < chunks) {
+        const float dec = Gs[3 * kC];
+        scale_rows(x, dec, dec);
+        add_outer(ln, ln, x, k_at, Ws, rb, v_at, 0);
+        store_op(ln, op_base + ((c + 1) & 1) * kOp, r0, 0, x);
+      }
+      if (maker) make_tables(c + 1, raw);
     }
 
-    // ---- back: dK, dV, dg
-    __syncthreads();
-    load_chunk(chunks - 1);  // (its dO rows were written over)
-    cp_async_commit();
-    g_next = load_gates(a.g + seq, tb + (chunks - 1) * kC, te);
+    // ---- back: dV, dK, dg. The last two chunks' tiles and tables are still there.
     load_state(x, a.E ? a.E + ((size_t)bh * (a.n_seg + 1) + seg + 1) * DM : a.dS ? a.dS + bh * DM : nullptr,
-               r0, a.D, a.M);
-    store_op(ops, r0, x);
+               r0, 0, a.D, a.M);
+    __syncthreads();
+    store_op(ln, op_base, r0, 0, x);
     // dg of chunk c from the parts its warps left (one warp)
     auto finish = [&](int c) {
       const float* at = parts + (c & 1) * kParts;
-      const int t = 2 * lane;
-      float xs[2], bs[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float rows = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) rows += at[w * kC + t + e];
-        xs[e] = rows - at[4 * kC + t + e] + alpha[c * kC + t + e];
-        bs[e] = at[5 * kC + t + e];
-      }
-      float down = xs[0] + xs[1], up = bs[0] + bs[1];
+      const float2 rows = *reinterpret_cast<const float2*>(alpha + c * kC + 2 * lane);
+      const float2 cols = *reinterpret_cast<const float2*>(at + 2 * lane);
+      const float2 be = *reinterpret_cast<const float2*>(at + kC + 2 * lane);
+      const float x0 = rows.x - cols.x, x1 = rows.y - cols.y;
+      float down = x0 + x1, up = be.x + be.y;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const float d = __shfl_down_sync(0xffffffffu, down, o);
@@ -304,172 +217,86 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       float after = __shfl_down_sync(0xffffffffu, down, 1), before = __shfl_up_sync(0xffffffffu, up, 1);
       if (lane == 31) after = 0.f;
       if (lane == 0) before = 0.f;
-      const float se = at[6 * kC] + at[6 * kC + 1] + at[6 * kC + 2] + at[6 * kC + 3];
-      const int tok = tb + c * kC + t;
+      const float se = at[2 * kC] + at[2 * kC + 1] + at[2 * kC + 2] + at[2 * kC + 3];
+      const int tok = tb + c * kC + 2 * lane;
       if (tok < te) a.dg[seq + tok] = __float2bfloat16_rn(se + down + before);
-      if (tok + 1 < te) a.dg[seq + tok + 1] = __float2bfloat16_rn(se + (xs[1] + after) + (before + bs[0]));
+      if (tok + 1 < te) a.dg[seq + tok + 1] = __float2bfloat16_rn(se + (x1 + after) + (before + be.x));
     };
 
     for (int c = chunks - 1; c >= 0; --c) {
       cp_async_wait<0>();
       __syncthreads();
-      const float2 g = g_next;
-      if (c > 0) {
-        load_chunk(c - 1);
-        g_next = load_gates(a.g + seq, tb + (c - 1) * kC, te);
-      }
+      if (c > 0 && c + 1 < chunks) load_chunk(c - 1);
       cp_async_commit();
-      if (c + 1 < chunks && warp == (c & 3)) finish(c + 1);
-      chunk_gates<true>(g, Gs, Vs);  // Vs: exp(G_i)
-      const float total = chunk_gates<false>(g, Gs, Ws);
-      const float dec = gated_decay(total * kLn2);
       const int step = chunks - 1 - c;
-      const uint32_t q_at = base + (c & 1) * kStage, k_at = q_at + kTile, v_at = k_at + kTile,
-                     do_at = v_at + kTile, op = base + 2 * kStage + (step & 1) * kOp;
+      const float *Gs = tables + (c & 1) * kTable, *Ws = Gs + kC, *Vs = Ws + kC;
       float* part = parts + (c & 1) * kParts;
+      const uint32_t q_at = base + (c & 1) * kStage, k_at = q_at + kTile, v_at = k_at + kTile,
+                     do_at = v_at + kTile, op = op_base + (step & 1) * kOp;
+      const bool maker = c > 0 && c + 1 < chunks && warp == (c & 3);
+      ushort2 raw = make_ushort2(0, 0);
+      if (maker) raw = raw_gates(c - 1);
+      uint4 sc[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[e] = states[(c * 4 + e) * kThreads];
+      if (c + 1 < chunks && warp == ((c + 1) & 3)) finish(c + 1);
+      const float dec = Gs[3 * kC], w0 = Ws[r0 + row], w1 = Ws[r0 + row + 8];
+      const float gj[2] = {Gs[r0 + row], Gs[r0 + row + 8]};
+      const int t0 = tb + c * kC + r0;
+      uint32_t f[4][4], p[4];
+      float d[8][4];
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) ln.load_a(f[ks], k_at, r0, ks);
+      product<true>(ln, d, f, op);
+      scale_rows(d, w0, w1);
+      masked_block<false, true>(ln, p, f, q_at, rb, gj, Gs);
+      add_block(ln, d, p, do_at, rb);
+#pragma unroll 1
+      for (int ib = rb + 1; ib < 4; ++ib) {
+        masked_block<false, false>(ln, p, f, q_at, ib, gj, Gs);
+        add_block(ln, d, p, do_at, ib);
+      }
+      store_rows(ln, out_at, r0, d, a.dv + (seq + t0) * a.M, te - t0, a.M, a.M);
       {
-        float se = 0.f;
+        float2 se = make_float2(0.f, 0.f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint4 s = scratch[(c * 4 + e) * kThreads];
-          se = fmaf(lo_of(s.x), x[2 * e][0], fmaf(hi_of(s.x), x[2 * e][1], se));
-          se = fmaf(lo_of(s.y), x[2 * e][2], fmaf(hi_of(s.y), x[2 * e][3], se));
-          se = fmaf(lo_of(s.z), x[2 * e + 1][0], fmaf(hi_of(s.z), x[2 * e + 1][1], se));
-          se = fmaf(lo_of(s.w), x[2 * e + 1][2], fmaf(hi_of(s.w), x[2 * e + 1][3], se));
+          se = fma2(both_of(sc[e].x), pair_of(x[2 * e], 0), se);
+          se = fma2(both_of(sc[e].y), pair_of(x[2 * e], 1), se);
+          se = fma2(both_of(sc[e].z), pair_of(x[2 * e + 1], 0), se);
+          se = fma2(both_of(sc[e].w), pair_of(x[2 * e + 1], 1), se);
         }
+        float s = se.x + se.y;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) se += __shfl_xor_sync(0xffffffffu, se, o);
-        if (lane == 0) part[6 * kC + warp] = se * dec;
-      }
-      uint32_t ka[4][4], va[4][4];
-      float dk[8][4], dv[8][4];
-      zero(dk);
-      zero(dv);
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        load_a<64>(ka[ks], k_at, r0, 2 * ks);
-        load_a<64>(va[ks], v_at, r0, 2 * ks);
+        for (int o = 1; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) part[2 * kC + warp] = s * dec;
       }
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-        for (int jp = 0; jp < 4; ++jp) {
-          uint32_t b[4];
-          load_b<64>(b, op, 16 * jp, 2 * ks);  // E^T
-          mma16816(dk[2 * jp], va[ks], b[0], b[1]);
-          mma16816(dk[2 * jp + 1], va[ks], b[2], b[3]);
-          load_b_t<64>(b, op, 16 * ks, 2 * jp);
-          mma16816(dv[2 * jp], ka[ks], b[0], b[1]);
-          mma16816(dv[2 * jp + 1], ka[ks], b[2], b[3]);
-        }
-      {
-        const float w0 = Ws[r0 + row], w1 = Ws[r0 + row + 8];
-        scale_rows(dk, w0, w1);
-        scale_rows(dv, w0, w1);
-        const float2 be = row_dots(smem + (v_at - base), r0, dv);
-        if ((lane & 3) == 0) {
-          part[5 * kC + r0 + row] = be.x;
-          part[5 * kC + r0 + row + 8] = be.y;
-        }
+      for (int ks = 0; ks < 4; ++ks) ln.load_a(f[ks], v_at, r0, ks);
+      product<false>(ln, d, f, op);
+      scale_rows(d, w0, w1);
+      const float2 be = row_dots(ln, k_at, r0, d);
+      masked_block<false, true>(ln, p, f, do_at, rb, gj, Gs);
+      add_block(ln, d, p, q_at, rb);
+#pragma unroll 1
+      for (int ib = rb + 1; ib < 4; ++ib) {
+        masked_block<false, false>(ln, p, f, do_at, ib, gj, Gs);
+        add_block(ln, d, p, q_at, ib);
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[j][e] *= dec;
-      const float gj[2] = {Gs[r0 + row], Gs[r0 + row + 8]};
-      float cols[2] = {0.f, 0.f};
-#pragma unroll
-      for (int ib = 0; ib < 4; ++ib) {
-        uint32_t db[4][4];
-#pragma unroll
-        for (int jp = 0; jp < 4; ++jp) load_b_t<64>(db[jp], do_at, 16 * ib, 2 * jp);
-        if (ib >= rb) {
-          float p[2][4] = {}, dp[2][4] = {};
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            uint32_t b[4];
-            load_b<64>(b, q_at, 16 * ib, 2 * ks);
-            mma16816(p[0], ka[ks], b[0], b[1]);
-            mma16816(p[1], ka[ks], b[2], b[3]);
-            load_b<64>(b, do_at, 16 * ib, 2 * ks);
-            mma16816(dp[0], va[ks], b[0], b[1]);
-            mma16816(dp[1], va[ks], b[2], b[3]);
-          }
-          uint32_t pa[4], dpa[4];
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const float2 gi = *reinterpret_cast<const float2*>(&Gs[16 * ib + 8 * t + col]);
-            float w[4], dw[4], rows[2] = {0.f, 0.f};
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int i = 8 * t + col + e, j = row + 8 * h, at = 2 * h + e;
-                const float L = ib > rb || i >= j ? ex2((e ? gi.y : gi.x) - gj[h]) : 0.f;
-                w[at] = p[t][at] * L;
-                dw[at] = dp[t][at] * L;
-                const float xx = ib > rb || i > j ? p[t][at] * dw[at] : 0.f;
-                rows[e] += xx;
-                cols[h] += xx;
-              }
-            pa[2 * t] = pack2(w[0], w[1]);
-            pa[2 * t + 1] = pack2(w[2], w[3]);
-            dpa[2 * t] = pack2(dw[0], dw[1]);
-            dpa[2 * t + 1] = pack2(dw[2], dw[3]);
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-              rows[0] += __shfl_xor_sync(0xffffffffu, rows[0], o);
-              rows[1] += __shfl_xor_sync(0xffffffffu, rows[1], o);
-            }
-            if (row == 0)
-              *reinterpret_cast<float2*>(part + warp * kC + 16 * ib + 8 * t + col) =
-                  make_float2(rows[0], rows[1]);
-          }
-#pragma unroll
-          for (int jp = 0; jp < 4; ++jp) {
-            mma16816(dv[2 * jp], pa, db[jp][0], db[jp][1]);
-            mma16816(dv[2 * jp + 1], pa, db[jp][2], db[jp][3]);
-            uint32_t b[4];
-            load_b_t<64>(b, q_at, 16 * ib, 2 * jp);
-            mma16816(dk[2 * jp], dpa, b[0], b[1]);
-            mma16816(dk[2 * jp + 1], dpa, b[2], b[3]);
-          }
-        } else if (row == 0) {
-          *reinterpret_cast<float2*>(part + warp * kC + 16 * ib + col) = make_float2(0.f, 0.f);
-          *reinterpret_cast<float2*>(part + warp * kC + 16 * ib + 8 + col) = make_float2(0.f, 0.f);
-        }
-        if (c > 0) {
-          uint32_t qa[4], hi[4], lo[4];
-          load_a_t<64>(qa, q_at, 16 * ib, 2 * rb);
-          const float2 w0 = *reinterpret_cast<const float2*>(&Vs[16 * ib + col]);
-          const float2 w8 = *reinterpret_cast<const float2*>(&Vs[16 * ib + 8 + col]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 w = e < 2 ? w0 : w8;
-            scale_split(qa[e], w.x, w.y, hi[e], lo[e]);
-          }
-#pragma unroll
-          for (int jp = 0; jp < 4; ++jp) {
-            mma16816(x[2 * jp], hi, db[jp][0], db[jp][1]);
-            mma16816(x[2 * jp + 1], hi, db[jp][2], db[jp][3]);
-            mma16816(x[2 * jp], lo, db[jp][0], db[jp][1]);
-            mma16816(x[2 * jp + 1], lo, db[jp][2], db[jp][3]);
-          }
-        }
-      }
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        cols[0] += __shfl_xor_sync(0xffffffffu, cols[0], o);
-        cols[1] += __shfl_xor_sync(0xffffffffu, cols[1], o);
-      }
+      const float2 all = row_dots(ln, k_at, r0, d);
       if ((lane & 3) == 0) {
-        part[4 * kC + r0 + row] = cols[0];
-        part[4 * kC + r0 + row + 8] = cols[1];
+        part[r0 + row] = all.x - be.x;
+        part[r0 + row + 8] = all.y - be.y;
+        part[kC + r0 + row] = be.x;
+        part[kC + r0 + row + 8] = be.y;
       }
-      if (c > 0) store_op(ops + ((step + 1) & 1) * kOp, r0, x);
-      const int t0 = tb + c * kC + r0;
-      store_rows(smem + (k_at - base), r0, dk, a.dk + (seq + t0) * a.D, te - t0, a.D);
-      store_rows(smem + (v_at - base), r0, dv, a.dv + (seq + t0) * a.M, te - t0, a.M);
+      store_rows(ln, out_at, r0, d, a.dk + (seq + t0) * a.D, te - t0, a.D, a.D);
+      if (c > 0) {
+        scale_rows(x, dec, dec);
+        add_outer(ln, ln, x, q_at, Vs, rb, do_at, 0);
+        store_op(ln, op_base + ((step + 1) & 1) * kOp, r0, 0, x);
+      }
+      if (maker) make_tables(c - 1, raw);
     }
     __syncthreads();
     if (warp == 0) finish(0);
@@ -500,7 +327,7 @@ GatedPlan gated_mma_backward_plan(int BH, int N) {
 }
 
 size_t gated_mma_backward_scratch(const GatedPlan& p) {
-  return sizeof(uint4) * (size_t)backward_grid(p) * kMaxChunks * 4 * kThreads;
+  return (size_t)backward_grid(p) * kScratch;
 }
 
 cudaError_t gated_mma_backward(const GatedBackward& f, const GatedPlan& p, const GatedWorkspace& w,
@@ -535,7 +362,7 @@ cudaError_t gated_mma_backward(const GatedBackward& f, const GatedPlan& p, const
   a.n_seg = p.n_seg;
   a.S0 = f.S0;
   a.dS = f.dS;
-  a.scratch = static_cast<uint4*>(w.scratch);
+  a.scratch = static_cast<char*>(w.scratch);
   if ((e = tcx::configure(gated_backward_kernel, kSmem)) != cudaSuccess) return e;
   e = tcx::launch_pdl(gated_backward_kernel, dim3((unsigned)backward_grid(p)), dim3(kThreads), kSmem,
                       st, a);

@@ -19,11 +19,6 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kC = 64;  // rows (tokens) of a tile
 
-template <int COLS>
-__device__ __forceinline__ uint32_t tile_at(uint32_t base, int row, int chunk) {
-  return base + (uint32_t)(row * COLS * 2 + ((chunk ^ (row & 7)) << 4));
-}
-
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -35,41 +30,46 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr));
 }
 
-// The four matrix fragments, each 16 x 16 of a tile with origin (row, 8 * chunk):
-// A, rows of the tile as rows of A
-template <int COLS>
-__device__ __forceinline__ void load_a(uint32_t (&r)[4], uint32_t base, int row, int chunk) {
-  const int l = threadIdx.x & 31;
-  ldsm(r, tile_at<COLS>(base, row + (l & 15), chunk + (l >> 4)));
-}
-// A, columns of the tile as rows of A
-template <int COLS>
-__device__ __forceinline__ void load_a_t(uint32_t (&r)[4], uint32_t base, int row, int chunk) {
-  const int l = threadIdx.x & 31;
-  ldsm_t(r, tile_at<COLS>(base, row + (l & 7) + ((l >> 4) << 3), chunk + ((l >> 3) & 1)));
-}
-// B for two neighbouring column tiles (r[0], r[1] and r[2], r[3]), rows of the tile as
-// columns of B
-template <int COLS>
-__device__ __forceinline__ void load_b(uint32_t (&r)[4], uint32_t base, int row, int chunk) {
-  const int l = threadIdx.x & 31;
-  ldsm(r, tile_at<COLS>(base, row + (l & 7) + ((l >> 4) << 3), chunk + ((l >> 3) & 1)));
-}
-// the same, rows of the tile as rows of B
-template <int COLS>
-__device__ __forceinline__ void load_b_t(uint32_t (&r)[4], uint32_t base, int row, int chunk) {
-  const int l = threadIdx.x & 31;
-  ldsm_t(r, tile_at<COLS>(base, row + (l & 15), chunk + (l >> 4)));
+__device__ __forceinline__ void stsm(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
 }
 
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
+// A lane's offsets in a tile, for the accesses below. Chunk c of a row r of any eight is
+// at (c ^ r) within its row, and tiles are aligned to their rows, so moving on by whole
+// column pairs is one exclusive or of the lane's address, and by rows an immediate.
+template <int COLS>
+struct Lane {
+  uint32_t a, b;
+  __device__ __forceinline__ Lane() {
+    const int l = threadIdx.x & 31, r = (l & 7) + ((l >> 4) << 3);
+    a = (l & 15) * COLS * 2 + (((l >> 4) ^ (l & 7)) << 4);
+    b = r * COLS * 2 + ((((l >> 3) & 1) ^ (l & 7)) << 4);
+  }
+  // the 16 x 16 fragments at (row, 16 * pair), row a multiple of 8:
+  // A, rows of the tile as rows of A. (Also the layout of two neighbouring accumulator
+  // tiles: r[0], r[1] are rows l / 4, l / 4 + 8 of the first, r[2], r[3] of the second.)
+  __device__ __forceinline__ void load_a(uint32_t (&r)[4], uint32_t base, int row, int pair) const {
+    ldsm(r, ((base + a) ^ (pair << 5)) + row * COLS * 2);
+  }
+  // A, columns of the tile as rows of A
+  __device__ __forceinline__ void load_a_t(uint32_t (&r)[4], uint32_t base, int row, int pair) const {
+    ldsm_t(r, ((base + b) ^ (pair << 5)) + row * COLS * 2);
+  }
+  // B for two neighbouring column tiles (r[0], r[1] and r[2], r[3]), rows of the tile as
+  // columns of B
+  __device__ __forceinline__ void load_b(uint32_t (&r)[4], uint32_t base, int row, int pair) const {
+    ldsm(r, ((base + b) ^ (pair << 5)) + row * COLS * 2);
+  }
+  // the same, rows of the tile as rows of B
+  __device__ __forceinline__ void load_b_t(uint32_t (&r)[4], uint32_t base, int row, int pair) const {
+    ldsm_t(r, ((base + a) ^ (pair << 5)) + row * COLS * 2);
+  }
+  // two neighbouring accumulator tiles, packed as load_a has them
+  __device__ __forceinline__ void store(uint32_t base, int row, int pair, const float (&c)[4],
+                                        const float (&d)[4]) const;
+};
 
 // Two floats rounded to bf16, `lo` in the lower half.
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -78,13 +78,75 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 __device__ __forceinline__ float lo_of(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_of(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+__device__ __forceinline__ float2 both_of(uint32_t u) { return make_float2(lo_of(u), hi_of(u)); }
 
-// bf16 pair u times (x, y), as the sum of two bf16 pairs: the product to 16 bits
-__device__ __forceinline__ void scale_split(uint32_t u, float x, float y, uint32_t& hi,
-                                            uint32_t& lo) {
-  const float a = lo_of(u) * x, b = hi_of(u) * y;
-  hi = pack2(a, b);
-  lo = pack2(a - lo_of(hi), b - hi_of(hi));
+template <int COLS>
+__device__ __forceinline__ void Lane<COLS>::store(uint32_t base, int row, int pair,
+                                                  const float (&c)[4], const float (&d)[4]) const {
+  stsm(((base + a) ^ (pair << 5)) + row * COLS * 2, pack2(c[0], c[1]), pack2(c[2], c[3]),
+       pack2(d[0], d[1]), pack2(d[2], d[3]));
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// the same from zero
+__device__ __forceinline__ void mma16816_0(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                           uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// The halves of an accumulator's row pairs (columns 2 (l % 4) + {0, 1} of rows l / 4 and
+// l / 4 + 8), two float32 at a time
+__device__ __forceinline__ float2& pair_of(float (&c)[4], int h) {
+  return *reinterpret_cast<float2*>(&c[2 * h]);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+        "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  uint64_t d;
+  asm("sub.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+
+template <int NT>
+__device__ __forceinline__ void scale_rows(float (&c)[NT][4], float top, float bottom) {
+  const float2 t = make_float2(top, top), b = make_float2(bottom, bottom);
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    pair_of(c[j], 0) = mul2(pair_of(c[j], 0), t);
+    pair_of(c[j], 1) = mul2(pair_of(c[j], 1), b);
+  }
+}
+
+// bf16 pair u times w, as the sum of two bf16 pairs: the product to 16 bits
+__device__ __forceinline__ void scale_split(uint32_t u, float2 w, uint32_t& hi, uint32_t& lo) {
+  const float2 p = mul2(both_of(u), w);
+  hi = pack2(p.x, p.y);
+  const float2 r = sub2(p, both_of(hi));
+  lo = pack2(r.x, r.y);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -106,18 +168,171 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// x, in a way that keeps what is computed from it where it is used: hoisted out of a
+// chunk loop, the addresses would hold registers through it.
+__device__ __forceinline__ int here(int x) {
+  asm volatile("" : "+r"(x));
+  return x;
+}
+
 // 64 rows of COLS columns, from column c0 of rows of `width` elements, to a tile;
 // rows from `rows` on and columns past `width` become zero (nothing is read there).
 template <int COLS, int THREADS>
 __device__ __forceinline__ void load_tile(uint32_t base, const bf16* src, int rows, int width,
                                           int c0) {
-  constexpr int PER = COLS / 8;
+  constexpr int PER = COLS / 8, STEP = THREADS / PER;  // rows the threads cover at once
+  static_assert(STEP % 8 == 0, "a thread's chunk stays where it is in its rows");
+  const int tid = here(threadIdx.x), row = tid / PER, chunk = tid % PER;
+  const uint32_t to = base + row * COLS * 2 + ((chunk ^ (row & 7)) << 4);
+  const bf16* from = src + (size_t)row * width + c0 + chunk * 8;
+  const bool wide = c0 + chunk * 8 < width;
 #pragma unroll
-  for (int i = 0; i < kC * PER / THREADS; ++i) {
-    const int at = threadIdx.x + i * THREADS, row = at / PER, chunk = at % PER;
-    const bool live = row < rows && c0 + chunk * 8 < width;
-    cp_async16(tile_at<COLS>(base, row, chunk),
-               live ? src + (size_t)row * width + c0 + chunk * 8 : src, live);
+  for (int i = 0; i < kC / STEP; ++i) {
+    const bool live = wide && row + i * STEP < rows;
+    cp_async16(to + i * STEP * COLS * 2, live ? from + (size_t)i * STEP * width : src, live);
+  }
+}
+
+// Rows r0 .. r0 + 15 of a warp's 16 x 64 result, through those rows of the tile at `tile`
+// (the warp's own meanwhile), written in 16-byte pieces to rows of `width` elements at
+// dst; `live` rows of them, columns up to `width`.
+template <int COLS>
+__device__ __forceinline__ void store_rows(const Lane<COLS>& ln, uint32_t tile, int r0,
+                                           const float (&c)[8][4], bf16* dst, int live, int width,
+                                           int stride) {
+  const int l = here(threadIdx.x & 31), r = l >> 3, ch = l & 7;
+  __syncwarp();
+#pragma unroll
+  for (int jp = 0; jp < 4; ++jp) ln.store(tile, r0, jp, c[2 * jp], c[2 * jp + 1]);
+  __syncwarp();
+  const uint32_t at = tile + (r0 + r) * COLS * 2 + ((ch ^ r) << 4);
+  bf16* to = dst + (size_t)r * stride + ch * 8;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"((at ^ ((e & 1) << 6)) + e * 4 * COLS * 2));
+    if (e * 4 + r < live && ch * 8 < width)
+      __stcs(reinterpret_cast<uint4*>(to + (size_t)e * 4 * stride), v);
+  }
+}
+
+// A state's rows r0 .. as an operand
+template <int NT>
+__device__ __forceinline__ void store_op(const Lane<64>& ln, uint32_t op, int r0, int c0,
+                                         const float (&x)[NT][4]) {
+#pragma unroll
+  for (int jp = 0; jp < NT / 2; ++jp) ln.store(op, r0, c0 / 16 + jp, x[2 * jp], x[2 * jp + 1]);
+}
+
+// x += (columns 16 col16.. of tile `a`, weighted by `w` along its rows)^T (columns c0.. of
+// tile `b`), over 64 rows. FIRST: from zero.
+template <int COLS, int NT, bool FIRST = false>
+__device__ __forceinline__ void add_outer(const Lane<COLS>& la, const Lane<64>& lb, float (&x)[NT][4],
+                                          uint32_t a, const float* w, int col16, uint32_t b, int c0) {
+  const int col = (threadIdx.x & 3) * 2;
+#pragma unroll
+  for (int at = 0; at < kC; at += 16) {
+    uint32_t f[4], hi[4], lo[4], y[NT / 2][4];
+    la.load_a_t(f, a, at, col16);
+#pragma unroll
+    for (int jp = 0; jp < NT / 2; ++jp) lb.load_b_t(y[jp], b, at, c0 / 16 + jp);
+    const float2 w0 = *reinterpret_cast<const float2*>(w + at + col);
+    const float2 w8 = *reinterpret_cast<const float2*>(w + at + 8 + col);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) scale_split(f[e], e < 2 ? w0 : w8, hi[e], lo[e]);
+#pragma unroll
+    for (int jp = 0; jp < NT / 2; ++jp) {
+      if (FIRST && at == 0) {
+        mma16816_0(x[2 * jp], hi, y[jp][0], y[jp][1]);
+        mma16816_0(x[2 * jp + 1], hi, y[jp][2], y[jp][3]);
+      } else {
+        mma16816(x[2 * jp], hi, y[jp][0], y[jp][1]);
+        mma16816(x[2 * jp + 1], hi, y[jp][2], y[jp][3]);
+      }
+    }
+#pragma unroll
+    for (int jp = 0; jp < NT / 2; ++jp) {
+      mma16816(x[2 * jp], lo, y[jp][0], y[jp][1]);
+      mma16816(x[2 * jp + 1], lo, y[jp][2], y[jp][3]);
+    }
+  }
+}
+
+// c = A B for A's fragments of 16 rows by 16 KS and the 64 columns of B, which are the
+// rows of the tile, or (TRANS) B's rows are
+template <bool TRANS, int KS>
+__device__ __forceinline__ void product(const Lane<64>& ln, float (&c)[8][4],
+                                        const uint32_t (&a)[KS][4], uint32_t tile) {
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+    for (int jp = 0; jp < 4; ++jp) {
+      uint32_t b[4];
+      if (TRANS)
+        ln.load_b_t(b, tile, 16 * ks, jp);
+      else
+        ln.load_b(b, tile, 16 * jp, ks);
+      if (ks == 0) {
+        mma16816_0(c[2 * jp], a[ks], b[0], b[1]);
+        mma16816_0(c[2 * jp + 1], a[ks], b[2], b[3]);
+      } else {
+        mma16816(c[2 * jp], a[ks], b[0], b[1]);
+        mma16816(c[2 * jp + 1], a[ks], b[2], b[3]);
+      }
+    }
+}
+
+// A block of 16 x 16 of (A B^T) * L as an A operand: A's fragments, B the rows 16 cb.. of
+// a tile, G the chunk's gate sums (gr: of A's rows l / 4 and l / 4 + 8). LOWER: A's rows
+// are the later tokens (L = exp(g_row - g_col)), else B's are. DIAGONAL: the block where
+// both are the same tokens, half of it zero.
+template <bool LOWER, bool DIAGONAL, int COLS, int KS>
+__device__ __forceinline__ void masked_block(const Lane<COLS>& ln, uint32_t (&out)[4],
+                                             const uint32_t (&a)[KS][4], uint32_t tile, int cb,
+                                             const float (&gr)[2], const float* G) {
+  const int l = threadIdx.x & 31, row = l >> 2, col = (l & 3) * 2;
+  float p[2][4];
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) {
+    uint32_t b[4];
+    ln.load_b(b, tile, 16 * cb, ks);
+    if (ks == 0) {
+      mma16816_0(p[0], a[ks], b[0], b[1]);
+      mma16816_0(p[1], a[ks], b[2], b[3]);
+    } else {
+      mma16816(p[0], a[ks], b[0], b[1]);
+      mma16816(p[1], a[ks], b[2], b[3]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const float2 gc = *reinterpret_cast<const float2*>(G + 16 * cb + 8 * t + col);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float2 g2 = make_float2(gr[h], gr[h]);
+      const float2 e = LOWER ? sub2(g2, gc) : sub2(gc, g2);
+      float2 w = mul2(pair_of(p[t], h), make_float2(ex2(e.x), ex2(e.y)));
+      if (DIAGONAL) {
+        const int c = 8 * t + col, r = row + 8 * h;
+        w.x = (LOWER ? c <= r : c >= r) ? w.x : 0.f;
+        w.y = (LOWER ? c + 1 <= r : c + 1 >= r) ? w.y : 0.f;
+      }
+      out[2 * t + h] = pack2(w.x, w.y);
+    }
+  }
+}
+
+// c += the block's product with the rows 16 cb.. of a tile of 64 columns
+__device__ __forceinline__ void add_block(const Lane<64>& ln, float (&c)[8][4], const uint32_t (&a)[4],
+                                          uint32_t tile, int cb) {
+#pragma unroll
+  for (int jp = 0; jp < 4; ++jp) {
+    uint32_t b[4];
+    ln.load_b_t(b, tile, 16 * cb, jp);
+    mma16816(c[2 * jp], a, b[0], b[1]);
+    mma16816(c[2 * jp + 1], a, b[2], b[3]);
   }
 }
 
