@@ -9,7 +9,9 @@ allocator). Every step of the computation runs in the library's CUDA kernels;
 there is no fallback. If the library is missing the calls raise.
 """
 
+import contextlib
 import ctypes
+import functools
 import os
 
 __all__ = [
@@ -137,12 +139,21 @@ def _on_device(device):
     per-device state (la_forward_noalloc's fixed scratch) on the current device, and the
     stream it is handed belongs to `device`."""
     import torch
+    if device.index is not None and torch.cuda.current_device() == device.index:
+        return _ALREADY
     return torch.cuda.device(device)
 
 
+_ALREADY = contextlib.nullcontext()
+
+
 def _stream_ptr(device):
+    """The current stream of `device`, as the library takes it (without the Stream object that
+    torch.cuda.current_stream would build, which costs as much as a small launch)."""
     import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    if device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _need_cuda(*ts, device=None):
@@ -160,7 +171,7 @@ def _need_cuda(*ts, device=None):
 
 def _expect(fn, name, t, shape, dtype):
     """`t` has exactly `shape` and `dtype` (the library reads and writes that many elements)."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{fn}: {name} must be {dtype} of shape {tuple(shape)}, "
                          f"got {t.dtype} of shape {tuple(t.shape)}")
 
@@ -653,30 +664,59 @@ def la_gated_backward_workspace_bytes(B, H, N, D, M, dtype=LA_BF16):
     return load_library().la_gated_backward_workspace_bytes(B, H, N, D, M, dtype)
 
 
+@functools.lru_cache(maxsize=4096)
+def _bytes(query, *dims):
+    """A workspace query's answer (it depends on the sizes alone)."""
+    return getattr(load_library(), query)(*dims)
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _scratch(like, nbytes, workspace):
+    """(workspace, its bytes): the caller's, or one of `nbytes` if any are needed."""
+    if workspace is not None:
+        workspace = _workspace(nbytes, like.device, workspace)
+        return workspace, workspace.numel() * workspace.element_size()
+    import torch
+    return (like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None), nbytes
+
+
+def _check_gated(fn, q, k, v, g, rank):
+    (B, *HN), D, M = _dims(fn, q, v, rank)
+    lead, dt = q.shape[:-1], q.dtype
+    if k.shape != q.shape or k.dtype != dt:
+        _expect(fn, "k", k, q.shape, dt)
+    if v.shape[:-1] != lead or v.dtype != dt:
+        _expect(fn, "v", v, (*lead, M), dt)
+    if g.shape != lead or g.dtype != dt:
+        _expect(fn, "g", g, lead, dt)
+    return (B, *HN, D, M), _dtype_code(q)
+
+
 def _forward_gated(fn, q, k, v, g, S0, out, S, want_state, workspace):
     import torch
-    (B, H, N), D, M = _dims(fn, q, v, 4)
-    _expect(fn, "k", k, q.shape, q.dtype)
-    _expect(fn, "v", v, (B, H, N, M), q.dtype)
-    _expect(fn, "g", g, (B, H, N), q.dtype)
+    (B, H, N, D, M), dt = _check_gated(fn, q, k, v, g, 4)
+    given = []
     for name, t in (("S0", S0), ("S", S)):
         if t is not None:
             _expect(fn, name, t, (B, H, D, M), torch.float32)
+            given.append(t)
     if out is not None:
-        _expect(fn, "out", out, (B, H, N, M), q.dtype)
-    dt = _dtype_code(q)
-    _need_cuda(q, k, v, g, *[t for t in (S0, S, out) if t is not None])
+        _expect(fn, "out", out, v.shape, q.dtype)
+        given.append(out)
+    _need_cuda(q, k, v, g, *given)
     lib = load_library()
     dev = q.device
-    out = torch.empty((B, H, N, M), dtype=q.dtype, device=dev) if out is None else out
+    out = torch.empty_like(v) if out is None else out
     if want_state and S is None:
-        S = torch.empty((B, H, D, M), dtype=torch.float32, device=dev)
-    ws = _workspace(lib.la_gated_workspace_bytes(B, H, N, D, M, dt), dev, workspace)
+        S = q.new_empty((B, H, D, M), dtype=torch.float32)
+    ws, nbytes = _scratch(q, _bytes("la_gated_workspace_bytes", B, H, N, D, M, dt), workspace)
     with _on_device(dev):
         st = lib.la_forward_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-                                  out.data_ptr(), 0 if S0 is None else S0.data_ptr(),
-                                  0 if S is None else S.data_ptr(), B, H, N, D, M, dt,
-                                  ws.data_ptr(), ws.numel() * ws.element_size(), _stream_ptr(dev))
+                                  out.data_ptr(), _ptr(S0), _ptr(S), B, H, N, D, M, dt, _ptr(ws),
+                                  nbytes, _stream_ptr(dev))
     _check(fn, st)
     return out, S
 
@@ -698,9 +738,11 @@ def _check_pool(fn, S_pool, H, D, M, B, slots):
     import torch
     if S_pool.dim() != 4:
         raise ValueError(f"{fn}: S_pool must be [pool, H, D, M]")
-    _expect(fn, "S_pool", S_pool, (S_pool.shape[0], H, D, M), torch.float32)
+    pool = S_pool.shape[0]
+    _expect(fn, "S_pool", S_pool, (pool, H, D, M), torch.float32)
     if slots is not None and (slots.dtype != torch.int32 or slots.numel() != B):
         raise ValueError("slots must be a contiguous int32 tensor of B entries")
+    return pool
 
 
 def la_extend_gated(q, k, v, g, S_pool, slots=None, lens=None, out=None, workspace=None):
@@ -712,28 +754,21 @@ def la_extend_gated(q, k, v, g, S_pool, slots=None, lens=None, out=None, workspa
     as they were (uninitialised if `out` is None)."""
     import torch
     fn = "la_extend_gated"
-    (B, H, N), D, M = _dims(fn, q, v, 4)
-    _expect(fn, "k", k, q.shape, q.dtype)
-    _expect(fn, "v", v, (B, H, N, M), q.dtype)
-    _expect(fn, "g", g, (B, H, N), q.dtype)
-    _check_pool(fn, S_pool, H, D, M, B, slots)
+    (B, H, N, D, M), dt = _check_gated(fn, q, k, v, g, 4)
+    pool = _check_pool(fn, S_pool, H, D, M, B, slots)
     if lens is not None and (lens.dtype != torch.int32 or lens.numel() != B):
         raise ValueError("lens must be a contiguous int32 tensor of B entries")
     if out is not None:
-        _expect(fn, "out", out, (B, H, N, M), q.dtype)
-    dt = _dtype_code(q)
+        _expect(fn, "out", out, v.shape, q.dtype)
     _need_cuda(q, k, v, g, S_pool, *[t for t in (out, slots, lens) if t is not None])
     lib = load_library()
     dev = q.device
-    out = torch.empty((B, H, N, M), dtype=q.dtype, device=dev) if out is None else out
-    ws = _workspace(lib.la_gated_workspace_bytes(B, H, N, D, M, dt), dev, workspace)
+    out = torch.empty_like(v) if out is None else out
+    ws, nbytes = _scratch(q, max(_bytes("la_gated_workspace_bytes", B, H, N, D, M, dt), 256), workspace)
     with _on_device(dev):
         st = lib.la_extend_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-                                 out.data_ptr(), S_pool.data_ptr(),
-                                 0 if slots is None else slots.data_ptr(),
-                                 0 if lens is None else lens.data_ptr(), S_pool.shape[0],
-                                 B, H, N, D, M, dt, ws.data_ptr(),
-                                 ws.numel() * ws.element_size(), _stream_ptr(dev))
+                                 out.data_ptr(), S_pool.data_ptr(), _ptr(slots), _ptr(lens), pool,
+                                 B, H, N, D, M, dt, ws.data_ptr(), nbytes, _stream_ptr(dev))
     _check(fn, st)
     return out
 
@@ -743,23 +778,18 @@ def la_decode_step_gated(q, k, v, g, S_pool, slots=None, out=None):
     [P,H,D,M] (entries slots, as in la_extend_gated) are updated in place; returns out [n,H,M]."""
     import torch
     fn = "la_decode_step_gated"
-    (n, H), D, M = _dims(fn, q, v, 3)
-    _expect(fn, "k", k, q.shape, q.dtype)
-    _expect(fn, "v", v, (n, H, M), q.dtype)
-    _expect(fn, "g", g, (n, H), q.dtype)
-    _check_pool(fn, S_pool, H, D, M, n, slots)
+    (n, H, D, M), dt = _check_gated(fn, q, k, v, g, 3)
+    pool = _check_pool(fn, S_pool, H, D, M, n, slots)
     if out is not None:
-        _expect(fn, "out", out, (n, H, M), q.dtype)
-    dt = _dtype_code(q)
+        _expect(fn, "out", out, v.shape, q.dtype)
     _need_cuda(q, k, v, g, S_pool, *[t for t in (out, slots) if t is not None])
     lib = load_library()
     dev = q.device
-    out = torch.empty((n, H, M), dtype=q.dtype, device=dev) if out is None else out
+    out = torch.empty_like(v) if out is None else out
     with _on_device(dev):
         st = lib.la_decode_step_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-                                      S_pool.data_ptr(), 0 if slots is None else slots.data_ptr(),
-                                      out.data_ptr(), S_pool.shape[0], n, H, D, M, dt,
-                                      _stream_ptr(dev))
+                                      S_pool.data_ptr(), _ptr(slots), out.data_ptr(), pool, n, H,
+                                      D, M, dt, _stream_ptr(dev))
     _check(fn, st)
     return out
 
@@ -772,39 +802,35 @@ def la_backward_gated(q, k, v, g, dout, S0=None, dS=None, dq=None, dk=None, dv=N
     dS [B,H,D,M] float32: the gradient with respect to the final state (None: zero)."""
     import torch
     fn, f32 = "la_backward_gated", torch.float32
-    (B, H, N), D, M = _dims(fn, q, v, 4)
-    _expect(fn, "k", k, q.shape, q.dtype)
-    _expect(fn, "v", v, (B, H, N, M), q.dtype)
-    _expect(fn, "g", g, (B, H, N), q.dtype)
-    _expect(fn, "dout", dout, (B, H, N, M), q.dtype)
+    (B, H, N, D, M), dt = _check_gated(fn, q, k, v, g, 4)
+    if dout.shape != v.shape or dout.dtype != v.dtype:
+        _expect(fn, "dout", dout, v.shape, v.dtype)
+    given = []
     for name, t in (("S0", S0), ("dS", dS), ("dS0", dS0)):
         if t is not None:
             _expect(fn, name, t, (B, H, D, M), f32)
+            given.append(t)
     if dS0 is not None and S0 is None:
         raise ValueError(f"{fn}: dS0 without S0")
-    grads = {"dq": (dq, (B, H, N, D)), "dk": (dk, (B, H, N, D)), "dv": (dv, (B, H, N, M)),
-             "dg": (dg, (B, H, N))}
-    for name, (t, shape) in grads.items():
+    for name, t, like in (("dq", dq, q), ("dk", dk, q), ("dv", dv, v), ("dg", dg, g)):
         if t is not None:
-            _expect(fn, name, t, shape, q.dtype)
-    dt = _dtype_code(q)
-    _need_cuda(q, k, v, g, dout,
-               *[t for t in (S0, dS, dS0, dq, dk, dv, dg) if t is not None])
+            _expect(fn, name, t, like.shape, q.dtype)
+            given.append(t)
+    _need_cuda(q, k, v, g, dout, *given)
     lib = load_library()
     dev = q.device
-    dq, dk, dv, dg = (torch.empty(shape, dtype=q.dtype, device=dev) if t is None else t
-                      for t, shape in grads.values())
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    dg = torch.empty_like(g) if dg is None else dg
     if S0 is not None and dS0 is None:
-        dS0 = torch.empty((B, H, D, M), dtype=f32, device=dev)
-    ws = _workspace(lib.la_gated_backward_workspace_bytes(B, H, N, D, M, dt), dev, workspace)
+        dS0 = torch.empty_like(S0)
+    ws, nbytes = _scratch(q, _bytes("la_gated_backward_workspace_bytes", B, H, N, D, M, dt), workspace)
     with _on_device(dev):
         st = lib.la_backward_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-                                   dout.data_ptr(), 0 if S0 is None else S0.data_ptr(),
-                                   0 if dS is None else dS.data_ptr(), dq.data_ptr(),
-                                   dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
-                                   0 if dS0 is None else dS0.data_ptr(), B, H, N, D, M, dt,
-                                   ws.data_ptr(), ws.numel() * ws.element_size(),
-                                   _stream_ptr(dev))
+                                   dout.data_ptr(), _ptr(S0), _ptr(dS), dq.data_ptr(),
+                                   dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), _ptr(dS0), B, H,
+                                   N, D, M, dt, _ptr(ws), nbytes, _stream_ptr(dev))
     _check(fn, st)
     return (dq, dk, dv, dg) if S0 is None else (dq, dk, dv, dg, dS0)
 
@@ -820,18 +846,27 @@ def _need_rows(*ts, device):
             raise ValueError(f"tensors must all be on {device}, got one on {t.device}")
 
 
-def _row_strides(fn, name, t, written=False):
-    """The strides of [B,H,N,*] t's first three dimensions, for the library (0 where a dimension
-    has one entry); rows that are written must not overlap."""
-    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+@functools.lru_cache(maxsize=1024)
+def _long3(a, b, c):
+    return (ctypes.c_longlong * 3)(a, b, c)
+
+
+def _row_strides(fn, name, t, packed=False, written=False):
+    """The strides of the batch, head and token of t [B,H,N,*] (packed: [N,H,*]), for the library
+    (0 where a dimension has one entry); rows that are written must not overlap."""
+    size, stride = t.shape, t.stride()
+    if size[-1] > 1 and stride[-1] != 1 and t.numel():
         raise ValueError(f"{fn}: {name}'s last dimension must be contiguous")
     if written and t.numel():
-        reach = t.shape[-1]
-        for stride, size in sorted((st, n) for st, n in zip(t.stride()[:3], t.shape[:3]) if n > 1):
-            if stride < reach:
+        reach = size[-1]
+        for st, n in sorted((st, n) for st, n in zip(stride[:-1], size[:-1]) if n > 1):
+            if st < reach:
                 raise ValueError(f"{fn}: rows of {name} overlap in memory")
-            reach = stride * (size - 1) + reach
-    return (ctypes.c_longlong * 3)(*[st if n > 1 else 0 for st, n in zip(t.stride()[:3], t.shape[:3])])
+            reach = st * (n - 1) + reach
+    if packed:
+        return _long3(0, stride[1] if size[1] > 1 else 0, stride[0] if size[0] > 1 else 0)
+    return _long3(stride[0] if size[0] > 1 else 0, stride[1] if size[1] > 1 else 0,
+                  stride[2] if size[2] > 1 else 0)
 
 
 def la_rotary_freqs(rot_dim, base=10000.0, scaling=None, factor=1.0, original_len=None, slow=1.0,
@@ -884,54 +919,56 @@ def la_rotary(q, k, freqs, positions=None, offset=0, interleaved=False, mscale=1
     the inputs themselves. Returns (q_out, k_out), contiguous unless passed in."""
     import torch
     fn = "la_rotary"
-    dt = _dtype_code(q)
-    if q.dim() not in (3, 4):
+    dt, shape = _dtype_code(q), q.shape
+    packed = len(shape) == 3
+    if packed:
+        B, (N, H, D) = 1, shape
+    elif len(shape) == 4:
+        B, H, N, D = shape
+    else:
         raise ValueError(f"{fn}: q must have 3 or 4 dimensions")
-    packed = q.dim() == 3
-
-    def lead(t):  # [B, H, N, D]
-        return t.transpose(0, 1).unsqueeze(0) if packed else t
-
+    Hk, given = 0, [q, freqs]
     if k is not None:
-        hk = k.shape[1] if k.dim() == q.dim() else -1
-        _expect(fn, "k", k, (q.shape[0], hk, *q.shape[2:]), q.dtype)
+        Hk = k.shape[1] if k.dim() == len(shape) else -1
+        _expect(fn, "k", k, (shape[0], Hk, *shape[2:]), q.dtype)
+        given.append(k)
     elif k_out is not None:
         raise ValueError(f"{fn}: k_out without k")
-    for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k)):
-        if t is not None:
-            _expect(fn, name, t, like.shape, q.dtype)
-    B, H, N, D = lead(q).shape
-    Hk = 0 if k is None else lead(k).shape[1]
     if freqs.dim() != 1 or freqs.dtype != torch.float64 or not freqs.is_contiguous():
         raise ValueError(f"{fn}: freqs must be a contiguous float64 tensor of R/2 entries")
     pos_b = 0
     if positions is not None:
+        p = positions.shape
         if positions.dtype != torch.int32 or not positions.is_contiguous() \
-                or tuple(positions.shape) not in ({(N,)} if packed else {(N,), (B, N)}):
+                or not (p == (N,) or (not packed and p == (B, N))):
             raise ValueError(f"{fn}: positions must be a contiguous int32 tensor of [N] or [B, N]")
-        pos_b = N if positions.dim() == 2 else 0
-    dev = q.device
-    qs = _row_strides(fn, "q", lead(q))
-    ks = None if k is None else _row_strides(fn, "k", lead(k))
+        pos_b = N if len(p) == 2 else 0
+        given.append(positions)
+    qs = _row_strides(fn, "q", q, packed)
+    ks = None if k is None else _row_strides(fn, "k", k, packed)
+    qos = kos = None
     if q_out is not None:
-        _row_strides(fn, "q_out", lead(q_out), written=True)
+        _expect(fn, "q_out", q_out, shape, q.dtype)
+        qos = _row_strides(fn, "q_out", q_out, packed, written=True)
+        given.append(q_out)
     if k_out is not None:
-        _row_strides(fn, "k_out", lead(k_out), written=True)
-    _need_rows(*[t for t in (q, k, freqs, positions, q_out, k_out) if t is not None], device=dev)
+        _expect(fn, "k_out", k_out, k.shape, q.dtype)
+        kos = _row_strides(fn, "k_out", k_out, packed, written=True)
+        given.append(k_out)
+    dev = q.device
+    _need_rows(*given, device=dev)
     lib = load_library()
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        q_out = q.new_empty(shape)
+        qos = _row_strides(fn, "q_out", q_out, packed)
     if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
-    qos = _row_strides(fn, "q_out", lead(q_out))
-    kos = None if k is None else _row_strides(fn, "k_out", lead(k_out))
+        k_out = k.new_empty(k.shape)
+        kos = _row_strides(fn, "k_out", k_out, packed)
     with _on_device(dev):
-        st = lib.la_rotary(q.data_ptr(), qs, q_out.data_ptr(), qos,
-                           0 if k is None else k.data_ptr(), ks,
-                           0 if k is None else k_out.data_ptr(), kos, freqs.data_ptr(),
-                           0 if positions is None else positions.data_ptr(), pos_b, int(offset),
-                           B, H, Hk, N, D, 2 * freqs.numel(), int(bool(interleaved)),
-                           int(bool(inverse)), float(mscale), dt, _stream_ptr(dev))
+        st = lib.la_rotary(q.data_ptr(), qs, q_out.data_ptr(), qos, _ptr(k), ks, _ptr(k_out), kos,
+                           freqs.data_ptr(), _ptr(positions), pos_b, int(offset), B, H, Hk, N, D,
+                           2 * freqs.shape[0], int(bool(interleaved)), int(bool(inverse)),
+                           float(mscale), dt, _stream_ptr(dev))
     _check(fn, st)
     return q_out, k_out
 
@@ -941,14 +978,16 @@ def la_norm_gate_workspace_bytes(B, H, N, M):
 
 
 def _norm_checks(fn, x, z, w):
-    if x.dim() != 4:
+    shape, dt = x.shape, x.dtype
+    if len(shape) != 4:
         raise ValueError(f"{fn}: x must have 4 dimensions")
-    B, H, N, M = x.shape
-    _expect(fn, "z", z, x.shape, x.dtype)
+    if z.shape != shape or z.dtype != dt:
+        _expect(fn, "z", z, shape, dt)
     if w.dim() not in (1, 2):
         raise ValueError(f"{fn}: w must be [M] or [H, M]")
-    _expect(fn, "w", w, (M,) if w.dim() == 1 else (H, M), x.dtype)
-    return B, H, N, M, _dtype_code(x)
+    if w.dtype != dt or w.shape != (shape[3:] if w.dim() == 1 else shape[1::2]):
+        _expect(fn, "w", w, tuple(shape[3:] if w.dim() == 1 else shape[1::2]), dt)
+    return shape, _dtype_code(x)
 
 
 def la_norm_gate(x, z, w, eps=1e-6, out=None):
@@ -959,20 +998,23 @@ def la_norm_gate(x, z, w, eps=1e-6, out=None):
     be a token-major [B,N,H,M] buffer's transpose. out: contiguous unless passed in."""
     import torch
     fn = "la_norm_gate"
-    B, H, N, M, dt = _norm_checks(fn, x, z, w)
+    (B, H, N, M), dt = _norm_checks(fn, x, z, w)
+    rows = [z]
     if out is not None:
         _expect(fn, "out", out, x.shape, x.dtype)
-        _row_strides(fn, "out", out, written=True)
+        outs = _row_strides(fn, "out", out, written=True)
+        rows.append(out)
     zs = _row_strides(fn, "z", z)
-    _need_cuda(x, w)
-    _need_rows(z, *([] if out is None else [out]), device=x.device)
-    lib = load_library()
     dev = x.device
-    out = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+    _need_cuda(x, w)
+    _need_rows(*rows, device=dev)
+    lib = load_library()
+    if out is None:
+        out = torch.empty_like(x)
+        outs = _row_strides(fn, "out", out)
     with _on_device(dev):
-        st = lib.la_norm_gate(x.data_ptr(), z.data_ptr(), zs, w.data_ptr(), out.data_ptr(),
-                              _row_strides(fn, "out", out), B, H, N, M, int(w.dim() == 2),
-                              float(eps), dt, _stream_ptr(dev))
+        st = lib.la_norm_gate(x.data_ptr(), z.data_ptr(), zs, w.data_ptr(), out.data_ptr(), outs,
+                              B, H, N, M, int(w.dim() == 2), float(eps), dt, _stream_ptr(dev))
     _check(fn, st)
     return out
 
@@ -982,27 +1024,33 @@ def la_norm_gate_backward(x, z, w, dy, eps=1e-6, dx=None, dz=None, dw=None, work
     has w's shape. dy and dz are strided as z is (dz: contiguous unless passed in)."""
     import torch
     fn = "la_norm_gate_backward"
-    B, H, N, M, dt = _norm_checks(fn, x, z, w)
-    _expect(fn, "dy", dy, x.shape, x.dtype)
-    for name, t, like in (("dx", dx, x), ("dz", dz, x), ("dw", dw, w)):
+    (B, H, N, M), dt = _norm_checks(fn, x, z, w)
+    if dy.shape != x.shape or dy.dtype != x.dtype:
+        _expect(fn, "dy", dy, x.shape, x.dtype)
+    rows, flat = [z, dy], [x, w]
+    for name, t, like in (("dx", dx, x), ("dw", dw, w)):
         if t is not None:
             _expect(fn, name, t, like.shape, x.dtype)
-    zs, dys = _row_strides(fn, "z", z), _row_strides(fn, "dy", dy)
+            flat.append(t)
     if dz is not None:
-        _row_strides(fn, "dz", dz, written=True)
-    _need_cuda(x, w, *[t for t in (dx, dw) if t is not None])
-    _need_rows(z, dy, *([] if dz is None else [dz]), device=x.device)
-    lib = load_library()
+        _expect(fn, "dz", dz, x.shape, x.dtype)
+        dzs = _row_strides(fn, "dz", dz, written=True)
+        rows.append(dz)
+    zs, dys = _row_strides(fn, "z", z), _row_strides(fn, "dy", dy)
     dev = x.device
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if dx is None else dx
-    dz = torch.empty(x.shape, dtype=x.dtype, device=dev) if dz is None else dz
-    dw = torch.empty(w.shape, dtype=x.dtype, device=dev) if dw is None else dw
-    ws = _workspace(lib.la_norm_gate_workspace_bytes(B, H, N, M), dev, workspace)
+    _need_cuda(*flat)
+    _need_rows(*rows, device=dev)
+    lib = load_library()
+    dx = torch.empty_like(x) if dx is None else dx
+    if dz is None:
+        dz = torch.empty_like(x)
+        dzs = _row_strides(fn, "dz", dz)
+    dw = torch.empty_like(w) if dw is None else dw
+    ws, nbytes = _scratch(x, _bytes("la_norm_gate_workspace_bytes", B, H, N, M), workspace)
     with _on_device(dev):
         st = lib.la_norm_gate_backward(x.data_ptr(), z.data_ptr(), zs, w.data_ptr(), dy.data_ptr(),
-                                       dys, dx.data_ptr(), dz.data_ptr(),
-                                       _row_strides(fn, "dz", dz), dw.data_ptr(), B, H, N, M,
-                                       int(w.dim() == 2), float(eps), dt, ws.data_ptr(),
-                                       ws.numel() * ws.element_size(), _stream_ptr(dev))
+                                       dys, dx.data_ptr(), dz.data_ptr(), dzs, dw.data_ptr(),
+                                       B, H, N, M, int(w.dim() == 2), float(eps), dt, _ptr(ws),
+                                       nbytes, _stream_ptr(dev))
     _check(fn, st)
     return dx, dz, dw

@@ -215,6 +215,7 @@ def test_every_new_call_runs_with_the_tensors_device_current(monkeypatch):
     monkeypatch.setattr(la, "_need_cuda", lambda *a, **k: None)
     monkeypatch.setattr(la, "_need_rows", lambda *a, **k: None)
     monkeypatch.setattr(la, "_stream_ptr", lambda dev: 0)
+    monkeypatch.setattr(la, "_bytes", lambda query, *dims: 256)
     q, v, g, S = _t(2, 3, 10, 16), _t(2, 3, 10, 8), _t(2, 3, 10), _t(2, 3, 16, 8, dtype=F32)
     assert la.la_forward_gated(q, q, v, g).shape == v.shape
     assert la.la_prefill_gated(q, q, v, g)[1].shape == S.shape
