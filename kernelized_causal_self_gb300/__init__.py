@@ -959,10 +959,10 @@ def la_rotary(q, k, freqs, positions=None, offset=0, interleaved=False, mscale=1
     _need_rows(*given, device=dev)
     lib = load_library()
     if q_out is None:
-        q_out = q.new_empty(shape)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         qos = _row_strides(fn, "q_out", q_out, packed)
     if k is not None and k_out is None:
-        k_out = k.new_empty(k.shape)
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
         kos = _row_strides(fn, "k_out", k_out, packed)
     with _on_device(dev):
         st = lib.la_rotary(q.data_ptr(), qs, q_out.data_ptr(), qos, _ptr(k), ks, _ptr(k_out), kos,

@@ -1,5 +1,5 @@
-// Gated recurrence on CUDA cores (float32 or bf16, D and M multiples of 8 up to
-// 128), its scan over segments, and its decode step.
+// Gated recurrence in float32 on CUDA cores (tensor cores would round its inputs; D
+// and M multiples of 8 up to 128), the scan over segments, and the decode step.
 //
 // One kernel carries every direction. With X a state and u, w, z three of the
 // inputs, it walks a segment's tokens updating X by an outer product and reading
@@ -39,13 +39,14 @@ constexpr int kTok = 16;       // tokens staged at a time
 constexpr int kCols = 32;      // columns of X per thread
 
 struct RecurArgs {
-  const void *u, *w, *z, *g;
-  void* y;               // outputs [BH][N][NR] (nullptr: state pass)
-  const void* p;         // [BH][N][NR]: dots[rb][bh][t] = sum over rows of p (X' z) (nullptr: none)
+  const float *u, *w, *z, *g;
+  float* y;              // outputs [BH][N][NR] (nullptr: state pass)
+  const float* p;        // [BH][N][NR]: dots[rb][bh][t] = sum over rows of p (X' z) (nullptr: none)
   float* dots;
   const float* E;        // forward: ends[rb][bh][seg] = <X', E[seg + 1]> at the segment's last
   float* ends;           //   token (nullptr: none)
   int NR, NC, N, BH, len, n_seg;
+  bool reverse;
   const int* lens;
   int H;
   // states: element (r, c) of an entry at r * rs + c * cs
@@ -60,25 +61,54 @@ struct RecurArgs {
 };
 
 // CP threads share a row, each with 32 of its columns (c = 4 (i CP + p) + 0..3, so
-// that the lanes of a warp read neighbouring 16-byte words).
+// that the lanes of a warp read neighbouring 16-byte words). 16 tokens are staged at a
+// time, the next 16 on their way in registers meanwhile.
 // Bound by the packed multiply-adds: three for two state elements per token,
 // ~100 cycles a token for a 64 x 64 state on one CTA.
-template <typename T, int CP, bool REV>
-__global__ void __launch_bounds__(kThreads) gated_recur_kernel(const RecurArgs a) {
-  constexpr int RB = kThreads / CP;
-  __shared__ __align__(16) float sw[kTok][kCols * CP], sz[kTok][kCols * CP];
+template <int CP, bool REV>
+__device__ __forceinline__ void recur_walk(const RecurArgs& a) {
+  constexpr int RB = kThreads / CP, COLS = kCols * CP;
+  constexpr int PC = kTok * COLS / kThreads, PR = kTok * RB / kThreads;  // staged per thread
+  __shared__ __align__(16) float sw[kTok][COLS], sz[kTok][COLS];
   __shared__ float su[kTok][RB], sy[kTok][RB + 1], sa[kTok], swz[kTok];
   const int tid = threadIdx.x, part = tid % CP, row = tid / CP;
   const int bh = blockIdx.x / a.n_seg, seg = blockIdx.x % a.n_seg;
   const int r0 = blockIdx.y * RB, nr = min(RB, a.NR - r0);
+  if (nr <= 0) return;
   const int n = gated_length(a.lens, a.H, bh, a.N);
   const int tb = min(seg * a.len, n), te = min(tb + a.len, n);
   const size_t seq = (size_t)bh * a.N;
-  const T* u = static_cast<const T*>(a.u) + seq * a.NR + r0;
-  const T* w = static_cast<const T*>(a.w) + seq * a.NC;
-  const T* z = static_cast<const T*>(a.z) + seq * a.NC;
-  const T* g = static_cast<const T*>(a.g) + seq;
-  T* y = static_cast<T*>(a.y) + (a.y ? seq * a.NR + r0 : 0);
+  const float* u = a.u + seq * a.NR + r0;
+  const float* w = a.w + seq * a.NC;
+  const float* z = a.z + seq * a.NC;
+  const float* g = a.g + seq;
+  float* y = a.y + (a.y ? seq * a.NR + r0 : 0);
+
+  float nw[PC], nz[PC], nu[PR], ng = 0.f;
+  // the tile `done` tokens into the walk: its first token and count
+  auto tile = [&](int done, int& t0) {
+    const int m = min(kTok, te - tb - done);
+    t0 = REV ? te - done - m : tb + done;
+    return m;
+  };
+  auto fetch = [&](int done) {
+    int t0;
+    const int m = tile(done, t0);
+#pragma unroll
+    for (int i = 0; i < PC; ++i) {
+      const int at = tid + i * kThreads, t = at / COLS, c = at % COLS;
+      const bool in = t < m && c < a.NC;
+      nw[i] = in ? w[(size_t)(t0 + t) * a.NC + c] : 0.f;
+      nz[i] = in && a.y ? z[(size_t)(t0 + t) * a.NC + c] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < PR; ++i) {
+      const int at = tid + i * kThreads, t = at / RB, r = at % RB;
+      nu[i] = t < m && r < nr ? u[(size_t)(t0 + t) * a.NR + r] : 0.f;
+    }
+    if (tid < kTok) ng = tid < m ? g[t0 + tid] : 0.f;
+  };
+  if (tb < te) fetch(0);
 
   const long long entry = a.entries.at(bh);
   if (entry < 0 && seg == 0 && blockIdx.y == 0 && tid == 0 && a.hdr)
@@ -100,21 +130,23 @@ __global__ void __launch_bounds__(kThreads) gated_recur_kernel(const RecurArgs a
 
   float decay = 1.f, end = 0.f;
   for (int done = 0; done < te - tb; done += kTok) {
-    const int m = min(kTok, te - tb - done);
-    const int t0 = REV ? te - done - m : tb + done;
+    int t0;
+    const int m = tile(done, t0);
     __syncthreads();
-    for (int i = tid; i < kTok * kCols * CP; i += kThreads) {
-      const int t = i / (kCols * CP), c = i % (kCols * CP);
-      const bool in = t < m && c < a.NC;
-      sw[t][c] = in ? to_f32<T>(w[(size_t)(t0 + t) * a.NC + c]) : 0.f;
-      if (a.y) sz[t][c] = in ? to_f32<T>(z[(size_t)(t0 + t) * a.NC + c]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < PC; ++i) {
+      const int at = tid + i * kThreads;
+      sw[at / COLS][at % COLS] = nw[i];
+      sz[at / COLS][at % COLS] = nz[i];
     }
-    for (int i = tid; i < kTok * RB; i += kThreads) {
-      const int t = i / RB, r = i % RB;
-      su[t][r] = t < m && r < nr ? to_f32<T>(u[(size_t)(t0 + t) * a.NR + r]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < PR; ++i) {
+      const int at = tid + i * kThreads;
+      su[at / RB][at % RB] = nu[i];
     }
-    if (tid < kTok) sa[tid] = tid < m ? gated_decay(to_f32<T>(g[t0 + tid])) : 1.f;
+    if (tid < kTok) sa[tid] = gated_decay(ng);
     __syncthreads();
+    if (done + kTok < te - tb) fetch(done + kTok);
     if (a.y) {  // w_t . z_t, eight threads a token
       float s = 0.f;
       for (int c = tid % 8; c < a.NC; c += 8) s = fmaf(sw[tid / 8][c], sz[tid / 8][c], s);
@@ -172,15 +204,14 @@ __global__ void __launch_bounds__(kThreads) gated_recur_kernel(const RecurArgs a
       __syncthreads();
       for (int i = tid; i < m * RB; i += kThreads) {
         const int t = i / RB, r = i % RB;
-        if (r < nr) y[(size_t)(t0 + t) * a.NR + r] = from_f32<T>(fmaf(su[t][r], swz[t], sy[t][r]));
+        if (r < nr) y[(size_t)(t0 + t) * a.NR + r] = fmaf(su[t][r], swz[t], sy[t][r]);
       }
       if (a.p) {
-        const T* p = static_cast<const T*>(a.p) + seq * a.NR + r0;
+        const float* p = a.p + seq * a.NR + r0;
         const int t = tid / 8;
         float s = 0.f;
         if (t < m)
-          for (int r = tid % 8; r < nr; r += 8)
-            s += sy[t][r] * to_f32<T>(p[(size_t)(t0 + t) * a.NR + r]);
+          for (int r = tid % 8; r < nr; r += 8) s = fmaf(sy[t][r], p[(size_t)(t0 + t) * a.NR + r], s);
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (t < m && tid % 8 == 0)
@@ -212,6 +243,20 @@ __global__ void __launch_bounds__(kThreads) gated_recur_kernel(const RecurArgs a
         if (c < a.NC) xout[(size_t)(r0 + row) * a.rs + (size_t)c * a.cs] = (&x[2 * i + j / 2].x)[j % 2];
       }
   if (a.decay && blockIdx.y == 0 && tid == 0) a.decay[(size_t)bh * a.n_seg + seg] = decay;
+}
+
+// blockIdx.z: one of up to three walks that do not depend on each other
+struct RecurJobs {
+  RecurArgs job[3];
+};
+template <int CP>
+__global__ void __launch_bounds__(kThreads, CP == 2 ? 4 : 3)
+gated_recur_kernel(const __grid_constant__ RecurJobs jobs) {
+  const RecurArgs& a = jobs.job[blockIdx.z];
+  if (a.reverse)
+    recur_walk<CP, true>(a);
+  else
+    recur_walk<CP, false>(a);
 }
 
 // Joins the segments: forward X[s + 1] = decay[s] X[s] + U[s] from X[0] = init,
@@ -278,10 +323,9 @@ gated_scan_kernel(const ScanJob first, const ScanJob second, const float* __rest
 // dg of one segment: from <X', E> at its last token back,
 //   dg_t = <X', E> + sum over s >= t of dot_q[s] - sum over t <= s < last of dot_k[s],
 // 256 tokens at a time (each dot the sum of its row blocks').
-template <typename T>
 __global__ void __launch_bounds__(256)
 gated_dg_kernel(const float* __restrict__ ends, const float* __restrict__ dot_q,
-                const float* __restrict__ dot_k, T* __restrict__ dg, int BH, int N, int len,
+                const float* __restrict__ dot_k, float* __restrict__ dg, int BH, int N, int len,
                 int n_seg, int rb) {
   __shared__ float part[8];
   const int bh = blockIdx.x / n_seg, seg = blockIdx.x % n_seg, tid = threadIdx.x;
@@ -307,39 +351,41 @@ gated_dg_kernel(const float* __restrict__ ends, const float* __restrict__ dot_q,
     __syncthreads();
     float before = carry;
     for (int i = 0; i < tid / 32; ++i) before += part[i];
-    if (t >= tb) dg[(size_t)bh * N + t] = from_f32<T>(before + s);
+    if (t >= tb) dg[(size_t)bh * N + t] = before + s;
     for (int i = 0; i < 8; ++i) carry += part[i];
   }
 }
 
-template <typename T, bool REV>
-cudaError_t launch_recur(const RecurArgs& a, cudaStream_t st) {
-  const int cp = a.NC <= kCols ? 1 : a.NC <= 2 * kCols ? 2 : 4;
-  const int rb = kThreads / cp;
-  const dim3 grid((unsigned)(a.BH * a.n_seg), (unsigned)((a.NR + rb - 1) / rb));
+// threads per row: the widest of a call's states decides, so that its walks share launches
+int column_parts(int D, int M) {
+  const int nc = D > M ? D : M;
+  return nc <= kCols ? 1 : nc <= 2 * kCols ? 2 : 4;
+}
+
+int row_blocks(int NR, int cp) { return (NR * cp + kThreads - 1) / kThreads; }
+
+cudaError_t launch_recur(const RecurJobs& jobs, int count, int D, int M, cudaStream_t st) {
+  const RecurArgs& a = jobs.job[0];
+  const int cp = column_parts(D, M);
+  const dim3 grid((unsigned)(a.BH * a.n_seg), (unsigned)row_blocks(D > M ? D : M, cp), count);
   if (cp == 1)
-    gated_recur_kernel<T, 1, REV><<<grid, kThreads, 0, st>>>(a);
+    gated_recur_kernel<1><<<grid, kThreads, 0, st>>>(jobs);
   else if (cp == 2)
-    gated_recur_kernel<T, 2, REV><<<grid, kThreads, 0, st>>>(a);
+    gated_recur_kernel<2><<<grid, kThreads, 0, st>>>(jobs);
   else
-    gated_recur_kernel<T, 4, REV><<<grid, kThreads, 0, st>>>(a);
+    gated_recur_kernel<4><<<grid, kThreads, 0, st>>>(jobs);
   count_launches(1);
   return cudaGetLastError();
 }
 
-int row_blocks(int NR, int NC) {
-  const int rb = kThreads / (NC <= kCols ? 1 : NC <= 2 * kCols ? 2 : 4);
-  return (NR + rb - 1) / rb;
-}
-
 // Segments of the CUDA-core path: enough CTAs to give each of the 152 SMs four
-// (latency-bound walks overlap), but at least 64 tokens each, since a segment costs
+// (latency-bound walks overlap), but at least 32 tokens each, since a segment costs
 // a state pass and a scan step; a backward's at most 512, over which dg's sum from
 // the segment's end back keeps float32's accuracy.
 GatedPlan plan_simt(int BH, int N, int D, int M, bool backward) {
-  const long long per = (long long)BH * row_blocks(M, D);
+  const long long per = (long long)BH * row_blocks(D > M ? D : M, column_parts(D, M));
   long long n_seg = (4 * 152 + per - 1) / per;
-  const long long most = (N + 63) / 64;
+  const long long most = (N + 31) / 32;
   if (n_seg > most) n_seg = most;
   if (backward && n_seg < (N + 511) / 512) n_seg = (N + 511) / 512;
   if (n_seg < 1) n_seg = 1;
@@ -374,11 +420,11 @@ GatedWorkspace carve(void* ws, const GatedPlan& p, int D, int M, bool backward, 
   return w;
 }
 
-cudaError_t simt_forward(const GatedForward& f, void* ws, cudaStream_t st) {
-  const GatedPlan p = plan_simt(f.B * f.H, f.N, f.D, f.M, false);
-  const GatedWorkspace w = carve(ws, p, f.D, f.M, false, 0);
-  RecurArgs a{};
-  a.g = f.g;
+cudaError_t simt_forward(const GatedForward& f, const GatedPlan& p, const GatedWorkspace& w,
+                         cudaStream_t st) {
+  RecurJobs jobs{};
+  RecurArgs& a = jobs.job[0];
+  a.g = static_cast<const float*>(f.g);
   a.N = f.N;
   a.BH = p.BH;
   a.len = p.len;
@@ -390,41 +436,43 @@ cudaError_t simt_forward(const GatedForward& f, void* ws, cudaStream_t st) {
   a.hdr = w.hdr;
   cudaError_t e;
   if (p.n_seg > 1) {
-    RecurArgs s = a;  // X = S: rows d
-    s.u = f.k;
-    s.w = f.v;
-    s.z = f.v;
+    RecurJobs states = jobs;  // X = S: rows d
+    RecurArgs& s = states.job[0];
+    s.u = static_cast<const float*>(f.k);
+    s.w = s.z = static_cast<const float*>(f.v);
     s.NR = f.D;
     s.NC = f.M;
     s.rs = f.M;
     s.cs = 1;
     s.seg_out = w.S;
     s.decay = w.decay;
-    if ((e = launch_recur<float, false>(s, st)) != cudaSuccess) return e;
+    if ((e = launch_recur(states, 1, f.D, f.M, st)) != cudaSuccess) return e;
     if ((e = gated_scan(p, w, f.S0, f.S, a.entries, a.DM, st)) != cudaSuccess) return e;
     a.seg_in = w.S;
   } else {
     a.init = f.S0;
     a.fin = f.S;
   }
-  a.u = f.v;  // X = S^T: rows m
-  a.w = f.k;
-  a.z = f.q;
-  a.y = f.out;
+  a.u = static_cast<const float*>(f.v);  // X = S^T: rows m
+  a.w = static_cast<const float*>(f.k);
+  a.z = static_cast<const float*>(f.q);
+  a.y = static_cast<float*>(f.out);
   a.NR = f.M;
   a.NC = f.D;
   a.rs = 1;
   a.cs = f.M;
-  return launch_recur<float, false>(a, st);
+  return launch_recur(jobs, 1, f.D, f.M, st);
 }
 
-template <typename T>
-cudaError_t simt_backward_t(const GatedBackward& f, void* ws, cudaStream_t st) {
-  const GatedPlan p = plan_simt(f.B * f.H, f.N, f.D, f.M, true);
-  const int rb_dm = row_blocks(f.D, f.M);  // rows d: S, dS
-  const GatedWorkspace w = carve(ws, p, f.D, f.M, true, rb_dm);
-  RecurArgs a{};
-  a.g = f.g;
+int backward_dots(int D, int M) { return row_blocks(D, column_parts(D, M)); }
+
+cudaError_t simt_backward(const GatedBackward& f, const GatedPlan& p, const GatedWorkspace& w,
+                          cudaStream_t st) {
+  const int rb = backward_dots(f.D, f.M);
+  const float *q = static_cast<const float*>(f.q), *k = static_cast<const float*>(f.k),
+              *v = static_cast<const float*>(f.v), *dout = static_cast<const float*>(f.dout);
+  RecurArgs a{};  // X = S, dS: rows d
+  a.g = static_cast<const float*>(f.g);
   a.N = f.N;
   a.BH = p.BH;
   a.len = p.len;
@@ -432,58 +480,55 @@ cudaError_t simt_backward_t(const GatedBackward& f, void* ws, cudaStream_t st) {
   a.H = f.H;
   a.DM = f.D * f.M;
   a.entries = GatedEntries{nullptr, 0, f.H};
-  RecurArgs rows_d = a;
-  rows_d.NR = f.D;
-  rows_d.NC = f.M;
-  rows_d.rs = f.M;
-  rows_d.cs = 1;
-  cudaError_t e;
-  RecurArgs s = rows_d;  // the segments' own states and gradients
-  s.u = f.k;
-  s.w = s.z = f.v;
+  a.NR = f.D;
+  a.NC = f.M;
+  a.rs = f.M;
+  a.cs = 1;
+  // the segments' own states and gradients
+  RecurJobs states{{a, a, a}};
+  RecurArgs &s = states.job[0], &r = states.job[1];
+  s.u = k;
+  s.w = s.z = v;
   s.seg_out = w.S;
   s.decay = w.decay;
-  if ((e = launch_recur<T, false>(s, st)) != cudaSuccess) return e;
-  s.u = f.q;
-  s.w = s.z = f.dout;
-  s.seg_out = w.E;
-  s.decay = nullptr;
-  if ((e = launch_recur<T, true>(s, st)) != cudaSuccess) return e;
+  r.reverse = true;
+  r.u = q;
+  r.w = r.z = dout;
+  r.seg_out = w.E;
+  cudaError_t e = launch_recur(states, 2, f.D, f.M, st);
+  if (e != cudaSuccess) return e;
   const GatedGradients back{f.dS, f.dS0};
   if ((e = gated_scan(p, w, f.S0, nullptr, a.entries, a.DM, st, &back)) != cudaSuccess) return e;
-  RecurArgs dq = rows_d;
-  dq.u = f.k;
-  dq.w = f.v;
-  dq.z = f.dout;
-  dq.y = f.dq;
-  dq.p = f.q;
+  RecurJobs grads{{a, a, a}};
+  RecurArgs &dq = grads.job[0], &dk = grads.job[1], &dv = grads.job[2];
+  dq.u = k;
+  dq.w = v;
+  dq.z = dout;
+  dq.y = static_cast<float*>(f.dq);
+  dq.p = q;
   dq.dots = w.dot_q;
   dq.E = w.E;
   dq.ends = w.ends;
   dq.seg_in = w.S;
-  if ((e = launch_recur<T, false>(dq, st)) != cudaSuccess) return e;
-  RecurArgs dk = rows_d;
-  dk.u = f.q;
-  dk.w = f.dout;
-  dk.z = f.v;
-  dk.y = f.dk;
-  dk.p = f.k;
+  dk.reverse = dv.reverse = true;
+  dk.u = q;
+  dk.w = dout;
+  dk.z = v;
+  dk.y = static_cast<float*>(f.dk);
+  dk.p = k;
   dk.dots = w.dot_k;
-  dk.seg_in = w.E;
-  if ((e = launch_recur<T, true>(dk, st)) != cudaSuccess) return e;
-  RecurArgs dv = a;  // rows m: dS^T
-  dv.u = f.dout;
-  dv.w = f.q;
-  dv.z = f.k;
-  dv.y = f.dv;
+  dk.seg_in = dv.seg_in = w.E;
+  dv.u = dout;  // rows m: dS^T
+  dv.w = q;
+  dv.z = k;
+  dv.y = static_cast<float*>(f.dv);
   dv.NR = f.M;
   dv.NC = f.D;
   dv.rs = 1;
   dv.cs = f.M;
-  dv.seg_in = w.E;
-  if ((e = launch_recur<T, true>(dv, st)) != cudaSuccess) return e;
-  gated_dg_kernel<T><<<(unsigned)(p.BH * p.n_seg), 256, 0, st>>>(
-      w.ends, w.dot_q, w.dot_k, static_cast<T*>(f.dg), p.BH, p.N, p.len, p.n_seg, rb_dm);
+  if ((e = launch_recur(grads, 3, f.D, f.M, st)) != cudaSuccess) return e;
+  gated_dg_kernel<<<(unsigned)(p.BH * p.n_seg), 256, 0, st>>>(
+      w.ends, w.dot_q, w.dot_k, static_cast<float*>(f.dg), p.BH, p.N, p.len, p.n_seg, rb);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -576,32 +621,32 @@ size_t gated_forward_workspace(int BH, int N, int D, int M, int dtype) {
   return carve(nullptr, forward_plan(BH, N, D, M, dtype), D, M, false, 0).bytes;
 }
 
-static bool backward_on_mma(int D, int M, int dtype) {
-  return dtype == LA_BF16 && gated_mma_backward_supported(D, M);
+static GatedPlan backward_plan(int BH, int N, int D, int M, int dtype) {
+  if (dtype == LA_F32) return plan_simt(BH, N, D, M, true);
+  return D <= 64 && M <= 64 ? gated_mma_backward_plan(BH, N) : gated_mma_wide_plan(BH, N, D, M);
+}
+
+static GatedWorkspace backward_workspace(void* ws, const GatedPlan& p, int D, int M, int dtype) {
+  if (dtype == LA_F32) return carve(ws, p, D, M, true, backward_dots(D, M));
+  return carve(ws, p, D, M, true, 0,
+               D <= 64 && M <= 64 ? gated_mma_backward_scratch(p) : gated_mma_wide_scratch(p, D, M));
 }
 
 size_t gated_backward_workspace(int BH, int N, int D, int M, int dtype) {
-  if (backward_on_mma(D, M, dtype)) {
-    const GatedPlan p = gated_mma_backward_plan(BH, N);
-    return carve(nullptr, p, D, M, true, 0, gated_mma_backward_scratch(p)).bytes;
-  }
-  return carve(nullptr, plan_simt(BH, N, D, M, true), D, M, true, row_blocks(D, M)).bytes;
+  return backward_workspace(nullptr, backward_plan(BH, N, D, M, dtype), D, M, dtype).bytes;
 }
 
 cudaError_t gated_forward(const GatedForward& f, void* ws, cudaStream_t st) {
-  if (f.dtype == LA_F32) return simt_forward(f, ws, st);
   const GatedPlan p = forward_plan(f.B * f.H, f.N, f.D, f.M, f.dtype);
-  return gated_mma_forward(f, carve(ws, p, f.D, f.M, false, 0), st);
+  const GatedWorkspace w = carve(ws, p, f.D, f.M, false, 0);
+  return f.dtype == LA_F32 ? simt_forward(f, p, w, st) : gated_mma_forward(f, p, w, st);
 }
 
 cudaError_t gated_backward(const GatedBackward& f, void* ws, cudaStream_t st) {
-  if (backward_on_mma(f.D, f.M, f.dtype)) {
-    const GatedPlan p = gated_mma_backward_plan(f.B * f.H, f.N);
-    return gated_mma_backward(
-        f, p, carve(ws, p, f.D, f.M, true, 0, gated_mma_backward_scratch(p)), st);
-  }
-  return f.dtype == LA_F32 ? simt_backward_t<float>(f, ws, st)
-                           : simt_backward_t<__nv_bfloat16>(f, ws, st);
+  const GatedPlan p = backward_plan(f.B * f.H, f.N, f.D, f.M, f.dtype);
+  const GatedWorkspace w = backward_workspace(ws, p, f.D, f.M, f.dtype);
+  if (f.dtype == LA_F32) return simt_backward(f, p, w, st);
+  return f.D <= 64 && f.M <= 64 ? gated_mma_backward(f, p, w, st) : gated_mma_wide_backward(f, p, w, st);
 }
 
 cudaError_t gated_decode(const void* q, const void* k, const void* v, const void* g, float* S,

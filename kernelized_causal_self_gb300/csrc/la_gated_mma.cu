@@ -36,100 +36,124 @@ namespace {
 
 constexpr int kThreads = 128;
 
-struct FwdArgs {
-  const bf16 *q, *k, *v, *g;  // state pass: k, v are the pair whose outer products are summed
+// One walk over a segment's chunks, with a state X [ZD][UD]:
+//   forward   out_i = z_i (exp(G_i) X) + sum over j <= i of L_ij (z_i . w_j) u_j
+//             X = exp(G) X + sum over j of exp(G - G_j) w_j u_j^T
+//   reverse   out_j = z_j (exp(G - G_j) X) + sum over i >= j of L_ij (z_j . w_i) u_i
+//             X = exp(G) X + sum over i of exp(G_i) w_i u_i^T,  last chunk first
+//   out  forward, z = q,    w = k,    u = v,    X = S
+//   dQ   forward, z = dout, w = v,    u = k,    X = S^T
+//   dK   reverse, z = v,    w = dout, u = q,    X = E^T
+//   dV   reverse, z = k,    w = q,    u = dout, X = E
+// (the gradients this way only for D or M over 64; up to 64, la_gated_mma_bwd.cu has
+// them in one kernel). A CTA has 64 of u's columns.
+struct WalkArgs {
+  const bf16 *z, *w, *u, *g;
   bf16* out;
-  int D, M, N, len, n_seg;
+  int ZD, UD, N, BH, len, n_seg;
+  int rs, cs;            // X's element (r, c) of an entry is at r * rs + c * cs
   const int* lens;
   int H;
-  const float* seg_in;
+  const float* seg_in;   // segments' entries of X (nullptr: one segment, `init`)
   float *seg_out, *decay;
   const float* init;
   float* fin;
   GatedEntries entries;
   WorkspaceHeader* hdr;
+  // for the gates' gradient: p . out by token and column block (forward; reverse: of what
+  // the chunk itself adds, and in `inter` of X's part); X of every chunk as the threads
+  // hold it (forward: written; reverse: read, and `ends` the warps' sums of X times it,
+  // decayed over the chunk)
+  const bf16* p;
+  float *dots, *inter, *ends;
+  float4* kept;
 };
 
 template <int DZ, bool OUT>
-struct FwdSmem {
-  static constexpr int kQ = OUT ? kC * DZ * 2 : 0, kK = kC * DZ * 2, kV = kC * 64 * 2;
-  static constexpr int kStage = kQ + kK + kV;
-  static constexpr int kS = OUT ? DZ * 64 * 2 : 0;  // S in bf16, [d][m], one of two
-  static constexpr int kBytes = 2 * kStage + 2 * kS + 4 * kC * 4 * 2;
+struct WalkSmem {
+  static constexpr int kZ = OUT ? kC * DZ * 2 : 0, kW = kC * DZ * 2, kU = kC * 64 * 2;
+  static constexpr int kStage = kZ + kW + kU;
+  static constexpr int kX = OUT ? DZ * 64 * 2 : 0;  // X in bf16, one of two
+  static constexpr int kBytes = 2 * kStage + 2 * kX + 4 * kC * 4 * 3;
 };
 
-// OUT: outputs (and, with one segment, the final state). Otherwise the state pass: the
-// segment's own S from zero, over k, v with weights exp(G - G_j), or (REV) its own
-// gradient of the incoming state from zero, over q, dout with weights exp(G_i), chunks
-// from the last to the first.
-// FRESH: a chunk's update of S is summed apart and then added, in float32 arithmetic that
-// rounds; the tensor cores' own sums truncate, which over thousands of chunks would
-// leave a bias in a state that hardly decays. Taken wherever S leaves the kernel in
-// float32; where it only goes on as a bf16 operand, it is summed in place, which leaves
-// registers for a third CTA per SM.
-template <int DZ, bool OUT, bool REV, bool FRESH>
-__device__ __forceinline__ void walk_chunks(const FwdArgs& a) {
-  using Sm = FwdSmem<DZ, OUT>;
+// OUT: outputs (and, with one segment, the final state), else the state pass: the
+// segment's own X from zero.
+// EXACT: a chunk's update of X is summed apart, with its operand to 24 bits, and added in
+// float32 arithmetic that rounds (the tensor cores' own sums truncate, which over
+// thousands of chunks would leave a bias in a state that hardly decays). Taken where X
+// leaves the kernel as a float32 result; where it only goes on as a bf16 operand, 16 bits
+// and sums in place do, and leave registers for more CTAs per SM.
+// DOTS: the parts of the gates' gradient.
+template <int DZ, bool OUT, bool REV, bool EXACT, bool DOTS = false>
+__device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
+  using Sm = WalkSmem<DZ, OUT>;
   constexpr int KS = DZ / 16, DT = DZ / 64;
   extern __shared__ __align__(128) uint8_t smem[];
-  const uint32_t base = tc::smem_u32(smem);
-  const uint32_t s_op = base + 2 * Sm::kStage;
+  const uint32_t base = tc::smem_u32(smem), x_op = base + 2 * Sm::kStage;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  float* Gs = reinterpret_cast<float*>(smem + 2 * Sm::kStage + 2 * Sm::kS) + warp * 2 * kC;
-  float* Ws = Gs + kC;
+  const int row = lane >> 2, col = (lane & 3) * 2;  // of an accumulator
+  float* Gs = reinterpret_cast<float*>(smem + 2 * Sm::kStage + 2 * Sm::kX) + warp * 3 * kC;
+  float *Ws = Gs + kC, *Vs = Ws + kC;
+  const Lane<DZ> ln;
+  const Lane<64> ln64;
 
   tc::pdl_wait();
   const int bh = blockIdx.x / a.n_seg, seg = blockIdx.x % a.n_seg;
-  const int m0 = blockIdx.y * 64;
-  // the causal product gives a chunk's last rows the most work: turn the rows' order
-  // from CTA to CTA, so that no scheduler gets all of them
+  const int c0 = blockIdx.y * 64;
+  // the causal product gives a chunk's rows unequal work: turn their order from CTA to
+  // CTA, so that no scheduler gets all of the most
   const int rb = (warp + blockIdx.x) & 3;
   const int n = gated_length(a.lens, a.H, bh, a.N);
   const int tb = min(seg * a.len, n), te = min(tb + a.len, n);
   const int chunks = (te - tb + kC - 1) / kC;
   const size_t seq = (size_t)bh * a.N;
   const long long entry = a.entries.at(bh);
-  if (entry < 0 && seg == 0 && m0 == 0 && tid == 0 && a.hdr) a.hdr->status = LA_ERR_INVALID_ARG;
+  if (entry < 0 && seg == 0 && c0 == 0 && tid == 0 && a.hdr) a.hdr->status = LA_ERR_INVALID_ARG;
+  const size_t entry_size = (size_t)a.ZD * a.UD;
 
-  const int row = lane >> 2, col = (lane & 3) * 2;  // of an accumulator
-  const Lane<DZ> ln;
-  const Lane<64> ln64;
-  float s[DT][8][4];
+  float x[DT][8][4];
   {
     const float* in = nullptr;
     if (OUT && a.seg_in)
-      in = a.seg_in + ((size_t)bh * (a.n_seg + 1) + seg) * a.D * a.M;
+      in = a.seg_in + ((size_t)bh * (a.n_seg + 1) + seg + (REV ? 1 : 0)) * entry_size;
     else if (OUT && a.init && entry >= 0)
-      in = a.init + (size_t)entry * a.D * a.M;
+      in = a.init + (size_t)entry * entry_size;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int d = dt * 64 + rb * 16 + row + 8 * h, m = m0 + 8 * j + col;
-          float2 x = make_float2(0.f, 0.f);
-          if (in && d < a.D && m < a.M) x = *reinterpret_cast<const float2*>(in + (size_t)d * a.M + m);
-          s[dt][j][2 * h] = x.x;
-          s[dt][j][2 * h + 1] = x.y;
+          const int r = dt * 64 + rb * 16 + row + 8 * h, c = c0 + 8 * j + col;
+          float2 v = make_float2(0.f, 0.f);
+          if (in && r < a.ZD && c < a.UD) {
+            const float* at = in + (size_t)r * a.rs + (size_t)c * a.cs;
+            if (a.cs == 1)
+              v = *reinterpret_cast<const float2*>(at);
+            else
+              v = make_float2(at[0], at[a.cs]);
+          }
+          x[dt][j][2 * h] = v.x;
+          x[dt][j][2 * h + 1] = v.y;
         }
   }
   auto keep_op = [&](int buf) {
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt) store_op(ln64, s_op + buf * Sm::kS, dt * 64 + rb * 16, 0, s[dt]);
+    for (int dt = 0; dt < DT; ++dt) store_op(ln64, x_op + buf * Sm::kX, dt * 64 + rb * 16, 0, x[dt]);
   };
   auto load_chunk = [&](int c) {
     const int t0 = tb + c * kC, rows = min(kC, te - t0);
     const uint32_t at = base + (c & 1) * Sm::kStage;
-    if (OUT) load_tile<DZ, kThreads>(at, a.q + (seq + t0) * a.D, rows, a.D, 0);
-    load_tile<DZ, kThreads>(at + Sm::kQ, a.k + (seq + t0) * a.D, rows, a.D, 0);
-    load_tile<64, kThreads>(at + Sm::kQ + Sm::kK, a.v + (seq + t0) * a.M, rows, a.M, m0);
+    if (OUT) load_tile<DZ, kThreads>(at, a.z + (seq + t0) * a.ZD, rows, a.ZD, 0);
+    load_tile<DZ, kThreads>(at + Sm::kZ, a.w + (seq + t0) * a.ZD, rows, a.ZD, 0);
+    load_tile<64, kThreads>(at + Sm::kZ + Sm::kW, a.u + (seq + t0) * a.UD, rows, a.UD, c0);
   };
   auto chunk_of = [&](int i) { return REV ? chunks - 1 - i : i; };
   auto raw_gates = [&](int c) { return load_gates(a.g + seq, tb + c * kC, te); };
 
   ushort2 g_next = make_ushort2(0, 0);
-  float dec_all = 0.f;  // sum of the segment's g, base 2
+  float all = 0.f;  // sum of the segment's gates, base 2
   if (chunks > 0) {
     load_chunk(chunk_of(0));
     g_next = raw_gates(chunk_of(0));
@@ -141,50 +165,112 @@ __device__ __forceinline__ void walk_chunks(const FwdArgs& a) {
     const int c = chunk_of(i);
     cp_async_wait<0>();
     __syncthreads();  // chunk i has landed; every warp is done with chunk i - 1
+    const uint32_t z_at = base + (c & 1) * Sm::kStage, w_at = z_at + Sm::kZ, u_at = w_at + Sm::kW;
+    const int r0 = rb * 16, t0 = tb + c * kC + r0;
+    uint32_t f[OUT ? KS : 1][4];
+    if (OUT) {
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) ln.load_a(f[ks], z_at, r0, ks);
+    }
+    if (DOTS) {  // z's rows are this warp's alone and read: p's take their place
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = e * 4 + (lane >> 3), ch = lane & 7;
+        const bool live = t0 + r < te && c0 + ch * 8 < a.UD;
+        cp_async16(z_at + (r0 + r) * DZ * 2 + ((ch ^ (r & 7)) << 4),
+                   live ? a.p + (seq + t0 + r) * a.UD + c0 + ch * 8 : a.p, live);
+      }
+      cp_async_commit();
+    }
     const float2 g = gates_of(g_next);
     if (i + 1 < chunks) {
       load_chunk(chunk_of(i + 1));
       g_next = raw_gates(chunk_of(i + 1));
     }
     cp_async_commit();
-    const float total = chunk_gates<REV>(g, Gs, Ws);
+    const float total = chunk_gates(g, Gs, Ws, REV ? Vs : nullptr);
     const float dec = gated_decay(total * kLn2);
-    dec_all += total;
+    all += total;
 
-    const uint32_t q_at = base + (c & 1) * Sm::kStage, k_at = q_at + Sm::kQ, v_at = k_at + Sm::kK;
-    float o[8][4];
     if (OUT) {
-      uint32_t qa[KS][4];
-      const float gi[2] = {Gs[rb * 16 + row], Gs[rb * 16 + row + 8]};
+      const size_t kept_at = ((((size_t)blockIdx.y * a.BH + bh) * ((a.N + kC - 1) / kC) + tb / kC + c) *
+                              DT * 8) * kThreads + tid;
+      if (DOTS && !REV) {
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) ln.load_a(qa[ks], q_at, rb * 16, ks);
-      product<true>(ln64, o, qa, s_op + (i & 1) * Sm::kS);
-      scale_rows(o, ex2(gi[0]), ex2(gi[1]));
+        for (int e = 0; e < DT * 8; ++e) a.kept[kept_at + (size_t)e * kThreads] = keep_tile(x[e >> 3][e & 7]);
+      }
+      if (DOTS && REV) {
+        float2 se = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < DT * 8; ++e)
+          se = dot_kept(a.kept[kept_at + (size_t)e * kThreads], x[e >> 3][e & 7], se);
+        float sum = se.x + se.y;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0)
+          a.ends[(((size_t)blockIdx.y * a.BH + bh) * ((a.N + kC - 1) / kC) + tb / kC + c) * 4 + warp] =
+              sum * dec;
+      }
+      float o[8][4];
+      const float gr[2] = {Gs[r0 + row], Gs[r0 + row + 8]};
+      product<true>(ln64, o, f, x_op + (i & 1) * Sm::kX);
+      if (REV)
+        scale_rows(o, Ws[r0 + row], Ws[r0 + row + 8]);
+      else
+        scale_rows(o, ex2(gr[0]), ex2(gr[1]));
+      const size_t dots_at = ((size_t)blockIdx.y * a.BH + bh) * a.N + t0 + row;
+      float2 inter = make_float2(0.f, 0.f);
+      if (DOTS && REV) {
+        cp_async_wait<1>();
+        __syncwarp();
+        inter = row_dots(ln, z_at, r0, o);
+      }
       uint32_t p[4];
 #pragma unroll 1
-      for (int jb = 0; jb < rb; ++jb) {
-        masked_block<true, false>(ln, p, qa, k_at, jb, gi, Gs);
-        add_block(ln64, o, p, v_at, jb);
+      for (int b = REV ? rb + 1 : 0; b < (REV ? 4 : rb); ++b) {
+        masked_block<!REV, false>(ln, p, f, w_at, b, gr, Gs);
+        add_block(ln64, o, p, u_at, b);
       }
-      masked_block<true, true>(ln, p, qa, k_at, rb, gi, Gs);
-      add_block(ln64, o, p, v_at, rb);
-      // through this warp's rows of the Q tile, which no other warp reads
-      const int t0 = tb + c * kC + rb * 16;
-      store_rows(ln, q_at, rb * 16, o, a.out + (seq + t0) * a.M + m0, te - t0, a.M - m0, a.M);
+      masked_block<!REV, true>(ln, p, f, w_at, rb, gr, Gs);
+      add_block(ln64, o, p, u_at, rb);
+      if (DOTS) {
+        if (!REV) {
+          cp_async_wait<1>();
+          __syncwarp();
+        }
+        float2 d = row_dots(ln, z_at, r0, o);
+        if (REV) {
+          d.x -= inter.x;
+          d.y -= inter.y;
+        }
+        if ((lane & 3) == 0) {
+          if (t0 + row < te) {
+            a.dots[dots_at] = d.x;
+            if (REV) a.inter[dots_at] = inter.x;
+          }
+          if (t0 + row + 8 < te) {
+            a.dots[dots_at + 8] = d.y;
+            if (REV) a.inter[dots_at + 8] = inter.y;
+          }
+        }
+      }
+      // through this warp's rows of z's tile, which no other warp reads
+      store_rows(ln, z_at, r0, o, a.out + (seq + t0) * a.UD + c0, te - t0, a.UD - c0, a.UD);
     }
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) {
-      if (FRESH) {
-        float u[8][4];
-        add_outer<DZ, 8, true>(ln, ln64, u, k_at, Ws, 4 * dt + rb, v_at, 0);
+      if (EXACT) {
+        float y[8][4];
+        add_outer<true>(ln, ln64, y, w_at, REV ? Vs : Ws, 4 * dt + rb, u_at, 0);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            pair_of(s[dt][j], h) = fma2(make_float2(dec, dec), pair_of(s[dt][j], h), pair_of(u[j], h));
+            pair_of(x[dt][j], h) = fma2(make_float2(dec, dec), pair_of(x[dt][j], h), pair_of(y[j], h));
       } else {
-        scale_rows(s[dt], dec, dec);
-        add_outer<DZ, 8>(ln, ln64, s[dt], k_at, Ws, 4 * dt + rb, v_at, 0);
+        scale_rows(x[dt], dec, dec);
+        add_outer<false>(ln, ln64, x[dt], w_at, REV ? Vs : Ws, 4 * dt + rb, u_at, 0);
       }
     }
     if (OUT && i + 1 < chunks) keep_op((i + 1) & 1);
@@ -192,9 +278,9 @@ __device__ __forceinline__ void walk_chunks(const FwdArgs& a) {
 
   float* to = nullptr;
   if (!OUT)
-    to = a.seg_out + ((size_t)bh * (a.n_seg + 1) + seg) * a.D * a.M;
+    to = a.seg_out + ((size_t)bh * (a.n_seg + 1) + seg) * entry_size;
   else if (a.fin && entry >= 0)
-    to = a.fin + (size_t)entry * a.D * a.M;
+    to = a.fin + (size_t)entry * entry_size;
   if (to)
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
@@ -202,53 +288,106 @@ __device__ __forceinline__ void walk_chunks(const FwdArgs& a) {
       for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int d = dt * 64 + rb * 16 + row + 8 * h, m = m0 + 8 * j + col;
-          if (d < a.D && m < a.M)
-            *reinterpret_cast<float2*>(to + (size_t)d * a.M + m) =
-                make_float2(s[dt][j][2 * h], s[dt][j][2 * h + 1]);
+          const int r = dt * 64 + rb * 16 + row + 8 * h, m = c0 + 8 * j + col;
+          if (r < a.ZD && m < a.UD)  // (only S and E leave: rs = UD, cs = 1)
+            *reinterpret_cast<float2*>(to + (size_t)r * a.UD + m) =
+                make_float2(x[dt][j][2 * h], x[dt][j][2 * h + 1]);
         }
-  if (!OUT && a.decay && m0 == 0 && tid == 0)
-    a.decay[(size_t)bh * a.n_seg + seg] = gated_decay(dec_all * kLn2);
+  if (!OUT && a.decay && c0 == 0 && tid == 0)
+    a.decay[(size_t)bh * a.n_seg + seg] = gated_decay(all * kLn2);
 }
 
-template <int DZ, bool FRESH>
-__global__ void __launch_bounds__(kThreads, DZ == 64 && !FRESH ? 3 : 2)
-gated_forward_kernel(const FwdArgs a) {
-  walk_chunks<DZ, true, false, FRESH>(a);
+template <int DZ, bool EXACT>
+__global__ void __launch_bounds__(kThreads, DZ == 64 && !EXACT ? 3 : 2)
+gated_forward_kernel(const WalkArgs a) {
+  walk_chunks<DZ, true, false, EXACT>(a);
 }
 
 // blockIdx.z: the segments' states, or their gradients
-template <int DZ>
+template <int DZ, bool EXACT>
 __global__ void __launch_bounds__(kThreads, DZ == 64 ? 3 : 2)
-gated_states_kernel(const FwdArgs a, const FwdArgs back) {
+gated_states_kernel(const WalkArgs a, const WalkArgs back) {
   if (blockIdx.z == 0)
-    walk_chunks<DZ, false, false, true>(a);
+    walk_chunks<DZ, false, false, EXACT>(a);
   else
-    walk_chunks<DZ, false, true, true>(back);
+    walk_chunks<DZ, false, true, EXACT>(back);
 }
 
-template <int DZ, bool FRESH>
-cudaError_t launch_forward(const FwdArgs& a, int BH, cudaStream_t st) {
-  using Sm = FwdSmem<DZ, true>;
-  auto kernel = gated_forward_kernel<DZ, FRESH>;
-  cudaError_t e = tcx::configure(kernel, Sm::kBytes);
+template <int DZ, bool REV, bool DOTS>
+__global__ void __launch_bounds__(kThreads, DZ == 64 ? 3 : 2) gated_gradient_kernel(const WalkArgs a) {
+  walk_chunks<DZ, true, REV, false, DOTS>(a);
+}
+
+template <typename K, typename... Args>
+cudaError_t launch(K kernel, int smem, dim3 grid, cudaStream_t st, Args... args) {
+  cudaError_t e = tcx::configure(kernel, smem);
   if (e != cudaSuccess) return e;
-  e = tcx::launch_pdl(kernel, dim3((unsigned)(BH * a.n_seg), (unsigned)((a.M + 63) / 64)),
-                      dim3(kThreads), Sm::kBytes, st, a);
+  e = tcx::launch_pdl(kernel, grid, dim3(kThreads), smem, st, args...);
   count_launches(1);
   return e;
 }
 
-template <int DZ>
-cudaError_t launch_states(const FwdArgs& a, const FwdArgs* back, int BH, cudaStream_t st) {
-  using Sm = FwdSmem<DZ, false>;
-  auto kernel = gated_states_kernel<DZ>;
-  cudaError_t e = tcx::configure(kernel, Sm::kBytes);
-  if (e != cudaSuccess) return e;
-  e = tcx::launch_pdl(kernel, dim3((unsigned)(BH * a.n_seg), (unsigned)((a.M + 63) / 64), back ? 2 : 1),
-                      dim3(kThreads), Sm::kBytes, st, a, back ? *back : a);
-  count_launches(1);
-  return e;
+dim3 walk_grid(const WalkArgs& a, int z = 1) {
+  return dim3((unsigned)(a.BH * a.n_seg), (unsigned)((a.UD + 63) / 64), (unsigned)z);
+}
+
+template <bool EXACT>
+cudaError_t launch_forward(const WalkArgs& a, cudaStream_t st) {
+  return a.ZD <= 64 ? launch(gated_forward_kernel<64, EXACT>, WalkSmem<64, true>::kBytes, walk_grid(a), st, a)
+                    : launch(gated_forward_kernel<128, EXACT>, WalkSmem<128, true>::kBytes, walk_grid(a), st, a);
+}
+
+template <bool EXACT>
+cudaError_t launch_states(const WalkArgs& a, const WalkArgs& back, int jobs, cudaStream_t st) {
+  return a.ZD <= 64
+             ? launch(gated_states_kernel<64, EXACT>, WalkSmem<64, false>::kBytes, walk_grid(a, jobs), st, a, back)
+             : launch(gated_states_kernel<128, EXACT>, WalkSmem<128, false>::kBytes, walk_grid(a, jobs), st, a, back);
+}
+
+template <bool REV, bool DOTS>
+cudaError_t launch_gradient(const WalkArgs& a, cudaStream_t st) {
+  return a.ZD <= 64
+             ? launch(gated_gradient_kernel<64, REV, DOTS>, WalkSmem<64, true>::kBytes, walk_grid(a), st, a)
+             : launch(gated_gradient_kernel<128, REV, DOTS>, WalkSmem<128, true>::kBytes, walk_grid(a), st, a);
+}
+
+// dg of a chunk from its dots (see la_gated_mma_bwd.cu): a warp each, two tokens a lane.
+__global__ void __launch_bounds__(kThreads)
+gated_chunk_dg_kernel(const float* __restrict__ dot_q, const float* __restrict__ dot_k,
+                      const float* __restrict__ inter, const float* __restrict__ ends,
+                      bf16* __restrict__ dg, int BH, int N, int blocks) {
+  tc::pdl_wait();
+  const int chunks = (N + kC - 1) / kC, lane = threadIdx.x & 31;
+  const long long at = (long long)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  if (at >= (long long)BH * chunks) return;
+  const long long bh = at / chunks;
+  const int t0 = (int)(at % chunks) * kC + 2 * lane;
+  float x[2] = {0.f, 0.f}, b[2] = {0.f, 0.f}, se = 0.f;
+  for (int y = 0; y < blocks; ++y) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const size_t i = ((size_t)y * BH + bh) * N + t0 + e;
+      if (t0 + e < N) {
+        x[e] += dot_q[i] - dot_k[i];
+        b[e] += inter[i];
+      }
+    }
+    const float4 w = *reinterpret_cast<const float4*>(ends + (((size_t)y * BH + bh) * chunks + at % chunks) * 4);
+    se += w.x + w.y + w.z + w.w;
+  }
+  float down = x[0] + x[1], up = b[0] + b[1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float d = __shfl_down_sync(0xffffffffu, down, o);
+    const float u = __shfl_up_sync(0xffffffffu, up, o);
+    if (lane + o < 32) down += d;
+    if (lane >= o) up += u;
+  }
+  float after = __shfl_down_sync(0xffffffffu, down, 1), before = __shfl_up_sync(0xffffffffu, up, 1);
+  if (lane == 31) after = 0.f;
+  if (lane == 0) before = 0.f;
+  if (t0 < N) dg[bh * N + t0] = __float2bfloat16_rn(se + down + before);
+  if (t0 + 1 < N) dg[bh * N + t0 + 1] = __float2bfloat16_rn(se + (x[1] + after) + (before + b[0]));
 }
 
 }  // namespace
@@ -273,14 +412,15 @@ GatedPlan gated_mma_forward_plan(int BH, int N, int D, int M) {
 
 cudaError_t gated_mma_states(const GatedPlan& p, const void* k, const void* v, const void* q,
                              const void* dout, const void* g, int D, int M, const int* lens, int H,
-                             const GatedWorkspace& w, cudaStream_t st) {
-  FwdArgs s{};
-  s.k = static_cast<const bf16*>(k);
-  s.v = static_cast<const bf16*>(v);
+                             bool exact, const GatedWorkspace& w, cudaStream_t st) {
+  WalkArgs s{};
+  s.w = static_cast<const bf16*>(k);
+  s.u = static_cast<const bf16*>(v);
   s.g = static_cast<const bf16*>(g);
-  s.D = D;
-  s.M = M;
+  s.ZD = D;
+  s.UD = M;
   s.N = p.N;
+  s.BH = p.BH;
   s.len = p.len;
   s.n_seg = p.n_seg;
   s.lens = lens;
@@ -288,26 +428,29 @@ cudaError_t gated_mma_states(const GatedPlan& p, const void* k, const void* v, c
   s.entries.H = H;
   s.seg_out = w.S;
   s.decay = w.decay;
-  FwdArgs back = s;
-  back.k = static_cast<const bf16*>(q);
-  back.v = static_cast<const bf16*>(dout);
+  WalkArgs back = s;
+  back.w = static_cast<const bf16*>(q);
+  back.u = static_cast<const bf16*>(dout);
   back.seg_out = w.E;
   back.decay = nullptr;
-  const FwdArgs* b = dout ? &back : nullptr;
-  return D <= 64 ? launch_states<64>(s, b, p.BH, st) : launch_states<128>(s, b, p.BH, st);
+  const int jobs = dout ? 2 : 1;
+  return exact ? launch_states<true>(s, back, jobs, st) : launch_states<false>(s, back, jobs, st);
 }
 
-cudaError_t gated_mma_forward(const GatedForward& f, const GatedWorkspace& w, cudaStream_t st) {
-  const GatedPlan p = gated_mma_forward_plan(f.B * f.H, f.N, f.D, f.M);
-  FwdArgs a{};
-  a.q = static_cast<const bf16*>(f.q);
-  a.k = static_cast<const bf16*>(f.k);
-  a.v = static_cast<const bf16*>(f.v);
+cudaError_t gated_mma_forward(const GatedForward& f, const GatedPlan& p, const GatedWorkspace& w,
+                              cudaStream_t st) {
+  WalkArgs a{};
+  a.z = static_cast<const bf16*>(f.q);
+  a.w = static_cast<const bf16*>(f.k);
+  a.u = static_cast<const bf16*>(f.v);
   a.g = static_cast<const bf16*>(f.g);
   a.out = static_cast<bf16*>(f.out);
-  a.D = f.D;
-  a.M = f.M;
+  a.ZD = f.D;
+  a.UD = f.M;
+  a.rs = f.M;
+  a.cs = 1;
   a.N = f.N;
+  a.BH = p.BH;
   a.len = p.len;
   a.n_seg = p.n_seg;
   a.lens = f.lens;
@@ -315,7 +458,8 @@ cudaError_t gated_mma_forward(const GatedForward& f, const GatedWorkspace& w, cu
   a.entries = GatedEntries{f.slots, f.pool, f.H};
   a.hdr = w.hdr;
   if (p.n_seg > 1) {
-    cudaError_t e = gated_mma_states(p, f.k, f.v, nullptr, nullptr, f.g, f.D, f.M, f.lens, f.H, w, st);
+    cudaError_t e = gated_mma_states(p, f.k, f.v, nullptr, nullptr, f.g, f.D, f.M, f.lens, f.H,
+                                     f.S != nullptr, w, st);
     if (e != cudaSuccess) return e;
     if ((e = gated_scan(p, w, f.S0, f.S, a.entries, f.D * f.M, st)) != cudaSuccess) return e;
     a.seg_in = w.S;
@@ -323,9 +467,78 @@ cudaError_t gated_mma_forward(const GatedForward& f, const GatedWorkspace& w, cu
     a.init = f.S0;
     a.fin = f.S;
   }
-  if (a.fin)
-    return f.D <= 64 ? launch_forward<64, true>(a, p.BH, st) : launch_forward<128, true>(a, p.BH, st);
-  return f.D <= 64 ? launch_forward<64, false>(a, p.BH, st) : launch_forward<128, false>(a, p.BH, st);
+  return a.fin ? launch_forward<true>(a, st) : launch_forward<false>(a, st);
+}
+
+// ---- the backward for D or M over 64: states, scans, then dQ, dK and dV a walk each
+
+GatedPlan gated_mma_wide_plan(int BH, int N, int D, int M) {
+  return gated_mma_plan(BH, N, D > M ? D : M, 2);
+}
+
+namespace {
+int wide_blocks(int D) { return (D + 63) / 64; }
+size_t wide_kept(const GatedPlan& p, int D, int M) {  // X of every chunk: rows of M, columns of D
+  return sizeof(float4) * 8 * kThreads * (size_t)wide_blocks(D) * wide_blocks(M) * p.BH * ((p.N + kC - 1) / kC);
+}
+}  // namespace
+
+size_t gated_mma_wide_scratch(const GatedPlan& p, int D, int M) {
+  const size_t blocks = wide_blocks(D), bh = p.BH;
+  return wide_kept(p, D, M) + 16 * blocks * bh * ((p.N + kC - 1) / kC) + 3 * align_up(4 * blocks * bh * p.N, 16);
+}
+
+cudaError_t gated_mma_wide_backward(const GatedBackward& f, const GatedPlan& p, const GatedWorkspace& w,
+                                    cudaStream_t st) {
+  const size_t blocks = wide_blocks(f.D), chunks = (p.N + kC - 1) / kC, dots = align_up(4 * blocks * p.BH * p.N, 16);
+  char* at = static_cast<char*>(w.scratch);
+  float4* kept = reinterpret_cast<float4*>(at);
+  float* ends = reinterpret_cast<float*>(at += wide_kept(p, f.D, f.M));
+  float* dot_q = reinterpret_cast<float*>(at += 16 * blocks * p.BH * chunks);
+  float* dot_k = reinterpret_cast<float*>(at += dots);
+  float* inter = reinterpret_cast<float*>(at += dots);
+  cudaError_t e = gated_mma_states(p, f.k, f.v, f.q, f.dout, f.g, f.D, f.M, nullptr, f.H,
+                                   f.dS0 != nullptr, w, st);
+  if (e != cudaSuccess) return e;
+  const GatedGradients back{f.dS, f.dS0};
+  if ((e = gated_scan(p, w, f.S0, nullptr, GatedEntries{nullptr, 0, f.H}, f.D * f.M, st, &back)) != cudaSuccess)
+    return e;
+  WalkArgs a{};
+  a.g = static_cast<const bf16*>(f.g);
+  a.N = f.N;
+  a.BH = p.BH;
+  a.len = p.len;
+  a.n_seg = p.n_seg;
+  a.H = f.H;
+  a.entries.H = f.H;
+  a.kept = kept;
+  a.ends = ends;
+  a.inter = inter;
+  WalkArgs dq = a, dk = a, dv = a;
+  dq.z = dk.w = dv.u = static_cast<const bf16*>(f.dout);
+  dq.w = dk.z = static_cast<const bf16*>(f.v);
+  dq.u = dk.p = dv.z = static_cast<const bf16*>(f.k);
+  dq.p = dk.u = dv.w = static_cast<const bf16*>(f.q);
+  dq.out = static_cast<bf16*>(f.dq);
+  dk.out = static_cast<bf16*>(f.dk);
+  dv.out = static_cast<bf16*>(f.dv);
+  dq.ZD = dk.ZD = dv.UD = f.M;
+  dq.UD = dk.UD = dv.ZD = f.D;
+  dq.rs = dk.rs = dv.cs = 1;
+  dq.cs = dk.cs = dv.rs = f.M;
+  dq.seg_in = w.S;
+  dk.seg_in = dv.seg_in = w.E;
+  dq.dots = dot_q;
+  dk.dots = dot_k;
+  if ((e = launch_gradient<false, true>(dq, st)) != cudaSuccess) return e;
+  if ((e = launch_gradient<true, true>(dk, st)) != cudaSuccess) return e;
+  if ((e = launch_gradient<true, false>(dv, st)) != cudaSuccess) return e;
+  const long long warps = (long long)p.BH * (long long)chunks;
+  e = tcx::launch_pdl(gated_chunk_dg_kernel, dim3((unsigned)((warps + 3) / 4)), dim3(kThreads), 0, st,
+                      (const float*)dot_q, (const float*)dot_k, (const float*)inter, (const float*)ends,
+                      static_cast<bf16*>(f.dg), p.BH, f.N, (int)blocks);
+  count_launches(1);
+  return e;
 }
 
 }  // namespace la

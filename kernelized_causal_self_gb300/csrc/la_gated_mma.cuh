@@ -24,12 +24,11 @@ __device__ __forceinline__ float2 gates_of(ushort2 g) {
   return make_float2(a < -200.f ? -200.f : a, b < -200.f ? -200.f : b);
 }
 
-// From a lane's two gates: G[i], their inclusive sums over the chunk, and W[i], the
-// weights of the token's outer product in the chunk's state: 2^(sum of the gates behind
-// it), or for the reverse direction 2^(sum up to and including it). Both are the
-// warp's own tables. Returns the chunk's sum.
-template <bool REV>
-__device__ __forceinline__ float chunk_gates(float2 g, float* G, float* W) {
+// From a lane's two gates, tables of the chunk (written by a warp for itself, or by one
+// for all): G[i], their sums up to and including token i; W[i] = 2^(sum of those behind i),
+// what is left of i's outer product in the state after the chunk; V[i] = 2^G[i] (nullptr:
+// not wanted). Returns the chunk's sum.
+__device__ __forceinline__ float chunk_gates(float2 g, float* G, float* W, float* V) {
   const int lane = threadIdx.x & 31;
   const float both = g.x + g.y;
   float up = both, down = both;
@@ -47,9 +46,8 @@ __device__ __forceinline__ float chunk_gates(float2 g, float* G, float* W) {
   const float2 incl = make_float2(before + g.x, up);
   __syncwarp();
   *reinterpret_cast<float2*>(G + 2 * lane) = incl;
-  *reinterpret_cast<float2*>(W + 2 * lane) =
-      REV ? make_float2(mma::ex2(incl.x), mma::ex2(incl.y))
-          : make_float2(mma::ex2(after + g.y), mma::ex2(after));
+  *reinterpret_cast<float2*>(W + 2 * lane) = make_float2(mma::ex2(after + g.y), mma::ex2(after));
+  if (V) *reinterpret_cast<float2*>(V + 2 * lane) = make_float2(mma::ex2(incl.x), mma::ex2(incl.y));
   __syncwarp();
   return __shfl_sync(0xffffffffu, up, 31);
 }
@@ -58,16 +56,21 @@ __device__ __forceinline__ float chunk_gates(float2 g, float* G, float* W) {
 GatedPlan gated_mma_plan(int BH, int N, int M, int resident);
 GatedPlan gated_mma_forward_plan(int BH, int N, int D, int M);
 // each segment's own state from zero and its decay, and (dout not nullptr) its own
-// gradient of the incoming state from zero
+// gradient of the incoming state from zero. exact: to float32's digits, for results.
 cudaError_t gated_mma_states(const GatedPlan& p, const void* k, const void* v, const void* q,
                              const void* dout, const void* g, int D, int M, const int* lens, int H,
-                             const GatedWorkspace& w, cudaStream_t st);
-cudaError_t gated_mma_forward(const GatedForward& f, const GatedWorkspace& w, cudaStream_t st);
-bool gated_mma_backward_supported(int D, int M);
+                             bool exact, const GatedWorkspace& w, cudaStream_t st);
+cudaError_t gated_mma_forward(const GatedForward& f, const GatedPlan& p, const GatedWorkspace& w,
+                              cudaStream_t st);
+// The backward, D and M up to 64 in one kernel, over that a kernel for each gradient.
+// scratch: bytes behind the plan's states.
 GatedPlan gated_mma_backward_plan(int BH, int N);
-// bytes of scratch behind the plan's states
 size_t gated_mma_backward_scratch(const GatedPlan& p);
 cudaError_t gated_mma_backward(const GatedBackward& f, const GatedPlan& p, const GatedWorkspace& w,
                                cudaStream_t st);
+GatedPlan gated_mma_wide_plan(int BH, int N, int D, int M);
+size_t gated_mma_wide_scratch(const GatedPlan& p, int D, int M);
+cudaError_t gated_mma_wide_backward(const GatedBackward& f, const GatedPlan& p, const GatedWorkspace& w,
+                                    cudaStream_t st);
 
 }  // namespace la

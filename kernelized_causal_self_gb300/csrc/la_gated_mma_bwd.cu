@@ -44,7 +44,7 @@ constexpr int kTable = 3 * kC + 4, kParts = 2 * kC + 4;
 constexpr int kSmem = 2 * kStage + 2 * kOp + kTile + 4 * 2 * (kTable + kParts);
 static_assert(kResident * (kSmem + 1024) <= 228 * 1024, "CTAs per SM");
 // scratch of a CTA: S of each chunk as the warps hold it, and q . dQ of each token
-constexpr int kScratchS = kMaxChunks * 4 * kThreads * (int)sizeof(uint4);
+constexpr int kScratchS = kMaxChunks * 8 * kThreads * (int)sizeof(float4);
 constexpr int kScratch = kScratchS + kMaxChunks * kC * (int)sizeof(float);
 
 struct BwdArgs {
@@ -73,28 +73,6 @@ __device__ __forceinline__ void load_state(float (&x)[NT][4], const float* from,
     }
 }
 
-// Rows r0.. of a 64 x 64 tile times c, summed over the columns: rows l / 4 and l / 4 + 8
-__device__ __forceinline__ float2 row_dots(const Lane<64>& ln, uint32_t tile, int r0,
-                                           float (&c)[8][4]) {
-  float2 top = make_float2(0.f, 0.f), bottom = top;
-#pragma unroll
-  for (int jp = 0; jp < 4; ++jp) {
-    uint32_t r[4];
-    ln.load_a(r, tile, r0, jp);
-    top = fma2(both_of(r[0]), pair_of(c[2 * jp], 0), top);
-    bottom = fma2(both_of(r[1]), pair_of(c[2 * jp], 1), bottom);
-    top = fma2(both_of(r[2]), pair_of(c[2 * jp + 1], 0), top);
-    bottom = fma2(both_of(r[3]), pair_of(c[2 * jp + 1], 1), bottom);
-  }
-  float2 s = make_float2(top.x + top.y, bottom.x + bottom.y);
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
-    s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
-  }
-  return s;
-}
-
 __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(const BwdArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t base = tc::smem_u32(smem);
@@ -109,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
   float* tables = reinterpret_cast<float*>(op_mem + 2 * kOp + kTile);
   float* parts = tables + 2 * kTable;
   char* own = a.scratch + (size_t)blockIdx.x * kScratch;
-  uint4* states = reinterpret_cast<uint4*>(own) + tid;  // [chunk][4][thread]
+  float4* states = reinterpret_cast<float4*>(own) + tid;  // [chunk][8][thread]
   float* alpha = reinterpret_cast<float*>(own + kScratchS);        // [chunk][64]: q . dQ
 
   tc::pdl_wait();
@@ -132,9 +110,7 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
     auto raw_gates = [&](int c) { return load_gates(a.g + seq, tb + c * kC, te); };
     auto make_tables = [&](int c, ushort2 raw) {
       float* G = tables + (c & 1) * kTable;
-      const float total = chunk_gates<false>(gates_of(raw), G, G + kC);
-      *reinterpret_cast<float2*>(G + 2 * kC + 2 * lane) =
-          make_float2(ex2(G[2 * lane]), ex2(G[2 * lane + 1]));
+      const float total = chunk_gates(gates_of(raw), G, G + kC, G + 2 * kC);
       if (lane == 0) G[3 * kC] = gated_decay(total * kLn2);
     };
 
@@ -160,10 +136,7 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       ushort2 raw = make_ushort2(0, 0);
       if (maker) raw = raw_gates(c + 1);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        states[(c * 4 + e) * kThreads] =
-            make_uint4(pack2(x[2 * e][0], x[2 * e][1]), pack2(x[2 * e][2], x[2 * e][3]),
-                       pack2(x[2 * e + 1][0], x[2 * e + 1][1]), pack2(x[2 * e + 1][2], x[2 * e + 1][3]));
+      for (int j = 0; j < 8; ++j) states[(c * 8 + j) * kThreads] = keep_tile(x[j]);
       uint32_t f[4][4], p[4];
       float d[8][4];
 #pragma unroll
@@ -188,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       if (c + 1 < chunks) {
         const float dec = Gs[3 * kC];
         scale_rows(x, dec, dec);
-        add_outer(ln, ln, x, k_at, Ws, rb, v_at, 0);
+        add_outer<false>(ln, ln, x, k_at, Ws, rb, v_at, 0);
         store_op(ln, op_base + ((c + 1) & 1) * kOp, r0, 0, x);
       }
       if (maker) make_tables(c + 1, raw);
@@ -236,9 +209,9 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       const bool maker = c > 0 && c + 1 < chunks && warp == (c & 3);
       ushort2 raw = make_ushort2(0, 0);
       if (maker) raw = raw_gates(c - 1);
-      uint4 sc[4];
+      float4 sc[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sc[e] = states[(c * 4 + e) * kThreads];
+      for (int j = 0; j < 8; ++j) sc[j] = states[(c * 8 + j) * kThreads];
       if (c + 1 < chunks && warp == ((c + 1) & 3)) finish(c + 1);
       const float dec = Gs[3 * kC], w0 = Ws[r0 + row], w1 = Ws[r0 + row + 8];
       const float gj[2] = {Gs[r0 + row], Gs[r0 + row + 8]};
@@ -260,12 +233,7 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       {
         float2 se = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          se = fma2(both_of(sc[e].x), pair_of(x[2 * e], 0), se);
-          se = fma2(both_of(sc[e].y), pair_of(x[2 * e], 1), se);
-          se = fma2(both_of(sc[e].z), pair_of(x[2 * e + 1], 0), se);
-          se = fma2(both_of(sc[e].w), pair_of(x[2 * e + 1], 1), se);
-        }
+        for (int j = 0; j < 8; ++j) se = dot_kept(sc[j], x[j], se);
         float s = se.x + se.y;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -293,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       store_rows(ln, out_at, r0, d, a.dk + (seq + t0) * a.D, te - t0, a.D, a.D);
       if (c > 0) {
         scale_rows(x, dec, dec);
-        add_outer(ln, ln, x, q_at, Vs, rb, do_at, 0);
+        add_outer<false>(ln, ln, x, q_at, Vs, rb, do_at, 0);
         store_op(ln, op_base + ((step + 1) & 1) * kOp, r0, 0, x);
       }
       if (maker) make_tables(c - 1, raw);
@@ -309,8 +277,6 @@ int backward_grid(const GatedPlan& p) {
 }
 
 }  // namespace
-
-bool gated_mma_backward_supported(int D, int M) { return D <= 64 && M <= 64; }
 
 // Segments of up to kMaxChunks chunks, of a length that fills whole waves of the
 // resident CTAs.
@@ -335,7 +301,8 @@ cudaError_t gated_mma_backward(const GatedBackward& f, const GatedPlan& p, const
   cudaError_t e;
   BwdArgs a{};
   if (p.n_seg > 1 || f.dS0) {
-    if ((e = gated_mma_states(p, f.k, f.v, f.q, f.dout, f.g, f.D, f.M, nullptr, f.H, w, st)) !=
+    if ((e = gated_mma_states(p, f.k, f.v, f.q, f.dout, f.g, f.D, f.M, nullptr, f.H, f.dS0 != nullptr,
+                              w, st)) !=
         cudaSuccess)
       return e;
     const GatedGradients back{f.dS, f.dS0};

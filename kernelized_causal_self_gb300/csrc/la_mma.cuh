@@ -141,12 +141,14 @@ __device__ __forceinline__ void scale_rows(float (&c)[NT][4], float top, float b
   }
 }
 
-// bf16 pair u times w, as the sum of two bf16 pairs: the product to 16 bits
-__device__ __forceinline__ void scale_split(uint32_t u, float2 w, uint32_t& hi, uint32_t& lo) {
+// bf16 pair u times w, as the sum of two bf16 pairs: the product to 16 bits. Returns what
+// the first leaves.
+__device__ __forceinline__ float2 scale_split(uint32_t u, float2 w, uint32_t& hi, uint32_t& lo) {
   const float2 p = mul2(both_of(u), w);
   hi = pack2(p.x, p.y);
   const float2 r = sub2(p, both_of(hi));
   lo = pack2(r.x, r.y);
+  return r;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -218,6 +220,39 @@ __device__ __forceinline__ void store_rows(const Lane<COLS>& ln, uint32_t tile, 
   }
 }
 
+// Rows r0.. of a tile's first 64 columns times c, summed over the columns: rows l / 4 and
+// l / 4 + 8
+template <int COLS>
+__device__ __forceinline__ float2 row_dots(const Lane<COLS>& ln, uint32_t tile, int r0,
+                                           float (&c)[8][4]) {
+  float2 top = make_float2(0.f, 0.f), bottom = top;
+#pragma unroll
+  for (int jp = 0; jp < 4; ++jp) {
+    uint32_t r[4];
+    ln.load_a(r, tile, r0, jp);
+    top = fma2(both_of(r[0]), pair_of(c[2 * jp], 0), top);
+    bottom = fma2(both_of(r[1]), pair_of(c[2 * jp], 1), bottom);
+    top = fma2(both_of(r[2]), pair_of(c[2 * jp + 1], 0), top);
+    bottom = fma2(both_of(r[3]), pair_of(c[2 * jp + 1], 1), bottom);
+  }
+  float2 s = make_float2(top.x + top.y, bottom.x + bottom.y);
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+    s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+  }
+  return s;
+}
+
+// An accumulator tile kept for the thread's own later use, and its dot with another's
+__device__ __forceinline__ float4 keep_tile(const float (&a)[4]) {
+  return make_float4(a[0], a[1], a[2], a[3]);
+}
+__device__ __forceinline__ float2 dot_kept(float4 kept, float (&a)[4], float2 s) {
+  s = fma2(make_float2(kept.x, kept.y), pair_of(a, 0), s);
+  return fma2(make_float2(kept.z, kept.w), pair_of(a, 1), s);
+}
+
 // A state's rows r0 .. as an operand
 template <int NT>
 __device__ __forceinline__ void store_op(const Lane<64>& ln, uint32_t op, int r0, int c0,
@@ -227,24 +262,30 @@ __device__ __forceinline__ void store_op(const Lane<64>& ln, uint32_t op, int r0
 }
 
 // x += (columns 16 col16.. of tile `a`, weighted by `w` along its rows)^T (columns c0.. of
-// tile `b`), over 64 rows. FIRST: from zero.
-template <int COLS, int NT, bool FIRST = false>
+// tile `b`), over 64 rows. EXACT: from zero, and the weighted columns to 24 bits.
+template <bool EXACT, int COLS, int NT>
 __device__ __forceinline__ void add_outer(const Lane<COLS>& la, const Lane<64>& lb, float (&x)[NT][4],
                                           uint32_t a, const float* w, int col16, uint32_t b, int c0) {
   const int col = (threadIdx.x & 3) * 2;
 #pragma unroll
   for (int at = 0; at < kC; at += 16) {
-    uint32_t f[4], hi[4], lo[4], y[NT / 2][4];
+    uint32_t f[4], hi[4], lo[4], last[4], y[NT / 2][4];
     la.load_a_t(f, a, at, col16);
 #pragma unroll
     for (int jp = 0; jp < NT / 2; ++jp) lb.load_b_t(y[jp], b, at, c0 / 16 + jp);
     const float2 w0 = *reinterpret_cast<const float2*>(w + at + col);
     const float2 w8 = *reinterpret_cast<const float2*>(w + at + 8 + col);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) scale_split(f[e], e < 2 ? w0 : w8, hi[e], lo[e]);
+    for (int e = 0; e < 4; ++e) {
+      const float2 r = scale_split(f[e], e < 2 ? w0 : w8, hi[e], lo[e]);
+      if (EXACT) {
+        const float2 rest = sub2(r, both_of(lo[e]));
+        last[e] = pack2(rest.x, rest.y);
+      }
+    }
 #pragma unroll
     for (int jp = 0; jp < NT / 2; ++jp) {
-      if (FIRST && at == 0) {
+      if (EXACT && at == 0) {
         mma16816_0(x[2 * jp], hi, y[jp][0], y[jp][1]);
         mma16816_0(x[2 * jp + 1], hi, y[jp][2], y[jp][3]);
       } else {
@@ -257,6 +298,12 @@ __device__ __forceinline__ void add_outer(const Lane<COLS>& la, const Lane<64>& 
       mma16816(x[2 * jp], lo, y[jp][0], y[jp][1]);
       mma16816(x[2 * jp + 1], lo, y[jp][2], y[jp][3]);
     }
+    if (EXACT)
+#pragma unroll
+      for (int jp = 0; jp < NT / 2; ++jp) {
+        mma16816(x[2 * jp], last, y[jp][0], y[jp][1]);
+        mma16816(x[2 * jp + 1], last, y[jp][2], y[jp][3]);
+      }
   }
 }
 

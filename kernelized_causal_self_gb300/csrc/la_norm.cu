@@ -53,7 +53,8 @@ __device__ __forceinline__ float row_sum(float s) {
   return s;
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + __expf(-z)); }
+// (the division's approximation is off by 2 steps of 2^-23; exp's overflow gives 0)
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
 // LANES: threads per row, the power of two that holds M / V pieces.
 template <typename T, int LANES, bool BWD>
@@ -71,47 +72,61 @@ __global__ void __launch_bounds__(kThreads) norm_gate_kernel(const NormArgs a) {
 #pragma unroll
   for (int i = 0; i < V; ++i) dw.e[i] = 0.f;
   const float inv_m = 1.f / a.M;
-  for (unsigned r0 = begin; r0 < end; r0 += ROWS) {
-    const unsigned row = r0 + row0;
-    const bool in = live && row < end;
-    const long long b = row / (unsigned)a.N, t = row % (unsigned)a.N;
-    Piece<T> x, z, dy;
-    const size_t xo = (((size_t)b * a.H + h) * a.N + t) * a.M + c;
-    if (in) {
-      x.load(static_cast<const T*>(a.x) + xo);
-      z.load(static_cast<const T*>(a.z) + b * a.zs[0] + h * a.zs[1] + t * a.zs[2] + c);
-      if (BWD) dy.load(static_cast<const T*>(a.dy) + b * a.dys[0] + h * a.dys[1] + t * a.dys[2] + c);
-    } else {
+  // AT rows a thread at once: their loads are all asked for before the first is used
+  constexpr int AT = BWD ? 1 : 2;
+  for (unsigned r0 = begin; r0 < end; r0 += AT * ROWS) {
+    Piece<T> x[AT], z[AT], dy[AT];
+    size_t xo[AT];
+    long long b[AT], t[AT];
+    bool in[AT];
 #pragma unroll
-      for (int i = 0; i < V; ++i) x.e[i] = z.e[i] = dy.e[i] = 0.f;
-    }
-    float ss = 0.f;
+    for (int k = 0; k < AT; ++k) {
+      const unsigned row = r0 + k * ROWS + row0;
+      in[k] = live && row < end;
+      b[k] = row / (unsigned)a.N;
+      t[k] = row % (unsigned)a.N;
+      xo[k] = (((size_t)b[k] * a.H + h) * a.N + t[k]) * a.M + c;
+      if (in[k]) {
+        x[k].load(static_cast<const T*>(a.x) + xo[k]);
+        z[k].load(static_cast<const T*>(a.z) + b[k] * a.zs[0] + h * a.zs[1] + t[k] * a.zs[2] + c);
+        if (BWD)
+          dy[k].load(static_cast<const T*>(a.dy) + b[k] * a.dys[0] + h * a.dys[1] + t[k] * a.dys[2] + c);
+      } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) ss = fmaf(x.e[i], x.e[i], ss);
-    const float r = rsqrtf(fmaf(row_sum<LANES>(ss), inv_m, a.eps));
-    if (!BWD) {
-      Piece<T> y;
-#pragma unroll
-      for (int i = 0; i < V; ++i) y.e[i] = x.e[i] * r * w.e[i] * (z.e[i] * sigmoid(z.e[i]));
-      if (in) y.store(static_cast<T*>(a.y) + b * a.ys[0] + h * a.ys[1] + t * a.ys[2] + c);
-    } else {
-      float dot = 0.f;
-      Piece<T> dn, dz;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float s = sigmoid(z.e[i]), n = x.e[i] * r, gate = z.e[i] * s;
-        const float dyn = dy.e[i] * n;
-        dn.e[i] = dy.e[i] * w.e[i] * gate;
-        dz.e[i] = dyn * w.e[i] * (s * fmaf(z.e[i], 1.f - s, 1.f));
-        if (in) dw.e[i] = fmaf(dyn, gate, dw.e[i]);
-        dot = fmaf(dn.e[i], n, dot);
+        for (int i = 0; i < V; ++i) x[k].e[i] = z[k].e[i] = dy[k].e[i] = 0.f;
       }
-      const float mean = row_sum<LANES>(dot) * inv_m;
+    }
 #pragma unroll
-      for (int i = 0; i < V; ++i) dn.e[i] = r * fmaf(-x.e[i] * r, mean, dn.e[i]);
-      if (in) {
-        dn.store(static_cast<T*>(a.dx) + xo);
-        dz.store(static_cast<T*>(a.dz) + b * a.dzs[0] + h * a.dzs[1] + t * a.dzs[2] + c);
+    for (int k = 0; k < AT; ++k) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) ss = fmaf(x[k].e[i], x[k].e[i], ss);
+      const float r = rsqrtf(fmaf(row_sum<LANES>(ss), inv_m, a.eps));
+      if (!BWD) {
+        Piece<T> y;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          y.e[i] = x[k].e[i] * r * w.e[i] * (z[k].e[i] * sigmoid(z[k].e[i]));
+        if (in[k]) y.store(static_cast<T*>(a.y) + b[k] * a.ys[0] + h * a.ys[1] + t[k] * a.ys[2] + c);
+      } else {
+        float dot = 0.f;
+        Piece<T> dn, dz;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float zi = z[k].e[i], s = sigmoid(zi), n = x[k].e[i] * r, gate = zi * s;
+          const float dyn = dy[k].e[i] * n;
+          dn.e[i] = dy[k].e[i] * w.e[i] * gate;
+          dz.e[i] = dyn * w.e[i] * (s * fmaf(zi, 1.f - s, 1.f));
+          if (in[k]) dw.e[i] = fmaf(dyn, gate, dw.e[i]);
+          dot = fmaf(dn.e[i], n, dot);
+        }
+        const float mean = row_sum<LANES>(dot) * inv_m;
+#pragma unroll
+        for (int i = 0; i < V; ++i) dn.e[i] = r * fmaf(-x[k].e[i] * r, mean, dn.e[i]);
+        if (in[k]) {
+          dn.store(static_cast<T*>(a.dx) + xo[k]);
+          dz.store(static_cast<T*>(a.dz) + b[k] * a.dzs[0] + h * a.dzs[1] + t[k] * a.dzs[2] + c);
+        }
       }
     }
   }

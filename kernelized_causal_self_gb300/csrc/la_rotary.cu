@@ -61,6 +61,10 @@ template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
   constexpr int PAIRS = !INTER ? V : V > 1 ? V / 2 : 1;
   constexpr int W = INTER && V == 1 ? 2 : V;  // elements of one access of a turned item
+  // a CTA works its frequencies out once: float64 is slow here (two lanes a clock per SM)
+  __shared__ unsigned long long steps[64];
+  if (threadIdx.x < a.R / 2) steps[threadIdx.x] = turn_step(a.freqs[threadIdx.x]);
+  __syncthreads();
   const int turned = INTER ? a.R / W : a.R / (2 * V);
   const int items = turned + (a.D - a.R) / V;
   const long long gid = (long long)blockIdx.x * kThreads + threadIdx.x;
@@ -84,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
   float c[PAIRS], s[PAIRS];
 #pragma unroll
   for (int j = 0; j < PAIRS; ++j) {
-    turn(turn_step(a.freqs[item * PAIRS + j]), pos, a.mscale, c[j], s[j]);
+    turn(steps[item * PAIRS + j], pos, a.mscale, c[j], s[j]);
     if (a.inverse) s[j] = -s[j];
   }
   const int at = item * W;
