@@ -74,7 +74,10 @@ struct WalkSmem {
   static constexpr int kZ = OUT ? kC * DZ * 2 : 0, kW = kC * DZ * 2, kU = kC * 64 * 2;
   static constexpr int kStage = kZ + kW + kU;
   static constexpr int kX = OUT ? DZ * 64 * 2 : 0;  // X in bf16, one of two
-  static constexpr int kBytes = 2 * kStage + 2 * kX + 4 * kC * 4 * 3;
+  // the state pass has little to do on a chunk, so it asks for two ahead; the outputs'
+  // walk is longer on a chunk than a load takes
+  static constexpr int kStages = OUT ? 2 : 3;
+  static constexpr int kBytes = kStages * kStage + 2 * kX + 2 * (int)sizeof(GateTables);
 };
 
 // OUT: outputs (and, with one segment, the final state), else the state pass: the
@@ -90,11 +93,10 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
   using Sm = WalkSmem<DZ, OUT>;
   constexpr int KS = DZ / 16, DT = DZ / 64;
   extern __shared__ __align__(128) uint8_t smem[];
-  const uint32_t base = tc::smem_u32(smem), x_op = base + 2 * Sm::kStage;
+  const uint32_t base = tc::smem_u32(smem), x_op = base + Sm::kStages * Sm::kStage;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = lane >> 2, col = (lane & 3) * 2;  // of an accumulator
-  float* Gs = reinterpret_cast<float*>(smem + 2 * Sm::kStage + 2 * Sm::kX) + warp * 3 * kC;
-  float *Ws = Gs + kC, *Vs = Ws + kC;
+  GateTables* tables = reinterpret_cast<GateTables*>(smem + Sm::kStages * Sm::kStage + 2 * Sm::kX);
   const Lane<DZ> ln;
   const Lane<64> ln64;
 
@@ -144,7 +146,7 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
   };
   auto load_chunk = [&](int c) {
     const int t0 = tb + c * kC, rows = min(kC, te - t0);
-    const uint32_t at = base + (c & 1) * Sm::kStage;
+    const uint32_t at = base + (c % Sm::kStages) * Sm::kStage;
     if (OUT) load_tile<DZ, kThreads>(at, a.z + (seq + t0) * a.ZD, rows, a.ZD, 0);
     load_tile<DZ, kThreads>(at + Sm::kZ, a.w + (seq + t0) * a.ZD, rows, a.ZD, 0);
     load_tile<64, kThreads>(at + Sm::kZ + Sm::kW, a.u + (seq + t0) * a.UD, rows, a.UD, c0);
@@ -152,20 +154,21 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
   auto chunk_of = [&](int i) { return REV ? chunks - 1 - i : i; };
   auto raw_gates = [&](int c) { return load_gates(a.g + seq, tb + c * kC, te); };
 
-  ushort2 g_next = make_ushort2(0, 0);
-  float all = 0.f;  // sum of the segment's gates, base 2
-  if (chunks > 0) {
-    load_chunk(chunk_of(0));
-    g_next = raw_gates(chunk_of(0));
+  float all = 0.f;  // warp 0: sum of the segment's gates, base 2
+  constexpr int kAhead = Sm::kStages - 1;
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    if (i < chunks) load_chunk(chunk_of(i));
+    cp_async_commit();
   }
-  cp_async_commit();
+  if (chunks > 0 && warp == 0) all = chunk_gates<REV, EXACT>(raw_gates(chunk_of(0)), tables[0]);
   if (OUT) keep_op(0);
 
   for (int i = 0; i < chunks; ++i) {
     const int c = chunk_of(i);
-    cp_async_wait<0>();
+    cp_async_wait<kAhead - 1>();
     __syncthreads();  // chunk i has landed; every warp is done with chunk i - 1
-    const uint32_t z_at = base + (c & 1) * Sm::kStage, w_at = z_at + Sm::kZ, u_at = w_at + Sm::kW;
+    const uint32_t z_at = base + (c % Sm::kStages) * Sm::kStage, w_at = z_at + Sm::kZ, u_at = w_at + Sm::kW;
     const int r0 = rb * 16, t0 = tb + c * kC + r0;
     uint32_t f[OUT ? KS : 1][4];
     if (OUT) {
@@ -183,15 +186,15 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
       }
       cp_async_commit();
     }
-    const float2 g = gates_of(g_next);
-    if (i + 1 < chunks) {
-      load_chunk(chunk_of(i + 1));
-      g_next = raw_gates(chunk_of(i + 1));
-    }
+    if (i + kAhead < chunks) load_chunk(chunk_of(i + kAhead));
     cp_async_commit();
-    const float total = chunk_gates(g, Gs, Ws, REV ? Vs : nullptr);
-    const float dec = gated_decay(total * kLn2);
-    all += total;
+    // the next chunk's tables are made by one warp, from gates asked for here
+    const bool maker = warp == 0 && i + 1 < chunks;
+    ushort2 raw = make_ushort2(0, 0);
+    if (maker) raw = raw_gates(chunk_of(i + 1));
+    const GateTables& t = tables[i & 1];
+    const float* Gs = t.G;
+    const float dec = t.decay;
 
     if (OUT) {
       const size_t kept_at = ((((size_t)blockIdx.y * a.BH + bh) * ((a.N + kC - 1) / kC) + tb / kC + c) *
@@ -216,7 +219,7 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
       const float gr[2] = {Gs[r0 + row], Gs[r0 + row + 8]};
       product<true>(ln64, o, f, x_op + (i & 1) * Sm::kX);
       if (REV)
-        scale_rows(o, Ws[r0 + row], Ws[r0 + row + 8]);
+        scale_rows(o, t.W[r0 + row], t.W[r0 + row + 8]);
       else
         scale_rows(o, ex2(gr[0]), ex2(gr[1]));
       const size_t dots_at = ((size_t)blockIdx.y * a.BH + bh) * a.N + t0 + row;
@@ -262,7 +265,7 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
     for (int dt = 0; dt < DT; ++dt) {
       if (EXACT) {
         float y[8][4];
-        add_outer<true>(ln, ln64, y, w_at, REV ? Vs : Ws, 4 * dt + rb, u_at, 0);
+        add_outer<true>(ln, ln64, y, w_at, t.X, 4 * dt + rb, u_at, 0);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -270,10 +273,11 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
             pair_of(x[dt][j], h) = fma2(make_float2(dec, dec), pair_of(x[dt][j], h), pair_of(y[j], h));
       } else {
         scale_rows(x[dt], dec, dec);
-        add_outer<false>(ln, ln64, x[dt], w_at, REV ? Vs : Ws, 4 * dt + rb, u_at, 0);
+        add_outer<false>(ln, ln64, x[dt], w_at, t.X, 4 * dt + rb, u_at, 0);
       }
     }
     if (OUT && i + 1 < chunks) keep_op((i + 1) & 1);
+    if (maker) all += chunk_gates<REV, EXACT>(raw, tables[(i + 1) & 1]);
   }
 
   float* to = nullptr;

@@ -24,12 +24,19 @@ __device__ __forceinline__ float2 gates_of(ushort2 g) {
   return make_float2(a < -200.f ? -200.f : a, b < -200.f ? -200.f : b);
 }
 
-// From a lane's two gates, tables of the chunk (written by a warp for itself, or by one
-// for all): G[i], their sums up to and including token i; W[i] = 2^(sum of those behind i),
-// what is left of i's outer product in the state after the chunk; V[i] = 2^G[i] (nullptr:
-// not wanted). Returns the chunk's sum.
-__device__ __forceinline__ float chunk_gates(float2 g, float* G, float* W, float* V) {
+// From a lane's two gates, tables of the chunk (made by one warp for all):
+//   G[i]  the gates' sums up to and including token i
+//   W[i]  2^(sum of those behind i), what is left of i's outer product in the state after
+//         the chunk; and with REV V[i] = 2^G[i]. The one of the two that weights operands
+//         (V with REV, else W) is kept as split_pair's in X, or if EXACT as float32.
+//   decay of the whole chunk; its sum is returned
+struct GateTables {
+  float G[mma::kC], W[mma::kC], X[mma::kC], decay, pad[3];
+};
+template <bool REV, bool EXACT>
+__device__ __forceinline__ float chunk_gates(ushort2 raw, GateTables& t) {
   const int lane = threadIdx.x & 31;
+  const float2 g = gates_of(raw);
   const float both = g.x + g.y;
   float up = both, down = both;
 #pragma unroll
@@ -44,12 +51,17 @@ __device__ __forceinline__ float chunk_gates(float2 g, float* G, float* W, float
   if (lane == 0) before = 0.f;
   if (lane == 31) after = 0.f;
   const float2 incl = make_float2(before + g.x, up);
-  __syncwarp();
-  *reinterpret_cast<float2*>(G + 2 * lane) = incl;
-  *reinterpret_cast<float2*>(W + 2 * lane) = make_float2(mma::ex2(after + g.y), mma::ex2(after));
-  if (V) *reinterpret_cast<float2*>(V + 2 * lane) = make_float2(mma::ex2(incl.x), mma::ex2(incl.y));
-  __syncwarp();
-  return __shfl_sync(0xffffffffu, up, 31);
+  const float2 left = make_float2(mma::ex2(after + g.y), mma::ex2(after));
+  const float2 w = REV ? make_float2(mma::ex2(incl.x), mma::ex2(incl.y)) : left;
+  reinterpret_cast<float2*>(t.G)[lane] = incl;
+  reinterpret_cast<float2*>(t.W)[lane] = left;
+  if (EXACT)
+    reinterpret_cast<float2*>(t.X)[lane] = w;
+  else
+    reinterpret_cast<uint2*>(t.X)[lane] = mma::split_pair(w);
+  const float total = __shfl_sync(0xffffffffu, up, 31);
+  if (lane == 0) t.decay = gated_decay(total * kLn2);
+  return total;
 }
 
 // Tensor-core path: bf16 (la_gated_mma.cu, la_gated_mma_bwd.cu)

@@ -37,11 +37,10 @@ constexpr int kThreads = 128, kResident = 2, kMaxChunks = 14;
 constexpr int kTile = kC * 64 * 2;
 constexpr int kStage = 4 * kTile;  // Q, K, V, dO
 constexpr int kOp = kTile;         // S or E in bf16, [d][m], one of two
-// floats per parity of the chunk: the gates' tables G, W, V and exp(G), and the parts of dg:
-// sums of X's columns, b, <S, E> by warp
-constexpr int kTable = 3 * kC + 4, kParts = 2 * kC + 4;
+// floats per parity of the chunk: the parts of dg (sums of X's columns, b, <S, E> by warp)
+constexpr int kParts = 2 * kC + 4;
 // two stages of tiles, the operand's two, outputs on their way out
-constexpr int kSmem = 2 * kStage + 2 * kOp + kTile + 4 * 2 * (kTable + kParts);
+constexpr int kSmem = 2 * kStage + 2 * kOp + kTile + 2 * ((int)sizeof(GateTables) + 4 * kParts);
 static_assert(kResident * (kSmem + 1024) <= 228 * 1024, "CTAs per SM");
 // scratch of a CTA: S of each chunk as the warps hold it, and q . dQ of each token
 constexpr int kScratchS = kMaxChunks * 8 * kThreads * (int)sizeof(float4);
@@ -84,8 +83,8 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
   const Lane<64> ln;
   uint8_t* op_mem = smem + 2 * kStage;
   const uint32_t op_base = base + 2 * kStage, out_at = op_base + 2 * kOp;
-  float* tables = reinterpret_cast<float*>(op_mem + 2 * kOp + kTile);
-  float* parts = tables + 2 * kTable;
+  GateTables* tables = reinterpret_cast<GateTables*>(op_mem + 2 * kOp + kTile);
+  float* parts = reinterpret_cast<float*>(tables + 2);
   char* own = a.scratch + (size_t)blockIdx.x * kScratch;
   float4* states = reinterpret_cast<float4*>(own) + tid;  // [chunk][8][thread]
   float* alpha = reinterpret_cast<float*>(own + kScratchS);        // [chunk][64]: q . dQ
@@ -106,18 +105,14 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       load_tile<64, kThreads>(at + 2 * kTile, a.v + (seq + t0) * a.M, rows, a.M, 0);
       load_tile<64, kThreads>(at + 3 * kTile, a.dout + (seq + t0) * a.M, rows, a.M, 0);
     };
-    // A chunk's tables are made by one warp while the chunk before it is worked on
+    // A chunk's tables are made by one warp while the chunk before it is worked on. Going
+    // forward K is weighted (W), going back Q (V).
     auto raw_gates = [&](int c) { return load_gates(a.g + seq, tb + c * kC, te); };
-    auto make_tables = [&](int c, ushort2 raw) {
-      float* G = tables + (c & 1) * kTable;
-      const float total = chunk_gates(gates_of(raw), G, G + kC, G + 2 * kC);
-      if (lane == 0) G[3 * kC] = gated_decay(total * kLn2);
-    };
 
     __syncthreads();  // the item before is done with
     load_chunk(0);
     cp_async_commit();
-    if (warp == 0) make_tables(0, raw_gates(0));
+    if (warp == 0) chunk_gates<false, false>(raw_gates(0), tables[0]);
 
     // ---- forward: dQ
     float x[8][4];  // S, then E
@@ -129,7 +124,8 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       __syncthreads();
       if (c + 1 < chunks) load_chunk(c + 1);
       cp_async_commit();
-      const float *Gs = tables + (c & 1) * kTable, *Ws = Gs + kC;
+      const GateTables& t = tables[c & 1];
+      const float* Gs = t.G;
       const uint32_t q_at = base + (c & 1) * kStage, k_at = q_at + kTile, v_at = k_at + kTile,
                      do_at = v_at + kTile;
       const bool maker = c + 1 < chunks && warp == (c & 3);
@@ -159,19 +155,19 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       const int t0 = tb + c * kC + r0;
       store_rows(ln, out_at, r0, d, a.dq + (seq + t0) * a.D, te - t0, a.D, a.D);
       if (c + 1 < chunks) {
-        const float dec = Gs[3 * kC];
-        scale_rows(x, dec, dec);
-        add_outer<false>(ln, ln, x, k_at, Ws, rb, v_at, 0);
+        scale_rows(x, t.decay, t.decay);
+        add_outer<false>(ln, ln, x, k_at, t.X, rb, v_at, 0);
         store_op(ln, op_base + ((c + 1) & 1) * kOp, r0, 0, x);
       }
-      if (maker) make_tables(c + 1, raw);
+      if (maker) chunk_gates<false, false>(raw, tables[(c + 1) & 1]);
     }
 
-    // ---- back: dV, dK, dg. The last two chunks' tiles and tables are still there.
+    // ---- back: dV, dK, dg. The last two chunks' tiles are still there.
     load_state(x, a.E ? a.E + ((size_t)bh * (a.n_seg + 1) + seg + 1) * DM : a.dS ? a.dS + bh * DM : nullptr,
                r0, 0, a.D, a.M);
     __syncthreads();
     store_op(ln, op_base, r0, 0, x);
+    if (warp == 0) chunk_gates<true, false>(raw_gates(chunks - 1), tables[(chunks - 1) & 1]);
     // dg of chunk c from the parts its warps left (one warp)
     auto finish = [&](int c) {
       const float* at = parts + (c & 1) * kParts;
@@ -202,18 +198,19 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       if (c > 0 && c + 1 < chunks) load_chunk(c - 1);
       cp_async_commit();
       const int step = chunks - 1 - c;
-      const float *Gs = tables + (c & 1) * kTable, *Ws = Gs + kC, *Vs = Ws + kC;
+      const GateTables& t = tables[c & 1];
+      const float* Gs = t.G;
       float* part = parts + (c & 1) * kParts;
       const uint32_t q_at = base + (c & 1) * kStage, k_at = q_at + kTile, v_at = k_at + kTile,
                      do_at = v_at + kTile, op = op_base + (step & 1) * kOp;
-      const bool maker = c > 0 && c + 1 < chunks && warp == (c & 3);
+      const bool maker = c > 0 && warp == (c & 3);
       ushort2 raw = make_ushort2(0, 0);
       if (maker) raw = raw_gates(c - 1);
       float4 sc[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) sc[j] = states[(c * 8 + j) * kThreads];
       if (c + 1 < chunks && warp == ((c + 1) & 3)) finish(c + 1);
-      const float dec = Gs[3 * kC], w0 = Ws[r0 + row], w1 = Ws[r0 + row + 8];
+      const float dec = t.decay, w0 = t.W[r0 + row], w1 = t.W[r0 + row + 8];
       const float gj[2] = {Gs[r0 + row], Gs[r0 + row + 8]};
       const int t0 = tb + c * kC + r0;
       uint32_t f[4][4], p[4];
@@ -261,10 +258,10 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       store_rows(ln, out_at, r0, d, a.dk + (seq + t0) * a.D, te - t0, a.D, a.D);
       if (c > 0) {
         scale_rows(x, dec, dec);
-        add_outer<false>(ln, ln, x, q_at, Vs, rb, do_at, 0);
+        add_outer<false>(ln, ln, x, q_at, t.X, rb, do_at, 0);
         store_op(ln, op_base + ((step + 1) & 1) * kOp, r0, 0, x);
       }
-      if (maker) make_tables(c - 1, raw);
+      if (maker) chunk_gates<true, false>(raw, tables[(c - 1) & 1]);
     }
     __syncthreads();
     if (warp == 0) finish(0);

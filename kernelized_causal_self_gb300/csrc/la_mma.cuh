@@ -141,14 +141,35 @@ __device__ __forceinline__ void scale_rows(float (&c)[NT][4], float top, float b
   }
 }
 
-// bf16 pair u times w, as the sum of two bf16 pairs: the product to 16 bits. Returns what
-// the first leaves.
-__device__ __forceinline__ float2 scale_split(uint32_t u, float2 w, uint32_t& hi, uint32_t& lo) {
+// A pair of float32 weights as two bf16 pairs, whose sum has 16 bits of it
+__device__ __forceinline__ uint2 split_pair(float2 w) {
+  const uint32_t hi = pack2(w.x, w.y);
+  const float2 r = sub2(w, both_of(hi));
+  return make_uint2(hi, pack2(r.x, r.y));
+}
+
+__device__ __forceinline__ uint32_t fma_bf2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
+// bf16 pair u times such weights as the sum of two bf16 pairs, 16 bits of the product:
+// hi = u w.x, whose remainder has at most eight bits and is exact, plus u w.y.
+__device__ __forceinline__ void scale_split(uint32_t u, uint2 w, uint32_t& hi, uint32_t& lo) {
+  hi = fma_bf2(u, w.x, 0x80008000u);  // (-0: a product of -0 stays one)
+  lo = fma_bf2(u, w.y, fma_bf2(u, w.x, hi ^ 0x80008000u));
+}
+
+// bf16 pair u times float32 weights as the sum of three bf16 pairs, 24 bits of the product
+__device__ __forceinline__ void scale_split3(uint32_t u, float2 w, uint32_t& hi, uint32_t& mid,
+                                             uint32_t& lo) {
   const float2 p = mul2(both_of(u), w);
   hi = pack2(p.x, p.y);
-  const float2 r = sub2(p, both_of(hi));
+  float2 r = sub2(p, both_of(hi));
+  mid = pack2(r.x, r.y);
+  r = sub2(r, both_of(mid));
   lo = pack2(r.x, r.y);
-  return r;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -188,6 +209,12 @@ __device__ __forceinline__ void load_tile(uint32_t base, const bf16* src, int ro
   const uint32_t to = base + row * COLS * 2 + ((chunk ^ (row & 7)) << 4);
   const bf16* from = src + (size_t)row * width + c0 + chunk * 8;
   const bool wide = c0 + chunk * 8 < width;
+  if (rows >= kC && c0 + COLS <= width) {  // (uniform: every chunk but a sequence's last)
+#pragma unroll
+    for (int i = 0; i < kC / STEP; ++i)
+      cp_async16(to + i * STEP * COLS * 2, from + (uint32_t)(i * STEP * width), true);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < kC / STEP; ++i) {
     const bool live = wide && row + i * STEP < rows;
@@ -261,27 +288,27 @@ __device__ __forceinline__ void store_op(const Lane<64>& ln, uint32_t op, int r0
   for (int jp = 0; jp < NT / 2; ++jp) ln.store(op, r0, c0 / 16 + jp, x[2 * jp], x[2 * jp + 1]);
 }
 
-// x += (columns 16 col16.. of tile `a`, weighted by `w` along its rows)^T (columns c0.. of
-// tile `b`), over 64 rows. EXACT: from zero, and the weighted columns to 24 bits.
+// x += (columns 16 col16.. of tile `a`, weighted along its rows)^T (columns c0.. of tile
+// `b`), over 64 rows. The weights: a table of split_pair's of neighbouring rows; EXACT: of
+// float32 pairs, and x is begun from zero.
 template <bool EXACT, int COLS, int NT>
 __device__ __forceinline__ void add_outer(const Lane<COLS>& la, const Lane<64>& lb, float (&x)[NT][4],
-                                          uint32_t a, const float* w, int col16, uint32_t b, int c0) {
-  const int col = (threadIdx.x & 3) * 2;
+                                          uint32_t a, const float* weights, int col16, uint32_t b, int c0) {
+  const uint2* w = reinterpret_cast<const uint2*>(weights) + (threadIdx.x & 3);
 #pragma unroll
   for (int at = 0; at < kC; at += 16) {
     uint32_t f[4], hi[4], lo[4], last[4], y[NT / 2][4];
     la.load_a_t(f, a, at, col16);
 #pragma unroll
     for (int jp = 0; jp < NT / 2; ++jp) lb.load_b_t(y[jp], b, at, c0 / 16 + jp);
-    const float2 w0 = *reinterpret_cast<const float2*>(w + at + col);
-    const float2 w8 = *reinterpret_cast<const float2*>(w + at + 8 + col);
+    const uint2 w0 = w[at / 2], w8 = w[at / 2 + 4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 r = scale_split(f[e], e < 2 ? w0 : w8, hi[e], lo[e]);
-      if (EXACT) {
-        const float2 rest = sub2(r, both_of(lo[e]));
-        last[e] = pack2(rest.x, rest.y);
-      }
+      const uint2 v = e < 2 ? w0 : w8;
+      if (EXACT)
+        scale_split3(f[e], make_float2(__uint_as_float(v.x), __uint_as_float(v.y)), hi[e], lo[e], last[e]);
+      else
+        scale_split(f[e], v, hi[e], lo[e]);
     }
 #pragma unroll
     for (int jp = 0; jp < NT / 2; ++jp) {
