@@ -115,6 +115,28 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
   const size_t entry_size = (size_t)a.ZD * a.UD;
 
   float x[DT][8][4];
+  auto keep_op = [&](int buf) {
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) store_op(ln64, x_op + buf * Sm::kX, dt * 64 + rb * 16, 0, x[dt]);
+  };
+  auto load_chunk = [&](int c) {
+    const int t0 = tb + c * kC, rows = min(kC, te - t0);
+    const uint32_t at = base + (c % Sm::kStages) * Sm::kStage;
+    if (OUT) load_tile<DZ, kThreads>(at, a.z + (seq + t0) * a.ZD, rows, a.ZD, 0);
+    load_tile<DZ, kThreads>(at + Sm::kZ, a.w + (seq + t0) * a.ZD, rows, a.ZD, 0);
+    load_tile<64, kThreads>(at + Sm::kZ + Sm::kW, a.u + (seq + t0) * a.UD, rows, a.UD, c0);
+  };
+  auto chunk_of = [&](int i) { return REV ? chunks - 1 - i : i; };
+  auto raw_gates = [&](int c) { return load_gates(a.g + seq, tb + c * kC, te); };
+
+  float all = 0.f;  // warp 0: sum of the segment's gates, base 2
+  constexpr int kAhead = Sm::kStages - 1;
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    if (i < chunks) load_chunk(chunk_of(i));
+    cp_async_commit();
+  }
+  if (chunks > 0 && warp == 0) all = chunk_gates<REV, EXACT>(raw_gates(chunk_of(0)), tables[0]);
   {
     const float* in = nullptr;
     if (OUT && a.seg_in)
@@ -140,28 +162,6 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
           x[dt][j][2 * h + 1] = v.y;
         }
   }
-  auto keep_op = [&](int buf) {
-#pragma unroll
-    for (int dt = 0; dt < DT; ++dt) store_op(ln64, x_op + buf * Sm::kX, dt * 64 + rb * 16, 0, x[dt]);
-  };
-  auto load_chunk = [&](int c) {
-    const int t0 = tb + c * kC, rows = min(kC, te - t0);
-    const uint32_t at = base + (c % Sm::kStages) * Sm::kStage;
-    if (OUT) load_tile<DZ, kThreads>(at, a.z + (seq + t0) * a.ZD, rows, a.ZD, 0);
-    load_tile<DZ, kThreads>(at + Sm::kZ, a.w + (seq + t0) * a.ZD, rows, a.ZD, 0);
-    load_tile<64, kThreads>(at + Sm::kZ + Sm::kW, a.u + (seq + t0) * a.UD, rows, a.UD, c0);
-  };
-  auto chunk_of = [&](int i) { return REV ? chunks - 1 - i : i; };
-  auto raw_gates = [&](int c) { return load_gates(a.g + seq, tb + c * kC, te); };
-
-  float all = 0.f;  // warp 0: sum of the segment's gates, base 2
-  constexpr int kAhead = Sm::kStages - 1;
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) {
-    if (i < chunks) load_chunk(chunk_of(i));
-    cp_async_commit();
-  }
-  if (chunks > 0 && warp == 0) all = chunk_gates<REV, EXACT>(raw_gates(chunk_of(0)), tables[0]);
   if (OUT) keep_op(0);
 
   for (int i = 0; i < chunks; ++i) {
@@ -322,37 +322,28 @@ __global__ void __launch_bounds__(kThreads, DZ == 64 ? 3 : 2) gated_gradient_ker
   walk_chunks<DZ, true, REV, false, DOTS>(a);
 }
 
-template <typename K, typename... Args>
-cudaError_t launch(K kernel, int smem, dim3 grid, cudaStream_t st, Args... args) {
-  cudaError_t e = tcx::configure(kernel, smem);
-  if (e != cudaSuccess) return e;
-  e = tcx::launch_pdl(kernel, grid, dim3(kThreads), smem, st, args...);
-  count_launches(1);
-  return e;
-}
-
 dim3 walk_grid(const WalkArgs& a, int z = 1) {
   return dim3((unsigned)(a.BH * a.n_seg), (unsigned)((a.UD + 63) / 64), (unsigned)z);
 }
 
 template <bool EXACT>
 cudaError_t launch_forward(const WalkArgs& a, cudaStream_t st) {
-  return a.ZD <= 64 ? launch(gated_forward_kernel<64, EXACT>, WalkSmem<64, true>::kBytes, walk_grid(a), st, a)
-                    : launch(gated_forward_kernel<128, EXACT>, WalkSmem<128, true>::kBytes, walk_grid(a), st, a);
+  return a.ZD <= 64 ? gated_launch<gated_forward_kernel<64, EXACT>>(WalkSmem<64, true>::kBytes, walk_grid(a), kThreads, st, a)
+                    : gated_launch<gated_forward_kernel<128, EXACT>>(WalkSmem<128, true>::kBytes, walk_grid(a), kThreads, st, a);
 }
 
 template <bool EXACT>
 cudaError_t launch_states(const WalkArgs& a, const WalkArgs& back, int jobs, cudaStream_t st) {
   return a.ZD <= 64
-             ? launch(gated_states_kernel<64, EXACT>, WalkSmem<64, false>::kBytes, walk_grid(a, jobs), st, a, back)
-             : launch(gated_states_kernel<128, EXACT>, WalkSmem<128, false>::kBytes, walk_grid(a, jobs), st, a, back);
+             ? gated_launch<gated_states_kernel<64, EXACT>>(WalkSmem<64, false>::kBytes, walk_grid(a, jobs), kThreads, st, a, back)
+             : gated_launch<gated_states_kernel<128, EXACT>>(WalkSmem<128, false>::kBytes, walk_grid(a, jobs), kThreads, st, a, back);
 }
 
 template <bool REV, bool DOTS>
 cudaError_t launch_gradient(const WalkArgs& a, cudaStream_t st) {
   return a.ZD <= 64
-             ? launch(gated_gradient_kernel<64, REV, DOTS>, WalkSmem<64, true>::kBytes, walk_grid(a), st, a)
-             : launch(gated_gradient_kernel<128, REV, DOTS>, WalkSmem<128, true>::kBytes, walk_grid(a), st, a);
+             ? gated_launch<gated_gradient_kernel<64, REV, DOTS>>(WalkSmem<64, true>::kBytes, walk_grid(a), kThreads, st, a)
+             : gated_launch<gated_gradient_kernel<128, REV, DOTS>>(WalkSmem<128, true>::kBytes, walk_grid(a), kThreads, st, a);
 }
 
 // dg of a chunk from its dots (see la_gated_mma_bwd.cu): a warp each, two tokens a lane.

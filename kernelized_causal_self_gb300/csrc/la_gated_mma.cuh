@@ -1,8 +1,11 @@
 // The gates of a 64-token chunk, as the tensor-core kernels use them.
 #pragma once
 
+#include <atomic>
+
 #include "la_gated.cuh"
 #include "la_mma.cuh"
+#include "la_tc_common.cuh"
 
 namespace la {
 
@@ -62,6 +65,30 @@ __device__ __forceinline__ float chunk_gates(ushort2 raw, GateTables& t) {
   const float total = __shfl_sync(0xffffffffu, up, 31);
   if (lane == 0) t.decay = gated_decay(total * kLn2);
   return total;
+}
+
+// tcx::configure, once per kernel and device (its two calls of the runtime cost as much as a
+// launch). The mask is the library's own state, as its launch count is.
+template <auto KERNEL>
+cudaError_t gated_configure(int smem) {
+  static std::atomic<unsigned long long> done{0};
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = device < 64 ? 1ull << device : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = tcx::configure(KERNEL, smem);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+template <auto KERNEL, typename... Args>
+cudaError_t gated_launch(int smem, dim3 grid, int threads, cudaStream_t st, const Args&... args) {
+  cudaError_t e = gated_configure<KERNEL>(smem);
+  if (e != cudaSuccess) return e;
+  e = tcx::launch_pdl(KERNEL, grid, dim3(threads), smem, st, args...);
+  count_launches(1);
+  return e;
 }
 
 // Tensor-core path: bf16 (la_gated_mma.cu, la_gated_mma_bwd.cu)

@@ -327,11 +327,7 @@ cudaError_t gated_mma_backward(const GatedBackward& f, const GatedPlan& p, const
   a.S0 = f.S0;
   a.dS = f.dS;
   a.scratch = static_cast<char*>(w.scratch);
-  if ((e = tcx::configure(gated_backward_kernel, kSmem)) != cudaSuccess) return e;
-  e = tcx::launch_pdl(gated_backward_kernel, dim3((unsigned)backward_grid(p)), dim3(kThreads), kSmem,
-                      st, a);
-  count_launches(1);
-  return e;
+  return gated_launch<gated_backward_kernel>(kSmem, dim3((unsigned)backward_grid(p)), kThreads, st, a);
 }
 
 }  // namespace la
