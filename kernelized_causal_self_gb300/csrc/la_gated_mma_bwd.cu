@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
 #pragma unroll
       for (int j = 0; j < 8; ++j) sc[j] = states[(c * 8 + j) * kThreads];
       if (c + 1 < chunks && warp == ((c + 1) & 3)) finish(c + 1);
-      const float dec = t.decay, w0 = t.W[r0 + row], w1 = t.W[r0 + row + 8];
+      const float dec = t.decay;
       const float gj[2] = {Gs[r0 + row], Gs[r0 + row + 8]};
       const int t0 = tb + c * kC + r0;
       uint32_t f[4][4], p[4];
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) ln.load_a(f[ks], k_at, r0, ks);
       product<true>(ln, d, f, op);
-      scale_rows(d, w0, w1);
+      scale_rows(d, t.W[r0 + row], t.W[r0 + row + 8]);
       masked_block<false, true>(ln, p, f, q_at, rb, gj, Gs);
       add_block(ln, d, p, do_at, rb);
 #pragma unroll 1
@@ -236,26 +236,31 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
         for (int o = 1; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (lane == 0) part[2 * kC + warp] = s * dec;
       }
+      // dK by the rows from the other end: the two causal halves add up to the same for
+      // every warp
+      const int kb = 3 - rb, k0 = kb * 16, tk = tb + c * kC + k0;
+      const float gk[2] = {Gs[k0 + row], Gs[k0 + row + 8]};
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) ln.load_a(f[ks], v_at, r0, ks);
+      for (int ks = 0; ks < 4; ++ks) ln.load_a(f[ks], v_at, k0, ks);
       product<false>(ln, d, f, op);
-      scale_rows(d, w0, w1);
-      const float2 be = row_dots(ln, k_at, r0, d);
-      masked_block<false, true>(ln, p, f, do_at, rb, gj, Gs);
-      add_block(ln, d, p, q_at, rb);
+      scale_rows(d, t.W[k0 + row], t.W[k0 + row + 8]);
+      const float2 be = row_dots(ln, k_at, k0, d);
+      masked_block<false, true>(ln, p, f, do_at, kb, gk, Gs);
+      add_block(ln, d, p, q_at, kb);
 #pragma unroll 1
-      for (int ib = rb + 1; ib < 4; ++ib) {
-        masked_block<false, false>(ln, p, f, do_at, ib, gj, Gs);
+      for (int ib = kb + 1; ib < 4; ++ib) {
+        masked_block<false, false>(ln, p, f, do_at, ib, gk, Gs);
         add_block(ln, d, p, q_at, ib);
       }
-      const float2 all = row_dots(ln, k_at, r0, d);
+      const float2 all = row_dots(ln, k_at, k0, d);
       if ((lane & 3) == 0) {
-        part[r0 + row] = all.x - be.x;
-        part[r0 + row + 8] = all.y - be.y;
-        part[kC + r0 + row] = be.x;
-        part[kC + r0 + row + 8] = be.y;
+        part[k0 + row] = all.x - be.x;
+        part[k0 + row + 8] = all.y - be.y;
+        part[kC + k0 + row] = be.x;
+        part[kC + k0 + row + 8] = be.y;
       }
-      store_rows(ln, out_at, r0, d, a.dk + (seq + t0) * a.D, te - t0, a.D, a.D);
+      // (through V's rows, which no other warp reads)
+      store_rows(ln, v_at, k0, d, a.dk + (seq + tk) * a.D, te - tk, a.D, a.D);
       if (c > 0) {
         scale_rows(x, dec, dec);
         add_outer<false>(ln, ln, x, q_at, t.X, rb, do_at, 0);
