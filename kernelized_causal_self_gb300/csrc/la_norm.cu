@@ -27,12 +27,12 @@ struct NormArgs {
   float eps;
 };
 
+// 16 bytes of a row as float32
 template <typename T>
 struct Piece {
   static constexpr int V = 16 / sizeof(T);
   float e[V];
-  __device__ void load(const T* p) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
+  __device__ void set(const uint4& u) {
     const T* t = reinterpret_cast<const T*>(&u);
 #pragma unroll
     for (int i = 0; i < V; ++i) e[i] = to_f32<T>(t[i]);
@@ -42,7 +42,25 @@ struct Piece {
     T* t = reinterpret_cast<T*>(&u);
 #pragma unroll
     for (int i = 0; i < V; ++i) t[i] = from_f32<T>(e[i]);
-    *reinterpret_cast<uint4*>(p) = u;
+    __stcs(reinterpret_cast<uint4*>(p), u);
+  }
+};
+
+// A thread's piece of the rows (b, h, t) of one head that it visits, `step` rows of t
+// apart: the address moves by additions (divisions only where t passes N).
+template <typename T>
+struct Rows {
+  T* p;
+  long long move, wrap;  // per step; from the end of a batch entry to the next
+  __device__ void start(const void* base, long long b, long long t, long long sb, long long st,
+                        long long at, int N, int step) {
+    p = const_cast<T*>(static_cast<const T*>(base)) + b * sb + t * st + at;
+    move = st * step;
+    wrap = sb - N * st;
+  }
+  __device__ void next(unsigned wraps) {
+    p += move;
+    if (wraps) p += wraps * wrap;
   }
 };
 
@@ -53,82 +71,103 @@ __device__ __forceinline__ float row_sum(float s) {
   return s;
 }
 
-// (the division's approximation is off by 2 steps of 2^-23; exp's overflow gives 0)
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// 1 / (1 + exp(-z)), its parts (the approximations are off by 2 steps of 2^-23 each; past
+// exp's range the quotient is 0, or 1)
+__device__ __forceinline__ float one_plus_exp(float z) { return 1.f + __expf(-z); }
 
-// LANES: threads per row, the power of two that holds M / V pieces.
+// LANES: threads per row, the power of two that holds M / V pieces. A row's loads are
+// asked for while the row before it is worked on.
 template <typename T, int LANES, bool BWD>
 __global__ void __launch_bounds__(kThreads) norm_gate_kernel(const NormArgs a) {
   constexpr int V = Piece<T>::V, ROWS = kThreads / LANES;
   const int lane = threadIdx.x % LANES, row0 = threadIdx.x / LANES;
-  const int h = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
+  // heads in neighbouring CTAs: a token-major tensor's rows of one token then move together
+  const int h = blockIdx.x % a.H, tile = blockIdx.x / a.H;
   const bool live = lane * V < a.M;
-  const unsigned n_rows = (unsigned)a.B * (unsigned)a.N;
+  const unsigned n_rows = (unsigned)a.B * (unsigned)a.N, N = a.N;
   const unsigned begin = (unsigned)tile * (unsigned)a.rows_per_tile;
   const unsigned end = min(begin + (unsigned)a.rows_per_tile, n_rows);
   const int c = live ? lane * V : 0;
   Piece<T> w, dw;
-  w.load(static_cast<const T*>(a.w) + (size_t)h * a.w_stride + c);
+  w.set(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.w) + (size_t)h * a.w_stride + c));
 #pragma unroll
   for (int i = 0; i < V; ++i) dw.e[i] = 0.f;
   const float inv_m = 1.f / a.M;
-  // AT rows a thread at once: their loads are all asked for before the first is used
-  constexpr int AT = BWD ? 1 : 2;
-  for (unsigned r0 = begin; r0 < end; r0 += AT * ROWS) {
-    Piece<T> x[AT], z[AT], dy[AT];
-    size_t xo[AT];
-    long long b[AT], t[AT];
-    bool in[AT];
-#pragma unroll
-    for (int k = 0; k < AT; ++k) {
-      const unsigned row = r0 + k * ROWS + row0;
-      in[k] = live && row < end;
-      b[k] = row / (unsigned)a.N;
-      t[k] = row % (unsigned)a.N;
-      xo[k] = (((size_t)b[k] * a.H + h) * a.N + t[k]) * a.M + c;
-      if (in[k]) {
-        x[k].load(static_cast<const T*>(a.x) + xo[k]);
-        z[k].load(static_cast<const T*>(a.z) + b[k] * a.zs[0] + h * a.zs[1] + t[k] * a.zs[2] + c);
-        if (BWD)
-          dy[k].load(static_cast<const T*>(a.dy) + b[k] * a.dys[0] + h * a.dys[1] + t[k] * a.dys[2] + c);
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[k].e[i] = z[k].e[i] = dy[k].e[i] = 0.f;
-      }
+
+  unsigned row = begin + row0;
+  const long long b0 = row / N;
+  unsigned t = row % N;  // of the row that is asked for next
+  const long long sb = (long long)a.H * a.N * a.M;
+  Rows<T> xr, zr, dyr, out, dzr;
+  xr.start(a.x, b0, t, sb, a.M, (long long)h * a.N * a.M + c, N, ROWS);
+  zr.start(a.z, b0, t, a.zs[0], a.zs[2], h * a.zs[1] + c, N, ROWS);
+  if (BWD) {
+    dyr.start(a.dy, b0, t, a.dys[0], a.dys[2], h * a.dys[1] + c, N, ROWS);
+    out.start(a.dx, b0, t, sb, a.M, (long long)h * a.N * a.M + c, N, ROWS);
+    dzr.start(a.dz, b0, t, a.dzs[0], a.dzs[2], h * a.dzs[1] + c, N, ROWS);
+  } else {
+    out.start(a.y, b0, t, a.ys[0], a.ys[2], h * a.ys[1] + c, N, ROWS);
+  }
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  uint4 nx = none, nz = none, ndy = none;
+  auto ask = [&]() {
+    const bool in = live && row < end;
+    nx = in ? __ldcs(reinterpret_cast<const uint4*>(xr.p)) : none;
+    nz = in ? __ldcs(reinterpret_cast<const uint4*>(zr.p)) : none;
+    if (BWD) ndy = in ? __ldcs(reinterpret_cast<const uint4*>(dyr.p)) : none;
+  };
+  ask();
+  for (unsigned r0 = begin; r0 < end; r0 += ROWS) {
+    const bool in = live && row < end;
+    Piece<T> x, z, dy;
+    x.set(nx);
+    z.set(nz);
+    if (BWD) dy.set(ndy);
+    // on to the next row
+    row += ROWS;
+    t += ROWS;
+    unsigned wraps = 0;
+    if (t >= N) {
+      wraps = t / N;
+      t -= wraps * N;
     }
+    xr.next(wraps);
+    zr.next(wraps);
+    if (BWD) dyr.next(wraps);
+    ask();
+
+    float ss = 0.f;
 #pragma unroll
-    for (int k = 0; k < AT; ++k) {
-      float ss = 0.f;
+    for (int i = 0; i < V; ++i) ss = fmaf(x.e[i], x.e[i], ss);
+    const float r = rsqrtf(fmaf(row_sum<LANES>(ss), inv_m, a.eps));
+    if (!BWD) {
+      Piece<T> y;
 #pragma unroll
-      for (int i = 0; i < V; ++i) ss = fmaf(x[k].e[i], x[k].e[i], ss);
-      const float r = rsqrtf(fmaf(row_sum<LANES>(ss), inv_m, a.eps));
-      if (!BWD) {
-        Piece<T> y;
+      for (int i = 0; i < V; ++i)
+        y.e[i] = x.e[i] * r * w.e[i] * __fdividef(z.e[i], one_plus_exp(z.e[i]));
+      if (in) y.store(out.p);
+    } else {
+      float dot = 0.f;
+      Piece<T> dn, dz;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          y.e[i] = x[k].e[i] * r * w.e[i] * (z[k].e[i] * sigmoid(z[k].e[i]));
-        if (in[k]) y.store(static_cast<T*>(a.y) + b[k] * a.ys[0] + h * a.ys[1] + t[k] * a.ys[2] + c);
-      } else {
-        float dot = 0.f;
-        Piece<T> dn, dz;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float zi = z[k].e[i], s = sigmoid(zi), n = x[k].e[i] * r, gate = zi * s;
-          const float dyn = dy[k].e[i] * n;
-          dn.e[i] = dy[k].e[i] * w.e[i] * gate;
-          dz.e[i] = dyn * w.e[i] * (s * fmaf(zi, 1.f - s, 1.f));
-          if (in[k]) dw.e[i] = fmaf(dyn, gate, dw.e[i]);
-          dot = fmaf(dn.e[i], n, dot);
-        }
-        const float mean = row_sum<LANES>(dot) * inv_m;
-#pragma unroll
-        for (int i = 0; i < V; ++i) dn.e[i] = r * fmaf(-x[k].e[i] * r, mean, dn.e[i]);
-        if (in[k]) {
-          dn.store(static_cast<T*>(a.dx) + xo[k]);
-          dz.store(static_cast<T*>(a.dz) + b[k] * a.dzs[0] + h * a.dzs[1] + t[k] * a.dzs[2] + c);
-        }
+      for (int i = 0; i < V; ++i) {
+        const float zi = z.e[i], s = __fdividef(1.f, one_plus_exp(zi)), n = x.e[i] * r, gate = zi * s;
+        const float dyn = dy.e[i] * n;
+        dn.e[i] = dy.e[i] * w.e[i] * gate;
+        dz.e[i] = dyn * w.e[i] * (s * fmaf(zi, 1.f - s, 1.f));
+        if (in) dw.e[i] = fmaf(dyn, gate, dw.e[i]);
+        dot = fmaf(dn.e[i], n, dot);
       }
+      const float mean = row_sum<LANES>(dot) * inv_m;
+#pragma unroll
+      for (int i = 0; i < V; ++i) dn.e[i] = r * fmaf(-x.e[i] * r, mean, dn.e[i]);
+      if (in) {
+        dn.store(out.p);
+        dz.store(dzr.p);
+      }
+      dzr.next(wraps);
     }
+    out.next(wraps);
   }
   if (BWD) {
     __shared__ float sums[ROWS][LANES * V + 1];
@@ -138,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) norm_gate_kernel(const NormArgs a) {
     for (int m = threadIdx.x; m < a.M; m += kThreads) {
       float s = 0.f;
       for (int i = 0; i < ROWS; ++i) s += sums[i][m];
-      a.partial[(size_t)blockIdx.x * a.M + m] = s;
+      a.partial[((size_t)h * a.tiles + tile) * a.M + m] = s;
     }
   }
 }
