@@ -54,6 +54,23 @@ struct alignas(sizeof(T) * V) Vec {
   T e[V];
 };
 
+// V elements, read or written once: 16 bytes at a time are marked to leave the cache first
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> read(const T* p) {
+  if constexpr (sizeof(T) * V == 16) {
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+    return *reinterpret_cast<const Vec<T, V>*>(&u);
+  }
+  return *reinterpret_cast<const Vec<T, V>*>(p);
+}
+template <typename T, int V>
+__device__ __forceinline__ void write(T* p, const Vec<T, V>& v) {
+  if constexpr (sizeof(T) * V == 16)
+    __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&v));
+  else
+    *reinterpret_cast<Vec<T, V>*>(p) = v;
+}
+
 // V elements at a time (16 bytes; one element where a layout or an address does not
 // allow that). An item is V elements of each half of the pairs (half layout), V / 2
 // neighbouring pairs (interleaved; one pair for V = 1) or V copied elements.
@@ -67,9 +84,11 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
   __syncthreads();
   const int turned = INTER ? a.R / W : a.R / (2 * V);
   const int items = turned + (a.D - a.R) / V;
-  const long long gid = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const long long t = gid / items;
-  const int item = (int)(gid % items);
+  // (the thread's token and item, with the 64-bit division once per CTA)
+  const long long first_item = (long long)blockIdx.x * kThreads, first_token = first_item / items;
+  const unsigned in_cta = (unsigned)(first_item - first_token * items) + threadIdx.x;
+  const long long t = first_token + in_cta / (unsigned)items;
+  const int item = (int)(in_cta % (unsigned)items);
   if (t >= a.N) return;
   const int b = blockIdx.z;
   const int first = blockIdx.y * a.per_thread;
@@ -80,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
       const int which = i >= a.heads[0], h = which ? i - a.heads[0] : i;
       const T* x = static_cast<const T*>(a.x[which]) + b * a.xs[which][0] + h * a.xs[which][1] + t * a.xs[which][2];
       T* y = static_cast<T*>(a.y[which]) + b * a.ys[which][0] + h * a.ys[which][1] + t * a.ys[which][2];
-      *reinterpret_cast<Vec<T, V>*>(y + at) = *reinterpret_cast<const Vec<T, V>*>(x + at);
+      write<T, V>(y + at, read<T, V>(x + at));
     }
     return;
   }
@@ -102,25 +121,25 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
       y[at] = from_f32<T>(lo * c[0] - hi * s[0]);
       y[at + 1] = from_f32<T>(lo * s[0] + hi * c[0]);
     } else if constexpr (INTER) {
-      Vec<T, V> w = *reinterpret_cast<const Vec<T, V>*>(x + at);
+      Vec<T, V> w = read<T, V>(x + at);
 #pragma unroll
       for (int j = 0; j < PAIRS; ++j) {
         const float lo = to_f32<T>(w.e[2 * j]), hi = to_f32<T>(w.e[2 * j + 1]);
         w.e[2 * j] = from_f32<T>(lo * c[j] - hi * s[j]);
         w.e[2 * j + 1] = from_f32<T>(lo * s[j] + hi * c[j]);
       }
-      *reinterpret_cast<Vec<T, V>*>(y + at) = w;
+      write<T, V>(y + at, w);
     } else {
-      Vec<T, V> wa = *reinterpret_cast<const Vec<T, V>*>(x + at);
-      Vec<T, V> wb = *reinterpret_cast<const Vec<T, V>*>(x + at + a.R / 2);
+      Vec<T, V> wa = read<T, V>(x + at);
+      Vec<T, V> wb = read<T, V>(x + at + a.R / 2);
 #pragma unroll
       for (int j = 0; j < PAIRS; ++j) {
         const float lo = to_f32<T>(wa.e[j]), hi = to_f32<T>(wb.e[j]);
         wa.e[j] = from_f32<T>(lo * c[j] - hi * s[j]);
         wb.e[j] = from_f32<T>(lo * s[j] + hi * c[j]);
       }
-      *reinterpret_cast<Vec<T, V>*>(y + at) = wa;
-      *reinterpret_cast<Vec<T, V>*>(y + at + a.R / 2) = wb;
+      write<T, V>(y + at, wa);
+      write<T, V>(y + at + a.R / 2, wb);
     }
   }
 }
