@@ -302,7 +302,7 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
 }
 
 template <int DZ, bool EXACT>
-__global__ void __launch_bounds__(kThreads, DZ == 64 && !EXACT ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, DZ == 64 ? 3 : 2)
 gated_forward_kernel(const WalkArgs a) {
   walk_chunks<DZ, true, false, EXACT>(a);
 }
