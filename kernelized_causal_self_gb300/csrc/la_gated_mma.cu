@@ -387,22 +387,37 @@ gated_chunk_dg_kernel(const float* __restrict__ dot_q, const float* __restrict__
 
 }  // namespace
 
-// Segments: one wave of the 152 SMs' resident CTAs, but no segment under four chunks
-// (each costs the state pass and the scan).
-GatedPlan gated_mma_plan(int BH, int N, int M, int resident) {
-  const long long per = (long long)BH * ((M + 63) / 64);
-  const long long chunks = (N + kC - 1) / kC;
-  long long n_seg = (long long)152 * resident / per;
-  if (n_seg > (chunks + 3) / 4) n_seg = (chunks + 3) / 4;
-  if (n_seg < 1) n_seg = 1;
-  long long len = (chunks + n_seg - 1) / n_seg;
-  if (len < 1) len = 1;
-  n_seg = (chunks + len - 1) / len;
-  return GatedPlan{BH, N, (int)(len * kC), n_seg < 1 ? 1 : (int)n_seg};
+GatedPlan gated_mma_plan(int BH, int N, int blocks, const GatedCosts& k) {
+  const long long chunks = N > 0 ? (N + kC - 1) / kC : 1, per = (long long)BH * blocks;
+  GatedPlan best{BH, N, (int)chunks * kC, 1};
+  float shortest = -1.f;
+  // one segment; what fills 1, 2, .. waves; segments of 16, 8, .. chunks (16 is within
+  // every bound); and the fewest that the bound allows
+  for (int w = 0; w < 38; ++w) {
+    long long n_seg = w == 0 ? 1 : w * (long long)k.slots / per;
+    if (w > 32) n_seg = (chunks + (512 >> (w - 28)) - 1) / (512 >> (w - 28));
+    if (k.most > 0 && n_seg * k.most < chunks) n_seg = (chunks + k.most - 1) / k.most;
+    if (n_seg < 1) n_seg = 1;
+    if (n_seg > chunks) n_seg = chunks;
+    const long long len = (chunks + n_seg - 1) / n_seg;
+    n_seg = (chunks + len - 1) / len;
+    const long long waves = (per * n_seg + k.slots - 1) / k.slots;
+    const float each = (float)(per * chunks) / (3 * 152), pass_chunks = each > len ? each : (float)len;
+    const float t = waves * (k.fixed + len * k.chunk) +
+                    (n_seg > 1 ? k.pass + pass_chunks * k.pass_chunk + 0.1f * n_seg : 0.f);
+    if (shortest < 0.f || t < shortest) {
+      shortest = t;
+      best.len = (int)(len * kC);
+      best.n_seg = (int)n_seg;
+    }
+  }
+  return best;
 }
 
 GatedPlan gated_mma_forward_plan(int BH, int N, int D, int M) {
-  return gated_mma_plan(BH, N, M, D <= 64 ? 3 : 2);
+  const int blocks = (M + 63) / 64;
+  return gated_mma_plan(BH, N, blocks, D <= 64 ? GatedCosts{3 * 152, 0, 3.f, 3.4f, 9.f, 1.7f}
+                                               : GatedCosts{2 * 152, 0, 3.f, 4.5f, 9.f, 2.5f});
 }
 
 cudaError_t gated_mma_states(const GatedPlan& p, const void* k, const void* v, const void* q,
@@ -468,7 +483,7 @@ cudaError_t gated_mma_forward(const GatedForward& f, const GatedPlan& p, const G
 // ---- the backward for D or M over 64: states, scans, then dQ, dK and dV a walk each
 
 GatedPlan gated_mma_wide_plan(int BH, int N, int D, int M) {
-  return gated_mma_plan(BH, N, D > M ? D : M, 2);
+  return gated_mma_plan(BH, N, ((D > M ? D : M) + 63) / 64, GatedCosts{2 * 152, 0, 9.f, 14.f, 12.f, 5.f});
 }
 
 namespace {

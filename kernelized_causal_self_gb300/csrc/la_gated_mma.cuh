@@ -92,7 +92,15 @@ cudaError_t gated_launch(int smem, dim3 grid, int threads, cudaStream_t st, cons
 }
 
 // Tensor-core path: bf16 (la_gated_mma.cu, la_gated_mma_bwd.cu)
-GatedPlan gated_mma_plan(int BH, int N, int M, int resident);
+// The cut of BH sequences of N tokens (each `blocks` CTAs wide) that the costs below, in
+// microseconds as measured, make the shortest: CTAs run in waves of `slots`, each for
+// `fixed` + `chunk` a chunk of its segment; several segments need the state pass (three
+// CTAs an SM, `pass_chunk` a chunk) and the scan (0.1 a segment) first, `pass` in all else.
+struct GatedCosts {
+  int slots, most;  // resident CTAs; chunks of a segment at most (0: any number)
+  float fixed, chunk, pass, pass_chunk;
+};
+GatedPlan gated_mma_plan(int BH, int N, int blocks, const GatedCosts& k);
 GatedPlan gated_mma_forward_plan(int BH, int N, int D, int M);
 // each segment's own state from zero and its decay, and (dout not nullptr) its own
 // gradient of the incoming state from zero. exact: to float32's digits, for results.

@@ -33,7 +33,7 @@ using namespace mma;
 
 namespace {
 
-constexpr int kThreads = 128, kResident = 2, kMaxChunks = 14;
+constexpr int kThreads = 128, kResident = 2, kMaxChunks = 16;
 constexpr int kTile = kC * 64 * 2;
 constexpr int kStage = 4 * kTile;  // Q, K, V, dO
 constexpr int kOp = kTile;         // S or E in bf16, [d][m], one of two
@@ -280,18 +280,8 @@ int backward_grid(const GatedPlan& p) {
 
 }  // namespace
 
-// Segments of up to kMaxChunks chunks, of a length that fills whole waves of the
-// resident CTAs.
 GatedPlan gated_mma_backward_plan(int BH, int N) {
-  const long long chunks = (N + kC - 1) / kC, total = chunks * BH, slots = 152 * kResident;
-  long long waves = (total + slots * kMaxChunks - 1) / (slots * kMaxChunks);
-  if (waves < 1) waves = 1;
-  long long len = (total + slots * waves - 1) / (slots * waves);
-  if (len > kMaxChunks) len = kMaxChunks;
-  if (len > chunks) len = chunks;
-  if (len < 1) len = 1;
-  const long long n_seg = (chunks + len - 1) / len;
-  return GatedPlan{BH, N, (int)(len * kC), n_seg < 1 ? 1 : (int)n_seg};
+  return gated_mma_plan(BH, N, 1, GatedCosts{152 * kResident, kMaxChunks, 4.f, 7.f, 12.f, 3.4f});
 }
 
 size_t gated_mma_backward_scratch(const GatedPlan& p) {
