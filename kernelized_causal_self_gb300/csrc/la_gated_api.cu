@@ -27,7 +27,8 @@ bool shape_ok(int B, int H, int N) {
 bool dtype_ok(int dtype) { return dtype == LA_F32 || dtype == LA_BF16; }
 
 bool gated_ok(int B, int H, int N, int D, int M, int dtype) {
-  return shape_ok(B, H, N) && dim_ok(D) && dim_ok(M) && dtype_ok(dtype);
+  // (token indices are ints, also past a segment's end)
+  return shape_ok(B, H, N) && N <= 1 << 30 && dim_ok(D) && dim_ok(M) && dtype_ok(dtype);
 }
 
 bool strides_ok(const long long* s, int per) {
