@@ -158,14 +158,16 @@ def _stream_ptr(device):
 
 def _need_cuda(*ts, device=None):
     """Contiguous CUDA tensors, all on `device` (default: the first one's)."""
+    index = None if device is None else device.index
     for t in ts:
-        if not t.is_cuda:
+        at = t.get_device()  # (an index: a device object costs more than the comparison)
+        if at < 0:
             raise ValueError("tensors must be on a CUDA device")
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
-        if device is None:
-            device = t.device
-        elif t.device != device:
+        if index is None:
+            index, device = at, t.device
+        elif at != index:
             raise ValueError(f"tensors must all be on {device}, got one on {t.device}")
 
 
@@ -684,15 +686,18 @@ def _scratch(like, nbytes, workspace):
 
 
 def _check_gated(fn, q, k, v, g, rank):
-    (B, *HN), D, M = _dims(fn, q, v, rank)
-    lead, dt = q.shape[:-1], q.dtype
-    if k.shape != q.shape or k.dtype != dt:
-        _expect(fn, "k", k, q.shape, dt)
-    if v.shape[:-1] != lead or v.dtype != dt:
-        _expect(fn, "v", v, (*lead, M), dt)
+    lead, last, dt = q.shape, v.shape, q.dtype
+    if len(lead) != rank or len(last) != rank:
+        raise ValueError(f"{fn}: q and v must have {rank} dimensions")
+    if k.shape != lead or k.dtype != dt:
+        _expect(fn, "k", k, lead, dt)
+    dims = (*lead, last[-1])
+    lead = lead[:-1]
+    if last[:-1] != lead or v.dtype != dt:
+        _expect(fn, "v", v, (*lead, last[-1]), dt)
     if g.shape != lead or g.dtype != dt:
         _expect(fn, "g", g, lead, dt)
-    return (B, *HN, D, M), _dtype_code(q)
+    return dims, _dtype_code(q)
 
 
 def _forward_gated(fn, q, k, v, g, S0, out, S, want_state, workspace):
@@ -736,13 +741,14 @@ def la_prefill_gated(q, k, v, g, S0=None, out=None, S=None, workspace=None):
 
 def _check_pool(fn, S_pool, H, D, M, B, slots):
     import torch
-    if S_pool.dim() != 4:
+    shape = S_pool.shape
+    if len(shape) != 4:
         raise ValueError(f"{fn}: S_pool must be [pool, H, D, M]")
-    pool = S_pool.shape[0]
-    _expect(fn, "S_pool", S_pool, (pool, H, D, M), torch.float32)
+    if shape[1:] != (H, D, M) or S_pool.dtype != torch.float32:
+        _expect(fn, "S_pool", S_pool, (shape[0], H, D, M), torch.float32)
     if slots is not None and (slots.dtype != torch.int32 or slots.numel() != B):
         raise ValueError("slots must be a contiguous int32 tensor of B entries")
-    return pool
+    return shape[0]
 
 
 def la_extend_gated(q, k, v, g, S_pool, slots=None, lens=None, out=None, workspace=None):
@@ -780,12 +786,17 @@ def la_decode_step_gated(q, k, v, g, S_pool, slots=None, out=None):
     fn = "la_decode_step_gated"
     (n, H, D, M), dt = _check_gated(fn, q, k, v, g, 3)
     pool = _check_pool(fn, S_pool, H, D, M, n, slots)
-    if out is not None:
-        _expect(fn, "out", out, v.shape, q.dtype)
-    _need_cuda(q, k, v, g, S_pool, *[t for t in (out, slots) if t is not None])
+    if out is None:
+        _need_cuda(q, k, v, g, S_pool)
+        out = torch.empty_like(v)
+    else:
+        if out.shape != v.shape or out.dtype != v.dtype:
+            _expect(fn, "out", out, v.shape, q.dtype)
+        _need_cuda(q, k, v, g, S_pool, out)
+    if slots is not None:
+        _need_cuda(slots, device=q.device)
     lib = load_library()
     dev = q.device
-    out = torch.empty_like(v) if out is None else out
     with _on_device(dev):
         st = lib.la_decode_step_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
                                       S_pool.data_ptr(), _ptr(slots), out.data_ptr(), pool, n, H,
@@ -839,10 +850,12 @@ def la_backward_gated(q, k, v, g, dout, S0=None, dS=None, dq=None, dk=None, dv=N
 
 def _need_rows(*ts, device):
     """CUDA tensors on `device` whose last dimension is contiguous (the others strided)."""
+    index = device.index
     for t in ts:
-        if not t.is_cuda:
+        at = t.get_device()
+        if at < 0:
             raise ValueError("tensors must be on a CUDA device")
-        if t.device != device:
+        if at != index:
             raise ValueError(f"tensors must all be on {device}, got one on {t.device}")
 
 
@@ -855,18 +868,19 @@ def _row_strides(fn, name, t, packed=False, written=False):
     """The strides of the batch, head and token of t [B,H,N,*] (packed: [N,H,*]), for the library
     (0 where a dimension has one entry); rows that are written must not overlap."""
     size, stride = t.shape, t.stride()
-    if size[-1] > 1 and stride[-1] != 1 and t.numel():
+    if stride[-1] != 1 and size[-1] > 1 and t.numel():
         raise ValueError(f"{fn}: {name}'s last dimension must be contiguous")
-    if written and t.numel():
+    if written and not t.is_contiguous():
         reach = size[-1]
         for st, n in sorted((st, n) for st, n in zip(stride[:-1], size[:-1]) if n > 1):
             if st < reach:
                 raise ValueError(f"{fn}: rows of {name} overlap in memory")
             reach = st * (n - 1) + reach
     if packed:
-        return _long3(0, stride[1] if size[1] > 1 else 0, stride[0] if size[0] > 1 else 0)
-    return _long3(stride[0] if size[0] > 1 else 0, stride[1] if size[1] > 1 else 0,
-                  stride[2] if size[2] > 1 else 0)
+        (n, h, _), (sn, sh, _) = size, stride
+        return _long3(0, sh if h > 1 else 0, sn if n > 1 else 0)
+    (b, h, n, _), (sb, sh, sn, _) = size, stride
+    return _long3(sb if b > 1 else 0, sh if h > 1 else 0, sn if n > 1 else 0)
 
 
 def la_rotary_freqs(rot_dim, base=10000.0, scaling=None, factor=1.0, original_len=None, slow=1.0,
@@ -919,44 +933,43 @@ def la_rotary(q, k, freqs, positions=None, offset=0, interleaved=False, mscale=1
     the inputs themselves. Returns (q_out, k_out), contiguous unless passed in."""
     import torch
     fn = "la_rotary"
-    dt, shape = _dtype_code(q), q.shape
+    dt, shape, dtype, dev = _dtype_code(q), q.shape, q.dtype, q.device
     packed = len(shape) == 3
     if packed:
-        B, (N, H, D) = 1, shape
+        B = 1
+        N, H, D = shape
     elif len(shape) == 4:
         B, H, N, D = shape
     else:
         raise ValueError(f"{fn}: q must have 3 or 4 dimensions")
-    Hk, given = 0, [q, freqs]
-    if k is not None:
-        Hk = k.shape[1] if k.dim() == len(shape) else -1
-        _expect(fn, "k", k, (shape[0], Hk, *shape[2:]), q.dtype)
-        given.append(k)
-    elif k_out is not None:
-        raise ValueError(f"{fn}: k_out without k")
-    if freqs.dim() != 1 or freqs.dtype != torch.float64 or not freqs.is_contiguous():
+    qs = _row_strides(fn, "q", q, packed)
+    if k is None:
+        if k_out is not None:
+            raise ValueError(f"{fn}: k_out without k")
+        Hk, ks, kos = 0, None, None
+    else:
+        kshape = k.shape
+        Hk = kshape[1] if len(kshape) == len(shape) else -1
+        if kshape[0] != shape[0] or kshape[2:] != shape[2:] or Hk < 0 or k.dtype != dtype:
+            _expect(fn, "k", k, (shape[0], Hk, *shape[2:]), dtype)
+        ks = _row_strides(fn, "k", k, packed)
+    if freqs.dtype != torch.float64 or len(freqs.shape) != 1 or not freqs.is_contiguous():
         raise ValueError(f"{fn}: freqs must be a contiguous float64 tensor of R/2 entries")
     pos_b = 0
     if positions is not None:
         p = positions.shape
-        if positions.dtype != torch.int32 or not positions.is_contiguous() \
-                or not (p == (N,) or (not packed and p == (B, N))):
+        if p != (N,):
+            pos_b = N
+        if (pos_b and (packed or p != (B, N))) or positions.dtype != torch.int32 \
+                or not positions.is_contiguous():
             raise ValueError(f"{fn}: positions must be a contiguous int32 tensor of [N] or [B, N]")
-        pos_b = N if len(p) == 2 else 0
-        given.append(positions)
-    qs = _row_strides(fn, "q", q, packed)
-    ks = None if k is None else _row_strides(fn, "k", k, packed)
-    qos = kos = None
     if q_out is not None:
-        _expect(fn, "q_out", q_out, shape, q.dtype)
-        qos = _row_strides(fn, "q_out", q_out, packed, written=True)
-        given.append(q_out)
+        _expect(fn, "q_out", q_out, shape, dtype)
+        qos = _row_strides(fn, "q_out", q_out, packed, True)
     if k_out is not None:
-        _expect(fn, "k_out", k_out, k.shape, q.dtype)
-        kos = _row_strides(fn, "k_out", k_out, packed, written=True)
-        given.append(k_out)
-    dev = q.device
-    _need_rows(*given, device=dev)
+        _expect(fn, "k_out", k_out, kshape, dtype)
+        kos = _row_strides(fn, "k_out", k_out, packed, True)
+    _need_rows(q, freqs, *[t for t in (k, positions, q_out, k_out) if t is not None], device=dev)
     lib = load_library()
     if q_out is None:
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
@@ -967,9 +980,10 @@ def la_rotary(q, k, freqs, positions=None, offset=0, interleaved=False, mscale=1
     with _on_device(dev):
         st = lib.la_rotary(q.data_ptr(), qs, q_out.data_ptr(), qos, _ptr(k), ks, _ptr(k_out), kos,
                            freqs.data_ptr(), _ptr(positions), pos_b, int(offset), B, H, Hk, N, D,
-                           2 * freqs.shape[0], int(bool(interleaved)), int(bool(inverse)),
+                           2 * freqs.shape[0], 1 if interleaved else 0, 1 if inverse else 0,
                            float(mscale), dt, _stream_ptr(dev))
-    _check(fn, st)
+    if st:
+        _check(fn, st)
     return q_out, k_out
 
 
