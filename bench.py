@@ -41,16 +41,16 @@ def load_peaks():
 
 
 # DRAM bytes per call measured with ncu (read + write, summed over the call's kernels) and the
-# kernel-source revision they were taken on; reported only while the sources still match.
-TRAFFIC_REVISION = "a3c3be67d9fcc426"
+# revision of those kernels' sources; reported only while the sources still match.
+TRAFFIC_REVISION = "d561c2d57415c3ad"
 TRAFFIC_BYTES = {"la_backward": 902.3e6, "la_forward": 398.1e6}
 
 
 def kernel_revision():
     import glob
     import hashlib
-    files = sorted(glob.glob(os.path.join(ROOT, "kernelized_causal_self_gb300", "csrc", "*")))
-    files.append(os.path.join(ROOT, "include", "la.h"))
+    csrc = os.path.join(ROOT, "kernelized_causal_self_gb300", "csrc")
+    files = sorted(glob.glob(os.path.join(csrc, "la_tc*")) + glob.glob(os.path.join(csrc, "la_common.cuh")))
     h = hashlib.sha256()
     for f in files:
         h.update(os.path.basename(f).encode())

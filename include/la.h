@@ -26,7 +26,8 @@
  * caller; the library never allocates, frees or synchronises. All calls are
  * asynchronous on `stream` (a cudaStream_t passed as void*, NULL = legacy
  * default stream). The only process-wide state is an atomic count of kernel
- * launches (la_kernel_launches), so calls from several host threads are safe.
+ * launches (la_kernel_launches) and which kernels a device has been prepared for
+ * (atomic flags), so calls from several host threads are safe.
  * Outputs must not alias inputs (S and Z of la_decode_step are updated in
  * place by design).
  *
@@ -360,11 +361,11 @@ int la_debug_noalloc_set_status(int status, int wait_site, void* stream);
 
 /*
  * la_workspace_status -- synchronises `stream` and reads the status word a
- * previous la_forward / la_prefill / la_extend / la_backward left in
- * `workspace`: LA_OK; LA_ERR_TIMEOUT if a bounded wait inside a kernel (for a
- * TMA copy or a group of tensor-core MMAs) gave up, the outputs of that call
- * then being invalid; LA_ERR_INVALID_ARG if la_extend met a slot outside its
- * pool. Clears the word. Debug / test use.
+ * previous la_forward / la_prefill / la_extend / la_backward / la_extend_gated
+ * left in `workspace`: LA_OK; LA_ERR_TIMEOUT if a bounded wait inside a kernel
+ * (for a TMA copy or a group of tensor-core MMAs) gave up, the outputs of that
+ * call then being invalid; LA_ERR_INVALID_ARG if la_extend or la_extend_gated met
+ * a slot outside its pool. Clears the word. Debug / test use.
  */
 int la_workspace_status(void* workspace, size_t workspace_bytes, void* stream);
 

@@ -13,16 +13,21 @@
 // S (of each 64), S in float32 accumulators that stay in registers over the whole
 // segment. What is rounded to bf16: Q K^T * L as an operand, and the copy of S in
 // shared memory that Q multiplies; the outputs, bf16 too, cannot show more. The update
-// of S takes K's weighted rows as two bf16 terms (16 bits), since S itself is summed
-// over the whole sequence and may be returned in float32.
+// of S takes K's weighted rows as two bf16 terms (16 bits): with one, the longest
+// forward takes 97 us instead of 105, but its outputs are off by 2.8e-3 (2-norm) instead
+// of 2.3e-3, against 1.7e-3 for their own rounding.
 //
 // Why warp-level products and not tcgen05: at 64 columns a chunk's products are small
 // next to its element-wise work (masks, weights, splits), which here happens in the
-// registers that hold the fragments, with no round trip through tensor memory, no
-// barrier between the product and its use, and three CTAs of four warps per SM to
-// hide one another's waits. The products of the longest case take ~31 us of the
-// tensor pipe at the 600 TFLOP/s these instructions reach; reading and writing
-// q, k, v and out takes 40 us.
+// registers that hold the fragments, with no round trip through tensor memory and no
+// barrier between a product and its use. The price is that these instructions hold up
+// their scheduler's others: the products' 1088 cycles a chunk and warp (at the 600
+// TFLOP/s they reach) and some 540 other instructions add up rather than overlap, to
+// 2350 cycles with three CTAs of four warps per SM.
+//
+// B4 H8 N16384 D = M = 64: states 33 us (138 MB moved: half of what HBM gives, tensor
+// pipe 49%), scan 6 us, outputs 67 us (252 MB; tensor pipe 51%, issue slots 36%); the
+// whole call 105 us against 40 us for reading q, k, v and writing out once.
 #include "la_gated.cuh"
 #include "la_gated_mma.cuh"
 #include "la_mma.cuh"

@@ -10,6 +10,9 @@
 // sums its piece of dw over its rows; the CTAs' sums are joined in a fixed order by
 // a second kernel (no atomics: the result repeats bit for bit). All arithmetic and
 // sums are float32; results are rounded once.
+// B4 H8 N16384 M64 bf16: forward 33 us for 201 MB (6.1 TB/s). Two rows a thread at once with
+// their addresses worked out anew took 43 us, with 222 instructions a row and thread.
+// B2 H6 N2001 M96 float32: backward 10.3 + 2.3 us for 46 MB (6.8 us at HBM's rate).
 #include "la_common.cuh"
 #include "la_internal.h"
 

@@ -13,8 +13,10 @@
 // 32 bits, as a signed number of half turns, go to sincospif.
 //
 // Bound by memory: q and k are read and written once. A thread owns a few pairs of
-// one token, works out their cosines and sines once and applies them to several
-// heads of q and k.
+// one token, works out their cosines and sines once and applies them to up to 8 heads of
+// q and k. B4 H8 + 8 N16384 D64 bf16, token-major in, head-major out: 49 us for 268 MB
+// (5.5 TB/s; 40 us at the rate of a plain copy). With the frequencies' float64 products
+// per thread and not per CTA it was 61 us; 4 heads a thread 50.6, 16 heads 49.2.
 #include "la_common.cuh"
 #include "la_internal.h"
 
