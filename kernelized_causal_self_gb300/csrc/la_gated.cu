@@ -550,6 +550,7 @@ gated_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
   __shared__ __align__(16) float red[kThreads * 4];
   const size_t sh = blockIdx.x;
   const int tid = threadIdx.x;
+  tc::pdl_wait();
   const long long entry = entries.at((int)sh);
   const int cg = M >> 2, rgs = kThreads / cg, col = tid % cg, rg = tid / cg;
   float4* S4 = reinterpret_cast<float4*>(S + (size_t)(entry < 0 ? 0 : entry) * D * M);
@@ -656,18 +657,18 @@ cudaError_t gated_backward(const GatedBackward& f, void* ws, cudaStream_t st) {
 cudaError_t gated_decode(const void* q, const void* k, const void* v, const void* g, float* S,
                          const int* slots, void* out, int pool, int n_streams, int H, int D, int M,
                          int dtype, cudaStream_t st) {
-  const GatedEntries e{slots, pool, H};
-  const unsigned n = (unsigned)(n_streams * H);
+  const GatedEntries entries{slots, pool, H};
+  const dim3 grid((unsigned)(n_streams * H)), block(kThreads);
+  cudaError_t e;
   if (dtype == LA_F32)
-    gated_decode_kernel<float><<<n, kThreads, 0, st>>>((const float*)q, (const float*)k,
-                                                      (const float*)v, (const float*)g, S,
-                                                      (float*)out, e, D, M);
+    e = tcx::launch_pdl(gated_decode_kernel<float>, grid, block, 0, st, (const float*)q, (const float*)k,
+                        (const float*)v, (const float*)g, S, (float*)out, entries, D, M);
   else
-    gated_decode_kernel<__nv_bfloat16><<<n, kThreads, 0, st>>>(
-        (const __nv_bfloat16*)q, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v,
-        (const __nv_bfloat16*)g, S, (__nv_bfloat16*)out, e, D, M);
+    e = tcx::launch_pdl(gated_decode_kernel<__nv_bfloat16>, grid, block, 0, st, (const __nv_bfloat16*)q,
+                        (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, (const __nv_bfloat16*)g, S,
+                        (__nv_bfloat16*)out, entries, D, M);
   count_launches(1);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace la

@@ -19,6 +19,7 @@
 // per thread and not per CTA it was 61 us; 4 heads a thread 50.6, 16 heads 49.2.
 #include "la_common.cuh"
 #include "la_internal.h"
+#include "la_tc_common.cuh"
 
 namespace la {
 namespace {
@@ -82,6 +83,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
   constexpr int W = INTER && V == 1 ? 2 : V;  // elements of one access of a turned item
   // a CTA works its frequencies out once: float64 is slow here (two lanes a clock per SM)
   __shared__ unsigned long long steps[64];
+  tc::pdl_wait();
   if (threadIdx.x < a.R / 2) steps[threadIdx.x] = turn_step(a.freqs[threadIdx.x]);
   __syncthreads();
   const int turned = INTER ? a.R / W : a.R / (2 * V);
@@ -158,9 +160,11 @@ cudaError_t launch(RotaryArgs a, int B, cudaStream_t st) {
   a.per_thread = per;
   // the grid's y and z end at 65535
   if (B > 65535 || (heads + per - 1) / per > 65535 || tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
-  rotary_kernel<T, V, INTER><<<dim3((unsigned)tiles, (heads + per - 1) / per, B), kThreads, 0, st>>>(a);
+  const cudaError_t e = tcx::launch_pdl(rotary_kernel<T, V, INTER>,
+                                        dim3((unsigned)tiles, (heads + per - 1) / per, B),
+                                        dim3(kThreads), 0, st, a);
   count_launches(1);
-  return cudaGetLastError();
+  return e;
 }
 
 template <typename T>
