@@ -257,6 +257,7 @@ template <int CP>
 __global__ void __launch_bounds__(kThreads, CP == 2 ? 4 : 3)
 gated_recur_kernel(const __grid_constant__ RecurJobs jobs) {
   const RecurArgs& a = jobs.job[blockIdx.z];
+  tc::pdl_wait();
   if (a.reverse)
     recur_walk<CP, true>(a);
   else
@@ -334,6 +335,7 @@ gated_dg_kernel(const float* __restrict__ ends, const float* __restrict__ dot_q,
   __shared__ float part[8];
   const int bh = blockIdx.x / n_seg, seg = blockIdx.x % n_seg, tid = threadIdx.x;
   const int tb = seg * len, te = min(tb + len, N);
+  tc::pdl_wait();
   float carry = 0.f;
   for (int r = 0; r < rb; ++r) carry += ends[((size_t)r * BH + bh) * n_seg + seg];
   for (int hi = te; hi > tb; hi -= 256) {
@@ -372,14 +374,11 @@ cudaError_t launch_recur(const RecurJobs& jobs, int count, int D, int M, cudaStr
   const RecurArgs& a = jobs.job[0];
   const int cp = column_parts(D, M);
   const dim3 grid((unsigned)(a.BH * a.n_seg), (unsigned)row_blocks(D > M ? D : M, cp), count);
-  if (cp == 1)
-    gated_recur_kernel<1><<<grid, kThreads, 0, st>>>(jobs);
-  else if (cp == 2)
-    gated_recur_kernel<2><<<grid, kThreads, 0, st>>>(jobs);
-  else
-    gated_recur_kernel<4><<<grid, kThreads, 0, st>>>(jobs);
+  const cudaError_t e = cp == 1   ? tcx::launch_pdl(gated_recur_kernel<1>, grid, dim3(kThreads), 0, st, jobs)
+                        : cp == 2 ? tcx::launch_pdl(gated_recur_kernel<2>, grid, dim3(kThreads), 0, st, jobs)
+                                  : tcx::launch_pdl(gated_recur_kernel<4>, grid, dim3(kThreads), 0, st, jobs);
   count_launches(1);
-  return cudaGetLastError();
+  return e;
 }
 
 // Segments of the CUDA-core path: enough CTAs to give each of the 152 SMs four
@@ -531,10 +530,11 @@ cudaError_t simt_backward(const GatedBackward& f, const GatedPlan& p, const Gate
   dv.rs = 1;
   dv.cs = f.M;
   if ((e = launch_recur(grads, 3, f.D, f.M, st)) != cudaSuccess) return e;
-  gated_dg_kernel<<<(unsigned)(p.BH * p.n_seg), 256, 0, st>>>(
-      w.ends, w.dot_q, w.dot_k, static_cast<float*>(f.dg), p.BH, p.N, p.len, p.n_seg, rb);
+  e = tcx::launch_pdl(gated_dg_kernel, dim3((unsigned)(p.BH * p.n_seg)), dim3(256), 0, st,
+                      (const float*)w.ends, (const float*)w.dot_q, (const float*)w.dot_k,
+                      static_cast<float*>(f.dg), p.BH, p.N, p.len, p.n_seg, rb);
   count_launches(1);
-  return cudaGetLastError();
+  return e;
 }
 
 // Decode step: one CTA per (stream, head). Bound by the state's read and write
