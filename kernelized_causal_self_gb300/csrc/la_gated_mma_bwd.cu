@@ -51,9 +51,9 @@ constexpr int kParts = 2 * kC + 4;
 // two stages of tiles, the operand's two, outputs on their way out
 constexpr int kSmem = 2 * kStage + 2 * kOp + kTile + 2 * ((int)sizeof(GateTables) + 4 * kParts);
 static_assert(kResident * (kSmem + 1024) <= 228 * 1024, "CTAs per SM");
-// scratch of a CTA: S of each chunk as the warps hold it, and q . dQ of each token
-constexpr int kScratchS = kMaxChunks * 8 * kThreads * (int)sizeof(float4);
-constexpr int kScratch = kScratchS + kMaxChunks * kC * (int)sizeof(float);
+// scratch of a CTA for each chunk of a segment: S as the warps hold it, and q . dQ of each
+// token
+constexpr size_t kKept = 8 * kThreads * sizeof(float4), kScratch = kKept + kC * sizeof(float);
 
 struct BwdArgs {
   const bf16 *q, *k, *v, *g, *dout;
@@ -94,9 +94,9 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
   const uint32_t op_base = base + 2 * kStage, out_at = op_base + 2 * kOp;
   GateTables* tables = reinterpret_cast<GateTables*>(op_mem + 2 * kOp + kTile);
   float* parts = reinterpret_cast<float*>(tables + 2);
-  char* own = a.scratch + (size_t)blockIdx.x * kScratch;
+  char* own = a.scratch + (size_t)blockIdx.x * (a.len / kC) * kScratch;
   float4* states = reinterpret_cast<float4*>(own) + tid;  // [chunk][8][thread]
-  float* alpha = reinterpret_cast<float*>(own + kScratchS);        // [chunk][64]: q . dQ
+  float* alpha = reinterpret_cast<float*>(own + (a.len / kC) * kKept);  // [chunk][64]: q . dQ
 
   tc::pdl_wait();
   const int items = a.BH * a.n_seg;
@@ -294,7 +294,7 @@ GatedPlan gated_mma_backward_plan(int BH, int N) {
 }
 
 size_t gated_mma_backward_scratch(const GatedPlan& p) {
-  return (size_t)backward_grid(p) * kScratch;
+  return (size_t)backward_grid(p) * (p.len / kC) * kScratch;
 }
 
 cudaError_t gated_mma_backward(const GatedBackward& f, const GatedPlan& p, const GatedWorkspace& w,

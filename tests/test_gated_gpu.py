@@ -101,7 +101,7 @@ SHAPES = [  # B, H, N, D, M
     (1, 3, 65, 64, 64), (1, 2, 128, 64, 64), (2, 2, 129, 64, 64), (1, 2, 1301, 64, 64),
     (3, 7, 200, 64, 64), (1, 2, 77, 128, 128), (1, 1, 700, 128, 128), (2, 2, 130, 40, 72),
     (1, 2, 90, 8, 128), (2, 1, 333, 128, 16), (1, 1, 257, 96, 64), (1, 2, 100, 64, 96),
-    (40, 8, 70, 64, 64),
+    (40, 8, 70, 64, 64), (1, 1, 2500, 64, 64), (2, 20, 1100, 64, 64), (1, 3, 1000, 96, 128),
 ]
 ids = lambda s: "b%dh%dn%dd%dm%d" % s  # noqa: E731
 
@@ -299,7 +299,59 @@ def test_no_tokens(la):
     assert not dS0.any()
 
 
+def test_pool_entries_past_32_bits(la):
+    """The last entry of a pool of more than 2^31 elements."""
+    H, D = 8, 64
+    P = 2 ** 31 // (H * D * D) + 3
+    pool = torch.empty(P, H, D, D, device=DEV)
+    pool[-1], pool[0] = 0.5, 2.0
+    q, k, v, g, *_ = _inputs(4, 1, H, 70, D, D, BF)
+    start = pool[-1:].clone()
+    slots = torch.tensor([P - 1], dtype=torch.int32, device=DEV)
+    cut = lambda i, j: [x[:, :, i:j].contiguous() for x in (q, k, v, g)]  # noqa: E731
+    out = la.la_extend_gated(*cut(0, 69), pool, slots=slots)
+    one = la.la_decode_step_gated(*(x[:, :, 69].contiguous() for x in (q, k, v, g)), pool, slots=slots)
+    want, wS = oracle.gated_forward(*map(_f64, (q, k, v, g, start)))
+    ao, aS = oracle.gated_forward(*_abs(q, k, v), _f64(g), _f64(start))
+    _close(torch.cat((out, one[:, :, None]), 2), want, ao, BF, 70 + 2 * D + 64, "out")
+    _close(pool[-1:], wS, aS, BF, 70 + 2 * D + 64, "S", state=True)
+    assert torch.all(pool[0] == 2.0)
+
+
 # -------------------------------------------------------- streams, graphs, repeats
+
+def test_two_calls_at_once_on_two_streams(la):
+    sets = [_inputs(s, 2, 4, 700, 64, 64, BF) for s in (41, 42)]
+    run = lambda q, k, v, g, do, S0, dS: (*la.la_prefill_gated(q, k, v, g, S0=S0),  # noqa: E731
+                                          *la.la_backward_gated(q, k, v, g, do, S0, dS))
+    want = [run(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(4):
+        got = []
+        for s, stream in zip(sets, streams):
+            with torch.cuda.stream(stream):
+                got.append(run(*s))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_outputs_and_workspaces_of_the_callers(la):
+    q, k, v, g, do, S0, dS = _inputs(6, 2, 3, 333, 64, 64, BF)
+    out, S = la.la_prefill_gated(q, k, v, g, S0=S0)
+    grads = la.la_backward_gated(q, k, v, g, do, S0, dS)
+    ws = torch.full((la.la_gated_workspace_bytes(2, 3, 333, 64, 64),), 255, dtype=torch.uint8, device=DEV)
+    bws = torch.full((la.la_gated_backward_workspace_bytes(2, 3, 333, 64, 64),), 255, dtype=torch.uint8, device=DEV)
+    o2, s2 = torch.full_like(out, torch.nan), torch.full_like(S, torch.nan)
+    got = la.la_prefill_gated(q, k, v, g, S0=S0, out=o2, S=s2, workspace=ws)
+    assert got[0] is o2 and got[1] is s2 and torch.equal(o2, out) and torch.equal(s2, S)
+    into = [torch.full_like(x, torch.nan) for x in grads]
+    got = la.la_backward_gated(q, k, v, g, do, S0, dS, *into, workspace=bws)
+    assert all(a is b for a, b in zip(got, into)) and all(torch.equal(a, b) for a, b in zip(got, grads))
+    with pytest.raises(ValueError):
+        la.la_forward_gated(q, k, v, g, workspace=ws[:100])
+
 
 def test_repeats_bit_for_bit_and_on_another_stream(la):
     q, k, v, g, do, S0, dS = _inputs(8, 2, 4, 1000, 64, 64, BF)

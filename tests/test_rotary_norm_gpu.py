@@ -130,6 +130,18 @@ def test_rotary_scaled_for_long_contexts(la, scaling):
     assert np.all(np.abs(_f64(far) - want) <= 1e-3 * np.abs(_f64(q)).max())
 
 
+def test_rotary_past_32_bits(la):
+    """The last tokens of a tensor of more than 2^31 elements, in place."""
+    N = 2 ** 31 // 128 + 100
+    q = torch.zeros(1, 1, N, 128, dtype=BF, device=DEV)
+    tail = _randn(8, 1, 1, 50, 128, dtype=BF)
+    q[:, :, -50:] = tail
+    freqs, _ = la.la_rotary_freqs(128, device=DEV)
+    la.la_rotary(q, None, freqs, q_out=q)
+    _rotary_close(q[:, :, -50:], tail, np.arange(N - 50, N), freqs, BF)
+    assert not q[:, :, :100].any()
+
+
 # ---------------------------------------------------------------- gated head norm
 
 def _norm_inputs(seed, B, H, N, M, dtype, heads, token_major):
