@@ -408,7 +408,9 @@ GatedPlan gated_mma_plan(int BH, int N, int blocks, const GatedCosts& k) {
     n_seg = (chunks + len - 1) / len;
     const long long waves = (per * n_seg + k.slots - 1) / k.slots;
     const float each = (float)(per * chunks) / (3 * 152), pass_chunks = each > len ? each : (float)len;
-    const float t = waves * (k.fixed + len * k.chunk) +
+    // (an SM's only CTA takes less than half as long on a chunk as one of three)
+    const float full = per * n_seg < k.slots ? (float)(per * n_seg) / k.slots : 1.f;
+    const float t = waves * (k.fixed + len * k.chunk * (0.45f + 0.55f * full)) +
                     (n_seg > 1 ? k.pass + pass_chunks * k.pass_chunk + 0.1f * n_seg : 0.f);
     if (shortest < 0.f || t < shortest) {
       shortest = t;

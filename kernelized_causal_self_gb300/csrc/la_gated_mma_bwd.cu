@@ -290,7 +290,7 @@ int backward_grid(const GatedPlan& p) {
 }  // namespace
 
 GatedPlan gated_mma_backward_plan(int BH, int N) {
-  return gated_mma_plan(BH, N, 1, GatedCosts{152 * kResident, kMaxChunks, 4.f, 7.f, 12.f, 3.4f});
+  return gated_mma_plan(BH, N, 1, GatedCosts{152 * kResident, kMaxChunks, 4.f, 7.f, 7.f, 3.4f});
 }
 
 size_t gated_mma_backward_scratch(const GatedPlan& p) {
