@@ -399,7 +399,8 @@ int la_workspace_wait_site(void* workspace, size_t workspace_bytes, void* stream
  * a chunk of tokens rounded to bf16, as far as an output in bf16 shows them.
  */
 
-/* Scratch needed by la_forward_gated and la_extend_gated, in bytes. */
+/* Scratch needed by la_forward_gated and la_extend_gated, in bytes; where it is 256 (the
+ * status header alone), la_forward_gated needs none and takes nullptr. */
 size_t la_gated_workspace_bytes(int B, int H, int N, int D, int M, int dtype);
 
 /*

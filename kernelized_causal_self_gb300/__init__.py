@@ -717,7 +717,8 @@ def _forward_gated(fn, q, k, v, g, S0, out, S, want_state, workspace):
     out = torch.empty_like(v) if out is None else out
     if want_state and S is None:
         S = q.new_empty((B, H, D, M), dtype=torch.float32)
-    ws, nbytes = _scratch(q, _bytes("la_gated_workspace_bytes", B, H, N, D, M, dt), workspace)
+    need = _bytes("la_gated_workspace_bytes", B, H, N, D, M, dt)
+    ws, nbytes = _scratch(q, need if need > 256 else 0, workspace)  # (256: a header it leaves alone)
     with _on_device(dev):
         st = lib.la_forward_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
                                   out.data_ptr(), _ptr(S0), _ptr(S), B, H, N, D, M, dt, _ptr(ws),

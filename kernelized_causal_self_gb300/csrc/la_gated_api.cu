@@ -69,8 +69,10 @@ int la_forward_gated(const void* q, const void* k, const void* v, const void* g,
   cudaStream_t st = as_stream(stream);
   if (N == 0) return copy_state(S, S0, (size_t)B * H * D * M, st);
   if (!ptrs_ok({q, k, v, g, out})) return LA_ERR_INVALID_ARG;
-  if (workspace == nullptr || !aligned(workspace, 16) ||
-      workspace_bytes < la::gated_forward_workspace(B * H, N, D, M, dtype))
+  // (the header alone is not used: there is no slot that could be outside a pool)
+  const size_t need = la::gated_forward_workspace(B * H, N, D, M, dtype);
+  if (need > la::kHeaderBytes &&
+      (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < need))
     return LA_ERR_WORKSPACE;
   const la::GatedForward f{q, k, v, g, out, S0, S, nullptr, nullptr, B, B, H, N, D, M, dtype};
   return from_cuda(la::gated_forward(f, workspace, st));

@@ -138,9 +138,10 @@ def test_abi_refuses_before_a_launch(lib):
     assert fwd(q=0) == bad and fwd(g=ODD) == bad and fwd(S0=ODD) == bad and fwd(S=ODD) == bad
     assert fwd(D=12) == bad and fwd(M=136) == bad and fwd(B=0) == bad and fwd(N=-1) == bad and fwd(dt=2) == bad
     assert fwd(B=1 << 16, H=1 << 16) == bad
-    assert fwd(w=None) == ws and fwd(wb=16) == ws and fwd(N=0, q=0) == la.LA_OK
+    assert fwd(N=0, q=0) == la.LA_OK
     need = la.la_gated_workspace_bytes(1, 1, 4000, 64, 64)
-    assert need > 256 and fwd(N=4000, wb=need - 1) == ws
+    assert need > 256 and fwd(N=4000, wb=need - 1) == ws and fwd(N=4000, w=None, wb=need) == ws
+    assert fwd(N=4000, w=ODD, wb=need) == ws
 
     def ext(pool=FAKE, slots=None, lens=None, P=4, B=2, N=8, w=FAKE):
         return lib.la_extend_gated(FAKE, FAKE, FAKE, FAKE, FAKE, pool, slots, lens, P, B, 2, N, 64, 64, 1,

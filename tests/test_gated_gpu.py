@@ -349,8 +349,9 @@ def test_outputs_and_workspaces_of_the_callers(la):
     into = [torch.full_like(x, torch.nan) for x in grads]
     got = la.la_backward_gated(q, k, v, g, do, S0, dS, *into, workspace=bws)
     assert all(a is b for a, b in zip(got, into)) and all(torch.equal(a, b) for a, b in zip(got, grads))
+    z = torch.zeros(1, 1, 4000, 64, dtype=BF, device=DEV)
     with pytest.raises(ValueError):
-        la.la_forward_gated(q, k, v, g, workspace=ws[:100])
+        la.la_forward_gated(z, z, z, z[..., 0].contiguous(), workspace=ws[:100])
 
 
 def test_repeats_bit_for_bit_and_on_another_stream(la):
