@@ -682,7 +682,7 @@ def _scratch(like, nbytes, workspace):
         workspace = _workspace(nbytes, like.device, workspace)
         return workspace, workspace.numel() * workspace.element_size()
     import torch
-    return (like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None), nbytes
+    return (torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes else None), nbytes
 
 
 def _check_gated(fn, q, k, v, g, rank):
@@ -716,7 +716,7 @@ def _forward_gated(fn, q, k, v, g, S0, out, S, want_state, workspace):
     dev = q.device
     out = torch.empty_like(v) if out is None else out
     if want_state and S is None:
-        S = q.new_empty((B, H, D, M), dtype=torch.float32)
+        S = torch.empty((B, H, D, M), dtype=torch.float32, device=dev)
     need = _bytes("la_gated_workspace_bytes", B, H, N, D, M, dt)
     ws, nbytes = _scratch(q, need if need > 256 else 0, workspace)  # (256: a header it leaves alone)
     with _on_device(dev):
@@ -1014,23 +1014,24 @@ def la_norm_gate(x, z, w, eps=1e-6, out=None):
     import torch
     fn = "la_norm_gate"
     (B, H, N, M), dt = _norm_checks(fn, x, z, w)
-    rows = [z]
-    if out is not None:
-        _expect(fn, "out", out, x.shape, x.dtype)
-        outs = _row_strides(fn, "out", out, written=True)
-        rows.append(out)
-    zs = _row_strides(fn, "z", z)
     dev = x.device
-    _need_cuda(x, w)
-    _need_rows(*rows, device=dev)
-    lib = load_library()
+    zs = _row_strides(fn, "z", z)
     if out is None:
+        _need_cuda(x, w)
+        _need_rows(z, device=dev)
         out = torch.empty_like(x)
         outs = _row_strides(fn, "out", out)
+    else:
+        _expect(fn, "out", out, x.shape, x.dtype)
+        outs = _row_strides(fn, "out", out, False, True)
+        _need_cuda(x, w)
+        _need_rows(z, out, device=dev)
+    lib = load_library()
     with _on_device(dev):
         st = lib.la_norm_gate(x.data_ptr(), z.data_ptr(), zs, w.data_ptr(), out.data_ptr(), outs,
-                              B, H, N, M, int(w.dim() == 2), float(eps), dt, _stream_ptr(dev))
-    _check(fn, st)
+                              B, H, N, M, w.dim() - 1, float(eps), dt, _stream_ptr(dev))
+    if st:
+        _check(fn, st)
     return out
 
 
@@ -1040,32 +1041,31 @@ def la_norm_gate_backward(x, z, w, dy, eps=1e-6, dx=None, dz=None, dw=None, work
     import torch
     fn = "la_norm_gate_backward"
     (B, H, N, M), dt = _norm_checks(fn, x, z, w)
-    if dy.shape != x.shape or dy.dtype != x.dtype:
-        _expect(fn, "dy", dy, x.shape, x.dtype)
-    rows, flat = [z, dy], [x, w]
-    for name, t, like in (("dx", dx, x), ("dw", dw, w)):
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    if dy.shape != shape or dy.dtype != dtype:
+        _expect(fn, "dy", dy, shape, dtype)
+    for name, t, like in (("dx", dx, shape), ("dz", dz, shape), ("dw", dw, w.shape)):
         if t is not None:
-            _expect(fn, name, t, like.shape, x.dtype)
-            flat.append(t)
-    if dz is not None:
-        _expect(fn, "dz", dz, x.shape, x.dtype)
-        dzs = _row_strides(fn, "dz", dz, written=True)
-        rows.append(dz)
+            _expect(fn, name, t, like, dtype)
     zs, dys = _row_strides(fn, "z", z), _row_strides(fn, "dy", dy)
-    dev = x.device
-    _need_cuda(*flat)
-    _need_rows(*rows, device=dev)
+    if dz is not None:
+        dzs = _row_strides(fn, "dz", dz, False, True)
+    _need_cuda(x, w, *[t for t in (dx, dw) if t is not None])
+    _need_rows(z, dy, *([] if dz is None else [dz]), device=dev)
     lib = load_library()
-    dx = torch.empty_like(x) if dx is None else dx
+    if dx is None:
+        dx = torch.empty_like(x)
     if dz is None:
         dz = torch.empty_like(x)
         dzs = _row_strides(fn, "dz", dz)
-    dw = torch.empty_like(w) if dw is None else dw
+    if dw is None:
+        dw = torch.empty_like(w)
     ws, nbytes = _scratch(x, _bytes("la_norm_gate_workspace_bytes", B, H, N, M), workspace)
     with _on_device(dev):
         st = lib.la_norm_gate_backward(x.data_ptr(), z.data_ptr(), zs, w.data_ptr(), dy.data_ptr(),
                                        dys, dx.data_ptr(), dz.data_ptr(), dzs, dw.data_ptr(),
-                                       B, H, N, M, int(w.dim() == 2), float(eps), dt, _ptr(ws),
+                                       B, H, N, M, w.dim() - 1, float(eps), dt, ws.data_ptr(),
                                        nbytes, _stream_ptr(dev))
-    _check(fn, st)
+    if st:
+        _check(fn, st)
     return dx, dz, dw
