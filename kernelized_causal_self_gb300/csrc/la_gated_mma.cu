@@ -74,15 +74,16 @@ struct WalkArgs {
   float4* kept;
 };
 
-template <int DZ, bool OUT>
+template <int DZ, bool OUT, bool FINE = false>
 struct WalkSmem {
   static constexpr int kZ = OUT ? kC * DZ * 2 : 0, kW = kC * DZ * 2, kU = kC * 64 * 2;
   static constexpr int kStage = kZ + kW + kU;
-  static constexpr int kX = OUT ? DZ * 64 * 2 : 0;  // X in bf16, one of two
+  static constexpr int kX = OUT ? DZ * 64 * 2 : 0;  // X in bf16, one of two; FINE: and their rest
   // the state pass has little to do on a chunk, so it asks for two ahead; the outputs'
   // walk is longer on a chunk than a load takes
   static constexpr int kStages = OUT ? 2 : 3;
-  static constexpr int kBytes = kStages * kStage + 2 * kX + 2 * (int)sizeof(GateTables);
+  static constexpr int kTables = kStages * kStage + (FINE ? 4 : 2) * kX;
+  static constexpr int kBytes = kTables + 2 * (int)sizeof(GateTables);
 };
 
 // OUT: outputs (and, with one segment, the final state), else the state pass: the
@@ -93,15 +94,16 @@ struct WalkSmem {
 // leaves the kernel as a float32 result; where it only goes on as a bf16 operand, 16 bits
 // and sums in place do, and leave registers for more CTAs per SM.
 // DOTS: the parts of the gates' gradient.
-template <int DZ, bool OUT, bool REV, bool EXACT, bool DOTS = false>
+// FINE: see gated_fine.
+template <int DZ, bool OUT, bool REV, bool EXACT, bool DOTS = false, bool FINE = false>
 __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
-  using Sm = WalkSmem<DZ, OUT>;
+  using Sm = WalkSmem<DZ, OUT, FINE>;
   constexpr int KS = DZ / 16, DT = DZ / 64;
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t base = tc::smem_u32(smem), x_op = base + Sm::kStages * Sm::kStage;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = lane >> 2, col = (lane & 3) * 2;  // of an accumulator
-  GateTables* tables = reinterpret_cast<GateTables*>(smem + Sm::kStages * Sm::kStage + 2 * Sm::kX);
+  GateTables* tables = reinterpret_cast<GateTables*>(smem + Sm::kTables);
   const Lane<DZ> ln;
   const Lane<64> ln64;
 
@@ -122,7 +124,10 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
   float x[DT][8][4];
   auto keep_op = [&](int buf) {
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt) store_op(ln64, x_op + buf * Sm::kX, dt * 64 + rb * 16, 0, x[dt]);
+    for (int dt = 0; dt < DT; ++dt) {
+      store_op(ln64, x_op + buf * Sm::kX, dt * 64 + rb * 16, 0, x[dt]);
+      if (FINE) store_op<true>(ln64, x_op + (2 + buf) * Sm::kX, dt * 64 + rb * 16, 0, x[dt]);
+    }
   };
   auto load_chunk = [&](int c) {
     const int t0 = tb + c * kC, rows = min(kC, te - t0);
@@ -223,6 +228,7 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
       float o[8][4];
       const float gr[2] = {Gs[r0 + row], Gs[r0 + row + 8]};
       product<true>(ln64, o, f, x_op + (i & 1) * Sm::kX);
+      if (FINE) product<true, true>(ln64, o, f, x_op + (2 + (i & 1)) * Sm::kX);
       if (REV)
         scale_rows(o, t.W[r0 + row], t.W[r0 + row + 8]);
       else
@@ -234,7 +240,7 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
         __syncwarp();
         inter = row_dots(ln, z_at, r0, o);
       }
-      uint32_t p[4];
+      uint32_t p[FINE ? 2 : 1][4];
 #pragma unroll 1
       for (int b = REV ? rb + 1 : 0; b < (REV ? 4 : rb); ++b) {
         masked_block<!REV, false>(ln, p, f, w_at, b, gr, Gs);
@@ -306,10 +312,10 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
     a.decay[(size_t)bh * a.n_seg + seg] = gated_decay(all * kLn2);
 }
 
-template <int DZ, bool EXACT>
-__global__ void __launch_bounds__(kThreads, DZ == 64 ? 3 : 2)
+template <int DZ, bool EXACT, bool FINE>
+__global__ void __launch_bounds__(kThreads, DZ == 64 ? FINE ? 2 : 3 : FINE ? 1 : 2)
 gated_forward_kernel(const WalkArgs a) {
-  walk_chunks<DZ, true, false, EXACT>(a);
+  walk_chunks<DZ, true, false, EXACT, false, FINE>(a);
 }
 
 // blockIdx.z: the segments' states, or their gradients
@@ -322,19 +328,22 @@ gated_states_kernel(const WalkArgs a, const WalkArgs back) {
     walk_chunks<DZ, false, true, EXACT>(back);
 }
 
-template <int DZ, bool REV, bool DOTS>
-__global__ void __launch_bounds__(kThreads, DZ == 64 ? 3 : 2) gated_gradient_kernel(const WalkArgs a) {
-  walk_chunks<DZ, true, REV, false, DOTS>(a);
+template <int DZ, bool REV, bool DOTS, bool FINE>
+__global__ void __launch_bounds__(kThreads, DZ == 64 ? FINE ? 2 : 3 : FINE ? 1 : 2)
+gated_gradient_kernel(const WalkArgs a) {
+  walk_chunks<DZ, true, REV, false, DOTS, FINE>(a);
 }
 
 dim3 walk_grid(const WalkArgs& a, int z = 1) {
   return dim3((unsigned)(a.BH * a.n_seg), (unsigned)((a.UD + 63) / 64), (unsigned)z);
 }
 
-template <bool EXACT>
-cudaError_t launch_forward(const WalkArgs& a, cudaStream_t st) {
-  return a.ZD <= 64 ? gated_launch<gated_forward_kernel<64, EXACT>>(WalkSmem<64, true>::kBytes, walk_grid(a), kThreads, st, a)
-                    : gated_launch<gated_forward_kernel<128, EXACT>>(WalkSmem<128, true>::kBytes, walk_grid(a), kThreads, st, a);
+template <int DZ, bool EXACT>
+cudaError_t launch_forward(const WalkArgs& a, bool fine, cudaStream_t st) {
+  return fine ? gated_launch<gated_forward_kernel<DZ, EXACT, true>>(WalkSmem<DZ, true, true>::kBytes,
+                                                                    walk_grid(a), kThreads, st, a)
+              : gated_launch<gated_forward_kernel<DZ, EXACT, false>>(WalkSmem<DZ, true>::kBytes,
+                                                                     walk_grid(a), kThreads, st, a);
 }
 
 template <bool EXACT>
@@ -344,11 +353,20 @@ cudaError_t launch_states(const WalkArgs& a, const WalkArgs& back, int jobs, cud
              : gated_launch<gated_states_kernel<128, EXACT>>(WalkSmem<128, false>::kBytes, walk_grid(a, jobs), kThreads, st, a, back);
 }
 
-template <bool REV, bool DOTS>
+template <bool REV, bool DOTS, bool FINE>
 cudaError_t launch_gradient(const WalkArgs& a, cudaStream_t st) {
-  return a.ZD <= 64
-             ? gated_launch<gated_gradient_kernel<64, REV, DOTS>>(WalkSmem<64, true>::kBytes, walk_grid(a), kThreads, st, a)
-             : gated_launch<gated_gradient_kernel<128, REV, DOTS>>(WalkSmem<128, true>::kBytes, walk_grid(a), kThreads, st, a);
+  return a.ZD <= 64 ? gated_launch<gated_gradient_kernel<64, REV, DOTS, FINE>>(
+                          WalkSmem<64, true, FINE>::kBytes, walk_grid(a), kThreads, st, a)
+                    : gated_launch<gated_gradient_kernel<128, REV, DOTS, FINE>>(
+                          WalkSmem<128, true, FINE>::kBytes, walk_grid(a), kThreads, st, a);
+}
+
+template <bool FINE>
+cudaError_t launch_gradients(const WalkArgs& dq, const WalkArgs& dk, const WalkArgs& dv, cudaStream_t st) {
+  cudaError_t e = launch_gradient<false, true, FINE>(dq, st);
+  if (e == cudaSuccess) e = launch_gradient<true, true, FINE>(dk, st);
+  if (e == cudaSuccess) e = launch_gradient<true, false, FINE>(dv, st);
+  return e;
 }
 
 // dg of a chunk from its dots (see la_gated_mma_bwd.cu): a warp each, two tokens a lane.
@@ -484,7 +502,9 @@ cudaError_t gated_mma_forward(const GatedForward& f, const GatedPlan& p, const G
     a.init = f.S0;
     a.fin = f.S;
   }
-  return a.fin ? launch_forward<true>(a, st) : launch_forward<false>(a, st);
+  const bool fine = gated_fine(p.BH * ((f.M + 63) / 64), p.N);
+  if (f.D <= 64) return a.fin ? launch_forward<64, true>(a, fine, st) : launch_forward<64, false>(a, fine, st);
+  return a.fin ? launch_forward<128, true>(a, fine, st) : launch_forward<128, false>(a, fine, st);
 }
 
 // ---- the backward for D or M over 64: states, scans, then dQ, dK and dV a walk each
@@ -547,9 +567,9 @@ cudaError_t gated_mma_wide_backward(const GatedBackward& f, const GatedPlan& p, 
   dk.seg_in = dv.seg_in = w.E;
   dq.dots = dot_q;
   dk.dots = dot_k;
-  if ((e = launch_gradient<false, true>(dq, st)) != cudaSuccess) return e;
-  if ((e = launch_gradient<true, true>(dk, st)) != cudaSuccess) return e;
-  if ((e = launch_gradient<true, false>(dv, st)) != cudaSuccess) return e;
+  e = gated_fine(p.BH * wide_blocks(f.D > f.M ? f.D : f.M), p.N) ? launch_gradients<true>(dq, dk, dv, st)
+                                                               : launch_gradients<false>(dq, dk, dv, st);
+  if (e != cudaSuccess) return e;
   const long long warps = (long long)p.BH * (long long)chunks;
   e = tcx::launch_pdl(gated_chunk_dg_kernel, dim3((unsigned)((warps + 3) / 4)), dim3(kThreads), 0, st,
                       (const float*)dot_q, (const float*)dot_k, (const float*)inter, (const float*)ends,

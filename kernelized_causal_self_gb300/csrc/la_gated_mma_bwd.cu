@@ -45,12 +45,13 @@ namespace {
 constexpr int kThreads = 128, kResident = 2, kMaxChunks = 16;
 constexpr int kTile = kC * 64 * 2;
 constexpr int kStage = 4 * kTile;  // Q, K, V, dO
-constexpr int kOp = kTile;         // S or E in bf16, [d][m], one of two
+constexpr int kOp = kTile;         // S or E in bf16, [d][m], one of two; FINE: and their rest
 // floats per parity of the chunk: the parts of dg (sums of X's columns, b, <S, E> by warp)
 constexpr int kParts = 2 * kC + 4;
 // two stages of tiles, the operand's two, outputs on their way out
-constexpr int kSmem = 2 * kStage + 2 * kOp + kTile + 2 * ((int)sizeof(GateTables) + 4 * kParts);
-static_assert(kResident * (kSmem + 1024) <= 228 * 1024, "CTAs per SM");
+template <bool FINE>
+constexpr int kSmem = 2 * kStage + (FINE ? 4 : 2) * kOp + kTile + 2 * ((int)sizeof(GateTables) + 4 * kParts);
+static_assert(kResident * (kSmem<true> + 1024) <= 228 * 1024, "CTAs per SM");
 // scratch of a CTA for each chunk of a segment: S as the warps hold it, and q . dQ of each
 // token
 constexpr size_t kKept = 8 * kThreads * sizeof(float4), kScratch = kKept + kC * sizeof(float);
@@ -81,6 +82,7 @@ __device__ __forceinline__ void load_state(float (&x)[NT][4], const float* from,
     }
 }
 
+template <bool FINE>
 __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(const BwdArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t base = tc::smem_u32(smem);
@@ -90,9 +92,10 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
   // CTA, so that no scheduler gets all of the most
   const int rb = (warp + blockIdx.x) & 3, r0 = rb * 16;
   const Lane<64> ln;
+  constexpr int kOps = FINE ? 4 : 2;
   uint8_t* op_mem = smem + 2 * kStage;
-  const uint32_t op_base = base + 2 * kStage, out_at = op_base + 2 * kOp;
-  GateTables* tables = reinterpret_cast<GateTables*>(op_mem + 2 * kOp + kTile);
+  const uint32_t op_base = base + 2 * kStage, out_at = op_base + kOps * kOp;
+  GateTables* tables = reinterpret_cast<GateTables*>(op_mem + kOps * kOp + kTile);
   float* parts = reinterpret_cast<float*>(tables + 2);
   char* own = a.scratch + (size_t)blockIdx.x * (a.len / kC) * kScratch;
   float4* states = reinterpret_cast<float4*>(own) + tid;  // [chunk][8][thread]
@@ -125,9 +128,13 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
 
     // ---- forward: dQ
     float x[8][4];  // S, then E
+    auto keep_op = [&](int buf) {
+      store_op(ln, op_base + buf * kOp, r0, 0, x);
+      if (FINE) store_op<true>(ln, op_base + (2 + buf) * kOp, r0, 0, x);
+    };
     load_state(x, a.S ? a.S + ((size_t)bh * (a.n_seg + 1) + seg) * DM : a.S0 ? a.S0 + bh * DM : nullptr,
                r0, 0, a.D, a.M);
-    store_op(ln, op_base, r0, 0, x);
+    keep_op(0);
     for (int c = 0; c < chunks; ++c) {
       cp_async_wait<0>();
       __syncthreads();
@@ -142,11 +149,12 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       if (maker) raw = raw_gates(c + 1);
 #pragma unroll
       for (int j = 0; j < 8; ++j) states[(c * 8 + j) * kThreads] = keep_tile(x[j]);
-      uint32_t f[4][4], p[4];
+      uint32_t f[4][4], p[FINE ? 2 : 1][4];
       float d[8][4];
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) ln.load_a(f[ks], do_at, r0, ks);
       product<false>(ln, d, f, op_base + (c & 1) * kOp);
+      if (FINE) product<false, true>(ln, d, f, op_base + (2 + (c & 1)) * kOp);
       const float gi[2] = {Gs[r0 + row], Gs[r0 + row + 8]};
       scale_rows(d, ex2(gi[0]), ex2(gi[1]));
 #pragma unroll 1
@@ -166,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       if (c + 1 < chunks) {
         scale_rows(x, t.decay, t.decay);
         add_outer<false>(ln, ln, x, k_at, t.X, rb, v_at, 0);
-        store_op(ln, op_base + ((c + 1) & 1) * kOp, r0, 0, x);
+        keep_op((c + 1) & 1);
       }
       if (maker) chunk_gates<false, false>(raw, tables[(c + 1) & 1]);
     }
@@ -175,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
     load_state(x, a.E ? a.E + ((size_t)bh * (a.n_seg + 1) + seg + 1) * DM : a.dS ? a.dS + bh * DM : nullptr,
                r0, 0, a.D, a.M);
     __syncthreads();
-    store_op(ln, op_base, r0, 0, x);
+    keep_op(0);
     if (warp == 0) chunk_gates<true, false>(raw_gates(chunks - 1), tables[(chunks - 1) & 1]);
     // dg of chunk c from the parts its warps left (one warp)
     auto finish = [&](int c) {
@@ -222,11 +230,12 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       const float dec = t.decay;
       const float gj[2] = {Gs[r0 + row], Gs[r0 + row + 8]};
       const int t0 = tb + c * kC + r0;
-      uint32_t f[4][4], p[4];
+      uint32_t f[4][4], p[FINE ? 2 : 1][4];
       float d[8][4];
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) ln.load_a(f[ks], k_at, r0, ks);
       product<true>(ln, d, f, op);
+      if (FINE) product<true, true>(ln, d, f, op + 2 * kOp);
       scale_rows(d, t.W[r0 + row], t.W[r0 + row + 8]);
       masked_block<false, true>(ln, p, f, q_at, rb, gj, Gs);
       add_block(ln, d, p, do_at, rb);
@@ -252,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) ln.load_a(f[ks], v_at, k0, ks);
       product<false>(ln, d, f, op);
+      if (FINE) product<false, true>(ln, d, f, op + 2 * kOp);
       scale_rows(d, t.W[k0 + row], t.W[k0 + row + 8]);
       const float2 be = row_dots(ln, k_at, k0, d);
       masked_block<false, true>(ln, p, f, do_at, kb, gk, Gs);
@@ -273,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       if (c > 0) {
         scale_rows(x, dec, dec);
         add_outer<false>(ln, ln, x, q_at, t.X, rb, do_at, 0);
-        store_op(ln, op_base + ((step + 1) & 1) * kOp, r0, 0, x);
+        keep_op((step + 1) & 1);
       }
       if (maker) chunk_gates<true, false>(raw, tables[(c - 1) & 1]);
     }
@@ -331,7 +341,10 @@ cudaError_t gated_mma_backward(const GatedBackward& f, const GatedPlan& p, const
   a.S0 = f.S0;
   a.dS = f.dS;
   a.scratch = static_cast<char*>(w.scratch);
-  return gated_launch<gated_backward_kernel>(kSmem, dim3((unsigned)backward_grid(p)), kThreads, st, a);
+  const dim3 grid((unsigned)backward_grid(p));
+  return gated_fine(p.BH, p.N)
+             ? gated_launch<gated_backward_kernel<true>>(kSmem<true>, grid, kThreads, st, a)
+             : gated_launch<gated_backward_kernel<false>>(kSmem<false>, grid, kThreads, st, a);
 }
 
 }  // namespace la

@@ -280,12 +280,27 @@ __device__ __forceinline__ float2 dot_kept(float4 kept, float (&a)[4], float2 s)
   return fma2(make_float2(kept.z, kept.w), pair_of(a, 1), s);
 }
 
-// A state's rows r0 .. as an operand
-template <int NT>
+// What is left of a, b behind their bf16 pair
+__device__ __forceinline__ float2 rest_of(float2 w, uint32_t hi) { return sub2(w, both_of(hi)); }
+
+// A state's rows r0 .. as an operand, or (REST) what that operand's rounding leaves
+template <bool REST = false, int NT>
 __device__ __forceinline__ void store_op(const Lane<64>& ln, uint32_t op, int r0, int c0,
                                          const float (&x)[NT][4]) {
 #pragma unroll
-  for (int jp = 0; jp < NT / 2; ++jp) ln.store(op, r0, c0 / 16 + jp, x[2 * jp], x[2 * jp + 1]);
+  for (int jp = 0; jp < NT / 2; ++jp) {
+    float y[2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int h = 0; h < 4; h += 2) {
+        const float2 w = make_float2(x[2 * jp + t][h], x[2 * jp + t][h + 1]);
+        const float2 v = REST ? rest_of(w, pack2(w.x, w.y)) : w;
+        y[t][h] = v.x;
+        y[t][h + 1] = v.y;
+      }
+    ln.store(op, r0, c0 / 16 + jp, y[0], y[1]);
+  }
 }
 
 // x += (columns 16 col16.. of tile `a`, weighted along its rows)^T (columns c0.. of tile
@@ -334,9 +349,9 @@ __device__ __forceinline__ void add_outer(const Lane<COLS>& la, const Lane<64>& 
   }
 }
 
-// c = A B for A's fragments of 16 rows by 16 KS and the 64 columns of B, which are the
-// rows of the tile, or (TRANS) B's rows are
-template <bool TRANS, int KS>
+// c = A B, or (ADD) c += A B, for A's fragments of 16 rows by 16 KS and the 64 columns of
+// B, which are the rows of the tile, or (TRANS) B's rows are
+template <bool TRANS, bool ADD = false, int KS>
 __device__ __forceinline__ void product(const Lane<64>& ln, float (&c)[8][4],
                                         const uint32_t (&a)[KS][4], uint32_t tile) {
 #pragma unroll
@@ -348,7 +363,7 @@ __device__ __forceinline__ void product(const Lane<64>& ln, float (&c)[8][4],
         ln.load_b_t(b, tile, 16 * ks, jp);
       else
         ln.load_b(b, tile, 16 * jp, ks);
-      if (ks == 0) {
+      if (ks == 0 && !ADD) {
         mma16816_0(c[2 * jp], a[ks], b[0], b[1]);
         mma16816_0(c[2 * jp + 1], a[ks], b[2], b[3]);
       } else {
@@ -358,12 +373,12 @@ __device__ __forceinline__ void product(const Lane<64>& ln, float (&c)[8][4],
     }
 }
 
-// A block of 16 x 16 of (A B^T) * L as an A operand: A's fragments, B the rows 16 cb.. of
+// A block of 16 x 16 of (A B^T) * L as an A operand of TERMS bf16 terms: A's fragments, B the rows 16 cb.. of
 // a tile, G the chunk's gate sums (gr: of A's rows l / 4 and l / 4 + 8). LOWER: A's rows
 // are the later tokens (L = exp(g_row - g_col)), else B's are. DIAGONAL: the block where
 // both are the same tokens, half of it zero.
-template <bool LOWER, bool DIAGONAL, int COLS, int KS>
-__device__ __forceinline__ void masked_block(const Lane<COLS>& ln, uint32_t (&out)[4],
+template <bool LOWER, bool DIAGONAL, int COLS, int KS, int TERMS>
+__device__ __forceinline__ void masked_block(const Lane<COLS>& ln, uint32_t (&out)[TERMS][4],
                                              const uint32_t (&a)[KS][4], uint32_t tile, int cb,
                                              const float (&gr)[2], const float* G) {
   const int l = threadIdx.x & 31, row = l >> 2, col = (l & 3) * 2;
@@ -393,20 +408,28 @@ __device__ __forceinline__ void masked_block(const Lane<COLS>& ln, uint32_t (&ou
         w.x = (LOWER ? c <= r : c >= r) ? w.x : 0.f;
         w.y = (LOWER ? c + 1 <= r : c + 1 >= r) ? w.y : 0.f;
       }
-      out[2 * t + h] = pack2(w.x, w.y);
+#pragma unroll
+      for (int i = 0; i < TERMS; ++i) {
+        out[i][2 * t + h] = pack2(w.x, w.y);
+        w = rest_of(w, out[i][2 * t + h]);
+      }
     }
   }
 }
 
 // c += the block's product with the rows 16 cb.. of a tile of 64 columns
-__device__ __forceinline__ void add_block(const Lane<64>& ln, float (&c)[8][4], const uint32_t (&a)[4],
-                                          uint32_t tile, int cb) {
+template <int TERMS>
+__device__ __forceinline__ void add_block(const Lane<64>& ln, float (&c)[8][4],
+                                          const uint32_t (&a)[TERMS][4], uint32_t tile, int cb) {
 #pragma unroll
   for (int jp = 0; jp < 4; ++jp) {
     uint32_t b[4];
     ln.load_b_t(b, tile, 16 * cb, jp);
-    mma16816(c[2 * jp], a, b[0], b[1]);
-    mma16816(c[2 * jp + 1], a, b[2], b[3]);
+#pragma unroll
+    for (int i = 0; i < TERMS; ++i) {
+      mma16816(c[2 * jp], a[i], b[0], b[1]);
+      mma16816(c[2 * jp + 1], a[i], b[2], b[3]);
+    }
   }
 }
 

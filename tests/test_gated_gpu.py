@@ -163,6 +163,34 @@ def test_backward(la, shape, dtype, states):
     _backward_close(la, q, k, v, g, do, S0 if states else None, dS if states else None, dtype)
 
 
+@pytest.mark.parametrize("gate", ["mixed", "slow"])
+@pytest.mark.parametrize("shape", [(1, 4, 5, 64, 64), (1, 2, 16, 128, 40), (1, 3, 17, 64, 64),
+                                   (2, 8, 64, 64, 64), (19, 8, 40, 64, 64), (1, 2, 200, 128, 96),
+                                   (1, 1, 700, 40, 72), (1, 2, 90, 8, 128), (1, 4, 1025, 64, 64)],
+                         ids=ids)
+def test_calls_of_few_chunks_show_only_their_outputs_rounding(la, shape, gate):
+    """bf16, up to 152 chunks: no operand is rounded to one bf16 term. A term keeps 16 bits in
+    each of two places (its chunk's operand or state, the state's own update), 2^-16 each."""
+    q, k, v, g, do, S0, dS = _inputs(sum(shape) + 2, *shape, BF, gate)
+    B, H, N, D, M = shape
+    chain, u = N + D + M + 64, HALF[BF]
+    n64 = [_f64(t) for t in (q, k, v, g, do, S0, dS)]
+    size = [np.abs(x) for x in n64]
+    size[3] = n64[3]
+    bound = oracle.gated_backward(*size)
+    dots = np.sum(size[0] * bound[0] + size[1] * bound[1], axis=(-1, -2)) + \
+        np.sum(bound[4], axis=(-1, -2))
+    names = ("out", "dq", "dk", "dv", "dg")
+    outs = (la.la_forward_gated(q, k, v, g, S0=S0), *la.la_backward_gated(q, k, v, g, do, S0=S0, dS=dS)[:4])
+    wants = (oracle.gated_forward(*n64[:4], n64[5])[0], *oracle.gated_backward(*n64)[:4])
+    sizes = (oracle.gated_forward(*size[:4], size[5])[0], *bound[:4])
+    for name, got, want, a in zip(names, outs, wants, sizes):
+        each = u * np.abs(want) + (2.0 ** -15 + chain * F32) * a
+        if name == "dg":
+            each = each + chain * F32 * dots[..., None]
+        assert np.all(np.abs(_f64(got) - want) <= each), name
+
+
 def test_backward_with_only_one_of_the_states(la):
     q, k, v, g, do, S0, dS = _inputs(3, 1, 2, 100, 64, 64, BF)
     _backward_close(la, q, k, v, g, do, S0, None, BF)
