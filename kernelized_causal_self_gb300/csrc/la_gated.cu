@@ -25,11 +25,10 @@
 // with <a S, E> of the segment's two states. It restarts in every segment, so that
 // rounding errors do not pile up over the sequence.
 //
-// B2 H8 N4096 D = M = 64: forward 113 us, backward 281 us, bound by the reads of w and z
-// from shared memory (two 16-byte words for six packed multiply-adds) and their waits.
-// (Tiles of 4 rows by 16 columns a thread, which read a fourth as much, took 115 and 312 us:
-// fewer and longer chains.) One segment of 32 tokens or more each: B2 H4 N777 D32 M48,
-// backward 41 us of kernels, with 64 at least 54.
+// B2 H8 N4096 D = M = 64: forward 113 us, backward 288 us; B16 H16 N512 181 and 410. Bound by
+// the reads of w and z from shared memory (two 16-byte words for six packed multiply-adds) and
+// their waits. (Tiles of 4 rows by 16 columns a thread, which read a fourth as much, took 115
+// and 312 us when this layout took 113 and 281: fewer and longer chains.)
 #include "la_gated.cuh"
 #include "la_gated_mma.cuh"
 #include "la_tc_common.cuh"
@@ -78,6 +77,7 @@ __device__ __forceinline__ void recur_walk(const RecurArgs<T>& a) {
   constexpr int PC = kTok * COLS / kThreads, PR = kTok * RB / kThreads;  // staged per thread
   __shared__ __align__(16) float sw[kTok][COLS], sz[kTok][COLS];
   __shared__ float su[kTok][RB], sy[kTok][RB + 1], sa[kTok], swz[kTok];
+  __shared__ unsigned slow_tokens;  // bit t: sa[t] is exp(g_t) - 1, else exp(g_t)
   const int tid = threadIdx.x, part = tid % CP, row = tid / CP;
   const int bh = blockIdx.x / a.n_seg, seg = blockIdx.x % a.n_seg;
   const int r0 = blockIdx.y * RB, nr = min(RB, a.NR - r0);
@@ -135,7 +135,8 @@ __device__ __forceinline__ void recur_walk(const RecurArgs<T>& a) {
       (&x[2 * i + j / 2].x)[j % 2] = in ? xin[(size_t)(r0 + row) * a.rs + (size_t)c * a.cs] : 0.f;
     }
 
-  float decay = 1.f, end = 0.f;
+  float end = 0.f;
+  double gates = 0.0;  // a token of each tile (a product of float32 factors drifts by its roundings)
   for (int done = 0; done < te - tb; done += kTok) {
     int t0;
     const int m = tile(done, t0);
@@ -151,7 +152,15 @@ __device__ __forceinline__ void recur_walk(const RecurArgs<T>& a) {
       const int at = tid + i * kThreads;
       su[at / RB][at % RB] = nu[i];
     }
-    if (tid < kTok) sa[tid] = gated_decay(ng);
+    if (tid < 32) {
+      const bool slow = tid < kTok && ng > -0.5f && ng < 0.5f;
+      if (tid < kTok) {
+        sa[tid] = slow ? expm1f(ng) : expf(ng);
+        gates += (double)ng;
+      }
+      const unsigned bits = __ballot_sync(0xffffffffu, slow);
+      if (tid == 0) slow_tokens = bits;
+    }
     __syncthreads();
     if (done + kTok < te - tb) fetch(done + kTok);
     if (a.y) {  // w_t . z_t, eight threads a token
@@ -161,10 +170,27 @@ __device__ __forceinline__ void recur_walk(const RecurArgs<T>& a) {
       for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       if (tid % 8 == 0) swz[tid / 8] = s;
     }
+    const unsigned slow_bits = slow_tokens;
     for (int k = 0; k < m; ++k) {
       const int t = REV ? m - 1 - k : k;
+      const bool slow = slow_bits >> t & 1;
       const float at = sa[t], ut = su[t][row];
       const float2 a2 = make_float2(at, at), u2 = make_float2(ut, ut);
+      // X + X (exp(g) - 1) near 1: exp(g) itself would keep too little of g, and with the same
+      // gate at every token its rounding does not average out (1200 tokens of g = -3.1e-4:
+      // final states off by 5.0e-6 instead of 8e-7). A branch a token, forward 5 to 10%.
+      // Measured and not kept: X c + X e with c 0 or 1 (forward 14%, backward 10%), both
+      // factors by predicates (spills; 20 to 30%), a loop of its own for tiles of slow gates
+      // (spills; no faster than the branch).
+      auto forget = [&]() {
+        if (slow) {
+#pragma unroll
+          for (int i = 0; i < kCols / 2; ++i) x[i] = fma2(a2, x[i], x[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kCols / 2; ++i) x[i] = mul2(a2, x[i]);
+        }
+      };
       if (!REV && a.E && t0 + t == te - 1) {
         const float* E = a.E + (a.seg_in ? (size_t)bh * (a.n_seg + 1) + seg + 1 : bh) * a.DM;
         if (row < nr)
@@ -174,19 +200,16 @@ __device__ __forceinline__ void recur_walk(const RecurArgs<T>& a) {
             for (int j = 0; j < 4; ++j) {
               const int c = 4 * (i * CP + part) + j;
               if (c < a.NC)
-                end = fmaf(at * (&x[2 * i + j / 2].x)[j % 2],
+                end = fmaf((slow ? 1.f + at : at) * (&x[2 * i + j / 2].x)[j % 2],
                            E[(size_t)(r0 + row) * a.rs + (size_t)c * a.cs], end);
             }
       }
+      if (!REV) forget();
       float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < kCols / 4; ++i) {
         const int c = 4 * (i * CP + part);
         const float4 wv = *reinterpret_cast<const float4*>(&sw[t][c]);
-        if (!REV) {
-          x[2 * i] = mul2(a2, x[2 * i]);
-          x[2 * i + 1] = mul2(a2, x[2 * i + 1]);
-        }
         if (a.y) {
           const float4 zv = *reinterpret_cast<const float4*>(&sz[t][c]);
           s2 = fma2(x[2 * i], make_float2(zv.x, zv.y), s2);
@@ -194,12 +217,8 @@ __device__ __forceinline__ void recur_walk(const RecurArgs<T>& a) {
         }
         x[2 * i] = fma2(u2, make_float2(wv.x, wv.y), x[2 * i]);
         x[2 * i + 1] = fma2(u2, make_float2(wv.z, wv.w), x[2 * i + 1]);
-        if (REV) {
-          x[2 * i] = mul2(a2, x[2 * i]);
-          x[2 * i + 1] = mul2(a2, x[2 * i + 1]);
-        }
       }
-      decay *= at;
+      if (REV) forget();
       if (a.y) {
         float s = s2.x + s2.y;
 #pragma unroll
@@ -249,7 +268,11 @@ __device__ __forceinline__ void recur_walk(const RecurArgs<T>& a) {
         const int c = 4 * (i * CP + part) + j;
         if (c < a.NC) xout[(size_t)(r0 + row) * a.rs + (size_t)c * a.cs] = (&x[2 * i + j / 2].x)[j % 2];
       }
-  if (a.decay && blockIdx.y == 0 && tid == 0) a.decay[(size_t)bh * a.n_seg + seg] = decay;
+  if (a.decay && blockIdx.y == 0 && tid < 32) {
+#pragma unroll
+    for (int o = kTok / 2; o > 0; o >>= 1) gates += __shfl_down_sync(0xffffffffu, gates, o);
+    if (tid == 0) a.decay[(size_t)bh * a.n_seg + seg] = gated_decay((float)gates);
+  }
 }
 
 // blockIdx.z: one of up to three walks that do not depend on each other
@@ -398,8 +421,8 @@ float walk_time(long long ctas, int per_sm, int len) {
 // The segments with which the walks take least: several fill the GPU, but cost the state
 // passes (0.65 of a walk of outputs) and the scan first. At least 32 tokens each, a
 // backward's at most 512, over which dg's sum from the segment's end back keeps float32's
-// accuracy. 128 tokens, D = M = 64: backward of 8 sequences 4 segments 29 us, one 45; of 152
-// 109 and 68, of 600 363 and 212. Forward of 60 sequences 28 and 36, of 600 143 and 67.
+// accuracy. 128 tokens, D = M = 64, several segments and one: backward of 8 sequences 29 and
+// 45 us, of 152 109 and 68, of 600 363 and 212; forward of 60 28 and 36, of 600 143 and 67.
 GatedPlan plan_simt(int BH, int N, int D, int M, bool backward) {
   const int cp = column_parts(D, M), per_sm = cp == 2 ? 4 : 3;
   const long long per = (long long)BH * row_blocks(D > M ? D : M, cp);
@@ -665,9 +688,9 @@ size_t gated_forward_workspace(int BH, int N, int D, int M, int dtype) {
 }
 
 // A backward of a few tokens does too: the tensor cores' chunks cost the same for 1 token
-// as for 64. D = M = 64, 1 and 512 sequences of 4 tokens 9.5 and 30 us (on the tensor cores
-// 10.2 and 60), of 16 tokens 13 and 44 (10 and 60), of 32 tokens 19 and 66; 128: 9.6 and 114
-// (24 and 289), 14 and 211, 22 and 367.
+// as for 64. D = M = 64, 1 and 512 sequences of 4 tokens 10 and 30 us (on the tensor cores
+// 11 and 60), of 16 tokens 14 and 45 (11 and 60), of 32 tokens 19 and 66; D = M = 128: 10 and
+// 115 (26 and 289), 15 and 209 (26 and 291), 22 and 367 (26 and 295).
 constexpr int kShort = 16;
 static bool backward_walks(int N, int dtype) { return dtype == LA_F32 || N <= kShort; }
 

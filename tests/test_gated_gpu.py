@@ -226,6 +226,28 @@ def test_backward_against_differences_of_the_forward(la):
         assert abs(diff - want) <= 2.0 ** -10 * size + 2.0 ** -15 * scale, (i, diff, want)
 
 
+def test_the_same_slow_gate_at_every_token(la):
+    """float32. A state is rounded twice a token (the decay, the outer product), each time by at
+    most half a step, 2-norm 2^-24 / sqrt(3), of either sign: sqrt(2 N) of those over N tokens
+    that it hardly forgets, and sqrt(D + M) more in an output. A rounded exp(g) would be off the
+    same way at every token: up to N 2^-25."""
+    B, H, N, D, M = 13, 16, 1200, 32, 32
+    q, k, v, _, do, S0, dS = _inputs(8, B, H, N, D, M, FL)
+    g = torch.full((B, H, N), -3.1e-4, device=DEV)
+    out, S = la.la_prefill_gated(q, k, v, g, S0=S0)
+    grads = la.la_backward_gated(q, k, v, g, do, S0=S0, dS=dS)
+    want, wS = oracle.gated_forward(*map(_f64, (q, k, v, g, S0)))
+    wants = oracle.gated_backward(*map(_f64, (q, k, v, g, do, S0, dS)))
+    step = F32 / 3 ** 0.5
+    for name, o, w, count in (("out", out, want, 2 * N + D + M), ("S", S, wS, 2 * N),
+                              ("dq", grads[0], wants[0], 2 * N + D + M),
+                              ("dk", grads[1], wants[1], 2 * N + D + M),
+                              ("dv", grads[2], wants[2], 2 * N + D + M),
+                              ("dS0", grads[4], wants[4], 2 * N)):
+        rel = np.linalg.norm(_f64(o) - w) / np.linalg.norm(w)
+        assert rel <= count ** 0.5 * step, (name, rel)
+
+
 # ------------------------------------------------------------------------ serving
 
 @pytest.mark.parametrize("dtype", [BF, FL], ids=["bf16", "f32"])
