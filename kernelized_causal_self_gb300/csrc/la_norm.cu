@@ -188,13 +188,13 @@ __global__ void __launch_bounds__(kThreads) norm_gate_kernel(const NormArgs a) {
 }
 
 // dw: sums of the CTAs' sums, one head's (w [H][M]) or all heads' (w [M]). 32
-// columns by 32 strided rows a CTA.
+// columns (blockIdx.y) of a head (blockIdx.x) by 32 strided rows a CTA.
 template <typename T>
 __global__ void __launch_bounds__(1024)
 norm_dw_kernel(const float* __restrict__ partial, T* __restrict__ dw, int rows, int M) {
   __shared__ float sums[32][33];
-  const int m = blockIdx.x * 32 + threadIdx.x;
-  const float* p = partial + (size_t)blockIdx.y * rows * M;
+  const int m = blockIdx.y * 32 + threadIdx.x;
+  const float* p = partial + (size_t)blockIdx.x * rows * M;
   tc::pdl_wait();
   float s = 0.f;
   if (m < M)
@@ -203,7 +203,7 @@ norm_dw_kernel(const float* __restrict__ partial, T* __restrict__ dw, int rows, 
   __syncthreads();
   if (threadIdx.y == 0 && m < M) {
     for (int i = 1; i < 32; ++i) s += sums[i][threadIdx.x];
-    dw[(size_t)blockIdx.y * M + m] = from_f32<T>(s);
+    dw[(size_t)blockIdx.x * M + m] = from_f32<T>(s);
   }
 }
 
@@ -276,7 +276,7 @@ cudaError_t norm_gate_backward(const NormGate& n, void* ws, cudaStream_t st) {
       n.dtype == LA_F32 ? launch<float, true>(a, st) : launch<__nv_bfloat16, true>(a, st);
   if (e != cudaSuccess) return e;
   const int rows = n.w_per_head ? a.tiles : a.tiles * n.H;
-  const dim3 grid((n.M + 31) / 32, n.w_per_head ? n.H : 1), block(32, 32);
+  const dim3 grid(n.w_per_head ? n.H : 1, (n.M + 31) / 32), block(32, 32);
   const float* partial = a.partial;
   e = n.dtype == LA_F32
           ? tcx::launch_pdl(norm_dw_kernel<float>, grid, block, 0, st, partial, (float*)n.dw, rows, n.M)

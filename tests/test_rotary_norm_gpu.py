@@ -197,6 +197,15 @@ def test_norm_gate_and_gradients(la, shape, dtype, heads, token_major):
         assert torch.equal(a, b)
 
 
+def test_norm_gate_of_more_heads_than_a_grid_is_high(la):
+    """w's gradient per head: one term each, dy n z s; a dozen float32 operations."""
+    x, z, w, dy = _norm_inputs(4, 1, 70001, 1, 8, FL, True, False)
+    dw = la.la_norm_gate_backward(x, z, w, dy)[2]
+    want = oracle.norm_gate_backward(*map(_f64, (x, z, w, dy)))[2]
+    grow = (8 + 64 + 8 * np.abs(_f64(z))[0, :, 0]) * 2.0 ** -24
+    assert np.all(np.abs(_f64(dw) - want) <= grow * np.abs(want) + 1e-37)
+
+
 def test_norm_gate_edges(la):
     x, z, w, dy = _norm_inputs(1, 2, 2, 6, 64, FL, False, False)
     e = x[:, :, :0].contiguous()
