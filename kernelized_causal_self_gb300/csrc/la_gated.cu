@@ -41,7 +41,6 @@ using tcx::mul2;
 
 constexpr int kThreads = 128;
 constexpr int kTok = 16;       // tokens staged at a time
-constexpr int kCols = 32;      // columns of X per thread
 
 template <typename T>
 struct RecurArgs {
@@ -68,14 +67,14 @@ struct RecurArgs {
   WorkspaceHeader* hdr;
 };
 
-// CP threads share a row, each with 32 of its columns (c = 4 (i CP + p) + 0..3, so
+// CP threads share a row, each with COLS of its columns (c = 4 (i CP + p) + 0..3, so
 // that the lanes of a warp read neighbouring 16-byte words). 16 tokens are staged at a
 // time, the next 16 on their way in registers meanwhile.
-template <int CP, bool REV, typename T>
+template <int CP, int COLS, bool REV, typename T>
 __device__ __forceinline__ void recur_walk(const RecurArgs<T>& a) {
-  constexpr int RB = kThreads / CP, COLS = kCols * CP;
-  constexpr int PC = kTok * COLS / kThreads, PR = kTok * RB / kThreads;  // staged per thread
-  __shared__ __align__(16) float sw[kTok][COLS], sz[kTok][COLS];
+  constexpr int RB = kThreads / CP, ALL = COLS * CP;
+  constexpr int PC = kTok * ALL / kThreads, PR = kTok * RB / kThreads;  // staged per thread
+  __shared__ __align__(16) float sw[kTok][ALL], sz[kTok][ALL];
   __shared__ float su[kTok][RB], sy[kTok][RB + 1], sa[kTok], swz[kTok];
   __shared__ unsigned slow_tokens;  // bit t: sa[t] is exp(g_t) - 1, else exp(g_t)
   const int tid = threadIdx.x, part = tid % CP, row = tid / CP;
@@ -103,7 +102,7 @@ __device__ __forceinline__ void recur_walk(const RecurArgs<T>& a) {
     const int m = tile(done, t0);
 #pragma unroll
     for (int i = 0; i < PC; ++i) {
-      const int at = tid + i * kThreads, t = at / COLS, c = at % COLS;
+      const int at = tid + i * kThreads, t = at / ALL, c = at % ALL;
       const bool in = t < m && c < a.NC;
       nw[i] = in ? to_f32<T>(w[(size_t)(t0 + t) * a.NC + c]) : 0.f;
       nz[i] = in && a.y ? to_f32<T>(z[(size_t)(t0 + t) * a.NC + c]) : 0.f;
@@ -125,9 +124,9 @@ __device__ __forceinline__ void recur_walk(const RecurArgs<T>& a) {
     xin = a.seg_in + ((size_t)bh * (a.n_seg + 1) + seg + (REV ? 1 : 0)) * a.DM;
   else if (a.init && entry >= 0)
     xin = a.init + (size_t)entry * a.DM;
-  float2 x[kCols / 2];
+  float2 x[COLS / 2];
 #pragma unroll
-  for (int i = 0; i < kCols / 4; ++i)
+  for (int i = 0; i < COLS / 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int c = 4 * (i * CP + part) + j;
@@ -144,8 +143,8 @@ __device__ __forceinline__ void recur_walk(const RecurArgs<T>& a) {
 #pragma unroll
     for (int i = 0; i < PC; ++i) {
       const int at = tid + i * kThreads;
-      sw[at / COLS][at % COLS] = nw[i];
-      sz[at / COLS][at % COLS] = nz[i];
+      sw[at / ALL][at % ALL] = nw[i];
+      sz[at / ALL][at % ALL] = nz[i];
     }
 #pragma unroll
     for (int i = 0; i < PR; ++i) {
@@ -185,17 +184,17 @@ __device__ __forceinline__ void recur_walk(const RecurArgs<T>& a) {
       auto forget = [&]() {
         if (slow) {
 #pragma unroll
-          for (int i = 0; i < kCols / 2; ++i) x[i] = fma2(a2, x[i], x[i]);
+          for (int i = 0; i < COLS / 2; ++i) x[i] = fma2(a2, x[i], x[i]);
         } else {
 #pragma unroll
-          for (int i = 0; i < kCols / 2; ++i) x[i] = mul2(a2, x[i]);
+          for (int i = 0; i < COLS / 2; ++i) x[i] = mul2(a2, x[i]);
         }
       };
       if (!REV && a.E && t0 + t == te - 1) {
         const float* E = a.E + (a.seg_in ? (size_t)bh * (a.n_seg + 1) + seg + 1 : bh) * a.DM;
         if (row < nr)
 #pragma unroll
-          for (int i = 0; i < kCols / 4; ++i)
+          for (int i = 0; i < COLS / 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int c = 4 * (i * CP + part) + j;
@@ -207,7 +206,7 @@ __device__ __forceinline__ void recur_walk(const RecurArgs<T>& a) {
       if (!REV) forget();
       float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < kCols / 4; ++i) {
+      for (int i = 0; i < COLS / 4; ++i) {
         const int c = 4 * (i * CP + part);
         const float4 wv = *reinterpret_cast<const float4*>(&sw[t][c]);
         if (a.y) {
@@ -262,7 +261,7 @@ __device__ __forceinline__ void recur_walk(const RecurArgs<T>& a) {
     xout = a.fin + (size_t)entry * a.DM;
   if (xout && row < nr)
 #pragma unroll
-    for (int i = 0; i < kCols / 4; ++i)
+    for (int i = 0; i < COLS / 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = 4 * (i * CP + part) + j;
@@ -275,20 +274,22 @@ __device__ __forceinline__ void recur_walk(const RecurArgs<T>& a) {
   }
 }
 
+constexpr int walks_per_sm(int cp, int cols) { return cols == 8 ? 5 : cp == 2 || cols < 32 ? 4 : 3; }
+
 // blockIdx.z: one of up to three walks that do not depend on each other
 template <typename T>
 struct RecurJobs {
   RecurArgs<T> job[3];
 };
-template <int CP, typename T>
-__global__ void __launch_bounds__(kThreads, CP == 2 ? 4 : 3)
+template <int CP, int COLS, typename T>
+__global__ void __launch_bounds__(kThreads, walks_per_sm(CP, COLS))
 gated_recur_kernel(const __grid_constant__ RecurJobs<T> jobs) {
   const RecurArgs<T>& a = jobs.job[blockIdx.z];
   tc::pdl_wait();
   if (a.reverse)
-    recur_walk<CP, true, T>(a);
+    recur_walk<CP, COLS, true, T>(a);
   else
-    recur_walk<CP, false, T>(a);
+    recur_walk<CP, COLS, false, T>(a);
 }
 
 // Joins the segments: forward X[s + 1] = decay[s] X[s] + U[s] from X[0] = init,
@@ -390,10 +391,23 @@ gated_dg_kernel(const float* __restrict__ ends, const float* __restrict__ dot_q,
   }
 }
 
-// threads per row: the widest of a call's states decides, so that its walks share launches
-int column_parts(int D, int M) {
+// Threads per row and columns per thread: the widest of a call's states decides, so that its
+// walks share launches. Few columns and rows are left idle, and more than 16 columns a thread
+// pay where there are as many (two threads of 32 for 64: 500 tokens of 60 sequences forward 74
+// us, four of 16 95). Against 32 columns for all: D = M = 32, 600 sequences of 300 tokens
+// forward 186 to 92 us, backward 487 to 285; 48, 60 sequences 40 to 35 and 96 to 83; 72, 60
+// sequences of 500 tokens 216 to 165 and 498 to 265.
+struct Columns {
+  int parts, each;
+};
+Columns columns(int D, int M) {
   const int nc = D > M ? D : M;
-  return nc <= kCols ? 1 : nc <= 2 * kCols ? 2 : 4;
+  return nc <= 32   ? Columns{4, 8}
+         : nc <= 48 ? Columns{2, 24}
+         : nc <= 64 ? Columns{2, 32}
+         : nc <= 80 ? Columns{4, 20}
+         : nc <= 96 ? Columns{4, 24}
+                    : Columns{4, 32};
 }
 
 int row_blocks(int NR, int cp) { return (NR * cp + kThreads - 1) / kThreads; }
@@ -401,11 +415,15 @@ int row_blocks(int NR, int cp) { return (NR * cp + kThreads - 1) / kThreads; }
 template <typename T>
 cudaError_t launch_recur(const RecurJobs<T>& jobs, int count, int D, int M, cudaStream_t st) {
   const RecurArgs<T>& a = jobs.job[0];
-  const int cp = column_parts(D, M);
-  const dim3 grid((unsigned)(a.BH * a.n_seg), (unsigned)row_blocks(D > M ? D : M, cp), count);
-  const cudaError_t e = cp == 1   ? tcx::launch_pdl(gated_recur_kernel<1, T>, grid, dim3(kThreads), 0, st, jobs)
-                        : cp == 2 ? tcx::launch_pdl(gated_recur_kernel<2, T>, grid, dim3(kThreads), 0, st, jobs)
-                                  : tcx::launch_pdl(gated_recur_kernel<4, T>, grid, dim3(kThreads), 0, st, jobs);
+  const Columns c = columns(D, M);
+  const dim3 grid((unsigned)(a.BH * a.n_seg), (unsigned)row_blocks(D > M ? D : M, c.parts), count);
+  auto launch = [&](auto kernel) { return tcx::launch_pdl(kernel, grid, dim3(kThreads), 0, st, jobs); };
+  const cudaError_t e = c.each == 8    ? launch(gated_recur_kernel<4, 8, T>)
+                        : c.each == 20 ? launch(gated_recur_kernel<4, 20, T>)
+                        : c.parts == 2 ? c.each == 24 ? launch(gated_recur_kernel<2, 24, T>)
+                                                      : launch(gated_recur_kernel<2, 32, T>)
+                        : c.each == 24 ? launch(gated_recur_kernel<4, 24, T>)
+                                       : launch(gated_recur_kernel<4, 32, T>);
   count_launches(1);
   return e;
 }
@@ -424,8 +442,9 @@ float walk_time(long long ctas, int per_sm, int len) {
 // accuracy. 128 tokens, D = M = 64, several segments and one: backward of 8 sequences 29 and
 // 45 us, of 152 109 and 68, of 600 363 and 212; forward of 60 28 and 36, of 600 143 and 67.
 GatedPlan plan_simt(int BH, int N, int D, int M, bool backward) {
-  const int cp = column_parts(D, M), per_sm = cp == 2 ? 4 : 3;
-  const long long per = (long long)BH * row_blocks(D > M ? D : M, cp);
+  const Columns c = columns(D, M);
+  const int per_sm = walks_per_sm(c.parts, c.each);
+  const long long per = (long long)BH * row_blocks(D > M ? D : M, c.parts);
   const long long most = N > 0 ? (N + 31) / 32 : 1, fewest = backward && N > 512 ? (N + 511) / 512 : 1;
   GatedPlan best{BH, N, kTok, 1};
   float shortest = -1.f;
@@ -518,7 +537,7 @@ cudaError_t simt_forward(const GatedForward& f, const GatedPlan& p, const GatedW
   return launch_recur(jobs, 1, f.D, f.M, st);
 }
 
-int backward_dots(int D, int M) { return row_blocks(D, column_parts(D, M)); }
+int backward_dots(int D, int M) { return row_blocks(D, columns(D, M).parts); }
 
 template <typename T>
 cudaError_t simt_backward(const GatedBackward& f, const GatedPlan& p, const GatedWorkspace& w,

@@ -191,6 +191,20 @@ def test_calls_of_few_chunks_show_only_their_outputs_rounding(la, shape, gate):
         assert np.all(np.abs(_f64(got) - want) <= each), name
 
 
+@pytest.mark.parametrize("dims", [(8, 8), (32, 24), (16, 48), (56, 64), (80, 72), (96, 88), (104, 8)],
+                         ids=str)
+def test_float32_heads_of_every_width(la, dims):
+    for B, H, N in ((1, 2, 33), (2, 1, 600), (40, 16, 40)):
+        D, M = dims
+        q, k, v, g, do, S0, dS = _inputs(D + N, B, H, N, D, M, FL)
+        out, S = la.la_prefill_gated(q, k, v, g, S0=S0)
+        want, wS = oracle.gated_forward(*map(_f64, (q, k, v, g, S0)))
+        ao, aS = oracle.gated_forward(*_abs(q, k, v), _f64(g), np.abs(_f64(S0)))
+        _close(out, want, ao, FL, N + D + M + 64, "out")
+        _close(S, wS, aS, FL, N + D + M + 64, "S", state=True)
+        _backward_close(la, q, k, v, g, do, S0, dS, FL)
+
+
 def test_backward_with_only_one_of_the_states(la):
     q, k, v, g, do, S0, dS = _inputs(3, 1, 2, 100, 64, 64, BF)
     _backward_close(la, q, k, v, g, do, S0, None, BF)
