@@ -406,7 +406,8 @@ size_t la_gated_workspace_bytes(int B, int H, int N, int D, int M, int dtype);
 
 /*
  * la_forward_gated -- out of N tokens, from the state S0 (float32 [B][H][D][M];
- * nullptr: zero), and the state after them in S (nullptr: not wanted). S may be S0.
+ * nullptr: zero), and the state after them in S (nullptr: not wanted). S may be S0, but
+ * not overlap it otherwise.
  * N == 0 copies S0 (or zero) to S.
  */
 int la_forward_gated(const void* q, const void* k, const void* v, const void* g, void* out,
@@ -443,8 +444,8 @@ size_t la_gated_backward_workspace_bytes(int B, int H, int N, int D, int M, int 
  * that la_forward_gated gives for q, k, v, g, S0. dS: nullptr for zero. dq, dk
  * [B][H][N][D], dv [B][H][N][M] and dg [B][H][N] in `dtype` (unlike la_backward's,
  * which are float32: these are added to leaves of the inputs' type); dS0 float32
- * [B][H][D][M], nullptr if not wanted. Nothing of the forward is needed: states are
- * recomputed. N == 0 copies dS (or zero) to dS0.
+ * [B][H][D][M], nullptr if not wanted; it may be dS, but not overlap it otherwise, nor S0
+ * at all. Nothing of the forward is needed: states are recomputed. N == 0 copies dS (or zero) to dS0.
  */
 int la_backward_gated(const void* q, const void* k, const void* v, const void* g, const void* dout,
                       const float* S0, const float* dS, void* dq, void* dk, void* dv, void* dg,

@@ -700,6 +700,13 @@ def _check_gated(fn, q, k, v, g, rank):
     return dims, _dtype_code(q)
 
 
+def _apart(fn, name, t, other, o, same_ok):
+    """Two float32 states do not share memory (same_ok: or are the same)."""
+    at, to = t.data_ptr(), o.data_ptr()
+    if abs(at - to) < 4 * t.numel() and not (same_ok and at == to):
+        raise ValueError(f"{fn}: {name} shares memory with {other}")
+
+
 def _forward_gated(fn, q, k, v, g, S0, out, S, want_state, workspace):
     import torch
     (B, H, N, D, M), dt = _check_gated(fn, q, k, v, g, 4)
@@ -708,6 +715,8 @@ def _forward_gated(fn, q, k, v, g, S0, out, S, want_state, workspace):
         if t is not None:
             _expect(fn, name, t, (B, H, D, M), torch.float32)
             given.append(t)
+    if S0 is not None and S is not None:
+        _apart(fn, "S", S, "S0", S0, True)
     if out is not None:
         _expect(fn, "out", out, v.shape, q.dtype)
         given.append(out)
@@ -811,7 +820,8 @@ def la_backward_gated(q, k, v, g, dout, S0=None, dS=None, dq=None, dk=None, dv=N
     """Gradients of sum(dout * out) + sum(dS * S) of la_prefill_gated(q, k, v, g, S0): (dq, dk,
     dv, dg) in the inputs' dtype, and dS0 [B,H,D,M] (float32) behind them if S0 is given.
 
-    dS [B,H,D,M] float32: the gradient with respect to the final state (None: zero)."""
+    dS [B,H,D,M] float32: the gradient with respect to the final state (None: zero). dS0 may be
+    dS itself."""
     import torch
     fn, f32 = "la_backward_gated", torch.float32
     (B, H, N, D, M), dt = _check_gated(fn, q, k, v, g, 4)
@@ -822,8 +832,12 @@ def la_backward_gated(q, k, v, g, dout, S0=None, dS=None, dq=None, dk=None, dv=N
         if t is not None:
             _expect(fn, name, t, (B, H, D, M), f32)
             given.append(t)
-    if dS0 is not None and S0 is None:
-        raise ValueError(f"{fn}: dS0 without S0")
+    if dS0 is not None:
+        if S0 is None:
+            raise ValueError(f"{fn}: dS0 without S0")
+        _apart(fn, "dS0", dS0, "S0", S0, False)
+        if dS is not None:
+            _apart(fn, "dS0", dS0, "dS", dS, True)
     for name, t, like in (("dq", dq, q), ("dk", dk, q), ("dv", dv, v), ("dg", dg, g)):
         if t is not None:
             _expect(fn, name, t, like.shape, q.dtype)

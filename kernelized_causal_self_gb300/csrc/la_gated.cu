@@ -558,9 +558,9 @@ cudaError_t simt_backward(const GatedBackward& f, const GatedPlan& p, const Gate
   a.NC = f.M;
   a.rs = f.M;
   a.cs = 1;
-  // One segment starts from the caller's states (unless dS0 is laid over one that the
+  // One segment starts from the caller's states (unless dS0 takes the place of dS, which the
   // other walks still read).
-  const bool whole = p.n_seg == 1 && (f.dS0 == nullptr || (f.dS0 != f.dS && f.dS0 != f.S0));
+  const bool whole = p.n_seg == 1 && (f.dS0 == nullptr || f.dS0 != f.dS);
   cudaError_t e;
   if (!whole) {  // the segments' own states and gradients
     RecurJobs<T> states{{a, a, a}};

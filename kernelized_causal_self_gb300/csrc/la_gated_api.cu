@@ -35,6 +35,13 @@ bool strides_ok(const long long* s, int per) {
   return s != nullptr && s[0] % per == 0 && s[1] % per == 0 && s[2] % per == 0;
 }
 
+// Whether two arrays of float32 states share memory without being the same array.
+bool overlap(const float* a, const float* b, size_t floats) {
+  if (a == nullptr || b == nullptr || a == b) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return (x > y ? x - y : y - x) < sizeof(float) * floats;
+}
+
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? LA_OK : LA_ERR_CUDA; }
 
 cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
@@ -66,6 +73,7 @@ int la_forward_gated(const void* q, const void* k, const void* v, const void* g,
                      void* workspace, size_t workspace_bytes, void* stream) {
   if (!gated_ok(B, H, N, D, M, dtype)) return LA_ERR_INVALID_ARG;
   if (!aligned(S0, 16) || !aligned(S, 16)) return LA_ERR_INVALID_ARG;
+  if (overlap(S0, S, (size_t)B * H * D * M)) return LA_ERR_INVALID_ARG;
   cudaStream_t st = as_stream(stream);
   if (N == 0) return copy_state(S, S0, (size_t)B * H * D * M, st);
   if (!ptrs_ok({q, k, v, g, out})) return LA_ERR_INVALID_ARG;
@@ -114,6 +122,11 @@ int la_backward_gated(const void* q, const void* k, const void* v, const void* g
                       size_t workspace_bytes, void* stream) {
   if (!gated_ok(B, H, N, D, M, dtype)) return LA_ERR_INVALID_ARG;
   if (!aligned(S0, 16) || !aligned(dS, 16) || !aligned(dS0, 16)) return LA_ERR_INVALID_ARG;
+  // dS0 is written while S0 is still read from (the states and their gradients are joined at
+  // once); each element of dS is read by the thread that writes its dS0.
+  const size_t floats = (size_t)B * H * D * M;
+  if ((dS0 != nullptr && dS0 == S0) || overlap(dS0, S0, floats) || overlap(dS0, dS, floats))
+    return LA_ERR_INVALID_ARG;
   cudaStream_t st = as_stream(stream);
   if (N == 0) return copy_state(dS0, dS, (size_t)B * H * D * M, st);
   if (!ptrs_ok({q, k, v, g, dout, dq, dk, dv, dg})) return LA_ERR_INVALID_ARG;

@@ -183,6 +183,43 @@ def test_abi_refuses_before_a_launch(lib):
     assert nback(dw=0) == bad and nback(dy=0) == bad and nback(w=0) == ws and nback(wb=300) == ws
 
 
+def test_abi_refuses_states_that_share_memory(lib):
+    """A gradient of the initial state may take the place of the final state's gradient, and a final
+    state that of the initial one, but no other two of them may touch: the walks from the two ends
+    run at once."""
+    bad, bytes_ = la.LA_ERR_INVALID_ARG, 4 * 3 * 16 * 8
+    far = FAKE + bytes_
+
+    def back(S0, dS, dS0, N=40, dt=1):
+        return lib.la_backward_gated(FAKE, FAKE, FAKE, FAKE, FAKE, S0, dS, FAKE, FAKE, FAKE, FAKE, dS0,
+                                     1, 3, N, 16, 8, dt, FAKE, 16, None)
+
+    for dt in (0, 1):
+        for N in (1, 40, 4000):
+            assert back(FAKE, None, FAKE, N, dt) == bad and back(FAKE, far, FAKE, N, dt) == bad
+            assert back(FAKE, None, FAKE + 16, N, dt) == bad and back(FAKE + 16, None, FAKE, N, dt) == bad
+            assert back(FAKE, None, far - 16, N, dt) == bad and back(None, FAKE, FAKE + 16, N, dt) == bad
+            # (a workspace that is too small is the next refusal)
+            assert back(FAKE, None, far, N, dt) == la.LA_ERR_WORKSPACE
+            assert back(far, FAKE, FAKE, N, dt) == la.LA_ERR_WORKSPACE
+
+    def fwd(S0, S):
+        return lib.la_forward_gated(FAKE, FAKE, FAKE, FAKE, FAKE, S0, S, 1, 3, 4000, 16, 8, 1, FAKE, 16, None)
+    assert fwd(FAKE, FAKE + 16) == bad and fwd(far - 16, FAKE) == bad
+    assert fwd(FAKE, FAKE) == la.LA_ERR_WORKSPACE and fwd(FAKE, far) == la.LA_ERR_WORKSPACE
+
+
+def test_binding_refuses_states_that_share_memory():
+    q, v, g, S = _t(2, 3, 10, 16), _t(2, 3, 10, 8), _t(2, 3, 10), _t(3, 3, 16, 8, dtype=F32)
+    _raises("dS0 shares memory with S0", la.la_backward_gated, q, q, v, g, v, S0=S[:2], dS0=S[:2])
+    _raises("dS0 shares memory with S0", la.la_backward_gated, q, q, v, g, v, S0=S[:2], dS0=S[1:])
+    _raises("dS0 shares memory with dS", la.la_backward_gated, q, q, v, g, v, S0=_t(2, 3, 16, 8, dtype=F32),
+            dS=S[:2], dS0=S[1:])
+    _raises("S shares memory with S0", la.la_prefill_gated, q, q, v, g, S0=S[:2], S=S[1:])
+    _raises("CUDA device", la.la_prefill_gated, q, q, v, g, S0=S[:2], S=S[:2])
+    _raises("CUDA device", la.la_backward_gated, q, q, v, g, v, S0=_t(2, 3, 16, 8, dtype=F32), dS=S[:2], dS0=S[:2])
+
+
 def test_workspace_queries_of_shapes_that_are_refused(lib):
     assert la.la_gated_workspace_bytes(0, 1, 1, 64, 64) == 256
     assert la.la_gated_backward_workspace_bytes(1, 1, 8, 63, 64) == 256

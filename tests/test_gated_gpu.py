@@ -351,6 +351,28 @@ def test_final_state_may_replace_the_initial_one(la):
         assert S2 is both and torch.equal(S2, S) and torch.equal(out2, out)
 
 
+@pytest.mark.parametrize("dtype", [BF, FL], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 2, 7, 64, 64), (2, 40, 20, 32, 48), (2, 3, 700, 64, 64), (1, 2, 300, 128, 96)],
+                         ids=ids)
+def test_initial_states_gradient_may_replace_the_final_ones(la, shape, dtype):
+    q, k, v, g, do, S0, dS = _inputs(sum(shape) + 5, *shape, dtype)
+    want = la.la_backward_gated(q, k, v, g, do, S0, dS)
+    both = dS.clone()
+    got = la.la_backward_gated(q, k, v, g, do, S0, both, dS0=both)
+    assert got[4] is both
+    B, H, N, D, M = shape
+    n64 = [_f64(t) for t in (q, k, v, g, do, S0, dS)]
+    size = [np.abs(x) for x in n64]
+    size[3] = n64[3]
+    bound = oracle.gated_backward(*size)
+    for name, a, b, x in zip(("dq", "dk", "dv", "dg", "dS0"), got, want, bound):
+        # (the two may sum in other orders: each is within its own bound)
+        u = 2 * (HALF[dtype] if name != "dS0" else 2.0 ** -17 if dtype == BF else F32)
+        dots = np.sum(size[0] * bound[0] + size[1] * bound[1], axis=(-1, -2)) + np.sum(bound[4], axis=(-1, -2))
+        extra = 2 * (N + D + M + 64) * F32 * dots[..., None] if name == "dg" else 0.0
+        assert np.all(np.abs(_f64(a) - _f64(b)) <= 2 * (u + (N + D + M + 64) * F32) * x + extra), name
+
+
 def test_no_tokens(la):
     q, k, v, g, do, S0, dS = _inputs(1, 2, 2, 0, 64, 64, BF)
     out, S = la.la_prefill_gated(q, k, v, g, S0=S0)
