@@ -205,6 +205,26 @@ def test_float32_heads_of_every_width(la, dims):
         _backward_close(la, q, k, v, g, do, S0, dS, FL)
 
 
+@pytest.mark.parametrize("states", [False, True], ids=["zero", "states"])
+@pytest.mark.parametrize("shape", [(2, 8, 700, 128, 128), (4, 10, 333, 96, 64), (3, 8, 450, 40, 128),
+                                   (40, 4, 65, 128, 72), (1, 2, 5003, 128, 128), (1, 3, 4100, 64, 64)], ids=ids)
+def test_calls_that_fill_the_multiprocessors(la, shape, states):
+    """bf16, forward and backward: more than 152 blocks of 64 tokens by 64 columns, the last of a
+    sequence a part of one, as a training step has them."""
+    B, H, N, D, M = shape
+    assert B * H * ((N + 63) // 64) * ((max(D, M) + 63) // 64) > 152 or N > 4000
+    q, k, v, g, do, S0, dS = _inputs(sum(shape) + 3, *shape, BF)
+    S0, dS = (S0, dS) if states else (None, None)
+    out, S = la.la_prefill_gated(q, k, v, g, S0=S0)
+    want, wS = oracle.gated_forward(*map(_f64, (q, k, v, g)), None if S0 is None else _f64(S0))
+    ao, aS = oracle.gated_forward(*_abs(q, k, v), _f64(g), None if S0 is None else np.abs(_f64(S0)))
+    chain = N + D + M + 64
+    _close(out, want, ao, BF, chain, "out")
+    _close(la.la_forward_gated(q, k, v, g, S0=S0), want, ao, BF, chain, "out without state")
+    _close(S, wS, aS, BF, chain, "S", state=True)
+    _backward_close(la, q, k, v, g, do, S0, dS, BF)
+
+
 def test_backward_with_only_one_of_the_states(la):
     q, k, v, g, do, S0, dS = _inputs(3, 1, 2, 100, 64, 64, BF)
     _backward_close(la, q, k, v, g, do, S0, None, BF)
