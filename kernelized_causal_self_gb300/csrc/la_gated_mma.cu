@@ -6,8 +6,8 @@
 //   O = diag(exp(G_i)) (Q S) + ((Q K^T) * L) V
 //   S = exp(G) S + (diag(exp(G - G_j)) K)^T V
 // All exponents are <= 0 for g <= 0, so nothing overflows, and sums that reach a
-// weight are taken from the end that weight decays from (G - G_j as a sum from the
-// chunk's end), so that a strong gate elsewhere in the chunk costs no digits.
+// weight are taken from the end that weight decays from (chunk_gates), so that a strong
+// gate elsewhere in the chunk costs no digits.
 //
 // Four warps share a chunk: warp r has its rows 16 r.. of Q and O and rows 16 r.. of
 // S (of each 64), S in float32 accumulators that stay in registers over the whole
@@ -139,14 +139,16 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
   auto chunk_of = [&](int i) { return REV ? chunks - 1 - i : i; };
   auto raw_gates = [&](int c) { return load_gates(a.g + seq, tb + c * kC, te); };
 
-  float all = 0.f;  // warp 0: sum of the segment's gates, base 2
+  // A chunk's tables are made by the warp whose rows have the fewest blocks in the causal product
+  const bool makes = rb == (REV ? 3 : 0);
+  float all = 0.f;  // (its own:) sum of the segment's gates, base 2
   constexpr int kAhead = Sm::kStages - 1;
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) {
     if (i < chunks) load_chunk(chunk_of(i));
     cp_async_commit();
   }
-  if (chunks > 0 && warp == 0) all = chunk_gates<REV, EXACT>(raw_gates(chunk_of(0)), tables[0]);
+  if (chunks > 0 && makes) all = chunk_gates<REV, EXACT>(raw_gates(chunk_of(0)), tables[0]);
   {
     const float* in = nullptr;
     if (OUT && a.seg_in)
@@ -198,12 +200,11 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
     }
     if (i + kAhead < chunks) load_chunk(chunk_of(i + kAhead));
     cp_async_commit();
-    // the next chunk's tables are made by one warp, from gates asked for here
-    const bool maker = warp == 0 && i + 1 < chunks;
+    // the next chunk's, from gates asked for here
+    const bool maker = makes && i + 1 < chunks;
     ushort2 raw = make_ushort2(0, 0);
     if (maker) raw = raw_gates(chunk_of(i + 1));
     const GateTables& t = tables[i & 1];
-    const float* Gs = t.G;
     const float dec = t.decay;
 
     if (OUT) {
@@ -226,13 +227,12 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
               sum * dec;
       }
       float o[8][4];
-      const float gr[2] = {Gs[r0 + row], Gs[r0 + row + 8]};
+      // of this warp's rows: what its own block of tokens leaves of them, or lets through
+      float wr[2] = {(REV ? t.out : t.in)[r0 + row], (REV ? t.out : t.in)[r0 + row + 8]};
       product<true>(ln64, o, f, x_op + (i & 1) * Sm::kX);
       if (FINE) product<true, true>(ln64, o, f, x_op + (2 + (i & 1)) * Sm::kX);
-      if (REV)
-        scale_rows(o, t.W[r0 + row], t.W[r0 + row + 8]);
-      else
-        scale_rows(o, ex2(gr[0]), ex2(gr[1]));
+      const float others = (REV ? t.behind : t.before)[rb];
+      scale_rows(o, wr[0] * others, wr[1] * others);
       const size_t dots_at = ((size_t)blockIdx.y * a.BH + bh) * a.N + t0 + row;
       float2 inter = make_float2(0.f, 0.f);
       if (DOTS && REV) {
@@ -241,13 +241,15 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
         inter = row_dots(ln, z_at, r0, o);
       }
       uint32_t p[FINE ? 2 : 1][4];
-#pragma unroll 1
-      for (int b = REV ? rb + 1 : 0; b < (REV ? 4 : rb); ++b) {
-        masked_block<!REV, false>(ln, p, f, w_at, b, gr, Gs);
-        add_block(ln64, o, p, u_at, b);
-      }
-      masked_block<!REV, true>(ln, p, f, w_at, rb, gr, Gs);
+      diagonal_block<!REV>(ln, p, f, w_at, rb, t.hi, t.lo);
       add_block(ln64, o, p, u_at, rb);
+#pragma unroll 1
+      for (int b = REV ? rb + 1 : rb - 1; REV ? b < 4 : b >= 0; b += REV ? 1 : -1) {
+        weighted_block(ln, p, f, w_at, b, REV ? t.in : t.out, wr);
+        add_block(ln64, o, p, u_at, b);
+        wr[0] *= t.total[b];
+        wr[1] *= t.total[b];
+      }
       if (DOTS) {
         if (!REV) {
           cp_async_wait<1>();
@@ -308,7 +310,7 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
             *reinterpret_cast<float2*>(to + (size_t)r * a.UD + m) =
                 make_float2(x[dt][j][2 * h], x[dt][j][2 * h + 1]);
         }
-  if (!OUT && a.decay && c0 == 0 && tid == 0)
+  if (!OUT && a.decay && c0 == 0 && makes && lane == 0)
     a.decay[(size_t)bh * a.n_seg + seg] = gated_decay(all * kLn2);
 }
 

@@ -27,44 +27,76 @@ __device__ __forceinline__ float2 gates_of(ushort2 g) {
   return make_float2(a < -200.f ? -200.f : a, b < -200.f ? -200.f : b);
 }
 
-// From a lane's two gates, tables of the chunk (made by one warp for all):
-//   G[i]  the gates' sums up to and including token i
-//   W[i]  2^(sum of those behind i), what is left of i's outer product in the state after
-//         the chunk; and with REV V[i] = 2^G[i]. The one of the two that weights operands
-//         (V with REV, else W) is kept as split_pair's in X, or if EXACT as float32.
+// a + b as the nearest float32, and what that leaves (exactly)
+__device__ __forceinline__ float two_sum(float a, float b, float& rest) {
+  const float s = a + b, from_b = s - a;
+  rest = (a - (s - from_b)) + (b - from_b);
+  return s;
+}
+
+// From a lane's two gates, tables of the chunk (made by one warp for all). Every weight is
+// made of sums within a block of 16 tokens, begun at the end that it decays from, and of the
+// sums of whole blocks: what a strong gate adds to another token's sum costs no digits.
+//   hi + lo [i]  the block's gates up to and including token i. In two terms, since weights
+//         within a block are made of differences of them (of one term, 40 resets before a
+//         chunk's other tokens left those weights off by 2e-3)
+//   in[i] = 2^(that), out[i] = 2^(the block's gates behind i), total[b] = 2^(block b's), so
+//         that token j's weight for token i of a later block is out[j] times the blocks
+//         between times in[i]
+//   before[b], behind[b] = 2^(the chunk's other blocks on that side of b)
+//   X[i]  weights of an operand's rows: 2^(sum of the chunk's gates behind i), what is left
+//         of i's outer product in the state after the chunk, with REV 2^(sum up to and
+//         including i); as split_pair's, or if EXACT as float32
 //   decay of the whole chunk; its sum is returned
 struct GateTables {
-  float G[mma::kC], W[mma::kC], X[mma::kC], decay, pad[3];
+  float hi[mma::kC], lo[mma::kC], in[mma::kC], out[mma::kC], X[mma::kC];
+  float total[4], before[4], behind[4], decay, pad[3];
 };
 template <bool REV, bool EXACT>
 __device__ __forceinline__ float chunk_gates(ushort2 raw, GateTables& t) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, block = lane >> 3, at = lane & 7;
   const float2 g = gates_of(raw);
-  const float both = g.x + g.y;
-  float up = both, down = both;
+  float hi, lo, rest, down = g.x + g.y;
+  hi = two_sum(g.x, g.y, lo);
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const float u = __shfl_up_sync(0xffffffffu, up, o);
-    const float d = __shfl_down_sync(0xffffffffu, down, o);
-    if (lane >= o) up += u;
-    if (lane + o < 32) down += d;
+  for (int o = 1; o < 8; o <<= 1) {
+    const float uh = __shfl_up_sync(0xffffffffu, hi, o, 8), ul = __shfl_up_sync(0xffffffffu, lo, o, 8);
+    const float d = __shfl_down_sync(0xffffffffu, down, o, 8);
+    if (at >= o) {
+      hi = two_sum(hi, uh, rest);
+      lo += ul + rest;
+    }
+    if (at + o < 8) down += d;
   }
-  float before = __shfl_up_sync(0xffffffffu, up, 1);
-  float after = __shfl_down_sync(0xffffffffu, down, 1);
-  if (lane == 0) before = 0.f;
-  if (lane == 31) after = 0.f;
-  const float2 incl = make_float2(before + g.x, up);
-  const float2 left = make_float2(mma::ex2(after + g.y), mma::ex2(after));
-  const float2 w = REV ? make_float2(mma::ex2(incl.x), mma::ex2(incl.y)) : left;
-  reinterpret_cast<float2*>(t.G)[lane] = incl;
-  reinterpret_cast<float2*>(t.W)[lane] = left;
+  float first_hi = __shfl_up_sync(0xffffffffu, hi, 1, 8), first_lo = __shfl_up_sync(0xffffffffu, lo, 1, 8);
+  float after = __shfl_down_sync(0xffffffffu, down, 1, 8);
+  if (at == 0) first_hi = first_lo = 0.f;
+  if (at == 7) after = 0.f;
+  first_hi = two_sum(first_hi, g.x, rest);
+  first_lo += rest;
+  const float2 upto = make_float2(first_hi + first_lo, hi + lo), left = make_float2(after + g.y, after);
+  const float t0 = __shfl_sync(0xffffffffu, upto.y, 7), t1 = __shfl_sync(0xffffffffu, upto.y, 15),
+              t2 = __shfl_sync(0xffffffffu, upto.y, 23), t3 = __shfl_sync(0xffffffffu, upto.y, 31);
+  const float before = block == 0 ? 0.f : block == 1 ? t0 : block == 2 ? t0 + t1 : t0 + t1 + t2;
+  const float behind = block == 3 ? 0.f : block == 2 ? t3 : block == 1 ? t2 + t3 : t1 + (t2 + t3);
+  const float2 w = REV ? make_float2(mma::ex2(before + upto.x), mma::ex2(before + upto.y))
+                       : make_float2(mma::ex2(left.x + behind), mma::ex2(left.y + behind));
+  reinterpret_cast<float2*>(t.hi)[lane] = make_float2(first_hi, hi);
+  reinterpret_cast<float2*>(t.lo)[lane] = make_float2(first_lo, lo);
+  reinterpret_cast<float2*>(t.in)[lane] = make_float2(mma::ex2(upto.x), mma::ex2(upto.y));
+  reinterpret_cast<float2*>(t.out)[lane] = make_float2(mma::ex2(left.x), mma::ex2(left.y));
   if (EXACT)
     reinterpret_cast<float2*>(t.X)[lane] = w;
   else
     reinterpret_cast<uint2*>(t.X)[lane] = mma::split_pair(w);
-  const float total = __shfl_sync(0xffffffffu, up, 31);
-  if (lane == 0) t.decay = gated_decay(total * kLn2);
-  return total;
+  if (at == 7) {
+    t.total[block] = mma::ex2(upto.y);
+    t.before[block] = mma::ex2(before);
+    t.behind[block] = mma::ex2(behind);
+  }
+  const float whole = t0 + t1 + (t2 + t3);
+  if (lane == 0) t.decay = gated_decay(whole * kLn2);
+  return whole;
 }
 
 // tcx::configure, once per kernel and device (its two calls of the runtime cost as much as a

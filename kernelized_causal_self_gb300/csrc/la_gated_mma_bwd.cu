@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       load_tile<64, kThreads>(at + 3 * kTile, a.dout + (seq + t0) * a.M, rows, a.M, 0);
     };
     // A chunk's tables are made by one warp while the chunk before it is worked on. Going
-    // forward K is weighted (W), going back Q (V).
+    // forward K is weighted, going back Q.
     auto raw_gates = [&](int c) { return load_gates(a.g + seq, tb + c * kC, te); };
 
     __syncthreads();  // the item before is done with
@@ -141,10 +141,9 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       if (c + 1 < chunks) load_chunk(c + 1);
       cp_async_commit();
       const GateTables& t = tables[c & 1];
-      const float* Gs = t.G;
       const uint32_t q_at = base + (c & 1) * kStage, k_at = q_at + kTile, v_at = k_at + kTile,
                      do_at = v_at + kTile;
-      const bool maker = c + 1 < chunks && warp == (c & 3);
+      const bool maker = c + 1 < chunks && rb == 0;  // (the warp with one block of the product)
       ushort2 raw = make_ushort2(0, 0);
       if (maker) raw = raw_gates(c + 1);
 #pragma unroll
@@ -155,15 +154,17 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       for (int ks = 0; ks < 4; ++ks) ln.load_a(f[ks], do_at, r0, ks);
       product<false>(ln, d, f, op_base + (c & 1) * kOp);
       if (FINE) product<false, true>(ln, d, f, op_base + (2 + (c & 1)) * kOp);
-      const float gi[2] = {Gs[r0 + row], Gs[r0 + row + 8]};
-      scale_rows(d, ex2(gi[0]), ex2(gi[1]));
-#pragma unroll 1
-      for (int jb = 0; jb < rb; ++jb) {
-        masked_block<true, false>(ln, p, f, v_at, jb, gi, Gs);
-        add_block(ln, d, p, k_at, jb);
-      }
-      masked_block<true, true>(ln, p, f, v_at, rb, gi, Gs);
+      float wi[2] = {t.in[r0 + row], t.in[r0 + row + 8]};
+      scale_rows(d, wi[0] * t.before[rb], wi[1] * t.before[rb]);
+      diagonal_block<true>(ln, p, f, v_at, rb, t.hi, t.lo);
       add_block(ln, d, p, k_at, rb);
+#pragma unroll 1
+      for (int jb = rb - 1; jb >= 0; --jb) {
+        weighted_block(ln, p, f, v_at, jb, t.out, wi);
+        add_block(ln, d, p, k_at, jb);
+        wi[0] *= t.total[jb];
+        wi[1] *= t.total[jb];
+      }
       const float2 dots = row_dots(ln, q_at, r0, d);
       if ((lane & 3) == 0) {
         alpha[c * kC + r0 + row] = dots.x;
@@ -216,7 +217,6 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       cp_async_commit();
       const int step = chunks - 1 - c;
       const GateTables& t = tables[c & 1];
-      const float* Gs = t.G;
       float* part = parts + (c & 1) * kParts;
       const uint32_t q_at = base + (c & 1) * kStage, k_at = q_at + kTile, v_at = k_at + kTile,
                      do_at = v_at + kTile, op = op_base + (step & 1) * kOp;
@@ -228,7 +228,6 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       for (int j = 0; j < 8; ++j) sc[j] = states[(c * 8 + j) * kThreads];
       if (c + 1 < chunks && warp == ((c + 1) & 3)) finish(c + 1);
       const float dec = t.decay;
-      const float gj[2] = {Gs[r0 + row], Gs[r0 + row + 8]};
       const int t0 = tb + c * kC + r0;
       uint32_t f[4][4], p[FINE ? 2 : 1][4];
       float d[8][4];
@@ -236,13 +235,16 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       for (int ks = 0; ks < 4; ++ks) ln.load_a(f[ks], k_at, r0, ks);
       product<true>(ln, d, f, op);
       if (FINE) product<true, true>(ln, d, f, op + 2 * kOp);
-      scale_rows(d, t.W[r0 + row], t.W[r0 + row + 8]);
-      masked_block<false, true>(ln, p, f, q_at, rb, gj, Gs);
+      float wj[2] = {t.out[r0 + row], t.out[r0 + row + 8]};
+      scale_rows(d, wj[0] * t.behind[rb], wj[1] * t.behind[rb]);
+      diagonal_block<false>(ln, p, f, q_at, rb, t.hi, t.lo);
       add_block(ln, d, p, do_at, rb);
 #pragma unroll 1
       for (int ib = rb + 1; ib < 4; ++ib) {
-        masked_block<false, false>(ln, p, f, q_at, ib, gj, Gs);
+        weighted_block(ln, p, f, q_at, ib, t.in, wj);
         add_block(ln, d, p, do_at, ib);
+        wj[0] *= t.total[ib];
+        wj[1] *= t.total[ib];
       }
       store_rows(ln, out_at, r0, d, a.dv + (seq + t0) * a.M, te - t0, a.M, a.M);
       {
@@ -257,19 +259,21 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       // dK by the rows from the other end: the two causal halves add up to the same for
       // every warp
       const int kb = 3 - rb, k0 = kb * 16, tk = tb + c * kC + k0;
-      const float gk[2] = {Gs[k0 + row], Gs[k0 + row + 8]};
+      float wk[2] = {t.out[k0 + row], t.out[k0 + row + 8]};
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) ln.load_a(f[ks], v_at, k0, ks);
       product<false>(ln, d, f, op);
       if (FINE) product<false, true>(ln, d, f, op + 2 * kOp);
-      scale_rows(d, t.W[k0 + row], t.W[k0 + row + 8]);
+      scale_rows(d, wk[0] * t.behind[kb], wk[1] * t.behind[kb]);
       const float2 be = row_dots(ln, k_at, k0, d);
-      masked_block<false, true>(ln, p, f, do_at, kb, gk, Gs);
+      diagonal_block<false>(ln, p, f, do_at, kb, t.hi, t.lo);
       add_block(ln, d, p, q_at, kb);
 #pragma unroll 1
       for (int ib = kb + 1; ib < 4; ++ib) {
-        masked_block<false, false>(ln, p, f, do_at, ib, gk, Gs);
+        weighted_block(ln, p, f, do_at, ib, t.in, wk);
         add_block(ln, d, p, q_at, ib);
+        wk[0] *= t.total[ib];
+        wk[1] *= t.total[ib];
       }
       const float2 all = row_dots(ln, k_at, k0, d);
       if ((lane & 3) == 0) {

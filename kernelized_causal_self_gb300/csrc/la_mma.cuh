@@ -373,16 +373,10 @@ __device__ __forceinline__ void product(const Lane<64>& ln, float (&c)[8][4],
     }
 }
 
-// A block of 16 x 16 of (A B^T) * L as an A operand of TERMS bf16 terms: A's fragments, B the rows 16 cb.. of
-// a tile, G the chunk's gate sums (gr: of A's rows l / 4 and l / 4 + 8). LOWER: A's rows
-// are the later tokens (L = exp(g_row - g_col)), else B's are. DIAGONAL: the block where
-// both are the same tokens, half of it zero.
-template <bool LOWER, bool DIAGONAL, int COLS, int KS, int TERMS>
-__device__ __forceinline__ void masked_block(const Lane<COLS>& ln, uint32_t (&out)[TERMS][4],
-                                             const uint32_t (&a)[KS][4], uint32_t tile, int cb,
-                                             const float (&gr)[2], const float* G) {
-  const int l = threadIdx.x & 31, row = l >> 2, col = (l & 3) * 2;
-  float p[2][4];
+// A block of 16 x 16 of A B^T: A's fragments, B the rows 16 cb.. of a tile
+template <int COLS, int KS>
+__device__ __forceinline__ void block_product(const Lane<COLS>& ln, float (&p)[2][4],
+                                              const uint32_t (&a)[KS][4], uint32_t tile, int cb) {
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks) {
     uint32_t b[4];
@@ -395,24 +389,62 @@ __device__ __forceinline__ void masked_block(const Lane<COLS>& ln, uint32_t (&ou
       mma16816(p[1], a[ks], b[2], b[3]);
     }
   }
+}
+
+// A pair of such a block as element e of an A operand of TERMS bf16 terms
+template <int TERMS>
+__device__ __forceinline__ void keep_terms(uint32_t (&out)[TERMS][4], int e, float2 w) {
+#pragma unroll
+  for (int i = 0; i < TERMS; ++i) {
+    out[i][e] = pack2(w.x, w.y);
+    w = rest_of(w, out[i][e]);
+  }
+}
+
+// The block times weights that are a product of one of the column, from `cols`, and one of
+// A's rows l / 4 and l / 4 + 8
+template <int COLS, int KS, int TERMS>
+__device__ __forceinline__ void weighted_block(const Lane<COLS>& ln, uint32_t (&out)[TERMS][4],
+                                               const uint32_t (&a)[KS][4], uint32_t tile, int cb,
+                                               const float* cols, const float (&rows)[2]) {
+  const int col = (threadIdx.x & 3) * 2;
+  float p[2][4];
+  block_product(ln, p, a, tile, cb);
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const float2 gc = *reinterpret_cast<const float2*>(G + 16 * cb + 8 * t + col);
+    const float2 c = *reinterpret_cast<const float2*>(cols + 16 * cb + 8 * t + col);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      keep_terms(out, 2 * t + h, mul2(pair_of(p[t], h), mul2(c, make_float2(rows[h], rows[h]))));
+  }
+}
+
+// The block where A's rows and B's are the same tokens, times exp2 of the gates between a
+// row's token and a column's (hi + lo: their sums up to each token), half of it zero. LOWER:
+// A's rows are the later tokens, else B's are.
+template <bool LOWER, int COLS, int KS, int TERMS>
+__device__ __forceinline__ void diagonal_block(const Lane<COLS>& ln, uint32_t (&out)[TERMS][4],
+                                               const uint32_t (&a)[KS][4], uint32_t tile, int cb,
+                                               const float* hi, const float* lo) {
+  const int l = threadIdx.x & 31, row = l >> 2, col = (l & 3) * 2;
+  float p[2][4];
+  block_product(ln, p, a, tile, cb);
+  hi += 16 * cb;
+  lo += 16 * cb;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const float2 ch = *reinterpret_cast<const float2*>(hi + 8 * t + col),
+                 cl = *reinterpret_cast<const float2*>(lo + 8 * t + col);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float2 g2 = make_float2(gr[h], gr[h]);
-      const float2 e = LOWER ? sub2(g2, gc) : sub2(gc, g2);
-      float2 w = mul2(pair_of(p[t], h), make_float2(ex2(e.x), ex2(e.y)));
-      if (DIAGONAL) {
-        const int c = 8 * t + col, r = row + 8 * h;
-        w.x = (LOWER ? c <= r : c >= r) ? w.x : 0.f;
-        w.y = (LOWER ? c + 1 <= r : c + 1 >= r) ? w.y : 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < TERMS; ++i) {
-        out[i][2 * t + h] = pack2(w.x, w.y);
-        w = rest_of(w, out[i][2 * t + h]);
-      }
+      const float gh = hi[row + 8 * h], gl = lo[row + 8 * h];
+      const float2 rh = make_float2(gh, gh), rl = make_float2(gl, gl);
+      const float2 d = LOWER ? sub2(rh, ch) : sub2(ch, rh), r = LOWER ? sub2(rl, cl) : sub2(cl, rl);
+      float2 w = mul2(pair_of(p[t], h), make_float2(ex2(d.x + r.x), ex2(d.y + r.y)));
+      const int c = 8 * t + col, i = row + 8 * h;
+      w.x = (LOWER ? c <= i : c >= i) ? w.x : 0.f;
+      w.y = (LOWER ? c + 1 <= i : c + 1 >= i) ? w.y : 0.f;
+      keep_terms(out, 2 * t + h, w);
     }
   }
 }

@@ -225,6 +225,46 @@ def test_calls_that_fill_the_multiprocessors(la, shape, states):
     _backward_close(la, q, k, v, g, do, S0, dS, BF)
 
 
+def _half_step(x):
+    """Half a step of bf16 at |x|."""
+    return np.exp2(np.floor(np.log2(np.maximum(np.abs(x), 1e-37))) - 8)
+
+
+@pytest.mark.parametrize("gate", ["slow", "many resets", "some resets"])
+@pytest.mark.parametrize("shape", [(1, 4, 63, 64, 64), (1, 3, 700, 64, 64), (1, 2, 200, 128, 96)], ids=ids)
+def test_resets_cost_the_tokens_behind_them_no_digits(la, shape, gate):
+    """bf16, up to 152 chunks. A term of an output is rounded in no more than two operands of two
+    bf16 terms each, 2^-17 of it, and in weights whose gates are summed to float32's digits, however
+    often the state is emptied among the same 64 tokens: 2^-15 of the absolute terms in all; then
+    the output by half a step of its own."""
+    B, H, N, D, M = shape
+    q, k, v, g, do, S0, dS = _inputs(sum(shape) + 7, *shape, BF, "slow")
+    at = torch.arange(N, device=DEV) % 64
+    if gate == "many resets":  # 40 in every 64, then tokens that forget very little
+        g[...] = torch.where(at < 40, -torch.inf, -1e-4)
+        q, k, v, do = (x.abs() for x in (q, k, v, do))  # (so that a weight off everywhere shows)
+    elif gate == "some resets":  # between tokens that forget little
+        g[..., at % 8 == 2] = torch.finfo(BF).min
+        g[..., at % 8 == 3] = -40.0
+    chain = N + D + M + 64
+    n64 = [_f64(t) for t in (q, k, v, g, do, S0, dS)]
+    size = [np.abs(x) for x in n64]
+    size[3] = n64[3]
+    bound = oracle.gated_backward(*size)
+    dots = np.sum(size[0] * bound[0] + size[1] * bound[1], axis=(-1, -2)) + \
+        np.sum(bound[4], axis=(-1, -2))
+    names = ("out", "dq", "dk", "dv", "dg")
+    outs = (la.la_forward_gated(q, k, v, g, S0=S0), *la.la_backward_gated(q, k, v, g, do, S0=S0, dS=dS)[:4])
+    wants = (oracle.gated_forward(*n64[:4], n64[5])[0], *oracle.gated_backward(*n64)[:4])
+    sizes = (oracle.gated_forward(*size[:4], size[5])[0], *bound[:4])
+    for name, got, want, a in zip(names, outs, wants, sizes):
+        off = (2.0 ** -15 + chain * F32) * a
+        if name == "dg":
+            off = off + chain * F32 * dots[..., None]
+        each = np.abs(_f64(got) - want) - _half_step(np.abs(want) + off) - off
+        assert np.all(each <= 0), (name, (each > 0).mean(), np.max(each / (a + 1e-30)))
+
+
 def test_backward_with_only_one_of_the_states(la):
     q, k, v, g, do, S0, dS = _inputs(3, 1, 2, 100, 64, 64, BF)
     _backward_close(la, q, k, v, g, do, S0, None, BF)
