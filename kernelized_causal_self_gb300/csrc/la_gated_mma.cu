@@ -11,23 +11,23 @@
 //
 // Four warps share a chunk: warp r has its rows 16 r.. of Q and O and rows 16 r.. of
 // S (of each 64), S in float32 accumulators that stay in registers over the whole
-// segment. What is rounded to bf16: Q K^T * L as an operand, and the copy of S in
-// shared memory that Q multiplies; the outputs, bf16 too, cannot show more. The update
-// of S takes K's weighted rows as two bf16 terms (16 bits): with one, the longest
-// forward takes 97 us instead of 105, but its outputs are off by 2.8e-3 (2-norm) instead
-// of 2.3e-3, against 1.7e-3 for their own rounding.
+// segment. What is multiplied by an input's rows and is not an input itself (Q K^T * L,
+// the copy of S in shared memory that Q multiplies, K's weighted rows in the update of S)
+// is taken as two bf16 terms, 16 bits: an output shows its own rounding only (1.66e-3 in
+// the 2-norm of random data). With one term of the first two, outputs were off by 2.35e-3,
+// in 106 us for the longest forward instead of 124; with one of the third too by 2.8e-3.
 //
 // Why warp-level products and not tcgen05: at 64 columns a chunk's products are small
 // next to its element-wise work (masks, weights, splits), which here happens in the
 // registers that hold the fragments, with no round trip through tensor memory and no
 // barrier between a product and its use. The price is that these instructions hold up
-// their scheduler's others: the products' 1088 cycles a chunk and warp (at the 600
-// TFLOP/s they reach) and some 540 other instructions add up rather than overlap, to
-// 2350 cycles with three CTAs of four warps per SM.
+// their scheduler's others: the products' 1504 cycles a chunk and warp (at the 600
+// TFLOP/s they reach) and some 600 other instructions add up rather than overlap, to
+// 3000 cycles with three CTAs of four warps per SM.
 //
 // B4 H8 N16384 D = M = 64: states 33 us (138 MB moved: half of what HBM gives, tensor
-// pipe 49%), scan 6 us, outputs 67 us (252 MB; tensor pipe 51%, issue slots 36%); the
-// whole call 105 us against 40 us for reading q, k, v and writing out once.
+// pipe 49%), scan 6 us, outputs 85 us (252 MB); the whole call 124 us against 40 us for
+// reading q, k, v and writing out once.
 #include "la_gated.cuh"
 #include "la_gated_mma.cuh"
 #include "la_mma.cuh"
@@ -74,15 +74,17 @@ struct WalkArgs {
   float4* kept;
 };
 
-template <int DZ, bool OUT, bool FINE = false>
+template <int DZ, bool OUT>
 struct WalkSmem {
+  // z: each warp its own rows, which it asks for as soon as it is done with the chunk before
   static constexpr int kZ = OUT ? kC * DZ * 2 : 0, kW = kC * DZ * 2, kU = kC * 64 * 2;
-  static constexpr int kStage = kZ + kW + kU;
-  static constexpr int kX = OUT ? DZ * 64 * 2 : 0;  // X in bf16, one of two; FINE: and their rest
+  static constexpr int kStage = kW + kU;
   // the state pass has little to do on a chunk, so it asks for two ahead; the outputs'
   // walk is longer on a chunk than a load takes
   static constexpr int kStages = OUT ? 2 : 3;
-  static constexpr int kTables = kStages * kStage + (FINE ? 4 : 2) * kX;
+  // X's two bf16 terms; heads over 64 have no room for the next chunk's beside them
+  static constexpr int kX = OUT ? DZ * 64 * 2 : 0, kOps = DZ == 64 ? 2 : 1;
+  static constexpr int kTables = kZ + kStages * kStage + 2 * kOps * kX;
   static constexpr int kBytes = kTables + 2 * (int)sizeof(GateTables);
 };
 
@@ -91,16 +93,16 @@ struct WalkSmem {
 // EXACT: a chunk's update of X is summed apart, with its operand to 24 bits, and added in
 // float32 arithmetic that rounds (the tensor cores' own sums truncate, which over
 // thousands of chunks would leave a bias in a state that hardly decays). Taken where X
-// leaves the kernel as a float32 result; where it only goes on as a bf16 operand, 16 bits
-// and sums in place do, and leave registers for more CTAs per SM.
+// leaves the kernel as a float32 result; where it only goes on as an operand of two bf16
+// terms, 16 bits and sums in place do, and leave registers for more CTAs per SM.
 // DOTS: the parts of the gates' gradient.
-// FINE: see gated_fine.
-template <int DZ, bool OUT, bool REV, bool EXACT, bool DOTS = false, bool FINE = false>
+template <int DZ, bool OUT, bool REV, bool EXACT, bool DOTS = false>
 __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
-  using Sm = WalkSmem<DZ, OUT, FINE>;
+  using Sm = WalkSmem<DZ, OUT>;
   constexpr int KS = DZ / 16, DT = DZ / 64;
   extern __shared__ __align__(128) uint8_t smem[];
-  const uint32_t base = tc::smem_u32(smem), x_op = base + Sm::kStages * Sm::kStage;
+  const uint32_t base = tc::smem_u32(smem), stages = base + Sm::kZ,
+                 x_op = stages + Sm::kStages * Sm::kStage;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = lane >> 2, col = (lane & 3) * 2;  // of an accumulator
   GateTables* tables = reinterpret_cast<GateTables*>(smem + Sm::kTables);
@@ -122,19 +124,23 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
   const size_t entry_size = (size_t)a.ZD * a.UD;
 
   float x[DT][8][4];
-  auto keep_op = [&](int buf) {
+  auto x_at = [&](int i) { return x_op + (Sm::kOps == 2 ? 2 * (i & 1) * Sm::kX : 0); };
+  auto keep_op = [&](int i) {  // X before the i-th chunk
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) {
-      store_op(ln64, x_op + buf * Sm::kX, dt * 64 + rb * 16, 0, x[dt]);
-      if (FINE) store_op<true>(ln64, x_op + (2 + buf) * Sm::kX, dt * 64 + rb * 16, 0, x[dt]);
+      store_op(ln64, x_at(i), dt * 64 + rb * 16, 0, x[dt]);
+      store_op<true>(ln64, x_at(i) + Sm::kX, dt * 64 + rb * 16, 0, x[dt]);
     }
   };
   auto load_chunk = [&](int c) {
     const int t0 = tb + c * kC, rows = min(kC, te - t0);
-    const uint32_t at = base + (c % Sm::kStages) * Sm::kStage;
-    if (OUT) load_tile<DZ, kThreads>(at, a.z + (seq + t0) * a.ZD, rows, a.ZD, 0);
-    load_tile<DZ, kThreads>(at + Sm::kZ, a.w + (seq + t0) * a.ZD, rows, a.ZD, 0);
-    load_tile<64, kThreads>(at + Sm::kZ + Sm::kW, a.u + (seq + t0) * a.UD, rows, a.UD, c0);
+    const uint32_t at = stages + (c % Sm::kStages) * Sm::kStage;
+    load_tile<DZ, kThreads>(at, a.w + (seq + t0) * a.ZD, rows, a.ZD, 0);
+    load_tile<64, kThreads>(at + Sm::kW, a.u + (seq + t0) * a.UD, rows, a.UD, c0);
+  };
+  auto load_z = [&](int c) {
+    const int t0 = tb + c * kC + rb * 16;
+    load_rows<DZ>(base, rb * 16, a.z + (seq + min(t0, te - 1)) * a.ZD, te - t0, a.ZD);
   };
   auto chunk_of = [&](int i) { return REV ? chunks - 1 - i : i; };
   auto raw_gates = [&](int c) { return load_gates(a.g + seq, tb + c * kC, te); };
@@ -146,6 +152,7 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) {
     if (i < chunks) load_chunk(chunk_of(i));
+    if (OUT && i < chunks) load_z(chunk_of(i));
     cp_async_commit();
   }
   if (chunks > 0 && makes) all = chunk_gates<REV, EXACT>(raw_gates(chunk_of(0)), tables[0]);
@@ -180,7 +187,7 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
     const int c = chunk_of(i);
     cp_async_wait<kAhead - 1>();
     __syncthreads();  // chunk i has landed; every warp is done with chunk i - 1
-    const uint32_t z_at = base + (c % Sm::kStages) * Sm::kStage, w_at = z_at + Sm::kZ, u_at = w_at + Sm::kW;
+    const uint32_t z_at = base, w_at = stages + (c % Sm::kStages) * Sm::kStage, u_at = w_at + Sm::kW;
     const int r0 = rb * 16, t0 = tb + c * kC + r0;
     uint32_t f[OUT ? KS : 1][4];
     if (OUT) {
@@ -229,8 +236,8 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
       float o[8][4];
       // of this warp's rows: what its own block of tokens leaves of them, or lets through
       float wr[2] = {(REV ? t.out : t.in)[r0 + row], (REV ? t.out : t.in)[r0 + row + 8]};
-      product<true>(ln64, o, f, x_op + (i & 1) * Sm::kX);
-      if (FINE) product<true, true>(ln64, o, f, x_op + (2 + (i & 1)) * Sm::kX);
+      product<true>(ln64, o, f, x_at(i));
+      product<true, true>(ln64, o, f, x_at(i) + Sm::kX);
       const float others = (REV ? t.behind : t.before)[rb];
       scale_rows(o, wr[0] * others, wr[1] * others);
       const size_t dots_at = ((size_t)blockIdx.y * a.BH + bh) * a.N + t0 + row;
@@ -240,7 +247,7 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
         __syncwarp();
         inter = row_dots(ln, z_at, r0, o);
       }
-      uint32_t p[FINE ? 2 : 1][4];
+      uint32_t p[2][4];
       diagonal_block<!REV>(ln, p, f, w_at, rb, t.hi, t.lo);
       add_block(ln64, o, p, u_at, rb);
 #pragma unroll 1
@@ -273,6 +280,9 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
       }
       // through this warp's rows of z's tile, which no other warp reads
       store_rows(ln, z_at, r0, o, a.out + (seq + t0) * a.UD + c0, te - t0, a.UD - c0, a.UD);
+      __syncwarp();
+      if (i + 1 < chunks) load_z(chunk_of(i + 1));
+      cp_async_commit();
     }
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) {
@@ -289,7 +299,8 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
         add_outer<false>(ln, ln64, x[dt], w_at, t.X, 4 * dt + rb, u_at, 0);
       }
     }
-    if (OUT && i + 1 < chunks) keep_op((i + 1) & 1);
+    if (OUT && Sm::kOps == 1) __syncthreads();  // every warp has multiplied X
+    if (OUT && i + 1 < chunks) keep_op(i + 1);
     if (maker) all += chunk_gates<REV, EXACT>(raw, tables[(i + 1) & 1]);
   }
 
@@ -314,10 +325,10 @@ __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
     a.decay[(size_t)bh * a.n_seg + seg] = gated_decay(all * kLn2);
 }
 
-template <int DZ, bool EXACT, bool FINE>
-__global__ void __launch_bounds__(kThreads, DZ == 64 ? FINE ? 2 : 3 : FINE ? 1 : 2)
+template <int DZ, bool EXACT>
+__global__ void __launch_bounds__(kThreads, DZ == 64 ? 3 : 2)
 gated_forward_kernel(const WalkArgs a) {
-  walk_chunks<DZ, true, false, EXACT, false, FINE>(a);
+  walk_chunks<DZ, true, false, EXACT>(a);
 }
 
 // blockIdx.z: the segments' states, or their gradients
@@ -330,10 +341,10 @@ gated_states_kernel(const WalkArgs a, const WalkArgs back) {
     walk_chunks<DZ, false, true, EXACT>(back);
 }
 
-template <int DZ, bool REV, bool DOTS, bool FINE>
-__global__ void __launch_bounds__(kThreads, DZ == 64 ? FINE ? 2 : 3 : FINE ? 1 : 2)
+template <int DZ, bool REV, bool DOTS>
+__global__ void __launch_bounds__(kThreads, DZ == 64 ? 3 : 2)
 gated_gradient_kernel(const WalkArgs a) {
-  walk_chunks<DZ, true, REV, false, DOTS, FINE>(a);
+  walk_chunks<DZ, true, REV, false, DOTS>(a);
 }
 
 dim3 walk_grid(const WalkArgs& a, int z = 1) {
@@ -341,11 +352,9 @@ dim3 walk_grid(const WalkArgs& a, int z = 1) {
 }
 
 template <int DZ, bool EXACT>
-cudaError_t launch_forward(const WalkArgs& a, bool fine, cudaStream_t st) {
-  return fine ? gated_launch<gated_forward_kernel<DZ, EXACT, true>>(WalkSmem<DZ, true, true>::kBytes,
-                                                                    walk_grid(a), kThreads, st, a)
-              : gated_launch<gated_forward_kernel<DZ, EXACT, false>>(WalkSmem<DZ, true>::kBytes,
-                                                                     walk_grid(a), kThreads, st, a);
+cudaError_t launch_forward(const WalkArgs& a, cudaStream_t st) {
+  return gated_launch<gated_forward_kernel<DZ, EXACT>>(WalkSmem<DZ, true>::kBytes, walk_grid(a), kThreads,
+                                                       st, a);
 }
 
 template <bool EXACT>
@@ -355,20 +364,12 @@ cudaError_t launch_states(const WalkArgs& a, const WalkArgs& back, int jobs, cud
              : gated_launch<gated_states_kernel<128, EXACT>>(WalkSmem<128, false>::kBytes, walk_grid(a, jobs), kThreads, st, a, back);
 }
 
-template <bool REV, bool DOTS, bool FINE>
+template <bool REV, bool DOTS>
 cudaError_t launch_gradient(const WalkArgs& a, cudaStream_t st) {
-  return a.ZD <= 64 ? gated_launch<gated_gradient_kernel<64, REV, DOTS, FINE>>(
-                          WalkSmem<64, true, FINE>::kBytes, walk_grid(a), kThreads, st, a)
-                    : gated_launch<gated_gradient_kernel<128, REV, DOTS, FINE>>(
-                          WalkSmem<128, true, FINE>::kBytes, walk_grid(a), kThreads, st, a);
-}
-
-template <bool FINE>
-cudaError_t launch_gradients(const WalkArgs& dq, const WalkArgs& dk, const WalkArgs& dv, cudaStream_t st) {
-  cudaError_t e = launch_gradient<false, true, FINE>(dq, st);
-  if (e == cudaSuccess) e = launch_gradient<true, true, FINE>(dk, st);
-  if (e == cudaSuccess) e = launch_gradient<true, false, FINE>(dv, st);
-  return e;
+  return a.ZD <= 64 ? gated_launch<gated_gradient_kernel<64, REV, DOTS>>(WalkSmem<64, true>::kBytes,
+                                                                         walk_grid(a), kThreads, st, a)
+                    : gated_launch<gated_gradient_kernel<128, REV, DOTS>>(WalkSmem<128, true>::kBytes,
+                                                                          walk_grid(a), kThreads, st, a);
 }
 
 // dg of a chunk from its dots (see la_gated_mma_bwd.cu): a warp each, two tokens a lane.
@@ -443,8 +444,8 @@ GatedPlan gated_mma_plan(int BH, int N, int blocks, const GatedCosts& k) {
 
 GatedPlan gated_mma_forward_plan(int BH, int N, int D, int M) {
   const int blocks = (M + 63) / 64;
-  return gated_mma_plan(BH, N, blocks, D <= 64 ? GatedCosts{3 * 152, 0, 3.f, 3.4f, 9.f, 1.7f}
-                                               : GatedCosts{2 * 152, 0, 3.f, 4.5f, 9.f, 2.5f});
+  return gated_mma_plan(BH, N, blocks, D <= 64 ? GatedCosts{3 * 152, 0, 3.f, 4.f, 9.f, 1.7f}
+                                               : GatedCosts{2 * 152, 0, 3.f, 4.9f, 9.f, 2.5f});
 }
 
 cudaError_t gated_mma_states(const GatedPlan& p, const void* k, const void* v, const void* q,
@@ -504,15 +505,14 @@ cudaError_t gated_mma_forward(const GatedForward& f, const GatedPlan& p, const G
     a.init = f.S0;
     a.fin = f.S;
   }
-  const bool fine = gated_fine(p.BH * ((f.M + 63) / 64), p.N);
-  if (f.D <= 64) return a.fin ? launch_forward<64, true>(a, fine, st) : launch_forward<64, false>(a, fine, st);
-  return a.fin ? launch_forward<128, true>(a, fine, st) : launch_forward<128, false>(a, fine, st);
+  if (f.D <= 64) return a.fin ? launch_forward<64, true>(a, st) : launch_forward<64, false>(a, st);
+  return a.fin ? launch_forward<128, true>(a, st) : launch_forward<128, false>(a, st);
 }
 
 // ---- the backward for D or M over 64: states, scans, then dQ, dK and dV a walk each
 
 GatedPlan gated_mma_wide_plan(int BH, int N, int D, int M) {
-  return gated_mma_plan(BH, N, ((D > M ? D : M) + 63) / 64, GatedCosts{2 * 152, 0, 9.f, 14.f, 12.f, 5.f});
+  return gated_mma_plan(BH, N, ((D > M ? D : M) + 63) / 64, GatedCosts{2 * 152, 0, 9.f, 18.5f, 12.f, 5.f});
 }
 
 namespace {
@@ -569,8 +569,9 @@ cudaError_t gated_mma_wide_backward(const GatedBackward& f, const GatedPlan& p, 
   dk.seg_in = dv.seg_in = w.E;
   dq.dots = dot_q;
   dk.dots = dot_k;
-  e = gated_fine(p.BH * wide_blocks(f.D > f.M ? f.D : f.M), p.N) ? launch_gradients<true>(dq, dk, dv, st)
-                                                               : launch_gradients<false>(dq, dk, dv, st);
+  e = launch_gradient<false, true>(dq, st);
+  if (e == cudaSuccess) e = launch_gradient<true, true>(dk, st);
+  if (e == cudaSuccess) e = launch_gradient<true, false>(dv, st);
   if (e != cudaSuccess) return e;
   const long long warps = (long long)p.BH * (long long)chunks;
   e = tcx::launch_pdl(gated_chunk_dg_kernel, dim3((unsigned)((warps + 3) / 4)), dim3(kThreads), 0, st,

@@ -123,18 +123,6 @@ cudaError_t gated_launch(int smem, dim3 grid, int threads, cudaStream_t st, cons
   return e;
 }
 
-// FINE: two bf16 terms, not one, for what is multiplied by an input's rows and is not an
-// input itself: the products * L, and the states. For calls of so few chunks (`blocks` CTAs
-// wide) that each has a multiprocessor to itself, where it takes 3 to 17% longer (D = M = 64:
-// forward of 16 heads and 64 tokens 4.2 us for 3.8, of 512 tokens 19 for 17; backward 6.6
-// for 5.9 and 14.8 for 13.9), less than the host takes to issue the call. Their errors are
-// averages over few values: with one term dg of 4 heads and 20 to 128 tokens was off by up to
-// 2.9 times bf16's own rounding (2-norm; typically 1.5) and the other outputs by 1.4 times
-// it, with two all by 1.00.
-inline bool gated_fine(int blocks, int N) {
-  return (long long)blocks * ((N + mma::kC - 1) / mma::kC) <= 152;
-}
-
 // Tensor-core path: bf16 (la_gated_mma.cu, la_gated_mma_bwd.cu)
 // The cut of BH sequences of N tokens (each `blocks` CTAs wide) that the costs below, in
 // microseconds as measured, make the shortest: CTAs run in waves of `slots`, each for

@@ -11,26 +11,27 @@
 //   X = (Q K^T) * (dO V^T) * L,  a_i = exp(G_i) q_i S dO_i,  b_j = exp(G - G_j) k_j E v_j
 // X's sum is one over s >= t of its row sums less its column sums, and those are what
 // the products within the chunk add to q_s . dQ_s and to k_s . dK_s. Both products take
-// the same rounded operand (dO V^T) * L, so what has to cancel in the difference does.
+// the same operand (dO V^T) * L, to 16 bits, so what has to cancel in the difference does.
 //
 // S is known going forward and E going back, so a CTA walks its segment of a few chunks
 // forward (dQ; each chunk's S to scratch of the CTA's own, in float32 for <S, E>) and then
-// back (dK, dV, dg). Both walks keep their state in float32 accumulators; rounded to bf16
-// are the operands (L's products, the copies of S and E that are multiplied) and the
-// gradients.
+// back (dK, dV, dg). Both walks keep their state in float32 accumulators; operands that are
+// not inputs (L's products, the copies of S and E that are multiplied, weighted rows) are
+// two bf16 terms, and only the gradients are rounded to one.
 //
 // Four warps share a chunk, warp r with its rows 16 r.. of the outputs and of the states.
 // Going back, dV is finished before dK is begun, so that one set of output accumulators is
-// live at a time. What bounds it is what bounds the forward: 334 products (2700 cycles) and
-// about 1600 other instructions a chunk and warp, which do not overlap, in 6900 cycles.
+// live at a time. What bounds it is what bounds the forward: 490 products (3900 cycles) and
+// about 1700 other instructions a chunk and warp, which do not overlap, in 8700 cycles.
 // Measured and not kept: a third CTA per SM in 168 registers (214 to 225 us for 196, more
 // barriers), eight warps in roles with half the registers each (248 us), two tiles of rows
 // a warp (298 us, spills).
 //
-// B4 H8 N16384 D = M = 64: states and gradients of segments 67 us, scans 11 us, this
-// kernel 196 us (888 MB moved: the second read of the tiles mostly misses L2, which
-// segments of 7 chunks avoid at the same time; tensor pipe 40%); the call 273 us against
-// 70 us for reading four tensors and writing four.
+// B4 H8 N16384 D = M = 64: states and gradients of segments 61 us, scans 11 us, this
+// kernel 246 us (888 MB moved: the second read of the tiles mostly misses L2, which
+// segments of 7 chunks avoid at the same time); the call 318 us against 70 us for reading
+// four tensors and writing four. With one bf16 term of each operand it took 269 us, and
+// gradients were off by 2.35e-3 (2-norm) instead of 1.66e-3, their own rounding.
 #include "la_gated.cuh"
 #include "la_gated_mma.cuh"
 #include "la_mma.cuh"
@@ -45,13 +46,12 @@ namespace {
 constexpr int kThreads = 128, kResident = 2, kMaxChunks = 16;
 constexpr int kTile = kC * 64 * 2;
 constexpr int kStage = 4 * kTile;  // Q, K, V, dO
-constexpr int kOp = kTile;         // S or E in bf16, [d][m], one of two; FINE: and their rest
+constexpr int kOp = kTile;         // a bf16 term of S or E, [d][m]
 // floats per parity of the chunk: the parts of dg (sums of X's columns, b, <S, E> by warp)
 constexpr int kParts = 2 * kC + 4;
-// two stages of tiles, the operand's two, outputs on their way out
-template <bool FINE>
-constexpr int kSmem = 2 * kStage + (FINE ? 4 : 2) * kOp + kTile + 2 * ((int)sizeof(GateTables) + 4 * kParts);
-static_assert(kResident * (kSmem<true> + 1024) <= 228 * 1024, "CTAs per SM");
+// two stages of tiles, the operand's two in two terms each, outputs on their way out
+constexpr int kSmem = 2 * kStage + 4 * kOp + kTile + 2 * ((int)sizeof(GateTables) + 4 * kParts);
+static_assert(kResident * (kSmem + 1024) <= 228 * 1024, "CTAs per SM");
 // scratch of a CTA for each chunk of a segment: S as the warps hold it, and q . dQ of each
 // token
 constexpr size_t kKept = 8 * kThreads * sizeof(float4), kScratch = kKept + kC * sizeof(float);
@@ -82,7 +82,6 @@ __device__ __forceinline__ void load_state(float (&x)[NT][4], const float* from,
     }
 }
 
-template <bool FINE>
 __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(const BwdArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t base = tc::smem_u32(smem);
@@ -92,10 +91,9 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
   // CTA, so that no scheduler gets all of the most
   const int rb = (warp + blockIdx.x) & 3, r0 = rb * 16;
   const Lane<64> ln;
-  constexpr int kOps = FINE ? 4 : 2;
   uint8_t* op_mem = smem + 2 * kStage;
-  const uint32_t op_base = base + 2 * kStage, out_at = op_base + kOps * kOp;
-  GateTables* tables = reinterpret_cast<GateTables*>(op_mem + kOps * kOp + kTile);
+  const uint32_t op_base = base + 2 * kStage, out_at = op_base + 4 * kOp;
+  GateTables* tables = reinterpret_cast<GateTables*>(op_mem + 4 * kOp + kTile);
   float* parts = reinterpret_cast<float*>(tables + 2);
   char* own = a.scratch + (size_t)blockIdx.x * (a.len / kC) * kScratch;
   float4* states = reinterpret_cast<float4*>(own) + tid;  // [chunk][8][thread]
@@ -130,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
     float x[8][4];  // S, then E
     auto keep_op = [&](int buf) {
       store_op(ln, op_base + buf * kOp, r0, 0, x);
-      if (FINE) store_op<true>(ln, op_base + (2 + buf) * kOp, r0, 0, x);
+      store_op<true>(ln, op_base + (2 + buf) * kOp, r0, 0, x);
     };
     load_state(x, a.S ? a.S + ((size_t)bh * (a.n_seg + 1) + seg) * DM : a.S0 ? a.S0 + bh * DM : nullptr,
                r0, 0, a.D, a.M);
@@ -148,12 +146,12 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       if (maker) raw = raw_gates(c + 1);
 #pragma unroll
       for (int j = 0; j < 8; ++j) states[(c * 8 + j) * kThreads] = keep_tile(x[j]);
-      uint32_t f[4][4], p[FINE ? 2 : 1][4];
+      uint32_t f[4][4], p[2][4];
       float d[8][4];
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) ln.load_a(f[ks], do_at, r0, ks);
       product<false>(ln, d, f, op_base + (c & 1) * kOp);
-      if (FINE) product<false, true>(ln, d, f, op_base + (2 + (c & 1)) * kOp);
+      product<false, true>(ln, d, f, op_base + (2 + (c & 1)) * kOp);
       float wi[2] = {t.in[r0 + row], t.in[r0 + row + 8]};
       scale_rows(d, wi[0] * t.before[rb], wi[1] * t.before[rb]);
       diagonal_block<true>(ln, p, f, v_at, rb, t.hi, t.lo);
@@ -229,12 +227,12 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
       if (c + 1 < chunks && warp == ((c + 1) & 3)) finish(c + 1);
       const float dec = t.decay;
       const int t0 = tb + c * kC + r0;
-      uint32_t f[4][4], p[FINE ? 2 : 1][4];
+      uint32_t f[4][4], p[2][4];
       float d[8][4];
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) ln.load_a(f[ks], k_at, r0, ks);
       product<true>(ln, d, f, op);
-      if (FINE) product<true, true>(ln, d, f, op + 2 * kOp);
+      product<true, true>(ln, d, f, op + 2 * kOp);
       float wj[2] = {t.out[r0 + row], t.out[r0 + row + 8]};
       scale_rows(d, wj[0] * t.behind[rb], wj[1] * t.behind[rb]);
       diagonal_block<false>(ln, p, f, q_at, rb, t.hi, t.lo);
@@ -263,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, kResident) gated_backward_kernel(con
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) ln.load_a(f[ks], v_at, k0, ks);
       product<false>(ln, d, f, op);
-      if (FINE) product<false, true>(ln, d, f, op + 2 * kOp);
+      product<false, true>(ln, d, f, op + 2 * kOp);
       scale_rows(d, wk[0] * t.behind[kb], wk[1] * t.behind[kb]);
       const float2 be = row_dots(ln, k_at, k0, d);
       diagonal_block<false>(ln, p, f, do_at, kb, t.hi, t.lo);
@@ -304,7 +302,7 @@ int backward_grid(const GatedPlan& p) {
 }  // namespace
 
 GatedPlan gated_mma_backward_plan(int BH, int N) {
-  return gated_mma_plan(BH, N, 1, GatedCosts{152 * kResident, kMaxChunks, 4.f, 7.f, 7.f, 3.4f});
+  return gated_mma_plan(BH, N, 1, GatedCosts{152 * kResident, kMaxChunks, 4.f, 8.7f, 7.f, 3.4f});
 }
 
 size_t gated_mma_backward_scratch(const GatedPlan& p) {
@@ -346,9 +344,7 @@ cudaError_t gated_mma_backward(const GatedBackward& f, const GatedPlan& p, const
   a.dS = f.dS;
   a.scratch = static_cast<char*>(w.scratch);
   const dim3 grid((unsigned)backward_grid(p));
-  return gated_fine(p.BH, p.N)
-             ? gated_launch<gated_backward_kernel<true>>(kSmem<true>, grid, kThreads, st, a)
-             : gated_launch<gated_backward_kernel<false>>(kSmem<false>, grid, kThreads, st, a);
+  return gated_launch<gated_backward_kernel>(kSmem, grid, kThreads, st, a);
 }
 
 }  // namespace la

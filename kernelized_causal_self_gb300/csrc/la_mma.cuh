@@ -222,6 +222,20 @@ __device__ __forceinline__ void load_tile(uint32_t base, const bf16* src, int ro
   }
 }
 
+// Rows r0 .. r0 + 15 of such a tile by one warp, from src on; `rows` of them, the others zero
+template <int COLS>
+__device__ __forceinline__ void load_rows(uint32_t base, int r0, const bf16* src, int rows, int width) {
+  constexpr int PER = COLS / 8, STEP = 32 / PER;
+  const int l = here(threadIdx.x & 31), row = l / PER, chunk = l % PER;
+#pragma unroll
+  for (int i = 0; i < 16 / STEP; ++i) {
+    const int r = row + i * STEP;
+    const bool live = chunk * 8 < width && r < rows;
+    cp_async16(base + (r0 + r) * COLS * 2 + ((chunk ^ (r & 7)) << 4),
+               live ? src + (size_t)r * width + chunk * 8 : src, live);
+  }
+}
+
 // Rows r0 .. r0 + 15 of a warp's 16 x 64 result, through those rows of the tile at `tile`
 // (the warp's own meanwhile), written in 16-byte pieces to rows of `width` elements at
 // dst; `live` rows of them, columns up to `width`.

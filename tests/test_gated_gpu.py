@@ -265,6 +265,35 @@ def test_resets_cost_the_tokens_behind_them_no_digits(la, shape, gate):
         assert np.all(each <= 0), (name, (each > 0).mean(), np.max(each / (a + 1e-30)))
 
 
+@pytest.mark.parametrize("gate", ["mixed", "slow"])
+@pytest.mark.parametrize("shape", [(2, 8, 1025, 64, 64), (20, 8, 130, 64, 64), (160, 8, 20, 64, 64),
+                                   (2, 8, 700, 128, 128), (4, 10, 333, 96, 64)], ids=ids)
+def test_calls_that_fill_the_multiprocessors_show_only_their_outputs_rounding(la, shape, gate):
+    """bf16: a sequence's outputs are as exact in a large batch as alone. A term keeps 16 bits in each
+    of two places, 2^-16 each (its chunk's operand or state, the state's own update); then the output
+    is rounded by half a step."""
+    q, k, v, g, do, S0, dS = _inputs(sum(shape) + 2, *shape, BF, gate)
+    B, H, N, D, M = shape
+    chain = N + D + M + 64
+    n64 = [_f64(t) for t in (q, k, v, g, do, S0, dS)]
+    size = [np.abs(x) for x in n64]
+    size[3] = n64[3]
+    bound = oracle.gated_backward(*size)
+    dots = np.sum(size[0] * bound[0] + size[1] * bound[1], axis=(-1, -2)) + \
+        np.sum(bound[4], axis=(-1, -2))
+    names = ("out", "out with S", "dq", "dk", "dv", "dg")
+    outs = (la.la_forward_gated(q, k, v, g, S0=S0), la.la_prefill_gated(q, k, v, g, S0=S0)[0],
+            *la.la_backward_gated(q, k, v, g, do, S0=S0, dS=dS)[:4])
+    want, a = oracle.gated_forward(*n64[:4], n64[5])[0], oracle.gated_forward(*size[:4], size[5])[0]
+    wants, sizes = (want, want, *oracle.gated_backward(*n64)[:4]), (a, a, *bound[:4])
+    for name, got, want, a in zip(names, outs, wants, sizes):
+        off = (2.0 ** -15 + chain * F32) * a
+        if name == "dg":
+            off = off + chain * F32 * dots[..., None]
+        each = np.abs(_f64(got) - want) - _half_step(np.abs(want) + off) - off
+        assert np.all(each <= 0), (name, (each > 0).mean(), np.max(each / (a + 1e-30)))
+
+
 def test_backward_with_only_one_of_the_states(la):
     q, k, v, g, do, S0, dS = _inputs(3, 1, 2, 100, 64, 64, BF)
     _backward_close(la, q, k, v, g, do, S0, None, BF)
