@@ -392,7 +392,7 @@ int la_workspace_wait_site(void* workspace, size_t workspace_bytes, void* stream
  *
  * g: [B][H][N] in `dtype`, natural logarithms, normally <= 0 (-inf empties the
  * state before its token is added). Growing states (g > 0) work while exp() of g's
- * sums over a segment of up to a few thousand tokens stays finite.
+ * sums over any 4096 successive tokens stays finite.
  * Everything else is laid out as for la_forward; states are float32 [B][H][D][M].
  * D, M: multiples of 8 in [8, 128]; N <= 2^30; dtype LA_F32 or LA_BF16. Sums and the
  * carried state are float32; in bf16 the tensor cores take the state and the weights within

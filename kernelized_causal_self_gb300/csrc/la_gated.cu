@@ -437,8 +437,9 @@ float walk_time(long long ctas, int per_sm, int len) {
 }
 
 // The segments with which the walks take least: several fill the GPU, but cost the state
-// passes (0.65 of a walk of outputs) and the scan first. At least 32 tokens each, a
-// backward's at most 512, over which dg's sum from the segment's end back keeps float32's
+// passes (0.65 of a walk of outputs) and the scan first. At least 32 tokens each, one of
+// several at most 4096 (its decay is one float32, which has to be finite where gates are
+// positive), a backward's at most 512, over which dg's sum from the segment's end back keeps float32's
 // accuracy. 128 tokens, D = M = 64, several segments and one: backward of 8 sequences 29 and
 // 45 us, of 152 109 and 68, of 600 363 and 212; forward of 60 28 and 36, of 600 143 and 67.
 GatedPlan plan_simt(int BH, int N, int D, int M, bool backward) {
@@ -450,6 +451,7 @@ GatedPlan plan_simt(int BH, int N, int D, int M, bool backward) {
   float shortest = -1.f;
   for (int k = 0; k <= 16; ++k) {
     long long n_seg = k == 0 ? 1 : k * 152LL / per;
+    if (n_seg > 1 && n_seg * 4096 < N) n_seg = (N + 4095) / 4096;
     if (n_seg > most) n_seg = most;
     if (n_seg < fewest) n_seg = fewest;
     const int len = N > 0 ? (int)(((N + n_seg - 1) / n_seg + kTok - 1) / kTok * kTok) : kTok;

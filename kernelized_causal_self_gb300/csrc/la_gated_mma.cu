@@ -93,7 +93,7 @@ struct WalkSmem {
 // EXACT: a chunk's update of X is summed apart, with its operand to 24 bits, and added in
 // float32 arithmetic that rounds (the tensor cores' own sums truncate, which over
 // thousands of chunks would leave a bias in a state that hardly decays). Taken where X
-// leaves the kernel as a float32 result; where it only goes on as an operand of two bf16
+// leaves the kernel as a float32 result and in long segments; where it only goes on as an operand of two bf16
 // terms, 16 bits and sums in place do, and leave registers for more CTAs per SM.
 // DOTS: the parts of the gates' gradient.
 template <int DZ, bool OUT, bool REV, bool EXACT, bool DOTS = false>
@@ -413,6 +413,10 @@ gated_chunk_dg_kernel(const float* __restrict__ dot_q, const float* __restrict__
 
 }  // namespace
 
+// One of several segments has at most 64 chunks, 4096 tokens: its decay is one float32, which has
+// to be finite where gates are positive, and its state is summed in place by the tensor cores.
+constexpr int kJoined = 64;
+
 GatedPlan gated_mma_plan(int BH, int N, int blocks, const GatedCosts& k) {
   const long long chunks = N > 0 ? (N + kC - 1) / kC : 1, per = (long long)BH * blocks;
   GatedPlan best{BH, N, (int)chunks * kC, 1};
@@ -424,6 +428,7 @@ GatedPlan gated_mma_plan(int BH, int N, int blocks, const GatedCosts& k) {
     if (w > 32) n_seg = (chunks + (512 >> (w - 28)) - 1) / (512 >> (w - 28));
     if (k.most > 0 && n_seg * k.most < chunks) n_seg = (chunks + k.most - 1) / k.most;
     if (n_seg < 1) n_seg = 1;
+    if (n_seg > 1 && n_seg * kJoined < chunks) n_seg = (chunks + kJoined - 1) / kJoined;
     if (n_seg > chunks) n_seg = chunks;
     const long long len = (chunks + n_seg - 1) / n_seg;
     n_seg = (chunks + len - 1) / len;
@@ -505,14 +510,18 @@ cudaError_t gated_mma_forward(const GatedForward& f, const GatedPlan& p, const G
     a.init = f.S0;
     a.fin = f.S;
   }
-  if (f.D <= 64) return a.fin ? launch_forward<64, true>(a, st) : launch_forward<64, false>(a, st);
-  return a.fin ? launch_forward<128, true>(a, st) : launch_forward<128, false>(a, st);
+  // A sequence of one segment may be of any length: from 16384 tokens on its state is summed as a
+  // result is. (456 sequences of positive terms, hardly forgotten: with sums in place outputs were
+  // 3e-5 too small there, 3.6e-4 at 65536 and 5.4e-4 at 131072 tokens; 17% of the time.)
+  const bool exact = a.fin || (p.n_seg == 1 && p.N > 16384);
+  if (f.D <= 64) return exact ? launch_forward<64, true>(a, st) : launch_forward<64, false>(a, st);
+  return exact ? launch_forward<128, true>(a, st) : launch_forward<128, false>(a, st);
 }
 
 // ---- the backward for D or M over 64: states, scans, then dQ, dK and dV a walk each
 
 GatedPlan gated_mma_wide_plan(int BH, int N, int D, int M) {
-  return gated_mma_plan(BH, N, ((D > M ? D : M) + 63) / 64, GatedCosts{2 * 152, 0, 9.f, 18.5f, 12.f, 5.f});
+  return gated_mma_plan(BH, N, ((D > M ? D : M) + 63) / 64, GatedCosts{2 * 152, kJoined, 9.f, 18.5f, 12.f, 5.f});
 }
 
 namespace {

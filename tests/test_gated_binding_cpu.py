@@ -209,6 +209,21 @@ def test_abi_refuses_states_that_share_memory(lib):
     assert fwd(FAKE, FAKE) == la.LA_ERR_WORKSPACE and fwd(FAKE, far) == la.LA_ERR_WORKSPACE
 
 
+@pytest.mark.parametrize("BH,N", [(1, 8192), (16, 1 << 18), (16, 1 << 20), (8, 1 << 20), (3, 1 << 24), (200, 1 << 20)])
+def test_one_of_several_segments_has_at_most_4096_tokens(lib, BH, N):
+    """So that exp() of a segment's gates is finite where la.h says so, and a state's sums are short.
+    The workspace tells the segments: a state of each and one more of every sequence."""
+    for dt, D, M in ((la.LA_BF16, 64, 64), (la.LA_BF16, 128, 128), (la.LA_F32, 64, 64), (la.LA_F32, 128, 128)):
+        bytes_ = la.la_gated_workspace_bytes(1, BH, N, D, M, dt)
+        segments = 1 if bytes_ == 256 else bytes_ // (4 * BH * D * M) - 1
+        assert segments == 1 or segments * 4096 >= N, (dt, D, segments)
+    D = 128  # the backward of wide heads joins states and gradients, however few the segments
+    bytes_ = la.la_gated_backward_workspace_bytes(1, BH, N, D, D, la.LA_BF16)
+    chunks = (N + 63) // 64
+    scratch = BH * (chunks * (4 * 64 * 1024 // 4 + 32) + 3 * 2 * 4 * N)
+    assert (bytes_ - scratch) // (2 * 4 * BH * D * D) - 1 >= N // 4096
+
+
 def test_binding_refuses_states_that_share_memory():
     q, v, g, S = _t(2, 3, 10, 16), _t(2, 3, 10, 8), _t(2, 3, 10), _t(3, 3, 16, 8, dtype=F32)
     _raises("dS0 shares memory with S0", la.la_backward_gated, q, q, v, g, v, S0=S[:2], dS0=S[:2])

@@ -351,6 +351,44 @@ def test_the_same_slow_gate_at_every_token(la):
         assert rel <= count ** 0.5 * step, (name, rel)
 
 
+@pytest.mark.parametrize("gate", [-1e-6, 0.02], ids=["hardly forgotten", "growing"])
+def test_long_sequences_in_few_segments(la, gate):
+    """bf16. Sums that truncate would leave every output of a state that hardly decays too small: the
+    outputs' mean relative error is that of n roundings of either sign, each below 2^-8 / sqrt(3),
+    and of operands that are rounded at 2^-17. Growing: the gates of 4096 tokens sum to 82, those of
+    the call to far more than a float32 exponential takes."""
+    if gate < 0:  # as many sequences as fill the GPU, each one segment
+        few, B, N = 4, 456, 1 << 16
+    else:
+        few, B, N = 1, 16, 1 << 18
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    q, k, v = (torch.rand((few, 1, N, 64), generator=gen, device=DEV).to(BF) for _ in range(3))
+    g = torch.full((few, 1, N), gate, device=DEV).to(BF)
+    if gate > 0:
+        # the state is emptied in the end, so that the results are finite
+        g[:, :, -5] = -torch.inf
+        k[:, :, :-5], q[:, :, :-5] = 0, 0
+    want = oracle.gated_forward(*(_f64(x[:, :, -8192:]) for x in (q, k, v, g)),
+                                None if gate > 0 else _early_state(k, v, g, N - 8192))[0]
+    rows = [x.expand(B // few, few, *x.shape[1:]).reshape(B, *x.shape[1:]).contiguous() for x in (q, k, v, g)]
+    out = la.la_forward_gated(*rows)
+    assert torch.isfinite(out).all()
+    tail = _f64(out[:few, :, -64:]) if gate < 0 else _f64(out[:few, :, -5:])
+    want = want[:, :, -tail.shape[2]:]
+    off = (tail - want) / want
+    assert np.all(np.abs(off) <= 2.0 ** -8 + 2.0 ** -12)
+    assert abs(off.mean()) <= 2.0 ** -16 + 5 * 2.0 ** -8 / (3 * off.size) ** 0.5
+    for b in range(few, B, few):
+        assert torch.equal(out[b:b + few], out[:few])
+
+
+def _early_state(k, v, g, n):
+    """The state after the first n tokens in float64: sums of k_t v_t^T, each left to decay."""
+    k, v, g = (x[:, :, :n].double() for x in (k, v, g))
+    left = torch.exp(g.flip(2).cumsum(2).flip(2) - g)
+    return torch.einsum("bhnd,bhnm->bhdm", k * left[..., None], v).cpu().numpy()
+
+
 # ------------------------------------------------------------------------ serving
 
 @pytest.mark.parametrize("dtype", [BF, FL], ids=["bf16", "f32"])
