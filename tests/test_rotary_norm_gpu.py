@@ -197,6 +197,38 @@ def test_norm_gate_and_gradients(la, shape, dtype, heads, token_major):
         assert torch.equal(a, b)
 
 
+def test_float32_norm_gate_keeps_its_digits_at_every_gate(la):
+    """Gates from -86 to 86 (where z sigmoid(z) is a normal float32). In half steps of 2^-24: the mean
+    of M squares (M + 1 roundings, halved by the root), rsqrt (4), expf (4), the sigmoid's sum and
+    quotient (5), products and the result (6): M / 2 + 20 in all; dz's sum of two terms and its
+    factor 1 - s add 8, of the absolute terms."""
+    H, M = 173, 8
+    x, _, w, dy = _norm_inputs(9, 1, H, 1, M, FL, True, False)
+    z = torch.linspace(-86, 86, H * M, device=DEV).view(1, H, 1, M)
+    y = la.la_norm_gate(x, z, w)
+    dx, dz, dw = la.la_norm_gate_backward(x, z, w, dy)
+    x6, z6, w6, dy6 = map(_f64, (x, z, w, dy))
+    f, grow = 2.0 ** -24, M / 2 + 20
+    want = oracle.norm_gate(x6, z6, w6)
+    assert np.all(np.abs(_f64(y) - want) <= grow * f * np.abs(want))
+    wdx, wdz, wdw = oracle.norm_gate_backward(x6, z6, w6, dy6)
+    assert np.all(np.abs(_f64(dw) - wdw) <= grow * f * np.abs(wdw))
+    n = np.abs(x6) / np.sqrt(np.mean(x6 * x6, -1, keepdims=True) + 1e-6)
+    s = np.where(z6 > 0, 1.0 / (1.0 + np.exp(-np.abs(z6))), np.exp(-np.abs(z6)) / (1.0 + np.exp(-np.abs(z6))))
+    size = np.abs(dy6 * w6[None, :, None]) * n * s * (1.0 + np.abs(z6) / (1.0 + np.exp(z6)))
+    assert np.all(np.abs(_f64(dz) - wdz) <= (grow + 8) * f * size)
+
+
+def test_gates_that_are_all_but_closed(la):
+    """As far as exp(z) is a normal float32 (in bf16 its next step down is not)."""
+    for dtype, low in ((FL, -87.3), (BF, -87.0)):
+        x, _, w, _ = _norm_inputs(3, 1, 1, 40, 64, dtype, False, False)
+        z = torch.linspace(low, -86.0, 40 * 64, device=DEV).view(1, 1, 40, 64).to(dtype)
+        want = oracle.norm_gate(*map(_f64, (x, z, w)))
+        got = _f64(la.la_norm_gate(x, z, w))
+        assert np.all(np.abs(got - want) <= (HALF[dtype] + 2.0 ** -14) * np.abs(want) + 2.0 ** -125)
+
+
 def test_norm_gate_of_more_heads_than_a_grid_is_high(la):
     """w's gradient per head: one term each, dy n z s; a dozen float32 operations."""
     x, z, w, dy = _norm_inputs(4, 1, 70001, 1, 8, FL, True, False)
