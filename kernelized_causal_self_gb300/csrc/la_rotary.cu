@@ -9,8 +9,9 @@
 // Angles: a float32 product pos * freq loses the angle at far positions (2^-24 of
 // 10^6 radians is 0.06). Here a frequency is a fraction of a turn in 64-bit fixed
 // point, so the phase pos * freq modulo one turn is one wrapping integer product,
-// off by at most |pos| 2^-54 turns (the float64 frequency's own rounding); its top
-// 32 bits, as a signed number of half turns, go to sincospif.
+// off by at most |pos| 2^-54 turns (the float64 frequency's own rounding); of its top
+// 32 bits, what is left of the nearest quarter turn goes to sincospif (of a whole half
+// turn, float32 keeps 9e-8 radians; of an eighth of a turn 2.3e-8).
 //
 // Bound by memory: q and k are read and written once. A thread owns a few pairs of
 // one token, works out their cosines and sines once and applies them to up to 8 heads of
@@ -33,10 +34,16 @@ __device__ __forceinline__ unsigned long long turn_step(double freq) {
 
 __device__ __forceinline__ void turn(unsigned long long step, long long pos, float mscale,
                                      float& c, float& s) {
-  const unsigned long long phase = step * (unsigned long long)pos;
-  sincospif((float)(int)(phase >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31 half turns
-  c *= mscale;
-  s *= mscale;
+  const unsigned top = (unsigned)(step * (unsigned long long)pos >> 32);
+  const unsigned quarters = (top + 0x20000000u) >> 30;  // the nearest: an eighth of a turn is left
+  const int rest = (int)(top - (quarters << 30));
+  float rc, rs;
+  sincospif((float)rest * 4.656612873077393e-10f, &rs, &rc);  // 2^-31 half turns
+  c = quarters & 1 ? -rs : rc;
+  s = quarters & 1 ? rc : rs;
+  const float scale = quarters & 2 ? -mscale : mscale;
+  c *= scale;
+  s *= scale;
 }
 
 struct RotaryArgs {

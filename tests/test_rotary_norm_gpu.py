@@ -130,6 +130,26 @@ def test_rotary_scaled_for_long_contexts(la, scaling):
     assert np.all(np.abs(_f64(far) - want) <= 1e-3 * np.abs(_f64(q)).max())
 
 
+@pytest.mark.parametrize("interleaved", [False, True], ids=["half", "interleaved"])
+def test_rotary_turns_by_the_angle_to_float32s_digits(la, interleaved):
+    """float32, pairs (a, 0), whose results are a cos and a sin. In half steps, 2^-24: 2 of the
+    function, 1 of the product. The angle: its top 32 bits (2^-32 turns), 2^-27 half turns where an
+    eighth of a turn is converted to float32, and 2^-54 turns a token: below 2^-25.2 radians."""
+    N, D = 3000, 64
+    q = _randn(11, 1, 2, N, D)
+    q[..., (slice(1, None, 2) if interleaved else slice(D // 2, None))] = 0.0
+    freqs, _ = la.la_rotary_freqs(D, device=DEV)
+    pos = torch.randint(-2 ** 20, 2 ** 20, (N,), device=DEV, dtype=torch.int32,
+                        generator=torch.Generator(device=DEV).manual_seed(3))
+    got = _f64(la.la_rotary(q, None, freqs, positions=pos, interleaved=interleaved)[0])
+    kw = dict(interleaved=interleaved)
+    want = oracle.rotary(_f64(q), pos.cpu().numpy(), _f64(freqs), **kw)
+    pairs = (lambda x: (x[..., 0::2], x[..., 1::2])) if interleaved else (lambda x: (x[..., :D // 2], x[..., D // 2:]))
+    (c, s), (gc, gs) = pairs(want), pairs(got)
+    for g, w, other in ((gc, c, s), (gs, s, c)):
+        assert np.all(np.abs(g - w) <= 3 * 2.0 ** -24 * np.abs(w) + 2.0 ** -25.2 * np.abs(other) + 1e-37)
+
+
 def test_rotary_past_32_bits(la):
     """The last tokens of a tensor of more than 2^31 elements, in place."""
     N = 2 ** 31 // 128 + 100
