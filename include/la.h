@@ -465,7 +465,7 @@ int la_backward_gated(const void* q, const void* k, const void* v, const void* g
  * input (same pointer and strides).
  * freqs: device double[R/2], radians per token. positions: device int[N] (or one
  * row of N per batch entry, pos_stride_b entries apart; 0: shared), any sign;
- * nullptr: offset + token index.
+ * nullptr: offset + token index, offset within +-2^62.
  * D: a multiple of 8 in [8, 128]; R even in [2, D]; B <= 65535.
  */
 int la_rotary(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides,

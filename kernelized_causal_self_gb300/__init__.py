@@ -970,6 +970,8 @@ def la_rotary(q, k, freqs, positions=None, offset=0, interleaved=False, mscale=1
         ks = _row_strides(fn, "k", k, packed)
     if freqs.dtype != torch.float64 or len(freqs.shape) != 1 or not freqs.is_contiguous():
         raise ValueError(f"{fn}: freqs must be a contiguous float64 tensor of R/2 entries")
+    if not -2 ** 62 <= offset <= 2 ** 62 or offset != int(offset):
+        raise ValueError(f"{fn}: offset must be a whole number within +-2^62")
     pos_b = 0
     if positions is not None:
         p = positions.shape

@@ -145,6 +145,8 @@ int la_rotary(const void* q, const long long* q_strides, void* q_out, const long
   if (!dtype_ok(dtype) || B < 1 || B > 65535 || H < 1 || Hk < 0 || N < 0 || !dim_ok(D) || R < 2 ||
       R > D || R % 2 != 0 || (long long)H + Hk > 65535)
     return LA_ERR_INVALID_ARG;
+  // (a position is offset + token)
+  if (offset > 1LL << 62 || offset < -(1LL << 62)) return LA_ERR_INVALID_ARG;
   if (N == 0) return LA_OK;
   const uintptr_t e = dtype == LA_F32 ? 4 : 2;
   if (q == nullptr || q_out == nullptr || !aligned(q, e) || !aligned(q_out, e) ||

@@ -209,6 +209,20 @@ def test_abi_refuses_states_that_share_memory(lib):
     assert fwd(FAKE, FAKE) == la.LA_ERR_WORKSPACE and fwd(FAKE, far) == la.LA_ERR_WORKSPACE
 
 
+def test_rotary_refuses_offsets_that_are_no_position(lib):
+    q, f, s = _t(1, 2, 4, 16), torch.zeros(4, dtype=torch.float64), (ctypes.c_longlong * 3)(64, 64, 64)
+    for offset in (2 ** 64, 2 ** 62 + 1, -2 ** 62 - 1, -2 ** 70):
+        _raises("offset", la.la_rotary, q, None, f, offset=offset)
+    _raises("offset", la.la_rotary, q, None, f, offset=1.5)
+    _raises("CUDA device", la.la_rotary, q, None, f, offset=2 ** 62)
+
+    def rot(offset, N):
+        return lib.la_rotary(FAKE, s, FAKE, s, None, None, None, None, FAKE, None, 0, offset, 1, 1, 0, N, 64, 64,
+                             0, 0, 1.0, 1, None)
+    assert rot(2 ** 62 + 1, 0) == la.LA_ERR_INVALID_ARG and rot(-2 ** 63, 0) == la.LA_ERR_INVALID_ARG
+    assert rot(2 ** 62, 0) == la.LA_OK and rot(-2 ** 62, 0) == la.LA_OK
+
+
 @pytest.mark.parametrize("BH,N", [(1, 8192), (16, 1 << 18), (16, 1 << 20), (8, 1 << 20), (3, 1 << 24), (200, 1 << 20)])
 def test_one_of_several_segments_has_at_most_4096_tokens(lib, BH, N):
     """So that exp() of a segment's gates is finite where la.h says so, and a state's sums are short.
