@@ -10,7 +10,7 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
-#include "la_tc.cuh"
+#include "la_tc_common.cuh"
 
 namespace la {
 namespace mma {
@@ -108,28 +108,9 @@ __device__ __forceinline__ void mma16816_0(float (&c)[4], const uint32_t (&a)[4]
 __device__ __forceinline__ float2& pair_of(float (&c)[4], int h) {
   return *reinterpret_cast<float2*>(&c[2 * h]);
 }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
-        "l"(*reinterpret_cast<uint64_t*>(&c)));
-  return *reinterpret_cast<float2*>(&d);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
-  return *reinterpret_cast<float2*>(&d);
-}
-__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
-  uint64_t d;
-  asm("sub.rn.f32x2 %0, %1, %2;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
-  return *reinterpret_cast<float2*>(&d);
-}
+using tcx::fma2;
+using tcx::mul2;
+using tcx::sub2;
 
 template <int NT>
 __device__ __forceinline__ void scale_rows(float (&c)[NT][4], float top, float bottom) {
