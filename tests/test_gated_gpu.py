@@ -601,6 +601,51 @@ def test_captured_and_replayed_on_new_inputs(la):
             assert torch.equal(o, w)
 
 
+@pytest.mark.parametrize("dtype", [BF, FL], ids=["bf16", "f32"])
+def test_serving_calls_captured_and_replayed_at_once(la, dtype):
+    """Two graphs, each of an extend and a decode step on its own pool, replayed on two streams with
+    new tokens, slots and lengths: the same as the calls themselves."""
+    B, H, N, D, P = 6, 4, 90, 64, 20
+    runs = []
+    for seed in (1, 2):
+        q, k, v, g, *_ = _inputs(seed, B, H, N, D, D, dtype)
+        q1, k1, v1, g1 = (x[:, :, 0].contiguous() for x in _inputs(seed + 10, B, H, 1, D, D, dtype)[:4])
+        gen = torch.Generator(device=DEV).manual_seed(seed)
+        pool = torch.randn((P, H, D, D), generator=gen, device=DEV)
+        slots = torch.arange(B, dtype=torch.int32, device=DEV)
+        lens = torch.full((B,), N, dtype=torch.int32, device=DEV)
+        out = torch.zeros_like(v)
+
+        def step(q=q, k=k, v=v, g=g, one=(q1, k1, v1, g1), pool=pool, slots=slots, lens=lens, out=out):
+            la.la_extend_gated(q, k, v, g, pool, slots=slots, lens=lens, out=out)
+            return out, la.la_decode_step_gated(*one, pool, slots=slots)
+        start = pool.clone()
+        step()
+        stream = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            got = step()
+        # what the replay finds: other tokens, slots (one of no entry) and lengths
+        q.copy_(_inputs(seed + 20, B, H, N, D, D, dtype)[0])
+        slots.copy_(torch.tensor([7, 19, 3, -1, 0, 11], dtype=torch.int32))
+        lens.copy_(torch.tensor([0, 1, 64, 65, N, 17], dtype=torch.int32))
+        pool.copy_(start)
+        out.fill_(3.0)
+        want = [x.clone() for x in step()] + [pool.clone()]
+        pool.copy_(start)
+        out.fill_(3.0)
+        runs.append((graph, stream, (*got, pool), want, step))  # (step holds the inputs)
+    torch.cuda.synchronize()
+    for graph, stream, *_ in runs:
+        with torch.cuda.stream(stream):
+            graph.replay()
+    torch.cuda.synchronize()
+    for _, _, got, want, _ in runs:
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------ the layer as it is used
 
 def test_layer_of_the_three_operators(la):
