@@ -396,8 +396,7 @@ int la_workspace_wait_site(void* workspace, size_t workspace_bytes, void* stream
  * Everything else is laid out as for la_forward; states are float32 [B][H][D][M].
  * D, M: multiples of 8 in [8, 128]; N <= 2^30; dtype LA_F32 or LA_BF16. Sums and the
  * carried state are float32; in bf16 the tensor cores take the state and the weights within
- * a chunk of tokens as two bf16 terms, 16 bits, of which an output in bf16 shows nothing
- * (gradients of up to 16 tokens: in float32).
+ * a chunk of tokens as two bf16 terms, 16 bits, of which an output in bf16 shows nothing.
  */
 
 /* Scratch needed by la_forward_gated and la_extend_gated, in bytes; where it is 256 (the

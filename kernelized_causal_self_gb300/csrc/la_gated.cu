@@ -444,7 +444,7 @@ float walk_time(long long ctas, int per_sm, int len) {
 // several at most 4096 (its decay is one float32, which has to be finite where gates are
 // positive), a backward's at most 512, over which dg's sum from the segment's end back keeps float32's
 // accuracy. 128 tokens, D = M = 64, several segments and one: backward of 8 sequences 29 and
-// 45 us, of 152 109 and 68, of 600 363 and 212; forward of 60 28 and 36, of 600 143 and 67.
+// 45 us, of 152 109 and 67, of 600 363 and 208; forward of 60 28 and 36, of 600 143 and 68.
 GatedPlan plan_simt(int BH, int N, int D, int M, bool backward) {
   const Columns c = columns(D, M);
   const int per_sm = walks_per_sm(c.parts, c.each);
@@ -711,26 +711,37 @@ size_t gated_forward_workspace(int BH, int N, int D, int M, int dtype) {
   return carve(nullptr, forward_plan(BH, N, D, M, dtype), D, M, false, 0).bytes;
 }
 
-// A backward of a few tokens does too: the tensor cores' chunks cost the same for 1 token
-// as for 64. D = M = 64, 1 and 512 sequences of 4 tokens 10 and 30 us (on the tensor cores
-// 11 and 60), of 16 tokens 14 and 45 (11 and 60), of 32 tokens 19 and 66; D = M = 128: 10 and
-// 115 (26 and 289), 15 and 209 (26 and 291), 22 and 367 (26 and 295).
+// A backward of a few tokens does too, where the tensor cores take several launches: their
+// chunks cost the same for 1 token as for 64. Up to 64 columns and without dS0 they take one,
+// and are faster for 2 tokens on. 512 sequences of 1, 4 and 16 tokens, us (on the tensor cores):
+// D = M = 64 without dS0 16, 20, 35 (17, 17, 17), with it 27, 31, 48 (65, 65, 66); 128 60, 85,
+// 184 (268, 268, 271). One sequence: 6, 8, 12 (7, 7, 7), 8, 10, 14 (11, 12, 12) and 6, 8, 13
+// (27, 27, 28).
 constexpr int kShort = 16;
-static bool backward_walks(int N, int dtype) { return dtype == LA_F32 || N <= kShort; }
-
-static GatedPlan backward_plan(int BH, int N, int D, int M, int dtype) {
-  if (backward_walks(N, dtype)) return plan_simt(BH, N, D, M, true);
-  return D <= 64 && M <= 64 ? gated_mma_backward_plan(BH, N) : gated_mma_wide_plan(BH, N, D, M);
+static bool one_launch(int D, int M) { return D <= 64 && M <= 64; }
+static bool backward_walks(int N, int D, int M, int dtype, bool dS0) {
+  return dtype == LA_F32 || (N <= kShort && (N == 1 || dS0 || !one_launch(D, M)));
 }
 
-static GatedWorkspace backward_workspace(void* ws, const GatedPlan& p, int D, int M, int dtype) {
-  if (backward_walks(p.N, dtype)) return carve(ws, p, D, M, true, backward_dots(D, M));
+static GatedPlan backward_plan(int BH, int N, int D, int M, bool walks) {
+  if (walks) return plan_simt(BH, N, D, M, true);
+  return one_launch(D, M) ? gated_mma_backward_plan(BH, N) : gated_mma_wide_plan(BH, N, D, M);
+}
+
+static GatedWorkspace backward_workspace(void* ws, const GatedPlan& p, int D, int M, bool walks) {
+  if (walks) return carve(ws, p, D, M, true, backward_dots(D, M));
   return carve(ws, p, D, M, true, 0,
-               D <= 64 && M <= 64 ? gated_mma_backward_scratch(p) : gated_mma_wide_scratch(p, D, M));
+               one_launch(D, M) ? gated_mma_backward_scratch(p) : gated_mma_wide_scratch(p, D, M));
 }
 
 size_t gated_backward_workspace(int BH, int N, int D, int M, int dtype) {
-  return backward_workspace(nullptr, backward_plan(BH, N, D, M, dtype), D, M, dtype).bytes;
+  size_t most = 0;
+  for (const bool dS0 : {false, true}) {
+    const bool walks = backward_walks(N, D, M, dtype, dS0);
+    const size_t bytes = backward_workspace(nullptr, backward_plan(BH, N, D, M, walks), D, M, walks).bytes;
+    if (bytes > most) most = bytes;
+  }
+  return most;
 }
 
 cudaError_t gated_forward(const GatedForward& f, void* ws, cudaStream_t st) {
@@ -740,12 +751,13 @@ cudaError_t gated_forward(const GatedForward& f, void* ws, cudaStream_t st) {
 }
 
 cudaError_t gated_backward(const GatedBackward& f, void* ws, cudaStream_t st) {
-  const GatedPlan p = backward_plan(f.B * f.H, f.N, f.D, f.M, f.dtype);
-  const GatedWorkspace w = backward_workspace(ws, p, f.D, f.M, f.dtype);
-  if (backward_walks(f.N, f.dtype))
+  const bool walks = backward_walks(f.N, f.D, f.M, f.dtype, f.dS0 != nullptr);
+  const GatedPlan p = backward_plan(f.B * f.H, f.N, f.D, f.M, walks);
+  const GatedWorkspace w = backward_workspace(ws, p, f.D, f.M, walks);
+  if (walks)
     return f.dtype == LA_F32 ? simt_backward<float>(f, p, w, st)
                              : simt_backward<__nv_bfloat16>(f, p, w, st);
-  return f.D <= 64 && f.M <= 64 ? gated_mma_backward(f, p, w, st) : gated_mma_wide_backward(f, p, w, st);
+  return one_launch(f.D, f.M) ? gated_mma_backward(f, p, w, st) : gated_mma_wide_backward(f, p, w, st);
 }
 
 cudaError_t gated_decode(const void* q, const void* k, const void* v, const void* g, float* S,
