@@ -442,8 +442,8 @@ float walk_time(long long ctas, int per_sm, int len) {
 // The segments with which the walks take least: several fill the GPU, but cost the state
 // passes (0.65 of a walk of outputs) and the scan first. At least 32 tokens each, one of
 // several at most 4096 (its decay is one float32, which has to be finite where gates are
-// positive), a backward's at most 512, over which dg's sum from the segment's end back keeps float32's
-// accuracy. 128 tokens, D = M = 64, several segments and one: backward of 8 sequences 29 and
+// positive), a backward's at most 512, over which dg's sum from the segment's end back keeps
+// float32's accuracy. 128 tokens, D = M = 64, several segments and one: backward of 8 sequences 29 and
 // 45 us, of 152 109 and 67, of 600 363 and 208; forward of 60 28 and 36, of 600 143 and 68.
 GatedPlan plan_simt(int BH, int N, int D, int M, bool backward) {
   const Columns c = columns(D, M);

@@ -93,8 +93,9 @@ struct WalkSmem {
 // EXACT: a chunk's update of X is summed apart, with its operand to 24 bits, and added in
 // float32 arithmetic that rounds (the tensor cores' own sums truncate, which over
 // thousands of chunks would leave a bias in a state that hardly decays). Taken where X
-// leaves the kernel as a float32 result and in long segments; where it only goes on as an operand of two bf16
-// terms, 16 bits and sums in place do, and leave registers for more CTAs per SM.
+// leaves the kernel as a float32 result and in long segments; where it only goes on as an
+// operand of two bf16 terms, 16 bits and sums in place do, and leave registers for more
+// CTAs per SM.
 // DOTS: the parts of the gates' gradient.
 template <int DZ, bool OUT, bool REV, bool EXACT, bool DOTS = false>
 __device__ __forceinline__ void walk_chunks(const WalkArgs& a) {
