@@ -59,6 +59,10 @@ enum la_status {
 
 enum la_dtype { LA_F32 = 0, LA_BF16 = 1 };
 
+/* Activations of la_ffn_gate: a sigmoid(a); a Phi(a) with the normal distribution Phi, and with
+ * its approximation (1 + tanh(sqrt(2 / pi) (a + 0.044715 a^3))) / 2. */
+enum la_activation { LA_SILU = 0, LA_GELU = 1, LA_GELU_TANH = 2 };
+
 /* Human-readable text for a status code; never NULL. */
 const char* la_status_string(int status);
 
@@ -498,6 +502,76 @@ int la_norm_gate_backward(const void* x, const void* z, const long long* z_strid
                           const long long* dz_strides, void* dw, int B, int H, int N, int M,
                           int w_per_head, float eps, int dtype, void* workspace,
                           size_t workspace_bytes, void* stream);
+
+/*
+ * The feed-forward half of a layer. Rows are tokens: x_stride and the other *_stride are the
+ * distances in elements from row to row, at least the row's length and multiples of 16 bytes;
+ * a row's elements are contiguous. Pointers are 16-byte aligned, row lengths C and F multiples
+ * of 8 up to 65536. Sums are float32; results are rounded to `dtype` once.
+ *
+ * Activations in 8 bits (checkpoints): codes, whole numbers of -127 .. 127, and for each block of
+ * 32 neighbours of a row (the last block may be shorter) a byte e, the exponent of the block's
+ * step 2^(e - 127): the smallest step, from e = 1 on, for which every |value| / step is below
+ * 127.5. Code i stands for code * step, its value rounded to the nearest step, ties to the even
+ * code. A block with an infinity or a NaN has e = 255 and restores as NaN throughout.
+ * codes [rows][C], 16-byte aligned; exps [rows][ceil(C / 32)].
+ */
+
+/* la_checkpoint -- puts x away. la_checkpoint_restore -- writes what the codes stand for. Bytes
+ * that la_checkpoint did not write are read as the formula says, e = 0 as a step of zero. */
+int la_checkpoint(const void* x, long long x_stride, signed char* codes, unsigned char* exps, long long rows,
+                  int C, int dtype, void* stream);
+int la_checkpoint_restore(const signed char* codes, const unsigned char* exps, void* x, long long x_stride,
+                          long long rows, int C, int dtype, void* stream);
+
+/*
+ * la_layer_norm -- y = (x - mean) / sqrt(var + eps) * w + b, mean and variance over the C
+ * elements of each row (C <= 16384; var is the mean of squared deviations). w, b: [C] (b may be
+ * nullptr: zero). y may be x itself (same pointer and stride), and shares memory with no other
+ * argument. codes, exps: a checkpoint of x to be written, or nullptr both. eps >= 0.
+ */
+int la_layer_norm(const void* x, long long x_stride, const void* w, const void* b, void* y, long long y_stride,
+                  signed char* codes, unsigned char* exps, long long rows, int C, float eps, int dtype,
+                  void* stream);
+
+/* Scratch needed by la_layer_norm_backward, in bytes. */
+size_t la_layer_norm_workspace_bytes(long long rows, int C);
+
+/*
+ * la_layer_norm_backward -- dx, dw [C] and db [C] from dy, all in `dtype`; dw and db are summed in
+ * a fixed order. The norm's input is x, or what a checkpoint stands for (x nullptr; codes, exps):
+ * exactly one of the two is given. dx may be x or dy itself. rows == 0 writes dw = db = 0.
+ */
+int la_layer_norm_backward(const void* x, long long x_stride, const signed char* codes, const unsigned char* exps,
+                           const void* w, const void* dy, long long dy_stride, void* dx, long long dx_stride,
+                           void* dw, void* db, long long rows, int C, float eps, int dtype, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Scratch needed by la_ffn_gate and la_ffn_gate_backward, in bytes. */
+size_t la_ffn_gate_workspace_bytes(int T, int C, int F, int dtype);
+size_t la_ffn_gate_backward_workspace_bytes(int T, int C, int F, int dtype);
+
+/*
+ * la_ffn_gate -- both projections of a gated feed-forward block, its activation and their
+ * product: h = act(a) * u with a = x wg^T and u = x wu^T. x: T rows of C; wg, wu [F][C]
+ * contiguous; h: T rows of F. act: enum la_activation. T <= 2^24. codes [T][2][F], exps
+ * [T][2][ceil(F / 32)]: a checkpoint of a and u to be written, or nullptr both. Outputs share no
+ * memory with inputs.
+ */
+int la_ffn_gate(const void* x, long long x_stride, const void* wg, const void* wu, void* h, long long h_stride,
+                signed char* codes, unsigned char* exps, int T, int C, int F, int act, int dtype, void* workspace,
+                size_t workspace_bytes, void* stream);
+
+/*
+ * la_ffn_gate_backward -- dx (T rows of C) and dwg, dwu [F][C] of sum(dh * h), in `dtype`. a and u
+ * are recomputed from x, or taken from a checkpoint (codes, exps) if one is given; either way
+ * da = dh u act'(a) and du = dh act(a) are rounded to `dtype` before dx = da wg + du wu,
+ * dwg = da^T x and dwu = du^T x are summed from them. T == 0 writes dwg = dwu = 0.
+ */
+int la_ffn_gate_backward(const void* x, long long x_stride, const void* wg, const void* wu, const void* dh,
+                         long long dh_stride, const signed char* codes, const unsigned char* exps, void* dx,
+                         long long dx_stride, void* dwg, void* dwu, int T, int C, int F, int act, int dtype,
+                         void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Failure-detection test hooks (the pages have no counterpart; test use only).

@@ -29,11 +29,16 @@ __all__ = [
     "la_backward_gated", "la_gated_workspace_bytes", "la_gated_backward_workspace_bytes",
     "la_rotary", "la_rotary_freqs", "la_norm_gate", "la_norm_gate_backward",
     "la_norm_gate_workspace_bytes",
+    "la_checkpoint", "la_checkpoint_restore", "la_layer_norm", "la_layer_norm_backward",
+    "la_layer_norm_workspace_bytes", "la_ffn_gate", "la_ffn_gate_backward",
+    "la_ffn_gate_workspace_bytes", "la_ffn_gate_backward_workspace_bytes",
+    "LA_SILU", "LA_GELU", "LA_GELU_TANH",
 ]
 
 LA_OK, LA_ERR_INVALID_ARG, LA_ERR_WORKSPACE, LA_ERR_CUDA, LA_ERR_TIMEOUT = 0, 1, 2, 3, 4
 LA_ERR_TOO_LARGE = 5
 LA_F32, LA_BF16 = 0, 1
+LA_SILU, LA_GELU, LA_GELU_TANH = 0, 1, 2
 LA_SITE_FORWARD_LOAD, LA_SITE_FORWARD_FUSED_LOAD, LA_SITE_BACKWARD_LOAD = 11, 16, 21
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -41,6 +46,7 @@ _LIB_PATH = os.path.join(_HERE, "_build", "liblagb300.so")
 _lib = None
 
 _c_int, _c_size, _vp = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+_c_ll, _c_float = ctypes.c_longlong, ctypes.c_float
 
 _SIGNATURES = {
     "la_status_string": (ctypes.c_char_p, [_c_int]),
@@ -79,6 +85,19 @@ _SIGNATURES = {
     "la_norm_gate_workspace_bytes": (_c_size, [_c_int] * 4),
     "la_norm_gate_backward": (_c_int, [_vp] * 10 + [_c_int] * 5
                               + [ctypes.c_float, _c_int, _vp, _c_size, _vp]),
+    "la_checkpoint": (_c_int, [_vp, _c_ll, _vp, _vp, _c_ll, _c_int, _c_int, _vp]),
+    "la_checkpoint_restore": (_c_int, [_vp, _vp, _vp, _c_ll, _c_ll, _c_int, _c_int, _vp]),
+    "la_layer_norm": (_c_int, [_vp, _c_ll, _vp, _vp, _vp, _c_ll, _vp, _vp, _c_ll, _c_int, _c_float,
+                               _c_int, _vp]),
+    "la_layer_norm_workspace_bytes": (_c_size, [_c_ll, _c_int]),
+    "la_layer_norm_backward": (_c_int, [_vp, _c_ll] + [_vp] * 4 + [_c_ll, _vp, _c_ll, _vp, _vp, _c_ll,
+                                        _c_int, _c_float, _c_int, _vp, _c_size, _vp]),
+    "la_ffn_gate_workspace_bytes": (_c_size, [_c_int] * 4),
+    "la_ffn_gate_backward_workspace_bytes": (_c_size, [_c_int] * 4),
+    "la_ffn_gate": (_c_int, [_vp, _c_ll, _vp, _vp, _vp, _c_ll, _vp, _vp] + [_c_int] * 5
+                    + [_vp, _c_size, _vp]),
+    "la_ffn_gate_backward": (_c_int, [_vp, _c_ll, _vp, _vp, _vp, _c_ll, _vp, _vp, _vp, _c_ll, _vp, _vp]
+                             + [_c_int] * 5 + [_vp, _c_size, _vp]),
     "la_debug_noalloc_set_status": (_c_int, [_c_int, _c_int, _vp]),
     "la_workspace_wait_site": (_c_int, [_vp, _c_size, _vp]),
     "la_debug_forward_fault": (_c_int, [_vp] * 4 + [_c_int] * 7 + [_vp, _c_size, _c_int,
@@ -1085,3 +1104,290 @@ def la_norm_gate_backward(x, z, w, dy, eps=1e-6, dx=None, dz=None, dw=None, work
     if st:
         _check(fn, st)
     return dx, dz, dw
+
+
+# ------------------------- layer norm, gated projections, activations in 8 bits
+
+_ACTIVATIONS = {"silu": LA_SILU, "gelu": LA_GELU, "gelu_tanh": LA_GELU_TANH}
+
+
+def _token_rows(fn, name, t):
+    """(rows, distance from row to row in elements) of t [..., C], its leading dimensions taken as
+    one; rows lie evenly apart and do not overlap."""
+    shape, stride = t.shape, t.stride()
+    C = shape[-1]
+    if t.is_contiguous():
+        return t.numel() // C if C else 0, C
+    if stride[-1] != 1 and C > 1:
+        raise ValueError(f"{fn}: {name}'s last dimension must be contiguous")
+    rows, ld = 1, None
+    for n, st in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+        if n == 1:
+            continue
+        if ld is None:
+            ld = st
+        elif st != ld * rows:
+            raise ValueError(f"{fn}: {name}'s rows must lie evenly apart in memory")
+        rows *= n
+    if rows == 0:
+        return 0, C
+    if ld is None or rows == 1:
+        ld = C
+    if ld < C:
+        raise ValueError(f"{fn}: rows of {name} overlap in memory")
+    return rows, ld
+
+
+def _kept(fn, shape, checkpoint, device=None):
+    """Checks a checkpoint (codes, exps) of values of the given shape."""
+    import torch
+    if not isinstance(checkpoint, (tuple, list)) or len(checkpoint) != 2:
+        raise ValueError(f"{fn}: a checkpoint is a pair (codes, exps)")
+    codes, exps = checkpoint
+    _expect(fn, "codes", codes, tuple(shape), torch.int8)
+    _expect(fn, "exps", exps, (*shape[:-1], -(-shape[-1] // 32)), torch.uint8)
+    if device is not None:
+        _need_cuda(codes, exps, device=device)
+    return codes, exps
+
+
+def _cuda_device(t):
+    if t.get_device() < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    return t.device
+
+
+def la_checkpoint(x, checkpoint=None):
+    """x [..., C] in 8 bits: (codes int8 [..., C], exps uint8 [..., ceil(C/32)]).
+
+    Each block of 32 neighbours has a step, the power of two 2^(exp - 127): the smallest (exp >= 1)
+    for which every |value| / step is below 127.5. A value is off by half a step at most. A block
+    that holds an infinity or a NaN restores as NaN. checkpoint: a pair to write to."""
+    import torch
+    fn = "la_checkpoint"
+    dt = _dtype_code(x)
+    if x.dim() < 1:
+        raise ValueError(f"{fn}: x must have at least 1 dimension")
+    rows, ld = _token_rows(fn, "x", x)
+    shape = tuple(x.shape)
+    if checkpoint is not None:
+        _kept(fn, shape, checkpoint)
+    dev = _cuda_device(x)
+    lib = load_library()
+    if checkpoint is None:
+        codes = torch.empty(shape, dtype=torch.int8, device=dev)
+        exps = torch.empty((*shape[:-1], -(-shape[-1] // 32)), dtype=torch.uint8, device=dev)
+    else:
+        codes, exps = _kept(fn, shape, checkpoint, dev)
+    with _on_device(dev):
+        st = lib.la_checkpoint(x.data_ptr(), ld, codes.data_ptr(), exps.data_ptr(), rows, shape[-1], dt,
+                               _stream_ptr(dev))
+    if st:
+        _check(fn, st)
+    return codes, exps
+
+
+def la_checkpoint_restore(codes, exps, dtype=None, out=None):
+    """The values that a checkpoint stands for, [..., C] in `dtype` (default: out's, or bfloat16,
+    which holds all of them exactly)."""
+    import torch
+    fn = "la_checkpoint_restore"
+    if codes.dim() < 1:
+        raise ValueError(f"{fn}: codes must have at least 1 dimension")
+    shape = tuple(codes.shape)
+    _kept(fn, shape, (codes, exps))
+    dtype = dtype or (torch.bfloat16 if out is None else out.dtype)
+    if out is not None:
+        _expect(fn, "out", out, shape, dtype)
+        _token_rows(fn, "out", out)
+    elif dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    dev = _cuda_device(codes)
+    _need_cuda(codes, exps)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    _need_rows(out, device=dev)
+    rows, ld = _token_rows(fn, "out", out)
+    lib = load_library()
+    with _on_device(dev):
+        st = lib.la_checkpoint_restore(codes.data_ptr(), exps.data_ptr(), out.data_ptr(), ld, rows,
+                                       shape[-1], _dtype_code(out), _stream_ptr(dev))
+    if st:
+        _check(fn, st)
+    return out
+
+
+def la_layer_norm_workspace_bytes(rows, C):
+    return load_library().la_layer_norm_workspace_bytes(rows, C)
+
+
+def la_layer_norm(x, w, b=None, eps=1e-5, out=None, checkpoint=None):
+    """out = (x - mean) / sqrt(var + eps) * w + b over the last dimension of x [..., C].
+
+    w [C], b [C] or None. Rows of x and out may be strided evenly; out may be x. checkpoint: a pair
+    (codes, exps), as la_checkpoint makes it, that receives x in 8 bits on the way."""
+    import torch
+    fn = "la_layer_norm"
+    dt, shape, dtype = _dtype_code(x), tuple(x.shape), x.dtype
+    if len(shape) < 1:
+        raise ValueError(f"{fn}: x must have at least 1 dimension")
+    C = shape[-1]
+    for name, t in (("w", w), ("b", b)):
+        if t is not None:
+            _expect(fn, name, t, (C,), dtype)
+    rows, ld = _token_rows(fn, "x", x)
+    if out is not None:
+        _expect(fn, "out", out, shape, dtype)
+        old = _token_rows(fn, "out", out)[1]
+    if checkpoint is not None:
+        _kept(fn, shape, checkpoint)
+    dev = _cuda_device(x)
+    _need_cuda(w, *([] if b is None else [b]), device=dev)
+    codes, exps = (None, None) if checkpoint is None else _kept(fn, shape, checkpoint, dev)
+    if out is None:
+        out, old = torch.empty(shape, dtype=dtype, device=dev), C
+    else:
+        _need_rows(out, device=dev)
+    lib = load_library()
+    with _on_device(dev):
+        st = lib.la_layer_norm(x.data_ptr(), ld, w.data_ptr(), _ptr(b), out.data_ptr(), old, _ptr(codes),
+                               _ptr(exps), rows, C, float(eps), dt, _stream_ptr(dev))
+    if st:
+        _check(fn, st)
+    return out
+
+
+def la_layer_norm_backward(x, w, dy, eps=1e-5, dx=None, dw=None, db=None, workspace=None):
+    """Gradients (dx, dw, db) of sum(dy * la_layer_norm(x, w, b, eps)), in dy's dtype.
+
+    x: the norm's input [..., C], or a checkpoint (codes, exps) of it. dx may be x or dy."""
+    import torch
+    fn = "la_layer_norm_backward"
+    dt, shape, dtype = _dtype_code(dy), tuple(dy.shape), dy.dtype
+    if len(shape) < 1:
+        raise ValueError(f"{fn}: dy must have at least 1 dimension")
+    C = shape[-1]
+    _expect(fn, "w", w, (C,), dtype)
+    kept = isinstance(x, (tuple, list))
+    if kept:
+        _kept(fn, shape, x)
+        ld = 0
+    else:
+        _expect(fn, "x", x, shape, dtype)
+        ld = _token_rows(fn, "x", x)[1]
+    rows, dyld = _token_rows(fn, "dy", dy)
+    for name, t, like in (("dx", dx, shape), ("dw", dw, (C,)), ("db", db, (C,))):
+        if t is not None:
+            _expect(fn, name, t, like, dtype)
+    dxld = C if dx is None else _token_rows(fn, "dx", dx)[1]
+    dev = _cuda_device(dy)
+    _need_cuda(w, *[t for t in (dw, db) if t is not None], device=dev)
+    _need_rows(*[t for t in (None if kept else x, dx) if t is not None], device=dev)
+    codes, exps = _kept(fn, shape, x, dev) if kept else (None, None)
+    lib = load_library()
+    dx = torch.empty(shape, dtype=dtype, device=dev) if dx is None else dx
+    dw = torch.empty_like(w) if dw is None else dw
+    db = torch.empty_like(w) if db is None else db
+    ws, nbytes = _scratch(dy, _bytes("la_layer_norm_workspace_bytes", rows, C), workspace)
+    with _on_device(dev):
+        st = lib.la_layer_norm_backward(0 if kept else x.data_ptr(), ld, _ptr(codes), _ptr(exps),
+                                        w.data_ptr(), dy.data_ptr(), dyld, dx.data_ptr(), dxld,
+                                        dw.data_ptr(), db.data_ptr(), rows, C, float(eps), dt,
+                                        _ptr(ws), nbytes, _stream_ptr(dev))
+    if st:
+        _check(fn, st)
+    return dx, dw, db
+
+
+def la_ffn_gate_workspace_bytes(T, C, F, dtype=LA_BF16):
+    return load_library().la_ffn_gate_workspace_bytes(T, C, F, dtype)
+
+
+def la_ffn_gate_backward_workspace_bytes(T, C, F, dtype=LA_BF16):
+    return load_library().la_ffn_gate_backward_workspace_bytes(T, C, F, dtype)
+
+
+def _ffn_checks(fn, x, wg, wu, activation):
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"{fn}: activation must be one of {', '.join(_ACTIVATIONS)}")
+    dt = _dtype_code(x)
+    if x.dim() < 1 or wg.dim() != 2:
+        raise ValueError(f"{fn}: x must be [..., C] and wg [F, C]")
+    F, C = wg.shape
+    _expect(fn, "wg", wg, (F, x.shape[-1]), x.dtype)
+    _expect(fn, "wu", wu, (F, C), x.dtype)
+    return C, F, dt, _ACTIVATIONS[activation]
+
+
+def la_ffn_gate(x, wg, wu, activation="silu", out=None, checkpoint=None, workspace=None):
+    """out = act(x wg^T) * (x wu^T): both projections of a gated feed-forward block, their activation
+    and their product. x [..., C], wg and wu [F, C], out [..., F].
+
+    activation: "silu", "gelu" or "gelu_tanh". checkpoint: a pair (codes int8 [..., 2, F], exps
+    uint8 [..., 2, ceil(F/32)]) that receives x wg^T and x wu^T in 8 bits, for the backward pass.
+    Rows of x and out may be strided evenly."""
+    import torch
+    fn = "la_ffn_gate"
+    C, F, dt, act = _ffn_checks(fn, x, wg, wu, activation)
+    lead, dtype = tuple(x.shape[:-1]), x.dtype
+    rows, ld = _token_rows(fn, "x", x)
+    if out is not None:
+        _expect(fn, "out", out, (*lead, F), dtype)
+        old = _token_rows(fn, "out", out)[1]
+    if checkpoint is not None:
+        _kept(fn, (*lead, 2, F), checkpoint)
+    dev = _cuda_device(x)
+    _need_cuda(wg, wu, device=dev)
+    codes, exps = (None, None) if checkpoint is None else _kept(fn, (*lead, 2, F), checkpoint, dev)
+    if out is None:
+        out, old = torch.empty((*lead, F), dtype=dtype, device=dev), F
+    else:
+        _need_rows(out, device=dev)
+    lib = load_library()
+    ws, nbytes = _scratch(x, _bytes("la_ffn_gate_workspace_bytes", rows, C, F, dt), workspace)
+    with _on_device(dev):
+        st = lib.la_ffn_gate(x.data_ptr(), ld, wg.data_ptr(), wu.data_ptr(), out.data_ptr(), old,
+                             _ptr(codes), _ptr(exps), rows, C, F, act, dt, _ptr(ws), nbytes,
+                             _stream_ptr(dev))
+    if st:
+        _check(fn, st)
+    return out
+
+
+def la_ffn_gate_backward(x, wg, wu, dh, activation="silu", checkpoint=None, dx=None, dwg=None, dwu=None,
+                         workspace=None):
+    """Gradients (dx, dwg, dwu) of sum(dh * la_ffn_gate(x, wg, wu, activation)), in the inputs' dtype.
+
+    checkpoint: the pair that la_ffn_gate filled; x wg^T and x wu^T are then taken from it instead
+    of being computed again. Rows of x, dh and dx may be strided evenly."""
+    import torch
+    fn = "la_ffn_gate_backward"
+    C, F, dt, act = _ffn_checks(fn, x, wg, wu, activation)
+    shape, dtype = tuple(x.shape), x.dtype
+    lead = shape[:-1]
+    _expect(fn, "dh", dh, (*lead, F), dtype)
+    rows, ld = _token_rows(fn, "x", x)
+    dhld = _token_rows(fn, "dh", dh)[1]
+    for name, t, like in (("dx", dx, shape), ("dwg", dwg, (F, C)), ("dwu", dwu, (F, C))):
+        if t is not None:
+            _expect(fn, name, t, like, dtype)
+    dxld = C if dx is None else _token_rows(fn, "dx", dx)[1]
+    if checkpoint is not None:
+        _kept(fn, (*lead, 2, F), checkpoint)
+    dev = _cuda_device(x)
+    _need_cuda(wg, wu, *[t for t in (dwg, dwu) if t is not None], device=dev)
+    _need_rows(dh, *([] if dx is None else [dx]), device=dev)
+    codes, exps = (None, None) if checkpoint is None else _kept(fn, (*lead, 2, F), checkpoint, dev)
+    lib = load_library()
+    dx = torch.empty(shape, dtype=dtype, device=dev) if dx is None else dx
+    dwg = torch.empty_like(wg) if dwg is None else dwg
+    dwu = torch.empty_like(wu) if dwu is None else dwu
+    ws, nbytes = _scratch(x, _bytes("la_ffn_gate_backward_workspace_bytes", rows, C, F, dt), workspace)
+    with _on_device(dev):
+        st = lib.la_ffn_gate_backward(x.data_ptr(), ld, wg.data_ptr(), wu.data_ptr(), dh.data_ptr(), dhld,
+                                      _ptr(codes), _ptr(exps), dx.data_ptr(), dxld, dwg.data_ptr(),
+                                      dwu.data_ptr(), rows, C, F, act, dt, _ptr(ws), nbytes,
+                                      _stream_ptr(dev))
+    if st:
+        _check(fn, st)
+    return dx, dwg, dwu

@@ -1,0 +1,59 @@
+// The gated projections' activations: f = act(a) and its derivative.
+//   silu       a s,  s = 1 / (1 + exp(-a));                  f' = s (1 + a (1 - s))
+//   gelu       a P(a),  P(a) = erfc(-a / sqrt(2)) / 2;       f' = P + a exp(-a^2 / 2) / sqrt(2 pi)
+//   gelu_tanh  a s(z),  z = c (a + 0.044715 a^3), c = 2 sqrt(2 / pi)  ((1 + tanh(y)) / 2 = s(2 y));
+//              f' = s + a s (1 - s) z'
+#pragma once
+
+#include "la_common.cuh"
+
+namespace la {
+namespace ffn {
+
+enum Act { kSilu = 0, kGelu = 1, kGeluTanh = 2 };
+
+// s = sigmoid(z) and 1 - s. FAST (results in bf16): by __expf, off by 2 + 1.17 |z| steps of
+// 2^-23, and a quotient off by 2; past |z| = 87 the smaller one is 0 instead of below 2^-125.
+// Otherwise from expf and a rounded quotient. 1 - s cancels nothing: both come from exp(-|z|).
+template <bool FAST>
+__device__ __forceinline__ void sigmoid(float z, float& s, float& rest) {
+  const float e = FAST ? __expf(-fabsf(z)) : expf(-fabsf(z));
+  const float large = FAST ? __fdividef(1.f, 1.f + e) : 1.f / (1.f + e);
+  const float small = e * large;
+  s = z < 0.f ? small : large;
+  rest = z < 0.f ? large : small;
+}
+
+template <int ACT, bool FAST>
+__device__ __forceinline__ float act(float a) {
+  if constexpr (ACT == kGelu) return 0.5f * a * erfcf(-0.70710678118654752f * a);
+  float z = a;
+  if constexpr (ACT == kGeluTanh) z = 1.5957691216057308f * a * fmaf(0.044715f * a, a, 1.f);
+  if constexpr (FAST) return a * __fdividef(1.f, 1.f + __expf(-z));  // (0 once exp(-z) is infinite)
+  float s, rest;
+  sigmoid<FAST>(z, s, rest);
+  return a * s;
+}
+
+template <int ACT, bool FAST>
+__device__ __forceinline__ void act_grad(float a, float& f, float& df) {
+  if constexpr (ACT == kGelu) {
+    const float p = 0.5f * erfcf(-0.70710678118654752f * a);
+    const float e = FAST ? __expf(-0.5f * a * a) : expf(-0.5f * a * a);
+    f = a * p;
+    df = fmaf(0.3989422804014327f * a, e, p);
+    return;
+  }
+  float z = a, dz = 1.f, s, rest;
+  if constexpr (ACT == kGeluTanh) {
+    const float q = 0.044715f * a * a;
+    z = 1.5957691216057308f * a * (1.f + q);
+    dz = 1.5957691216057308f * fmaf(3.f, q, 1.f);
+  }
+  sigmoid<FAST>(z, s, rest);
+  f = a * s;
+  df = s * fmaf(a * dz, rest, 1.f);
+}
+
+}  // namespace ffn
+}  // namespace la

@@ -175,4 +175,46 @@ size_t norm_gate_workspace(int B, int H, int N, int M);
 cudaError_t norm_gate(const NormGate& n, cudaStream_t st);
 cudaError_t norm_gate_backward(const NormGate& n, void* ws, cudaStream_t st);
 
+// ---- activations in 8 bits: codes [rows][C], exps [rows][ceil(C / 32)]; rows of x are
+// x_stride elements apart
+struct Checkpoint {
+  void* x;  // read by pack, written by restore
+  signed char* codes;
+  unsigned char* exps;
+  long long rows, x_stride;
+  int C, dtype;
+};
+cudaError_t checkpoint_pack(const Checkpoint& c, cudaStream_t st);
+cudaError_t checkpoint_restore(const Checkpoint& c, cudaStream_t st);
+
+// ---- layer norm; strides in elements from row to row. codes, exps: an 8-bit checkpoint of x,
+// written by the forward pass if wanted, read by the backward pass instead of x if given
+struct LayerNorm {
+  const void *x, *w, *b, *dy;
+  void *y, *dx, *dw, *db;
+  signed char* codes;
+  unsigned char* exps;
+  long long rows, x_stride, y_stride, dy_stride, dx_stride;
+  int C, dtype;
+  float eps;
+};
+size_t layer_norm_workspace(long long rows, int C);
+cudaError_t layer_norm(const LayerNorm& n, cudaStream_t st);
+cudaError_t layer_norm_backward(const LayerNorm& n, void* ws, cudaStream_t st);
+
+// ---- gated projections h = act(x wg^T) * (x wu^T); codes [T][2][F], exps [T][2][ceil(F / 32)]:
+// a checkpoint of both products, written by the forward pass if wanted, read by the backward
+// pass if given (it recomputes them otherwise)
+struct FfnGate {
+  const void *x, *wg, *wu, *dh;
+  void *h, *dx, *dwg, *dwu;
+  signed char* codes;
+  unsigned char* exps;
+  long long x_stride, h_stride, dh_stride, dx_stride;
+  int T, C, F, act, dtype;
+};
+size_t ffn_simt_backward_workspace(int T, int C, int F, int dtype);
+cudaError_t ffn_simt_forward(const FfnGate& f, cudaStream_t st);
+cudaError_t ffn_simt_backward(const FfnGate& f, void* ws, cudaStream_t st);
+
 }  // namespace la

@@ -11,8 +11,18 @@ differences): elu_plus_one, elu_plus_one_grad, masked_attention,
 masked_attention_rows, linearized_attention, recurrent_attention, forward, prefill, decode_step,
 backward, denominators, poly2_feature, random_fourier_feature. No function here is parity
 unpinned. gated_forward, gated_backward, rotary, norm_gate and norm_gate_backward are pinned
-in ``tests/test_gated_oracle.py``.
+in ``tests/test_gated_oracle.py``; layer_norm, layer_norm_backward, activation, ffn_gate,
+ffn_gate_backward and checkpoint in ``tests/test_ffn_oracle.py``.
 """
+
+from .ffn import (  # noqa: F401
+    activation,
+    checkpoint,
+    ffn_gate,
+    ffn_gate_backward,
+    layer_norm,
+    layer_norm_backward,
+)
 
 from .gated import (  # noqa: F401
     gated_backward,
