@@ -6,6 +6,7 @@
 #pragma once
 
 #include "la_common.cuh"
+#include "la_internal.h"
 
 namespace la {
 namespace ffn {
@@ -56,4 +57,12 @@ __device__ __forceinline__ void act_grad(float a, float& f, float& df) {
 }
 
 }  // namespace ffn
+
+// out (and out2 with count 2): the sums over `splits` parts of partial [count][splits][rows][C],
+// added in order
+cudaError_t ffn_join(const float* partial, void* out, void* out2, long long out_stride, int rows, int count, int C,
+                     int splits, int dtype, cudaStream_t st);
+// dact [2][T][F]: da = dh u act'(a), du = dh act(a), a and u from f's checkpoint
+cudaError_t ffn_kept_grads(const FfnGate& f, void* dact, cudaStream_t st);
+
 }  // namespace la

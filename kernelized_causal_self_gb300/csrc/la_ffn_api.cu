@@ -23,7 +23,7 @@ size_t size_of(int dtype) { return dtype == LA_F32 ? 4 : 2; }
 
 // n elements a row, rows `stride` elements apart: 16-byte pieces that do not overlap
 bool stride_ok(long long stride, int n, int dtype) {
-  return stride >= n && stride <= 1LL << 40 && stride % (dtype == LA_F32 ? 4 : 8) == 0;
+  return stride >= n && stride <= 1LL << 37 && stride % (dtype == LA_F32 ? 4 : 8) == 0;
 }
 
 bool rows_ok(long long rows, int C, int dtype) {
@@ -81,7 +81,7 @@ size_t ffn_workspace(int T, int C, int F, int dtype) {
 }
 
 size_t ffn_backward_workspace(int T, int C, int F, int dtype) {
-  return la::ffn_simt_backward_workspace(T, C, F, dtype);
+  return dtype == LA_F32 ? la::ffn_simt_backward_workspace(T, C, F, dtype) : la::ffn_tc_backward_workspace(T, C, F);
 }
 
 }  // namespace
@@ -228,7 +228,8 @@ int la_ffn_gate(const void* x, long long x_stride, const void* wg, const void* w
   f.F = F;
   f.act = act;
   f.dtype = dtype;
-  return from_cuda(la::ffn_simt_forward(f, as_stream(stream)));
+  return from_cuda(dtype == LA_F32 ? la::ffn_simt_forward(f, as_stream(stream))
+                                   : la::ffn_tc_forward(f, workspace, as_stream(stream)));
 }
 
 int la_ffn_gate_backward(const void* x, long long x_stride, const void* wg, const void* wu, const void* dh,
@@ -270,7 +271,7 @@ int la_ffn_gate_backward(const void* x, long long x_stride, const void* wg, cons
   f.F = F;
   f.act = act;
   f.dtype = dtype;
-  return from_cuda(la::ffn_simt_backward(f, workspace, st));
+  return from_cuda(dtype == LA_F32 ? la::ffn_simt_backward(f, workspace, st) : la::ffn_tc_backward(f, workspace, st));
 }
 
 }  // extern "C"

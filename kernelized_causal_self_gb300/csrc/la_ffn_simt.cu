@@ -310,22 +310,14 @@ cudaError_t launch(Args a, cudaStream_t st) {
 }
 
 template <typename T>
-cudaError_t join(const Args& a, int rows, int count, long long stride, cudaStream_t st) {
-  const long long n = (long long)rows * a.C / 4;
-  const int ctas = (int)((n + 255) / 256 < 8 * kSms ? (n + 255) / 256 : 8 * kSms);
-  const float* partial = a.partial;
-  const cudaError_t e = launch_pdl(ffn_join_kernel<T>, dim3(ctas, count), dim3(256), 0, st, partial,
-                                   static_cast<T*>(a.out), static_cast<T*>(a.out2), stride, rows, a.C, a.splits);
-  count_launches(1);
-  return e;
+cudaError_t grads(const Args& a, int act, cudaStream_t st) {
+  return act == kSilu   ? launch<T, kGrads, kSilu>(a, st)
+         : act == kGelu ? launch<T, kGrads, kGelu>(a, st)
+                        : launch<T, kGrads, kGeluTanh>(a, st);
 }
 
 template <typename T>
-cudaError_t grads(const Args& a, bool kept, int act, cudaStream_t st) {
-  if (!kept)
-    return act == kSilu   ? launch<T, kGrads, kSilu>(a, st)
-           : act == kGelu ? launch<T, kGrads, kGelu>(a, st)
-                          : launch<T, kGrads, kGeluTanh>(a, st);
+cudaError_t kept_grads(const Args& a, int act, cudaStream_t st) {
   const long long n = (long long)a.T * (a.F / 4);
   const dim3 grid((unsigned)((n + 255) / 256 < 16 * kSms ? (n + 255) / 256 : 16 * kSms));
   const cudaError_t e =
@@ -337,44 +329,67 @@ cudaError_t grads(const Args& a, bool kept, int act, cudaStream_t st) {
 }
 
 template <typename T>
-cudaError_t backward(const FfnGate& f, void* ws, cudaStream_t st) {
+cudaError_t join(const float* partial, void* out, void* out2, long long stride, int rows, int count, int C, int splits,
+                 cudaStream_t st) {
+  const long long n = (long long)rows * C / 4;
+  const int ctas = (int)((n + 255) / 256 < 8 * kSms ? (n + 255) / 256 : 8 * kSms);
+  const cudaError_t e = launch_pdl(ffn_join_kernel<T>, dim3(ctas, count), dim3(256), 0, st, partial,
+                                   static_cast<T*>(out), static_cast<T*>(out2), stride, rows, C, splits);
+  count_launches(1);
+  return e;
+}
+
+Args args_of(const FfnGate& f) {
   Args a{};
   a.x = f.x, a.wg = f.wg, a.wu = f.wu, a.dh = f.dh;
   a.codes = f.codes, a.exps = f.exps;
   a.x_stride = f.x_stride, a.dh_stride = f.dh_stride;
-  a.T = f.T, a.C = f.C, a.F = f.F;
+  a.T = f.T, a.C = f.C, a.F = f.F, a.splits = 1;
+  return a;
+}
+
+template <typename T>
+cudaError_t backward(const FfnGate& f, void* ws, cudaStream_t st) {
+  Args a = args_of(f);
   char* at = static_cast<char*>(ws) + kHeaderBytes;
   a.dact = at;
   a.partial = reinterpret_cast<float*>(at + align_up(2 * sizeof(T) * (size_t)f.T * f.F, 256));
-  a.splits = 1;
-  cudaError_t e = grads<T>(a, f.codes != nullptr, f.act, st);
+  cudaError_t e = f.codes != nullptr ? ffn_kept_grads(f, a.dact, st) : grads<T>(a, f.act, st);
   if (e != cudaSuccess) return e;
   a.out = f.dx, a.out_stride = f.dx_stride;
   a.splits = splits_of(f.T, f.C, 2LL * f.F, 1);
   e = launch<T, kDx, kSilu>(a, st);
-  if (e == cudaSuccess && a.splits > 1) e = join<T>(a, f.T, 1, f.dx_stride, st);
+  if (e == cudaSuccess && a.splits > 1) e = join<T>(a.partial, a.out, nullptr, f.dx_stride, f.T, 1, f.C, a.splits, st);
   if (e != cudaSuccess) return e;
   a.out = f.dwg, a.out2 = f.dwu;
   a.splits = splits_of(f.F, f.C, f.T, 2);
   e = launch<T, kDw, kSilu>(a, st);
-  if (e == cudaSuccess && a.splits > 1) e = join<T>(a, f.F, 2, f.C, st);
+  if (e == cudaSuccess && a.splits > 1) e = join<T>(a.partial, a.out, a.out2, f.C, f.F, 2, f.C, a.splits, st);
   return e;
 }
 
 template <typename T>
 cudaError_t forward(const FfnGate& f, cudaStream_t st) {
-  Args a{};
-  a.x = f.x, a.wg = f.wg, a.wu = f.wu;
+  Args a = args_of(f);
   a.out = f.h, a.out_stride = f.h_stride;
-  a.codes = f.codes, a.exps = f.exps;
-  a.x_stride = f.x_stride;
-  a.T = f.T, a.C = f.C, a.F = f.F, a.splits = 1;
   return f.act == kSilu   ? launch<T, kForward, kSilu>(a, st)
          : f.act == kGelu ? launch<T, kForward, kGelu>(a, st)
                           : launch<T, kForward, kGeluTanh>(a, st);
 }
 
 }  // namespace
+
+cudaError_t ffn_join(const float* partial, void* out, void* out2, long long out_stride, int rows, int count, int C,
+                     int splits, int dtype, cudaStream_t st) {
+  return dtype == LA_F32 ? join<float>(partial, out, out2, out_stride, rows, count, C, splits, st)
+                         : join<__nv_bfloat16>(partial, out, out2, out_stride, rows, count, C, splits, st);
+}
+
+cudaError_t ffn_kept_grads(const FfnGate& f, void* dact, cudaStream_t st) {
+  Args a = args_of(f);
+  a.dact = dact;
+  return f.dtype == LA_F32 ? kept_grads<float>(a, f.act, st) : kept_grads<__nv_bfloat16>(a, f.act, st);
+}
 
 size_t ffn_simt_backward_workspace(int T, int C, int F, int dtype) {
   const int sx = splits_of(T, C, 2LL * F, 1), sw = splits_of(F, C, T, 2);

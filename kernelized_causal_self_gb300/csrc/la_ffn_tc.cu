@@ -1,0 +1,499 @@
+// The gated projections in bf16 on the tensor cores: a = x wg^T, u = x wu^T, h = act(a) u, and
+// the backward pass da = dh u act'(a), du = dh act(a), dx = da wg + du wu, dwg = da^T x,
+// dwu = du^T x (da and du in bf16, in the workspace).
+//
+// One persistent kernel for all five products. A pair of CTAs (cta_group::2) makes a tile of
+// 256 x 256: each CTA copies its 128 rows of A and its half of B's 256 rows by TMA, 64 terms
+// of the sum a stage, the even one issues the MMAs, and each finds its 128 x 256 of D in its
+// own tensor memory, where two accumulators take turns, so that four warps write one tile's
+// results while the next is summed.
+//   kForward, kGrads  A = x, B = 128 rows of wg (even CTA) and the same rows of wu (odd CTA): a
+//                     row's a and u come to lie in one thread, 128 columns apart, and nothing
+//                     but h (or da, du) leaves the SM. kGrads has dh's tile copied in as well.
+//   kDx               A = [da | du], B = [wg; wu] read along c: one sum over 2 F terms.
+//   kDw               A = da or du and B = x, both read along their rows (tokens are the sum).
+// Results go through a swizzled staging tile of 32 rows a warp and leave by TMA, which clips
+// what is past the matrix; copies past its edge read zeros, so ragged sizes need no masks.
+// Sums with few tiles are cut along k (float32 parts, added in order by a second kernel).
+#include <cuda_bf16.h>
+
+#include "la_checkpoint.cuh"
+#include "la_ffn.cuh"
+#include "la_internal.h"
+#include "la_tc_common.cuh"
+
+namespace la {
+namespace {
+
+using namespace tcx;
+using namespace ffn;
+
+enum Kind { kForward, kGrads, kDx, kDw };
+
+constexpr int kThreads = 192;     // four warps of results, one that copies, one that multiplies
+constexpr int kTileBytes = 16384;  // 128 x 64 bf16
+constexpr int kStageBytes = 2 * kTileBytes;
+constexpr int kStore = 4096;       // a warp's staging tile: 32 rows x 64 bf16
+constexpr int stages_of(int kind) { return kind == kGrads ? 4 : 6; }
+constexpr int staging_of(int kind) { return (kind == kGrads ? 4 : 2) * kStore; }  // a warp
+constexpr int smem_of(int kind) {
+  return 1024 + stages_of(kind) * kStageBytes + 4 * staging_of(kind) + (kind == kGrads ? 2 * kTileBytes : 0) + 256;
+}
+
+struct Args {
+  CUtensorMap a, b0, b1;    // operands (b0, b1: wg and wu; kDw: b0 = x)
+  CUtensorMap out0, out1;   // h; da, du; dx; dwg, dwu
+  CUtensorMap dh;           // kGrads
+  WorkspaceHeader* hdr;
+  float* partial;           // kDx, kDw: [dw: 2][splits][rows][C] if the sum is cut
+  signed char* codes;       // kForward: a checkpoint of a, u
+  unsigned char* exps;
+  int rows, cols;           // of the result (kForward, kGrads: T, F)
+  int m_tiles, n_tiles, splits, tiles;
+  int steps, per;           // k steps of 64 in the whole sum; kDx: of one of its two parts
+  int clear;                // the call's first kernel clears the status header
+};
+
+struct Tile {
+  int m, n, part, split, k0, k1;  // part: kDw: dwg or dwu
+};
+
+template <int KIND>
+__device__ __forceinline__ Tile tile_of(const Args& a, int t) {
+  Tile r;
+  r.n = t % a.n_tiles;
+  t /= a.n_tiles;
+  r.m = t % a.m_tiles;
+  t /= a.m_tiles;
+  r.part = KIND == kDw ? t % 2 : 0;
+  r.split = KIND == kDw ? t / 2 : t;
+  r.k0 = (int)((long long)a.steps * r.split / a.splits);
+  r.k1 = (int)((long long)a.steps * (r.split + 1) / a.splits);
+  return r;
+}
+
+// Wait codes of this file's kernels (la_workspace_wait_site)
+enum Site { kSiteEmpty = 81, kSiteFull, kSiteAccEmpty, kSiteAccFull, kSiteDhFull, kSiteDhEmpty, kSiteDrain };
+
+template <int KIND, int ACT>
+__global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_constant__ Args a) {
+  constexpr int S = stages_of(KIND);
+  constexpr bool DUAL = KIND == kForward || KIND == kGrads;
+  extern __shared__ uint8_t smraw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
+  uint8_t* stages = sm;                                  // [stage][A | B]
+  uint8_t* dht = stages + S * kStageBytes;               // kGrads: dh's tile, two blocks of 64 columns
+  uint8_t* staging = dht + (KIND == kGrads ? 2 * kTileBytes : 0);
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + 4 * staging_of(KIND));  // S (the even CTA's count)
+  uint64_t* empty = full + S;                            // S: the MMAs are done with the stage
+  uint64_t* acc_full = empty + S;                        // 2: an accumulator holds its tile
+  uint64_t* acc_empty = acc_full + 2;                    // 2 (the even CTA's): both CTAs have read it
+  uint64_t* dh_full = acc_empty + 2;
+  uint64_t* dh_empty = dh_full + 1;
+  uint64_t* drain = dh_empty + 1;
+  volatile int* abort = reinterpret_cast<volatile int*>(drain + 1);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1) + 1;
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_ctarank();
+  const int cluster = blockIdx.x / 2, clusters = gridDim.x / 2;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 8);  // four warps of each CTA
+    }
+    mbar_init(dh_full, 1);
+    mbar_init(dh_empty, 4);
+    mbar_init(drain, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc_pair(tslot, 512);
+    tmem_relinquish_pair();
+  }
+  fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  fence_after_sync();
+  const uint32_t tbase = *tslot;
+  pdl_wait();
+  WorkspaceHeader* hdr = a.hdr;
+  // (a wait that runs out is recorded two seconds after its kernel began, long after this)
+  if (a.clear && blockIdx.x == 0 && threadIdx.x == 0) hdr->status = hdr->wait_site = 0;
+
+  if (warp == 4) {
+    // ------------------------------------------------------------------ copies
+    if (lane == 0) {
+      long long n = 0;  // stages asked for
+      int nt = 0;
+      bool ok = true;
+      for (int t = cluster; t < a.tiles && ok; t += clusters, ++nt) {
+        const Tile w = tile_of<KIND>(a, t);
+        const int row = w.m * 256 + (int)rank * 128;
+        for (int k = w.k0; k < w.k1; ++k, ++n) {
+          const int s = (int)(n % S);
+          if (n >= S && !mbar_wait_abort(&empty[s], (uint32_t)((n / S - 1) & 1), abort, hdr, kSiteEmpty)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+          const uint32_t bar = cluster_map(smem_u32(&full[s]), 0);
+          uint8_t *ta = stages + s * kStageBytes, *tb = ta + kTileBytes;
+          if constexpr (DUAL) {
+            tma_load_3d_pair(ta, &a.a, bar, k * 64, row, 0);
+            tma_load_3d_pair(tb, rank ? &a.b1 : &a.b0, bar, k * 64, w.n * 128, 0);
+          } else if constexpr (KIND == kDx) {
+            const int part = k >= a.per, kk = (part ? k - a.per : k) * 64;
+            const int col = w.n * 256 + (int)rank * 128;
+            tma_load_3d_pair(ta, &a.a, bar, kk, row, part);
+            tma_load_3d_pair(tb, part ? &a.b1 : &a.b0, bar, col, kk, 0);
+            tma_load_3d_pair(tb + kTileBytes / 2, part ? &a.b1 : &a.b0, bar, col + 64, kk, 0);
+          } else {
+            const int col = w.n * 256 + (int)rank * 128;
+            tma_load_3d_pair(ta, &a.a, bar, row, k * 64, w.part);
+            tma_load_3d_pair(ta + kTileBytes / 2, &a.a, bar, row + 64, k * 64, w.part);
+            tma_load_3d_pair(tb, &a.b0, bar, col, k * 64, 0);
+            tma_load_3d_pair(tb + kTileBytes / 2, &a.b0, bar, col + 64, k * 64, 0);
+          }
+        }
+        if constexpr (KIND == kGrads) {
+          // dh's tile, behind the tile's operands: its room is free once the last tile's results are out
+          if (ok && nt > 0) ok = mbar_wait_abort(dh_empty, (uint32_t)((nt - 1) & 1), abort, hdr, kSiteDhEmpty);
+          if (ok) {
+            mbar_arrive_expect_tx(dh_full, 2 * kTileBytes);
+            tma_load_3d(dht, &a.dh, dh_full, w.n * 128, row, 0);
+            tma_load_3d(dht + kTileBytes, &a.dh, dh_full, w.n * 128 + 64, row, 0);
+          }
+        }
+      }
+      // the pair's copies have all landed before either CTA lets go of its shared memory
+      if (rank == 0)
+        for (long long k = n > S ? n - S : 0; k < n; ++k)
+          if (!mbar_wait(&full[k % S], (uint32_t)((k / S) & 1))) record_timeout(hdr, kSiteDrain);
+      if (KIND == kGrads && nt > 0 && !mbar_wait(dh_full, (uint32_t)((nt - 1) & 1)))
+        record_timeout(hdr, kSiteDrain);
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    // ------------------------------------------------------------------ products
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t id = idesc_bf16(256, 256, KIND == kDw, !DUAL);
+      long long n = 0;
+      int nt = 0;
+      bool ok = true;
+      for (int t = cluster; t < a.tiles && ok; t += clusters, ++nt) {
+        const Tile w = tile_of<KIND>(a, t);
+        const int b = nt & 1;
+        if (nt >= 2) ok = mbar_wait_abort(&acc_empty[b], (uint32_t)((nt / 2 - 1) & 1), abort, hdr, kSiteAccEmpty);
+        if (!ok) break;
+        fence_after_sync();
+        const uint32_t d = tbase + 256 * b;
+        for (int k = w.k0; k < w.k1; ++k, ++n) {
+          const int s = (int)(n % S);
+          if (!mbar_wait_abort(&full[s], (uint32_t)((n / S) & 1), abort, hdr, kSiteFull)) {
+            ok = false;
+            break;
+          }
+          fence_after_sync();
+          const uint32_t ta = smem_u32(stages + s * kStageBytes), tb = ta + kTileBytes;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            // along k: 32 bytes of a row a step; along m or n: 16 rows, blocks of 64 columns 8 KB apart
+            const uint64_t da = KIND == kDw ? sdesc(ta + q * 2048, kTileBytes / 2, 1024) : sdesc(ta + q * 32, 16, 1024);
+            const uint64_t db = DUAL ? sdesc(tb + q * 32, 16, 1024) : sdesc(tb + q * 2048, kTileBytes / 2, 1024);
+            mma_ss_pair(d, da, db, id, k > w.k0 || q > 0);
+          }
+          mma_commit_pair(&empty[s]);
+        }
+        if (ok) mma_commit_pair(&acc_full[b]);
+      }
+      mma_commit_pair_own(drain);
+      if (!mbar_wait(drain, 0)) record_timeout(hdr, kSiteDrain);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------ results
+    uint8_t* mine = staging + warp * staging_of(KIND);
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const uint32_t freed = cluster_map(smem_u32(acc_empty), 0);
+    const int trow = warp * 32 + lane;  // of the CTA's 128
+    int nt = 0, turn = 0;
+    for (int t = cluster; t < a.tiles; t += clusters, ++nt) {
+      const Tile w = tile_of<KIND>(a, t);
+      const int b = nt & 1, row0 = w.m * 256 + (int)rank * 128 + warp * 32, row = row0 + lane;
+      if (!mbar_wait_warp(&acc_full[b], (uint32_t)((nt / 2) & 1), abort, hdr, kSiteAccFull)) break;
+      if (KIND == kGrads && !mbar_wait_warp(dh_full, (uint32_t)(nt & 1), abort, hdr, kSiteDhFull)) break;
+      fence_after_sync();
+      const uint32_t d = tbase + 256 * b + lanes;
+      constexpr int GROUPS = DUAL ? 2 : 4;  // of 64 columns
+#pragma unroll 1
+      for (int g = 0; g < GROUPS; ++g) {
+        const int col = w.n * (DUAL ? 128 : 256) + g * 64;
+        const bool cut = !DUAL && a.splits > 1;
+        // the staging tile's last copy has read it (of two in turn; kGrads: two pairs)
+        uint8_t* st = mine + turn * (staging_of(KIND) / 2);
+        if (!cut) {
+          turn ^= 1;
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {  // 32 columns
+          uint32_t p[32], q[32];
+          if constexpr (DUAL) {
+            tmem_ld32x2(d + g * 64 + c * 32, p, d + 128 + g * 64 + c * 32, q);
+            const float *fa = reinterpret_cast<const float*>(p), *fu = reinterpret_cast<const float*>(q);
+            if constexpr (KIND == kForward) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int j = e * 8 + i * 2;
+                  o[i] = pack_bf16(act<ACT, true>(fa[j]) * fu[j], act<ACT, true>(fa[j + 1]) * fu[j + 1]);
+                }
+                *reinterpret_cast<uint4*>(st + sw128(lane, c * 64 + e * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+              }
+              if (a.codes != nullptr) {  // a thread has a block of 32 of a and of u
+                const int f = col + c * 32, nb = q8::blocks_of(a.cols);
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                  const float* x = v ? fu : fa;
+                  uint32_t top = 0;
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) top = max(top, q8::bits_of(x[j]));
+                  const uint32_t e = q8::step_of(top);
+                  const float inv = q8::inverse_step(e);
+                  if (row < a.rows && f < a.cols) {
+                    const size_t r = 2 * (size_t)row + v;
+                    signed char* to = a.codes + r * a.cols + f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                      if (f + j * 8 < a.cols)
+                        *reinterpret_cast<uint2*>(to + j * 8) =
+                            make_uint2(q8::codes4(x + j * 8, inv, e), q8::codes4(x + j * 8 + 4, inv, e));
+                    a.exps[r * nb + f / q8::kBlock] = (unsigned char)e;
+                  }
+                }
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t at = sw128(lane, c * 64 + e * 16);
+                const uint4 v = *reinterpret_cast<const uint4*>(dht + g * kTileBytes + sw128(trow, c * 64 + e * 16));
+                const uint32_t dh[4] = {v.x, v.y, v.z, v.w};
+                uint32_t oa[4], ou[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int j = e * 8 + i * 2;
+                  const float d0 = bf16_lo_f(dh[i]), d1 = bf16_hi_f(dh[i]);
+                  float f0, f1, g0, g1;
+                  act_grad<ACT, true>(fa[j], f0, g0);
+                  act_grad<ACT, true>(fa[j + 1], f1, g1);
+                  oa[i] = pack_bf16(d0 * fu[j] * g0, d1 * fu[j + 1] * g1);
+                  ou[i] = pack_bf16(d0 * f0, d1 * f1);
+                }
+                *reinterpret_cast<uint4*>(st + at) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+                *reinterpret_cast<uint4*>(st + kStore + at) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+              }
+            }
+          } else {
+            tmem_ld32(d + g * 64 + c * 32, p);
+            if (cut) {
+              const size_t r = (size_t)(KIND == kDw ? w.part * a.splits + w.split : w.split) * a.rows + row;
+              float* to = a.partial + r * a.cols + col + c * 32;
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (row < a.rows && col + c * 32 + j * 4 < a.cols)
+                  *reinterpret_cast<uint4*>(to + j * 4) = make_uint4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
+            } else {
+              const float* f = reinterpret_cast<const float*>(p);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<uint4*>(st + sw128(lane, c * 64 + e * 16)) =
+                    make_uint4(pack_bf16(f[e * 8], f[e * 8 + 1]), pack_bf16(f[e * 8 + 2], f[e * 8 + 3]),
+                               pack_bf16(f[e * 8 + 4], f[e * 8 + 5]), pack_bf16(f[e * 8 + 6], f[e * 8 + 7]));
+            }
+          }
+        }
+        if (g == GROUPS - 1) {  // the accumulator (and dh's tile) may be written again
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive_cluster(freed + 8 * b);
+            if (KIND == kGrads) mbar_arrive(dh_empty);
+          }
+        }
+        if (!cut) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (row0 < a.rows && col < a.cols) {
+              tma_store_3d(KIND == kDw && w.part ? &a.out1 : &a.out0, st, col, row0, 0);
+              if (KIND == kGrads) tma_store_3d(&a.out1, st + kStore, col, row0, 0);
+            }
+            bulk_commit();
+          }
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all<0>();
+    __syncwarp();
+  }
+  fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  fence_after_sync();
+  if (warp == 0) tmem_dealloc_pair(tbase, 512);
+}
+
+constexpr int kPairs = 76;  // of the 152 SMs
+
+int ceil_div(long long a, int b) { return (int)((a + b - 1) / b); }
+
+// Parts of a sum of `steps` steps of 64: the ones with the least time by this count, in SM
+// clocks of a pair: 512 a step, and behind a tile's last step about 3000 until its results
+// are out; a part's results are 8 bytes a value more to move (written and read again, at about
+// 3500 bytes a clock over all SMs).
+int splits_of(int tiles, int steps, double values) {
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= 16 && s <= steps; ++s) {
+    const int waves = ceil_div((long long)tiles * s, kPairs);
+    const double t = (double)waves * ceil_div(steps, s) * 512 + 3000 + (s > 1 ? 4000 + s * values * 8 / 3500 : 0);
+    if (s == 1 || t < least) best = s, least = t;
+  }
+  return best;
+}
+
+template <int KIND, int ACT>
+cudaError_t launch(Args& a, cudaStream_t st) {
+  a.tiles = a.m_tiles * a.n_tiles * a.splits * (KIND == kDw ? 2 : 1);
+  cudaError_t e = configure(ffn_tc_kernel<KIND, ACT>, smem_of(KIND));
+  if (e != cudaSuccess) return e;
+  const int pairs = a.tiles < sm_count() / 2 ? a.tiles : sm_count() / 2;
+  e = launch_cluster_pdl(ffn_tc_kernel<KIND, ACT>, dim3(2 * pairs), dim3(kThreads), smem_of(KIND), st, 2, a);
+  count_launches(1);
+  return e;
+}
+
+template <int KIND>
+cudaError_t launch_act(Args& a, int act, cudaStream_t st) {
+  return act == kSilu   ? launch<KIND, kSilu>(a, st)
+         : act == kGelu ? launch<KIND, kGelu>(a, st)
+                        : launch<KIND, kGeluTanh>(a, st);
+}
+
+// rows of `cols` elements `ld` apart, in boxes of b1 rows by 64 columns
+bool rows_map(CUtensorMap* m, const void* p, long long cols, long long rows, long long ld, int b1, int mats = 1) {
+  // (a single row's distance is of no use, but has to be one that the map takes)
+  return make_tmap_bf16_strided(m, p, cols, rows, mats, rows > 1 ? ld : cols, (size_t)rows * cols, 64, b1, 1);
+}
+
+struct Plan {
+  int dx_splits, dw_splits;
+  size_t dact, partial;  // bytes
+};
+
+Plan plan_of(int T, int C, int F) {
+  Plan p;
+  p.dx_splits = splits_of(ceil_div(T, 256) * ceil_div(C, 256), 2 * ceil_div(F, 64), (double)T * C);
+  p.dw_splits = splits_of(2 * ceil_div(F, 256) * ceil_div(C, 256), ceil_div(T, 64), 2.0 * F * C);
+  p.dact = align_up(2 * sizeof(__nv_bfloat16) * (size_t)T * F, 256);
+  const size_t x = p.dx_splits > 1 ? (size_t)p.dx_splits * T * C : 0;
+  const size_t w = p.dw_splits > 1 ? 2 * (size_t)p.dw_splits * F * C : 0;
+  p.partial = sizeof(float) * (x > w ? x : w);
+  return p;
+}
+
+}  // namespace
+
+size_t ffn_tc_backward_workspace(int T, int C, int F) {
+  const Plan p = plan_of(T, C, F);
+  return kHeaderBytes + p.dact + p.partial;
+}
+
+cudaError_t ffn_tc_forward(const FfnGate& f, void* ws, cudaStream_t st) {
+  Args a{};
+  a.hdr = static_cast<WorkspaceHeader*>(ws);
+  if (!rows_map(&a.a, f.x, f.C, f.T, f.x_stride, 128) || !rows_map(&a.b0, f.wg, f.C, f.F, f.C, 128) ||
+      !rows_map(&a.b1, f.wu, f.C, f.F, f.C, 128) || !rows_map(&a.out0, f.h, f.F, f.T, f.h_stride, 32))
+    return cudaErrorInvalidValue;
+  a.codes = f.codes;
+  a.exps = f.exps;
+  a.rows = f.T;
+  a.cols = f.F;
+  a.m_tiles = ceil_div(f.T, 256);
+  a.n_tiles = ceil_div(f.F, 128);
+  a.splits = 1;
+  a.steps = ceil_div(f.C, 64);
+  a.clear = 1;
+  return launch_act<kForward>(a, f.act, st);
+}
+
+cudaError_t ffn_tc_backward(const FfnGate& f, void* ws, cudaStream_t st) {
+  const Plan plan = plan_of(f.T, f.C, f.F);
+  char* at = static_cast<char*>(ws) + kHeaderBytes;
+  __nv_bfloat16 *da = reinterpret_cast<__nv_bfloat16*>(at), *du = da + (size_t)f.T * f.F;
+  float* partial = reinterpret_cast<float*>(at + plan.dact);
+  Args a{};
+  a.hdr = static_cast<WorkspaceHeader*>(ws);
+  cudaError_t e;
+  if (f.codes != nullptr) {
+    e = ffn_kept_grads(f, da, st);
+    a.clear = 1;
+  } else {
+    if (!rows_map(&a.a, f.x, f.C, f.T, f.x_stride, 128) || !rows_map(&a.b0, f.wg, f.C, f.F, f.C, 128) ||
+        !rows_map(&a.b1, f.wu, f.C, f.F, f.C, 128) || !rows_map(&a.dh, f.dh, f.F, f.T, f.dh_stride, 128) ||
+        !rows_map(&a.out0, da, f.F, f.T, f.F, 32) || !rows_map(&a.out1, du, f.F, f.T, f.F, 32))
+      return cudaErrorInvalidValue;
+    a.rows = f.T;
+    a.cols = f.F;
+    a.m_tiles = ceil_div(f.T, 256);
+    a.n_tiles = ceil_div(f.F, 128);
+    a.splits = 1;
+    a.steps = ceil_div(f.C, 64);
+    a.clear = 1;
+    e = launch_act<kGrads>(a, f.act, st);
+    a.clear = 0;
+  }
+  if (e != cudaSuccess) return e;
+
+  a.partial = partial;
+  a.cols = f.C;
+  a.n_tiles = ceil_div(f.C, 256);
+  // dx = [da | du] [wg; wu]
+  if (!rows_map(&a.a, da, f.F, f.T, f.F, 128, 2) || !rows_map(&a.b0, f.wg, f.C, f.F, f.C, 64) ||
+      !rows_map(&a.b1, f.wu, f.C, f.F, f.C, 64) || !rows_map(&a.out0, f.dx, f.C, f.T, f.dx_stride, 32))
+    return cudaErrorInvalidValue;
+  a.rows = f.T;
+  a.m_tiles = ceil_div(f.T, 256);
+  a.splits = plan.dx_splits;
+  a.per = ceil_div(f.F, 64);
+  a.steps = 2 * a.per;
+  e = launch<kDx, kSilu>(a, st);
+  a.clear = 0;
+  if (e == cudaSuccess && a.splits > 1)
+    e = ffn_join(partial, f.dx, nullptr, f.dx_stride, f.T, 1, f.C, a.splits, f.dtype, st);
+  if (e != cudaSuccess) return e;
+
+  // dwg, dwu = [da; du]^T x
+  if (!rows_map(&a.a, da, f.F, f.T, f.F, 64, 2) || !rows_map(&a.b0, f.x, f.C, f.T, f.x_stride, 64) ||
+      !rows_map(&a.out0, f.dwg, f.C, f.F, f.C, 32) || !rows_map(&a.out1, f.dwu, f.C, f.F, f.C, 32))
+    return cudaErrorInvalidValue;
+  a.rows = f.F;
+  a.m_tiles = ceil_div(f.F, 256);
+  a.splits = plan.dw_splits;
+  a.steps = ceil_div(f.T, 64);
+  e = launch<kDw, kSilu>(a, st);
+  if (e == cudaSuccess && a.splits > 1)
+    e = ffn_join(partial, f.dwg, f.dwu, f.C, f.F, 2, f.C, a.splits, f.dtype, st);
+  return e;
+}
+
+}  // namespace la

@@ -23,12 +23,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }  // namespace
 
 static bool make_tmap_3d(CUtensorMap* map, CUtensorMapDataType type, uint64_t esize, const void* base,
-                         uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1,
-                         uint32_t b2) {
+                         uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2,
+                         uint32_t b0, uint32_t b1, uint32_t b2) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (enc == nullptr) return false;
   cuuint64_t dims[3] = {d0, d1, d2};
-  cuuint64_t strides[2] = {d0 * esize, d0 * d1 * esize};
+  cuuint64_t strides[2] = {s1 * esize, s2 * esize};
   cuuint32_t box[3] = {b0, b1, b2};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = enc(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
@@ -39,12 +39,17 @@ static bool make_tmap_3d(CUtensorMap* map, CUtensorMapDataType type, uint64_t es
 
 bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                        uint32_t b0, uint32_t b1, uint32_t b2) {
-  return make_tmap_3d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, d0, d1, d2, b0, b1, b2);
+  return make_tmap_3d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, d0, d1, d2, d0, d0 * d1, b0, b1, b2);
+}
+
+bool make_tmap_bf16_strided(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                            uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2) {
+  return make_tmap_3d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, d0, d1, d2, s1, s2, b0, b1, b2);
 }
 
 bool make_tmap_f32_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                       uint32_t b0, uint32_t b1, uint32_t b2) {
-  return make_tmap_3d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, d0, d1, d2, b0, b1, b2);
+  return make_tmap_3d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, d0, d1, d2, d0, d0 * d1, b0, b1, b2);
 }
 
 }  // namespace la
