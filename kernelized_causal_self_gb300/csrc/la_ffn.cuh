@@ -25,9 +25,34 @@ __device__ __forceinline__ void sigmoid(float z, float& s, float& rest) {
   rest = z < 0.f ? large : small;
 }
 
+// P(a) of the gelu and e = exp(-a^2 / 2). FAST: with t = 1 / (1 + 0.375 |a| / sqrt(2)) a polynomial
+// of t for erfc(|a| / sqrt(2)) / e, fitted (least squares, reweighted towards the largest error) to
+// 6.4e-7 relative for |a| up to 13, past which e is 0: P(a) and 1 - P(a) keep their digits.
+template <bool FAST>
+__device__ __forceinline__ float normal(float a, float& e) {
+  if constexpr (!FAST) {
+    e = expf(-0.5f * a * a);
+    return 0.5f * erfcf(-0.70710678118654752f * a);
+  }
+  e = __expf(-0.5f * a * a);
+  const float t = __fdividef(1.f, fmaf(0.265165043f, fabsf(a), 1.f));
+  float q = -0.06754790f;
+  q = fmaf(q, t, 0.19396870f);
+  q = fmaf(q, t, -0.06479833f);
+  q = fmaf(q, t, 0.14153051f);
+  q = fmaf(q, t, 0.08333239f);
+  q = fmaf(q, t, 0.10784457f);
+  q = fmaf(q, t, 0.10566973f);
+  const float tail = q * t * e;  // of |a|
+  return a < 0.f ? tail : 1.f - tail;
+}
+
 template <int ACT, bool FAST>
 __device__ __forceinline__ float act(float a) {
-  if constexpr (ACT == kGelu) return 0.5f * a * erfcf(-0.70710678118654752f * a);
+  if constexpr (ACT == kGelu) {
+    float e;
+    return a * normal<FAST>(a, e);
+  }
   float z = a;
   if constexpr (ACT == kGeluTanh) z = 1.5957691216057308f * a * fmaf(0.044715f * a, a, 1.f);
   if constexpr (FAST) return a * __fdividef(1.f, 1.f + __expf(-z));  // (0 once exp(-z) is infinite)
@@ -39,8 +64,8 @@ __device__ __forceinline__ float act(float a) {
 template <int ACT, bool FAST>
 __device__ __forceinline__ void act_grad(float a, float& f, float& df) {
   if constexpr (ACT == kGelu) {
-    const float p = 0.5f * erfcf(-0.70710678118654752f * a);
-    const float e = FAST ? __expf(-0.5f * a * a) : expf(-0.5f * a * a);
+    float e;
+    const float p = normal<FAST>(a, e);
     f = a * p;
     df = fmaf(0.3989422804014327f * a, e, p);
     return;

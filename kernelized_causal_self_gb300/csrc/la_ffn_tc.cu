@@ -5,7 +5,7 @@
 // One persistent kernel for all five products. A pair of CTAs (cta_group::2) makes a tile of
 // 256 x 256: each CTA copies its 128 rows of A and its half of B's 256 rows by TMA, 64 terms
 // of the sum a stage, the even one issues the MMAs, and each finds its 128 x 256 of D in its
-// own tensor memory, where two accumulators take turns, so that four warps write one tile's
+// own tensor memory, where two accumulators take turns, so that eight warps write one tile's
 // results while the next is summed.
 //   kForward, kGrads  A = x, B = 128 rows of wg (even CTA) and the same rows of wu (odd CTA): a
 //                     row's a and u come to lie in one thread, 128 columns apart, and nothing
@@ -30,14 +30,15 @@ using namespace ffn;
 
 enum Kind { kForward, kGrads, kDx, kDw };
 
-constexpr int kThreads = 192;     // four warps of results, one that copies, one that multiplies
+constexpr int kWarps = 8;          // warps of results: two for each 32 rows, half the columns each
+constexpr int kThreads = 32 * (kWarps + 2);  // one that copies, one that multiplies
 constexpr int kTileBytes = 16384;  // 128 x 64 bf16
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kStore = 4096;       // a warp's staging tile: 32 rows x 64 bf16
 constexpr int stages_of(int kind) { return kind == kGrads ? 4 : 6; }
-constexpr int staging_of(int kind) { return (kind == kGrads ? 4 : 2) * kStore; }  // a warp
+constexpr int staging_of(int kind) { return (kind == kGrads ? 2 : 1) * kStore; }  // a warp
 constexpr int smem_of(int kind) {
-  return 1024 + stages_of(kind) * kStageBytes + 4 * staging_of(kind) + (kind == kGrads ? 2 * kTileBytes : 0) + 256;
+  return 1024 + stages_of(kind) * kStageBytes + kWarps * staging_of(kind) + (kind == kGrads ? 2 * kTileBytes : 0) + 256;
 }
 
 struct Args {
@@ -84,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
   uint8_t* stages = sm;                                  // [stage][A | B]
   uint8_t* dht = stages + S * kStageBytes;               // kGrads: dh's tile, two blocks of 64 columns
   uint8_t* staging = dht + (KIND == kGrads ? 2 * kTileBytes : 0);
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + 4 * staging_of(KIND));  // S (the even CTA's count)
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kWarps * staging_of(KIND));  // S (the even CTA's count)
   uint64_t* empty = full + S;                            // S: the MMAs are done with the stage
   uint64_t* acc_full = empty + S;                        // 2: an accumulator holds its tile
   uint64_t* acc_empty = acc_full + 2;                    // 2 (the even CTA's): both CTAs have read it
@@ -104,10 +105,10 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 8);  // four warps of each CTA
+      mbar_init(&acc_empty[b], 2 * kWarps);
     }
     mbar_init(dh_full, 1);
-    mbar_init(dh_empty, 4);
+    mbar_init(dh_empty, kWarps);
     mbar_init(drain, 1);
     *abort = 0;
     fence_mbar_init();
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
   // (a wait that runs out is recorded two seconds after its kernel began, long after this)
   if (a.clear && blockIdx.x == 0 && threadIdx.x == 0) hdr->status = hdr->wait_site = 0;
 
-  if (warp == 4) {
+  if (warp == kWarps) {
     // ------------------------------------------------------------------ copies
     if (lane == 0) {
       long long n = 0;  // stages asked for
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
         record_timeout(hdr, kSiteDrain);
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == kWarps + 1) {
     // ------------------------------------------------------------------ products
     if (lane == 0 && rank == 0) {
       constexpr uint32_t id = idesc_bf16(256, 256, KIND == kDw, !DUAL);
@@ -219,27 +220,25 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
   } else {
     // ------------------------------------------------------------------ results
     uint8_t* mine = staging + warp * staging_of(KIND);
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
     const uint32_t freed = cluster_map(smem_u32(acc_empty), 0);
-    const int trow = warp * 32 + lane;  // of the CTA's 128
-    int nt = 0, turn = 0;
+    const int trow = warp % 4 * 32 + lane;  // of the CTA's 128
+    constexpr int GROUPS = DUAL ? 1 : 2;    // of 64 columns
+    int nt = 0;
     for (int t = cluster; t < a.tiles; t += clusters, ++nt) {
       const Tile w = tile_of<KIND>(a, t);
-      const int b = nt & 1, row0 = w.m * 256 + (int)rank * 128 + warp * 32, row = row0 + lane;
+      const int b = nt & 1, row0 = w.m * 256 + (int)rank * 128 + warp % 4 * 32, row = row0 + lane;
       if (!mbar_wait_warp(&acc_full[b], (uint32_t)((nt / 2) & 1), abort, hdr, kSiteAccFull)) break;
       if (KIND == kGrads && !mbar_wait_warp(dh_full, (uint32_t)(nt & 1), abort, hdr, kSiteDhFull)) break;
       fence_after_sync();
       const uint32_t d = tbase + 256 * b + lanes;
-      constexpr int GROUPS = DUAL ? 2 : 4;  // of 64 columns
 #pragma unroll 1
-      for (int g = 0; g < GROUPS; ++g) {
+      for (int g = warp / 4 * GROUPS; g < (warp / 4 + 1) * GROUPS; ++g) {
         const int col = w.n * (DUAL ? 128 : 256) + g * 64;
         const bool cut = !DUAL && a.splits > 1;
-        // the staging tile's last copy has read it (of two in turn; kGrads: two pairs)
-        uint8_t* st = mine + turn * (staging_of(KIND) / 2);
-        if (!cut) {
-          turn ^= 1;
-          if (lane == 0) bulk_wait_read<1>();
+        uint8_t* st = mine;
+        if (!cut) {  // the last copy out of the staging tile has read it
+          if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
         }
 #pragma unroll
@@ -321,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
             }
           }
         }
-        if (g == GROUPS - 1) {  // the accumulator (and dh's tile) may be written again
+        if (g % GROUPS == GROUPS - 1) {  // the accumulator (and dh's tile) may be written again
           fence_before_sync();
           __syncwarp();
           if (lane == 0) {
