@@ -130,20 +130,20 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
   if (warp == kWarps) {
     // ------------------------------------------------------------------ copies
     if (lane == 0) {
-      long long n = 0;  // stages asked for
+      const uint32_t bars = cluster_map(smem_u32(full), 0);
+      uint32_t s = 0, phase = 1;  // (a stage not used yet counts as emptied once)
       int nt = 0;
       bool ok = true;
       for (int t = cluster; t < a.tiles && ok; t += clusters, ++nt) {
         const Tile w = tile_of<KIND>(a, t);
         const int row = w.m * 256 + (int)rank * 128;
-        for (int k = w.k0; k < w.k1; ++k, ++n) {
-          const int s = (int)(n % S);
-          if (n >= S && !mbar_wait_abort(&empty[s], (uint32_t)((n / S - 1) & 1), abort, hdr, kSiteEmpty)) {
+        for (int k = w.k0; k < w.k1; ++k) {
+          if (!mbar_wait_abort(&empty[s], phase, abort, hdr, kSiteEmpty)) {
             ok = false;
             break;
           }
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
-          const uint32_t bar = cluster_map(smem_u32(&full[s]), 0);
+          const uint32_t bar = bars + 8 * s;
           uint8_t *ta = stages + s * kStageBytes, *tb = ta + kTileBytes;
           if constexpr (DUAL) {
             tma_load_3d_pair(ta, &a.a, bar, k * 64, row, 0);
@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
             tma_load_3d_pair(tb, &a.b0, bar, col, k * 64, 0);
             tma_load_3d_pair(tb + kTileBytes / 2, &a.b0, bar, col + 64, k * 64, 0);
           }
+          if (++s == S) s = 0, phase ^= 1;
         }
         if constexpr (KIND == kGrads) {
           // dh's tile, behind the tile's operands: its room is free once the last tile's results are out
@@ -173,9 +174,10 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
         }
       }
       // the pair's copies have all landed before either CTA lets go of its shared memory
+      // (stages before s were last asked for in this turn, the others in the one before, if any)
       if (rank == 0)
-        for (long long k = n > S ? n - S : 0; k < n; ++k)
-          if (!mbar_wait(&full[k % S], (uint32_t)((k / S) & 1))) record_timeout(hdr, kSiteDrain);
+        for (uint32_t k = 0; k < S; ++k)
+          if (!mbar_wait(&full[k], k < s ? phase ^ 1 : phase)) record_timeout(hdr, kSiteDrain);
       if (KIND == kGrads && nt > 0 && !mbar_wait(dh_full, (uint32_t)((nt - 1) & 1)))
         record_timeout(hdr, kSiteDrain);
     }
@@ -184,7 +186,12 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
     // ------------------------------------------------------------------ products
     if (lane == 0 && rank == 0) {
       constexpr uint32_t id = idesc_bf16(256, 256, KIND == kDw, !DUAL);
-      long long n = 0;
+      // along k: 32 bytes of a row a step of 16; along m or n: 16 rows, blocks of 64 columns 8 KB apart
+      const uint32_t at = smem_u32(stages);
+      const uint64_t da0 = KIND == kDw ? sdesc(at, kTileBytes / 2, 1024) : sdesc(at, 16, 1024);
+      const uint64_t db0 = DUAL ? sdesc(at + kTileBytes, 16, 1024) : sdesc(at + kTileBytes, kTileBytes / 2, 1024);
+      constexpr uint32_t STEP_A = (KIND == kDw ? 2048 : 32) / 16, STEP_B = (DUAL ? 32 : 2048) / 16;
+      uint32_t s = 0, phase = 0;
       int nt = 0;
       bool ok = true;
       for (int t = cluster; t < a.tiles && ok; t += clusters, ++nt) {
@@ -194,22 +201,18 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
         if (!ok) break;
         fence_after_sync();
         const uint32_t d = tbase + 256 * b;
-        for (int k = w.k0; k < w.k1; ++k, ++n) {
-          const int s = (int)(n % S);
-          if (!mbar_wait_abort(&full[s], (uint32_t)((n / S) & 1), abort, hdr, kSiteFull)) {
+        for (int k = w.k0; k < w.k1; ++k) {
+          if (!mbar_wait_abort(&full[s], phase, abort, hdr, kSiteFull)) {
             ok = false;
             break;
           }
           fence_after_sync();
-          const uint32_t ta = smem_u32(stages + s * kStageBytes), tb = ta + kTileBytes;
+          // (addresses are the descriptors' low bits, in units of 16 bytes)
+          const uint64_t da = da0 + s * (kStageBytes / 16), db = db0 + s * (kStageBytes / 16);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            // along k: 32 bytes of a row a step; along m or n: 16 rows, blocks of 64 columns 8 KB apart
-            const uint64_t da = KIND == kDw ? sdesc(ta + q * 2048, kTileBytes / 2, 1024) : sdesc(ta + q * 32, 16, 1024);
-            const uint64_t db = DUAL ? sdesc(tb + q * 32, 16, 1024) : sdesc(tb + q * 2048, kTileBytes / 2, 1024);
-            mma_ss_pair(d, da, db, id, k > w.k0 || q > 0);
-          }
+          for (int q = 0; q < 4; ++q) mma_ss_pair(d, da + q * STEP_A, db + q * STEP_B, id, k > w.k0 || q > 0);
           mma_commit_pair(&empty[s]);
+          if (++s == S) s = 0, phase ^= 1;
         }
         if (ok) mma_commit_pair(&acc_full[b]);
       }
