@@ -23,7 +23,12 @@ __device__ __forceinline__ uint32_t step_of(uint32_t top) {
   return top >= 0x7F800000u ? 255u : (uint32_t)max(e, 1);
 }
 
-__device__ __forceinline__ uint32_t bits_of(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+// the largest magnitude of three, NaN if one is (whose bits are above infinity's)
+__device__ __forceinline__ float top3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 
 // one over the step (any finite number for e = 255, whose codes are masked)
 __device__ __forceinline__ float inverse_step(uint32_t e) {
@@ -79,9 +84,10 @@ __device__ __forceinline__ void values_of(const typename Codes<V>::type& c, floa
 // The largest magnitude's bits over the 32 / V neighbouring lanes that hold a block
 template <int V>
 __device__ __forceinline__ uint32_t block_top(const float* x) {
-  uint32_t top = 0;
+  float most = fabsf(x[0]);
 #pragma unroll
-  for (int i = 0; i < V; ++i) top = max(top, bits_of(x[i]));
+  for (int i = 1; i + 1 < V; i += 2) most = top3(most, x[i], x[i + 1]);
+  uint32_t top = __float_as_uint(top3(most, x[V - 1], x[V - 1]));
 #pragma unroll
   for (int o = kBlock / V / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
   return top;

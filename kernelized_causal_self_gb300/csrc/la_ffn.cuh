@@ -7,78 +7,122 @@
 
 #include "la_common.cuh"
 #include "la_internal.h"
+#include "la_tc_common.cuh"
 
 namespace la {
 namespace ffn {
 
 enum Act { kSilu = 0, kGelu = 1, kGeluTanh = 2 };
 
-// s = sigmoid(z) and 1 - s. FAST (results in bf16): by __expf, off by 2 + 1.17 |z| steps of
-// 2^-23, and a quotient off by 2; past |z| = 87 the smaller one is 0 instead of below 2^-125.
-// Otherwise from expf and a rounded quotient. 1 - s cancels nothing: both come from exp(-|z|).
-template <bool FAST>
+// float32 results: expf, erfcf and rounded quotients. 1 - s cancels nothing: both come from
+// exp(-|z|).
 __device__ __forceinline__ void sigmoid(float z, float& s, float& rest) {
-  const float e = FAST ? __expf(-fabsf(z)) : expf(-fabsf(z));
-  const float large = FAST ? __fdividef(1.f, 1.f + e) : 1.f / (1.f + e);
-  const float small = e * large;
+  const float e = expf(-fabsf(z));
+  const float large = 1.f / (1.f + e), small = e * large;
   s = z < 0.f ? small : large;
   rest = z < 0.f ? large : small;
 }
 
-// P(a) of the gelu and e = exp(-a^2 / 2). FAST: with t = 1 / (1 + 0.375 |a| / sqrt(2)) a polynomial
-// of t for erfc(|a| / sqrt(2)) / e, fitted (least squares, reweighted towards the largest error) to
-// 6.4e-7 relative for |a| up to 13, past which e is 0: P(a) and 1 - P(a) keep their digits.
-template <bool FAST>
-__device__ __forceinline__ float normal(float a, float& e) {
-  if constexpr (!FAST) {
-    e = expf(-0.5f * a * a);
-    return 0.5f * erfcf(-0.70710678118654752f * a);
-  }
-  e = __expf(-0.5f * a * a);
-  const float t = __fdividef(1.f, fmaf(0.265165043f, fabsf(a), 1.f));
-  float q = -0.06754790f;
-  q = fmaf(q, t, 0.19396870f);
-  q = fmaf(q, t, -0.06479833f);
-  q = fmaf(q, t, 0.14153051f);
-  q = fmaf(q, t, 0.08333239f);
-  q = fmaf(q, t, 0.10784457f);
-  q = fmaf(q, t, 0.10566973f);
-  const float tail = q * t * e;  // of |a|
-  return a < 0.f ? tail : 1.f - tail;
-}
-
-template <int ACT, bool FAST>
-__device__ __forceinline__ float act(float a) {
-  if constexpr (ACT == kGelu) {
-    float e;
-    return a * normal<FAST>(a, e);
-  }
-  float z = a;
-  if constexpr (ACT == kGeluTanh) z = 1.5957691216057308f * a * fmaf(0.044715f * a, a, 1.f);
-  if constexpr (FAST) return a * __fdividef(1.f, 1.f + __expf(-z));  // (0 once exp(-z) is infinite)
-  float s, rest;
-  sigmoid<FAST>(z, s, rest);
-  return a * s;
-}
-
-template <int ACT, bool FAST>
+template <int ACT>
 __device__ __forceinline__ void act_grad(float a, float& f, float& df) {
   if constexpr (ACT == kGelu) {
-    float e;
-    const float p = normal<FAST>(a, e);
+    const float p = 0.5f * erfcf(-0.70710678118654752f * a);
     f = a * p;
-    df = fmaf(0.3989422804014327f * a, e, p);
+    df = fmaf(0.3989422804014327f * a, expf(-0.5f * a * a), p);
     return;
   }
   float z = a, dz = 1.f, s, rest;
   if constexpr (ACT == kGeluTanh) {
-    const float q = 0.044715f * a * a;
-    z = 1.5957691216057308f * a * (1.f + q);
+    const float b = fminf(fmaxf(a, -16.f), 16.f);  // (s is 0 or 1 there, and nothing overflows)
+    const float q = 0.044715f * b * b;
+    z = 1.5957691216057308f * b * (1.f + q);
     dz = 1.5957691216057308f * fmaf(3.f, q, 1.f);
   }
-  sigmoid<FAST>(z, s, rest);
+  sigmoid(z, s, rest);
   f = a * s;
   df = s * fmaf(a * dz, rest, 1.f);
+}
+
+template <int ACT>
+__device__ __forceinline__ float act(float a) {
+  float f, df;
+  act_grad<ACT>(a, f, df);
+  return f;
+}
+
+// bf16 results, two neighbours at once in packed arithmetic, with the hardware's base-2
+// exponential and reciprocal (each off by 2 steps of 2^-23 at most, zero below 2^-126: 2^-17 in
+// all for exponents below 30, far below the result's rounding).
+__device__ __forceinline__ float2 ex2(float2 x) {
+  float2 y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(x.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(x.y));
+  return y;
+}
+__device__ __forceinline__ float2 rcp(float2 x) {
+  float2 y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(x.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(x.y));
+  return y;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// s = 1 / (1 + 2^y), y = -z log2(e): 0 once 2^y is infinite
+__device__ __forceinline__ float2 sigmoid2(float2 y) { return rcp(tcx::add2(ex2(y), both(1.f))); }
+
+// y of the gelu_tanh's sigmoid, and q = 0.044715 a^2, of a within +-16, where s is 0 or 1
+__device__ __forceinline__ float2 tanh_arg(float2 a, float2& q) {
+  a = make_float2(fminf(fmaxf(a.x, -16.f), 16.f), fminf(fmaxf(a.y, -16.f), 16.f));
+  q = tcx::mul2(tcx::mul2(a, both(0.044715f)), a);
+  return tcx::mul2(tcx::mul2(a, both(-2.302208198f)), tcx::add2(q, both(1.f)));
+}
+
+// P(a) and e = exp(-a^2 / 2). With t = 1 / (1 + 0.375 |a| / sqrt(2)), a polynomial of t for
+// erfc(|a| / sqrt(2)) / e, fitted (least squares, reweighted towards the largest error) to 6.4e-7
+// relative for |a| up to 13, past which e is 0: P(a) and 1 - P(a) keep their digits.
+__device__ __forceinline__ float2 normal2(float2 a, float2& e) {
+  using namespace tcx;
+  e = ex2(mul2(mul2(a, both(-0.72134752f)), a));
+  const float2 t = rcp(fma2(make_float2(fabsf(a.x), fabsf(a.y)), both(0.265165043f), both(1.f)));
+  float2 q = both(-0.06754790f);
+  q = fma2(q, t, both(0.19396870f));
+  q = fma2(q, t, both(-0.06479833f));
+  q = fma2(q, t, both(0.14153051f));
+  q = fma2(q, t, both(0.08333239f));
+  q = fma2(q, t, both(0.10784457f));
+  q = fma2(q, t, both(0.10566973f));
+  const float2 tail = mul2(mul2(q, t), e);  // of |a|
+  const float2 rest = sub2(both(1.f), tail);
+  return make_float2(a.x < 0.f ? tail.x : rest.x, a.y < 0.f ? tail.y : rest.y);
+}
+
+template <int ACT>
+__device__ __forceinline__ float2 act2(float2 a) {
+  float2 q;
+  if constexpr (ACT == kGelu) return tcx::mul2(a, normal2(a, q));
+  if constexpr (ACT == kGeluTanh) return tcx::mul2(a, sigmoid2(tanh_arg(a, q)));
+  return tcx::mul2(a, sigmoid2(tcx::mul2(a, both(-1.44269504f))));
+}
+
+// (1 - s is a difference here, off by 2^-24 and 0 where s is 1)
+template <int ACT>
+__device__ __forceinline__ void act_grad2(float2 a, float2& f, float2& df) {
+  using namespace tcx;
+  float2 q;
+  if constexpr (ACT == kGelu) {
+    const float2 p = normal2(a, q);
+    f = mul2(a, p);
+    df = fma2(mul2(a, both(0.39894228f)), q, p);
+  } else if constexpr (ACT == kGeluTanh) {
+    const float2 s = sigmoid2(tanh_arg(a, q));
+    f = mul2(a, s);
+    const float2 dz = fma2(q, both(4.787307365f), both(1.595769122f));
+    df = fma2(mul2(f, dz), sub2(both(1.f), s), s);
+  } else {
+    const float2 s = sigmoid2(mul2(a, both(-1.44269504f)));
+    f = mul2(a, s);
+    df = fma2(f, sub2(both(1.f), s), s);
+  }
 }
 
 }  // namespace ffn

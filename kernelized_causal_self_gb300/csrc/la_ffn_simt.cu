@@ -50,6 +50,15 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(tc::pack_bf16(v.x, v.y), tc::pack_bf16(v.z, v.w));
 }
 
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  store4(p, make_float4(v[0], v[1], v[2], v[3]));
+  store4(p + 4, make_float4(v[4], v[5], v[6], v[7]));
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(tc::pack_bf16(v[0], v[1]), tc::pack_bf16(v[2], v[3]),
+                                            tc::pack_bf16(v[4], v[5]), tc::pack_bf16(v[6], v[7]));
+}
+
 template <typename T, int KIND, int ACT, int BM, int BN>
 __global__ void __launch_bounds__(BM * BN / 64, BM == 128 ? 2 : 8) ffn_simt_kernel(const Args a) {
   constexpr int THREADS = BM * BN / 64, TX = BN / 8, PAD = 4;
@@ -158,7 +167,6 @@ __global__ void __launch_bounds__(BM * BN / 64, BM == 128 ? 2 : 8) ffn_simt_kern
     __syncthreads();
   }
 
-  constexpr bool FAST = sizeof(T) == 2;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int m = m0 + (i < 4 ? 0 : BM / 2) + ty * 4 + i % 4;
@@ -174,10 +182,10 @@ __global__ void __launch_bounds__(BM * BN / 64, BM == 128 ? 2 : 8) ffn_simt_kern
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if constexpr (KIND == kForward) {
-          o[j] = act<ACT, FAST>(lo[j]) * hi[j];
+          o[j] = act<ACT>(lo[j]) * hi[j];
         } else {
           float fa, df;
-          act_grad<ACT, FAST>(lo[j], fa, df);
+          act_grad<ACT>(lo[j], fa, df);
           o[j] = dv[j] * hi[j] * df;
           o2[j] = dv[j] * fa;
         }
@@ -241,36 +249,43 @@ __global__ void __launch_bounds__(256) ffn_join_kernel(const float* partial, T* 
   }
 }
 
-// da, du from a checkpoint of a and u, 4 neighbours a thread
+// da, du from a checkpoint of a and u: 8 neighbours a thread, all of a block's step. Bound by
+// memory (T 4096, F 5632 in bf16: 186 MB).
 template <typename T, int ACT>
 __global__ void __launch_bounds__(256) ffn_kept_grads_kernel(const Args a) {
-  const int per = a.F / 4, nb = q8::blocks_of(a.F);
-  const long long n = (long long)a.T * per;
+  const unsigned per = a.F / 8, nb = q8::blocks_of(a.F);
   const size_t part = (size_t)a.T * a.F;
   tc::pdl_wait();
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-    const long long t = i / per;
-    const int f = (int)(i - t * per) * 4;
-    const size_t row = 2 * (size_t)t;
-    const float4 d = load4(static_cast<const T*>(a.dh) + t * a.dh_stride + f);
-    float g[4], u[4];
-    q8::values_of<4>(*reinterpret_cast<const uint32_t*>(a.codes + row * a.F + f),
-                     q8::step_value(a.exps[row * nb + f / q8::kBlock]), g);
-    q8::values_of<4>(*reinterpret_cast<const uint32_t*>(a.codes + (row + 1) * a.F + f),
-                     q8::step_value(a.exps[(row + 1) * nb + f / q8::kBlock]), u);
-    const float dv[4] = {d.x, d.y, d.z, d.w};
-    float da[4], du[4];
+  const unsigned long long at = (unsigned long long)blockIdx.x * 256;  // (one 64-bit division a CTA)
+  const unsigned i = (unsigned)(at % per) + threadIdx.x;
+  const size_t t = at / per + i / per;
+  if (t >= a.T) return;
+  const unsigned f = i % per * 8;
+  const size_t row = 2 * t;
+  const T* dh = static_cast<const T*>(a.dh) + (long long)t * a.dh_stride + f;
+  const uint2 ca = __ldcs(reinterpret_cast<const uint2*>(a.codes + row * a.F + f));
+  const uint2 cu = __ldcs(reinterpret_cast<const uint2*>(a.codes + (row + 1) * a.F + f));
+  const float4 d0 = load4(dh), d1 = load4(dh + 4);
+  float g[8], u[8];
+  q8::values_of<8>(ca, q8::step_value(a.exps[row * nb + f / q8::kBlock]), g);
+  q8::values_of<8>(cu, q8::step_value(a.exps[(row + 1) * nb + f / q8::kBlock]), u);
+  const float dv[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+  float da[8], du[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float fa, df;
-      act_grad<ACT, sizeof(T) == 2>(g[j], fa, df);
-      da[j] = dv[j] * u[j] * df;
-      du[j] = dv[j] * fa;
+  for (int j = 0; j < 8; j += 2) {
+    float2 fa, df;
+    if constexpr (sizeof(T) == 2) {
+      act_grad2<ACT>(make_float2(g[j], g[j + 1]), fa, df);
+    } else {
+      act_grad<ACT>(g[j], fa.x, df.x);
+      act_grad<ACT>(g[j + 1], fa.y, df.y);
     }
-    T* to = static_cast<T*>(a.dact) + (size_t)t * a.F + f;
-    store4(to, make_float4(da[0], da[1], da[2], da[3]));
-    store4(to + part, make_float4(du[0], du[1], du[2], du[3]));
+    da[j] = dv[j] * u[j] * df.x, da[j + 1] = dv[j + 1] * u[j + 1] * df.y;
+    du[j] = dv[j] * fa.x, du[j + 1] = dv[j + 1] * fa.y;
   }
+  T* to = static_cast<T*>(a.dact) + t * a.F + f;
+  store8(to, da);
+  store8(to + part, du);
 }
 
 constexpr int kSms = 152;
@@ -318,8 +333,7 @@ cudaError_t grads(const Args& a, int act, cudaStream_t st) {
 
 template <typename T>
 cudaError_t kept_grads(const Args& a, int act, cudaStream_t st) {
-  const long long n = (long long)a.T * (a.F / 4);
-  const dim3 grid((unsigned)((n + 255) / 256 < 16 * kSms ? (n + 255) / 256 : 16 * kSms));
+  const dim3 grid((unsigned)(((long long)a.T * (a.F / 8) + 255) / 256));  // (T <= 2^24, F <= 2^16: an int)
   const cudaError_t e =
       act == kSilu   ? launch_pdl(ffn_kept_grads_kernel<T, kSilu>, grid, dim3(256), 0, st, a)
       : act == kGelu ? launch_pdl(ffn_kept_grads_kernel<T, kGelu>, grid, dim3(256), 0, st, a)

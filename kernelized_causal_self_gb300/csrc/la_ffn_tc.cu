@@ -35,10 +35,9 @@ constexpr int kThreads = 32 * (kWarps + 2);  // one that copies, one that multip
 constexpr int kTileBytes = 16384;  // 128 x 64 bf16
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kStore = 4096;       // a warp's staging tile: 32 rows x 64 bf16
-constexpr int stages_of(int kind) { return kind == kGrads ? 4 : 6; }
-constexpr int staging_of(int kind) { return (kind == kGrads ? 2 : 1) * kStore; }  // a warp
+constexpr int stages_of(int kind) { return kind == kGrads ? 5 : 6; }
 constexpr int smem_of(int kind) {
-  return 1024 + stages_of(kind) * kStageBytes + kWarps * staging_of(kind) + (kind == kGrads ? 2 * kTileBytes : 0) + 256;
+  return 1024 + stages_of(kind) * kStageBytes + kWarps * kStore + (kind == kGrads ? 2 * kTileBytes : 0) + 256;
 }
 
 struct Args {
@@ -56,21 +55,26 @@ struct Args {
 };
 
 struct Tile {
-  int m, n, part, split, k0, k1;  // part: kDw: dwg or dwu
+  int m, n, part, split;  // part: kDw: dwg or dwu
 };
 
 template <int KIND>
-__device__ __forceinline__ Tile tile_of(const Args& a, int t) {
+__device__ __forceinline__ Tile tile_of(const Args& a, uint32_t t) {
   Tile r;
-  r.n = t % a.n_tiles;
-  t /= a.n_tiles;
-  r.m = t % a.m_tiles;
-  t /= a.m_tiles;
-  r.part = KIND == kDw ? t % 2 : 0;
-  r.split = KIND == kDw ? t / 2 : t;
-  r.k0 = (int)((long long)a.steps * r.split / a.splits);
-  r.k1 = (int)((long long)a.steps * (r.split + 1) / a.splits);
+  const uint32_t row = t / (uint32_t)a.n_tiles, mat = row / (uint32_t)a.m_tiles;
+  r.n = (int)(t - row * (uint32_t)a.n_tiles);
+  r.m = (int)(row - mat * (uint32_t)a.m_tiles);
+  r.part = KIND == kDw ? (int)(mat & 1) : 0;
+  r.split = (int)(KIND == kDw ? mat >> 1 : mat);
   return r;
+}
+
+// The steps of tile t's sum (the whole one in kForward and kGrads, which are not cut). At most
+// 2^18 steps and 16 parts.
+template <int KIND>
+__device__ __forceinline__ int first_step(const Args& a, int split) {
+  if (KIND == kForward || KIND == kGrads || a.splits == 1) return split ? a.steps : 0;
+  return (int)((uint32_t)(a.steps * split) / (uint32_t)a.splits);
 }
 
 // Wait codes of this file's kernels (la_workspace_wait_site)
@@ -85,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
   uint8_t* stages = sm;                                  // [stage][A | B]
   uint8_t* dht = stages + S * kStageBytes;               // kGrads: dh's tile, two blocks of 64 columns
   uint8_t* staging = dht + (KIND == kGrads ? 2 * kTileBytes : 0);
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kWarps * staging_of(KIND));  // S (the even CTA's count)
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kWarps * kStore);  // S (the even CTA's count)
   uint64_t* empty = full + S;                            // S: the MMAs are done with the stage
   uint64_t* acc_full = empty + S;                        // 2: an accumulator holds its tile
   uint64_t* acc_empty = acc_full + 2;                    // 2 (the even CTA's): both CTAs have read it
@@ -136,8 +140,8 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
       bool ok = true;
       for (int t = cluster; t < a.tiles && ok; t += clusters, ++nt) {
         const Tile w = tile_of<KIND>(a, t);
-        const int row = w.m * 256 + (int)rank * 128;
-        for (int k = w.k0; k < w.k1; ++k) {
+        const int row = w.m * 256 + (int)rank * 128, end = first_step<KIND>(a, w.split + 1);
+        for (int k = first_step<KIND>(a, w.split); k < end; ++k) {
           if (!mbar_wait_abort(&empty[s], phase, abort, hdr, kSiteEmpty)) {
             ok = false;
             break;
@@ -195,13 +199,17 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
       int nt = 0;
       bool ok = true;
       for (int t = cluster; t < a.tiles && ok; t += clusters, ++nt) {
-        const Tile w = tile_of<KIND>(a, t);
+        int n = a.steps;
+        if (!DUAL && a.splits > 1) {
+          const int split = tile_of<KIND>(a, t).split;
+          n = first_step<KIND>(a, split + 1) - first_step<KIND>(a, split);
+        }
         const int b = nt & 1;
         if (nt >= 2) ok = mbar_wait_abort(&acc_empty[b], (uint32_t)((nt / 2 - 1) & 1), abort, hdr, kSiteAccEmpty);
         if (!ok) break;
         fence_after_sync();
         const uint32_t d = tbase + 256 * b;
-        for (int k = w.k0; k < w.k1; ++k) {
+        for (int k = 0; k < n; ++k) {
           if (!mbar_wait_abort(&full[s], phase, abort, hdr, kSiteFull)) {
             ok = false;
             break;
@@ -210,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
           // (addresses are the descriptors' low bits, in units of 16 bytes)
           const uint64_t da = da0 + s * (kStageBytes / 16), db = db0 + s * (kStageBytes / 16);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) mma_ss_pair(d, da + q * STEP_A, db + q * STEP_B, id, k > w.k0 || q > 0);
+          for (int q = 0; q < 4; ++q) mma_ss_pair(d, da + q * STEP_A, db + q * STEP_B, id, (k | q) != 0);
           mma_commit_pair(&empty[s]);
           if (++s == S) s = 0, phase ^= 1;
         }
@@ -222,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ results
-    uint8_t* mine = staging + warp * staging_of(KIND);
+    uint8_t* mine = staging + warp * kStore;
     const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
     const uint32_t freed = cluster_map(smem_u32(acc_empty), 0);
     const int trow = warp % 4 * 32 + lane;  // of the CTA's 128
@@ -240,10 +248,20 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
         const int col = w.n * (DUAL ? 128 : 256) + g * 64;
         const bool cut = !DUAL && a.splits > 1;
         uint8_t* st = mine;
-        if (!cut) {  // the last copy out of the staging tile has read it
+        uint32_t gu[KIND == kGrads ? 32 : 1];  // du, which follows da through the staging tile
+        auto leave = [&](const CUtensorMap* to) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (row0 < a.rows && col < a.cols) tma_store_3d(to, st, col, row0, 0);
+            bulk_commit();
+          }
+        };
+        auto left = [&]() {  // the last copy out of the staging tile has read it
           if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
-        }
+        };
+        if (!cut) left();
 #pragma unroll
         for (int c = 0; c < 2; ++c) {  // 32 columns
           uint32_t p[32], q[32];
@@ -257,7 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   const int j = e * 8 + i * 2;
-                  o[i] = pack_bf16(act<ACT, true>(fa[j]) * fu[j], act<ACT, true>(fa[j + 1]) * fu[j + 1]);
+                  const float2 h = mul2(act2<ACT>(make_float2(fa[j], fa[j + 1])), make_float2(fu[j], fu[j + 1]));
+                  o[i] = pack_bf16(h.x, h.y);
                 }
                 *reinterpret_cast<uint4*>(st + sw128(lane, c * 64 + e * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
               }
@@ -266,10 +285,10 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
                   const float* x = v ? fu : fa;
-                  uint32_t top = 0;
+                  float top = fabsf(x[0]);
 #pragma unroll
-                  for (int j = 0; j < 32; ++j) top = max(top, q8::bits_of(x[j]));
-                  const uint32_t e = q8::step_of(top);
+                  for (int j = 1; j < 31; j += 2) top = q8::top3(top, x[j], x[j + 1]);
+                  const uint32_t e = q8::step_of(__float_as_uint(q8::top3(top, x[31], x[31])));
                   const float inv = q8::inverse_step(e);
                   if (row < a.rows && f < a.cols) {
                     const size_t r = 2 * (size_t)row + v;
@@ -289,19 +308,18 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
                 const uint32_t at = sw128(lane, c * 64 + e * 16);
                 const uint4 v = *reinterpret_cast<const uint4*>(dht + g * kTileBytes + sw128(trow, c * 64 + e * 16));
                 const uint32_t dh[4] = {v.x, v.y, v.z, v.w};
-                uint32_t oa[4], ou[4];
+                uint32_t oa[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   const int j = e * 8 + i * 2;
-                  const float d0 = bf16_lo_f(dh[i]), d1 = bf16_hi_f(dh[i]);
-                  float f0, f1, g0, g1;
-                  act_grad<ACT, true>(fa[j], f0, g0);
-                  act_grad<ACT, true>(fa[j + 1], f1, g1);
-                  oa[i] = pack_bf16(d0 * fu[j] * g0, d1 * fu[j + 1] * g1);
-                  ou[i] = pack_bf16(d0 * f0, d1 * f1);
+                  const float2 dv = make_float2(bf16_lo_f(dh[i]), bf16_hi_f(dh[i]));
+                  float2 f, df;
+                  act_grad2<ACT>(make_float2(fa[j], fa[j + 1]), f, df);
+                  const float2 da = mul2(mul2(dv, make_float2(fu[j], fu[j + 1])), df), du = mul2(dv, f);
+                  oa[i] = pack_bf16(da.x, da.y);
+                  gu[c * 16 + e * 4 + i] = pack_bf16(du.x, du.y);
                 }
                 *reinterpret_cast<uint4*>(st + at) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
-                *reinterpret_cast<uint4*>(st + kStore + at) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
               }
             }
           } else {
@@ -331,16 +349,13 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
             if (KIND == kGrads) mbar_arrive(dh_empty);
           }
         }
-        if (!cut) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (row0 < a.rows && col < a.cols) {
-              tma_store_3d(KIND == kDw && w.part ? &a.out1 : &a.out0, st, col, row0, 0);
-              if (KIND == kGrads) tma_store_3d(&a.out1, st + kStore, col, row0, 0);
-            }
-            bulk_commit();
-          }
+        if (!cut) leave(KIND == kDw && w.part ? &a.out1 : &a.out0);
+        if constexpr (KIND == kGrads) {
+          left();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4*>(st + sw128(lane, e * 16)) = make_uint4(gu[4 * e], gu[4 * e + 1], gu[4 * e + 2], gu[4 * e + 3]);
+          leave(&a.out1);
         }
       }
     }
