@@ -31,7 +31,8 @@ using namespace ffn;
 enum Kind { kForward, kGrads, kDx, kDw };
 
 constexpr int kWarps = 8;          // warps of results: two for each 32 rows, half the columns each
-constexpr int kThreads = 32 * (kWarps + 2);  // one that copies, one that multiplies
+// one more that copies, one that multiplies, kGrads: one that copies dh
+constexpr int threads_of(int kind) { return 32 * (kWarps + (kind == kGrads ? 3 : 2)); }
 constexpr int kTileBytes = 16384;  // 128 x 64 bf16
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kStore = 4096;       // a warp's staging tile: 32 rows x 64 bf16
@@ -81,7 +82,7 @@ __device__ __forceinline__ int first_step(const Args& a, int split) {
 enum Site { kSiteEmpty = 81, kSiteFull, kSiteAccEmpty, kSiteAccFull, kSiteDhFull, kSiteDhEmpty, kSiteDrain };
 
 template <int KIND, int ACT>
-__global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __grid_constant__ Args a) {
   constexpr int S = stages_of(KIND);
   constexpr bool DUAL = KIND == kForward || KIND == kGrads;
   extern __shared__ uint8_t smraw[];
@@ -136,9 +137,8 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
     if (lane == 0) {
       const uint32_t bars = cluster_map(smem_u32(full), 0);
       uint32_t s = 0, phase = 1;  // (a stage not used yet counts as emptied once)
-      int nt = 0;
       bool ok = true;
-      for (int t = cluster; t < a.tiles && ok; t += clusters, ++nt) {
+      for (int t = cluster; t < a.tiles && ok; t += clusters) {
         const Tile w = tile_of<KIND>(a, t);
         const int row = w.m * 256 + (int)rank * 128, end = first_step<KIND>(a, w.split + 1);
         for (int k = first_step<KIND>(a, w.split); k < end; ++k) {
@@ -167,23 +167,31 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc_kernel(const __grid_consta
           }
           if (++s == S) s = 0, phase ^= 1;
         }
-        if constexpr (KIND == kGrads) {
-          // dh's tile, behind the tile's operands: its room is free once the last tile's results are out
-          if (ok && nt > 0) ok = mbar_wait_abort(dh_empty, (uint32_t)((nt - 1) & 1), abort, hdr, kSiteDhEmpty);
-          if (ok) {
-            mbar_arrive_expect_tx(dh_full, 2 * kTileBytes);
-            tma_load_3d(dht, &a.dh, dh_full, w.n * 128, row, 0);
-            tma_load_3d(dht + kTileBytes, &a.dh, dh_full, w.n * 128 + 64, row, 0);
-          }
-        }
       }
       // the pair's copies have all landed before either CTA lets go of its shared memory
       // (stages before s were last asked for in this turn, the others in the one before, if any)
       if (rank == 0)
         for (uint32_t k = 0; k < S; ++k)
           if (!mbar_wait(&full[k], k < s ? phase ^ 1 : phase)) record_timeout(hdr, kSiteDrain);
-      if (KIND == kGrads && nt > 0 && !mbar_wait(dh_full, (uint32_t)((nt - 1) & 1)))
-        record_timeout(hdr, kSiteDrain);
+    }
+    __syncwarp();
+  } else if (KIND == kGrads && warp == kWarps + 2) {
+    // ------------------------------------------------------------------ dh's tiles
+    // (a thread of its own: its wait for the results to be out holds up no operand)
+    if (lane == 0) {
+      int nt = 0;
+      bool ok = true;
+      for (int t = cluster; t < a.tiles && ok; t += clusters) {
+        const Tile w = tile_of<KIND>(a, t);
+        const int row = w.m * 256 + (int)rank * 128;
+        if (nt > 0) ok = mbar_wait_abort(dh_empty, (uint32_t)((nt - 1) & 1), abort, hdr, kSiteDhEmpty);
+        if (!ok) break;
+        mbar_arrive_expect_tx(dh_full, 2 * kTileBytes);
+        tma_load_3d(dht, &a.dh, dh_full, w.n * 128, row, 0);
+        tma_load_3d(dht + kTileBytes, &a.dh, dh_full, w.n * 128 + 64, row, 0);
+        ++nt;
+      }
+      if (nt > 0 && !mbar_wait(dh_full, (uint32_t)((nt - 1) & 1))) record_timeout(hdr, kSiteDrain);
     }
     __syncwarp();
   } else if (warp == kWarps + 1) {
@@ -394,7 +402,7 @@ cudaError_t launch(Args& a, cudaStream_t st) {
   cudaError_t e = configure(ffn_tc_kernel<KIND, ACT>, smem_of(KIND));
   if (e != cudaSuccess) return e;
   const int pairs = a.tiles < sm_count() / 2 ? a.tiles : sm_count() / 2;
-  e = launch_cluster_pdl(ffn_tc_kernel<KIND, ACT>, dim3(2 * pairs), dim3(kThreads), smem_of(KIND), st, 2, a);
+  e = launch_cluster_pdl(ffn_tc_kernel<KIND, ACT>, dim3(2 * pairs), dim3(threads_of(KIND)), smem_of(KIND), st, 2, a);
   count_launches(1);
   return e;
 }
