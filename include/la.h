@@ -547,8 +547,9 @@ int la_layer_norm_backward(const void* x, long long x_stride, const signed char*
                            void* dw, void* db, long long rows, int C, float eps, int dtype, void* workspace,
                            size_t workspace_bytes, void* stream);
 
-/* Scratch needed by la_ffn_gate and la_ffn_gate_backward, in bytes. */
-size_t la_ffn_gate_workspace_bytes(int T, int C, int F, int dtype);
+/* Scratch needed by la_ffn_gate (checkpoint: whether it writes one; where it needs 0 it takes
+ * nullptr) and by la_ffn_gate_backward, in bytes. */
+size_t la_ffn_gate_workspace_bytes(int T, int C, int F, int checkpoint, int dtype);
 size_t la_ffn_gate_backward_workspace_bytes(int T, int C, int F, int dtype);
 
 /*

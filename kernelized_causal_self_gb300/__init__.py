@@ -92,7 +92,7 @@ _SIGNATURES = {
     "la_layer_norm_workspace_bytes": (_c_size, [_c_ll, _c_int]),
     "la_layer_norm_backward": (_c_int, [_vp, _c_ll] + [_vp] * 4 + [_c_ll, _vp, _c_ll, _vp, _vp, _c_ll,
                                         _c_int, _c_float, _c_int, _vp, _c_size, _vp]),
-    "la_ffn_gate_workspace_bytes": (_c_size, [_c_int] * 4),
+    "la_ffn_gate_workspace_bytes": (_c_size, [_c_int] * 5),
     "la_ffn_gate_backward_workspace_bytes": (_c_size, [_c_int] * 4),
     "la_ffn_gate": (_c_int, [_vp, _c_ll, _vp, _vp, _vp, _c_ll, _vp, _vp] + [_c_int] * 5
                     + [_vp, _c_size, _vp]),
@@ -1107,6 +1107,9 @@ def la_norm_gate_backward(x, z, w, dy, eps=1e-6, dx=None, dz=None, dw=None, work
 
 
 # ------------------------- layer norm, gated projections, activations in 8 bits
+#
+# (These are called for single tokens, where a call's checks cost as much as its kernel: whole
+# comparisons first, and what is wrong is looked for only where one fails.)
 
 _ACTIVATIONS = {"silu": LA_SILU, "gelu": LA_GELU, "gelu_tanh": LA_GELU_TANH}
 
@@ -1114,10 +1117,13 @@ _ACTIVATIONS = {"silu": LA_SILU, "gelu": LA_GELU, "gelu_tanh": LA_GELU_TANH}
 def _token_rows(fn, name, t):
     """(rows, distance from row to row in elements) of t [..., C], its leading dimensions taken as
     one; rows lie evenly apart and do not overlap."""
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
+    if not shape:
+        raise ValueError(f"{fn}: {name} must have at least 1 dimension")
     C = shape[-1]
     if t.is_contiguous():
-        return t.numel() // C if C else 0, C
+        return (t.numel() // C if C else 0), C
+    stride = t.stride()
     if stride[-1] != 1 and C > 1:
         raise ValueError(f"{fn}: {name}'s last dimension must be contiguous")
     rows, ld = 1, None
@@ -1129,32 +1135,53 @@ def _token_rows(fn, name, t):
         elif st != ld * rows:
             raise ValueError(f"{fn}: {name}'s rows must lie evenly apart in memory")
         rows *= n
-    if rows == 0:
-        return 0, C
-    if ld is None or rows == 1:
+    if ld is None:
         ld = C
     if ld < C:
         raise ValueError(f"{fn}: rows of {name} overlap in memory")
     return rows, ld
 
 
-def _kept(fn, shape, checkpoint, device=None):
+def _kept(fn, shape, checkpoint):
     """Checks a checkpoint (codes, exps) of values of the given shape."""
     import torch
     if not isinstance(checkpoint, (tuple, list)) or len(checkpoint) != 2:
         raise ValueError(f"{fn}: a checkpoint is a pair (codes, exps)")
     codes, exps = checkpoint
-    _expect(fn, "codes", codes, tuple(shape), torch.int8)
-    _expect(fn, "exps", exps, (*shape[:-1], -(-shape[-1] // 32)), torch.uint8)
-    if device is not None:
-        _need_cuda(codes, exps, device=device)
+    if codes.shape != shape or codes.dtype != torch.int8:
+        _expect(fn, "codes", codes, shape, torch.int8)
+    blocks = (*shape[:-1], -(-shape[-1] // 32))
+    if exps.shape != blocks or exps.dtype != torch.uint8:
+        _expect(fn, "exps", exps, blocks, torch.uint8)
     return codes, exps
 
 
-def _cuda_device(t):
-    if t.get_device() < 0:
+def _on(index, whole, rows=()):
+    """CUDA tensors of device `index`; `whole` ones contiguous."""
+    for t in whole:
+        if t.get_device() != index or not t.is_contiguous():
+            import torch
+            _need_cuda(t, device=torch.device("cuda", max(index, 0)))
+    for t in rows:
+        if t.get_device() != index:
+            import torch
+            _need_rows(t, device=torch.device("cuda", max(index, 0)))
+    if index < 0:
         raise ValueError("tensors must be on a CUDA device")
-    return t.device
+
+
+def _call(fn, index, args):
+    """The library's `fn` on the current stream of device `index`, which is made current."""
+    import torch
+    lib = _lib or load_library()
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
+        st = getattr(lib, fn)(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            st = getattr(lib, fn)(*args, stream)
+    if st:
+        _check(fn, st)
 
 
 def la_checkpoint(x, checkpoint=None):
@@ -1165,25 +1192,17 @@ def la_checkpoint(x, checkpoint=None):
     that holds an infinity or a NaN restores as NaN. checkpoint: a pair to write to."""
     import torch
     fn = "la_checkpoint"
-    dt = _dtype_code(x)
-    if x.dim() < 1:
-        raise ValueError(f"{fn}: x must have at least 1 dimension")
+    dt, shape, index = _dtype_code(x), x.shape, x.get_device()
     rows, ld = _token_rows(fn, "x", x)
-    shape = tuple(x.shape)
-    if checkpoint is not None:
-        _kept(fn, shape, checkpoint)
-    dev = _cuda_device(x)
-    lib = load_library()
     if checkpoint is None:
+        _on(index, ())
+        dev = x.device
         codes = torch.empty(shape, dtype=torch.int8, device=dev)
         exps = torch.empty((*shape[:-1], -(-shape[-1] // 32)), dtype=torch.uint8, device=dev)
     else:
-        codes, exps = _kept(fn, shape, checkpoint, dev)
-    with _on_device(dev):
-        st = lib.la_checkpoint(x.data_ptr(), ld, codes.data_ptr(), exps.data_ptr(), rows, shape[-1], dt,
-                               _stream_ptr(dev))
-    if st:
-        _check(fn, st)
+        codes, exps = _kept(fn, shape, checkpoint)
+        _on(index, (codes, exps))
+    _call(fn, index, (x.data_ptr(), ld, codes.data_ptr(), exps.data_ptr(), rows, shape[-1], dt))
     return codes, exps
 
 
@@ -1192,28 +1211,22 @@ def la_checkpoint_restore(codes, exps, dtype=None, out=None):
     which holds all of them exactly)."""
     import torch
     fn = "la_checkpoint_restore"
-    if codes.dim() < 1:
+    shape, index = codes.shape, codes.get_device()
+    if not shape:
         raise ValueError(f"{fn}: codes must have at least 1 dimension")
-    shape = tuple(codes.shape)
     _kept(fn, shape, (codes, exps))
-    dtype = dtype or (torch.bfloat16 if out is None else out.dtype)
-    if out is not None:
-        _expect(fn, "out", out, shape, dtype)
-        _token_rows(fn, "out", out)
-    elif dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
-    dev = _cuda_device(codes)
-    _need_cuda(codes, exps)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
-    _need_rows(out, device=dev)
+        dtype = dtype or torch.bfloat16
+        if dtype is not torch.float32 and dtype is not torch.bfloat16:
+            raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+        _on(index, (codes, exps))
+        out = torch.empty(shape, dtype=dtype, device=codes.device)
+    else:
+        _expect(fn, "out", out, shape, dtype or out.dtype)
+        _token_rows(fn, "out", out)
+        _on(index, (codes, exps), (out,))
     rows, ld = _token_rows(fn, "out", out)
-    lib = load_library()
-    with _on_device(dev):
-        st = lib.la_checkpoint_restore(codes.data_ptr(), exps.data_ptr(), out.data_ptr(), ld, rows,
-                                       shape[-1], _dtype_code(out), _stream_ptr(dev))
-    if st:
-        _check(fn, st)
+    _call(fn, index, (codes.data_ptr(), exps.data_ptr(), out.data_ptr(), ld, rows, shape[-1], _dtype_code(out)))
     return out
 
 
@@ -1228,32 +1241,30 @@ def la_layer_norm(x, w, b=None, eps=1e-5, out=None, checkpoint=None):
     (codes, exps), as la_checkpoint makes it, that receives x in 8 bits on the way."""
     import torch
     fn = "la_layer_norm"
-    dt, shape, dtype = _dtype_code(x), tuple(x.shape), x.dtype
-    if len(shape) < 1:
-        raise ValueError(f"{fn}: x must have at least 1 dimension")
-    C = shape[-1]
-    for name, t in (("w", w), ("b", b)):
-        if t is not None:
-            _expect(fn, name, t, (C,), dtype)
+    dt, shape, dtype, index = _dtype_code(x), x.shape, x.dtype, x.get_device()
     rows, ld = _token_rows(fn, "x", x)
-    if out is not None:
+    width = shape[-1:]
+    if w.shape != width or w.dtype != dtype:
+        _expect(fn, "w", w, width, dtype)
+    whole = (w,)
+    if b is not None:
+        if b.shape != width or b.dtype != dtype:
+            _expect(fn, "b", b, width, dtype)
+        whole = (w, b)
+    codes = exps = None
+    if checkpoint is not None:
+        codes, exps = _kept(fn, shape, checkpoint)
+        whole = (*whole, codes, exps)
+    if out is None:
+        _on(index, whole)
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+        old = shape[-1]
+    else:
         _expect(fn, "out", out, shape, dtype)
         old = _token_rows(fn, "out", out)[1]
-    if checkpoint is not None:
-        _kept(fn, shape, checkpoint)
-    dev = _cuda_device(x)
-    _need_cuda(w, *([] if b is None else [b]), device=dev)
-    codes, exps = (None, None) if checkpoint is None else _kept(fn, shape, checkpoint, dev)
-    if out is None:
-        out, old = torch.empty(shape, dtype=dtype, device=dev), C
-    else:
-        _need_rows(out, device=dev)
-    lib = load_library()
-    with _on_device(dev):
-        st = lib.la_layer_norm(x.data_ptr(), ld, w.data_ptr(), _ptr(b), out.data_ptr(), old, _ptr(codes),
-                               _ptr(exps), rows, C, float(eps), dt, _stream_ptr(dev))
-    if st:
-        _check(fn, st)
+        _on(index, whole, (out,))
+    _call(fn, index, (x.data_ptr(), ld, w.data_ptr(), _ptr(b), out.data_ptr(), old, _ptr(codes), _ptr(exps), rows,
+                      shape[-1], eps, dt))
     return out
 
 
@@ -1263,44 +1274,43 @@ def la_layer_norm_backward(x, w, dy, eps=1e-5, dx=None, dw=None, db=None, worksp
     x: the norm's input [..., C], or a checkpoint (codes, exps) of it. dx may be x or dy."""
     import torch
     fn = "la_layer_norm_backward"
-    dt, shape, dtype = _dtype_code(dy), tuple(dy.shape), dy.dtype
-    if len(shape) < 1:
-        raise ValueError(f"{fn}: dy must have at least 1 dimension")
-    C = shape[-1]
-    _expect(fn, "w", w, (C,), dtype)
-    kept = isinstance(x, (tuple, list))
-    if kept:
-        _kept(fn, shape, x)
-        ld = 0
-    else:
-        _expect(fn, "x", x, shape, dtype)
-        ld = _token_rows(fn, "x", x)[1]
+    dt, shape, dtype, index = _dtype_code(dy), dy.shape, dy.dtype, dy.get_device()
     rows, dyld = _token_rows(fn, "dy", dy)
-    for name, t, like in (("dx", dx, shape), ("dw", dw, (C,)), ("db", db, (C,))):
+    C = shape[-1]
+    if w.shape != (C,) or w.dtype != dtype:
+        _expect(fn, "w", w, (C,), dtype)
+    whole, strided = [w], []
+    if isinstance(x, (tuple, list)):
+        codes, exps = _kept(fn, shape, x)
+        whole += (codes, exps)
+        xp, ld, cp, ep = 0, 0, codes.data_ptr(), exps.data_ptr()
+    else:
+        if x.shape != shape or x.dtype != dtype:
+            _expect(fn, "x", x, shape, dtype)
+        strided.append(x)
+        xp, ld, cp, ep = x.data_ptr(), _token_rows(fn, "x", x)[1], 0, 0
+    dxld = C
+    if dx is not None:
+        _expect(fn, "dx", dx, shape, dtype)
+        dxld = _token_rows(fn, "dx", dx)[1]
+        strided.append(dx)
+    for name, t in (("dw", dw), ("db", db)):
         if t is not None:
-            _expect(fn, name, t, like, dtype)
-    dxld = C if dx is None else _token_rows(fn, "dx", dx)[1]
-    dev = _cuda_device(dy)
-    _need_cuda(w, *[t for t in (dw, db) if t is not None], device=dev)
-    _need_rows(*[t for t in (None if kept else x, dx) if t is not None], device=dev)
-    codes, exps = _kept(fn, shape, x, dev) if kept else (None, None)
-    lib = load_library()
-    dx = torch.empty(shape, dtype=dtype, device=dev) if dx is None else dx
+            _expect(fn, name, t, (C,), dtype)
+            whole.append(t)
+    _on(index, whole, strided)
+    if dx is None:
+        dx = torch.empty(shape, dtype=dtype, device=dy.device)
     dw = torch.empty_like(w) if dw is None else dw
     db = torch.empty_like(w) if db is None else db
     ws, nbytes = _scratch(dy, _bytes("la_layer_norm_workspace_bytes", rows, C), workspace)
-    with _on_device(dev):
-        st = lib.la_layer_norm_backward(0 if kept else x.data_ptr(), ld, _ptr(codes), _ptr(exps),
-                                        w.data_ptr(), dy.data_ptr(), dyld, dx.data_ptr(), dxld,
-                                        dw.data_ptr(), db.data_ptr(), rows, C, float(eps), dt,
-                                        _ptr(ws), nbytes, _stream_ptr(dev))
-    if st:
-        _check(fn, st)
+    _call(fn, index, (xp, ld, cp, ep, w.data_ptr(), dy.data_ptr(), dyld, dx.data_ptr(), dxld, dw.data_ptr(),
+                      db.data_ptr(), rows, C, eps, dt, _ptr(ws), nbytes))
     return dx, dw, db
 
 
-def la_ffn_gate_workspace_bytes(T, C, F, dtype=LA_BF16):
-    return load_library().la_ffn_gate_workspace_bytes(T, C, F, dtype)
+def la_ffn_gate_workspace_bytes(T, C, F, checkpoint=False, dtype=LA_BF16):
+    return load_library().la_ffn_gate_workspace_bytes(T, C, F, int(bool(checkpoint)), dtype)
 
 
 def la_ffn_gate_backward_workspace_bytes(T, C, F, dtype=LA_BF16):
@@ -1308,15 +1318,20 @@ def la_ffn_gate_backward_workspace_bytes(T, C, F, dtype=LA_BF16):
 
 
 def _ffn_checks(fn, x, wg, wu, activation):
-    if activation not in _ACTIVATIONS:
+    """(rows, their distance, C, F, dtype code, activation code)."""
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"{fn}: activation must be one of {', '.join(_ACTIVATIONS)}")
-    dt = _dtype_code(x)
-    if x.dim() < 1 or wg.dim() != 2:
+    dt, dtype, shape = _dtype_code(x), x.dtype, wg.shape
+    rows, ld = _token_rows(fn, "x", x)
+    if len(shape) != 2:
         raise ValueError(f"{fn}: x must be [..., C] and wg [F, C]")
-    F, C = wg.shape
-    _expect(fn, "wg", wg, (F, x.shape[-1]), x.dtype)
-    _expect(fn, "wu", wu, (F, C), x.dtype)
-    return C, F, dt, _ACTIVATIONS[activation]
+    F, C = shape
+    if C != x.shape[-1] or wg.dtype != dtype:
+        _expect(fn, "wg", wg, (F, x.shape[-1]), dtype)
+    if wu.shape != shape or wu.dtype != dtype:
+        _expect(fn, "wu", wu, shape, dtype)
+    return rows, ld, C, F, dt, act
 
 
 def la_ffn_gate(x, wg, wu, activation="silu", out=None, checkpoint=None, workspace=None):
@@ -1328,29 +1343,23 @@ def la_ffn_gate(x, wg, wu, activation="silu", out=None, checkpoint=None, workspa
     Rows of x and out may be strided evenly."""
     import torch
     fn = "la_ffn_gate"
-    C, F, dt, act = _ffn_checks(fn, x, wg, wu, activation)
-    lead, dtype = tuple(x.shape[:-1]), x.dtype
-    rows, ld = _token_rows(fn, "x", x)
-    if out is not None:
-        _expect(fn, "out", out, (*lead, F), dtype)
-        old = _token_rows(fn, "out", out)[1]
+    rows, ld, C, F, dt, act = _ffn_checks(fn, x, wg, wu, activation)
+    index, shape = x.get_device(), (*x.shape[:-1], F)
+    whole, cp, ep, kept = (wg, wu), 0, 0, 0
     if checkpoint is not None:
-        _kept(fn, (*lead, 2, F), checkpoint)
-    dev = _cuda_device(x)
-    _need_cuda(wg, wu, device=dev)
-    codes, exps = (None, None) if checkpoint is None else _kept(fn, (*lead, 2, F), checkpoint, dev)
+        codes, exps = _kept(fn, (*shape[:-1], 2, F), checkpoint)
+        whole, cp, ep, kept = (wg, wu, codes, exps), codes.data_ptr(), exps.data_ptr(), 1
     if out is None:
-        out, old = torch.empty((*lead, F), dtype=dtype, device=dev), F
+        _on(index, whole)
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        old = F
     else:
-        _need_rows(out, device=dev)
-    lib = load_library()
-    ws, nbytes = _scratch(x, _bytes("la_ffn_gate_workspace_bytes", rows, C, F, dt), workspace)
-    with _on_device(dev):
-        st = lib.la_ffn_gate(x.data_ptr(), ld, wg.data_ptr(), wu.data_ptr(), out.data_ptr(), old,
-                             _ptr(codes), _ptr(exps), rows, C, F, act, dt, _ptr(ws), nbytes,
-                             _stream_ptr(dev))
-    if st:
-        _check(fn, st)
+        _expect(fn, "out", out, shape, x.dtype)
+        old = _token_rows(fn, "out", out)[1]
+        _on(index, whole, (out,))
+    ws, nbytes = _scratch(x, _bytes("la_ffn_gate_workspace_bytes", rows, C, F, kept, dt), workspace)
+    _call(fn, index, (x.data_ptr(), ld, wg.data_ptr(), wu.data_ptr(), out.data_ptr(), old, cp, ep, rows, C, F, act,
+                      dt, _ptr(ws), nbytes))
     return out
 
 
@@ -1362,32 +1371,31 @@ def la_ffn_gate_backward(x, wg, wu, dh, activation="silu", checkpoint=None, dx=N
     of being computed again. Rows of x, dh and dx may be strided evenly."""
     import torch
     fn = "la_ffn_gate_backward"
-    C, F, dt, act = _ffn_checks(fn, x, wg, wu, activation)
-    shape, dtype = tuple(x.shape), x.dtype
-    lead = shape[:-1]
-    _expect(fn, "dh", dh, (*lead, F), dtype)
-    rows, ld = _token_rows(fn, "x", x)
+    rows, ld, C, F, dt, act = _ffn_checks(fn, x, wg, wu, activation)
+    index, dtype, shape = x.get_device(), x.dtype, x.shape
+    hidden = (*shape[:-1], F)
+    if dh.shape != hidden or dh.dtype != dtype:
+        _expect(fn, "dh", dh, hidden, dtype)
     dhld = _token_rows(fn, "dh", dh)[1]
-    for name, t, like in (("dx", dx, shape), ("dwg", dwg, (F, C)), ("dwu", dwu, (F, C))):
+    whole, strided, dxld, cp, ep = [wg, wu], [dh], C, 0, 0
+    if dx is not None:
+        _expect(fn, "dx", dx, shape, dtype)
+        dxld = _token_rows(fn, "dx", dx)[1]
+        strided.append(dx)
+    for name, t in (("dwg", dwg), ("dwu", dwu)):
         if t is not None:
-            _expect(fn, name, t, like, dtype)
-    dxld = C if dx is None else _token_rows(fn, "dx", dx)[1]
+            _expect(fn, name, t, (F, C), dtype)
+            whole.append(t)
     if checkpoint is not None:
-        _kept(fn, (*lead, 2, F), checkpoint)
-    dev = _cuda_device(x)
-    _need_cuda(wg, wu, *[t for t in (dwg, dwu) if t is not None], device=dev)
-    _need_rows(dh, *([] if dx is None else [dx]), device=dev)
-    codes, exps = (None, None) if checkpoint is None else _kept(fn, (*lead, 2, F), checkpoint, dev)
-    lib = load_library()
-    dx = torch.empty(shape, dtype=dtype, device=dev) if dx is None else dx
+        codes, exps = _kept(fn, (*shape[:-1], 2, F), checkpoint)
+        whole += (codes, exps)
+        cp, ep = codes.data_ptr(), exps.data_ptr()
+    _on(index, whole, strided)
+    if dx is None:
+        dx = torch.empty(shape, dtype=dtype, device=x.device)
     dwg = torch.empty_like(wg) if dwg is None else dwg
     dwu = torch.empty_like(wu) if dwu is None else dwu
     ws, nbytes = _scratch(x, _bytes("la_ffn_gate_backward_workspace_bytes", rows, C, F, dt), workspace)
-    with _on_device(dev):
-        st = lib.la_ffn_gate_backward(x.data_ptr(), ld, wg.data_ptr(), wu.data_ptr(), dh.data_ptr(), dhld,
-                                      _ptr(codes), _ptr(exps), dx.data_ptr(), dxld, dwg.data_ptr(),
-                                      dwu.data_ptr(), rows, C, F, act, dt, _ptr(ws), nbytes,
-                                      _stream_ptr(dev))
-    if st:
-        _check(fn, st)
+    _call(fn, index, (x.data_ptr(), ld, wg.data_ptr(), wu.data_ptr(), dh.data_ptr(), dhld, cp, ep, dx.data_ptr(),
+                      dxld, dwg.data_ptr(), dwu.data_ptr(), rows, C, F, act, dt, _ptr(ws), nbytes))
     return dx, dwg, dwu

@@ -75,9 +75,11 @@ int from_cuda(cudaError_t e) { return e == cudaSuccess ? LA_OK : LA_ERR_CUDA; }
 
 cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
-size_t ffn_workspace(int T, int C, int F, int dtype) {
-  (void)T, (void)C, (void)F, (void)dtype;
-  return la::kHeaderBytes;
+bool few(int T, bool kept, int dtype) { return T <= la::ffn_few_tokens(dtype) && !kept; }
+
+// the tensor-core kernels' status header
+size_t ffn_workspace(int T, bool kept, int dtype) {
+  return dtype == LA_F32 || few(T, kept, dtype) ? 0 : la::kHeaderBytes;
 }
 
 size_t ffn_backward_workspace(int T, int C, int F, int dtype) {
@@ -190,9 +192,9 @@ int la_layer_norm_backward(const void* x, long long x_stride, const signed char*
   return from_cuda(la::layer_norm_backward(n, workspace, st));
 }
 
-size_t la_ffn_gate_workspace_bytes(int T, int C, int F, int dtype) {
-  if (!ffn_ok(T, C, F, LA_SILU, dtype) || T == 0) return la::kHeaderBytes;
-  return ffn_workspace(T, C, F, dtype);
+size_t la_ffn_gate_workspace_bytes(int T, int C, int F, int checkpoint, int dtype) {
+  if (!ffn_ok(T, C, F, LA_SILU, dtype)) return la::kHeaderBytes;
+  return ffn_workspace(T, checkpoint != 0, dtype);
 }
 
 size_t la_ffn_gate_backward_workspace_bytes(int T, int C, int F, int dtype) {
@@ -212,7 +214,8 @@ int la_ffn_gate(const void* x, long long x_stride, const void* wg, const void* w
   if (!apart({{h, span(T, h_stride, F, dtype)}, {codes, kept * F}, {exps, kept * exps_of(F)}},
              {{x, span(T, x_stride, C, dtype)}, {wg, w}, {wu, w}}))
     return LA_ERR_INVALID_ARG;
-  if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < ffn_workspace(T, C, F, dtype))
+  const size_t need = ffn_workspace(T, codes != nullptr, dtype);
+  if (need > 0 && (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < need))
     return LA_ERR_WORKSPACE;
   la::FfnGate f{};
   f.x = x;
@@ -228,6 +231,7 @@ int la_ffn_gate(const void* x, long long x_stride, const void* wg, const void* w
   f.F = F;
   f.act = act;
   f.dtype = dtype;
+  if (few(T, codes != nullptr, dtype)) return from_cuda(la::ffn_few_forward(f, as_stream(stream)));
   return from_cuda(dtype == LA_F32 ? la::ffn_simt_forward(f, as_stream(stream))
                                    : la::ffn_tc_forward(f, workspace, as_stream(stream)));
 }

@@ -399,7 +399,7 @@ int splits_of(int tiles, int steps, double values) {
 template <int KIND, int ACT>
 cudaError_t launch(Args& a, cudaStream_t st) {
   a.tiles = a.m_tiles * a.n_tiles * a.splits * (KIND == kDw ? 2 : 1);
-  cudaError_t e = configure(ffn_tc_kernel<KIND, ACT>, smem_of(KIND));
+  cudaError_t e = configure_once<ffn_tc_kernel<KIND, ACT>>(smem_of(KIND));
   if (e != cudaSuccess) return e;
   const int pairs = a.tiles < sm_count() / 2 ? a.tiles : sm_count() / 2;
   e = launch_cluster_pdl(ffn_tc_kernel<KIND, ACT>, dim3(2 * pairs), dim3(threads_of(KIND)), smem_of(KIND), st, 2, a);

@@ -99,24 +99,9 @@ __device__ __forceinline__ float chunk_gates(ushort2 raw, GateTables& t) {
   return whole;
 }
 
-// tcx::configure, once per kernel and device (its two calls of the runtime cost as much as a
-// launch). The mask is the library's own state, as its launch count is.
-template <auto KERNEL>
-cudaError_t gated_configure(int smem) {
-  static std::atomic<unsigned long long> done{0};
-  int device = 0;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = device < 64 ? 1ull << device : 0;
-  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  e = tcx::configure(KERNEL, smem);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-  return e;
-}
-
 template <auto KERNEL, typename... Args>
 cudaError_t gated_launch(int smem, dim3 grid, int threads, cudaStream_t st, const Args&... args) {
-  cudaError_t e = gated_configure<KERNEL>(smem);
+  cudaError_t e = tcx::configure_once<KERNEL>(smem);
   if (e != cudaSuccess) return e;
   e = tcx::launch_pdl(KERNEL, grid, dim3(threads), smem, st, args...);
   count_launches(1);

@@ -216,6 +216,9 @@ struct FfnGate {
 size_t ffn_simt_backward_workspace(int T, int C, int F, int dtype);
 cudaError_t ffn_simt_forward(const FfnGate& f, cudaStream_t st);
 cudaError_t ffn_simt_backward(const FfnGate& f, void* ws, cudaStream_t st);
+// up to ffn_few_tokens tokens, without a checkpoint
+int ffn_few_tokens(int dtype);
+cudaError_t ffn_few_forward(const FfnGate& f, cudaStream_t st);
 // bf16 on tensor cores; the workspace's status header is used (and cleared)
 size_t ffn_tc_backward_workspace(int T, int C, int F);
 cudaError_t ffn_tc_forward(const FfnGate& f, void* ws, cudaStream_t st);
