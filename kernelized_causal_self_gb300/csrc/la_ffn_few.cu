@@ -1,13 +1,14 @@
 // The gated projections of a few tokens (serving: one of each stream), h = act(x wg^T) (x wu^T).
 // Bound by the weights' bytes, which are read once: a CTA takes some rows f of wg and the same of
-// wu, its four warps share their elements, and the sums are joined in shared memory in order, so
+// wu, its eight warps share their elements, and the sums are joined in shared memory in order, so
 // that a and u meet in one thread.
 //
 // bf16: 8 rows of wg and 8 of wu are the 16 rows of mma.sync's m16n8k16 A, 8 tokens its columns.
 // The order of the terms of a sum is free, so a lane loads 16 neighbouring bytes of its two rows
 // and takes them as the terms of two products, and the same 16 bytes of its token's x: no
 // shared memory, no transposition, every byte of a 64-byte piece of a row used at once.
-//   T 1, C 2048, F 5632: 46 MB of weights in 8.1 us (5.7 TB/s).
+// Measured, T 1 in bf16: C 4096, F 11008 29.9 us (180 MB, 6.0 TB/s), C 2048, F 5632 10.1 us (46 MB;
+// four warps with twice the loads in flight 12.8, sixteen 13.9), C 512, F 1408 2.2 us.
 // float32: 2 rows of each matrix and 8 tokens are 32 sums a lane, which the warp's 32 lanes add up
 // in 31 exchanges, each lane ending with one of them.
 #include "la_ffn.cuh"
@@ -20,7 +21,7 @@ namespace {
 using namespace tcx;
 using namespace ffn;
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
 
 struct Args {
   const void *x, *wg, *wu;
@@ -165,17 +166,18 @@ template <int ACT>
 cudaError_t launch(const Args& a, int dtype, cudaStream_t st) {
   const dim3 block(32 * kWarps), grid(dtype == LA_F32 ? a.F / 2 : a.F / 8);
   const cudaError_t e = dtype == LA_F32 ? launch_pdl(ffn_few_f32_kernel<ACT>, grid, block, 0, st, a)
-                        : a.T <= 8      ? launch_pdl(ffn_few_kernel<ACT, 1, 8>, grid, block, 0, st, a)
-                        : a.T <= 16     ? launch_pdl(ffn_few_kernel<ACT, 2, 8>, grid, block, 0, st, a)
-                        : a.T <= 32     ? launch_pdl(ffn_few_kernel<ACT, 4, 4>, grid, block, 0, st, a)
-                                        : launch_pdl(ffn_few_kernel<ACT, 8, 4>, grid, block, 0, st, a);
+                        : a.T <= 8      ? launch_pdl(ffn_few_kernel<ACT, 1, 4>, grid, block, 0, st, a)
+                        : a.T <= 16     ? launch_pdl(ffn_few_kernel<ACT, 2, 4>, grid, block, 0, st, a)
+                                        : launch_pdl(ffn_few_kernel<ACT, 4, 4>, grid, block, 0, st, a);
   count_launches(1);
   return e;
 }
 
 }  // namespace
 
-int ffn_few_tokens(int dtype) { return dtype == LA_F32 ? 8 : 64; }
+// bf16: 32 tokens take 15.7 us at C 2048, F 5632 here and 16.0 in tiles of 256 tokens, 64 tokens 38.
+// float32: 8 take 27 us, 9 take 174 in tiles of 64.
+int ffn_few_tokens(int dtype) { return dtype == LA_F32 ? 8 : 32; }
 
 cudaError_t ffn_few_forward(const FfnGate& f, cudaStream_t st) {
   Args a;

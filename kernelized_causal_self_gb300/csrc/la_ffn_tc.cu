@@ -43,10 +43,10 @@ constexpr int smem_of(int kind) {
 
 struct Args {
   CUtensorMap a, b0, b1;    // operands (b0, b1: wg and wu; kDw: b0 = x)
-  CUtensorMap out0, out1;   // h; da, du; dx; dwg, dwu
+  CUtensorMap out0, out1;   // h; da, du; dx; dwg, dwu; out0 if the sum is cut: its parts in
+                            // float32, [dw: 2][splits][rows][C]
   CUtensorMap dh;           // kGrads
   WorkspaceHeader* hdr;
-  float* partial;           // kDx, kDw: [dw: 2][splits][rows][C] if the sum is cut
   signed char* codes;       // kForward: a checkpoint of a, u
   unsigned char* exps;
   int rows, cols;           // of the result (kForward, kGrads: T, F)
@@ -121,6 +121,14 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
   if (warp == 0) {
     tmem_alloc_pair(tslot, 512);
     tmem_relinquish_pair();
+  }
+  if (warp == kWarps && lane == 0) {
+    prefetch_tensormap(&a.a);
+    prefetch_tensormap(&a.b0);
+    prefetch_tensormap(&a.out0);
+    if (KIND != kDw) prefetch_tensormap(&a.b1);
+    if (KIND == kGrads) prefetch_tensormap(&a.dh);
+    if (KIND == kGrads || KIND == kDw) prefetch_tensormap(&a.out1);
   }
   fence_before_sync();
   __syncthreads();
@@ -257,11 +265,11 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
         const bool cut = !DUAL && a.splits > 1;
         uint8_t* st = mine;
         uint32_t gu[KIND == kGrads ? 32 : 1];  // du, which follows da through the staging tile
-        auto leave = [&](const CUtensorMap* to) {
+        auto leave = [&](const CUtensorMap* to, int from, int mat) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (row0 < a.rows && col < a.cols) tma_store_3d(to, st, col, row0, 0);
+            if (row0 < a.rows && from < a.cols) tma_store_3d(to, st, from, row0, mat);
             bulk_commit();
           }
         };
@@ -332,13 +340,12 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
             }
           } else {
             tmem_ld32(d + g * 64 + c * 32, p);
-            if (cut) {
-              const size_t r = (size_t)(KIND == kDw ? w.part * a.splits + w.split : w.split) * a.rows + row;
-              float* to = a.partial + r * a.cols + col + c * 32;
+            if (cut) {  // 32 float32 are a staging row
+              left();
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (row < a.rows && col + c * 32 + j * 4 < a.cols)
-                  *reinterpret_cast<uint4*>(to + j * 4) = make_uint4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<uint4*>(st + sw128(lane, e * 16)) = make_uint4(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3]);
+              leave(&a.out0, col + c * 32, KIND == kDw ? w.part * a.splits + w.split : w.split);
             } else {
               const float* f = reinterpret_cast<const float*>(p);
 #pragma unroll
@@ -357,13 +364,13 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
             if (KIND == kGrads) mbar_arrive(dh_empty);
           }
         }
-        if (!cut) leave(KIND == kDw && w.part ? &a.out1 : &a.out0);
+        if (!cut) leave(KIND == kDw && w.part ? &a.out1 : &a.out0, col, 0);
         if constexpr (KIND == kGrads) {
           left();
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             *reinterpret_cast<uint4*>(st + sw128(lane, e * 16)) = make_uint4(gu[4 * e], gu[4 * e + 1], gu[4 * e + 2], gu[4 * e + 3]);
-          leave(&a.out1);
+          leave(&a.out1, col, 0);
         }
       }
     }
@@ -418,6 +425,11 @@ cudaError_t launch_act(Args& a, int act, cudaStream_t st) {
 bool rows_map(CUtensorMap* m, const void* p, long long cols, long long rows, long long ld, int b1, int mats = 1) {
   // (a single row's distance is of no use, but has to be one that the map takes)
   return make_tmap_bf16_strided(m, p, cols, rows, mats, rows > 1 ? ld : cols, (size_t)rows * cols, 64, b1, 1);
+}
+
+// Parts of a cut sum, [parts][rows][C] in float32
+bool parts_map(CUtensorMap* m, const float* p, int C, int rows, int parts) {
+  return make_tmap_f32_3d(m, p, C, rows, parts, 32, 32, 1);
 }
 
 struct Plan {
@@ -489,12 +501,13 @@ cudaError_t ffn_tc_backward(const FfnGate& f, void* ws, cudaStream_t st) {
   }
   if (e != cudaSuccess) return e;
 
-  a.partial = partial;
   a.cols = f.C;
   a.n_tiles = ceil_div(f.C, 256);
   // dx = [da | du] [wg; wu]
   if (!rows_map(&a.a, da, f.F, f.T, f.F, 128, 2) || !rows_map(&a.b0, f.wg, f.C, f.F, f.C, 64) ||
-      !rows_map(&a.b1, f.wu, f.C, f.F, f.C, 64) || !rows_map(&a.out0, f.dx, f.C, f.T, f.dx_stride, 32))
+      !rows_map(&a.b1, f.wu, f.C, f.F, f.C, 64) ||
+      !(plan.dx_splits > 1 ? parts_map(&a.out0, partial, f.C, f.T, plan.dx_splits)
+                           : rows_map(&a.out0, f.dx, f.C, f.T, f.dx_stride, 32)))
     return cudaErrorInvalidValue;
   a.rows = f.T;
   a.m_tiles = ceil_div(f.T, 256);
@@ -509,7 +522,9 @@ cudaError_t ffn_tc_backward(const FfnGate& f, void* ws, cudaStream_t st) {
 
   // dwg, dwu = [da; du]^T x
   if (!rows_map(&a.a, da, f.F, f.T, f.F, 64, 2) || !rows_map(&a.b0, f.x, f.C, f.T, f.x_stride, 64) ||
-      !rows_map(&a.out0, f.dwg, f.C, f.F, f.C, 32) || !rows_map(&a.out1, f.dwu, f.C, f.F, f.C, 32))
+      !(plan.dw_splits > 1 ? parts_map(&a.out0, partial, f.C, f.F, 2 * plan.dw_splits)
+                           : rows_map(&a.out0, f.dwg, f.C, f.F, f.C, 32)) ||
+      !rows_map(&a.out1, f.dwu, f.C, f.F, f.C, 32))
     return cudaErrorInvalidValue;
   a.rows = f.F;
   a.m_tiles = ceil_div(f.F, 256);
