@@ -149,6 +149,11 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
       for (int t = cluster; t < a.tiles && ok; t += clusters) {
         const Tile w = tile_of<KIND>(a, t);
         const int row = w.m * 256 + (int)rank * 128, end = first_step<KIND>(a, w.split + 1);
+        if (DUAL && t + clusters < a.tiles) {
+          // x of the next tile into L2, a tile's time ahead: the tiles of the same rows share its steps
+          const Tile v = tile_of<KIND>(a, t + clusters);
+          for (int k = v.n; k < a.steps; k += a.n_tiles) tma_prefetch_3d(&a.a, k * 64, v.m * 256 + (int)rank * 128, 0);
+        }
         for (int k = first_step<KIND>(a, w.split); k < end; ++k) {
           if (!mbar_wait_abort(&empty[s], phase, abort, hdr, kSiteEmpty)) {
             ok = false;
@@ -176,11 +181,13 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
           if (++s == S) s = 0, phase ^= 1;
         }
       }
-      // the pair's copies have all landed before either CTA lets go of its shared memory
-      // (stages before s were last asked for in this turn, the others in the one before, if any)
-      if (rank == 0)
-        for (uint32_t k = 0; k < S; ++k)
-          if (!mbar_wait(&full[k], k < s ? phase ^ 1 : phase)) record_timeout(hdr, kSiteDrain);
+      // A CTA lets go of its shared memory once its last stages are multiplied and every commit to it has
+      // come in; if a wait ran out, once the pair's copies have landed. (Stages before s were used
+      // in this turn, the others in the one before.)
+      for (uint32_t k = 0; k < S; ++k) {
+        const uint32_t turn = k < s ? phase ^ 1 : phase;
+        if (ok ? !mbar_wait(&empty[k], turn) : rank == 0 && !mbar_wait(&full[k], turn)) record_timeout(hdr, kSiteDrain);
+      }
     }
     __syncwarp();
   } else if (KIND == kGrads && warp == kWarps + 2) {
@@ -389,15 +396,15 @@ constexpr int kPairs = 76;  // of the 152 SMs
 int ceil_div(long long a, int b) { return (int)((a + b - 1) / b); }
 
 // Parts of a sum of `steps` steps of 64: the ones with the least time by this count, in SM
-// clocks of a pair: 512 a step, and behind a tile's last step about 3000 until its results
+// clocks of a pair: 700 a step, and behind a tile's last step about 3000 until its results
 // are out; a part's results are 8 bytes a value more to move (written and read again, at about
-// 3500 bytes a clock over all SMs).
+// 3500 bytes a clock over all SMs), by one more launch.
 int splits_of(int tiles, int steps, double values) {
   int best = 1;
   double least = 0;
   for (int s = 1; s <= 16 && s <= steps; ++s) {
     const int waves = ceil_div((long long)tiles * s, kPairs);
-    const double t = (double)waves * ceil_div(steps, s) * 512 + 3000 + (s > 1 ? 4000 + s * values * 8 / 3500 : 0);
+    const double t = (double)waves * ceil_div(steps, s) * 700 + 3000 + (s > 1 ? 4000 + s * values * 8 / 3500 : 0);
     if (s == 1 || t < least) best = s, least = t;
   }
   return best;

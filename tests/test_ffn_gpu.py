@@ -304,7 +304,8 @@ def _ffn_inputs(T, C, F, dtype, seed=1):
 
 FFN_SIZES = [(1, 8, 8), (1, 64, 128), (1, 2048, 1032), (2, 72, 40), (5, 136, 264), (7, 1000, 24), (8, 256, 680), (9, 520, 72), (16, 64, 64), (17, 200, 96), (33, 64, 1032),
              (64, 512, 256), (65, 128, 136), (127, 64, 128), (128, 128, 256), (129, 264, 136), (200, 1032, 8),
-             (256, 256, 512), (300, 8, 520), (513, 104, 280), (777, 256, 680)]
+             (256, 256, 512), (300, 8, 520), (513, 104, 280), (777, 256, 680), (1500, 264, 1032),
+             (2100, 136, 520)]
 
 
 @TYPES
