@@ -63,7 +63,7 @@ struct RowSum {
 enum Mode { kForward, kForwardKeep, kBackward, kBackwardKept };
 
 template <typename T, int G, int P, int MODE>
-__global__ void __launch_bounds__(G > 256 ? G : 256)
+__global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 ? 1 : MODE < kBackward ? 3 : 2)
 layer_norm_kernel(const Args a) {
   constexpr int V = 16 / sizeof(T), THREADS = G > 256 ? G : 256, ROWS = THREADS / G;
   constexpr bool BWD = MODE == kBackward || MODE == kBackwardKept;
@@ -83,22 +83,34 @@ layer_norm_kernel(const Args a) {
     if (!live[p]) col[p] = 0;
   }
   tc::pdl_wait();
-  float w[P][V], b[P][V], dw[P][V], db[P][V];
-  auto load = [&](const void* base, long long at, float (&to)[V]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const T*>(base) + at);
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  uint4 wu[P], bu[P];  // as they are stored: converted where they are used
+  // sums of dw and db: in registers, or (rows of 1024 threads, which have 64 each) in shared memory
+  constexpr bool SHARED = BWD && G == 1024;
+  constexpr int PR = SHARED ? 1 : P;
+  float dw[PR][V], db[PR][V];
+  extern __shared__ float4 acc[];  // [dw, db][P][V / 4][G]
+  float4* mine = acc + threadIdx.x;
+  auto piece = [&](const void* base, long long at) {
+    return *reinterpret_cast<const uint4*>(static_cast<const T*>(base) + at);
+  };
+  auto values = [](const uint4& u, float (&to)[V]) {
     const T* t = reinterpret_cast<const T*>(&u);
 #pragma unroll
     for (int i = 0; i < V; ++i) to[i] = to_f32<T>(t[i]);
   };
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    load(a.w, col[p], w[p]);
-#pragma unroll
-    for (int i = 0; i < V; ++i) b[p][i] = dw[p][i] = db[p][i] = 0.f;
-    if (!BWD && a.b != nullptr) load(a.b, col[p], b[p]);
+    wu[p] = live[p] ? piece(a.w, col[p]) : none;
+    bu[p] = !BWD && live[p] && a.b != nullptr ? piece(a.b, col[p]) : none;
   }
+#pragma unroll
+  for (int p = 0; p < PR; ++p)
+#pragma unroll
+    for (int i = 0; i < V; ++i) dw[p][i] = db[p][i] = 0.f;
+  if (SHARED)
+    for (int i = 0; i < 2 * P * (V / 4); ++i) mine[i * G] = make_float4(0.f, 0.f, 0.f, 0.f);
 
-  const uint4 none = make_uint4(0, 0, 0, 0);
   uint4 nx[P], ndy[P];
   Code ncode[P];
   uint32_t ne[P];
@@ -135,15 +147,9 @@ layer_norm_kernel(const Args a) {
       if constexpr (MODE == kBackwardKept) {
         q8::values_of<V>(ncode[p], q8::step_value(ne[p]), x[p]);
       } else {
-        const T* t = reinterpret_cast<const T*>(&nx[p]);
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[p][i] = to_f32<T>(t[i]);
+        values(nx[p], x[p]);
       }
-      if (BWD) {
-        const T* t = reinterpret_cast<const T*>(&ndy[p]);
-#pragma unroll
-        for (int i = 0; i < V; ++i) dy[p][i] = to_f32<T>(t[i]);
-      }
+      if (BWD) values(ndy[p], dy[p]);
     }
     ask(row + step);
     if constexpr (MODE == kForwardKeep) {
@@ -179,26 +185,49 @@ layer_norm_kernel(const Args a) {
     if (!BWD) {
 #pragma unroll
       for (int p = 0; p < P; ++p) {
+        float w[V], b[V];
+        values(wu[p], w);
+        values(bu[p], b);
         uint4 u;
         T* t = reinterpret_cast<T*>(&u);
 #pragma unroll
-        for (int i = 0; i < V; ++i) t[i] = from_f32<T>(fmaf(x[p][i] * r, w[p][i], b[p][i]));
+        for (int i = 0; i < V; ++i) t[i] = from_f32<T>(fmaf(x[p][i] * r, w[i], b[i]));
         if (live[p] && row < a.rows)
           *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * a.out_stride + col[p]) = u;
       }
     } else {
       float m[2] = {0.f, 0.f};
 #pragma unroll
-      for (int p = 0; p < P; ++p)
+      for (int p = 0; p < P; ++p) {
+        float w[V];
+        values(wu[p], w);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           x[p][i] *= r;
-          dw[p][i] = fmaf(dy[p][i], x[p][i], dw[p][i]);
-          db[p][i] += dy[p][i];
-          dy[p][i] *= live[p] ? w[p][i] : 0.f;
+          if constexpr (!SHARED) {
+            dw[p][i] = fmaf(dy[p][i], x[p][i], dw[p][i]);
+            db[p][i] += dy[p][i];
+          }
+        }
+        if constexpr (SHARED) {
+#pragma unroll
+          for (int i = 0; i < V; i += 4) {
+            float4 *tw = mine + (p * (V / 4) + i / 4) * G, *tb = tw + P * (V / 4) * G;
+            float4 sw = *tw, sb = *tb;
+            sw.x = fmaf(dy[p][i], x[p][i], sw.x), sw.y = fmaf(dy[p][i + 1], x[p][i + 1], sw.y);
+            sw.z = fmaf(dy[p][i + 2], x[p][i + 2], sw.z), sw.w = fmaf(dy[p][i + 3], x[p][i + 3], sw.w);
+            sb.x += dy[p][i], sb.y += dy[p][i + 1], sb.z += dy[p][i + 2], sb.w += dy[p][i + 3];
+            *tw = sw;
+            *tb = sb;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          dy[p][i] *= w[i];
           m[0] += dy[p][i];
           m[1] = fmaf(dy[p][i], x[p][i], m[1]);
         }
+      }
       sum2(m);
       const float m0 = m[0] * inv_c, m1 = m[1] * inv_c;
 #pragma unroll
@@ -224,7 +253,7 @@ layer_norm_kernel(const Args a) {
         for (int p = 0; p < P; ++p)
 #pragma unroll
           for (int i = 0; i < V; ++i)
-            sums[group][(p * G + lane) * V + i] = which ? db[p][i] : dw[p][i];
+            sums[group][(p * G + lane) * V + i] = which ? db[p % PR][i] : dw[p % PR][i];
         __syncthreads();
         for (int c = threadIdx.x; c < a.C; c += THREADS) {
           float t = 0.f;
@@ -236,7 +265,16 @@ layer_norm_kernel(const Args a) {
         for (int p = 0; p < P; ++p)
           if (live[p])
 #pragma unroll
-            for (int i = 0; i < V; ++i) to[col[p] + i] = which ? db[p][i] : dw[p][i];
+            for (int i = 0; i < V; i += 4) {
+              float4 v;
+              if constexpr (SHARED) {
+                v = mine[((which * P + p) * (V / 4) + i / 4) * G];
+              } else {
+                const float* s = which ? &db[p][i] : &dw[p][i];
+                v = make_float4(s[0], s[1], s[2], s[3]);
+              }
+              *reinterpret_cast<float4*>(to + col[p] + i) = v;
+            }
       }
     }
   }
@@ -271,7 +309,10 @@ int threads_per_row(int C) {
   return g;
 }
 
-// CTAs: three on each of the 152 SMs, the backward pass two, fewer where rows are few
+// CTAs: twice the three that an SM holds, the backward pass's two (whose sums cost per CTA), fewer
+// where rows are few. 65536 x 512 in bf16: 24.6 us (5.5 TB/s) with three CTAs of 80 registers an SM,
+// 27.5 with four of 64 or two, 27 with two rows asked for ahead, 28 to 34 with none; backward 37.6
+// (5.3 TB/s), 81 with three CTAs an SM.
 int ctas_of(long long rows, int C, bool bwd) {
   const int g = threads_per_row(C), at_once = g < 256 ? 256 / g : 1;
   const long long all = (rows + at_once - 1) / at_once;
@@ -282,8 +323,11 @@ int ctas_of(long long rows, int C, bool bwd) {
 
 template <typename T, int G, int P, int MODE>
 cudaError_t launch_one(const Args& a, int ctas, cudaStream_t st) {
-  const cudaError_t e = tcx::launch_pdl(layer_norm_kernel<T, G, P, MODE>, dim3(ctas),
-                                        dim3(G > 256 ? G : 256), 0, st, a);
+  constexpr int smem = (MODE == kBackward || MODE == kBackwardKept) && G == 1024 ? 2 * P * (16 / sizeof(T) / 4) * G * 16 : 0;
+  cudaError_t e = cudaSuccess;
+  if (smem > 0) e = tcx::configure_once<layer_norm_kernel<T, G, P, MODE>>(smem);
+  if (e != cudaSuccess) return e;
+  e = tcx::launch_pdl(layer_norm_kernel<T, G, P, MODE>, dim3(ctas), dim3(G > 256 ? G : 256), smem, st, a);
   count_launches(1);
   return e;
 }
