@@ -125,13 +125,24 @@ __device__ __forceinline__ void act_grad2(float2 a, float2& f, float2& df) {
   }
 }
 
+// The next of a float32's three bf16 parts, for two neighbours, which keep the rest: its top 16 bits,
+// then what is left rounded, twice (each rest is exact). Cut, not rounded, at first, so that the
+// largest values stay finite.
+__device__ __forceinline__ uint32_t take_part(float& x, float& y, int part) {
+  const uint32_t u = part == 0 ? __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632) : tc::pack_bf16(x, y);
+  x -= tcx::bf16_lo_f(u);
+  y -= tcx::bf16_hi_f(u);
+  return u;
+}
+
 }  // namespace ffn
 
 // out (and out2 with count 2): the sums over `splits` parts of partial [count][splits][rows][C],
 // added in order
 cudaError_t ffn_join(const float* partial, void* out, void* out2, long long out_stride, int rows, int count, int C,
                      int splits, int dtype, cudaStream_t st);
-// dact [2][T][F]: da = dh u act'(a), du = dh act(a), a and u from f's checkpoint
+// dact: da = dh u act'(a), du = dh act(a), a and u from f's checkpoint; in bf16 [2][T][F], in float32
+// as their three bf16 parts, [2][3][T][F]
 cudaError_t ffn_kept_grads(const FfnGate& f, void* dact, cudaStream_t st);
 
 }  // namespace la

@@ -77,13 +77,14 @@ cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 bool few(int T, bool kept, int dtype) { return T <= la::ffn_few_tokens(dtype) && !kept; }
 
-// the tensor-core kernels' status header
-size_t ffn_workspace(int T, bool kept, int dtype) {
-  return dtype == LA_F32 || few(T, kept, dtype) ? 0 : la::kHeaderBytes;
+// (bf16: the tensor-core kernels' status header)
+size_t ffn_workspace(int T, int C, int F, bool kept, int dtype) {
+  if (few(T, kept, dtype)) return 0;
+  return dtype == LA_F32 ? la::ffn_tc32_workspace(T, C, F, false) : la::kHeaderBytes;
 }
 
 size_t ffn_backward_workspace(int T, int C, int F, int dtype) {
-  return dtype == LA_F32 ? la::ffn_simt_backward_workspace(T, C, F, dtype) : la::ffn_tc_backward_workspace(T, C, F);
+  return dtype == LA_F32 ? la::ffn_tc32_workspace(T, C, F, true) : la::ffn_tc_backward_workspace(T, C, F);
 }
 
 }  // namespace
@@ -194,7 +195,7 @@ int la_layer_norm_backward(const void* x, long long x_stride, const signed char*
 
 size_t la_ffn_gate_workspace_bytes(int T, int C, int F, int checkpoint, int dtype) {
   if (!ffn_ok(T, C, F, LA_SILU, dtype)) return la::kHeaderBytes;
-  return ffn_workspace(T, checkpoint != 0, dtype);
+  return ffn_workspace(T, C, F, checkpoint != 0, dtype);
 }
 
 size_t la_ffn_gate_backward_workspace_bytes(int T, int C, int F, int dtype) {
@@ -214,7 +215,7 @@ int la_ffn_gate(const void* x, long long x_stride, const void* wg, const void* w
   if (!apart({{h, span(T, h_stride, F, dtype)}, {codes, kept * F}, {exps, kept * exps_of(F)}},
              {{x, span(T, x_stride, C, dtype)}, {wg, w}, {wu, w}}))
     return LA_ERR_INVALID_ARG;
-  const size_t need = ffn_workspace(T, codes != nullptr, dtype);
+  const size_t need = ffn_workspace(T, C, F, codes != nullptr, dtype);
   if (need > 0 && (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < need))
     return LA_ERR_WORKSPACE;
   la::FfnGate f{};
@@ -232,7 +233,7 @@ int la_ffn_gate(const void* x, long long x_stride, const void* wg, const void* w
   f.act = act;
   f.dtype = dtype;
   if (few(T, codes != nullptr, dtype)) return from_cuda(la::ffn_few_forward(f, as_stream(stream)));
-  return from_cuda(dtype == LA_F32 ? la::ffn_simt_forward(f, as_stream(stream))
+  return from_cuda(dtype == LA_F32 ? la::ffn_tc32_forward(f, workspace, as_stream(stream))
                                    : la::ffn_tc_forward(f, workspace, as_stream(stream)));
 }
 
@@ -275,7 +276,7 @@ int la_ffn_gate_backward(const void* x, long long x_stride, const void* wg, cons
   f.F = F;
   f.act = act;
   f.dtype = dtype;
-  return from_cuda(dtype == LA_F32 ? la::ffn_simt_backward(f, workspace, st) : la::ffn_tc_backward(f, workspace, st));
+  return from_cuda(dtype == LA_F32 ? la::ffn_tc32_backward(f, workspace, st) : la::ffn_tc_backward(f, workspace, st));
 }
 
 }  // extern "C"

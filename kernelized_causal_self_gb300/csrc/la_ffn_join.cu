@@ -1,0 +1,148 @@
+// What the gated projections' backward passes need beside their products: da = dh u act'(a) and
+// du = dh act(a) from a checkpoint of a and u, and the parts of cut sums added in order. Both are
+// bound by memory.
+#include "la_checkpoint.cuh"
+#include "la_ffn.cuh"
+#include "la_internal.h"
+#include "la_tc_common.cuh"
+
+namespace la {
+namespace {
+
+using namespace tcx;
+using namespace ffn;
+
+constexpr int kSms = 152;
+
+// 4 neighbours as float32
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(bf16_lo_f(u.x), bf16_hi_f(u.x), bf16_lo_f(u.y), bf16_hi_f(u.y));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(tc::pack_bf16(v.x, v.y), tc::pack_bf16(v.z, v.w));
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(tc::pack_bf16(v[0], v[1]), tc::pack_bf16(v[2], v[3]),
+                                            tc::pack_bf16(v[4], v[5]), tc::pack_bf16(v[6], v[7]));
+}
+
+// The parts of split sums, added in order: matrix blockIdx.y of [.][splits][rows][C]
+template <typename T>
+__global__ void __launch_bounds__(256) ffn_join_kernel(const float* partial, T* out, T* out2, long long out_stride,
+                                                       int rows, int C, int splits) {
+  const long long n = (long long)rows * C / 4;
+  const float* p = partial + (size_t)blockIdx.y * splits * rows * C;
+  T* to = blockIdx.y ? out2 : out;
+  tc::pdl_wait();
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+    float4 s = load4(p + 4 * i);
+    for (int k = 1; k < splits; ++k) {
+      const float4 v = load4(p + (size_t)k * rows * C + 4 * i);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    const long long row = 4 * i / C;
+    store4(to + row * out_stride + (4 * i - row * C), s);
+  }
+}
+
+// da, du from a checkpoint of a and u: 8 neighbours a thread, all of a block's step. Bound by
+// memory (T 4096, F 5632 in bf16: 186 MB).
+struct Kept {
+  const void* dh;
+  const signed char* codes;
+  const unsigned char* exps;
+  __nv_bfloat16* dact;
+  long long dh_stride;
+  int T, F;
+};
+
+template <typename T, int ACT>
+__global__ void __launch_bounds__(256) ffn_kept_grads_kernel(const Kept a) {
+  const unsigned per = a.F / 8, nb = q8::blocks_of(a.F);
+  const size_t part = (size_t)a.T * a.F;
+  tc::pdl_wait();
+  const unsigned long long at = (unsigned long long)blockIdx.x * 256;  // (one 64-bit division a CTA)
+  const unsigned i = (unsigned)(at % per) + threadIdx.x;
+  const size_t t = at / per + i / per;
+  if (t >= a.T) return;
+  const unsigned f = i % per * 8;
+  const size_t row = 2 * t;
+  const T* dh = static_cast<const T*>(a.dh) + (long long)t * a.dh_stride + f;
+  const uint2 ca = __ldcs(reinterpret_cast<const uint2*>(a.codes + row * a.F + f));
+  const uint2 cu = __ldcs(reinterpret_cast<const uint2*>(a.codes + (row + 1) * a.F + f));
+  const float4 d0 = load4(dh), d1 = load4(dh + 4);
+  float g[8], u[8];
+  q8::values_of<8>(ca, q8::step_value(a.exps[row * nb + f / q8::kBlock]), g);
+  q8::values_of<8>(cu, q8::step_value(a.exps[(row + 1) * nb + f / q8::kBlock]), u);
+  const float dv[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+  float da[8], du[8];
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    float2 fa, df;
+    if constexpr (sizeof(T) == 2) {
+      act_grad2<ACT>(make_float2(g[j], g[j + 1]), fa, df);
+    } else {
+      act_grad<ACT>(g[j], fa.x, df.x);
+      act_grad<ACT>(g[j + 1], fa.y, df.y);
+    }
+    da[j] = dv[j] * u[j] * df.x, da[j + 1] = dv[j + 1] * u[j + 1] * df.y;
+    du[j] = dv[j] * fa.x, du[j + 1] = dv[j + 1] * fa.y;
+  }
+  __nv_bfloat16* to = a.dact + t * a.F + f;
+  if constexpr (sizeof(T) == 2) {
+    store8(to, da);
+    store8(to + part, du);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        float* v = i ? du : da;
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = take_part(v[2 * j], v[2 * j + 1], p);
+        *reinterpret_cast<uint4*>(to + (i * 3 + p) * part) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+  }
+}
+
+template <typename T>
+cudaError_t kept_grads(const Kept& a, int act, cudaStream_t st) {
+  const dim3 grid((unsigned)(((long long)a.T * (a.F / 8) + 255) / 256));  // (T <= 2^24, F <= 2^16: an int)
+  const cudaError_t e =
+      act == kSilu   ? launch_pdl(ffn_kept_grads_kernel<T, kSilu>, grid, dim3(256), 0, st, a)
+      : act == kGelu ? launch_pdl(ffn_kept_grads_kernel<T, kGelu>, grid, dim3(256), 0, st, a)
+                     : launch_pdl(ffn_kept_grads_kernel<T, kGeluTanh>, grid, dim3(256), 0, st, a);
+  count_launches(1);
+  return e;
+}
+
+template <typename T>
+cudaError_t join(const float* partial, void* out, void* out2, long long stride, int rows, int count, int C, int splits,
+                 cudaStream_t st) {
+  const long long n = (long long)rows * C / 4;
+  const int ctas = (int)((n + 255) / 256 < 8 * kSms ? (n + 255) / 256 : 8 * kSms);
+  const cudaError_t e = launch_pdl(ffn_join_kernel<T>, dim3(ctas, count), dim3(256), 0, st, partial,
+                                   static_cast<T*>(out), static_cast<T*>(out2), stride, rows, C, splits);
+  count_launches(1);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t ffn_join(const float* partial, void* out, void* out2, long long out_stride, int rows, int count, int C,
+                     int splits, int dtype, cudaStream_t st) {
+  return dtype == LA_F32 ? join<float>(partial, out, out2, out_stride, rows, count, C, splits, st)
+                         : join<__nv_bfloat16>(partial, out, out2, out_stride, rows, count, C, splits, st);
+}
+
+cudaError_t ffn_kept_grads(const FfnGate& f, void* dact, cudaStream_t st) {
+  const Kept a{f.dh, f.codes, f.exps, static_cast<__nv_bfloat16*>(dact), f.dh_stride, f.T, f.F};
+  return f.dtype == LA_F32 ? kept_grads<float>(a, f.act, st) : kept_grads<__nv_bfloat16>(a, f.act, st);
+}
+
+}  // namespace la

@@ -17,31 +17,22 @@
 // Sums with few tiles are cut along k (float32 parts, added in order by a second kernel).
 #include <cuda_bf16.h>
 
-#include "la_checkpoint.cuh"
-#include "la_ffn.cuh"
-#include "la_internal.h"
-#include "la_tc_common.cuh"
+#include "la_ffn_tc.cuh"
 
 namespace la {
 namespace {
 
-using namespace tcx;
 using namespace ffn;
 
-enum Kind { kForward, kGrads, kDx, kDw };
-
-constexpr int kWarps = 8;          // warps of results: two for each 32 rows, half the columns each
-// one more that copies, one that multiplies, kGrads: one that copies dh
+// one more warp that copies, one that multiplies, kGrads: one that copies dh
 constexpr int threads_of(int kind) { return 32 * (kWarps + (kind == kGrads ? 3 : 2)); }
-constexpr int kTileBytes = 16384;  // 128 x 64 bf16
 constexpr int kStageBytes = 2 * kTileBytes;
-constexpr int kStore = 4096;       // a warp's staging tile: 32 rows x 64 bf16
 constexpr int stages_of(int kind) { return kind == kGrads ? 5 : 6; }
 constexpr int smem_of(int kind) {
   return 1024 + stages_of(kind) * kStageBytes + kWarps * kStore + (kind == kGrads ? 2 * kTileBytes : 0) + 256;
 }
 
-struct Args {
+struct Args : Grid {
   CUtensorMap a, b0, b1;    // operands (b0, b1: wg and wu; kDw: b0 = x)
   CUtensorMap out0, out1;   // h; da, du; dx; dwg, dwu; out0 if the sum is cut: its parts in
                             // float32, [dw: 2][splits][rows][C]
@@ -49,37 +40,8 @@ struct Args {
   WorkspaceHeader* hdr;
   signed char* codes;       // kForward: a checkpoint of a, u
   unsigned char* exps;
-  int rows, cols;           // of the result (kForward, kGrads: T, F)
-  int m_tiles, n_tiles, splits, tiles;
-  int steps, per;           // k steps of 64 in the whole sum; kDx: of one of its two parts
   int clear;                // the call's first kernel clears the status header
 };
-
-struct Tile {
-  int m, n, part, split;  // part: kDw: dwg or dwu
-};
-
-template <int KIND>
-__device__ __forceinline__ Tile tile_of(const Args& a, uint32_t t) {
-  Tile r;
-  const uint32_t row = t / (uint32_t)a.n_tiles, mat = row / (uint32_t)a.m_tiles;
-  r.n = (int)(t - row * (uint32_t)a.n_tiles);
-  r.m = (int)(row - mat * (uint32_t)a.m_tiles);
-  r.part = KIND == kDw ? (int)(mat & 1) : 0;
-  r.split = (int)(KIND == kDw ? mat >> 1 : mat);
-  return r;
-}
-
-// The steps of tile t's sum (the whole one in kForward and kGrads, which are not cut). At most
-// 2^18 steps and 16 parts.
-template <int KIND>
-__device__ __forceinline__ int first_step(const Args& a, int split) {
-  if (KIND == kForward || KIND == kGrads || a.splits == 1) return split ? a.steps : 0;
-  return (int)((uint32_t)(a.steps * split) / (uint32_t)a.splits);
-}
-
-// Wait codes of this file's kernels (la_workspace_wait_site)
-enum Site { kSiteEmpty = 81, kSiteFull, kSiteAccEmpty, kSiteAccFull, kSiteDhFull, kSiteDhEmpty, kSiteDrain };
 
 template <int KIND, int ACT>
 __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __grid_constant__ Args a) {
@@ -391,25 +353,6 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
   if (warp == 0) tmem_dealloc_pair(tbase, 512);
 }
 
-constexpr int kPairs = 76;  // of the 152 SMs
-
-int ceil_div(long long a, int b) { return (int)((a + b - 1) / b); }
-
-// Parts of a sum of `steps` steps of 64: the ones with the least time by this count, in SM
-// clocks of a pair: 700 a step, and behind a tile's last step about 3000 until its results
-// are out; a part's results are 8 bytes a value more to move (written and read again, at about
-// 3500 bytes a clock over all SMs), by one more launch.
-int splits_of(int tiles, int steps, double values) {
-  int best = 1;
-  double least = 0;
-  for (int s = 1; s <= 16 && s <= steps; ++s) {
-    const int waves = ceil_div((long long)tiles * s, kPairs);
-    const double t = (double)waves * ceil_div(steps, s) * 700 + 3000 + (s > 1 ? 4000 + s * values * 8 / 3500 : 0);
-    if (s == 1 || t < least) best = s, least = t;
-  }
-  return best;
-}
-
 template <int KIND, int ACT>
 cudaError_t launch(Args& a, cudaStream_t st) {
   a.tiles = a.m_tiles * a.n_tiles * a.splits * (KIND == kDw ? 2 : 1);
@@ -428,17 +371,6 @@ cudaError_t launch_act(Args& a, int act, cudaStream_t st) {
                         : launch<KIND, kGeluTanh>(a, st);
 }
 
-// rows of `cols` elements `ld` apart, in boxes of b1 rows by 64 columns
-bool rows_map(CUtensorMap* m, const void* p, long long cols, long long rows, long long ld, int b1, int mats = 1) {
-  // (a single row's distance is of no use, but has to be one that the map takes)
-  return make_tmap_bf16_strided(m, p, cols, rows, mats, rows > 1 ? ld : cols, (size_t)rows * cols, 64, b1, 1);
-}
-
-// Parts of a cut sum, [parts][rows][C] in float32
-bool parts_map(CUtensorMap* m, const float* p, int C, int rows, int parts) {
-  return make_tmap_f32_3d(m, p, C, rows, parts, 32, 32, 1);
-}
-
 struct Plan {
   int dx_splits, dw_splits;
   size_t dact, partial;  // bytes
@@ -446,8 +378,8 @@ struct Plan {
 
 Plan plan_of(int T, int C, int F) {
   Plan p;
-  p.dx_splits = splits_of(ceil_div(T, 256) * ceil_div(C, 256), 2 * ceil_div(F, 64), (double)T * C);
-  p.dw_splits = splits_of(2 * ceil_div(F, 256) * ceil_div(C, 256), ceil_div(T, 64), 2.0 * F * C);
+  p.dx_splits = splits_of(ceil_div(T, 256) * ceil_div(C, 256), 2 * ceil_div(F, 64), 700, (double)T * C);
+  p.dw_splits = splits_of(2 * ceil_div(F, 256) * ceil_div(C, 256), ceil_div(T, 64), 700, 2.0 * F * C);
   p.dact = align_up(2 * sizeof(__nv_bfloat16) * (size_t)T * F, 256);
   const size_t x = p.dx_splits > 1 ? (size_t)p.dx_splits * T * C : 0;
   const size_t w = p.dw_splits > 1 ? 2 * (size_t)p.dw_splits * F * C : 0;
@@ -513,7 +445,7 @@ cudaError_t ffn_tc_backward(const FfnGate& f, void* ws, cudaStream_t st) {
   // dx = [da | du] [wg; wu]
   if (!rows_map(&a.a, da, f.F, f.T, f.F, 128, 2) || !rows_map(&a.b0, f.wg, f.C, f.F, f.C, 64) ||
       !rows_map(&a.b1, f.wu, f.C, f.F, f.C, 64) ||
-      !(plan.dx_splits > 1 ? parts_map(&a.out0, partial, f.C, f.T, plan.dx_splits)
+      !(plan.dx_splits > 1 ? rows_map_f32(&a.out0, partial, f.C, f.T, f.C, plan.dx_splits)
                            : rows_map(&a.out0, f.dx, f.C, f.T, f.dx_stride, 32)))
     return cudaErrorInvalidValue;
   a.rows = f.T;
@@ -529,7 +461,7 @@ cudaError_t ffn_tc_backward(const FfnGate& f, void* ws, cudaStream_t st) {
 
   // dwg, dwu = [da; du]^T x
   if (!rows_map(&a.a, da, f.F, f.T, f.F, 64, 2) || !rows_map(&a.b0, f.x, f.C, f.T, f.x_stride, 64) ||
-      !(plan.dw_splits > 1 ? parts_map(&a.out0, partial, f.C, f.F, 2 * plan.dw_splits)
+      !(plan.dw_splits > 1 ? rows_map_f32(&a.out0, partial, f.C, f.F, f.C, 2 * plan.dw_splits)
                            : rows_map(&a.out0, f.dwg, f.C, f.F, f.C, 32)) ||
       !rows_map(&a.out1, f.dwu, f.C, f.F, f.C, 32))
     return cudaErrorInvalidValue;

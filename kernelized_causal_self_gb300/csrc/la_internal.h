@@ -213,9 +213,6 @@ struct FfnGate {
   long long x_stride, h_stride, dh_stride, dx_stride;
   int T, C, F, act, dtype;
 };
-size_t ffn_simt_backward_workspace(int T, int C, int F, int dtype);
-cudaError_t ffn_simt_forward(const FfnGate& f, cudaStream_t st);
-cudaError_t ffn_simt_backward(const FfnGate& f, void* ws, cudaStream_t st);
 // up to ffn_few_tokens tokens, without a checkpoint
 int ffn_few_tokens(int dtype);
 cudaError_t ffn_few_forward(const FfnGate& f, cudaStream_t st);
@@ -223,5 +220,9 @@ cudaError_t ffn_few_forward(const FfnGate& f, cudaStream_t st);
 size_t ffn_tc_backward_workspace(int T, int C, int F);
 cudaError_t ffn_tc_forward(const FfnGate& f, void* ws, cudaStream_t st);
 cudaError_t ffn_tc_backward(const FfnGate& f, void* ws, cudaStream_t st);
+// the same in float32, as three bf16 a value
+size_t ffn_tc32_workspace(int T, int C, int F, bool backward);
+cudaError_t ffn_tc32_forward(const FfnGate& f, void* ws, cudaStream_t st);
+cudaError_t ffn_tc32_backward(const FfnGate& f, void* ws, cudaStream_t st);
 
 }  // namespace la

@@ -448,5 +448,7 @@ bool make_tmap_bf16_strided(CUtensorMap* map, const void* base, uint64_t d0, uin
 // The same over a float32 tensor (the box's inner extent b0 * 4 bytes must be <= 128).
 bool make_tmap_f32_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                       uint32_t b0, uint32_t b1, uint32_t b2);
+bool make_tmap_f32_strided(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                           uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2);
 
 }  // namespace la

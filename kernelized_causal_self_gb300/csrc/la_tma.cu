@@ -52,4 +52,9 @@ bool make_tmap_f32_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t 
   return make_tmap_3d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, d0, d1, d2, d0, d0 * d1, b0, b1, b2);
 }
 
+bool make_tmap_f32_strided(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                           uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2) {
+  return make_tmap_3d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, d0, d1, d2, s1, s2, b0, b1, b2);
+}
+
 }  // namespace la
