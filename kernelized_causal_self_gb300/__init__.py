@@ -144,13 +144,18 @@ def _check(fn, status):
         raise LAError(fn, status)
 
 
+_DTYPE_CODES = {}
+
+
 def _dtype_code(t):
-    import torch
-    if t.dtype == torch.float32:
-        return LA_F32
-    if t.dtype == torch.bfloat16:
-        return LA_BF16
-    raise TypeError(f"unsupported dtype {t.dtype} (float32 or bfloat16)")
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        import torch
+        _DTYPE_CODES.update({torch.float32: LA_F32, torch.bfloat16: LA_BF16})
+        code = _DTYPE_CODES.get(t.dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {t.dtype} (float32 or bfloat16)")
+    return code
 
 
 def _on_device(device):
@@ -1158,28 +1163,27 @@ def _kept(fn, shape, checkpoint):
 
 def _on(index, whole, rows=()):
     """CUDA tensors of device `index`; `whole` ones contiguous."""
+    if index < 0:
+        raise ValueError("tensors must be on a CUDA device")
     for t in whole:
         if t.get_device() != index or not t.is_contiguous():
             import torch
-            _need_cuda(t, device=torch.device("cuda", max(index, 0)))
+            _need_cuda(t, device=torch.device("cuda", index))
     for t in rows:
         if t.get_device() != index:
             import torch
-            _need_rows(t, device=torch.device("cuda", max(index, 0)))
-    if index < 0:
-        raise ValueError("tensors must be on a CUDA device")
+            _need_rows(t, device=torch.device("cuda", index))
 
 
-def _call(fn, index, args):
+def _call(fn, index, *args):
     """The library's `fn` on the current stream of device `index`, which is made current."""
     import torch
-    lib = _lib or load_library()
-    stream = torch._C._cuda_getCurrentRawStream(index)
+    f = getattr(_lib or load_library(), fn)
     if torch._C._cuda_getDevice() == index:
-        st = getattr(lib, fn)(*args, stream)
+        st = f(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
-            st = getattr(lib, fn)(*args, stream)
+            st = f(*args, torch._C._cuda_getCurrentRawStream(index))
     if st:
         _check(fn, st)
 
@@ -1202,7 +1206,7 @@ def la_checkpoint(x, checkpoint=None):
     else:
         codes, exps = _kept(fn, shape, checkpoint)
         _on(index, (codes, exps))
-    _call(fn, index, (x.data_ptr(), ld, codes.data_ptr(), exps.data_ptr(), rows, shape[-1], dt))
+    _call(fn, index, x.data_ptr(), ld, codes.data_ptr(), exps.data_ptr(), rows, shape[-1], dt)
     return codes, exps
 
 
@@ -1226,7 +1230,7 @@ def la_checkpoint_restore(codes, exps, dtype=None, out=None):
         _token_rows(fn, "out", out)
         _on(index, (codes, exps), (out,))
     rows, ld = _token_rows(fn, "out", out)
-    _call(fn, index, (codes.data_ptr(), exps.data_ptr(), out.data_ptr(), ld, rows, shape[-1], _dtype_code(out)))
+    _call(fn, index, codes.data_ptr(), exps.data_ptr(), out.data_ptr(), ld, rows, shape[-1], _dtype_code(out))
     return out
 
 
@@ -1243,28 +1247,24 @@ def la_layer_norm(x, w, b=None, eps=1e-5, out=None, checkpoint=None):
     fn = "la_layer_norm"
     dt, shape, dtype, index = _dtype_code(x), x.shape, x.dtype, x.get_device()
     rows, ld = _token_rows(fn, "x", x)
-    width = shape[-1:]
+    C, width, whole, bp, cp, ep = shape[-1], shape[-1:], (w,), 0, 0, 0
     if w.shape != width or w.dtype != dtype:
         _expect(fn, "w", w, width, dtype)
-    whole = (w,)
     if b is not None:
         if b.shape != width or b.dtype != dtype:
             _expect(fn, "b", b, width, dtype)
-        whole = (w, b)
-    codes = exps = None
+        whole, bp = (w, b), b.data_ptr()
     if checkpoint is not None:
         codes, exps = _kept(fn, shape, checkpoint)
-        whole = (*whole, codes, exps)
+        whole, cp, ep = (*whole, codes, exps), codes.data_ptr(), exps.data_ptr()
     if out is None:
         _on(index, whole)
-        out = torch.empty(shape, dtype=dtype, device=x.device)
-        old = shape[-1]
+        out, old = torch.empty(shape, dtype=dtype, device=x.device), C
     else:
         _expect(fn, "out", out, shape, dtype)
         old = _token_rows(fn, "out", out)[1]
         _on(index, whole, (out,))
-    _call(fn, index, (x.data_ptr(), ld, w.data_ptr(), _ptr(b), out.data_ptr(), old, _ptr(codes), _ptr(exps), rows,
-                      shape[-1], eps, dt))
+    _call(fn, index, x.data_ptr(), ld, w.data_ptr(), bp, out.data_ptr(), old, cp, ep, rows, C, eps, dt)
     return out
 
 
@@ -1304,8 +1304,8 @@ def la_layer_norm_backward(x, w, dy, eps=1e-5, dx=None, dw=None, db=None, worksp
     dw = torch.empty_like(w) if dw is None else dw
     db = torch.empty_like(w) if db is None else db
     ws, nbytes = _scratch(dy, _bytes("la_layer_norm_workspace_bytes", rows, C), workspace)
-    _call(fn, index, (xp, ld, cp, ep, w.data_ptr(), dy.data_ptr(), dyld, dx.data_ptr(), dxld, dw.data_ptr(),
-                      db.data_ptr(), rows, C, eps, dt, _ptr(ws), nbytes))
+    _call(fn, index, xp, ld, cp, ep, w.data_ptr(), dy.data_ptr(), dyld, dx.data_ptr(), dxld, dw.data_ptr(),
+          db.data_ptr(), rows, C, eps, dt, ws.data_ptr(), nbytes)
     return dx, dw, db
 
 
@@ -1358,8 +1358,8 @@ def la_ffn_gate(x, wg, wu, activation="silu", out=None, checkpoint=None, workspa
         old = _token_rows(fn, "out", out)[1]
         _on(index, whole, (out,))
     ws, nbytes = _scratch(x, _bytes("la_ffn_gate_workspace_bytes", rows, C, F, kept, dt), workspace)
-    _call(fn, index, (x.data_ptr(), ld, wg.data_ptr(), wu.data_ptr(), out.data_ptr(), old, cp, ep, rows, C, F, act,
-                      dt, _ptr(ws), nbytes))
+    _call(fn, index, x.data_ptr(), ld, wg.data_ptr(), wu.data_ptr(), out.data_ptr(), old, cp, ep, rows, C, F, act, dt,
+          _ptr(ws), nbytes)
     return out
 
 
@@ -1396,6 +1396,6 @@ def la_ffn_gate_backward(x, wg, wu, dh, activation="silu", checkpoint=None, dx=N
     dwg = torch.empty_like(wg) if dwg is None else dwg
     dwu = torch.empty_like(wu) if dwu is None else dwu
     ws, nbytes = _scratch(x, _bytes("la_ffn_gate_backward_workspace_bytes", rows, C, F, dt), workspace)
-    _call(fn, index, (x.data_ptr(), ld, wg.data_ptr(), wu.data_ptr(), dh.data_ptr(), dhld, cp, ep, dx.data_ptr(),
-                      dxld, dwg.data_ptr(), dwu.data_ptr(), rows, C, F, act, dt, _ptr(ws), nbytes))
+    _call(fn, index, x.data_ptr(), ld, wg.data_ptr(), wu.data_ptr(), dh.data_ptr(), dhld, cp, ep, dx.data_ptr(), dxld,
+          dwg.data_ptr(), dwu.data_ptr(), rows, C, F, act, dt, ws.data_ptr(), nbytes)
     return dx, dwg, dwu

@@ -14,45 +14,10 @@ namespace ffn {
 
 enum Act { kSilu = 0, kGelu = 1, kGeluTanh = 2 };
 
-// float32 results: expf, erfcf and rounded quotients. 1 - s cancels nothing: both come from
-// exp(-|z|).
-__device__ __forceinline__ void sigmoid(float z, float& s, float& rest) {
-  const float e = expf(-fabsf(z));
-  const float large = 1.f / (1.f + e), small = e * large;
-  s = z < 0.f ? small : large;
-  rest = z < 0.f ? large : small;
-}
-
-template <int ACT>
-__device__ __forceinline__ void act_grad(float a, float& f, float& df) {
-  if constexpr (ACT == kGelu) {
-    const float p = 0.5f * erfcf(-0.70710678118654752f * a);
-    f = a * p;
-    df = fmaf(0.3989422804014327f * a, expf(-0.5f * a * a), p);
-    return;
-  }
-  float z = a, dz = 1.f, s, rest;
-  if constexpr (ACT == kGeluTanh) {
-    const float b = fminf(fmaxf(a, -16.f), 16.f);  // (s is 0 or 1 there, and nothing overflows)
-    const float q = 0.044715f * b * b;
-    z = 1.5957691216057308f * b * (1.f + q);
-    dz = 1.5957691216057308f * fmaf(3.f, q, 1.f);
-  }
-  sigmoid(z, s, rest);
-  f = a * s;
-  df = s * fmaf(a * dz, rest, 1.f);
-}
-
-template <int ACT>
-__device__ __forceinline__ float act(float a) {
-  float f, df;
-  act_grad<ACT>(a, f, df);
-  return f;
-}
-
-// bf16 results, two neighbours at once in packed arithmetic, with the hardware's base-2
-// exponential and reciprocal (each off by 2 steps of 2^-23 at most, zero below 2^-126: 2^-17 in
-// all for exponents below 30, far below the result's rounding).
+// Two neighbours at once in packed float32 arithmetic, with the hardware's base-2 exponential
+// and reciprocal, each off by 2 steps of 2^-23 at most, results below 2^-126 zero. An exponential's
+// argument y is rounded, by |y| 2^-24: where s is small, at y = 20, it is off by 2^-19 of itself,
+// and by less than 2^-22 of the largest s, as a sum that is off by 2^-22 makes of it.
 __device__ __forceinline__ float2 ex2(float2 x) {
   float2 y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(x.x));
@@ -77,20 +42,22 @@ __device__ __forceinline__ float2 tanh_arg(float2 a, float2& q) {
   return tcx::mul2(tcx::mul2(a, both(-2.302208198f)), tcx::add2(q, both(1.f)));
 }
 
-// P(a) and e = exp(-a^2 / 2). With t = 1 / (1 + 0.375 |a| / sqrt(2)), a polynomial of t for
-// erfc(|a| / sqrt(2)) / e, fitted (least squares, reweighted towards the largest error) to 6.4e-7
-// relative for |a| up to 13, past which e is 0: P(a) and 1 - P(a) keep their digits.
+// P(a) and e = exp(-a^2 / 2). With t = 1 / (1 + 0.33 |a| / sqrt(2)), a polynomial of t for
+// erfc(|a| / sqrt(2)) / e, fitted (least squares, reweighted towards the largest error) to 8.2e-8
+// relative for |a| up to 13, past which e is 0: P(a) and 1 - P(a) keep their digits (4.4e-7 as
+// evaluated).
 __device__ __forceinline__ float2 normal2(float2 a, float2& e) {
   using namespace tcx;
   e = ex2(mul2(mul2(a, both(-0.72134752f)), a));
-  const float2 t = rcp(fma2(make_float2(fabsf(a.x), fabsf(a.y)), both(0.265165043f), both(1.f)));
-  float2 q = both(-0.06754790f);
-  q = fma2(q, t, both(0.19396870f));
-  q = fma2(q, t, both(-0.06479833f));
-  q = fma2(q, t, both(0.14153051f));
-  q = fma2(q, t, both(0.08333239f));
-  q = fma2(q, t, both(0.10784457f));
-  q = fma2(q, t, both(0.10566973f));
+  const float2 t = rcp(fma2(make_float2(fabsf(a.x), fabsf(a.y)), both(0.233345238f), both(1.f)));
+  float2 q = both(-0.0679643825f);
+  q = fma2(q, t, both(0.231344029f));
+  q = fma2(q, t, both(-0.17771931f));
+  q = fma2(q, t, both(0.20627065f));
+  q = fma2(q, t, both(0.0225054026f));
+  q = fma2(q, t, both(0.100961886f));
+  q = fma2(q, t, both(0.0914186239f));
+  q = fma2(q, t, both(0.0931830555f));
   const float2 tail = mul2(mul2(q, t), e);  // of |a|
   const float2 rest = sub2(both(1.f), tail);
   return make_float2(a.x < 0.f ? tail.x : rest.x, a.y < 0.f ? tail.y : rest.y);

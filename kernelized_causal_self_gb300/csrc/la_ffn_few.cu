@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(32 * kWarps) ffn_few_f32_kernel(const Args a) 
     for (int i = 1; i < kWarps; ++i) s += sums[i][lane];
     const float u = __shfl_down_sync(0xffffffffu, s, 16);
     const int n = lane % 8, f = f0 + lane / 8;
-    if (lane < 16 && n < a.T) static_cast<float*>(a.h)[n * a.h_stride + f] = act<ACT>(s) * u;
+    if (lane < 16 && n < a.T) static_cast<float*>(a.h)[n * a.h_stride + f] = act2<ACT>(make_float2(s, 0.f)).x * u;
   }
 }
 

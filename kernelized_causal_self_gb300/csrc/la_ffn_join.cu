@@ -83,12 +83,7 @@ __global__ void __launch_bounds__(256) ffn_kept_grads_kernel(const Kept a) {
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
     float2 fa, df;
-    if constexpr (sizeof(T) == 2) {
-      act_grad2<ACT>(make_float2(g[j], g[j + 1]), fa, df);
-    } else {
-      act_grad<ACT>(g[j], fa.x, df.x);
-      act_grad<ACT>(g[j + 1], fa.y, df.y);
-    }
+    act_grad2<ACT>(make_float2(g[j], g[j + 1]), fa, df);
     da[j] = dv[j] * u[j] * df.x, da[j + 1] = dv[j + 1] * u[j + 1] * df.y;
     du[j] = dv[j] * fa.x, du[j + 1] = dv[j + 1] * fa.y;
   }

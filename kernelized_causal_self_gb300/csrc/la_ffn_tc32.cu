@@ -258,22 +258,37 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc32_kernel(const __grid_cons
             }
           }
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[c * 32 + j] = act<ACT>(v[c * 32 + j]) * v[64 + c * 32 + j];
+          for (int j = c * 32; j < c * 32 + 32; j += 2) {
+            const float2 h = mul2(act2<ACT>(make_float2(v[j], v[j + 1])), make_float2(v[64 + j], v[64 + j + 1]));
+            v[j] = h.x, v[j + 1] = h.y;
+          }
           leave32(v + c * 32, &a.out0, f, 0);
         }
       } else if constexpr (KIND == kGrads) {
         const float* dh = a.dh + row * a.dh_stride + col0;
+        float4 next[4];  // dh, 16 columns at a time, one time ahead
+        auto ask = [&](int j0) {
 #pragma unroll
-        for (int j = 0; j < 64; j += 4) {  // da and du take the places of a and u
-          const float4 d4 = row < a.rows && col0 + j < a.cols ? __ldg(reinterpret_cast<const float4*>(dh + j))
-                                                             : make_float4(0.f, 0.f, 0.f, 0.f);
-          const float d[4] = {d4.x, d4.y, d4.z, d4.w};
+          for (int i = 0; i < 4; ++i)
+            next[i] = row < a.rows && col0 + j0 + 4 * i < a.cols ? __ldg(reinterpret_cast<const float4*>(dh + j0 + 4 * i))
+                                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        ask(0);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float f, df;
-            act_grad<ACT>(v[j + i], f, df);
-            v[j + i] = d[i] * v[64 + j + i] * df;
-            v[64 + j + i] = d[i] * f;
+        for (int j0 = 0; j0 < 64; j0 += 16) {  // da and du take the places of a and u
+          float d[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[4 * i] = next[i].x, d[4 * i + 1] = next[i].y, d[4 * i + 2] = next[i].z, d[4 * i + 3] = next[i].w;
+          if (j0 < 48) ask(j0 + 16);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const int j = j0 + i;
+            const float2 dv = make_float2(d[i], d[i + 1]);
+            float2 f, df;
+            act_grad2<ACT>(make_float2(v[j], v[j + 1]), f, df);
+            const float2 da = mul2(mul2(dv, make_float2(v[64 + j], v[64 + j + 1])), df), du = mul2(dv, f);
+            v[j] = da.x, v[j + 1] = da.y;
+            v[64 + j] = du.x, v[64 + j + 1] = du.y;
           }
         }
 #pragma unroll
