@@ -43,6 +43,7 @@ LA_SITE_FORWARD_LOAD, LA_SITE_FORWARD_FUSED_LOAD, LA_SITE_BACKWARD_LOAD = 11, 16
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "liblagb300.so")
+_MARSHAL_PATH = os.path.join(_HERE, "_build", "la_marshal.so")
 _lib = None
 
 _c_int, _c_size, _vp = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
@@ -1113,8 +1114,34 @@ def la_norm_gate_backward(x, z, w, dy, eps=1e-6, dx=None, dz=None, dw=None, work
 
 # ------------------------- layer norm, gated projections, activations in 8 bits
 #
-# (These are called for single tokens, where a call's checks cost as much as its kernel: whole
-# comparisons first, and what is wrong is looked for only where one fails.)
+# Each function asks la_marshal (csrc/la_marshal.cpp) first, which does the whole call if its tensors
+# are contiguous and on the current device, and nothing otherwise: single tokens come this way,
+# whose kernels take less than the checks below in Python.
+
+_fast = None
+
+
+def _marshal():
+    """The marshalling module, connected to the library; raises if either has not been built."""
+    global _fast
+    if _fast is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries are the module's)
+        lib = load_library()
+        if not os.path.exists(_MARSHAL_PATH):
+            raise RuntimeError(
+                f"binding not built: {_MARSHAL_PATH} is missing "
+                "(run `python -c 'import __graft_entry__ as g; g.build()'`)")
+        loader = importlib.machinery.ExtensionFileLoader("la_marshal", _MARSHAL_PATH)
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_file_location("la_marshal", _MARSHAL_PATH, loader=loader))
+        loader.exec_module(module)
+        module.connect(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in module.names()])
+        _fast = module
+    return _fast
+
 
 _ACTIVATIONS = {"silu": LA_SILU, "gelu": LA_GELU, "gelu_tanh": LA_GELU_TANH}
 
@@ -1195,6 +1222,9 @@ def la_checkpoint(x, checkpoint=None):
     for which every |value| / step is below 127.5. A value is off by half a step at most. A block
     that holds an infinity or a NaN restores as NaN. checkpoint: a pair to write to."""
     import torch
+    done = (_fast or _marshal()).checkpoint(x, checkpoint)
+    if done is not NotImplemented:
+        return done
     fn = "la_checkpoint"
     dt, shape, index = _dtype_code(x), x.shape, x.get_device()
     rows, ld = _token_rows(fn, "x", x)
@@ -1214,6 +1244,10 @@ def la_checkpoint_restore(codes, exps, dtype=None, out=None):
     """The values that a checkpoint stands for, [..., C] in `dtype` (default: out's, or bfloat16,
     which holds all of them exactly)."""
     import torch
+    if out is None and (dtype is None or dtype in (torch.float32, torch.bfloat16)):
+        done = (_fast or _marshal()).checkpoint_restore(codes, exps, LA_F32 if dtype is torch.float32 else LA_BF16)
+        if done is not NotImplemented:
+            return done
     fn = "la_checkpoint_restore"
     shape, index = codes.shape, codes.get_device()
     if not shape:
@@ -1244,6 +1278,9 @@ def la_layer_norm(x, w, b=None, eps=1e-5, out=None, checkpoint=None):
     w [C], b [C] or None. Rows of x and out may be strided evenly; out may be x. checkpoint: a pair
     (codes, exps), as la_checkpoint makes it, that receives x in 8 bits on the way."""
     import torch
+    done = (_fast or _marshal()).layer_norm(x, w, b, eps, out, checkpoint)
+    if done is not NotImplemented:
+        return done if out is None else out
     fn = "la_layer_norm"
     dt, shape, dtype, index = _dtype_code(x), x.shape, x.dtype, x.get_device()
     rows, ld = _token_rows(fn, "x", x)
@@ -1273,6 +1310,10 @@ def la_layer_norm_backward(x, w, dy, eps=1e-5, dx=None, dw=None, db=None, worksp
 
     x: the norm's input [..., C], or a checkpoint (codes, exps) of it. dx may be x or dy."""
     import torch
+    if dx is None and dw is None and db is None and workspace is None:
+        done = (_fast or _marshal()).layer_norm_backward(x, w, dy, eps)
+        if done is not NotImplemented:
+            return done
     fn = "la_layer_norm_backward"
     dt, shape, dtype, index = _dtype_code(dy), dy.shape, dy.dtype, dy.get_device()
     rows, dyld = _token_rows(fn, "dy", dy)
@@ -1342,6 +1383,10 @@ def la_ffn_gate(x, wg, wu, activation="silu", out=None, checkpoint=None, workspa
     uint8 [..., 2, ceil(F/32)]) that receives x wg^T and x wu^T in 8 bits, for the backward pass.
     Rows of x and out may be strided evenly."""
     import torch
+    if workspace is None:
+        done = (_fast or _marshal()).ffn_gate(x, wg, wu, _ACTIVATIONS.get(activation, -1), out, checkpoint)
+        if done is not NotImplemented:
+            return done if out is None else out
     fn = "la_ffn_gate"
     rows, ld, C, F, dt, act = _ffn_checks(fn, x, wg, wu, activation)
     index, shape = x.get_device(), (*x.shape[:-1], F)
@@ -1370,6 +1415,10 @@ def la_ffn_gate_backward(x, wg, wu, dh, activation="silu", checkpoint=None, dx=N
     checkpoint: the pair that la_ffn_gate filled; x wg^T and x wu^T are then taken from it instead
     of being computed again. Rows of x, dh and dx may be strided evenly."""
     import torch
+    if dx is None and dwg is None and dwu is None and workspace is None:
+        done = (_fast or _marshal()).ffn_gate_backward(x, wg, wu, _ACTIVATIONS.get(activation, -1), dh, checkpoint)
+        if done is not NotImplemented:
+            return done
     fn = "la_ffn_gate_backward"
     rows, ld, C, F, dt, act = _ffn_checks(fn, x, wg, wu, activation)
     index, dtype, shape = x.get_device(), x.dtype, x.shape

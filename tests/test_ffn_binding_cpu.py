@@ -176,3 +176,37 @@ def test_abi_ffn(lib):
     assert need(100, 64, 128, 0, 1) == need(4, 64, 128, 1, 1) == need(-1, 64, 128, 0, 1) == 256
     assert need(4, 64, 128, 0, 1) == need(4, 64, 128, 0, 0) == 0
     assert need(100, 64, 128, 0, 0) >= 256 + 6 * 64 * (100 + 2 * 128)
+
+
+def test_marshalling_leaves_what_it_does_not_do(lib):
+    """The C++ marshalling answers NotImplemented, and launches nothing, for anything but plain CUDA
+    tensors; its functions are the library's."""
+    m = la._marshal()
+    assert set(m.names()) <= set(la._SIGNATURES)
+    x, w, h = _t(4, 40), _t(40), _t(8, 40)
+    pair = _pair(4, 40)
+    before = la.la_kernel_launches()
+    for args in ((x, None), (x, pair), (None, None), (x,), (3, None)):
+        assert m.checkpoint(*args) is NotImplemented
+    for args in ((*pair, 0), (*pair, 7), (x, pair[1], 0), (None, None, 0)):
+        assert m.checkpoint_restore(*args) is NotImplemented
+    for args in ((x, w, None, 1e-5, None, None), (x, w, w, 0, None, pair), (x, w, w, 1e-5, x), ([1], w, w, 1e-5, None, None)):
+        assert m.layer_norm(*args) is NotImplemented
+    for args in ((x, w, x, 1e-5), (pair, w, x, 1e-5), (None, w, x, 1e-5), (x, w, x)):
+        assert m.layer_norm_backward(*args) is NotImplemented
+    for args in ((x, h, h, 0, None, None), (x, h, h, -1, x, pair), (x, h[0], h, 0, None, None), (x, h, h)):
+        assert m.ffn_gate(*args) is NotImplemented
+    for args in ((x, h, h, 0, _t(4, 8), None), (x, h, h, 0, _t(4, 8), pair), (x, h, h, 0, None)):
+        assert m.ffn_gate_backward(*args) is NotImplemented
+    assert la.la_kernel_launches() == before
+    with pytest.raises(ValueError):
+        m.connect(1, 2)
+    with pytest.raises(ValueError):
+        m.connect(*[0] * len(m.names()))
+
+
+def test_missing_marshalling_module_raises(monkeypatch):
+    monkeypatch.setattr(la, "_fast", None)
+    monkeypatch.setattr(la, "_MARSHAL_PATH", "/nowhere/la_marshal.so")
+    with pytest.raises(RuntimeError, match="not built"):
+        la.la_layer_norm(_t(4, 40), _t(40))

@@ -462,6 +462,68 @@ def test_calls_on_another_stream_and_in_a_graph(la):
         assert all(torch.equal(p, q) for p, q in zip(got, ref))
 
 
+class _Nothing:
+    """A marshalling module that does no call itself."""
+
+    def __getattr__(self, name):
+        return lambda *args: NotImplemented
+
+
+@TYPES
+def test_calls_marshalled_in_cpp_are_those_in_python(la, monkeypatch, dtype):
+    T, C, F = 50, 72, 136
+    x, wg, wu, dh = _ffn_inputs(T, C, F, dtype)
+    w, b, big = _randn(7, C, dtype=dtype), _randn(8, C, dtype=dtype), x.reshape(5, 10, C)
+
+    def calls():
+        pair, both = la.la_checkpoint(big), (torch.zeros(T, 2, F, dtype=torch.int8, device=DEV),
+                                             torch.zeros(T, 2, 5, dtype=torch.uint8, device=DEV))
+        kept, out = la.la_checkpoint(x), torch.zeros_like(big)
+        h = la.la_ffn_gate(x, wg, wu, "gelu", checkpoint=both)
+        assert la.la_layer_norm(big, w, b, out=out) is out
+        return [*pair, la.la_checkpoint_restore(*pair), la.la_checkpoint_restore(*pair, dtype=FL), out,
+                la.la_layer_norm(big, w, eps=0.25), la.la_layer_norm(x, w, b, checkpoint=kept), *kept,
+                *la.la_layer_norm_backward(big, w, big), *la.la_layer_norm_backward(kept, w, x, eps=0.5),
+                h, *both, la.la_ffn_gate(big, wg, wu), la.la_ffn_gate(x[0], wg, wu, out=torch.zeros(F, dtype=dtype, device=DEV)),
+                *la.la_ffn_gate_backward(big, wg, wu, dh.view(5, 10, F)),
+                *la.la_ffn_gate_backward(x, wg, wu, dh, "gelu", checkpoint=both)]
+    n0 = la.la_kernel_launches()
+    fast, n1 = calls(), la.la_kernel_launches()
+    monkeypatch.setattr(la, "_fast", _Nothing())
+    slow, n2 = calls(), la.la_kernel_launches()
+    assert n1 - n0 == n2 - n1
+    for p, q in zip(fast, slow):
+        assert p.shape == q.shape and p.dtype == q.dtype and p.device == q.device and torch.equal(p, q)
+
+
+def test_a_status_is_left_in_the_workspace(la):
+    """The tensor-core calls clear the status header of a workspace of any contents."""
+    for dtype in (BF, FL):
+        x, wg, wu, dh = _ffn_inputs(100, 64, 72, dtype)
+        dt = la.LA_BF16 if dtype == BF else la.LA_F32
+        for pair in (None, _kept_like(100, 2, 72)):
+            ws = torch.full((la.la_ffn_gate_workspace_bytes(100, 64, 72, pair is not None, dt),), 3, dtype=torch.uint8,
+                            device=DEV)
+            la.la_ffn_gate(x, wg, wu, checkpoint=pair, workspace=ws)
+            assert la.la_workspace_status(ws) == la.LA_OK
+            ws = torch.full((la.la_ffn_gate_backward_workspace_bytes(100, 64, 72, dt),), 3, dtype=torch.uint8, device=DEV)
+            la.la_ffn_gate_backward(x, wg, wu, dh, checkpoint=pair, workspace=ws)
+            assert la.la_workspace_status(ws) == la.LA_OK
+
+
+def test_outputs_that_share_memory_are_refused(la):
+    x, wg, wu, dh = _ffn_inputs(40, 72, 72, BF)
+    w = _randn(5, 72, dtype=BF)
+    for call in (lambda: la.la_ffn_gate(x, wg, wu, out=x), lambda: la.la_ffn_gate(x, wg, wu, out=wg[:40]),
+                 lambda: la.la_ffn_gate_backward(x, wg, wu, dh, dx=x), lambda: la.la_ffn_gate_backward(x, wg, wu, dh, dwg=wu),
+                 lambda: la.la_layer_norm(x[:39], w, out=x[1:]), lambda: la.la_layer_norm(x[:1], w, out=w[None]),
+                 lambda: la.la_layer_norm_backward(x, w, dh, dw=w)):
+        before = la.la_kernel_launches()
+        with pytest.raises(la.LAError, match="invalid argument"):
+            call()
+        assert la.la_kernel_launches() == before
+
+
 def test_a_workspace_of_the_callers(la):
     T, C, F = 200, 128, 264
     x, wg, wu, dh = _ffn_inputs(T, C, F, BF)
