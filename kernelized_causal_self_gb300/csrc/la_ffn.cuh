@@ -104,10 +104,15 @@ __device__ __forceinline__ uint32_t take_part(float& x, float& y, int part) {
 
 }  // namespace ffn
 
-// out (and out2 with count 2): the sums over `splits` parts of partial [count][splits][rows][C],
-// added in order
-cudaError_t ffn_join(const float* partial, void* out, void* out2, long long out_stride, int rows, int count, int C,
-                     int splits, int dtype, cudaStream_t st);
+// A matrix `to` of `rows` rows `stride` apart: the sums over `splits` parts of from
+// [splits][rows][C], added in order; `n` of them, of C columns each, at once
+struct Join {
+  const float* from;
+  void* to;
+  long long stride;
+  int rows, splits;
+};
+cudaError_t ffn_join(const Join* j, int n, int C, int dtype, cudaStream_t st);
 // dact: da = dh u act'(a), du = dh act(a), a and u from f's checkpoint; in bf16 [2][T][F], in float32
 // as their three bf16 parts, [2][3][T][F]
 cudaError_t ffn_kept_grads(const FfnGate& f, void* dact, cudaStream_t st);

@@ -12,8 +12,6 @@ namespace {
 using namespace tcx;
 using namespace ffn;
 
-constexpr int kSms = 152;
-
 // 4 neighbours as float32
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
@@ -30,22 +28,42 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
                                             tc::pack_bf16(v[4], v[5]), tc::pack_bf16(v[6], v[7]));
 }
 
-// The parts of split sums, added in order: matrix blockIdx.y of [.][splits][rows][C]
+struct Joins {
+  Join j[3];
+};
+
+constexpr int kEach = 4;  // times 4 neighbours a thread: its loads of a part are in flight together
+
+// Matrix blockIdx.y
 template <typename T>
-__global__ void __launch_bounds__(256) ffn_join_kernel(const float* partial, T* out, T* out2, long long out_stride,
-                                                       int rows, int C, int splits) {
-  const long long n = (long long)rows * C / 4;
-  const float* p = partial + (size_t)blockIdx.y * splits * rows * C;
-  T* to = blockIdx.y ? out2 : out;
-  tc::pdl_wait();
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-    float4 s = load4(p + 4 * i);
-    for (int k = 1; k < splits; ++k) {
-      const float4 v = load4(p + (size_t)k * rows * C + 4 * i);
-      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+__global__ void __launch_bounds__(256) ffn_join_kernel(const Joins all, int C) {
+  const Join& m = all.j[blockIdx.y];
+  const unsigned per = C / 4;
+  const size_t n = (size_t)m.rows * per, plane = n * 4;
+  const size_t at = (size_t)blockIdx.x * (256 * kEach) + threadIdx.x;
+  pdl_wait();
+  const float* p = m.from + at * 4;
+  float4 s[kEach];
+#pragma unroll
+  for (int j = 0; j < kEach; ++j)
+    if (at + j * 256 < n) s[j] = __ldcs(reinterpret_cast<const float4*>(p + j * 1024));
+#pragma unroll 2
+  for (int k = 1; k < m.splits; ++k) {
+    p += plane;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      if (at + j * 256 >= n) continue;
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(p + j * 1024));
+      s[j].x += v.x, s[j].y += v.y, s[j].z += v.z, s[j].w += v.w;
     }
-    const long long row = 4 * i / C;
-    store4(to + row * out_stride + (4 * i - row * C), s);
+  }
+  const size_t row0 = at / per;  // (one 64-bit division a thread)
+  const unsigned c0 = (unsigned)(at - row0 * per);
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    if (at + j * 256 >= n) continue;
+    const unsigned i = c0 + j * 256;
+    store4(static_cast<T*>(m.to) + (long long)(row0 + i / per) * m.stride + i % per * 4, s[j]);
   }
 }
 
@@ -116,23 +134,20 @@ cudaError_t kept_grads(const Kept& a, int act, cudaStream_t st) {
   return e;
 }
 
-template <typename T>
-cudaError_t join(const float* partial, void* out, void* out2, long long stride, int rows, int count, int C, int splits,
-                 cudaStream_t st) {
-  const long long n = (long long)rows * C / 4;
-  const int ctas = (int)((n + 255) / 256 < 8 * kSms ? (n + 255) / 256 : 8 * kSms);
-  const cudaError_t e = launch_pdl(ffn_join_kernel<T>, dim3(ctas, count), dim3(256), 0, st, partial,
-                                   static_cast<T*>(out), static_cast<T*>(out2), stride, rows, C, splits);
-  count_launches(1);
-  return e;
-}
-
 }  // namespace
 
-cudaError_t ffn_join(const float* partial, void* out, void* out2, long long out_stride, int rows, int count, int C,
-                     int splits, int dtype, cudaStream_t st) {
-  return dtype == LA_F32 ? join<float>(partial, out, out2, out_stride, rows, count, C, splits, st)
-                         : join<__nv_bfloat16>(partial, out, out2, out_stride, rows, count, C, splits, st);
+cudaError_t ffn_join(const Join* j, int n, int C, int dtype, cudaStream_t st) {
+  Joins all{};
+  long long most = 0;
+  for (int i = 0; i < n; ++i) {
+    all.j[i] = j[i];
+    if (j[i].rows > most) most = j[i].rows;
+  }
+  const dim3 grid((unsigned)((most * (C / 4) + 256 * kEach - 1) / (256 * kEach)), n);  // (rows <= 2^24, C <= 2^16: an int)
+  const cudaError_t e = dtype == LA_F32 ? launch_pdl(ffn_join_kernel<float>, grid, dim3(256), 0, st, all, C)
+                                        : launch_pdl(ffn_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, all, C);
+  count_launches(1);
+  return e;
 }
 
 cudaError_t ffn_kept_grads(const FfnGate& f, void* dact, cudaStream_t st) {

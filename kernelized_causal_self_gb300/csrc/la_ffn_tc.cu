@@ -2,7 +2,7 @@
 // the backward pass da = dh u act'(a), du = dh act(a), dx = da wg + du wu, dwg = da^T x,
 // dwu = du^T x (da and du in bf16, in the workspace).
 //
-// One persistent kernel for all five products. A pair of CTAs (cta_group::2) makes a tile of
+// One persistent kernel for all five products (in two launches, dx and the weights' in one). A pair of CTAs (cta_group::2) makes a tile of
 // 256 x 256: each CTA copies its 128 rows of A and its half of B's 256 rows by TMA, 64 terms
 // of the sum a stage, the even one issues the MMAs, and each finds its 128 x 256 of D in its
 // own tensor memory, where two accumulators take turns, so that eight warps write one tile's
@@ -10,8 +10,8 @@
 //   kForward, kGrads  A = x, B = 128 rows of wg (even CTA) and the same rows of wu (odd CTA): a
 //                     row's a and u come to lie in one thread, 128 columns apart, and nothing
 //                     but h (or da, du) leaves the SM. kGrads has dh's tile copied in as well.
-//   kDx               A = [da | du], B = [wg; wu] read along c: one sum over 2 F terms.
-//   kDw               A = da or du and B = x, both read along their rows (tokens are the sum).
+//   kSums, dx         A = [da | du], B = [wg; wu] read along c: one sum over 2 F terms.
+//   kSums, dwg, dwu   A = da or du and B = x, both read along their rows (tokens are the sum).
 // Results go through a swizzled staging tile of 32 rows a warp and leave by TMA, which clips
 // what is past the matrix; copies past its edge read zeros, so ragged sizes need no masks.
 // Sums with few tiles are cut along k (float32 parts, added in order by a second kernel).
@@ -32,10 +32,11 @@ constexpr int smem_of(int kind) {
   return 1024 + stages_of(kind) * kStageBytes + kWarps * kStore + (kind == kGrads ? 2 * kTileBytes : 0) + 256;
 }
 
-struct Args : Grid {
-  CUtensorMap a, b0, b1;    // operands (b0, b1: wg and wu; kDw: b0 = x)
-  CUtensorMap out0, out1;   // h; da, du; dx; dwg, dwu; out0 if the sum is cut: its parts in
-                            // float32, [dw: 2][splits][rows][C]
+struct Args : Grids {
+  CUtensorMap a, b0, b1;         // operands: x or da, du; wg; wu
+  CUtensorMap aw, bw;            // of dwg and dwu: da, du and x, both read along their rows
+  CUtensorMap out0, out1, out2;  // h; da, du; dx, dwg, dwu. Of cut sums their parts in float32: out0
+                                 // [splits][T][C], out1 [2][splits][F][C]
   CUtensorMap dh;           // kGrads
   WorkspaceHeader* hdr;
   signed char* codes;       // kForward: a checkpoint of a, u
@@ -88,9 +89,13 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
     prefetch_tensormap(&a.a);
     prefetch_tensormap(&a.b0);
     prefetch_tensormap(&a.out0);
-    if (KIND != kDw) prefetch_tensormap(&a.b1);
+    prefetch_tensormap(&a.b1);
     if (KIND == kGrads) prefetch_tensormap(&a.dh);
-    if (KIND == kGrads || KIND == kDw) prefetch_tensormap(&a.out1);
+    if (KIND != kForward) prefetch_tensormap(&a.out1);
+    if (KIND == kSums) {
+      prefetch_tensormap(&a.aw);
+      prefetch_tensormap(&a.bw);
+    }
   }
   fence_before_sync();
   __syncthreads();
@@ -108,15 +113,16 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
       const uint32_t bars = cluster_map(smem_u32(full), 0);
       uint32_t s = 0, phase = 1;  // (a stage not used yet counts as emptied once)
       bool ok = true;
-      for (int t = cluster; t < a.tiles && ok; t += clusters) {
+      for (int t, i = 0; ok && (t = dealt<KIND>(a, cluster, clusters, i)) >= 0; ++i) {
         const Tile w = tile_of<KIND>(a, t);
-        const int row = w.m * 256 + (int)rank * 128, end = first_step<KIND>(a, w.split + 1);
-        if (DUAL && t + clusters < a.tiles) {
+        const Grid& g = a.g[w.dw];
+        const int row = w.m * 256 + (int)rank * 128, end = first_step(g, w.split + 1);
+        if (DUAL && t + clusters < g.tiles) {
           // x of the next tile into L2, a tile's time ahead: the tiles of the same rows share its steps
           const Tile v = tile_of<KIND>(a, t + clusters);
-          for (int k = v.n; k < a.steps; k += a.n_tiles) tma_prefetch_3d(&a.a, k * 64, v.m * 256 + (int)rank * 128, 0);
+          for (int k = v.n; k < g.steps; k += g.n_tiles) tma_prefetch_3d(&a.a, k * 64, v.m * 256 + (int)rank * 128, 0);
         }
-        for (int k = first_step<KIND>(a, w.split); k < end; ++k) {
+        for (int k = first_step(g, w.split); k < end; ++k) {
           if (!mbar_wait_abort(&empty[s], phase, abort, hdr, kSiteEmpty)) {
             ok = false;
             break;
@@ -127,18 +133,18 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
           if constexpr (DUAL) {
             tma_load_3d_pair(ta, &a.a, bar, k * 64, row, 0);
             tma_load_3d_pair(tb, rank ? &a.b1 : &a.b0, bar, k * 64, w.n * 128, 0);
-          } else if constexpr (KIND == kDx) {
-            const int part = k >= a.per, kk = (part ? k - a.per : k) * 64;
+          } else if (!w.dw) {
+            const int part = k >= g.per, kk = (part ? k - g.per : k) * 64;
             const int col = w.n * 256 + (int)rank * 128;
             tma_load_3d_pair(ta, &a.a, bar, kk, row, part);
             tma_load_3d_pair(tb, part ? &a.b1 : &a.b0, bar, col, kk, 0);
             tma_load_3d_pair(tb + kTileBytes / 2, part ? &a.b1 : &a.b0, bar, col + 64, kk, 0);
           } else {
             const int col = w.n * 256 + (int)rank * 128;
-            tma_load_3d_pair(ta, &a.a, bar, row, k * 64, w.part);
-            tma_load_3d_pair(ta + kTileBytes / 2, &a.a, bar, row + 64, k * 64, w.part);
-            tma_load_3d_pair(tb, &a.b0, bar, col, k * 64, 0);
-            tma_load_3d_pair(tb + kTileBytes / 2, &a.b0, bar, col + 64, k * 64, 0);
+            tma_load_3d_pair(ta, &a.aw, bar, row, k * 64, w.part);
+            tma_load_3d_pair(ta + kTileBytes / 2, &a.aw, bar, row + 64, k * 64, w.part);
+            tma_load_3d_pair(tb, &a.bw, bar, col, k * 64, 0);
+            tma_load_3d_pair(tb + kTileBytes / 2, &a.bw, bar, col + 64, k * 64, 0);
           }
           if (++s == S) s = 0, phase ^= 1;
         }
@@ -158,7 +164,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
     if (lane == 0) {
       int nt = 0;
       bool ok = true;
-      for (int t = cluster; t < a.tiles && ok; t += clusters) {
+      for (int t; (t = dealt<KIND>(a, cluster, clusters, nt)) >= 0;) {
         const Tile w = tile_of<KIND>(a, t);
         const int row = w.m * 256 + (int)rank * 128;
         if (nt > 0) ok = mbar_wait_abort(dh_empty, (uint32_t)((nt - 1) & 1), abort, hdr, kSiteDhEmpty);
@@ -174,21 +180,24 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
   } else if (warp == kWarps + 1) {
     // ------------------------------------------------------------------ products
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t id = idesc_bf16(256, 256, KIND == kDw, !DUAL);
       // along k: 32 bytes of a row a step of 16; along m or n: 16 rows, blocks of 64 columns 8 KB apart
       const uint32_t at = smem_u32(stages);
-      const uint64_t da0 = KIND == kDw ? sdesc(at, kTileBytes / 2, 1024) : sdesc(at, 16, 1024);
+      const uint64_t da_k = sdesc(at, 16, 1024), da_m = sdesc(at, kTileBytes / 2, 1024);
       const uint64_t db0 = DUAL ? sdesc(at + kTileBytes, 16, 1024) : sdesc(at + kTileBytes, kTileBytes / 2, 1024);
-      constexpr uint32_t STEP_A = (KIND == kDw ? 2048 : 32) / 16, STEP_B = (DUAL ? 32 : 2048) / 16;
+      constexpr uint32_t ALONG_K = 32 / 16, ALONG_MN = 2048 / 16, STEP_B = DUAL ? ALONG_K : ALONG_MN;
       uint32_t s = 0, phase = 0;
       int nt = 0;
       bool ok = true;
-      for (int t = cluster; t < a.tiles && ok; t += clusters, ++nt) {
-        int n = a.steps;
-        if (!DUAL && a.splits > 1) {
-          const int split = tile_of<KIND>(a, t).split;
-          n = first_step<KIND>(a, split + 1) - first_step<KIND>(a, split);
+      for (int t; ok && (t = dealt<KIND>(a, cluster, clusters, nt)) >= 0; ++nt) {
+        int n = a.g[0].steps, dw = 0;
+        if (!DUAL) {
+          const Tile w = tile_of<KIND>(a, t);
+          dw = w.dw;
+          n = first_step(a.g[dw], w.split + 1) - first_step(a.g[dw], w.split);
         }
+        const uint64_t da0 = !DUAL && dw ? da_m : da_k;
+        const uint32_t step_a = !DUAL && dw ? ALONG_MN : ALONG_K;
+        const uint32_t id = !DUAL && dw ? idesc_bf16(256, 256, true, true) : idesc_bf16(256, 256, false, !DUAL);
         const int b = nt & 1;
         if (nt >= 2) ok = mbar_wait_abort(&acc_empty[b], (uint32_t)((nt / 2 - 1) & 1), abort, hdr, kSiteAccEmpty);
         if (!ok) break;
@@ -203,7 +212,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
           // (addresses are the descriptors' low bits, in units of 16 bytes)
           const uint64_t da = da0 + s * (kStageBytes / 16), db = db0 + s * (kStageBytes / 16);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) mma_ss_pair(d, da + q * STEP_A, db + q * STEP_B, id, (k | q) != 0);
+          for (int q = 0; q < 4; ++q) mma_ss_pair(d, da + q * step_a, db + q * STEP_B, id, (k | q) != 0);
           mma_commit_pair(&empty[s]);
           if (++s == S) s = 0, phase ^= 1;
         }
@@ -221,8 +230,9 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
     const int trow = warp % 4 * 32 + lane;  // of the CTA's 128
     constexpr int GROUPS = DUAL ? 1 : 2;    // of 64 columns
     int nt = 0;
-    for (int t = cluster; t < a.tiles; t += clusters, ++nt) {
+    for (int t; (t = dealt<KIND>(a, cluster, clusters, nt)) >= 0; ++nt) {
       const Tile w = tile_of<KIND>(a, t);
+      const Grid& grid = a.g[w.dw];
       const int b = nt & 1, row0 = w.m * 256 + (int)rank * 128 + warp % 4 * 32, row = row0 + lane;
       if (!mbar_wait_warp(&acc_full[b], (uint32_t)((nt / 2) & 1), abort, hdr, kSiteAccFull)) break;
       if (KIND == kGrads && !mbar_wait_warp(dh_full, (uint32_t)(nt & 1), abort, hdr, kSiteDhFull)) break;
@@ -231,14 +241,14 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
 #pragma unroll 1
       for (int g = warp / 4 * GROUPS; g < (warp / 4 + 1) * GROUPS; ++g) {
         const int col = w.n * (DUAL ? 128 : 256) + g * 64;
-        const bool cut = !DUAL && a.splits > 1;
+        const bool cut = !DUAL && grid.splits > 1;
         uint8_t* st = mine;
         uint32_t gu[KIND == kGrads ? 32 : 1];  // du, which follows da through the staging tile
         auto leave = [&](const CUtensorMap* to, int from, int mat) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (row0 < a.rows && from < a.cols) tma_store_3d(to, st, from, row0, mat);
+            if (row0 < grid.rows && from < grid.cols) tma_store_3d(to, st, from, row0, mat);
             bulk_commit();
           }
         };
@@ -266,7 +276,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
                 *reinterpret_cast<uint4*>(st + sw128(lane, c * 64 + e * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
               }
               if (a.codes != nullptr) {  // a thread has a block of 32 of a and of u
-                const int f = col + c * 32, nb = q8::blocks_of(a.cols);
+                const int f = col + c * 32, nb = q8::blocks_of(grid.cols);
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
                   const float* x = v ? fu : fa;
@@ -275,12 +285,12 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
                   for (int j = 1; j < 31; j += 2) top = q8::top3(top, x[j], x[j + 1]);
                   const uint32_t e = q8::step_of(__float_as_uint(q8::top3(top, x[31], x[31])));
                   const float inv = q8::inverse_step(e);
-                  if (row < a.rows && f < a.cols) {
+                  if (row < grid.rows && f < grid.cols) {
                     const size_t r = 2 * (size_t)row + v;
-                    signed char* to = a.codes + r * a.cols + f;
+                    signed char* to = a.codes + r * grid.cols + f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                      if (f + j * 8 < a.cols)
+                      if (f + j * 8 < grid.cols)
                         *reinterpret_cast<uint2*>(to + j * 8) =
                             make_uint2(q8::codes4(x + j * 8, inv, e), q8::codes4(x + j * 8 + 4, inv, e));
                     a.exps[r * nb + f / q8::kBlock] = (unsigned char)e;
@@ -314,7 +324,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 *reinterpret_cast<uint4*>(st + sw128(lane, e * 16)) = make_uint4(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3]);
-              leave(&a.out0, col + c * 32, KIND == kDw ? w.part * a.splits + w.split : w.split);
+              leave(w.dw ? &a.out1 : &a.out0, col + c * 32, w.part * grid.splits + w.split);
             } else {
               const float* f = reinterpret_cast<const float*>(p);
 #pragma unroll
@@ -333,7 +343,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
             if (KIND == kGrads) mbar_arrive(dh_empty);
           }
         }
-        if (!cut) leave(KIND == kDw && w.part ? &a.out1 : &a.out0, col, 0);
+        if (!cut) leave(!w.dw ? &a.out0 : w.part ? &a.out2 : &a.out1, col, 0);
         if constexpr (KIND == kGrads) {
           left();
 #pragma unroll
@@ -354,69 +364,55 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
 }
 
 template <int KIND, int ACT>
-cudaError_t launch(Args& a, cudaStream_t st) {
-  a.tiles = a.m_tiles * a.n_tiles * a.splits * (KIND == kDw ? 2 : 1);
+cudaError_t launch(const Args& a, cudaStream_t st) {
   cudaError_t e = configure_once<ffn_tc_kernel<KIND, ACT>>(smem_of(KIND));
   if (e != cudaSuccess) return e;
-  const int pairs = a.tiles < sm_count() / 2 ? a.tiles : sm_count() / 2;
+  const int tiles = a.g[0].tiles + a.g[1].tiles;
+  const int pairs = tiles < sm_count() / 2 ? tiles : sm_count() / 2;
   e = launch_cluster_pdl(ffn_tc_kernel<KIND, ACT>, dim3(2 * pairs), dim3(threads_of(KIND)), smem_of(KIND), st, 2, a);
   count_launches(1);
   return e;
 }
 
 template <int KIND>
-cudaError_t launch_act(Args& a, int act, cudaStream_t st) {
+cudaError_t launch_act(const Args& a, int act, cudaStream_t st) {
   return act == kSilu   ? launch<KIND, kSilu>(a, st)
          : act == kGelu ? launch<KIND, kGelu>(a, st)
                         : launch<KIND, kGeluTanh>(a, st);
 }
 
-struct Plan {
-  int dx_splits, dw_splits;
-  size_t dact, partial;  // bytes
-};
+constexpr int kStep = 700;  // clocks of a pair for 64 terms
 
-Plan plan_of(int T, int C, int F) {
-  Plan p;
-  p.dx_splits = splits_of(ceil_div(T, 256) * ceil_div(C, 256), 2 * ceil_div(F, 64), 700, (double)T * C);
-  p.dw_splits = splits_of(2 * ceil_div(F, 256) * ceil_div(C, 256), ceil_div(T, 64), 700, 2.0 * F * C);
-  p.dact = align_up(2 * sizeof(__nv_bfloat16) * (size_t)T * F, 256);
-  const size_t x = p.dx_splits > 1 ? (size_t)p.dx_splits * T * C : 0;
-  const size_t w = p.dw_splits > 1 ? 2 * (size_t)p.dw_splits * F * C : 0;
-  p.partial = sizeof(float) * (x > w ? x : w);
-  return p;
+// a = x wg^T, u = x wu^T
+bool products(Args& a, const FfnGate& f) {
+  static_cast<Grids&>(a) = products_grid(f.T, f.C, f.F);
+  a.clear = 1;
+  return rows_map(&a.a, f.x, f.C, f.T, f.x_stride, 128) && rows_map(&a.b0, f.wg, f.C, f.F, f.C, 128) &&
+         rows_map(&a.b1, f.wu, f.C, f.F, f.C, 128);
 }
+
+size_t dact_bytes(int T, int F) { return align_up(2 * sizeof(__nv_bfloat16) * (size_t)T * F, 256); }
 
 }  // namespace
 
 size_t ffn_tc_backward_workspace(int T, int C, int F) {
-  const Plan p = plan_of(T, C, F);
-  return kHeaderBytes + p.dact + p.partial;
+  const Grids g = sums_grids(T, C, F, kStep);
+  return kHeaderBytes + dact_bytes(T, F) + sizeof(float) * (dx_parts(g) + dw_parts(g));
 }
 
 cudaError_t ffn_tc_forward(const FfnGate& f, void* ws, cudaStream_t st) {
   Args a{};
   a.hdr = static_cast<WorkspaceHeader*>(ws);
-  if (!rows_map(&a.a, f.x, f.C, f.T, f.x_stride, 128) || !rows_map(&a.b0, f.wg, f.C, f.F, f.C, 128) ||
-      !rows_map(&a.b1, f.wu, f.C, f.F, f.C, 128) || !rows_map(&a.out0, f.h, f.F, f.T, f.h_stride, 32))
-    return cudaErrorInvalidValue;
   a.codes = f.codes;
   a.exps = f.exps;
-  a.rows = f.T;
-  a.cols = f.F;
-  a.m_tiles = ceil_div(f.T, 256);
-  a.n_tiles = ceil_div(f.F, 128);
-  a.splits = 1;
-  a.steps = ceil_div(f.C, 64);
-  a.clear = 1;
+  if (!products(a, f) || !rows_map(&a.out0, f.h, f.F, f.T, f.h_stride, 32)) return cudaErrorInvalidValue;
   return launch_act<kForward>(a, f.act, st);
 }
 
 cudaError_t ffn_tc_backward(const FfnGate& f, void* ws, cudaStream_t st) {
-  const Plan plan = plan_of(f.T, f.C, f.F);
   char* at = static_cast<char*>(ws) + kHeaderBytes;
   __nv_bfloat16 *da = reinterpret_cast<__nv_bfloat16*>(at), *du = da + (size_t)f.T * f.F;
-  float* partial = reinterpret_cast<float*>(at + plan.dact);
+  float* parts = reinterpret_cast<float*>(at + dact_bytes(f.T, f.F));
   Args a{};
   a.hdr = static_cast<WorkspaceHeader*>(ws);
   cudaError_t e;
@@ -424,55 +420,27 @@ cudaError_t ffn_tc_backward(const FfnGate& f, void* ws, cudaStream_t st) {
     e = ffn_kept_grads(f, da, st);
     a.clear = 1;
   } else {
-    if (!rows_map(&a.a, f.x, f.C, f.T, f.x_stride, 128) || !rows_map(&a.b0, f.wg, f.C, f.F, f.C, 128) ||
-        !rows_map(&a.b1, f.wu, f.C, f.F, f.C, 128) || !rows_map(&a.dh, f.dh, f.F, f.T, f.dh_stride, 128) ||
+    if (!products(a, f) || !rows_map(&a.dh, f.dh, f.F, f.T, f.dh_stride, 128) ||
         !rows_map(&a.out0, da, f.F, f.T, f.F, 32) || !rows_map(&a.out1, du, f.F, f.T, f.F, 32))
       return cudaErrorInvalidValue;
-    a.rows = f.T;
-    a.cols = f.F;
-    a.m_tiles = ceil_div(f.T, 256);
-    a.n_tiles = ceil_div(f.F, 128);
-    a.splits = 1;
-    a.steps = ceil_div(f.C, 64);
-    a.clear = 1;
     e = launch_act<kGrads>(a, f.act, st);
     a.clear = 0;
   }
   if (e != cudaSuccess) return e;
 
-  a.cols = f.C;
-  a.n_tiles = ceil_div(f.C, 256);
-  // dx = [da | du] [wg; wu]
+  const Grids g = sums_grids(f.T, f.C, f.F, kStep);
+  static_cast<Grids&>(a) = g;
+  const int sx = g.g[0].splits, sw = g.g[1].splits;
   if (!rows_map(&a.a, da, f.F, f.T, f.F, 128, 2) || !rows_map(&a.b0, f.wg, f.C, f.F, f.C, 64) ||
-      !rows_map(&a.b1, f.wu, f.C, f.F, f.C, 64) ||
-      !(plan.dx_splits > 1 ? rows_map_f32(&a.out0, partial, f.C, f.T, f.C, plan.dx_splits)
-                           : rows_map(&a.out0, f.dx, f.C, f.T, f.dx_stride, 32)))
+      !rows_map(&a.b1, f.wu, f.C, f.F, f.C, 64) || !rows_map(&a.aw, da, f.F, f.T, f.F, 64, 2) ||
+      !rows_map(&a.bw, f.x, f.C, f.T, f.x_stride, 64) ||
+      !(sx > 1 ? rows_map_f32(&a.out0, parts, f.C, f.T, f.C, sx) : rows_map(&a.out0, f.dx, f.C, f.T, f.dx_stride, 32)) ||
+      !(sw > 1 ? rows_map_f32(&a.out1, parts + dx_parts(g), f.C, f.F, f.C, 2 * sw)
+               : rows_map(&a.out1, f.dwg, f.C, f.F, f.C, 32)) ||
+      !rows_map(&a.out2, f.dwu, f.C, f.F, f.C, 32))
     return cudaErrorInvalidValue;
-  a.rows = f.T;
-  a.m_tiles = ceil_div(f.T, 256);
-  a.splits = plan.dx_splits;
-  a.per = ceil_div(f.F, 64);
-  a.steps = 2 * a.per;
-  e = launch<kDx, kSilu>(a, st);
-  a.clear = 0;
-  if (e == cudaSuccess && a.splits > 1)
-    e = ffn_join(partial, f.dx, nullptr, f.dx_stride, f.T, 1, f.C, a.splits, f.dtype, st);
-  if (e != cudaSuccess) return e;
-
-  // dwg, dwu = [da; du]^T x
-  if (!rows_map(&a.a, da, f.F, f.T, f.F, 64, 2) || !rows_map(&a.b0, f.x, f.C, f.T, f.x_stride, 64) ||
-      !(plan.dw_splits > 1 ? rows_map_f32(&a.out0, partial, f.C, f.F, f.C, 2 * plan.dw_splits)
-                           : rows_map(&a.out0, f.dwg, f.C, f.F, f.C, 32)) ||
-      !rows_map(&a.out1, f.dwu, f.C, f.F, f.C, 32))
-    return cudaErrorInvalidValue;
-  a.rows = f.F;
-  a.m_tiles = ceil_div(f.F, 256);
-  a.splits = plan.dw_splits;
-  a.steps = ceil_div(f.T, 64);
-  e = launch<kDw, kSilu>(a, st);
-  if (e == cudaSuccess && a.splits > 1)
-    e = ffn_join(partial, f.dwg, f.dwu, f.C, f.F, 2, f.C, a.splits, f.dtype, st);
-  return e;
+  e = launch<kSums, kSilu>(a, st);
+  return e == cudaSuccess ? join_sums(f, g, parts, st) : e;
 }
 
 }  // namespace la

@@ -25,9 +25,11 @@ constexpr int S = 2;
 constexpr int kStageBytes = 6 * kTileBytes;  // A's three parts, B's three
 constexpr int kSmem = 1024 + S * kStageBytes + kWarps * kStore + 256;
 
-struct Args : Grid {
-  CUtensorMap a, b0, b1;  // operands' parts: [3][rows][cols]; a in kDx, kDw: [da, du][3]
-  CUtensorMap out0, out1;  // h; the parts of da, du; dx; dwg, dwu; out0 if the sum is cut: its parts
+struct Args : Grids {
+  CUtensorMap a, b0, b1;         // operands' parts: [3][rows][cols], of da, du [2][3][T][F]
+  CUtensorMap aw, bw;            // of dwg and dwu: da, du and x, both read along their rows
+  CUtensorMap out0, out1, out2;  // h; the parts of da, du; dx, dwg, dwu. Of cut sums their parts: out0
+                                 // [splits][T][C], out1 [2][splits][F][C]
   WorkspaceHeader* hdr;
   signed char* codes;
   unsigned char* exps;
@@ -75,7 +77,12 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc32_kernel(const __grid_cons
     prefetch_tensormap(&a.a);
     prefetch_tensormap(&a.b0);
     prefetch_tensormap(&a.out0);
-    if (KIND != kDw) prefetch_tensormap(&a.b1);
+    prefetch_tensormap(&a.b1);
+    if (KIND == kSums) {
+      prefetch_tensormap(&a.aw);
+      prefetch_tensormap(&a.bw);
+      prefetch_tensormap(&a.out1);
+    }
   }
   fence_before_sync();
   __syncthreads();
@@ -93,18 +100,19 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc32_kernel(const __grid_cons
       const uint32_t bars = cluster_map(smem_u32(full), 0);
       uint32_t s = 0, phase = 1;  // (a stage not used yet counts as emptied once)
       bool ok = true;
-      for (int t = cluster; t < a.tiles && ok; t += clusters) {
+      for (int t, i = 0; ok && (t = dealt<KIND>(a, cluster, clusters, i)) >= 0; ++i) {
         const Tile w = tile_of<KIND>(a, t);
-        const int row = w.m * 256 + (int)rank * 128, end = first_step<KIND>(a, w.split + 1);
-        for (int k = first_step<KIND>(a, w.split); k < end; ++k) {
+        const Grid& g = a.g[w.dw];
+        const int row = w.m * 256 + (int)rank * 128, end = first_step(g, w.split + 1);
+        for (int k = first_step(g, w.split); k < end; ++k) {
           if (!mbar_wait_abort(&empty[s], phase, abort, hdr, kSiteEmpty)) {
             ok = false;
             break;
           }
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
           const uint32_t bar = bars + 8 * s;
-          const int part = KIND == kDx && k >= a.per ? 1 : 0, kk = (k - part * a.per) * 64;
-          const CUtensorMap* mb = (DUAL ? rank != 0 : part != 0) ? &a.b1 : &a.b0;
+          const int part = KIND == kSums && !w.dw && k >= g.per ? 1 : 0, kk = (k - part * g.per) * 64;
+          const CUtensorMap* mb = w.dw ? &a.bw : (DUAL ? rank != 0 : part != 0) ? &a.b1 : &a.b0;
           uint8_t *ta = stages + s * kStageBytes, *tb = ta + 3 * kTileBytes;
 #pragma unroll
           for (int i = 0; i < 3; ++i, ta += kTileBytes, tb += kTileBytes) {
@@ -113,11 +121,11 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc32_kernel(const __grid_cons
               tma_load_3d_pair(tb, mb, bar, kk, w.n * 128, i);
             } else {
               const int col = w.n * 256 + (int)rank * 128;
-              if constexpr (KIND == kDx) {
+              if (!w.dw) {
                 tma_load_3d_pair(ta, &a.a, bar, kk, row, part * 3 + i);
               } else {
-                tma_load_3d_pair(ta, &a.a, bar, row, kk, w.part * 3 + i);
-                tma_load_3d_pair(ta + kTileBytes / 2, &a.a, bar, row + 64, kk, w.part * 3 + i);
+                tma_load_3d_pair(ta, &a.aw, bar, row, kk, w.part * 3 + i);
+                tma_load_3d_pair(ta + kTileBytes / 2, &a.aw, bar, row + 64, kk, w.part * 3 + i);
               }
               tma_load_3d_pair(tb, mb, bar, col, kk, i);
               tma_load_3d_pair(tb + kTileBytes / 2, mb, bar, col + 64, kk, i);
@@ -136,20 +144,23 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc32_kernel(const __grid_cons
   } else if (warp == kWarps + 1) {
     // ------------------------------------------------------------------ products
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t id = idesc_bf16(256, 256, KIND == kDw, !DUAL);
       const uint32_t at = smem_u32(stages);
-      const uint64_t da0 = KIND == kDw ? sdesc(at, kTileBytes / 2, 1024) : sdesc(at, 16, 1024);
+      const uint64_t da_k = sdesc(at, 16, 1024), da_m = sdesc(at, kTileBytes / 2, 1024);
       const uint64_t db0 = DUAL ? sdesc(at + 3 * kTileBytes, 16, 1024) : sdesc(at + 3 * kTileBytes, kTileBytes / 2, 1024);
-      constexpr uint32_t STEP_A = (KIND == kDw ? 2048 : 32) / 16, STEP_B = (DUAL ? 32 : 2048) / 16, PART = kTileBytes / 16;
+      constexpr uint32_t ALONG_K = 32 / 16, ALONG_MN = 2048 / 16, STEP_B = DUAL ? ALONG_K : ALONG_MN, PART = kTileBytes / 16;
       constexpr int ia[6] = {2, 0, 1, 1, 0, 0}, ib[6] = {0, 2, 1, 0, 1, 0};  // the smallest products first
       uint32_t s = 0, phase = 0, n = 0;
       bool ok = true;
-      for (int t = cluster; t < a.tiles && ok; t += clusters) {
-        int steps = a.steps;
-        if (!DUAL && a.splits > 1) {
-          const int split = tile_of<KIND>(a, t).split;
-          steps = first_step<KIND>(a, split + 1) - first_step<KIND>(a, split);
+      for (int t, i = 0; ok && (t = dealt<KIND>(a, cluster, clusters, i)) >= 0; ++i) {
+        int steps = a.g[0].steps, dw = 0;
+        if (!DUAL) {
+          const Tile w = tile_of<KIND>(a, t);
+          dw = w.dw;
+          steps = first_step(a.g[dw], w.split + 1) - first_step(a.g[dw], w.split);
         }
+        const uint64_t da0 = !DUAL && dw ? da_m : da_k;
+        const uint32_t step_a = !DUAL && dw ? ALONG_MN : ALONG_K;
+        const uint32_t id = !DUAL && dw ? idesc_bf16(256, 256, true, true) : idesc_bf16(256, 256, false, !DUAL);
         for (int k = 0; k < steps; ++k, ++n) {
           const uint32_t b = n & 1;
           if (n >= 2) ok = mbar_wait_abort(&acc_empty[b], (n / 2 - 1) & 1, abort, hdr, kSiteAccEmpty);
@@ -161,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc32_kernel(const __grid_cons
           for (int c = 0; c < 6; ++c)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              mma_ss_pair(tbase + 256 * b, da + ia[c] * PART + q * STEP_A, db + ib[c] * PART + q * STEP_B, id, (c | q) != 0);
+              mma_ss_pair(tbase + 256 * b, da + ia[c] * PART + q * step_a, db + ib[c] * PART + q * STEP_B, id, (c | q) != 0);
           mma_commit_pair(&empty[s]);
           mma_commit_pair(&acc_full[b]);
           if (++s == S) s = 0, phase ^= 1;
@@ -182,20 +193,21 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc32_kernel(const __grid_cons
     };
     uint32_t n = 0;
     bool ok = true;
-    for (int t = cluster; t < a.tiles && ok; t += clusters) {
+    for (int t, i = 0; ok && (t = dealt<KIND>(a, cluster, clusters, i)) >= 0; ++i) {
       const Tile w = tile_of<KIND>(a, t);
+      const Grid& g = a.g[w.dw];
       const int row0 = w.m * 256 + (int)rank * 128 + warp % 4 * 32, row = row0 + lane;
       // a thread's 128 sums of its row: 64 columns of a and the same of u, or 128 columns
       float v[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) v[j] = 0.f;
-      if (KIND == kGrads && row < a.rows) {  // the thread's piece of dh, into L2 while the sums are made
+      if (KIND == kGrads && row < g.rows) {  // the thread's piece of dh, into L2 while the sums are made
         const int col = w.n * 128 + 64 * half;
-        for (int j = 0; j < 64 && col + j < a.cols; j += 32)
+        for (int j = 0; j < 64 && col + j < g.cols; j += 32)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(a.dh + row * a.dh_stride + col + j));
       }
-      const int end = first_step<KIND>(a, w.split + 1);
-      for (int k = first_step<KIND>(a, w.split); k < end; ++k, ++n) {
+      const int end = first_step(g, w.split + 1);
+      for (int k = first_step(g, w.split); k < end; ++k, ++n) {
         const uint32_t b = n & 1;
         if (!mbar_wait_warp(&acc_full[b], n / 2 & 1, abort, hdr, kSiteAccFull)) {
           ok = false;
@@ -219,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc32_kernel(const __grid_cons
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (row0 < a.rows && col < a.cols) tma_store_3d(to, st, col, row0, mat);
+          if (row0 < g.rows && col < g.cols) tma_store_3d(to, st, col, row0, mat);
           bulk_commit();
         }
       };
@@ -236,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc32_kernel(const __grid_cons
         for (int c = 0; c < 2; ++c) {
           const int f = col0 + c * 32;
           if (a.codes != nullptr) {  // a thread has a block of 32 of a and of u
-            const int nb = q8::blocks_of(a.cols);
+            const int nb = q8::blocks_of(g.cols);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float* x = v + i * 64 + c * 32;
@@ -245,12 +257,12 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc32_kernel(const __grid_cons
               for (int j = 1; j < 31; j += 2) top = q8::top3(top, x[j], x[j + 1]);
               const uint32_t e = q8::step_of(__float_as_uint(q8::top3(top, x[31], x[31])));
               const float inv = q8::inverse_step(e);
-              if (row < a.rows && f < a.cols) {
+              if (row < g.rows && f < g.cols) {
                 const size_t r = 2 * (size_t)row + i;
-                signed char* to = a.codes + r * a.cols + f;
+                signed char* to = a.codes + r * g.cols + f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                  if (f + j * 8 < a.cols)
+                  if (f + j * 8 < g.cols)
                     *reinterpret_cast<uint2*>(to + j * 8) =
                         make_uint2(q8::codes4(x + j * 8, inv, e), q8::codes4(x + j * 8 + 4, inv, e));
                 a.exps[r * nb + f / q8::kBlock] = (unsigned char)e;
@@ -270,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc32_kernel(const __grid_cons
         auto ask = [&](int j0) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            next[i] = row < a.rows && col0 + j0 + 4 * i < a.cols ? __ldg(reinterpret_cast<const float4*>(dh + j0 + 4 * i))
+            next[i] = row < g.rows && col0 + j0 + 4 * i < g.cols ? __ldg(reinterpret_cast<const float4*>(dh + j0 + 4 * i))
                                                                  : make_float4(0.f, 0.f, 0.f, 0.f);
         };
         ask(0);
@@ -306,11 +318,10 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_tc32_kernel(const __grid_cons
             leave(&a.out0, col0, i * 3 + part);
           }
       } else {
-        const bool cut = a.splits > 1;
+        const bool cut = g.splits > 1;
+        const CUtensorMap* to = !w.dw ? &a.out0 : !cut && w.part ? &a.out2 : &a.out1;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          leave32(v + c * 32, !cut && KIND == kDw && w.part ? &a.out1 : &a.out0, col0 + c * 32,
-                  !cut ? 0 : KIND == kDw ? w.part * a.splits + w.split : w.split);
+        for (int c = 0; c < 4; ++c) leave32(v + c * 32, to, col0 + c * 32, cut ? w.part * g.splits + w.split : 0);
       }
     }
     if (lane == 0) bulk_wait_all<0>();
@@ -369,12 +380,10 @@ __global__ void __launch_bounds__(256) ffn_cut_kernel(const Cut c) {
 
 template <int KIND, int ACT>
 cudaError_t launch(Args& a, cudaStream_t st) {
-  a.m_tiles = ceil_div(a.rows, 256);
-  a.n_tiles = ceil_div(a.cols, KIND == kForward || KIND == kGrads ? 128 : 256);
-  a.tiles = a.m_tiles * a.n_tiles * a.splits * (KIND == kDw ? 2 : 1);
   cudaError_t e = configure_once<ffn_tc32_kernel<KIND, ACT>>(kSmem);
   if (e != cudaSuccess) return e;
-  const int pairs = a.tiles < sm_count() / 2 ? a.tiles : sm_count() / 2;
+  const int tiles = a.g[0].tiles + a.g[1].tiles;
+  const int pairs = tiles < sm_count() / 2 ? tiles : sm_count() / 2;
   e = launch_cluster_pdl(ffn_tc32_kernel<KIND, ACT>, dim3(2 * pairs), dim3(kThreads), kSmem, st, 2, a);
   count_launches(1);
   a.clear = 0;
@@ -390,11 +399,10 @@ cudaError_t launch_act(Args& a, int act, cudaStream_t st) {
 
 // The workspace: header, the parts of x, wg, wu, then (backward) of da, du, and of cut sums
 struct Plan {
-  int dx_splits, dw_splits;
-  size_t w, dact, partial, end;  // offsets in bytes
+  size_t w, dact, sums, end;  // offsets in bytes
 };
 
-constexpr int kStep = 6 * 550;  // clocks of 64 terms
+constexpr int kStep = 6 * 550;  // clocks of a pair for 64 terms
 
 Plan plan_of(int T, int C, int F, bool backward) {
   Plan p{};
@@ -402,12 +410,9 @@ Plan plan_of(int T, int C, int F, bool backward) {
   p.dact = p.w + align_up(12 * (size_t)F * C, 256);
   p.end = p.dact;
   if (!backward) return p;
-  p.dx_splits = splits_of(ceil_div(T, 256) * ceil_div(C, 256), 2 * ceil_div(F, 64), kStep, (double)T * C);
-  p.dw_splits = splits_of(2 * ceil_div(F, 256) * ceil_div(C, 256), ceil_div(T, 64), kStep, 2.0 * F * C);
-  p.partial = p.dact + align_up(12 * (size_t)T * F, 256);
-  const size_t x = p.dx_splits > 1 ? (size_t)p.dx_splits * T * C : 0;
-  const size_t w = p.dw_splits > 1 ? 2 * (size_t)p.dw_splits * F * C : 0;
-  p.end = p.partial + sizeof(float) * (x > w ? x : w);
+  const Grids g = sums_grids(T, C, F, kStep);
+  p.sums = p.dact + align_up(12 * (size_t)T * F, 256);
+  p.end = p.sums + sizeof(float) * (dx_parts(g) + dw_parts(g));
   return p;
 }
 
@@ -429,10 +434,7 @@ cudaError_t cut(const FfnGate& f, char* ws, const Plan& p, Parts& to, cudaStream
 
 // a = x wg^T, u = x wu^T
 bool products(Args& a, const FfnGate& f, const Parts& p) {
-  a.rows = f.T;
-  a.cols = f.F;
-  a.splits = 1;
-  a.steps = ceil_div(f.C, 64);
+  static_cast<Grids&>(a) = products_grid(f.T, f.C, f.F);
   a.clear = 1;
   return rows_map(&a.a, p.x, f.C, f.T, f.C, 128, 3) && rows_map(&a.b0, p.wg, f.C, f.F, f.C, 128, 3) &&
          rows_map(&a.b1, p.wu, f.C, f.F, f.C, 128, 3);
@@ -458,7 +460,7 @@ cudaError_t ffn_tc32_backward(const FfnGate& f, void* ws, cudaStream_t st) {
   const Plan plan = plan_of(f.T, f.C, f.F, true);
   char* at = static_cast<char*>(ws);
   __nv_bfloat16* dact = reinterpret_cast<__nv_bfloat16*>(at + plan.dact);  // [da, du][3][T][F]
-  float* partial = reinterpret_cast<float*>(at + plan.partial);
+  float* parts = reinterpret_cast<float*>(at + plan.sums);
   Parts p;
   cudaError_t e = cut(f, at, plan, p, st);
   if (e != cudaSuccess) return e;
@@ -475,35 +477,19 @@ cudaError_t ffn_tc32_backward(const FfnGate& f, void* ws, cudaStream_t st) {
   }
   if (e != cudaSuccess) return e;
 
-  a.cols = f.C;
-  // dx = [da | du] [wg; wu]
+  const Grids g = sums_grids(f.T, f.C, f.F, kStep);
+  static_cast<Grids&>(a) = g;
+  const int sx = g.g[0].splits, sw = g.g[1].splits;
   if (!rows_map(&a.a, dact, f.F, f.T, f.F, 128, 6) || !rows_map(&a.b0, p.wg, f.C, f.F, f.C, 64, 3) ||
-      !rows_map(&a.b1, p.wu, f.C, f.F, f.C, 64, 3) ||
-      !(plan.dx_splits > 1 ? rows_map_f32(&a.out0, partial, f.C, f.T, f.C, plan.dx_splits)
-                           : rows_map_f32(&a.out0, f.dx, f.C, f.T, f.dx_stride)))
+      !rows_map(&a.b1, p.wu, f.C, f.F, f.C, 64, 3) || !rows_map(&a.aw, dact, f.F, f.T, f.F, 64, 6) ||
+      !rows_map(&a.bw, p.x, f.C, f.T, f.C, 64, 3) ||
+      !(sx > 1 ? rows_map_f32(&a.out0, parts, f.C, f.T, f.C, sx) : rows_map_f32(&a.out0, f.dx, f.C, f.T, f.dx_stride)) ||
+      !(sw > 1 ? rows_map_f32(&a.out1, parts + dx_parts(g), f.C, f.F, f.C, 2 * sw)
+               : rows_map_f32(&a.out1, f.dwg, f.C, f.F, f.C)) ||
+      !rows_map_f32(&a.out2, f.dwu, f.C, f.F, f.C))
     return cudaErrorInvalidValue;
-  a.rows = f.T;
-  a.splits = plan.dx_splits;
-  a.per = ceil_div(f.F, 64);
-  a.steps = 2 * a.per;
-  e = launch<kDx, kSilu>(a, st);
-  if (e == cudaSuccess && a.splits > 1)
-    e = ffn_join(partial, f.dx, nullptr, f.dx_stride, f.T, 1, f.C, a.splits, f.dtype, st);
-  if (e != cudaSuccess) return e;
-
-  // dwg, dwu = [da; du]^T x
-  if (!rows_map(&a.a, dact, f.F, f.T, f.F, 64, 6) || !rows_map(&a.b0, p.x, f.C, f.T, f.C, 64, 3) ||
-      !(plan.dw_splits > 1 ? rows_map_f32(&a.out0, partial, f.C, f.F, f.C, 2 * plan.dw_splits)
-                           : rows_map_f32(&a.out0, f.dwg, f.C, f.F, f.C)) ||
-      !rows_map_f32(&a.out1, f.dwu, f.C, f.F, f.C))
-    return cudaErrorInvalidValue;
-  a.rows = f.F;
-  a.splits = plan.dw_splits;
-  a.steps = ceil_div(f.T, 64);
-  e = launch<kDw, kSilu>(a, st);
-  if (e == cudaSuccess && a.splits > 1)
-    e = ffn_join(partial, f.dwg, f.dwu, f.C, f.F, 2, f.C, a.splits, f.dtype, st);
-  return e;
+  e = launch<kSums, kSilu>(a, st);
+  return e == cudaSuccess ? join_sums(f, g, parts, st) : e;
 }
 
 }  // namespace la
