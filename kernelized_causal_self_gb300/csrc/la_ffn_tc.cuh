@@ -5,6 +5,7 @@
 #include "la_checkpoint.cuh"
 #include "la_ffn.cuh"
 #include "la_internal.h"
+#include "la_pair.cuh"
 #include "la_tc_common.cuh"
 
 namespace la {

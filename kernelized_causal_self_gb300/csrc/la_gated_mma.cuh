@@ -5,6 +5,7 @@
 
 #include "la_gated.cuh"
 #include "la_mma.cuh"
+#include "la_pair.cuh"
 #include "la_tc_common.cuh"
 
 namespace la {

@@ -12,6 +12,7 @@
 // by a second kernel (no atomics: results repeat bit for bit). Everything is float32, rounded once.
 #include "la_checkpoint.cuh"
 #include "la_internal.h"
+#include "la_pair.cuh"
 #include "la_tc_common.cuh"
 
 namespace la {

@@ -4,8 +4,6 @@
 
 #include <cuda_bf16.h>
 
-#include <atomic>
-
 #include "la_common.cuh"
 #include "la_internal.h"
 #include "la_tc.cuh"
@@ -495,21 +493,6 @@ inline cudaError_t configure(K kernel, int smem) {
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                               (int)cudaSharedmemCarveoutMaxShared);
-}
-
-// configure, once per kernel and device (its two calls of the runtime cost as much as a
-// launch). The mask is the library's own state, as its launch count is.
-template <auto KERNEL>
-cudaError_t configure_once(int smem) {
-  static std::atomic<unsigned long long> done{0};
-  int device = 0;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = device < 64 ? 1ull << device : 0;
-  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  e = configure(KERNEL, smem);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-  return e;
 }
 
 // CTAs of `kernel` that fit on one SM (at least 1): the larger of the runtime's

@@ -2,7 +2,7 @@
 // run time via the runtime API, so the library does not link libcuda).
 #include <cudaTypedefs.h>
 
-#include "la_tc.cuh"
+#include "la_pair.cuh"
 
 namespace la {
 namespace {
