@@ -27,9 +27,9 @@ using namespace ffn;
 // one more warp that copies, one that multiplies, kGrads: one that copies dh
 constexpr int threads_of(int kind) { return 32 * (kWarps + (kind == kGrads ? 3 : 2)); }
 constexpr int kStageBytes = 2 * kTileBytes;
-constexpr int stages_of(int kind) { return kind == kGrads ? 5 : 6; }
+constexpr int stages_of(int kind) { return kind == kGrads ? 4 : 6; }
 constexpr int smem_of(int kind) {
-  return 1024 + stages_of(kind) * kStageBytes + kWarps * kStore + (kind == kGrads ? 2 * kTileBytes : 0) + 256;
+  return 1024 + stages_of(kind) * kStageBytes + kWarps * kStore + (kind == kGrads ? 4 * kTileBytes : 0) + 256;
 }
 
 struct Args : Grids {
@@ -51,15 +51,16 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
   extern __shared__ uint8_t smraw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
   uint8_t* stages = sm;                                  // [stage][A | B]
-  uint8_t* dht = stages + S * kStageBytes;               // kGrads: dh's tile, two blocks of 64 columns
-  uint8_t* staging = dht + (KIND == kGrads ? 2 * kTileBytes : 0);
+  uint8_t* dht = stages + S * kStageBytes;               // kGrads: dh's tiles, two in turn, each two
+                                                         // blocks of 64 columns
+  uint8_t* staging = dht + (KIND == kGrads ? 4 * kTileBytes : 0);
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + kWarps * kStore);  // S (the even CTA's count)
   uint64_t* empty = full + S;                            // S: the MMAs are done with the stage
   uint64_t* acc_full = empty + S;                        // 2: an accumulator holds its tile
   uint64_t* acc_empty = acc_full + 2;                    // 2 (the even CTA's): both CTAs have read it
-  uint64_t* dh_full = acc_empty + 2;
-  uint64_t* dh_empty = dh_full + 1;
-  uint64_t* drain = dh_empty + 1;
+  uint64_t* dh_full = acc_empty + 2;                     // 2
+  uint64_t* dh_empty = dh_full + 2;                      // 2: du, which took dh's place, has left
+  uint64_t* drain = dh_empty + 2;
   volatile int* abort = reinterpret_cast<volatile int*>(drain + 1);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1) + 1;
 
@@ -74,9 +75,9 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 2 * kWarps);
+      mbar_init(&dh_full[b], 1);
+      mbar_init(&dh_empty[b], kWarps);
     }
-    mbar_init(dh_full, 1);
-    mbar_init(dh_empty, kWarps);
     mbar_init(drain, 1);
     *abort = 0;
     fence_mbar_init();
@@ -167,14 +168,16 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
       for (int t; (t = dealt<KIND>(a, cluster, clusters, nt)) >= 0;) {
         const Tile w = tile_of<KIND>(a, t);
         const int row = w.m * 256 + (int)rank * 128;
-        if (nt > 0) ok = mbar_wait_abort(dh_empty, (uint32_t)((nt - 1) & 1), abort, hdr, kSiteDhEmpty);
+        const int b = nt & 1;
+        if (nt >= 2) ok = mbar_wait_abort(&dh_empty[b], (uint32_t)((nt / 2 - 1) & 1), abort, hdr, kSiteDhEmpty);
         if (!ok) break;
-        mbar_arrive_expect_tx(dh_full, 2 * kTileBytes);
-        tma_load_3d(dht, &a.dh, dh_full, w.n * 128, row, 0);
-        tma_load_3d(dht + kTileBytes, &a.dh, dh_full, w.n * 128 + 64, row, 0);
+        mbar_arrive_expect_tx(&dh_full[b], 2 * kTileBytes);
+        tma_load_3d(dht + 2 * b * kTileBytes, &a.dh, &dh_full[b], w.n * 128, row, 0);
+        tma_load_3d(dht + (2 * b + 1) * kTileBytes, &a.dh, &dh_full[b], w.n * 128 + 64, row, 0);
         ++nt;
       }
-      if (nt > 0 && !mbar_wait(dh_full, (uint32_t)((nt - 1) & 1))) record_timeout(hdr, kSiteDrain);
+      for (int t = nt > 2 ? nt - 2 : 0; t < nt; ++t)
+        if (!mbar_wait(&dh_full[t & 1], (uint32_t)(t / 2 & 1))) record_timeout(hdr, kSiteDrain);
     }
     __syncwarp();
   } else if (warp == kWarps + 1) {
@@ -227,7 +230,6 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
     uint8_t* mine = staging + warp * kStore;
     const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
     const uint32_t freed = cluster_map(smem_u32(acc_empty), 0);
-    const int trow = warp % 4 * 32 + lane;  // of the CTA's 128
     constexpr int GROUPS = DUAL ? 1 : 2;    // of 64 columns
     int nt = 0;
     for (int t; (t = dealt<KIND>(a, cluster, clusters, nt)) >= 0; ++nt) {
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
       const Grid& grid = a.g[w.dw];
       const int b = nt & 1, row0 = w.m * 256 + (int)rank * 128 + warp % 4 * 32, row = row0 + lane;
       if (!mbar_wait_warp(&acc_full[b], (uint32_t)((nt / 2) & 1), abort, hdr, kSiteAccFull)) break;
-      if (KIND == kGrads && !mbar_wait_warp(dh_full, (uint32_t)(nt & 1), abort, hdr, kSiteDhFull)) break;
+      if (KIND == kGrads && !mbar_wait_warp(&dh_full[b], (uint32_t)(nt / 2 & 1), abort, hdr, kSiteDhFull)) break;
       fence_after_sync();
       const uint32_t d = tbase + 256 * b + lanes;
 #pragma unroll 1
@@ -243,12 +245,16 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
         const int col = w.n * (DUAL ? 128 : 256) + g * 64;
         const bool cut = !DUAL && grid.splits > 1;
         uint8_t* st = mine;
-        uint32_t gu[KIND == kGrads ? 32 : 1];  // du, which follows da through the staging tile
+        // kGrads: the warp's 32 rows of dh's block, where du takes dh's place, value by value
+        uint8_t* dut = dht + (2 * b + g) * kTileBytes + warp % 4 * kStore;
         auto leave = [&](const CUtensorMap* to, int from, int mat) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (row0 < grid.rows && from < grid.cols) tma_store_3d(to, st, from, row0, mat);
+            if (row0 < grid.rows && from < grid.cols) {
+              tma_store_3d(to, st, from, row0, mat);
+              if (KIND == kGrads) tma_store_3d(&a.out1, dut, from, row0, mat);
+            }
             bulk_commit();
           }
         };
@@ -257,6 +263,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
           __syncwarp();
         };
         if (!cut) left();
+        if (KIND == kGrads && nt > 0 && lane == 0) mbar_arrive(&dh_empty[b ^ 1]);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {  // 32 columns
           uint32_t p[32], q[32];
@@ -301,9 +308,9 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const uint32_t at = sw128(lane, c * 64 + e * 16);
-                const uint4 v = *reinterpret_cast<const uint4*>(dht + g * kTileBytes + sw128(trow, c * 64 + e * 16));
+                const uint4 v = *reinterpret_cast<const uint4*>(dut + at);
                 const uint32_t dh[4] = {v.x, v.y, v.z, v.w};
-                uint32_t oa[4];
+                uint32_t oa[4], ou[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   const int j = e * 8 + i * 2;
@@ -312,9 +319,10 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
                   act_grad2<ACT>(make_float2(fa[j], fa[j + 1]), f, df);
                   const float2 da = mul2(mul2(dv, make_float2(fu[j], fu[j + 1])), df), du = mul2(dv, f);
                   oa[i] = pack_bf16(da.x, da.y);
-                  gu[c * 16 + e * 4 + i] = pack_bf16(du.x, du.y);
+                  ou[i] = pack_bf16(du.x, du.y);
                 }
                 *reinterpret_cast<uint4*>(st + at) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+                *reinterpret_cast<uint4*>(dut + at) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
               }
             }
           } else {
@@ -335,22 +343,12 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) ffn_tc_kernel(const __gri
             }
           }
         }
-        if (g % GROUPS == GROUPS - 1) {  // the accumulator (and dh's tile) may be written again
+        if (g % GROUPS == GROUPS - 1) {  // the accumulator may be written again
           fence_before_sync();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive_cluster(freed + 8 * b);
-            if (KIND == kGrads) mbar_arrive(dh_empty);
-          }
+          if (lane == 0) mbar_arrive_cluster(freed + 8 * b);
         }
         if (!cut) leave(!w.dw ? &a.out0 : w.part ? &a.out2 : &a.out1, col, 0);
-        if constexpr (KIND == kGrads) {
-          left();
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<uint4*>(st + sw128(lane, e * 16)) = make_uint4(gu[4 * e], gu[4 * e + 1], gu[4 * e + 2], gu[4 * e + 3]);
-          leave(&a.out1, col, 0);
-        }
       }
     }
     if (lane == 0) bulk_wait_all<0>();
