@@ -365,8 +365,8 @@ int la_debug_noalloc_set_status(int status, int wait_site, void* stream);
 
 /*
  * la_workspace_status -- synchronises `stream` and reads the status word a
- * previous la_forward / la_prefill / la_extend / la_backward / la_extend_gated
- * left in `workspace`: LA_OK; LA_ERR_TIMEOUT if a bounded wait inside a kernel
+ * previous la_forward / la_prefill / la_extend / la_backward / la_extend_gated, or
+ * la_ffn_gate / la_ffn_gate_backward that needs a workspace, left in `workspace`: LA_OK; LA_ERR_TIMEOUT if a bounded wait inside a kernel
  * (for a TMA copy or a group of tensor-core MMAs) gave up, the outputs of that
  * call then being invalid; LA_ERR_INVALID_ARG if la_extend or la_extend_gated met
  * a slot outside its pool. Clears the word. Debug / test use.
@@ -557,7 +557,7 @@ size_t la_ffn_gate_backward_workspace_bytes(int T, int C, int F, int dtype);
  * product: h = act(a) * u with a = x wg^T and u = x wu^T. x: T rows of C; wg, wu [F][C]
  * contiguous; h: T rows of F. act: enum la_activation. T <= 2^24. codes [T][2][F], exps
  * [T][2][ceil(F / 32)]: a checkpoint of a and u to be written, or nullptr both. Outputs share no
- * memory with inputs.
+ * memory with inputs. In float32 a row with an infinity may give NaN where an infinity is due.
  */
 int la_ffn_gate(const void* x, long long x_stride, const void* wg, const void* wu, void* h, long long h_stride,
                 signed char* codes, unsigned char* exps, int T, int C, int F, int act, int dtype, void* workspace,

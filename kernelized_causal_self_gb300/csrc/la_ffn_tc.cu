@@ -15,6 +15,11 @@
 // Results go through a swizzled staging tile of 32 rows a warp and leave by TMA, which clips
 // what is past the matrix; copies past its edge read zeros, so ragged sizes need no masks.
 // Sums with few tiles are cut along k (float32 parts, added in order by a second kernel).
+//
+// Bound by the tensor cores, and by shared memory's bandwidth where a value's results are many
+// (operands alone take most of it). T 65536, C 512, F 1408: h in 115 us (1640 TFLOP/s; 131 under the
+// power limit), da and du in 148, dx, dwg and dwu in 232 (1630 TFLOP/s); T 4096, C 2048, F 5632: h in 105
+// to 113, 128 with a checkpoint.
 #include <cuda_bf16.h>
 
 #include "la_ffn_tc.cuh"
