@@ -1301,7 +1301,7 @@ def la_layer_norm(x, w, b=None, eps=1e-5, out=None, checkpoint=None):
         _expect(fn, "out", out, shape, dtype)
         old = _token_rows(fn, "out", out)[1]
         _on(index, whole, (out,))
-    _call(fn, index, x.data_ptr(), ld, w.data_ptr(), bp, out.data_ptr(), old, cp, ep, rows, C, eps, dt)
+    _call(fn, index, x.data_ptr(), ld, w.data_ptr(), bp, out.data_ptr(), old, cp, ep, rows, C, float(eps), dt)
     return out
 
 
@@ -1346,7 +1346,7 @@ def la_layer_norm_backward(x, w, dy, eps=1e-5, dx=None, dw=None, db=None, worksp
     db = torch.empty_like(w) if db is None else db
     ws, nbytes = _scratch(dy, _bytes("la_layer_norm_workspace_bytes", rows, C), workspace)
     _call(fn, index, xp, ld, cp, ep, w.data_ptr(), dy.data_ptr(), dyld, dx.data_ptr(), dxld, dw.data_ptr(),
-          db.data_ptr(), rows, C, eps, dt, ws.data_ptr(), nbytes)
+          db.data_ptr(), rows, C, float(eps), dt, ws.data_ptr(), nbytes)
     return dx, dw, db
 
 

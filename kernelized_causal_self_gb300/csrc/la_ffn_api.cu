@@ -45,17 +45,32 @@ bool kept_ok(const void* codes, const void* exps, bool needed) {
   return codes != nullptr ? aligned(codes, 16) : !needed;
 }
 
+// `rows` rows of `width` bytes, `stride` bytes apart
 struct Span {
   const void* p;
-  size_t bytes;
+  size_t width, stride, rows;
 };
 
-// Whether memory that is written is also another argument's.
+Span span(const void* p, size_t bytes) { return {p, bytes, bytes, bytes > 0 ? 1u : 0u}; }
+
+Span span(const void* p, long long rows, long long stride, int n, int dtype) {
+  return {p, size_of(dtype) * n, size_of(dtype) * (size_t)stride, (size_t)rows};
+}
+
+bool meet(const Span& a, const Span& b) {
+  if (a.p == nullptr || b.p == nullptr || a.rows == 0 || b.rows == 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  if (x >= y + (b.rows - 1) * b.stride + b.width || y >= x + (a.rows - 1) * a.stride + a.width) return false;
+  // rows equally far apart, each in columns of its own of one buffer
+  if (a.rows > 1 && b.rows > 1 && a.stride == b.stride) {
+    const uintptr_t at = y >= x ? (y - x) % a.stride : a.stride - 1 - (x - y - 1) % a.stride;
+    return at < a.width || at + b.width > a.stride;
+  }
+  return true;
+}
+
+// Whether memory that is written is no other argument's.
 bool apart(std::initializer_list<Span> written, std::initializer_list<Span> read) {
-  auto meet = [](const Span& a, const Span& b) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return a.p != nullptr && b.p != nullptr && a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
-  };
   for (const Span& w : written) {
     for (const Span& r : read)
       if (meet(w, r)) return false;
@@ -63,10 +78,6 @@ bool apart(std::initializer_list<Span> written, std::initializer_list<Span> read
       if (&o != &w && meet(w, o)) return false;
   }
   return true;
-}
-
-size_t span(long long rows, long long stride, int n, int dtype) {
-  return rows > 0 ? size_of(dtype) * ((size_t)(rows - 1) * stride + n) : 0;
 }
 
 size_t exps_of(int n) { return (size_t)(n + 31) / 32; }
@@ -96,7 +107,7 @@ int la_checkpoint(const void* x, long long x_stride, signed char* codes, unsigne
   if (!rows_ok(rows, C, dtype)) return LA_ERR_INVALID_ARG;
   if (rows == 0) return LA_OK;
   if (!ptrs_ok({x}) || !stride_ok(x_stride, C, dtype) || !kept_ok(codes, exps, true) ||
-      !apart({{codes, (size_t)rows * C}, {exps, (size_t)rows * exps_of(C)}}, {{x, span(rows, x_stride, C, dtype)}}))
+      !apart({span(codes, (size_t)rows * C), span(exps, (size_t)rows * exps_of(C))}, {span(x, rows, x_stride, C, dtype)}))
     return LA_ERR_INVALID_ARG;
   const la::Checkpoint c{const_cast<void*>(x), codes, exps, rows, x_stride, C, dtype};
   return from_cuda(la::checkpoint_pack(c, as_stream(stream)));
@@ -107,7 +118,7 @@ int la_checkpoint_restore(const signed char* codes, const unsigned char* exps, v
   if (!rows_ok(rows, C, dtype)) return LA_ERR_INVALID_ARG;
   if (rows == 0) return LA_OK;
   if (!ptrs_ok({x}) || !stride_ok(x_stride, C, dtype) || !kept_ok(codes, exps, true) ||
-      !apart({{x, span(rows, x_stride, C, dtype)}}, {{codes, (size_t)rows * C}, {exps, (size_t)rows * exps_of(C)}}))
+      !apart({span(x, rows, x_stride, C, dtype)}, {span(codes, (size_t)rows * C), span(exps, (size_t)rows * exps_of(C))}))
     return LA_ERR_INVALID_ARG;
   const la::Checkpoint c{x, const_cast<signed char*>(codes), const_cast<unsigned char*>(exps), rows, x_stride, C, dtype};
   return from_cuda(la::checkpoint_restore(c, as_stream(stream)));
@@ -121,11 +132,12 @@ int la_layer_norm(const void* x, long long x_stride, const void* w, const void* 
   if (!ptrs_ok({x, w, y}) || !aligned(b, 16) || !stride_ok(x_stride, C, dtype) || !stride_ok(y_stride, C, dtype) ||
       !kept_ok(codes, exps, false))
     return LA_ERR_INVALID_ARG;
-  const size_t e = size_of(dtype) * C, xs = span(rows, x_stride, C, dtype), ys = span(rows, y_stride, C, dtype);
+  const size_t e = size_of(dtype) * C;
+  const Span xs = span(x, rows, x_stride, C, dtype), ys = span(y, rows, y_stride, C, dtype), none = span(nullptr, 0);
   // y may be x itself: a row is in registers before it is written
   const bool itself = y == x && y_stride == x_stride;
-  if (!apart({{y, ys}, {codes, (size_t)rows * C}, {exps, (size_t)rows * exps_of(C)}}, {{w, e}, {b, e}}) ||
-      !apart({{itself ? nullptr : y, ys}, {codes, (size_t)rows * C}, {exps, (size_t)rows * exps_of(C)}}, {{x, xs}}))
+  if (!apart({ys, span(codes, (size_t)rows * C), span(exps, (size_t)rows * exps_of(C))}, {span(w, e), span(b, e)}) ||
+      !apart({itself ? none : ys, span(codes, (size_t)rows * C), span(exps, (size_t)rows * exps_of(C))}, {xs}))
     return LA_ERR_INVALID_ARG;
   la::LayerNorm n{};
   n.x = x;
@@ -156,7 +168,7 @@ int la_layer_norm_backward(const void* x, long long x_stride, const signed char*
   cudaStream_t st = as_stream(stream);
   const size_t e = size_of(dtype) * C;
   if (rows == 0) {
-    if (!apart({{dw, e}, {db, e}}, {})) return LA_ERR_INVALID_ARG;
+    if (!apart({span(dw, e), span(db, e)}, {})) return LA_ERR_INVALID_ARG;
     const cudaError_t r = cudaMemsetAsync(dw, 0, e, st);
     return from_cuda(r == cudaSuccess ? cudaMemsetAsync(db, 0, e, st) : r);
   }
@@ -164,13 +176,13 @@ int la_layer_norm_backward(const void* x, long long x_stride, const signed char*
       !aligned(x, 16) || (x != nullptr && !stride_ok(x_stride, C, dtype)) || !stride_ok(dy_stride, C, dtype) ||
       !stride_ok(dx_stride, C, dtype))
     return LA_ERR_INVALID_ARG;
-  const size_t xs = x ? span(rows, x_stride, C, dtype) : 0, ys = span(rows, dy_stride, C, dtype),
-               ds = span(rows, dx_stride, C, dtype);
+  const Span xs = span(x, rows, x_stride, C, dtype), ys = span(dy, rows, dy_stride, C, dtype),
+             ds = span(dx, rows, dx_stride, C, dtype), none = span(nullptr, 0);
   // dx may be x or dy itself, as y may be x
   const bool is_x = dx == x && dx_stride == x_stride, is_dy = dx == dy && dx_stride == dy_stride;
-  if (!apart({{dx, ds}, {dw, e}, {db, e}}, {{w, e}, {codes, (size_t)rows * C}, {exps, (size_t)rows * exps_of(C)},
-                                            {is_x ? nullptr : x, xs}, {is_dy ? nullptr : dy, ys}}) ||
-      !apart({{dw, e}, {db, e}}, {{x, xs}, {dy, ys}}))
+  if (!apart({ds, span(dw, e), span(db, e)}, {span(w, e), span(codes, (size_t)rows * C), span(exps, (size_t)rows * exps_of(C)),
+                                            is_x ? none : xs, is_dy ? none : ys}) ||
+      !apart({span(dw, e), span(db, e)}, {xs, ys}))
     return LA_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < la::layer_norm_workspace(rows, C))
     return LA_ERR_WORKSPACE;
@@ -212,8 +224,8 @@ int la_ffn_gate(const void* x, long long x_stride, const void* wg, const void* w
       !kept_ok(codes, exps, false))
     return LA_ERR_INVALID_ARG;
   const size_t w = size_of(dtype) * C * F, kept = 2 * (size_t)T;
-  if (!apart({{h, span(T, h_stride, F, dtype)}, {codes, kept * F}, {exps, kept * exps_of(F)}},
-             {{x, span(T, x_stride, C, dtype)}, {wg, w}, {wu, w}}))
+  if (!apart({span(h, T, h_stride, F, dtype), span(codes, kept * F), span(exps, kept * exps_of(F))},
+             {span(x, T, x_stride, C, dtype), span(wg, w), span(wu, w)}))
     return LA_ERR_INVALID_ARG;
   const size_t need = ffn_workspace(T, C, F, codes != nullptr, dtype);
   if (need > 0 && (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < need))
@@ -245,16 +257,16 @@ int la_ffn_gate_backward(const void* x, long long x_stride, const void* wg, cons
   cudaStream_t st = as_stream(stream);
   const size_t w = size_of(dtype) * C * F, kept = 2 * (size_t)T;
   if (T == 0) {
-    if (!apart({{dwg, w}, {dwu, w}}, {})) return LA_ERR_INVALID_ARG;
+    if (!apart({span(dwg, w), span(dwu, w)}, {})) return LA_ERR_INVALID_ARG;
     const cudaError_t e = cudaMemsetAsync(dwg, 0, w, st);
     return from_cuda(e == cudaSuccess ? cudaMemsetAsync(dwu, 0, w, st) : e);
   }
   if (!ptrs_ok({x, wg, wu, dh, dx}) || !stride_ok(x_stride, C, dtype) || !stride_ok(dh_stride, F, dtype) ||
       !stride_ok(dx_stride, C, dtype) || !kept_ok(codes, exps, false))
     return LA_ERR_INVALID_ARG;
-  if (!apart({{dx, span(T, dx_stride, C, dtype)}, {dwg, w}, {dwu, w}},
-             {{x, span(T, x_stride, C, dtype)}, {wg, w}, {wu, w}, {dh, span(T, dh_stride, F, dtype)},
-              {codes, kept * F}, {exps, kept * exps_of(F)}}))
+  if (!apart({span(dx, T, dx_stride, C, dtype), span(dwg, w), span(dwu, w)},
+             {span(x, T, x_stride, C, dtype), span(wg, w), span(wu, w), span(dh, T, dh_stride, F, dtype),
+              span(codes, kept * F), span(exps, kept * exps_of(F))}))
     return LA_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < ffn_backward_workspace(T, C, F, dtype))
     return LA_ERR_WORKSPACE;

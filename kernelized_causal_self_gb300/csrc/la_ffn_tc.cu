@@ -2,9 +2,9 @@
 // the backward pass da = dh u act'(a), du = dh act(a), dx = da wg + du wu, dwg = da^T x,
 // dwu = du^T x (da and du in bf16, in the workspace).
 //
-// One persistent kernel for all five products (in two launches, dx and the weights' in one). A pair of CTAs (cta_group::2) makes a tile of
-// 256 x 256: each CTA copies its 128 rows of A and its half of B's 256 rows by TMA, 64 terms
-// of the sum a stage, the even one issues the MMAs, and each finds its 128 x 256 of D in its
+// One persistent kernel for all five products (in two launches, dx and the weights' in one). A
+// pair of CTAs (cta_group::2) makes a tile of 256 x 256: each CTA copies its 128 rows of A and its
+// half of B's 256 rows by TMA, 64 terms of the sum a stage, the even one issues the MMAs, and each finds its 128 x 256 of D in its
 // own tensor memory, where two accumulators take turns, so that eight warps write one tile's
 // results while the next is summed.
 //   kForward, kGrads  A = x, B = 128 rows of wg (even CTA) and the same rows of wu (odd CTA): a
@@ -42,11 +42,11 @@ struct Args : Grids {
   CUtensorMap aw, bw;            // of dwg and dwu: da, du and x, both read along their rows
   CUtensorMap out0, out1, out2;  // h; da, du; dx, dwg, dwu. Of cut sums their parts in float32: out0
                                  // [splits][T][C], out1 [2][splits][F][C]
-  CUtensorMap dh;           // kGrads
+  CUtensorMap dh;                // kGrads
   WorkspaceHeader* hdr;
-  signed char* codes;       // kForward: a checkpoint of a, u
+  signed char* codes;            // kForward: a checkpoint of a, u
   unsigned char* exps;
-  int clear;                // the call's first kernel clears the status header
+  int clear;                     // the call's first kernel clears the status header
 };
 
 template <int KIND, int ACT>

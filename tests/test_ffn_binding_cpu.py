@@ -127,6 +127,9 @@ def test_abi_layer_norm(lib):
     assert fwd(eps=-1e-5) == bad and fwd(eps=float("nan")) == bad
     assert fwd(xs=63) == bad and fwd(ys=56) == bad and fwd(ys=68) == bad
     assert fwd(codes=FAR[4]) == bad and fwd(exps=FAR[4]) == bad
+    # columns of one buffer: refused only where they meet
+    assert fwd(xs=192, y=FAR[0] + 256, ys=192, w=0) == bad and fwd(xs=192, y=FAR[0] + 64, ys=192) == bad
+    assert fwd(xs=192, y=FAR[0] + 320, ys=192) == bad and fwd(x=FAR[0] + 64, xs=192, y=FAR[0], ys=192) == bad
     assert fwd(y=FAR[0], ys=128) == bad and fwd(y=FAR[0] + 128) == bad and fwd(y=FAR[1]) == bad
     assert fwd(codes=FAR[0], exps=FAR[5]) == bad and fwd(codes=FAR[3], exps=FAR[5]) == bad
     assert fwd(rows=0, x=0) == la.LA_OK

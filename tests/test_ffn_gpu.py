@@ -418,6 +418,55 @@ def test_ffn_rows_that_are_not_finite_stay_alone(la, T, dtype):
     assert big.isfinite().all()
 
 
+@TYPES
+def test_columns_of_one_buffer(la, dtype):
+    """Inputs and outputs may be columns of one buffer, which share no memory."""
+    T, C, F = 70, 72, 136
+    x, wg, wu, dh = _ffn_inputs(T, C, F, dtype)
+    w = _randn(9, C, dtype=dtype)
+    buf = torch.full((T, 2 * C + 2 * F), 2.0, dtype=dtype, device=DEV)
+    xv, yv, hv, dhv = buf[:, :C], buf[:, C:2 * C], buf[:, 2 * C:2 * C + F], buf[:, 2 * C + F:]
+    xv.copy_(x)
+    dhv.copy_(dh)
+    y = la.la_layer_norm(x, w)
+    h = la.la_ffn_gate(y, wg, wu)
+    la.la_layer_norm(xv, w, out=yv)
+    la.la_ffn_gate(yv, wg, wu, out=hv)
+    want = la.la_ffn_gate_backward(y, wg, wu, dh)
+    got = la.la_ffn_gate_backward(yv, wg, wu, dhv, dx=xv)
+    for p, q in ((yv, y), (hv, h), (dhv, dh), *zip(got, want)):
+        assert torch.equal(p, q)
+
+
+def test_more_elements_than_32_bits_count(la):
+    """270000 rows of 8192: the last rows' results are those of the rows alone, bit for bit."""
+    T, C, F, n = 270000, 64, 8192, 300
+    x, wg, wu, _ = _ffn_inputs(T, C, F, BF)
+    last = x[-n:].contiguous()
+    pair, own = _kept_like(T, 2, F), _kept_like(n, 2, F)
+    h, hl = la.la_ffn_gate(x, wg, wu, checkpoint=pair), la.la_ffn_gate(last, wg, wu, checkpoint=own)
+    assert h.numel() > 2 ** 31 and torch.equal(h[-n:], hl)
+    assert torch.equal(pair[0][-n:], own[0]) and torch.equal(pair[1][-n:], own[1])
+    for kept, kl in ((None, None), (pair, own)):
+        grads, gl = la.la_ffn_gate_backward(x, wg, wu, h, checkpoint=kept), la.la_ffn_gate_backward(last, wg, wu, hl, checkpoint=kl)
+        # (dx's sums may be cut at other places)
+        _norm2(grads[0][-n:], _f64(gl[0]), HALF[BF], "dx")
+        del grads
+    w, b = _randn(8, F, dtype=BF), _randn(9, F, dtype=BF)
+    del pair
+    pair = _kept_like(T, F)
+    y = la.la_layer_norm(h, w, b, checkpoint=pair)
+    kl = la.la_checkpoint(hl)
+    assert torch.equal(y[-n:], la.la_layer_norm(hl, w, b))
+    assert torch.equal(pair[0][-n:], kl[0]) and torch.equal(pair[1][-n:], kl[1])
+    again = la.la_checkpoint(h)
+    assert torch.equal(again[0], pair[0]) and torch.equal(again[1], pair[1])
+    assert torch.equal(la.la_checkpoint_restore(*again)[-n:], la.la_checkpoint_restore(*kl))
+    for xin, xl in ((h, hl), (pair, kl)):
+        dx = la.la_layer_norm_backward(xin, w, y)[0]
+        assert torch.equal(dx[-n:], la.la_layer_norm_backward(xl, w, y[-n:].contiguous())[0])
+
+
 def test_calls_on_another_stream_and_in_a_graph(la):
     """A norm, projections and the way back, captured and replayed on new inputs in two graphs, with
     workspaces of their own, and on two streams at once."""
