@@ -9,8 +9,9 @@
 // shared memory, no transposition, every byte of a 64-byte piece of a row used at once.
 // Measured, T 1 in bf16: C 4096, F 11008 29.9 us (180 MB, 6.0 TB/s), C 2048, F 5632 10.1 us (46 MB;
 // four warps with twice the loads in flight 12.8, sixteen 13.9), C 512, F 1408 2.2 us.
-// float32: 2 rows of each matrix and 8 tokens are 32 sums a lane, which the warp's 32 lanes add up
-// in 31 exchanges, each lane ending with one of them.
+// float32: 2 rows of each matrix and NT tokens are 4 NT sums a lane, which the warp's lanes add up by
+// exchanging halves, each lane ending with one of them. C 2048, F 5632: 1 token 14.3 us (92 MB,
+// 6.4 TB/s; with one piece in flight 15.7, four 17.8; as 8 tokens 19.3), 4 tokens 18.6, 8 25.7.
 #include "la_ffn.cuh"
 #include "la_internal.h"
 #include "la_tc_common.cuh"
@@ -103,11 +104,16 @@ __global__ void __launch_bounds__(32 * kWarps) ffn_few_kernel(const Args a) {
   }
 }
 
-// 32 values a lane, added over the warp: lane i ends with the sum of value i
-__device__ __forceinline__ float sums_to_lanes(float (&v)[32]) {
+// N values a lane, added over the warp: lane i ends with the sum of value i % N
+template <int N>
+__device__ __forceinline__ float sums_to_lanes(float (&v)[N]) {
   const int lane = threadIdx.x % 32;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = 16; o >= N; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int i = 0; i < o; ++i) {
@@ -118,8 +124,10 @@ __device__ __forceinline__ float sums_to_lanes(float (&v)[32]) {
   return v[0];
 }
 
-template <int ACT>
+// NT: tokens. U: pieces of 128 terms a warp has in flight.
+template <int ACT, int NT, int U>
 __global__ void __launch_bounds__(32 * kWarps) ffn_few_f32_kernel(const Args a) {
+  constexpr int N = 4 * NT;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int f0 = blockIdx.x * 2;
   const float* w[4];
@@ -127,45 +135,58 @@ __global__ void __launch_bounds__(32 * kWarps) ffn_few_f32_kernel(const Args a) 
   for (int r = 0; r < 4; ++r)
     w[r] = static_cast<const float*>(r < 2 ? a.wg : a.wu) + (size_t)(f0 + r % 2) * a.C;
   const float* x = static_cast<const float*>(a.x);
-  float v[32];  // value r * 8 + token
+  float v[N];  // value r * NT + token
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = 0.f;
+  for (int i = 0; i < N; ++i) v[i] = 0.f;
   tc::pdl_wait();
-#pragma unroll 2
-  for (int k = (warp * 32 + lane) * 4; k < a.C; k += kWarps * 128) {
-    float4 p[4];
+  for (int k0 = (warp * 32 + lane) * 4; k0 < a.C; k0 += U * kWarps * 128) {
+    uint4 p[U][4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const uint4 u = load_once(w[r] + k);
-      p[r] = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
-    }
+    for (int j = 0; j < U; ++j)
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      if (n < a.T) {
+      for (int r = 0; r < 4; ++r) {
+        const int k = k0 + j * kWarps * 128;
+        p[j][r] = k < a.C ? load_once(w[r] + k) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int k = k0 + j * kWarps * 128;
+      if (k >= a.C) continue;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (n >= a.T) continue;
         const float4 y = __ldg(reinterpret_cast<const float4*>(x + n * a.x_stride + k));
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          v[r * 8 + n] = fmaf(p[r].x, y.x, fmaf(p[r].y, y.y, fmaf(p[r].z, y.z, fmaf(p[r].w, y.w, v[r * 8 + n]))));
+        for (int r = 0; r < 4; ++r) {
+          float& s = v[r * NT + n];
+          s = fmaf(__uint_as_float(p[j][r].x), y.x, s);
+          s = fmaf(__uint_as_float(p[j][r].y), y.y, s);
+          s = fmaf(__uint_as_float(p[j][r].z), y.z, s);
+          s = fmaf(__uint_as_float(p[j][r].w), y.w, s);
+        }
       }
     }
   }
-  __shared__ float sums[kWarps][32];
-  sums[warp][lane] = sums_to_lanes(v);
+  __shared__ float sums[kWarps][N];
+  const float mine = sums_to_lanes(v);
+  if (lane < N) sums[warp][lane] = mine;
   __syncthreads();
-  if (warp == 0) {
-    float s = sums[0][lane];
+  if (threadIdx.x < 2 * NT) {  // row f0 + threadIdx.x / NT of both matrices
+    float g = 0.f, u = 0.f;
 #pragma unroll
-    for (int i = 1; i < kWarps; ++i) s += sums[i][lane];
-    const float u = __shfl_down_sync(0xffffffffu, s, 16);
-    const int n = lane % 8, f = f0 + lane / 8;
-    if (lane < 16 && n < a.T) static_cast<float*>(a.h)[n * a.h_stride + f] = act2<ACT>(make_float2(s, 0.f)).x * u;
+    for (int i = 0; i < kWarps; ++i) g += sums[i][threadIdx.x], u += sums[i][2 * NT + threadIdx.x];
+    const int n = threadIdx.x % NT;
+    if (n < a.T)
+      static_cast<float*>(a.h)[n * a.h_stride + f0 + threadIdx.x / NT] = act2<ACT>(make_float2(g, 0.f)).x * u;
   }
 }
 
 template <int ACT>
 cudaError_t launch(const Args& a, int dtype, cudaStream_t st) {
   const dim3 block(32 * kWarps), grid(dtype == LA_F32 ? a.F / 2 : a.F / 8);
-  const cudaError_t e = dtype == LA_F32 ? launch_pdl(ffn_few_f32_kernel<ACT>, grid, block, 0, st, a)
+  const cudaError_t e = dtype == LA_F32 && a.T == 1   ? launch_pdl(ffn_few_f32_kernel<ACT, 1, 2>, grid, block, 0, st, a)
+                        : dtype == LA_F32 && a.T <= 4 ? launch_pdl(ffn_few_f32_kernel<ACT, 4, 2>, grid, block, 0, st, a)
+                        : dtype == LA_F32             ? launch_pdl(ffn_few_f32_kernel<ACT, 8, 2>, grid, block, 0, st, a)
                         : a.T <= 8      ? launch_pdl(ffn_few_kernel<ACT, 1, 4>, grid, block, 0, st, a)
                         : a.T <= 16     ? launch_pdl(ffn_few_kernel<ACT, 2, 4>, grid, block, 0, st, a)
                                         : launch_pdl(ffn_few_kernel<ACT, 4, 4>, grid, block, 0, st, a);
@@ -176,7 +197,7 @@ cudaError_t launch(const Args& a, int dtype, cudaStream_t st) {
 }  // namespace
 
 // bf16: 32 tokens take 15.7 us at C 2048, F 5632 here and 16.0 in tiles of 256 tokens, 64 tokens 38.
-// float32: 8 take 27 us, 9 take 174 in tiles of 64.
+// float32: 8 take 26 us, 9 take 100 in tiles.
 int ffn_few_tokens(int dtype) { return dtype == LA_F32 ? 8 : 32; }
 
 cudaError_t ffn_few_forward(const FfnGate& f, cudaStream_t st) {
