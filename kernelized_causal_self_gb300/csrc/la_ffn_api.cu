@@ -86,11 +86,11 @@ int from_cuda(cudaError_t e) { return e == cudaSuccess ? LA_OK : LA_ERR_CUDA; }
 
 cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
-bool few(int T, bool kept, int dtype) { return T <= la::ffn_few_tokens(dtype) && !kept; }
+bool few(int T, int F, bool kept, int dtype) { return !kept && la::ffn_few(T, F, dtype); }
 
 // (bf16: the tensor-core kernels' status header)
 size_t ffn_workspace(int T, int C, int F, bool kept, int dtype) {
-  if (few(T, kept, dtype)) return 0;
+  if (few(T, F, kept, dtype)) return 0;
   return dtype == LA_F32 ? la::ffn_tc32_workspace(T, C, F, false) : la::kHeaderBytes;
 }
 
@@ -244,7 +244,7 @@ int la_ffn_gate(const void* x, long long x_stride, const void* wg, const void* w
   f.F = F;
   f.act = act;
   f.dtype = dtype;
-  if (few(T, codes != nullptr, dtype)) return from_cuda(la::ffn_few_forward(f, as_stream(stream)));
+  if (few(T, F, codes != nullptr, dtype)) return from_cuda(la::ffn_few_forward(f, as_stream(stream)));
   return from_cuda(dtype == LA_F32 ? la::ffn_tc32_forward(f, workspace, as_stream(stream))
                                    : la::ffn_tc_forward(f, workspace, as_stream(stream)));
 }

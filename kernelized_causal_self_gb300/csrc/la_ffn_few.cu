@@ -9,9 +9,13 @@
 // shared memory, no transposition, every byte of a 64-byte piece of a row used at once.
 // Measured, T 1 in bf16: C 4096, F 11008 29.9 us (180 MB, 6.0 TB/s), C 2048, F 5632 10.1 us (46 MB;
 // four warps with twice the loads in flight 12.8, sixteen 13.9), C 512, F 1408 2.2 us.
-// float32: 2 rows of each matrix and NT tokens are 4 NT sums a lane, which the warp's lanes add up by
-// exchanging halves, each lane ending with one of them. C 2048, F 5632: 1 token 14.3 us (92 MB,
-// 6.4 TB/s; with one piece in flight 15.7, four 17.8; as 8 tokens 19.3), 4 tokens 18.6, 8 25.7.
+// Groups of 32 tokens are CTAs of their own, whose weights come from L2.
+// float32: one token on the CUDA cores, 2 rows of each matrix a CTA: C 2048, F 5632 14.5 us (92 MB, 6.4
+// TB/s; one piece in flight 15.7, four 17.8). From two on as in bf16, with each value as three bf16
+// parts and six products of them (la_ffn_tc32.cu), cut up in registers, 16 bytes of a row one product;
+// the largest products' sums are taken out every 32 terms, and the others', 2^-8 of them, kept apart.
+// The next pieces are asked for before one is used: 8, 16 and 32 tokens 19.7, 26.3, 36.1 us (all loads
+// first 21.3, 30.9, 41.5), 64 67, which mma.sync's rate then bounds; on the CUDA cores 8 took 25.7.
 #include "la_ffn.cuh"
 #include "la_internal.h"
 #include "la_tc_common.cuh"
@@ -52,14 +56,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 template <int ACT, int NT, int U>
 __global__ void __launch_bounds__(32 * kWarps) ffn_few_kernel(const Args a) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  const int f0 = blockIdx.x * 8, steps = (a.C + 31) / 32;
+  const int f0 = blockIdx.x * 8, steps = (a.C + 31) / 32, first = blockIdx.y * (NT * 8);
   const size_t row = (size_t)(f0 + g) * a.C;  // (F is a multiple of 8)
   const __nv_bfloat16 *wg = static_cast<const __nv_bfloat16*>(a.wg) + row, *wu = static_cast<const __nv_bfloat16*>(a.wu) + row;
   const uint4 none = make_uint4(0, 0, 0, 0);
   const __nv_bfloat16* x[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
-    x[n] = n * 8 + g < a.T ? static_cast<const __nv_bfloat16*>(a.x) + (n * 8 + g) * a.x_stride : nullptr;
+    x[n] = first + n * 8 + g < a.T ? static_cast<const __nv_bfloat16*>(a.x) + (first + n * 8 + g) * a.x_stride : nullptr;
   float d[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
@@ -97,37 +101,16 @@ __global__ void __launch_bounds__(32 * kWarps) ffn_few_kernel(const Args a) {
       s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
     const float2 h = mul2(act2<ACT>(make_float2(s.x, s.y)), make_float2(s.z, s.w));
-    const int tok = n * 8 + t * 2;
+    const int tok = first + n * 8 + t * 2;
     __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.h) + tok * a.h_stride + f0 + g;
     if (tok < a.T) to[0] = __float2bfloat16_rn(h.x);
     if (tok + 1 < a.T) to[a.h_stride] = __float2bfloat16_rn(h.y);
   }
 }
 
-// N values a lane, added over the warp: lane i ends with the sum of value i % N
-template <int N>
-__device__ __forceinline__ float sums_to_lanes(float (&v)[N]) {
-  const int lane = threadIdx.x % 32;
-#pragma unroll
-  for (int o = 16; o >= N; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-#pragma unroll
-  for (int o = N / 2; o > 0; o >>= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-    }
-  }
-  return v[0];
-}
-
-// NT: tokens. U: pieces of 128 terms a warp has in flight.
-template <int ACT, int NT, int U>
-__global__ void __launch_bounds__(32 * kWarps) ffn_few_f32_kernel(const Args a) {
-  constexpr int N = 4 * NT;
+// U: pieces of 128 terms a warp has in flight.
+template <int ACT, int U>
+__global__ void __launch_bounds__(32 * kWarps) ffn_one_f32_kernel(const Args a) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int f0 = blockIdx.x * 2;
   const float* w[4];
@@ -135,9 +118,7 @@ __global__ void __launch_bounds__(32 * kWarps) ffn_few_f32_kernel(const Args a) 
   for (int r = 0; r < 4; ++r)
     w[r] = static_cast<const float*>(r < 2 ? a.wg : a.wu) + (size_t)(f0 + r % 2) * a.C;
   const float* x = static_cast<const float*>(a.x);
-  float v[N];  // value r * NT + token
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = 0.f;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
   tc::pdl_wait();
   for (int k0 = (warp * 32 + lane) * 4; k0 < a.C; k0 += U * kWarps * 128) {
     uint4 p[U][4];
@@ -152,53 +133,145 @@ __global__ void __launch_bounds__(32 * kWarps) ffn_few_f32_kernel(const Args a) 
     for (int j = 0; j < U; ++j) {
       const int k = k0 + j * kWarps * 128;
       if (k >= a.C) continue;
+      const float4 y = __ldg(reinterpret_cast<const float4*>(x + k));
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (n >= a.T) continue;
-        const float4 y = __ldg(reinterpret_cast<const float4*>(x + n * a.x_stride + k));
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float& s = v[r * NT + n];
-          s = fmaf(__uint_as_float(p[j][r].x), y.x, s);
-          s = fmaf(__uint_as_float(p[j][r].y), y.y, s);
-          s = fmaf(__uint_as_float(p[j][r].z), y.z, s);
-          s = fmaf(__uint_as_float(p[j][r].w), y.w, s);
-        }
+      for (int r = 0; r < 4; ++r) {
+        v[r] = fmaf(__uint_as_float(p[j][r].x), y.x, v[r]);
+        v[r] = fmaf(__uint_as_float(p[j][r].y), y.y, v[r]);
+        v[r] = fmaf(__uint_as_float(p[j][r].z), y.z, v[r]);
+        v[r] = fmaf(__uint_as_float(p[j][r].w), y.w, v[r]);
       }
     }
   }
-  __shared__ float sums[kWarps][N];
-  const float mine = sums_to_lanes(v);
-  if (lane < N) sums[warp][lane] = mine;
+  __shared__ float sums[kWarps][4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) v[r] += __shfl_xor_sync(0xffffffffu, v[r], o);
+    if (lane == r) sums[warp][r] = v[r];
+  }
   __syncthreads();
-  if (threadIdx.x < 2 * NT) {  // row f0 + threadIdx.x / NT of both matrices
+  if (threadIdx.x < 2) {
     float g = 0.f, u = 0.f;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) g += sums[i][threadIdx.x], u += sums[i][2 * NT + threadIdx.x];
-    const int n = threadIdx.x % NT;
-    if (n < a.T)
-      static_cast<float*>(a.h)[n * a.h_stride + f0 + threadIdx.x / NT] = act2<ACT>(make_float2(g, 0.f)).x * u;
+    for (int i = 0; i < kWarps; ++i) g += sums[i][threadIdx.x], u += sums[i][2 + threadIdx.x];
+    static_cast<float*>(a.h)[f0 + threadIdx.x] = act2<ACT>(make_float2(g, 0.f)).x * u;
+  }
+}
+
+// NT: groups of 8 tokens. U: pieces of 16 terms a warp has in flight.
+template <int ACT, int NT, int U>
+__global__ void __launch_bounds__(32 * kWarps, NT < 4 ? 3 : 2) ffn_few_parts_kernel(const Args a) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const int f0 = blockIdx.x * 8, steps = (a.C + 15) / 16, first = blockIdx.y * (NT * 8);
+  const size_t row = (size_t)(f0 + g) * a.C;  // (F is a multiple of 8)
+  const float *wg = static_cast<const float*>(a.wg) + row, *wu = static_cast<const float*>(a.wu) + row;
+  const float* x[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int tok = first + n * 8 + g;
+    x[n] = tok < a.T ? static_cast<const float*>(a.x) + tok * a.x_stride : nullptr;
+  }
+  float sum[NT][4], rest[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[n][i] = rest[n][i] = 0.f;
+  tc::pdl_wait();
+  uint4 p[U], q[U];  // pieces of 16 terms of the rows; the next ones are asked for when one is used
+  auto ask = [&](int j, int step) {
+    const int k = step * 16 + t * 4;
+    p[j] = k < a.C ? load_once(wg + k) : make_uint4(0, 0, 0, 0);
+    q[j] = k < a.C ? load_once(wu + k) : make_uint4(0, 0, 0, 0);
+  };
+#pragma unroll
+  for (int j = 0; j < U; ++j) ask(j, warp + j * kWarps);
+  for (int s0 = warp; s0 < steps; s0 += U * kWarps) {
+    float d[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int k = (s0 + j * kWarps) * 16 + t * 4;
+      float v[8] = {__uint_as_float(p[j].x), __uint_as_float(p[j].y), __uint_as_float(q[j].x), __uint_as_float(q[j].y),
+                    __uint_as_float(p[j].z), __uint_as_float(p[j].w), __uint_as_float(q[j].z), __uint_as_float(q[j].w)};
+      ask(j, s0 + (U + j) * kWarps);
+      uint32_t w[3][4];
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) w[i][r] = take_part(v[2 * r], v[2 * r + 1], i);
+uint32_t b[NT][3][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float4 y = k < a.C && x[n] != nullptr ? __ldg(reinterpret_cast<const float4*>(x[n] + k)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) b[n][i][0] = take_part(y.x, y.y, i), b[n][i][1] = take_part(y.z, y.w, i);
+      }
+      // (products on other accumulators do not wait for one another)
+#pragma unroll
+      for (int i = 0; i < 6; ++i) {
+        constexpr int of_w[6] = {0, 2, 0, 1, 1, 0}, of_x[6] = {0, 0, 2, 1, 0, 1};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint32_t* m = w[of_w[i]];
+          mma16816(i == 0 ? d[n] : rest[n], m[0], m[1], m[2], m[3], b[n][of_x[i]][0], b[n][of_x[i]][1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[n][i] += d[n][i];
+  }
+  __shared__ float4 sums[kWarps][NT][32];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[n][i] += rest[n][i];
+    sums[warp][n][lane] = make_float4(sum[n][0], sum[n][1], sum[n][2], sum[n][3]);
+  }
+  __syncthreads();
+  for (int n = warp; n < NT; n += kWarps) {
+    float4 s = sums[0][n][lane];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+      const float4 v = sums[w][n][lane];
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    const float2 h = mul2(act2<ACT>(make_float2(s.x, s.y)), make_float2(s.z, s.w));
+    const int tok = first + n * 8 + t * 2;
+    float* to = static_cast<float*>(a.h) + tok * a.h_stride + f0 + g;
+    if (tok < a.T) to[0] = h.x;
+    if (tok + 1 < a.T) to[a.h_stride] = h.y;
   }
 }
 
 template <int ACT>
 cudaError_t launch(const Args& a, int dtype, cudaStream_t st) {
-  const dim3 block(32 * kWarps), grid(dtype == LA_F32 ? a.F / 2 : a.F / 8);
-  const cudaError_t e = dtype == LA_F32 && a.T == 1   ? launch_pdl(ffn_few_f32_kernel<ACT, 1, 2>, grid, block, 0, st, a)
-                        : dtype == LA_F32 && a.T <= 4 ? launch_pdl(ffn_few_f32_kernel<ACT, 4, 2>, grid, block, 0, st, a)
-                        : dtype == LA_F32             ? launch_pdl(ffn_few_f32_kernel<ACT, 8, 2>, grid, block, 0, st, a)
-                        : a.T <= 8      ? launch_pdl(ffn_few_kernel<ACT, 1, 4>, grid, block, 0, st, a)
-                        : a.T <= 16     ? launch_pdl(ffn_few_kernel<ACT, 2, 4>, grid, block, 0, st, a)
-                                        : launch_pdl(ffn_few_kernel<ACT, 4, 4>, grid, block, 0, st, a);
+  const dim3 block(32 * kWarps), grid(a.F / 8, a.T <= 16 ? 1 : (a.T + 31) / 32);
+  const cudaError_t e = dtype == LA_F32
+                            ? (a.T == 1    ? launch_pdl(ffn_one_f32_kernel<ACT, 2>, dim3(a.F / 2), block, 0, st, a)
+                               : a.T <= 8  ? launch_pdl(ffn_few_parts_kernel<ACT, 1, 2>, grid, block, 0, st, a)
+                               : a.T <= 16 ? launch_pdl(ffn_few_parts_kernel<ACT, 2, 2>, grid, block, 0, st, a)
+                                           : launch_pdl(ffn_few_parts_kernel<ACT, 4, 2>, grid, block, 0, st, a))
+                            : (a.T <= 8    ? launch_pdl(ffn_few_kernel<ACT, 1, 4>, grid, block, 0, st, a)
+                               : a.T <= 16 ? launch_pdl(ffn_few_kernel<ACT, 2, 4>, grid, block, 0, st, a)
+                                           : launch_pdl(ffn_few_kernel<ACT, 4, 4>, grid, block, 0, st, a));
   count_launches(1);
   return e;
 }
 
 }  // namespace
 
-// bf16: 32 tokens take 15.7 us at C 2048, F 5632 here and 16.0 in tiles of 256 tokens, 64 tokens 38.
-// float32: 8 take 26 us, 9 take 100 in tiles.
-int ffn_few_tokens(int dtype) { return dtype == LA_F32 ? 8 : 32; }
+// Few tokens, or a small product, of which the tiles of 256 tokens leave most tensor cores idle.
+// bf16, here and in tiles: 32 tokens at C 2048, F 5632 15.7 and 16.0 us, 64 38 and 16; at C 512, F 1408
+// 64 4.1 and 8.0; at C 64, F 168 300 2.5 and 6.3. float32: 64 tokens at C 2048, F 5632 67 and 100 us; at
+// C 512, F 1408 186 14.7 and 22.9; at C 256, F 680 382 9.5 and 15.6.
+bool ffn_few(int T, int F, int dtype) {
+  const bool f32 = dtype == LA_F32;
+  return T <= (f32 ? 64 : 32) || (long long)T * F <= (f32 ? 1 << 18 : 1 << 17);
+}
 
 cudaError_t ffn_few_forward(const FfnGate& f, cudaStream_t st) {
   Args a;

@@ -213,8 +213,8 @@ struct FfnGate {
   long long x_stride, h_stride, dh_stride, dx_stride;
   int T, C, F, act, dtype;
 };
-// up to ffn_few_tokens tokens, without a checkpoint
-int ffn_few_tokens(int dtype);
+// few tokens (ffn_few), without a checkpoint
+bool ffn_few(int T, int F, int dtype);
 cudaError_t ffn_few_forward(const FfnGate& f, cudaStream_t st);
 // bf16 on tensor cores; the workspace's status header is used (and cleared)
 size_t ffn_tc_backward_workspace(int T, int C, int F);

@@ -305,7 +305,7 @@ def _ffn_inputs(T, C, F, dtype, seed=1):
 FFN_SIZES = [(1, 8, 8), (1, 64, 128), (1, 2048, 1032), (2, 72, 40), (5, 136, 264), (7, 1000, 24), (8, 256, 680), (9, 520, 72), (16, 64, 64), (17, 200, 96), (33, 64, 1032),
              (64, 512, 256), (65, 128, 136), (127, 64, 128), (128, 128, 256), (129, 264, 136), (200, 1032, 8),
              (256, 256, 512), (300, 8, 520), (513, 104, 280), (777, 256, 680), (1500, 264, 1032),
-             (2100, 136, 520)]
+             (2100, 136, 520), (512, 72, 256), (513, 72, 256), (1024, 72, 256), (1025, 72, 256)]
 
 
 @TYPES
@@ -548,14 +548,15 @@ def test_calls_marshalled_in_cpp_are_those_in_python(la, monkeypatch, dtype):
 def test_a_status_is_left_in_the_workspace(la):
     """The tensor-core calls clear the status header of a workspace of any contents."""
     for dtype in (BF, FL):
-        x, wg, wu, dh = _ffn_inputs(100, 64, 72, dtype)
+        x, wg, wu, dh = _ffn_inputs(2000, 64, 136, dtype)
         dt = la.LA_BF16 if dtype == BF else la.LA_F32
-        for pair in (None, _kept_like(100, 2, 72)):
-            ws = torch.full((la.la_ffn_gate_workspace_bytes(100, 64, 72, pair is not None, dt),), 3, dtype=torch.uint8,
+        assert la.la_ffn_gate_workspace_bytes(2000, 64, 136, False, dt) > 0
+        for pair in (None, _kept_like(2000, 2, 136)):
+            ws = torch.full((la.la_ffn_gate_workspace_bytes(2000, 64, 136, pair is not None, dt),), 3, dtype=torch.uint8,
                             device=DEV)
             la.la_ffn_gate(x, wg, wu, checkpoint=pair, workspace=ws)
             assert la.la_workspace_status(ws) == la.LA_OK
-            ws = torch.full((la.la_ffn_gate_backward_workspace_bytes(100, 64, 72, dt),), 3, dtype=torch.uint8, device=DEV)
+            ws = torch.full((la.la_ffn_gate_backward_workspace_bytes(2000, 64, 136, dt),), 3, dtype=torch.uint8, device=DEV)
             la.la_ffn_gate_backward(x, wg, wu, dh, checkpoint=pair, workspace=ws)
             assert la.la_workspace_status(ws) == la.LA_OK
 
