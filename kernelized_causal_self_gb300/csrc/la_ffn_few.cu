@@ -1,4 +1,5 @@
-// The gated projections of a few tokens (serving: one of each stream), h = act(x wg^T) (x wu^T).
+// The gated projections of a few tokens (serving: one of each stream), h = act(x wg^T) (x wu^T), and
+// da, du of the backward pass from the same products.
 // Bound by the weights' bytes, which are read once: a CTA takes some rows f of wg and the same of
 // wu, its eight warps share their elements, and the sums are joined in shared memory in order, so
 // that a and u meet in one thread.
@@ -29,9 +30,9 @@ using namespace ffn;
 constexpr int kWarps = 8;
 
 struct Args {
-  const void *x, *wg, *wu;
-  void* h;
-  long long x_stride, h_stride;
+  const void *x, *wg, *wu, *dh;
+  void* out;  // h, or da and du: [2][T][F], in float32 their parts, [2][3][T][F]
+  long long x_stride, out_stride, dh_stride;
   int T, C, F;
 };
 
@@ -52,8 +53,37 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Lane 4 g + t has in s what is a of tokens tok, tok + 1 and row f, and u of the same
+template <typename T, int ACT, bool GRADS>
+__device__ __forceinline__ void finish(const Args& a, float4 s, int tok, int f) {
+  if constexpr (!GRADS) {
+    const float2 h = mul2(act2<ACT>(make_float2(s.x, s.y)), make_float2(s.z, s.w));
+    T* to = static_cast<T*>(a.out) + tok * a.out_stride + f;
+    if (tok < a.T) to[0] = from_f32<T>(h.x);
+    if (tok + 1 < a.T) to[a.out_stride] = from_f32<T>(h.y);
+  } else {
+    float2 fa, df;
+    act_grad2<ACT>(make_float2(s.x, s.y), fa, df);
+    const size_t plane = (size_t)a.T * a.F;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (tok + i >= a.T) continue;
+      const float dh = to_f32(static_cast<const T*>(a.dh)[(tok + i) * a.dh_stride + f]);
+      float da = dh * (i ? s.w * df.y : s.z * df.x), du = dh * (i ? fa.y : fa.x);
+      __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + (size_t)(tok + i) * a.F + f;
+      constexpr int P = sizeof(T) == 2 ? 1 : 3;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const uint32_t u = P == 1 ? tc::pack_bf16(da, du) : take_part(da, du, p);
+        to[p * plane] = __ushort_as_bfloat16((unsigned short)u);
+        to[(P + p) * plane] = __ushort_as_bfloat16((unsigned short)(u >> 16));
+      }
+    }
+  }
+}
+
 // NT: groups of 8 tokens. U: pieces of 32 terms a warp has in flight.
-template <int ACT, int NT, int U>
+template <int ACT, bool GRADS, int NT, int U>
 __global__ void __launch_bounds__(32 * kWarps) ffn_few_kernel(const Args a) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int f0 = blockIdx.x * 8, steps = (a.C + 31) / 32, first = blockIdx.y * (NT * 8);
@@ -92,7 +122,6 @@ __global__ void __launch_bounds__(32 * kWarps) ffn_few_kernel(const Args a) {
 #pragma unroll
   for (int n = 0; n < NT; ++n) sums[warp][n][lane] = make_float4(d[n][0], d[n][1], d[n][2], d[n][3]);
   __syncthreads();
-  // a lane has a of tokens 2 t, 2 t + 1 (of its group) and row f0 + g, and u of the same
   for (int n = warp; n < NT; n += kWarps) {
     float4 s = sums[0][n][lane];
 #pragma unroll
@@ -100,11 +129,7 @@ __global__ void __launch_bounds__(32 * kWarps) ffn_few_kernel(const Args a) {
       const float4 v = sums[w][n][lane];
       s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
-    const float2 h = mul2(act2<ACT>(make_float2(s.x, s.y)), make_float2(s.z, s.w));
-    const int tok = first + n * 8 + t * 2;
-    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.h) + tok * a.h_stride + f0 + g;
-    if (tok < a.T) to[0] = __float2bfloat16_rn(h.x);
-    if (tok + 1 < a.T) to[a.h_stride] = __float2bfloat16_rn(h.y);
+    finish<__nv_bfloat16, ACT, GRADS>(a, s, first + n * 8 + t * 2, f0 + g);
   }
 }
 
@@ -155,12 +180,12 @@ __global__ void __launch_bounds__(32 * kWarps) ffn_one_f32_kernel(const Args a) 
     float g = 0.f, u = 0.f;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) g += sums[i][threadIdx.x], u += sums[i][2 + threadIdx.x];
-    static_cast<float*>(a.h)[f0 + threadIdx.x] = act2<ACT>(make_float2(g, 0.f)).x * u;
+    static_cast<float*>(a.out)[f0 + threadIdx.x] = act2<ACT>(make_float2(g, 0.f)).x * u;
   }
 }
 
 // NT: groups of 8 tokens. U: pieces of 16 terms a warp has in flight.
-template <int ACT, int NT, int U>
+template <int ACT, bool GRADS, int NT, int U>
 __global__ void __launch_bounds__(32 * kWarps, NT < 4 ? 3 : 2) ffn_few_parts_kernel(const Args a) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int f0 = blockIdx.x * 8, steps = (a.C + 15) / 16, first = blockIdx.y * (NT * 8);
@@ -201,7 +226,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT < 4 ? 3 : 2) ffn_few_parts_ker
       for (int i = 0; i < 3; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) w[i][r] = take_part(v[2 * r], v[2 * r + 1], i);
-uint32_t b[NT][3][2];
+      uint32_t b[NT][3][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float4 y = k < a.C && x[n] != nullptr ? __ldg(reinterpret_cast<const float4*>(x[n] + k)) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -239,27 +264,30 @@ uint32_t b[NT][3][2];
       const float4 v = sums[w][n][lane];
       s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
-    const float2 h = mul2(act2<ACT>(make_float2(s.x, s.y)), make_float2(s.z, s.w));
-    const int tok = first + n * 8 + t * 2;
-    float* to = static_cast<float*>(a.h) + tok * a.h_stride + f0 + g;
-    if (tok < a.T) to[0] = h.x;
-    if (tok + 1 < a.T) to[a.h_stride] = h.y;
+    finish<float, ACT, GRADS>(a, s, first + n * 8 + t * 2, f0 + g);
   }
 }
 
-template <int ACT>
+template <int ACT, bool GRADS>
 cudaError_t launch(const Args& a, int dtype, cudaStream_t st) {
   const dim3 block(32 * kWarps), grid(a.F / 8, a.T <= 16 ? 1 : (a.T + 31) / 32);
-  const cudaError_t e = dtype == LA_F32
-                            ? (a.T == 1    ? launch_pdl(ffn_one_f32_kernel<ACT, 2>, dim3(a.F / 2), block, 0, st, a)
-                               : a.T <= 8  ? launch_pdl(ffn_few_parts_kernel<ACT, 1, 2>, grid, block, 0, st, a)
-                               : a.T <= 16 ? launch_pdl(ffn_few_parts_kernel<ACT, 2, 2>, grid, block, 0, st, a)
-                                           : launch_pdl(ffn_few_parts_kernel<ACT, 4, 2>, grid, block, 0, st, a))
-                            : (a.T <= 8    ? launch_pdl(ffn_few_kernel<ACT, 1, 4>, grid, block, 0, st, a)
-                               : a.T <= 16 ? launch_pdl(ffn_few_kernel<ACT, 2, 4>, grid, block, 0, st, a)
-                                           : launch_pdl(ffn_few_kernel<ACT, 4, 4>, grid, block, 0, st, a));
   count_launches(1);
-  return e;
+  if (dtype != LA_F32)
+    return a.T <= 8    ? launch_pdl(ffn_few_kernel<ACT, GRADS, 1, 4>, grid, block, 0, st, a)
+           : a.T <= 16 ? launch_pdl(ffn_few_kernel<ACT, GRADS, 2, 4>, grid, block, 0, st, a)
+                       : launch_pdl(ffn_few_kernel<ACT, GRADS, 4, 4>, grid, block, 0, st, a);
+  if (a.T == 1 && !GRADS) return launch_pdl(ffn_one_f32_kernel<ACT, 2>, dim3(a.F / 2), block, 0, st, a);
+  return a.T <= 8    ? launch_pdl(ffn_few_parts_kernel<ACT, GRADS, 1, 2>, grid, block, 0, st, a)
+         : a.T <= 16 ? launch_pdl(ffn_few_parts_kernel<ACT, GRADS, 2, 2>, grid, block, 0, st, a)
+                     : launch_pdl(ffn_few_parts_kernel<ACT, GRADS, 4, 2>, grid, block, 0, st, a);
+}
+
+template <bool GRADS>
+cudaError_t launch_act(const FfnGate& f, void* out, long long out_stride, cudaStream_t st) {
+  const Args a{f.x, f.wg, f.wu, f.dh, out, f.x_stride, out_stride, f.dh_stride, f.T, f.C, f.F};
+  return f.act == kSilu   ? launch<kSilu, GRADS>(a, f.dtype, st)
+         : f.act == kGelu ? launch<kGelu, GRADS>(a, f.dtype, st)
+                          : launch<kGeluTanh, GRADS>(a, f.dtype, st);
 }
 
 }  // namespace
@@ -267,26 +295,15 @@ cudaError_t launch(const Args& a, int dtype, cudaStream_t st) {
 // Few tokens, or a small product, of which the tiles of 256 tokens leave most tensor cores idle.
 // bf16, here and in tiles: 32 tokens at C 2048, F 5632 15.7 and 16.0 us, 64 38 and 16; at C 512, F 1408
 // 64 4.1 and 8.0; at C 64, F 168 300 2.5 and 6.3. float32: 64 tokens at C 2048, F 5632 67 and 100 us; at
-// C 512, F 1408 186 14.7 and 22.9; at C 256, F 680 382 9.5 and 15.6.
+// C 512, F 1408 186 14.7 and 22.9; at C 256, F 680 382 9.5 and 15.6. da and du: bf16 32 tokens at C 480,
+// F 1920 3.8 and 8.6, at C 2048, F 5632 20.4 and 20.3; float32 186 at C 512, F 1408 17.3 and 24.9.
 bool ffn_few(int T, int F, int dtype) {
   const bool f32 = dtype == LA_F32;
   return T <= (f32 ? 64 : 32) || (long long)T * F <= (f32 ? 1 << 18 : 1 << 17);
 }
 
-cudaError_t ffn_few_forward(const FfnGate& f, cudaStream_t st) {
-  Args a;
-  a.x = f.x;
-  a.wg = f.wg;
-  a.wu = f.wu;
-  a.h = f.h;
-  a.x_stride = f.x_stride;
-  a.h_stride = f.h_stride;
-  a.T = f.T;
-  a.C = f.C;
-  a.F = f.F;
-  return f.act == kSilu   ? launch<kSilu>(a, f.dtype, st)
-         : f.act == kGelu ? launch<kGelu>(a, f.dtype, st)
-                          : launch<kGeluTanh>(a, f.dtype, st);
-}
+cudaError_t ffn_few_forward(const FfnGate& f, cudaStream_t st) { return launch_act<false>(f, f.h, f.h_stride, st); }
+
+cudaError_t ffn_few_grads(const FfnGate& f, void* dact, cudaStream_t st) { return launch_act<true>(f, dact, f.F, st); }
 
 }  // namespace la

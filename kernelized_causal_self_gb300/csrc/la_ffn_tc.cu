@@ -419,8 +419,8 @@ cudaError_t ffn_tc_backward(const FfnGate& f, void* ws, cudaStream_t st) {
   Args a{};
   a.hdr = static_cast<WorkspaceHeader*>(ws);
   cudaError_t e;
-  if (f.codes != nullptr) {
-    e = ffn_kept_grads(f, da, st);
+  if (f.codes != nullptr || ffn_few(f.T, f.F, f.dtype)) {
+    e = f.codes != nullptr ? ffn_kept_grads(f, da, st) : ffn_few_grads(f, da, st);
     a.clear = 1;
   } else {
     if (!products(a, f) || !rows_map(&a.dh, f.dh, f.F, f.T, f.dh_stride, 128) ||

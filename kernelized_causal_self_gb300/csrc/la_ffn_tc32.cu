@@ -467,8 +467,8 @@ cudaError_t ffn_tc32_backward(const FfnGate& f, void* ws, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   Args a{};
   a.hdr = static_cast<WorkspaceHeader*>(ws);
-  if (f.codes != nullptr) {
-    e = ffn_kept_grads(f, dact, st);
+  if (f.codes != nullptr || ffn_few(f.T, f.F, f.dtype)) {
+    e = f.codes != nullptr ? ffn_kept_grads(f, dact, st) : ffn_few_grads(f, dact, st);
     a.clear = 1;
   } else {
     a.dh = static_cast<const float*>(f.dh);

@@ -216,6 +216,8 @@ struct FfnGate {
 // few tokens (ffn_few), without a checkpoint
 bool ffn_few(int T, int F, int dtype);
 cudaError_t ffn_few_forward(const FfnGate& f, cudaStream_t st);
+// dact as ffn_kept_grads leaves it
+cudaError_t ffn_few_grads(const FfnGate& f, void* dact, cudaStream_t st);
 // bf16 on tensor cores; the workspace's status header is used (and cleared)
 size_t ffn_tc_backward_workspace(int T, int C, int F);
 cudaError_t ffn_tc_forward(const FfnGate& f, void* ws, cudaStream_t st);
