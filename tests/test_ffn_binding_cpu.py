@@ -161,7 +161,7 @@ def test_abi_ffn(lib):
     assert fwd(xs=56) == bad and fwd(hs=120) == bad and fwd(hs=132) == bad
     assert fwd(codes=FAR[5]) == bad and fwd(codes=ODD, exps=FAR[6]) == bad
     assert fwd(h=FAR[0]) == bad and fwd(h=FAR[1] + 1024) == bad and fwd(codes=FAR[3], exps=FAR[6]) == bad
-    for many in ({"T": 100}, {"codes": FAR[5], "exps": FAR[6]}):
+    for many in ({"T": 4000}, {"codes": FAR[5], "exps": FAR[6]}):
         assert fwd(wsp=0, **many) == ws and fwd(wsb=128, **many) == ws and fwd(wsp=ODD, **many) == ws
     assert fwd(T=0, x=0, wsp=0) == la.LA_OK
 
@@ -176,9 +176,9 @@ def test_abi_ffn(lib):
     assert need > 256 and back(wsb=need - 1) == ws and back(wsp=0) == ws
     assert lib.la_ffn_gate_backward_workspace_bytes(4, 63, 128, 1) == 256
     need = lib.la_ffn_gate_workspace_bytes
-    assert need(100, 64, 128, 0, 1) == need(4, 64, 128, 1, 1) == need(-1, 64, 128, 0, 1) == 256
-    assert need(4, 64, 128, 0, 1) == need(4, 64, 128, 0, 0) == 0
-    assert need(100, 64, 128, 0, 0) >= 256 + 6 * 64 * (100 + 2 * 128)
+    assert need(4000, 64, 128, 0, 1) == need(4, 64, 128, 1, 1) == need(-1, 64, 128, 0, 1) == 256
+    assert need(4, 64, 128, 0, 1) == need(4, 64, 128, 0, 0) == need(100, 64, 128, 0, 0) == 0
+    assert need(4000, 64, 128, 0, 0) >= 256 + 6 * 64 * (4000 + 2 * 128)
 
 
 def test_marshalling_leaves_what_it_does_not_do(lib):
