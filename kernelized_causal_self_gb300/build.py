@@ -69,7 +69,7 @@ def _marshal_command(out):
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             *[f for p in inc for f in ("-isystem", p)], "-I" + os.path.join(ROOT, "include"),
             os.path.join(CSRC, "la_marshal.cpp"), "-o", out, "-L" + libs, "-Wl,-rpath," + libs,
-            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
 
 
 def build(force=False, verbose=False, extra_flags=()):
