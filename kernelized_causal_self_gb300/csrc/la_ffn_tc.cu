@@ -384,7 +384,7 @@ cudaError_t launch_act(const Args& a, int act, cudaStream_t st) {
                         : launch<KIND, kGeluTanh>(a, st);
 }
 
-constexpr int kStep = 700;  // clocks of a pair for 64 terms
+constexpr Costs kCosts{700, 4300};
 
 // a = x wg^T, u = x wu^T
 bool products(Args& a, const FfnGate& f) {
@@ -399,7 +399,7 @@ size_t dact_bytes(int T, int F) { return align_up(2 * sizeof(__nv_bfloat16) * (s
 }  // namespace
 
 size_t ffn_tc_backward_workspace(int T, int C, int F) {
-  const Grids g = sums_grids(T, C, F, kStep);
+  const Grids& g = sums_grids(T, C, F, kCosts);
   return kHeaderBytes + dact_bytes(T, F) + sizeof(float) * (dx_parts(g) + dw_parts(g));
 }
 
@@ -431,7 +431,7 @@ cudaError_t ffn_tc_backward(const FfnGate& f, void* ws, cudaStream_t st) {
   }
   if (e != cudaSuccess) return e;
 
-  const Grids g = sums_grids(f.T, f.C, f.F, kStep);
+  const Grids& g = sums_grids(f.T, f.C, f.F, kCosts);
   static_cast<Grids&>(a) = g;
   const int sx = g.g[0].splits, sw = g.g[1].splits;
   if (!rows_map(&a.a, da, f.F, f.T, f.F, 128, 2) || !rows_map(&a.b0, f.wg, f.C, f.F, f.C, 64) ||

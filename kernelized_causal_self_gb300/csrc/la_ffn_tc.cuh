@@ -72,7 +72,7 @@ __device__ __forceinline__ Tile tile_of(const Grids& a, uint32_t t) {
   return r;
 }
 
-// Where a split's steps begin (kForward's and kGrads' sums are not cut). At most 2^18 steps and 16 parts.
+// Where a split's steps begin (kForward's and kGrads' sums are not cut). At most 2^18 steps and 32 parts.
 __device__ __forceinline__ int first_step(const Grid& g, int split) {
   return g.splits == 1 ? (split ? g.steps : 0) : (int)((uint32_t)(g.steps * split) / (uint32_t)g.splits);
 }
@@ -82,11 +82,19 @@ enum Site { kSiteEmpty = 81, kSiteFull, kSiteAccEmpty, kSiteAccFull, kSiteDhFull
 
 inline int ceil_div(long long a, int b) { return (int)((a + b - 1) / b); }
 
+// What a tile of sums costs in SM clocks: 64 terms, and its results, which are written while the next tile
+// is summed
+struct Costs {
+  int step, results;
+};
+
 // The grids of dx and of dwg, dwu, whose tiles one launch deals to 76 pairs of CTAs, with the sums
-// cut into the parts, and the tiles dealt, that take the least time by this count: a step costs
-// `step` SM clocks, a tile 500 more; a part's results are 8 bytes a value more to move (written and
-// read again, at about 3500 bytes a clock over all SMs), by one more launch.
-inline Grids sums_grids(int T, int C, int F, int step) {
+// cut into the parts, and the tiles dealt, that take the least time by this count: a tile costs its
+// steps and 500 clocks more, or its results if they take longer; a part's results are 8 bytes a value
+// more to move (written and read again, at about 3500 bytes a clock over all SMs), by one more launch.
+// T 25, C 1536, F 5120 in bf16: all pairs done after 19 to 20 us; not counting results some after 15 and
+// some after 26.
+inline Grids count_sums_grids(int T, int C, int F, Costs cost) {
   constexpr int P = 76;
   Grids r{};
   Grid &x = r.g[0], &w = r.g[1];
@@ -97,13 +105,17 @@ inline Grids sums_grids(int T, int C, int F, int step) {
   x.per = ceil_div(F, 64);
   x.steps = 2 * x.per, w.steps = ceil_div(T, 64);
   const long long nx = (long long)x.m_tiles * x.n_tiles, nw = 2LL * w.m_tiles * w.n_tiles;
-  const int tried[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 14, 16};
+  const int tried[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 14, 16, 24, 32};
+  const auto tile = [&](const Grid& g, int splits) {
+    const double sums = (double)ceil_div(g.steps, splits) * cost.step + 500;
+    return sums > cost.results ? sums : cost.results;
+  };
   double least = 0;
   for (int sx : tried)
     for (int sw : tried) {
       if (sx > x.steps || sw > w.steps) continue;
       const long long tx = nx * sx, tw = nw * sw, more = tx % P, less = P - more;
-      const double cx = (double)ceil_div(x.steps, sx) * step + 500, cw = (double)ceil_div(w.steps, sw) * step + 500;
+      const double cx = tile(x, sx), cw = tile(w, sw);
       double moved = 0;
       if (sx > 1 || sw > 1)
         moved = 4000 + ((sx > 1 ? (double)sx * T * C : 0) + (sw > 1 ? 2.0 * sw * F * C : 0)) * 8 / 3500;
@@ -120,6 +132,17 @@ inline Grids sums_grids(int T, int C, int F, int step) {
   x.tiles = (int)(nx * x.splits);
   w.tiles = (int)(nw * w.splits);
   return r;
+}
+
+// (counted once for a size: a call asks three times, 0.6 us each)
+inline const Grids& sums_grids(int T, int C, int F, Costs cost) {
+  thread_local struct {
+    int T, C, F, step;
+    Grids grids;
+  } last{};
+  if (last.T != T || last.C != C || last.F != F || last.step != cost.step)
+    last = {T, C, F, cost.step, count_sums_grids(T, C, F, cost)};
+  return last.grids;
 }
 
 // Floats of the parts of dx, then of dwg and dwu

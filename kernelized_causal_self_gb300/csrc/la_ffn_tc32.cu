@@ -403,7 +403,7 @@ struct Plan {
   size_t w, dact, sums, end;  // offsets in bytes
 };
 
-constexpr int kStep = 6 * 550;  // clocks of a pair for 64 terms
+constexpr Costs kCosts{6 * 550, 6000};
 
 Plan plan_of(int T, int C, int F, bool backward) {
   Plan p{};
@@ -411,7 +411,7 @@ Plan plan_of(int T, int C, int F, bool backward) {
   p.dact = p.w + align_up(12 * (size_t)F * C, 256);
   p.end = p.dact;
   if (!backward) return p;
-  const Grids g = sums_grids(T, C, F, kStep);
+  const Grids& g = sums_grids(T, C, F, kCosts);
   p.sums = p.dact + align_up(12 * (size_t)T * F, 256);
   p.end = p.sums + sizeof(float) * (dx_parts(g) + dw_parts(g));
   return p;
@@ -478,7 +478,7 @@ cudaError_t ffn_tc32_backward(const FfnGate& f, void* ws, cudaStream_t st) {
   }
   if (e != cudaSuccess) return e;
 
-  const Grids g = sums_grids(f.T, f.C, f.F, kStep);
+  const Grids& g = sums_grids(f.T, f.C, f.F, kCosts);
   static_cast<Grids&>(a) = g;
   const int sx = g.g[0].splits, sw = g.g[1].splits;
   if (!rows_map(&a.a, dact, f.F, f.T, f.F, 128, 6) || !rows_map(&a.b0, p.wg, f.C, f.F, f.C, 64, 3) ||
