@@ -548,7 +548,8 @@ int la_layer_norm_backward(const void* x, long long x_stride, const signed char*
                            size_t workspace_bytes, void* stream);
 
 /* Scratch needed by la_ffn_gate (checkpoint: whether it writes one; where it needs 0 it takes
- * nullptr) and by la_ffn_gate_backward, in bytes. */
+ * nullptr, and leaves what it is given as it was) and by la_ffn_gate_backward, in bytes, for these
+ * sizes: more tokens may need less, so that one workspace for several T has to hold the most of them. */
 size_t la_ffn_gate_workspace_bytes(int T, int C, int F, int checkpoint, int dtype);
 size_t la_ffn_gate_backward_workspace_bytes(int T, int C, int F, int dtype);
 

@@ -305,7 +305,8 @@ def _ffn_inputs(T, C, F, dtype, seed=1):
 FFN_SIZES = [(1, 8, 8), (1, 64, 128), (1, 2048, 1032), (2, 72, 40), (5, 136, 264), (7, 1000, 24), (8, 256, 680), (9, 520, 72), (16, 64, 64), (17, 200, 96), (33, 64, 1032),
              (64, 512, 256), (65, 128, 136), (127, 64, 128), (128, 128, 256), (129, 264, 136), (200, 1032, 8),
              (256, 256, 512), (300, 8, 520), (513, 104, 280), (777, 256, 680), (1500, 264, 1032),
-             (2100, 136, 520), (512, 72, 256), (513, 72, 256), (1024, 72, 256), (1025, 72, 256)]
+             (2100, 136, 520), (512, 72, 256), (513, 72, 256), (1024, 72, 256), (1025, 72, 256),
+             (1032, 264, 264)]
 
 
 @TYPES
@@ -366,28 +367,30 @@ def test_ffn_gradients_by_differences(la, act, dtype):
 
 
 @TYPES
-def test_ffn_layouts(la, dtype):
-    x, wg, wu, dh = _ffn_inputs(90, 72, 136, dtype)
+@pytest.mark.parametrize("a, b", [(9, 10), (45, 50)])
+def test_ffn_layouts(la, a, b, dtype):
+    T = a * b
+    x, wg, wu, dh = _ffn_inputs(T, 72, 136, dtype)
     want = la.la_ffn_gate(x, wg, wu)
     grads = la.la_ffn_gate_backward(x, wg, wu, dh)
-    xs = torch.full((9, 10, 200), 7.0, device=DEV, dtype=dtype)
-    xs[..., 64:136] = x.view(9, 10, 72)
-    hs = torch.full((9, 10, 3, 136), 5.0, device=DEV, dtype=dtype)
+    xs = torch.full((a, b, 200), 7.0, device=DEV, dtype=dtype)
+    xs[..., 64:136] = x.view(a, b, 72)
+    hs = torch.full((a, b, 3, 136), 5.0, device=DEV, dtype=dtype)
     xv = xs[..., 64:136]
     h = la.la_ffn_gate(xv, wg, wu, out=hs[:, :, 1])
-    assert h.shape == (9, 10, 136) and torch.equal(h.reshape(90, 136), want)
+    assert h.shape == (a, b, 136) and torch.equal(h.reshape(T, 136), want)
     assert torch.all(hs[:, :, 0] == 5.0) and torch.all(hs[:, :, 2] == 5.0)
-    hs[:, :, 1] = dh.view(9, 10, 136)
-    dxs = torch.full((9, 10, 80), 5.0, device=DEV, dtype=dtype)
+    hs[:, :, 1] = dh.view(a, b, 136)
+    dxs = torch.full((a, b, 80), 5.0, device=DEV, dtype=dtype)
     dwg, dwu = torch.empty_like(wg), torch.empty_like(wu)
     got = la.la_ffn_gate_backward(xv, wg, wu, hs[:, :, 1], dx=dxs[..., :72], dwg=dwg, dwu=dwu)
-    assert torch.equal(got[0].reshape(90, 72), grads[0]) and torch.equal(dwg, grads[1]) and torch.equal(dwu, grads[2])
+    assert torch.equal(got[0].reshape(T, 72), grads[0]) and torch.equal(dwg, grads[1]) and torch.equal(dwu, grads[2])
     assert torch.all(dxs[..., 72:] == 5.0)
-    pair = _kept_like(9, 10, 2, 136)
+    pair = _kept_like(a, b, 2, 136)
     la.la_ffn_gate(xv, wg, wu, checkpoint=pair)
-    flat = _kept_like(90, 2, 136)
+    flat = _kept_like(T, 2, 136)
     la.la_ffn_gate(x, wg, wu, checkpoint=flat)
-    assert torch.equal(pair[0].reshape(90, 2, 136), flat[0]) and torch.equal(pair[1].reshape(90, 2, 5), flat[1])
+    assert torch.equal(pair[0].reshape(T, 2, 136), flat[0]) and torch.equal(pair[1].reshape(T, 2, 5), flat[1])
     one = la.la_ffn_gate(x[4], wg, wu)
     assert one.shape == (136,)
     _ffn_close(one[None], x[4:5], wg, wu, "silu", dtype)
@@ -397,7 +400,7 @@ def test_ffn_layouts(la, dtype):
 
 
 @TYPES
-@pytest.mark.parametrize("T", [3, 40, 300])
+@pytest.mark.parametrize("T", [3, 40, 300, 1600])
 def test_ffn_rows_that_are_not_finite_stay_alone(la, T, dtype):
     x, wg, wu, dh = _ffn_inputs(T, 136, 200, dtype)
     bad = T // 2
@@ -419,9 +422,10 @@ def test_ffn_rows_that_are_not_finite_stay_alone(la, T, dtype):
 
 
 @TYPES
-def test_columns_of_one_buffer(la, dtype):
+@pytest.mark.parametrize("T", [70, 2100])
+def test_columns_of_one_buffer(la, T, dtype):
     """Inputs and outputs may be columns of one buffer, which share no memory."""
-    T, C, F = 70, 72, 136
+    C, F = 72, 136
     x, wg, wu, dh = _ffn_inputs(T, C, F, dtype)
     w = _randn(9, C, dtype=dtype)
     buf = torch.full((T, 2 * C + 2 * F), 2.0, dtype=dtype, device=DEV)
@@ -467,10 +471,11 @@ def test_more_elements_than_32_bits_count(la):
         assert torch.equal(dx[-n:], la.la_layer_norm_backward(xl, w, y[-n:].contiguous())[0])
 
 
-def test_calls_on_another_stream_and_in_a_graph(la):
+@pytest.mark.parametrize("T", [300, 600])
+def test_calls_on_another_stream_and_in_a_graph(la, T):
     """A norm, projections and the way back, captured and replayed on new inputs in two graphs, with
     workspaces of their own, and on two streams at once."""
-    T, C, F = 300, 136, 264
+    C, F = 136, 264
     x, wg, wu, dh = _ffn_inputs(T, C, F, BF)
     w, b = _randn(9, C, dtype=BF), _randn(10, C, dtype=BF)
 
@@ -480,7 +485,7 @@ def test_calls_on_another_stream_and_in_a_graph(la):
         h = la.la_ffn_gate(y, wg, wu, checkpoint=pair)
         dy, dwg, dwu = la.la_ffn_gate_backward(y, wg, wu, dh, checkpoint=pair)
         again = la.la_ffn_gate_backward(y, wg, wu, dh)
-        return (h, dwg, dwu, *la.la_layer_norm_backward(x, w, dy), *again)
+        return (h, dwg, dwu, *la.la_layer_norm_backward(x, w, dy), *again, la.la_ffn_gate(y, wg, wu))
     ins = [_randn(20 + i, T, C, dtype=BF) for i in range(4)]
     want = [[t.clone() for t in step(v)] for v in ins]
     torch.cuda.synchronize()
