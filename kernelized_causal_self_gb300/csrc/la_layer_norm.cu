@@ -286,19 +286,26 @@ template <typename T>
 __global__ void __launch_bounds__(1024)
 layer_norm_sums_kernel(const float* __restrict__ partial, T* dw, T* db, int rows, int C) {
   __shared__ float sums[32][33];
-  const int c = blockIdx.x * 32 + threadIdx.x;
+  int c = blockIdx.x * 32 + threadIdx.x;
   const float* p = partial + (size_t)blockIdx.y * rows * C;
   T* to = blockIdx.y ? db : dw;
   tc::pdl_wait();
   float s = 0.f;
   if (c < C)
-    for (int r = threadIdx.y; r < rows; r += 32) s += p[(size_t)r * C + c];
+    for (int r = threadIdx.y; r < rows; r += 32 * 5) {  // (five loads in flight: 304 rows are two turns)
+      float v[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) v[i] = r + 32 * i < rows ? p[(size_t)(r + 32 * i) * C + c] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 5; ++i) s += v[i];
+    }
   sums[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
-  if (threadIdx.y == 0 && c < C) {
-    for (int i = 1; i < 32; ++i) s += sums[i][threadIdx.x];
-    to[c] = from_f32<T>(s);
-  }
+  s = sums[threadIdx.x][threadIdx.y];  // (a warp has a column now)
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+  c = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && c < C) to[c] = from_f32<T>(s);
 }
 
 // Threads that share a row, and the rows that a CTA of 256 (or G, if more) has at once
