@@ -69,7 +69,7 @@ __device__ __forceinline__ void finish(const Args& a, float4 s, int tok, int f) 
     for (int i = 0; i < 2; ++i) {
       if (tok + i >= a.T) continue;
       const float dh = to_f32(static_cast<const T*>(a.dh)[(tok + i) * a.dh_stride + f]);
-      float da = dh * (i ? s.w * df.y : s.z * df.x), du = dh * (i ? fa.y : fa.x);
+      float da = dh * (i ? s.w : s.z) * (i ? df.y : df.x), du = dh * (i ? fa.y : fa.x);
       __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + (size_t)(tok + i) * a.F + f;
       constexpr int P = sizeof(T) == 2 ? 1 : 3;
 #pragma unroll
