@@ -513,12 +513,14 @@ int la_norm_gate_backward(const void* x, const void* z, const long long* z_strid
  * 32 neighbours of a row (the last block may be shorter) a byte e, the exponent of the block's
  * step 2^(e - 127): the smallest step, from e = 1 on, for which every |value| / step is below
  * 127.5. Code i stands for code * step, its value rounded to the nearest step, ties to the even
- * code. A block with an infinity or a NaN has e = 255 and restores as NaN throughout.
+ * code, but for no more than the largest bf16, +-(2^128 - 2^120): a finite value is off by half a
+ * step at most. A block with an infinity or a NaN has e = 255 and restores as NaN throughout.
  * codes [rows][C], 16-byte aligned; exps [rows][ceil(C / 32)].
  */
 
 /* la_checkpoint -- puts x away. la_checkpoint_restore -- writes what the codes stand for. Bytes
- * that la_checkpoint did not write are read as the formula says, e = 0 as a step of zero. */
+ * that la_checkpoint did not write are read as the formula says, e = 0 as a step of zero and e = 255 as
+ * NaN whatever the code. */
 int la_checkpoint(const void* x, long long x_stride, signed char* codes, unsigned char* exps, long long rows,
                   int C, int dtype, void* stream);
 int la_checkpoint_restore(const signed char* codes, const unsigned char* exps, void* x, long long x_stride,

@@ -1219,8 +1219,9 @@ def la_checkpoint(x, checkpoint=None):
     """x [..., C] in 8 bits: (codes int8 [..., C], exps uint8 [..., ceil(C/32)]).
 
     Each block of 32 neighbours has a step, the power of two 2^(exp - 127): the smallest (exp >= 1)
-    for which every |value| / step is below 127.5. A value is off by half a step at most. A block
-    that holds an infinity or a NaN restores as NaN. checkpoint: a pair to write to."""
+    for which every |value| / step is below 127.5. A value is off by half a step at most (codes stand for
+    no more than the largest bfloat16). A block that holds an infinity or a NaN restores as NaN.
+    checkpoint: a pair to write to."""
     import torch
     done = (_fast or _marshal()).checkpoint(x, checkpoint)
     if done is not NotImplemented:

@@ -1,10 +1,13 @@
 // Activations in 8 bits: whole numbers of -127 .. 127 and, for each block of 32 neighbours of a
 // row, a step that is a power of two: 2^(e - 127) for the block's byte e. The step is the
 // smallest, from e = 1 on, for which the block's largest magnitude rounds to 127 or less, so a
-// value is off by half a step at most, 2^-7 of that magnitude (and 2^-127). Powers of two make
+// value is off by half a step at most, 1/127.5 of that magnitude (and 2^-127). Powers of two make
 // every scaling exact: what is stored does not depend on the order or the type of the
-// arithmetic. A block that holds an infinity or a NaN gets e = 255 and zeros, which restore as
-// 0 * inf = NaN.
+// arithmetic. A block that holds an infinity or a NaN gets e = 255, which restores as NaN.
+//
+// From 63.75 2^122 on a magnitude is 64 steps of 2^122, and 2^128 is no float32: what a code stands
+// for is bounded by the largest bf16, 2^128 - 2^120, which is closer than 2^120 to all of those
+// values (so finite values restore finite, in both types as the same).
 #pragma once
 
 #include "la_common.cuh"
@@ -35,7 +38,9 @@ __device__ __forceinline__ float inverse_step(uint32_t e) {
   return __uint_as_float((e == 255u ? 127u : 254u - e) << 23);
 }
 
-__device__ __forceinline__ float step_value(uint32_t e) { return __uint_as_float(e << 23); }
+__device__ __forceinline__ float step_value(uint32_t e) {
+  return __uint_as_float(e == 255u ? 0x7FFFFFFFu : e << 23);
+}
 
 // round(x / step), ties to even, in the low byte: adding 1.5 2^23 leaves the whole number there
 __device__ __forceinline__ uint32_t code_of(float x, float inverse) {
@@ -53,8 +58,13 @@ __device__ __forceinline__ uint32_t codes4(const float* x, float inverse, uint32
   return e == 255u ? 0u : c;
 }
 
+// (the smaller magnitude of the two with the product's sign, NaN if the step is)
 __device__ __forceinline__ float value_of(uint32_t codes, int i, float step) {
-  return (float)(signed char)(codes >> (8 * i)) * step;
+  float v;
+  asm("min.NaN.xorsign.abs.f32 %0, %1, %2;"
+      : "=f"(v)
+      : "f"((float)(signed char)(codes >> (8 * i)) * step), "f"(__uint_as_float(0x7F7F0000u)));
+  return v;
 }
 
 // Codes of V neighbours that a thread holds, as bytes in memory

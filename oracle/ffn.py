@@ -60,7 +60,7 @@ def ffn_gate_backward(x, wg, wu, dh, kind="silu", kept=None):
 def checkpoint(x):
     """(codes, exps, values) of x [..., C] in blocks of 32: the step 2^(exp - 127) is the smallest,
     from exp = 1 on, with every |value| / step below 127.5; exp = 255 and NaN for a block that is
-    not finite."""
+    not finite. Values are bounded by the largest bf16, 2^128 - 2^120."""
     x = np.asarray(x, np.float64)
     n = x.shape[-1]
     v = np.concatenate([x, np.zeros((*x.shape[:-1], -n % 32))], -1).reshape(*x.shape[:-1], -1, 32)
@@ -72,6 +72,7 @@ def checkpoint(x):
     with np.errstate(invalid="ignore"):
         codes = np.where(bad[..., None], 0.0, np.rint(v / step[..., None]))
     exps = np.where(bad, 255, np.log2(step) + 127).astype(np.uint8)
-    values = codes * np.where(bad, np.nan, step)[..., None]
+    most = 2.0 ** 128 - 2.0 ** 120
+    values = np.clip(codes * np.where(bad, np.nan, step)[..., None], -most, most)
     cut = lambda t: t.reshape(*x.shape[:-1], -1)[..., :n]  # noqa: E731
     return cut(codes).astype(np.int8), exps, cut(values)

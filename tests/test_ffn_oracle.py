@@ -84,3 +84,14 @@ def test_checkpoint_is_within_half_a_step():
     assert top.min() >= 64  # half the step would not have done
     again = oracle.checkpoint(values)
     assert np.array_equal(again[2], values)
+
+
+def test_checkpoint_of_the_largest_values():
+    """2^128 is no float32: what codes stand for ends at the largest bfloat16, within half a step."""
+    most = 2.0 ** 128 - 2.0 ** 120
+    x = np.zeros((4, 32))
+    x[0, 0], x[1, 0], x[2, 0], x[3, 0] = most, -63.75 * 2.0 ** 122, 2.0 ** 128 - 2.0 ** 104, 127.25 * 2.0 ** 121
+    codes, exps, values = oracle.checkpoint(x)
+    assert codes[:, 0].tolist() == [64, -64, 64, 127] and exps[:, 0].tolist() == [249, 249, 249, 248]
+    assert values[:, 0].tolist() == [most, -most, most, 127 * 2.0 ** 121]
+    assert np.all(np.abs(values - x) <= 2.0 ** (exps.astype(float) - 128))

@@ -1,0 +1,98 @@
+"""The feed-forward half's calls at the ends of what they take, on the GPU against the float64 oracle.
+Bounds as in test_ffn_gpu.py where no others are given."""
+
+import numpy as np
+import pytest
+
+import oracle
+from tests.test_ffn_gpu import BF, DEV, FL, HALF, TYPES, _f64, _ffn_inputs, _kept_equal, _randn, la  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+# --------------------------------------------------------------------- checkpoints
+
+def _largest(dtype):
+    """Rows with the largest finite values of either type, and the values about the border 63.75 2^122
+    from which on a block's step is 2^122."""
+    x = _randn(1, 12, 72, dtype=FL)
+    big = [torch.finfo(BF).max, 63.75 * 2.0 ** 122, 0.5 * (127 + 127.5) * 2.0 ** 121, 127 * 2.0 ** 121]
+    big += [torch.finfo(FL).max if dtype == FL else 2.0 ** 127]
+    for i, v in enumerate(big):
+        x[2 * i, 3], x[2 * i + 1, 40] = v, -v
+        x[2 * i, 5] = 1e38
+    assert x.isfinite().all()
+    return x.to(dtype)
+
+
+@TYPES
+def test_a_checkpoint_of_the_largest_values_restores_finite(la, dtype):
+    x = _largest(dtype)
+    if dtype == BF:  # (what lies between two bf16 rounds to one of them: infinity above the largest)
+        assert x.isfinite().all()
+    pair = la.la_checkpoint(x)
+    values = _kept_equal(pair, x)
+    assert np.isfinite(values).all()
+    unit = np.repeat(2.0 ** (pair[1].cpu().numpy().astype(float) - 127), 32, -1)[:, :72]
+    assert np.all(np.abs(values - _f64(x)) <= unit / 2)
+    for out in (BF, FL):
+        back = la.la_checkpoint_restore(*pair, dtype=out)
+        assert np.array_equal(_f64(back), values)
+    again = la.la_checkpoint(la.la_checkpoint_restore(*pair, dtype=FL))
+    assert torch.equal(again[0], pair[0]) and torch.equal(again[1], pair[1])
+
+
+def test_restored_bytes_of_any_kind(la):
+    """code * step, its magnitude no more than the largest bf16; e = 0 a step of zero, e = 255 NaN."""
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    codes = torch.randint(-128, 128, (512, 64), generator=gen, device=DEV, dtype=torch.int8)
+    exps = torch.arange(1024, device=DEV).remainder(256).to(torch.uint8).view(512, 2)
+    e = exps.cpu().numpy().astype(float)
+    step = np.repeat(np.where(e == 255, np.nan, np.where(e == 0, 0.0, 2.0 ** (e - 127))), 32, -1)
+    most = 2.0 ** 128 - 2.0 ** 120
+    want = np.clip(codes.cpu().numpy() * step, -most, most)
+    for out in (BF, FL):
+        back = _f64(la.la_checkpoint_restore(codes, exps, dtype=out))
+        assert np.array_equal(back, want, equal_nan=True)
+
+
+@TYPES
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gradients_through_a_checkpoint_of_the_largest_values(la, act, dtype):
+    """a and u up to the largest finite values: da = dh u act'(a) with dh so small that it is finite. What
+    the blocks hold are whole multiples of 2^122 and 2^117: act(a) is 0 or a, its derivative 0, 1 or, at 0, 1/2."""
+    T, C, F = 4, 8, 64
+    a = torch.zeros(F, device=DEV)
+    a[0:32:4], a[1:32:4], a[2:32:4] = torch.finfo(BF).max, -3e38, 1e37
+    a[32::4], a[33::4], a[34::4] = 1e37, -9e36, 7e36
+    u = a.flip(0)
+    both = torch.stack((a, u))[None].expand(T, 2, F).contiguous()
+    pair = la.la_checkpoint(both)
+    kept = oracle.checkpoint(_f64(both))[2]
+    x, wg, wu, _ = _ffn_inputs(T, C, F, dtype)
+    dh = _randn(9, T, F, dtype=dtype, scale=2.0 ** -118)
+    got = la.la_ffn_gate_backward(x, wg, wu, dh, act, checkpoint=pair)
+    assert all(g.isfinite().all() for g in got)
+    f, df = np.maximum(kept[:, 0], 0.0), 0.5 + 0.5 * np.sign(kept[:, 0])
+    X, WG, WU, DH = (_f64(t) for t in (x, wg, wu, dh))
+    da, du = DH * kept[:, 1] * df, DH * f
+    want = da @ WG + du @ WU, da.T @ X, du.T @ X
+    tols = (np.abs(da) @ np.abs(WG) + np.abs(du) @ np.abs(WU), np.abs(da).T @ np.abs(X), np.abs(du).T @ np.abs(X))
+    for g, w, t in zip(got, want, tols):
+        # da, du rounded once, two products and the sum of at most 2 F terms before it, the result
+        assert np.all(np.abs(_f64(g) - w) <= HALF[dtype] * np.abs(w) + (HALF[dtype] + (2 * F + 8) * 2.0 ** -23) * t)
+
+
+@TYPES
+def test_norm_gradients_through_a_checkpoint_of_the_largest_values(la, dtype):
+    """Finite blocks stay finite: such a row's squares are past float32, its root zero, and dx with it."""
+    x, w, dy = _largest(dtype), _randn(2, 72, dtype=dtype), _randn(3, 12, 72, dtype=dtype)
+    x[:10, 5] = 0.0  # (a second large value, with which the row's sum is past float32 too)
+    kept = la.la_checkpoint(x)
+    dx, dw, db = la.la_layer_norm_backward(kept, w, dy)
+    assert not any(t.isnan().any() for t in (dx, dw, db))
+    plain = [10, 11]  # rows of ordinary values
+    alone = la.la_layer_norm_backward((kept[0][plain], kept[1][plain]), w, dy[plain])
+    assert torch.equal(dx[plain], alone[0])
