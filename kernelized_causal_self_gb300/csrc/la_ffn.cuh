@@ -84,7 +84,7 @@ __device__ __forceinline__ void act_grad2(float2 a, float2& f, float2& df) {
     const float2 s = sigmoid2(tanh_arg(a, q));
     f = mul2(a, s);
     const float2 dz = fma2(q, both(4.787307365f), both(1.595769122f));
-    df = fma2(mul2(f, dz), sub2(both(1.f), s), s);
+    df = fma2(mul2(f, sub2(both(1.f), s)), dz, s);  // (f dz alone is past float32 from f = 6e36 on)
   } else {
     const float2 s = sigmoid2(mul2(a, both(-1.44269504f)));
     f = mul2(a, s);

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 import oracle
-from tests.test_ffn_gpu import BF, DEV, FL, HALF, TYPES, _f64, _ffn_inputs, _kept_equal, _randn, la  # noqa: F401
+from tests.test_ffn_gpu import ACTS, BF, DEV, FL, HALF, TYPES, _f64, _ffn_inputs, _kept_equal, _randn, la  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -59,7 +59,7 @@ def test_restored_bytes_of_any_kind(la):
 
 
 @TYPES
-@pytest.mark.parametrize("act", ["silu", "gelu"])
+@ACTS
 def test_gradients_through_a_checkpoint_of_the_largest_values(la, act, dtype):
     """a and u up to the largest finite values: da = dh u act'(a) with dh so small that it is finite. What
     the blocks hold are whole multiples of 2^122 and 2^117: act(a) is 0 or a, its derivative 0, 1 or, at 0, 1/2."""
@@ -96,3 +96,26 @@ def test_norm_gradients_through_a_checkpoint_of_the_largest_values(la, dtype):
     plain = [10, 11]  # rows of ordinary values
     alone = la.la_layer_norm_backward((kept[0][plain], kept[1][plain]), w, dy[plain])
     assert torch.equal(dx[plain], alone[0])
+
+
+# ------------------------------------------------------------------------ projections
+
+@TYPES
+@ACTS
+@pytest.mark.parametrize("T", [1, 40, 2100])
+def test_gradients_of_the_largest_products(la, T, act, dtype):
+    """a of 1e34 to 3e38 and their negatives: act'(a) is 1 or 0, so that da = dh u (u = 1) or 0, finite
+    as the formula has it."""
+    F, C = 136, 16
+    a = torch.tensor([1e34, 2e36, 7e36, 3e37, 1e38, 3e38, 20.0, 1e20], device=DEV).repeat(F // 8)
+    a[::3] *= -1
+    x, wg, wu = (torch.zeros(n, C, dtype=dtype, device=DEV) for n in (T, F, F))
+    x[:, 0], wu[:, 0] = 1.0, 1.0
+    wg[:, 0] = a.to(dtype)
+    a = _f64(wg[:, 0])
+    dh = torch.zeros(T, F, dtype=dtype, device=DEV)
+    dh[0] = 0.5
+    _, dwg, dwu = la.la_ffn_gate_backward(x, wg, wu, dh, act)
+    f, df = np.maximum(a, 0.0), (a > 0).astype(float)  # (at +-20 to 4e-8)
+    assert np.all(np.abs(_f64(dwg[:, 0]) - 0.5 * df) <= HALF[dtype] + 1e-7)
+    assert np.all(np.abs(_f64(dwu[:, 0]) - 0.5 * f) <= (2 * HALF[dtype] + 2.0 ** -22) * f + 1e-7)
