@@ -507,7 +507,9 @@ int la_norm_gate_backward(const void* x, const void* z, const long long* z_strid
  * The feed-forward half of a layer. Rows are tokens: x_stride and the other *_stride are the
  * distances in elements from row to row, at least the row's length and multiples of 16 bytes;
  * a row's elements are contiguous. Pointers are 16-byte aligned, row lengths C and F multiples
- * of 8 up to 65536. Sums are float32; results are rounded to `dtype` once.
+ * of 8 up to 65536. Sums are float32; results are rounded to `dtype` once. (bf16 products on the
+ * tensor cores cut off towards zero within a sum: one of n terms of one sign is n 6e-9 of itself too
+ * small, where n counts up to 65536 terms of a forward row and up to 32768 of a gradient.)
  *
  * Activations in 8 bits (checkpoints): codes, whole numbers of -127 .. 127, and for each block of
  * 32 neighbours of a row (the last block may be shorter) a byte e, the exponent of the block's

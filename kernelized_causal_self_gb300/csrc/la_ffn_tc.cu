@@ -14,7 +14,7 @@
 //   kSums, dwg, dwu   A = da or du and B = x, both read along their rows (tokens are the sum).
 // Results go through a swizzled staging tile of 32 rows a warp and leave by TMA, which clips
 // what is past the matrix; copies past its edge read zeros, so ragged sizes need no masks.
-// Sums with few tiles are cut along k (float32 parts, added in order by a second kernel).
+// Sums with few tiles, or of many terms, are cut along k (float32 parts, added in order by a second kernel).
 //
 // Bound by the tensor cores, and by shared memory's bandwidth where a value's results are many
 // (operands alone take most of it). T 65536, C 512, F 1408: h in 115 us (1640 TFLOP/s; 131 under the
@@ -384,7 +384,10 @@ cudaError_t launch_act(const Args& a, int act, cudaStream_t st) {
                         : launch<KIND, kGeluTanh>(a, st);
 }
 
-constexpr Costs kCosts{700, 4300};
+// At most 32768 terms a part. The tensor cores' adder cuts off towards zero: a sum of n terms of one sign
+// comes out n 4.6e-9 to n 6.2e-9 of itself too small (measured, 7.6e-5 of 16384, 1.6e-3 of 262144
+// tokens, where half a step of bf16 is 3.9e-3), while parts are added in float32, rounded.
+constexpr Costs kCosts{700, 4300, 512};
 
 // a = x wg^T, u = x wu^T
 bool products(Args& a, const FfnGate& f) {

@@ -2,6 +2,8 @@
 // share: which tile of which product a pair of CTAs makes, how sums are cut, and tensor maps.
 #pragma once
 
+#include <algorithm>
+
 #include "la_checkpoint.cuh"
 #include "la_ffn.cuh"
 #include "la_internal.h"
@@ -72,7 +74,7 @@ __device__ __forceinline__ Tile tile_of(const Grids& a, uint32_t t) {
   return r;
 }
 
-// Where a split's steps begin (kForward's and kGrads' sums are not cut). At most 2^18 steps and 32 parts.
+// Where a split's steps begin (kForward's and kGrads' sums are not cut). At most 2^18 steps and 512 parts.
 __device__ __forceinline__ int first_step(const Grid& g, int split) {
   return g.splits == 1 ? (split ? g.steps : 0) : (int)((uint32_t)(g.steps * split) / (uint32_t)g.splits);
 }
@@ -83,9 +85,9 @@ enum Site { kSiteEmpty = 81, kSiteFull, kSiteAccEmpty, kSiteAccFull, kSiteDhFull
 inline int ceil_div(long long a, int b) { return (int)((a + b - 1) / b); }
 
 // What a tile of sums costs in SM clocks: 64 terms, and its results, which are written while the next tile
-// is summed
+// is summed; and the most steps that a part may have
 struct Costs {
-  int step, results;
+  int step, results, most;
 };
 
 // The grids of dx and of dwg, dwu, whose tiles one launch deals to 76 pairs of CTAs, with the sums
@@ -106,13 +108,15 @@ inline Grids count_sums_grids(int T, int C, int F, Costs cost) {
   x.steps = 2 * x.per, w.steps = ceil_div(T, 64);
   const long long nx = (long long)x.m_tiles * x.n_tiles, nw = 2LL * w.m_tiles * w.n_tiles;
   const int tried[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 14, 16, 24, 32};
+  const int least_x = ceil_div(x.steps, cost.most), least_w = ceil_div(w.steps, cost.most);
   const auto tile = [&](const Grid& g, int splits) {
     const double sums = (double)ceil_div(g.steps, splits) * cost.step + 500;
     return sums > cost.results ? sums : cost.results;
   };
   double least = 0;
-  for (int sx : tried)
-    for (int sw : tried) {
+  for (int try_x : tried)
+    for (int try_w : tried) {
+      const int sx = std::max(try_x, least_x), sw = std::max(try_w, least_w);
       if (sx > x.steps || sw > w.steps) continue;
       const long long tx = nx * sx, tw = nw * sw, more = tx % P, less = P - more;
       const double cx = tile(x, sx), cw = tile(w, sw);

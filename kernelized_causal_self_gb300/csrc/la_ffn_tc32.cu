@@ -403,7 +403,7 @@ struct Plan {
   size_t w, dact, sums, end;  // offsets in bytes
 };
 
-constexpr Costs kCosts{6 * 550, 6000};
+constexpr Costs kCosts{6 * 550, 6000, 1 << 20};  // (parts of any length: sums are taken out every 64 terms)
 
 Plan plan_of(int T, int C, int F, bool backward) {
   Plan p{};

@@ -119,3 +119,24 @@ def test_gradients_of_the_largest_products(la, T, act, dtype):
     f, df = np.maximum(a, 0.0), (a > 0).astype(float)  # (at +-20 to 4e-8)
     assert np.all(np.abs(_f64(dwg[:, 0]) - 0.5 * df) <= HALF[dtype] + 1e-7)
     assert np.all(np.abs(_f64(dwu[:, 0]) - 0.5 * f) <= (2 * HALF[dtype] + 2.0 ** -22) * f + 1e-7)
+
+
+def test_sums_of_many_tokens_do_not_drift(la):
+    """dwu of T equal positive terms, T = 3 * 2^18. The tensor cores' adder cuts off towards zero: an
+    addition of 16 terms loses one to two units, 2^-23 of the sum so far, which grows evenly. A part of
+    n terms is n / 16 * 2^-23 of itself too small, by two units, and parts are added in float32, rounded
+    (24 of them: 2^-20). With n = 32768 at most the mean loss is 2^-12. The results' own rounding to bf16 is up
+    as often as down: 128 x 128 different products, each off by up to 2^-8, evenly, are off by 2^-8 / sqrt(3 2^14) =
+    2^-15.8 in the mean, and four times that is 2^-13.8. One part of 2^18 terms or more loses 1.3e-3 > 2^-10."""
+    T, C, F = 3 << 18, 512, 1408
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    v, d = ((torch.rand(n, generator=gen, device=DEV) + 1).to(BF) for n in (C, F))
+    v[0] = 1.0
+    x, dh = v.expand(T, C).contiguous(), d.expand(T, F).contiguous()
+    wg, wu = torch.zeros(F, C, dtype=BF, device=DEV), torch.zeros(F, C, dtype=BF, device=DEV)
+    wg[:, 0] = 32.0  # a = 32, silu(a) = 32 to 2^-45, u = 0
+    dx, dwg, dwu = la.la_ffn_gate_backward(x, wg, wu, dh)
+    rel = dwu.double() / (32.0 * T * d.double()[:, None] * v.double()[None]) - 1
+    assert abs(rel.mean().item()) <= 2.0 ** -12 + 2.0 ** -13
+    assert rel.abs().max().item() <= HALF[BF] + 32768 * 2.0 ** -23
+    assert not dwg.any() and torch.equal(dx[0], dx[-1])
