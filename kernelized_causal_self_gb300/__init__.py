@@ -1146,6 +1146,13 @@ def _marshal():
 _ACTIVATIONS = {"silu": LA_SILU, "gelu": LA_GELU, "gelu_tanh": LA_GELU_TANH}
 
 
+def _c_sizes(fn, *sizes):
+    """Sizes that pass as a C int, which ctypes would otherwise cut to their low 32 bits."""
+    for n in sizes:
+        if not -0x80000000 <= n <= 0x7fffffff:
+            raise ValueError(f"{fn}: a size of {n} is past 32 bits")
+
+
 def _token_rows(fn, name, t):
     """(rows, distance from row to row in elements) of t [..., C], its leading dimensions taken as
     one; rows lie evenly apart and do not overlap."""
@@ -1153,6 +1160,8 @@ def _token_rows(fn, name, t):
     if not shape:
         raise ValueError(f"{fn}: {name} must have at least 1 dimension")
     C = shape[-1]
+    if C > 0x7fffffff:
+        _c_sizes(fn, C)
     if t.is_contiguous():
         return (t.numel() // C if C else 0), C
     stride = t.stride()
@@ -1270,6 +1279,7 @@ def la_checkpoint_restore(codes, exps, dtype=None, out=None):
 
 
 def la_layer_norm_workspace_bytes(rows, C):
+    _c_sizes("la_layer_norm_workspace_bytes", C)
     return load_library().la_layer_norm_workspace_bytes(rows, C)
 
 
@@ -1352,10 +1362,12 @@ def la_layer_norm_backward(x, w, dy, eps=1e-5, dx=None, dw=None, db=None, worksp
 
 
 def la_ffn_gate_workspace_bytes(T, C, F, checkpoint=False, dtype=LA_BF16):
+    _c_sizes("la_ffn_gate_workspace_bytes", T, C, F)
     return load_library().la_ffn_gate_workspace_bytes(T, C, F, int(bool(checkpoint)), dtype)
 
 
 def la_ffn_gate_backward_workspace_bytes(T, C, F, dtype=LA_BF16):
+    _c_sizes("la_ffn_gate_backward_workspace_bytes", T, C, F)
     return load_library().la_ffn_gate_backward_workspace_bytes(T, C, F, dtype)
 
 
@@ -1369,6 +1381,8 @@ def _ffn_checks(fn, x, wg, wu, activation):
     if len(shape) != 2:
         raise ValueError(f"{fn}: x must be [..., C] and wg [F, C]")
     F, C = shape
+    if rows > 0x7fffffff or F > 0x7fffffff:
+        _c_sizes(fn, rows, F)
     if C != x.shape[-1] or wg.dtype != dtype:
         _expect(fn, "wg", wg, (F, x.shape[-1]), dtype)
     if wu.shape != shape or wu.dtype != dtype:
