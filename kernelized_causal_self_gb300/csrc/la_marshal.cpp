@@ -41,6 +41,29 @@ static_assert(sizeof(Library) == sizeof(kNames), "one pointer for each name");
 
 PyObject* other() { Py_RETURN_NOTIMPLEMENTED; }
 
+// Allocations and the library's calls run without Python's lock: a launch waits while its stream's queue
+// is full, an allocation may wait for the GPU, and other threads (which the GPU may wait for) go on.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// f() without the lock
+template <typename F>
+auto unlocked(F f) {
+  Unlocked u;
+  return f();
+}
+
+// A C int, -1 for what is none
+int int_of(PyObject* o) {
+  const long v = PyLong_AsLong(o);
+  if (v == -1 && PyErr_Occurred()) PyErr_Clear();
+  return v < -1 || v > 0x7fffffff ? -1 : (int)v;
+}
+
 // What a call's tensors have in common
 struct Call {
   c10::DeviceIndex device = -1;
@@ -91,8 +114,9 @@ struct Call {
   at::Tensor empty(at::IntArrayRef sizes, at::ScalarType t) const {
     return at::Tensor(at::detail::empty_cuda(sizes, t, at::Device(at::kCUDA, device), std::nullopt));
   }
-  at::Tensor given_or_empty(PyObject* o, at::IntArrayRef sizes) {
-    if (o == Py_None) return ok ? empty(sizes, type) : at::Tensor();
+  // what is given, or undefined for None
+  at::Tensor given(PyObject* o, at::IntArrayRef sizes) {
+    if (o == Py_None) return at::Tensor();
     const at::Tensor* t = like(o, sizes);
     return ok ? *t : at::Tensor();
   }
@@ -140,10 +164,13 @@ PyObject* checkpoint(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t C = x->size(-1);
     c10::SmallVector<int64_t, 6> blocks(x->sizes().begin(), x->sizes().end());
     blocks.back() = (C + 31) / 32;
-    at::Tensor codes = c.empty(x->sizes(), at::kChar), exps = c.empty(blocks, at::kByte);
-    if (!fits(C) || lib.checkpoint(x->data_ptr(), C, codes_of(&codes), exps_of(&exps), rows_of(*x, C), (int)C, c.dtype,
-                                   c.stream()) != LA_OK)
-      return other();
+    if (!fits(C)) return other();
+    at::Tensor codes, exps;
+    const int status = unlocked([&] {
+      codes = c.empty(x->sizes(), at::kChar), exps = c.empty(blocks, at::kByte);
+      return lib.checkpoint(x->data_ptr(), C, codes_of(&codes), exps_of(&exps), rows_of(*x, C), (int)C, c.dtype, c.stream());
+    });
+    if (status != LA_OK) return other();
     return tuple({codes, exps});
   });
 }
@@ -156,16 +183,19 @@ PyObject* checkpoint_restore(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor* codes = c.plain(a[0]);
     if (!c.ok || !codes->is_cuda() || codes->dim() < 1 || codes->scalar_type() != at::kChar) return other();
     c.device = codes->get_device();
-    c.dtype = (int)PyLong_AsLong(a[2]);
+    c.dtype = int_of(a[2]);
     if (c.device != c10::cuda::current_device() || (c.dtype != LA_F32 && c.dtype != LA_BF16)) return other();
     const int64_t C = codes->size(-1);
     c10::SmallVector<int64_t, 6> blocks(codes->sizes().begin(), codes->sizes().end());
     blocks.back() = (C + 31) / 32;
     const at::Tensor* exps = c.typed(a[1], blocks, at::kByte);
     if (!c.ok || !fits(C)) return other();
-    at::Tensor out = c.empty(codes->sizes(), c.dtype == LA_F32 ? at::kFloat : at::kBFloat16);
-    if (lib.restore(codes_of(codes), exps_of(exps), out.data_ptr(), C, rows_of(*codes, C), (int)C, c.dtype, c.stream()) != LA_OK)
-      return other();
+    at::Tensor out;
+    const int status = unlocked([&] {
+      out = c.empty(codes->sizes(), c.dtype == LA_F32 ? at::kFloat : at::kBFloat16);
+      return lib.restore(codes_of(codes), exps_of(exps), out.data_ptr(), C, rows_of(*codes, C), (int)C, c.dtype, c.stream());
+    });
+    if (status != LA_OK) return other();
     return THPVariable_Wrap(out);
   });
 }
@@ -182,10 +212,15 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor *b = c.ok && a[2] != Py_None ? c.like(a[2], {C}) : nullptr, *codes = nullptr, *exps = nullptr;
     if (c.ok) c.pair(a[5], x->sizes(), codes, exps);
     if (!c.ok || !fits(C)) return other();
-    at::Tensor out = c.given_or_empty(a[4], x->sizes());
-    if (!c.ok || lib.norm(x->data_ptr(), C, ptr(w), ptr(b), out.data_ptr(), C, codes_of(codes), exps_of(exps), rows_of(*x, C),
-                          (int)C, (float)PyFloat_AS_DOUBLE(a[3]), c.dtype, c.stream()) != LA_OK)
-      return other();
+    at::Tensor out = c.given(a[4], x->sizes());
+    if (!c.ok) return other();
+    const float eps = (float)PyFloat_AS_DOUBLE(a[3]);
+    const int status = unlocked([&] {
+      if (!out.defined()) out = c.empty(x->sizes(), c.type);
+      return lib.norm(x->data_ptr(), C, ptr(w), ptr(b), out.data_ptr(), C, codes_of(codes), exps_of(exps), rows_of(*x, C),
+                      (int)C, eps, c.dtype, c.stream());
+    });
+    if (status != LA_OK) return other();
     return THPVariable_Wrap(out);
   });
 }
@@ -205,13 +240,16 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       x = c.like(a[0], dy->sizes());
     const long long rows = rows_of(*dy, C);
     if (!c.ok || !fits(C)) return other();
-    at::Tensor dx = c.empty(dy->sizes(), c.type), dw = c.empty({C}, c.type), db = c.empty({C}, c.type);
-    const size_t bytes = lib.norm_bytes(rows, (int)C);
-    const c10::DataPtr ws = c.scratch(bytes);
-    if (lib.norm_backward(ptr(x), C, codes_of(codes), exps_of(exps), ptr(w), dy->data_ptr(), C, dx.data_ptr(), C,
-                          dw.data_ptr(), db.data_ptr(), rows, (int)C, (float)PyFloat_AS_DOUBLE(a[3]), c.dtype, ws.get(),
-                          bytes, c.stream()) != LA_OK)
-      return other();
+    at::Tensor dx, dw, db;
+    const float eps = (float)PyFloat_AS_DOUBLE(a[3]);
+    const int status = unlocked([&] {
+      dx = c.empty(dy->sizes(), c.type), dw = c.empty({C}, c.type), db = c.empty({C}, c.type);
+      const size_t bytes = lib.norm_bytes(rows, (int)C);
+      const c10::DataPtr ws = c.scratch(bytes);
+      return lib.norm_backward(ptr(x), C, codes_of(codes), exps_of(exps), ptr(w), dy->data_ptr(), C, dx.data_ptr(), C,
+                               dw.data_ptr(), db.data_ptr(), rows, (int)C, eps, c.dtype, ws.get(), bytes, c.stream());
+    });
+    if (status != LA_OK) return other();
     return tuple({dx, dw, db});
   });
 }
@@ -252,13 +290,18 @@ PyObject* ffn_gate(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor *codes = nullptr, *exps = nullptr;
     if (c.ok) c.pair(a[5], f.hidden(true), codes, exps);
     if (!c.ok) return other();
-    at::Tensor out = c.given_or_empty(a[4], f.hidden(false));
+    const auto hidden = f.hidden(false);
+    at::Tensor out = c.given(a[4], hidden);
     if (!c.ok) return other();
-    const size_t bytes = lib.ffn_bytes((int)f.rows, (int)f.C, (int)f.F, codes != nullptr, c.dtype);
-    const c10::DataPtr ws = c.scratch(bytes);
-    if (lib.ffn(f.x->data_ptr(), f.C, ptr(f.wg), ptr(f.wu), out.data_ptr(), f.F, codes_of(codes), exps_of(exps),
-                (int)f.rows, (int)f.C, (int)f.F, (int)PyLong_AsLong(a[3]), c.dtype, ws.get(), bytes, c.stream()) != LA_OK)
-      return other();
+    const int act = int_of(a[3]);
+    const int status = unlocked([&] {
+      if (!out.defined()) out = c.empty(hidden, c.type);
+      const size_t bytes = lib.ffn_bytes((int)f.rows, (int)f.C, (int)f.F, codes != nullptr, c.dtype);
+      const c10::DataPtr ws = c.scratch(bytes);
+      return lib.ffn(f.x->data_ptr(), f.C, ptr(f.wg), ptr(f.wu), out.data_ptr(), f.F, codes_of(codes), exps_of(exps),
+                     (int)f.rows, (int)f.C, (int)f.F, act, c.dtype, ws.get(), bytes, c.stream());
+    });
+    if (status != LA_OK) return other();
     return THPVariable_Wrap(out);
   });
 }
@@ -272,13 +315,17 @@ PyObject* ffn_gate_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor *codes = nullptr, *exps = nullptr, *dh = c.ok ? c.like(a[4], f.hidden(false)) : nullptr;
     if (c.ok) c.pair(a[5], f.hidden(true), codes, exps);
     if (!c.ok) return other();
-    at::Tensor dx = c.empty(f.x->sizes(), c.type), dwg = c.empty({f.F, f.C}, c.type), dwu = c.empty({f.F, f.C}, c.type);
-    const size_t bytes = lib.ffn_backward_bytes((int)f.rows, (int)f.C, (int)f.F, c.dtype);
-    const c10::DataPtr ws = c.scratch(bytes);
-    if (lib.ffn_backward(f.x->data_ptr(), f.C, ptr(f.wg), ptr(f.wu), ptr(dh), f.F, codes_of(codes), exps_of(exps),
-                         dx.data_ptr(), f.C, dwg.data_ptr(), dwu.data_ptr(), (int)f.rows, (int)f.C, (int)f.F,
-                         (int)PyLong_AsLong(a[3]), c.dtype, ws.get(), bytes, c.stream()) != LA_OK)
-      return other();
+    at::Tensor dx, dwg, dwu;
+    const int act = int_of(a[3]);
+    const int status = unlocked([&] {
+      dx = c.empty(f.x->sizes(), c.type), dwg = c.empty({f.F, f.C}, c.type), dwu = c.empty({f.F, f.C}, c.type);
+      const size_t bytes = lib.ffn_backward_bytes((int)f.rows, (int)f.C, (int)f.F, c.dtype);
+      const c10::DataPtr ws = c.scratch(bytes);
+      return lib.ffn_backward(f.x->data_ptr(), f.C, ptr(f.wg), ptr(f.wu), ptr(dh), f.F, codes_of(codes), exps_of(exps),
+                              dx.data_ptr(), f.C, dwg.data_ptr(), dwu.data_ptr(), (int)f.rows, (int)f.C, (int)f.F, act,
+                              c.dtype, ws.get(), bytes, c.stream());
+    });
+    if (status != LA_OK) return other();
     return tuple({dx, dwg, dwu});
   });
 }

@@ -1,6 +1,9 @@
 """The feed-forward half's calls at the ends of what they take, on the GPU against the float64 oracle.
 Bounds as in test_ffn_gpu.py where no others are given."""
 
+import threading
+import time
+
 import numpy as np
 import pytest
 
@@ -140,3 +143,39 @@ def test_sums_of_many_tokens_do_not_drift(la):
     assert abs(rel.mean().item()) <= 2.0 ** -12 + 2.0 ** -13
     assert rel.abs().max().item() <= HALF[BF] + 32768 * 2.0 ** -23
     assert not dwg.any() and torch.equal(dx[0], dx[-1])
+
+
+# ------------------------------------------------------------------------------ threads
+
+def test_other_threads_run_while_a_call_waits(la):
+    """A launch waits while the stream's queue is full: here behind a kernel of about a second, which ends
+    by itself. Another Python thread goes on meanwhile."""
+    x = _randn(1, 4, 64, dtype=BF)
+    la.la_checkpoint(x)
+    torch.cuda.synchronize()
+    ticks, stop = [], threading.Event()
+
+    def tick():
+        while not stop.is_set():
+            ticks.append(time.perf_counter())
+            time.sleep(0.002)
+    other = threading.Thread(target=tick)
+    other.start()
+    try:
+        torch.cuda._sleep(2_000_000_000)
+        start = time.perf_counter()
+        longest = 0.0
+        for _ in range(20000):
+            t = time.perf_counter()
+            la.la_checkpoint(x)
+            longest = max(longest, time.perf_counter() - t)
+            if longest > 0.3 or time.perf_counter() - start > 5.0:
+                break
+    finally:
+        stop.set()
+        other.join()
+        torch.cuda.synchronize()
+    if longest <= 0.3:
+        pytest.skip("the stream's queue did not fill")
+    gaps = np.diff(ticks)
+    assert gaps.max() < longest / 2, (gaps.max(), longest)
