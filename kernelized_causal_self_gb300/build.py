@@ -3,13 +3,16 @@
 Compiles every ``csrc/*.cu`` to an object in parallel with nvcc, then links
 ``_build/liblagb300.so``. The library is a plain C ABI (``include/la.h``):
 CUDA runtime linked statically, driver entry points resolved at run time,
-so the shared object loads on a machine without a GPU. ``csrc/la_marshal.cpp``, which
-marshals the binding's most frequent calls, is compiled beside them with g++ against the
-installed torch into ``_build/la_marshal.so`` (it reaches the library through pointers).
+so the shared object loads on a machine without a GPU: nvcc is all it takes.
+``csrc/la_marshal.cpp``, which marshals the binding's most frequent calls, is compiled beside
+them with g++ against the installed torch into ``_build/la_marshal.so`` (it reaches the library
+through pointers), again for another torch or Python. Where torch is not installed it is left
+out; where it does not compile the library is there all the same, and the build says so.
 """
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -41,19 +44,40 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    pats = ("*.cu", "*.cuh", "*.h", "*.cpp")
-    files = [f for p in pats for f in glob.glob(os.path.join(CSRC, p))]
-    files += glob.glob(os.path.join(ROOT, "include", "*.h"))
-    files.append(os.path.abspath(__file__))
-    return files
+def _newer(built, *patterns):
+    """Whether `built` exists and no file of the patterns is newer."""
+    if not os.path.exists(built):
+        return False
+    files = [f for p in patterns for f in glob.glob(p)]
+    return all(os.path.getmtime(f) <= os.path.getmtime(built) for f in (*files, os.path.abspath(__file__)))
+
+
+def _lib_up_to_date():
+    return _newer(LIB, *(os.path.join(CSRC, p) for p in ("*.cu", "*.cuh", "*.h")), os.path.join(ROOT, "include", "*.h"))
+
+
+def _made_for():
+    """The torch and the Python that la_marshal.so is made for (None: no torch)."""
+    try:
+        return f"torch {importlib.metadata.version('torch')}, {sys.implementation.cache_tag}"
+    except importlib.metadata.PackageNotFoundError:
+        return None
+
+
+def _marshal_up_to_date():
+    want = _made_for()
+    if want is None:
+        return True
+    try:
+        with open(MARSHAL + ".for") as f:
+            made = f.read()
+    except OSError:
+        return False
+    return made == want and _newer(MARSHAL, os.path.join(CSRC, "la_marshal.cpp"), os.path.join(ROOT, "include", "*.h"))
 
 
 def up_to_date():
-    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    return _lib_up_to_date() and _marshal_up_to_date()
 
 
 def _marshal_command(out):
@@ -72,39 +96,58 @@ def _marshal_command(out):
             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
 
 
-def build(force=False, verbose=False, extra_flags=()):
-    """Build the shared library if any source is newer; returns its path."""
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
+def _run(cmd):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    return r.returncode, r.stdout + r.stderr
+
+
+def _build_marshal():
+    """Compiles la_marshal.so; the compiler's complaint if it does not."""
+    out, made = MARSHAL + ".tmp", _made_for()
+    try:
+        rc, text = _run(_marshal_command(out))
+    except (ImportError, AttributeError, OSError) as e:  # (a torch that does not load, no g++)
+        return f"{type(e).__name__}: {e}"
+    if rc != 0:
+        return text
+    os.replace(out, MARSHAL)
+    with open(MARSHAL + ".for", "w") as f:
+        f.write(made)
+    return None
+
+
+def _build_lib(ex, verbose, extra_flags):
     nvcc = _nvcc()
     srcs = _sources()
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
-
-    def compile_one(pair):
-        src, obj = pair
-        cmd = (_marshal_command(obj) if src.endswith(".cpp")
-               else [nvcc, *NVCC_FLAGS, *extra_flags, "-c", src, "-o", obj])
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        return src, r.returncode, r.stdout + r.stderr
-
-    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        pairs = [(os.path.join(CSRC, "la_marshal.cpp"), MARSHAL + ".tmp"), *zip(srcs, objs)]
-        results = list(ex.map(compile_one, pairs))
-    failed = [(s, out) for s, rc, out in results if rc != 0]
-    for s, rc, out in results:
-        if verbose and out.strip():
-            sys.stderr.write(f"--- {os.path.basename(s)}\n{out}")
+    results = list(ex.map(lambda pair: _run([nvcc, *NVCC_FLAGS, *extra_flags, "-c", pair[0], "-o", pair[1]]),
+                          zip(srcs, objs)))
+    said = [f"--- {os.path.basename(s)}\n{out}" for s, (rc, out) in zip(srcs, results) if out.strip()]
+    if verbose:
+        sys.stderr.write("".join(said))
+    failed = [f"--- {os.path.basename(s)}\n{out}" for s, (rc, out) in zip(srcs, results) if rc != 0]
     if failed:
-        msg = "\n".join(f"--- {os.path.basename(s)}\n{out}" for s, out in failed)
-        raise RuntimeError("compilation failed:\n" + msg)
+        raise RuntimeError("compilation failed:\n" + "\n".join(failed))
     tmp = LIB + ".tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
+    rc, out = _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"])
+    if rc != 0:
+        raise RuntimeError("link failed:\n" + out)
     os.replace(tmp, LIB)
-    os.replace(MARSHAL + ".tmp", MARSHAL)
+
+
+def build(force=False, verbose=False, extra_flags=()):
+    """Build what is older than its sources; returns the library's path."""
+    lib, marshal = force or not _lib_up_to_date(), force and _made_for() is not None or not _marshal_up_to_date()
+    if not lib and not marshal:
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        pending = ex.submit(_build_marshal) if marshal else None
+        if lib:
+            _build_lib(ex, verbose, extra_flags)
+        failed = pending.result() if pending else None
+    if failed:
+        raise RuntimeError(f"the library is built, {LIB}, but la_marshal.cpp, a part of the Python binding, is not:\n{failed}")
     return LIB
 
 
