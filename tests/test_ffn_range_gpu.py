@@ -8,7 +8,8 @@ import numpy as np
 import pytest
 
 import oracle
-from tests.test_ffn_gpu import ACTS, BF, DEV, FL, HALF, TYPES, _f64, _ffn_inputs, _kept_equal, _randn, la  # noqa: F401
+from tests.test_ffn_gpu import (ACTS, BF, DEV, FL, HALF, TYPES, _f64, _ffn_close, _ffn_grads_close, _ffn_inputs,  # noqa: F401
+                                _kept_equal, _kept_like, _randn, la)
 
 pytestmark = pytest.mark.gpu
 
@@ -122,6 +123,34 @@ def test_gradients_of_the_largest_products(la, T, act, dtype):
     f, df = np.maximum(a, 0.0), (a > 0).astype(float)  # (at +-20 to 4e-8)
     assert np.all(np.abs(_f64(dwg[:, 0]) - 0.5 * df) <= HALF[dtype] + 1e-7)
     assert np.all(np.abs(_f64(dwu[:, 0]) - 0.5 * f) <= (2 * HALF[dtype] + 2.0 ** -22) * f + 1e-7)
+
+
+@TYPES
+@pytest.mark.parametrize("kept", [False, True], ids=["recomputed", "kept"])
+@pytest.mark.parametrize("size, act", [((2600, 520, 2056), "silu"), ((3000, 456, 2184), "gelu"), ((2313, 392, 2824), "gelu_tanh")],
+                         ids=["t2600c520f2056", "t3000c456f2184", "t2313c392f2824"])
+def test_many_tiles_for_each_pair(la, size, act, kept, dtype):
+    """More than two tiles of h, and of da and du, for each of 76 pairs of CTAs, and more steps of 64 than
+    stages: accumulators, stages, staging tiles and dh's tiles are all used again. Every row is compared."""
+    T, C, F = size
+    assert -(-T // 256) * -(-F // 128) > 2 * 76 and C > 6 * 64
+    x, wg, wu, dh = _ffn_inputs(*size, dtype)
+    pair = _kept_like(T, 2, F) if kept else None
+    h = la.la_ffn_gate(x, wg, wu, act, checkpoint=pair)
+    _ffn_close(h, x, wg, wu, act, dtype)
+    values = None
+    if kept:
+        au = _f64(la.la_checkpoint_restore(*pair, dtype=FL))
+        values = au[:, 0], au[:, 1]
+        unit = np.repeat(2.0 ** (pair[1].cpu().numpy().astype(float) - 127), 32, -1)[..., :F]
+        X = _f64(x)
+        for i, w in enumerate((wg, wu)):
+            off = C * 2.0 ** -23 * (np.abs(X) @ np.abs(_f64(w)).T)
+            assert np.all(np.abs(au[:, i] - X @ _f64(w).T) <= unit[:, i] / 2 + off)
+    grads = la.la_ffn_gate_backward(x, wg, wu, dh, act, checkpoint=pair)
+    _ffn_grads_close(grads, x, wg, wu, dh, act, dtype, values)
+    again = la.la_ffn_gate_backward(x, wg, wu, dh, act, checkpoint=pair)
+    assert all(torch.equal(p, q) for p, q in zip(grads, again))
 
 
 def test_sums_of_many_tokens_do_not_drift(la):
