@@ -174,6 +174,63 @@ def test_sums_of_many_tokens_do_not_drift(la):
     assert not dwg.any() and torch.equal(dx[0], dx[-1])
 
 
+def _grid(act):
+    """Whole multiples of a power of two, 8 bits each: exact in bf16, and as x w with x = 1."""
+    top, step = (80.0, 0.5) if act == "silu" else (13.0, 0.0625) if act == "gelu" else (5.0, 0.03125)
+    a = np.arange(-top, top + step, step)
+    return np.concatenate([a, np.full(-len(a) % 8, 1.0)])
+
+
+def _act_bound(a, act):
+    """Relative error of act(a) in float32, in steps of 2^-24, by the roundings on the way. A base-2
+    exponential and a reciprocal are off by 4, a product, sum or constant by 1.
+    silu: the exponent by 2 |a| (constant, product), the sigmoid by that, 4 + 1 + 4, and two products.
+    gelu_tanh: z by 6 of itself (constants and products), then the same.
+    gelu: a^2 / 2 by 3 of itself (constant, two products), exponential 4, reciprocal 4 + 3 of its
+    argument; the polynomial of 8 terms, 2 for its fit, 2 roundings a term of twice its sum at most; 3
+    products behind it."""
+    if act == "silu":
+        return 2 * np.abs(a) + 12
+    if act == "gelu":
+        return 1.5 * a * a + 4 + 7 * 2 + 2 + 32 + 3
+    z = 2 * np.sqrt(2 / np.pi) * (a + 0.044715 * a ** 3)
+    return 6 * np.abs(z) + 12
+
+
+@TYPES
+@ACTS
+@pytest.mark.parametrize("T", [1, 5, 1000])
+def test_activations_far_from_zero_keep_their_digits(la, T, act, dtype):
+    """h, da and du where act(a) is small: with x = (1, 0, ...) and wu = (1, 0, ...) a is wg's first column
+    and u = 1 in every kernel, without an error, and dwg = da, dwu = du of the first token."""
+    a = _grid(act)
+    F, C = len(a), 16
+    x, wg, wu = (torch.zeros(n, C, dtype=dtype, device=DEV) for n in (T, F, F))
+    x[:, 0], wu[:, 0] = 1.0, 1.0
+    wg[:, 0] = torch.from_numpy(a).to(DEV).to(dtype)
+    assert np.array_equal(_f64(wg[:, 0]), a)
+    dh = torch.zeros(T, F, dtype=dtype, device=DEV)
+    dh[0] = 1.0
+    h = la.la_ffn_gate(x, wg, wu, act)
+    _, dwg, dwu = la.la_ffn_gate_backward(x, wg, wu, dh, act)
+    f, df = oracle.activation(a, act)
+    off = _act_bound(a, act) * 2.0 ** -24
+    least = 100 * 2.0 ** -126  # what is below is zero
+    half = HALF[dtype]
+    assert np.all(np.abs(_f64(h) - f) <= (half + off) * np.abs(f) + least)
+    # (sums of one term and zeros, in bf16 of rounded da and du; the result's own rounding; 2^-22 as a sum)
+    own = 2 * half + 2.0 ** -22
+    assert np.all(np.abs(_f64(dwu[:, 0]) - f) <= (own + off) * np.abs(f) + least)
+    # act' is a sum s + a s (1 - s) z' (gelu: P + a e), whose terms are off by `off` and three products, and
+    # 1 - s by 1 step of 1
+    s = np.where(a == 0, 0.5, f / np.where(a == 0, 1.0, a))
+    terms = np.abs(s) + np.abs(df - s)
+    one = np.abs(f) * (1.0 if act != "gelu_tanh" else 1.6 * (1 + 0.14 * a * a))
+    tol = own * np.abs(df) + (off + 4 * 2.0 ** -24) * terms + 2.0 ** -24 * one + least
+    assert np.all(np.abs(_f64(dwg[:, 0]) - df) <= tol)
+    assert not dwg[:, 1:].any() and not dwu[:, 1:].any()
+
+
 # ------------------------------------------------------------------------------ threads
 
 def test_other_threads_run_while_a_call_waits(la):
