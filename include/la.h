@@ -562,7 +562,9 @@ size_t la_ffn_gate_backward_workspace_bytes(int T, int C, int F, int dtype);
  * product: h = act(a) * u with a = x wg^T and u = x wu^T. x: T rows of C; wg, wu [F][C]
  * contiguous; h: T rows of F. act: enum la_activation. T <= 2^24. codes [T][2][F], exps
  * [T][2][ceil(F / 32)]: a checkpoint of a and u to be written, or nullptr both. Outputs share no
- * memory with inputs. In float32 a row with an infinity may give NaN where an infinity is due.
+ * memory with inputs. In float32 a row of x, wg or wu with an infinity gives NaN where an infinity is
+ * due, its largest of three parts being infinite and the others NaN, but in a call of T == 1 without a
+ * checkpoint, which multiplies float32.
  */
 int la_ffn_gate(const void* x, long long x_stride, const void* wg, const void* wu, void* h, long long h_stride,
                 signed char* codes, unsigned char* exps, int T, int C, int F, int act, int dtype, void* workspace,

@@ -17,6 +17,7 @@
 // the largest products' sums are taken out every 32 terms, and the others', 2^-8 of them, kept apart.
 // The next pieces are asked for before one is used: 8, 16 and 32 tokens 19.7, 26.3, 36.1 us (all loads
 // first 21.3, 30.9, 41.5), 64 67, which mma.sync's rate then bounds; on the CUDA cores 8 took 25.7.
+// (Parts of an infinity are an infinity and NaN: only the CUDA cores' one token gives infinities.)
 #include "la_ffn.cuh"
 #include "la_internal.h"
 #include "la_tc_common.cuh"

@@ -231,6 +231,41 @@ def test_activations_far_from_zero_keep_their_digits(la, T, act, dtype):
     assert not dwg[:, 1:].any() and not dwu[:, 1:].any()
 
 
+@TYPES
+@pytest.mark.parametrize("T", [1, 2, 40, 1600])
+@pytest.mark.parametrize("kept", [False, True], ids=["recomputed", "kept"])
+def test_a_row_with_an_infinity(la, T, kept, dtype):
+    """bf16 gives what the formula gives: a = +inf and u = +-inf multiply to infinities, a = -inf gives NaN.
+    float32 gives NaN for those infinities, but for a call of one token without a checkpoint. The other rows stay
+    as they were."""
+    C, F = 136, 200
+    x, wg, wu, dh = _ffn_inputs(T, C, F, dtype)
+    bad = T // 2
+    for value in (float("inf"), -float("inf")):
+        y = x.clone()
+        y[bad, 3] = value
+        pair, clean = (_kept_like(T, 2, F) if kept else None for _ in range(2))
+        want = la.la_ffn_gate(x, wg, wu, checkpoint=clean)
+        h = la.la_ffn_gate(y, wg, wu, checkpoint=pair)
+        rows = [i for i in range(T) if i != bad]
+        assert torch.equal(h[rows], want[rows])
+        a, u = (value * np.sign(_f64(w[:, 3])) for w in (wg, wu))
+        due = np.where(a > 0, u, np.nan)
+        got = _f64(h[bad])
+        assert not np.isfinite(got).any()
+        if dtype == BF or (T == 1 and not kept):
+            assert np.array_equal(got, due, equal_nan=True)
+        else:
+            assert np.isnan(got).all()
+        if kept:
+            assert torch.all(pair[1][bad] == 255) and torch.equal(pair[1][rows], clean[1][rows])
+            assert torch.equal(pair[0][rows], clean[0][rows])
+        ref = la.la_ffn_gate_backward(x, wg, wu, dh, checkpoint=clean)
+        dx, dwg, dwu = la.la_ffn_gate_backward(y, wg, wu, dh, checkpoint=pair)
+        assert torch.equal(dx[rows], ref[0][rows])
+        assert not dx[bad].isfinite().any() and not dwg.isfinite().any()
+
+
 # ------------------------------------------------------------------------------ threads
 
 def test_other_threads_run_while_a_call_waits(la):
