@@ -531,7 +531,8 @@ int la_checkpoint_restore(const signed char* codes, const unsigned char* exps, v
 /*
  * la_layer_norm -- y = (x - mean) / sqrt(var + eps) * w + b, mean and variance over the C
  * elements of each row (C <= 16384; var is the mean of squared deviations). w, b: [C] (b may be
- * nullptr: zero). y may be x itself (same pointer and stride), and shares memory with no other
+ * nullptr: zero). Sums and squares are float32: a row whose squared deviations add up to more than 2^128
+ * has y = b, one whose elements do NaN. y may be x itself (same pointer and stride), and shares memory with no other
  * argument. codes, exps: a checkpoint of x to be written, or nullptr both. eps >= 0.
  */
 int la_layer_norm(const void* x, long long x_stride, const void* w, const void* b, void* y, long long y_stride,

@@ -1,5 +1,5 @@
 // The gated projections of a few tokens (serving: one of each stream), h = act(x wg^T) (x wu^T), and
-// da, du of the backward pass from the same products.
+// da, du of the backward pass from the same products (in bf16 rounded to it once, as in la_ffn_tc.cu).
 // Bound by the weights' bytes, which are read once: a CTA takes some rows f of wg and the same of
 // wu, its eight warps share their elements, and the sums are joined in shared memory in order, so
 // that a and u meet in one thread.

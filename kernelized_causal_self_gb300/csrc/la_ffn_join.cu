@@ -1,6 +1,6 @@
 // What the gated projections' backward passes need beside their products: da = dh u act'(a) and
-// du = dh act(a) from a checkpoint of a and u, and the parts of cut sums added in order. Both are
-// bound by memory.
+// du = dh act(a) from a checkpoint of a and u (rounded to bf16 once in bf16, as in la_ffn_tc.cu, three
+// parts in float32), and the parts of cut sums added in order. Both are bound by memory.
 #include "la_checkpoint.cuh"
 #include "la_ffn.cuh"
 #include "la_internal.h"

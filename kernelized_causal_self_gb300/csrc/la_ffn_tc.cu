@@ -1,6 +1,9 @@
 // The gated projections in bf16 on the tensor cores: a = x wg^T, u = x wu^T, h = act(a) u, and
 // the backward pass da = dh u act'(a), du = dh act(a), dx = da wg + du wu, dwg = da^T x,
-// dwu = du^T x (da and du in bf16, in the workspace).
+// dwu = du^T x (da and du in bf16, in the workspace). da and du have to be bf16 for the tensor cores to
+// multiply them: a second term of each would double the sums' multiplications, two thirds of the whole.
+// It costs half a step, 2^-8, of every factor: dx, dwg, dwu of random data are 2.35e-3 off in the
+// 2-norm where results of float32 factors, rounded themselves, are 1.66e-3.
 //
 // One persistent kernel for all five products (in two launches, dx and the weights' in one). A
 // pair of CTAs (cta_group::2) makes a tile of 256 x 256: each CTA copies its 128 rows of A and its

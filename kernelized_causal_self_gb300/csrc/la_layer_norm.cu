@@ -320,7 +320,9 @@ int threads_per_row(int C) {
 // CTAs: twice the three that an SM holds, the backward pass's two (whose sums cost per CTA), fewer
 // where rows are few. 65536 x 512 in bf16: 24.6 us (5.5 TB/s) with three CTAs of 80 registers an SM,
 // 27.5 with four of 64 or two, 27 with two rows asked for ahead, 28 to 34 with none; backward 37.6
-// (5.3 TB/s), 81 with three CTAs an SM. What would be a wave and a part of one is one of CTAs that
+// (5.3 TB/s), 81 with three CTAs an SM. In float32, whose rows of 264 to 4096 spill 8 to 36 bytes a thread
+// at 80 registers, 42.3 us (6.3 TB/s) and backward 60.0 (6.7); 20000 x 1000 26.6 and 40.0 (6.0 TB/s both),
+// 32.4 with a checkpoint, 38.3 from one. What would be a wave and a part of one is one of CTAs that
 // take two: 2001 x 1000 in float32 kept in 8 bits 7.1 -> 6.3 us, 4096 x 512 in bf16 4.7 -> 4.2.
 int ctas_of(long long rows, int C, bool bwd) {
   const int g = threads_per_row(C), at_once = g < 256 ? 256 / g : 1;
